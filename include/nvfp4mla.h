@@ -436,6 +436,188 @@ int sparse_mla_decode_fp8_token(const void* q, const void* kv_cache_tok, int64_t
                                 int B, int Q, int H, int topk, float softmax_scale, void* out, float* lse,
                                 void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
 
+/*
+ * The 8-bit cache of models whose layers keep keys and values per head
+ * (grouped-query, multi-query and multi-head attention): a paged cache in E4M3
+ * with one power-of-two scale for each block of 16 tokens and head, for keys
+ * and values apart. (The pages describe MLA layers only; the page size, the
+ * page table, the causal rule of the Q new tokens and the status words are
+ * those of the calls above, so one server's tables serve both kinds of layer.)
+ *
+ * Page (kv8_page_bytes bytes; Hk = kv_heads, D = head_dim):
+ *   [0, 64 Hk D)            key codes, E4M3 [Hk, 64, D]
+ *   [64 Hk D, 128 Hk D)     value codes, E4M3 [Hk, 64, D]
+ *   then 8 bytes per head   the scale bytes of its keys' four blocks, then of
+ *                           its values'; byte e stands for 2^(e - 127)
+ *   zeros to a multiple of 128 bytes
+ * A stored value is code x 2^(e - 127). A power of two costs no precision,
+ * since E4M3 keeps its own exponent, and moves no mantissa bit when a block's
+ * scale has to grow: only codes that become subnormal are rounded again.
+ */
+#define NVFP4MLA_BLOCK_TOKENS 16  /* tokens per scale of the 8-bit cache         */
+enum { NVFP4MLA_BF16 = 0, NVFP4MLA_FP16 = 1 }; /* element types of k, v, q, out   */
+
+/* Bytes of one page: 1 <= kv_heads <= 256, head_dim 64 or 128; 0 otherwise. */
+size_t kv8_page_bytes(int kv_heads, int head_dim);
+
+/*
+ * kv8_append: write a step's new keys and values into the cache: one token a
+ * request, or whole prompts.
+ *
+ * Request b's new tokens are rows cu_tokens[b] .. cu_tokens[b+1]-1 of k and v
+ * and take positions seq_lens[b] - n_b .. seq_lens[b] - 1 (n_b their number).
+ * Of each block of 16 positions that gets a new token, and each head, keys and
+ * values apart:
+ *   e    = the smallest e with amax <= 448 x 2^(e - 127), 1 <= e <= 253, amax
+ *          over the block's new finite values; at least the block's byte
+ *          before, when the block holds tokens from before this call
+ *   code = E4M3(x / 2^(e - 127)), nearest even, saturating at +-448 (so an
+ *          infinity becomes +-448 and takes no part in amax); NaN becomes 0x7F
+ *          with its sign bit
+ *   the codes of the block's tokens from before become E4M3(value / 2^(e-127))
+ * Nothing else of the cache changes: not the rows behind the last new token.
+ *
+ *   k, v              dtype [num_tokens, kv_heads, head_dim], 16-byte aligned;
+ *                     token and head strides in elements, multiples of 8
+ *   dtype             NVFP4MLA_BF16 or NVFP4MLA_FP16
+ *   cu_tokens         int32 [B + 1], not decreasing, cu_tokens[B] <= num_tokens
+ *   seq_lens          int32 [B]: cached tokens of request b with the new ones
+ *   page_table        int32 [B, max_pages_per_seq] contiguous; a page that gets
+ *                     new tokens must belong to one request only
+ *   cache             uint8 [num_pages, kv8_page_bytes], 128-byte aligned
+ *   dev_status        optional. A block is left out, and counted once
+ *                     (NVFP4MLA_STAT_BAD_PAGE), when its page-table entry is
+ *                     no page of the cache or lies outside the table; a request
+ *                     whose new tokens are not rows of k or would take
+ *                     positions below 0 is left out and counted
+ *                     (NVFP4MLA_STAT_BAD_SLOT)
+ * num_tokens or B of 0 enqueues nothing. All pointers: device memory of the
+ * current device (checked; else NVFP4MLA_ERR_INVALID_ARG).
+ */
+int kv8_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+               int64_t v_head_stride, int dtype, int64_t num_tokens, const int32_t* cu_tokens,
+               const int32_t* seq_lens, const int32_t* page_table, int64_t max_pages_per_seq, int B, int kv_heads,
+               int head_dim, void* cache, int64_t num_pages, int32_t* dev_status, void* stream);
+
+/* Bytes of workspace that kv8_decode needs for these sizes on a GPU with
+ * num_sms SMs (num_sms <= 0: the current device); 0 for invalid sizes. */
+size_t kv8_decode_workspace_size(int B, int Q, int H, int kv_heads, int head_dim, int num_sms);
+
+/*
+ * kv8_decode: attention of each request's Q newest tokens over its cached
+ * tokens in the 8-bit cache: a decode step (Q = 1) or a speculative-verify
+ * step. Query head h reads key/value head h / (H / kv_heads).
+ *
+ * Query j of request b stands at position p = seq_lens[b] - Q + j and attends
+ * to the positions t with 0 <= t <= p, and t > p - window when window > 0:
+ *   z_t = softmax_scale * <q[b,j,h,:], K_t>
+ *   out[b,j,h,:] = sum_t exp(z_t - m) V_t / sum_t exp(z_t - m)
+ *   lse[b,j,h]   = m + ln(sum_t exp(z_t - m)),  m = max_t z_t
+ * A query with no position gets out = 0 and lse = -inf. A NaN in an attended
+ * position's row reaches the outputs that the formula gives it to; what lies
+ * in positions not attended to reaches none. A query row with an infinity or
+ * a NaN gives NaN.
+ *
+ *   q                 dtype [B, Q, H, head_dim], 16-byte aligned; element
+ *                     strides q_token_stride (of b*Q + j) and q_head_stride,
+ *                     multiples of 8
+ *   cache, page_table, seq_lens   as kv8_append; 64-token pages whose entry is
+ *                     no page of the cache, or lies outside the table, are
+ *                     left out and counted once (NVFP4MLA_STAT_BAD_PAGE)
+ *   B, Q, H           B >= 1, 1 <= Q <= 16, H a multiple of kv_heads,
+ *                     H / kv_heads <= 128
+ *   softmax_scale     > 0, finite;  window  >= 0 (0: none)
+ *   out               dtype [B, Q, H, head_dim] contiguous, 16-byte aligned
+ *   lse               fp32 [B, Q, H]
+ *   workspace         device scratch, 256-byte aligned, at least
+ *                     kv8_decode_workspace_size(...) bytes; contents need no
+ *                     initialisation and are clobbered. Calls that share a
+ *                     workspace must be ordered (one stream, or events).
+ *   flags             0, or NVFP4MLA_FLAG_MAX_CTAS(n), optionally with
+ *                     NVFP4MLA_FLAG_TEST_TIMEOUT (testing aids, as for
+ *                     sparse_mla_decode)
+ * All pointers: device memory of the current device.
+ */
+int kv8_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype, const void* cache,
+               int64_t num_pages, const int32_t* page_table, int64_t max_pages_per_seq, const int32_t* seq_lens, int B,
+               int Q, int H, int kv_heads, int head_dim, float softmax_scale, int window, void* out, float* lse,
+               void* workspace, size_t workspace_bytes, int32_t* dev_status, uint32_t flags, void* stream);
+
+/*
+ * Pages of a cache: who holds which. Every paged cache of this library works
+ * with them, as they know pages by their bytes only (22,528 for the NVFP4
+ * cache, kv8_page_bytes for the 8-bit one). The state is three device arrays:
+ *   page_table   int32 [num_seqs, max_pages_per_seq], -1 = none
+ *   seq_lens     int32 [num_seqs], 0 = the sequence is empty
+ *   refcounts    int32 [num_pages], 16-byte aligned: how many table entries
+ *                hold the page; 0 = the page is free
+ * A row's entries behind ceil(seq_lens / 64) are -1: these calls keep it so.
+ * Fresh pages are the lowest-numbered free ones, in the requests' order, so
+ * the results are the same on every run. Nothing is read back by the host.
+ * layers caches of num_pages pages each, layer_stride bytes apart, share the
+ * tables (layer_stride is ignored when layers is 1). cache and layer_stride:
+ * 16-byte aligned; page_bytes: a multiple of 16.
+ * Problems in the data are left out and counted in dev_status
+ * (NVFP4MLA_STAT_BAD_PAGE for pages, NVFP4MLA_STAT_BAD_SLOT for sequences).
+ * All pointers: device memory of the current device. Calls on one state must
+ * be ordered.
+ */
+
+/* kv_pages_copy: page dst[i] becomes a copy of page src[i], in every layer. A
+ * pair with a -1 is skipped, one with another number that is no page is left
+ * out and counted. No dst may appear twice, nor as a src of another pair. */
+int kv_pages_copy(void* cache, int64_t layers, int64_t layer_stride, int64_t num_pages, int64_t page_bytes,
+                  const int32_t* src, const int32_t* dst, int64_t n, int32_t* dev_status, void* stream);
+
+/* kv_pages_free: sequences seqs[0..n) give up their pages: every entry of the
+ * row becomes -1, its page's count goes down by one, the length becomes 0. A
+ * sequence listed twice is freed once; -1 is skipped. */
+int kv_pages_free(int32_t* page_table, int64_t max_pages_per_seq, int32_t* seq_lens, int num_seqs,
+                  int32_t* refcounts, int64_t num_pages, const int32_t* seqs, int n, int32_t* dev_status,
+                  void* stream);
+
+/* kv_pages_fork: sequence dst[i], empty before, becomes a copy of sequence
+ * src[i]: its full pages are shared (counted once more), its part-full last
+ * page, if any, is copied to a fresh page, so that both may append.
+ * new_pages[i] is the fresh
+ * page, -1 when none was needed, -2 when the pair was refused and dst left as
+ * it was: dst not empty or named before in dst, no free page left, or a bad
+ * number (counted). Of pairs with the same dst the first that is not otherwise
+ * bad counts. The i-th pair's fresh page is the next free one after those of
+ * the pairs before it. A shared entry that is no page becomes -1 (counted).
+ * n <= NVFP4MLA_MAX_REQUESTS. */
+#define NVFP4MLA_MAX_REQUESTS 16384
+int kv_pages_fork(void* cache, int64_t layers, int64_t layer_stride, int64_t num_pages, int64_t page_bytes,
+                  int32_t* page_table, int64_t max_pages_per_seq, int32_t* seq_lens, int num_seqs,
+                  int32_t* refcounts, const int32_t* src, const int32_t* dst, int n, int32_t* new_pages,
+                  int32_t* dev_status, void* stream);
+
+/* kv_pages_extend: sequence s grows by add[s] >= 0 tokens: fresh pages
+ * are added to its row until it holds seq_lens[s] + add[s] tokens and its
+ * length becomes that. granted[s] is 1, or 0
+ * when it was refused and left as it was: too few free pages, or (counted) a
+ * row too short for the new length, a negative add or a negative length. The
+ * pages that a refused sequence would have got stay free. granted may be NULL.
+ * num_seqs <= NVFP4MLA_MAX_REQUESTS. */
+int kv_pages_extend(int32_t* page_table, int64_t max_pages_per_seq, int32_t* seq_lens, int num_seqs,
+                    int32_t* refcounts, int64_t num_pages, const int32_t* add, int32_t* granted,
+                    int32_t* dev_status, void* stream);
+
+/* Bytes of workspace that kv_pages_compact needs; 0 for an invalid num_pages. */
+size_t kv_pages_compact_workspace_size(int64_t num_pages);
+
+/* kv_pages_compact: the pages in use (count > 0; n of them) move to the front:
+ * the i-th page in use at n or above goes to the i-th free page below n, with
+ * its count; every table entry follows. remap[p] is where page p went (itself
+ * when it did not move, -1 for a free page), num_live[0] is n. Table entries
+ * that name a free page or no page become -1 and are counted. workspace:
+ * 256-byte aligned, at least kv_pages_compact_workspace_size bytes, contents
+ * need no initialisation. */
+int kv_pages_compact(void* cache, int64_t layers, int64_t layer_stride, int64_t num_pages, int64_t page_bytes,
+                     int32_t* page_table, int64_t max_pages_per_seq, int num_seqs, int32_t* refcounts,
+                     int32_t* remap, int32_t* num_live, void* workspace, size_t workspace_bytes,
+                     int32_t* dev_status, void* stream);
+
 /* Human-readable name of a return code (static string, never NULL). */
 const char* nvfp4mla_status_string(int status);
 

@@ -9,7 +9,9 @@ C entry points (see include/nvfp4mla.h): mla_kv_pack,
 sparse_mla_decode_workspace_size, sparse_mla_decode, sparse_mla_decode_plan,
 sparse_mla_decode_noalloc, indexer_topk, fp8_kv_pack, nvfp4_stage_fp8,
 sparse_mla_decode_fp8, fp8_token_kv_pack, sparse_mla_decode_fp8_token,
-sparse_mla_decode_shared, nvfp4mla_status_string.
+sparse_mla_decode_shared, kv8_page_bytes, kv8_append, kv8_decode_workspace_size,
+kv8_decode, kv_pages_copy, kv_pages_free, kv_pages_fork, kv_pages_extend,
+kv_pages_compact_workspace_size, kv_pages_compact, nvfp4mla_status_string.
 """
 from __future__ import annotations
 
@@ -86,6 +88,27 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.sparse_mla_decode_fp8_token.argtypes = [vp, vp, i64, vp, i64, vp, vp, i32, i32, i32, i32, ctypes.c_float,
                                                     vp, vp, vp, sz, vp, vp]
         lib.sparse_mla_decode_fp8_token.restype = i32
+        lib.kv8_page_bytes.argtypes = [i32, i32]
+        lib.kv8_page_bytes.restype = sz
+        lib.kv8_append.argtypes = [vp, i64, i64, vp, i64, i64, i32, i64, vp, vp, vp, i64, i32, i32, i32, vp, i64, vp, vp]
+        lib.kv8_append.restype = i32
+        lib.kv8_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+        lib.kv8_decode_workspace_size.restype = sz
+        lib.kv8_decode.argtypes = [vp, i64, i64, i32, vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, ctypes.c_float,
+                                   i32, vp, vp, vp, sz, vp, u32, vp]
+        lib.kv8_decode.restype = i32
+        lib.kv_pages_copy.argtypes = [vp, i64, i64, i64, i64, vp, vp, i64, vp, vp]
+        lib.kv_pages_copy.restype = i32
+        lib.kv_pages_free.argtypes = [vp, i64, vp, i32, vp, i64, vp, i32, vp, vp]
+        lib.kv_pages_free.restype = i32
+        lib.kv_pages_fork.argtypes = [vp, i64, i64, i64, i64, vp, i64, vp, i32, vp, vp, vp, i32, vp, vp, vp]
+        lib.kv_pages_fork.restype = i32
+        lib.kv_pages_extend.argtypes = [vp, i64, vp, i32, vp, i64, vp, vp, vp, vp]
+        lib.kv_pages_extend.restype = i32
+        lib.kv_pages_compact_workspace_size.argtypes = [i64]
+        lib.kv_pages_compact_workspace_size.restype = sz
+        lib.kv_pages_compact.argtypes = [vp, i64, i64, i64, i64, vp, i64, i32, vp, vp, vp, vp, sz, vp, vp]
+        lib.kv_pages_compact.restype = i32
         lib.nvfp4mla_status_string.argtypes = [i32]
         lib.nvfp4mla_status_string.restype = ctypes.c_char_p
         _LIB = lib
@@ -417,3 +440,244 @@ def sparse_mla_decode_shared(q, kv_cache, page_table, shared_indices, member_mas
     if rc != 0:
         raise NvFp4MlaError(rc, "sparse_mla_decode_shared")
     return out, lse
+
+
+# ------------------------------------------------------------------ 8-bit per-head cache
+def _kv8_dtype(t, name) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return 0    # NVFP4MLA_BF16
+    if t.dtype == torch.float16:
+        return 1    # NVFP4MLA_FP16
+    raise TypeError(f"{name}: expected torch.bfloat16 or torch.float16, got {t.dtype}")
+
+
+def _kv8_cache_check(cache, kv_heads, head_dim):
+    import torch
+    _check(cache, "cache", torch.uint8, ndim=2)
+    if cache.shape[1] != kv8_page_bytes(kv_heads, head_dim):
+        raise ValueError("cache must be [num_pages, kv8_page_bytes(kv_heads, head_dim)]")
+
+
+def kv8_page_bytes(kv_heads: int, head_dim: int) -> int:
+    """Bytes of one 64-token page of the 8-bit per-head cache (head_dim 64 or 128)."""
+    n = int(load_library().kv8_page_bytes(kv_heads, head_dim))
+    if n == 0:
+        raise ValueError("kv_heads must be 1..256 and head_dim 64 or 128")
+    return n
+
+
+def kv8_append(k, v, cu_tokens, seq_lens, page_table, cache, dev_status=None, stream=None) -> None:
+    """Write new keys and values (bf16 or fp16 [N, kv_heads, head_dim], any token and head strides) into
+    the 8-bit cache uint8 [P, kv8_page_bytes]. Request b's are rows cu_tokens[b] .. cu_tokens[b+1]-1 and
+    become its newest tokens; cu_tokens int32 [B+1], seq_lens int32 [B] with the new ones counted,
+    page_table int32 [B, max_pages]."""
+    import torch
+    dt = _kv8_dtype(k, "k")
+    _check(k, "k", k.dtype, None, 3, contiguous=False)
+    dev = k.device
+    _check(v, "v", k.dtype, dev, 3, contiguous=False)
+    n, hk, d = k.shape
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    if n and (k.stride(2) != 1 or v.stride(2) != 1):
+        raise ValueError("k and v must be contiguous along the feature axis")
+    _kv8_cache_check(cache, hk, d)
+    _check(cache, "cache", torch.uint8, dev)
+    _check(cu_tokens, "cu_tokens", torch.int32, dev, 1)
+    _check(seq_lens, "seq_lens", torch.int32, dev, 1)
+    _check(page_table, "page_table", torch.int32, dev, 2)
+    B = seq_lens.shape[0]
+    if cu_tokens.shape[0] != B + 1 or page_table.shape[0] != B:
+        raise ValueError("shape mismatch")
+    if dev_status is not None:
+        _check(dev_status, "dev_status", torch.int32, dev, 1)
+    # the stride of an axis of one entry is never used and may be anything
+    ks, vs = ((t.stride(0) if n > 1 else 0, t.stride(1) if hk > 1 else 0) for t in (k, v))
+    rc = load_library().kv8_append(_ptr(k), *ks, _ptr(v), *vs, dt, n, _ptr(cu_tokens), _ptr(seq_lens),
+                                   _ptr(page_table), page_table.shape[1], B, hk, d, _ptr(cache), cache.shape[0], _ptr(dev_status), _stream_ptr(stream))
+    if rc != 0:
+        raise NvFp4MlaError(rc, "kv8_append")
+
+
+def kv8_decode_workspace_size(B: int, Q: int, H: int, kv_heads: int, head_dim: int, num_sms: int = 0) -> int:
+    return int(load_library().kv8_decode_workspace_size(B, Q, H, kv_heads, head_dim, num_sms))
+
+
+def kv8_decode(q, cache, page_table, seq_lens, kv_heads: int, softmax_scale, window: int = 0, out=None, lse=None,
+               workspace=None, dev_status=None, max_ctas: int = 0, stream=None, test_timeout: bool = False):
+    """Attention of each request's Q newest tokens over its cached tokens: q bf16 or fp16 [B, Q, H, head_dim]
+    (batch and query axes of one stride, any head stride), cache uint8 [P, kv8_page_bytes], page_table int32
+    [B, max_pages], seq_lens int32 [B]; window > 0: the newest `window` positions only. Returns (out as q's
+    type [B, Q, H, head_dim], lse fp32 [B, Q, H])."""
+    import torch
+    dt = _kv8_dtype(q, "q")
+    _check(q, "q", q.dtype, None, 4, contiguous=False)
+    dev = q.device
+    B, Q, H, d = q.shape
+    s0, s1, s2, s3 = q.stride()
+    if s3 != 1 or (B > 1 and Q > 1 and s0 != Q * s1):
+        raise ValueError("q must be contiguous along the feature axis, and its batch stride Q times its query stride")
+    _kv8_cache_check(cache, kv_heads, d)
+    _check(cache, "cache", torch.uint8, dev)
+    _check(page_table, "page_table", torch.int32, dev, 2)
+    _check(seq_lens, "seq_lens", torch.int32, dev, 1)
+    if seq_lens.shape[0] != B or page_table.shape[0] != B:
+        raise ValueError("shape mismatch")
+    if out is None:
+        out = torch.empty((B, Q, H, d), dtype=q.dtype, device=dev)
+    if lse is None:
+        lse = torch.empty((B, Q, H), dtype=torch.float32, device=dev)
+    _check(out, "out", q.dtype, dev, 4)
+    _check(lse, "lse", torch.float32, dev, 3)
+    if out.shape != q.shape or lse.shape != q.shape[:3]:
+        raise ValueError("out must be [B, Q, H, head_dim] and lse [B, Q, H]")
+    if workspace is None:
+        workspace = torch.empty(max(kv8_decode_workspace_size(B, Q, H, kv_heads, d), 1), dtype=torch.uint8, device=dev)
+    if dev_status is not None:
+        _check(dev_status, "dev_status", torch.int32, dev, 1)
+    token_stride, head_stride = s1 if Q > 1 else s0 if B > 1 else 0, s2 if H > 1 else 0
+    rc = load_library().kv8_decode(_ptr(q), token_stride, head_stride, dt, _ptr(cache), cache.shape[0], _ptr(page_table),
+                                   page_table.shape[1], _ptr(seq_lens), B, Q, H, kv_heads, d, float(softmax_scale),
+                                   int(window), _ptr(out), _ptr(lse), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _ptr(dev_status),
+                                   (int(max_ctas) & 0xFFFF) | (FLAG_TEST_TIMEOUT if test_timeout else 0),
+                                   _stream_ptr(stream))
+    if rc != 0:
+        raise NvFp4MlaError(rc, "kv8_decode")
+    return out, lse
+
+
+# ------------------------------------------------------------------ pages
+def _pages_of(cache, layered):
+    """(layers, layer stride in bytes, pages, bytes of a page) of a cache uint8 [P, ...], or [layers, P, ...]."""
+    import torch
+    _check(cache, "cache", torch.uint8)
+    first = 1 if layered else 0
+    if cache.dim() < first + 2:
+        raise ValueError("cache must be [num_pages, ...]" if not layered else "cache must be [layers, num_pages, ...]")
+    pages = cache.shape[first]
+    each = cache.numel() // max(1, pages * (cache.shape[0] if layered else 1))
+    return (cache.shape[0], pages * each, pages, each) if layered else (1, 0, pages, each)
+
+
+def _page_state(page_table, refcounts, dev, seq_lens=None, dev_status=None):
+    import torch
+    _check(page_table, "page_table", torch.int32, dev, 2)
+    _check(refcounts, "refcounts", torch.int32, dev, 1)
+    if seq_lens is not None:
+        _check(seq_lens, "seq_lens", torch.int32, dev, 1)
+        if seq_lens.shape[0] != page_table.shape[0]:
+            raise ValueError("seq_lens and page_table must have one row per sequence")
+    if dev_status is not None:
+        _check(dev_status, "dev_status", torch.int32, dev, 1)
+
+
+def kv_pages_copy(cache, src, dst, dev_status=None, stream=None, layered: bool = False) -> None:
+    """Page dst[i] of the cache (uint8 [P, ...]; layered: [layers, P, ...]) becomes a copy of page src[i]
+    (int32 [n], -1 = skip). No dst twice, and none that is another pair's src."""
+    import torch
+    layers, stride, pages, each = _pages_of(cache, layered)
+    dev = cache.device
+    _check(src, "src", torch.int32, dev, 1)
+    _check(dst, "dst", torch.int32, dev, 1)
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must have the same length")
+    if dev_status is not None:
+        _check(dev_status, "dev_status", torch.int32, dev, 1)
+    rc = load_library().kv_pages_copy(_ptr(cache), layers, stride, pages, each, _ptr(src), _ptr(dst), src.shape[0],
+                                      _ptr(dev_status), _stream_ptr(stream))
+    if rc != 0:
+        raise NvFp4MlaError(rc, "kv_pages_copy")
+
+
+def kv_pages_free(page_table, seq_lens, refcounts, seqs, dev_status=None, stream=None) -> None:
+    """Sequences seqs (int32 [n], -1 = skip) give up their pages: page_table int32 [S, max_pages], seq_lens
+    int32 [S] and refcounts int32 [P] are updated in place."""
+    import torch
+    dev = page_table.device
+    _page_state(page_table, refcounts, dev, seq_lens, dev_status)
+    _check(seqs, "seqs", torch.int32, dev, 1)
+    rc = load_library().kv_pages_free(_ptr(page_table), page_table.shape[1], _ptr(seq_lens), page_table.shape[0],
+                                      _ptr(refcounts), refcounts.shape[0], _ptr(seqs), seqs.shape[0],
+                                      _ptr(dev_status), _stream_ptr(stream))
+    if rc != 0:
+        raise NvFp4MlaError(rc, "kv_pages_free")
+
+
+def kv_pages_fork(cache, page_table, seq_lens, refcounts, src, dst, new_pages=None, dev_status=None, stream=None,
+                  layered: bool = False):
+    """Sequences dst (int32 [n], empty before) become copies of sequences src: full pages shared, a part-full
+    last page copied to a fresh one in the cache (uint8 [P, ...]; layered: [layers, P, ...]). Updates the
+    tables in place; returns new_pages int32 [n]: the fresh page, -1 none needed, -2 refused."""
+    import torch
+    layers, stride, pages, each = _pages_of(cache, layered)
+    dev = cache.device
+    _page_state(page_table, refcounts, dev, seq_lens, dev_status)
+    if refcounts.shape[0] != pages:
+        raise ValueError("refcounts must have one entry per page of the cache")
+    _check(src, "src", torch.int32, dev, 1)
+    _check(dst, "dst", torch.int32, dev, 1)
+    if new_pages is None:
+        new_pages = torch.empty_like(src)
+    _check(new_pages, "new_pages", torch.int32, dev, 1)
+    if src.shape != dst.shape or new_pages.shape != src.shape:
+        raise ValueError("src, dst and new_pages must have the same length")
+    rc = load_library().kv_pages_fork(_ptr(cache), layers, stride, pages, each, _ptr(page_table), page_table.shape[1],
+                                      _ptr(seq_lens), page_table.shape[0], _ptr(refcounts), _ptr(src), _ptr(dst),
+                                      src.shape[0], _ptr(new_pages), _ptr(dev_status), _stream_ptr(stream))
+    if rc != 0:
+        raise NvFp4MlaError(rc, "kv_pages_fork")
+    return new_pages
+
+
+def kv_pages_extend(page_table, seq_lens, refcounts, add, granted=None, dev_status=None, stream=None) -> None:
+    """Sequence s grows by add[s] tokens (int32 [S]): fresh pages as needed, and the longer length. granted
+    (int32 [S], optional): 1, or 0 for a sequence that was refused and left as it was."""
+    import torch
+    dev = page_table.device
+    _page_state(page_table, refcounts, dev, seq_lens, dev_status)
+    for t, name in ((add, "add"), (granted, "granted")):
+        if t is not None:
+            _check(t, name, torch.int32, dev, 1)
+            if t.shape != seq_lens.shape:
+                raise ValueError(f"{name} must have one entry per sequence")
+    rc = load_library().kv_pages_extend(_ptr(page_table), page_table.shape[1], _ptr(seq_lens), page_table.shape[0],
+                                        _ptr(refcounts), refcounts.shape[0], _ptr(add), _ptr(granted),
+                                        _ptr(dev_status), _stream_ptr(stream))
+    if rc != 0:
+        raise NvFp4MlaError(rc, "kv_pages_extend")
+
+
+def kv_pages_compact_workspace_size(num_pages: int) -> int:
+    return int(load_library().kv_pages_compact_workspace_size(num_pages))
+
+
+def kv_pages_compact(cache, page_table, refcounts, remap=None, num_live=None, workspace=None, dev_status=None,
+                     stream=None, layered: bool = False):
+    """The pages in use move to the front of the cache (uint8 [P, ...]; layered: [layers, P, ...]); tables and
+    counts follow in place. Returns (remap int32 [P]: where each page went, -1 for a free one; num_live int32
+    [1]: how many are in use)."""
+    import torch
+    layers, stride, pages, each = _pages_of(cache, layered)
+    dev = cache.device
+    _page_state(page_table, refcounts, dev, None, dev_status)
+    if refcounts.shape[0] != pages:
+        raise ValueError("refcounts must have one entry per page of the cache")
+    if remap is None:
+        remap = torch.empty_like(refcounts)
+    if num_live is None:
+        num_live = torch.empty(1, dtype=torch.int32, device=dev)
+    _check(remap, "remap", torch.int32, dev, 1)
+    _check(num_live, "num_live", torch.int32, dev, 1)
+    if remap.shape != refcounts.shape or num_live.shape[0] < 1:
+        raise ValueError("remap must have one entry per page, num_live one")
+    if workspace is None:
+        workspace = torch.empty(kv_pages_compact_workspace_size(pages), dtype=torch.uint8, device=dev)
+    rc = load_library().kv_pages_compact(_ptr(cache), layers, stride, pages, each, _ptr(page_table),
+                                         page_table.shape[1], page_table.shape[0], _ptr(refcounts), _ptr(remap),
+                                         _ptr(num_live), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                         _ptr(dev_status), _stream_ptr(stream))
+    if rc != 0:
+        raise NvFp4MlaError(rc, "kv_pages_compact")
+    return remap, num_live

@@ -104,14 +104,11 @@ static bool sizes_ok(int B, int Q, int H, int topk) {
   return H == 16 || H == 32 || H == 64 || H == 128;
 }
 
-static inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 // Memory the decode kernels may read or write with this pointer: device or managed memory of the
 // current device, or page-locked host memory mapped for the device at the same address (the
 // kernels then move those bytes over the host link themselves). Anything else (pageable host
 // memory, another device's memory, an unknown pointer) is invalid and rejected before any launch.
-enum PtrKind { kPtrInvalid, kPtrDevice, kPtrHost };
-static PtrKind pointer_kind(const void* p) {
+PtrKind pointer_kind(const void* p) {
   cudaPointerAttributes a;
   if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -131,10 +128,7 @@ static PtrKind pointer_kind(const void* p) {
 }
 
 // cuTensorMapEncodeTiled, fetched once through the runtime (no link-time libcuda dependency).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-static EncodeTiledFn encode_tiled_fn() {
+EncodeTiledFn encode_tiled_fn() {
   static EncodeTiledFn fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -162,13 +156,9 @@ static bool encode_cache_map(CUtensorMap* map, const void* cache, int64_t num_pa
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace nvfp4mla
-
-using namespace nvfp4mla;
-
 // A tag no earlier call of this process used (odd, so never 0): the merge grid recognises the
 // partials of this call by it, so the workspace needs no clearing between calls.
-static uint64_t next_call_tag() {
+uint64_t next_call_tag() {
   static std::atomic<uint64_t> counter{0};
   static const uint64_t seed = (uint64_t)std::chrono::steady_clock::now().time_since_epoch().count();
   uint64_t z = seed + 0x9E3779B97F4A7C15ull * (counter.fetch_add(1, std::memory_order_relaxed) + 1);
@@ -176,6 +166,10 @@ static uint64_t next_call_tag() {
   z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
   return (z ^ (z >> 31)) | 1ull;
 }
+
+}  // namespace nvfp4mla
+
+using namespace nvfp4mla;
 
 // The decode grid for these sizes and flags on the current device: the stream-K split unless a
 // cluster flag makes make_schedule pick the cluster schedule and all its clusters can be resident

@@ -105,6 +105,16 @@ cudaError_t launch_topk(const float* logits, int64_t stride, const int32_t* seq_
                         int32_t* out, cudaStream_t stream);
 
 int device_sm_count();
+
+// Host helpers of the entry points (api.cu).
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+enum PtrKind { kPtrInvalid, kPtrDevice, kPtrHost };
+PtrKind pointer_kind(const void* p);
+uint64_t next_call_tag();
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled_fn();
 // Workspace bytes sparse_mla_decode needs for these sizes and flags on the current device (same
 // checks and return codes as the call).
 int decode_workspace_need(int B, int Q, int H, int topk, uint32_t flags, size_t* need);

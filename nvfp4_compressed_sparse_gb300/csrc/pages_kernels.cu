@@ -1,0 +1,574 @@
+// Page operators: copy, free, fork, extend and compact the pages of a paged cache.
+//
+// The tables are small and the pages large, so each call is a planning kernel over the counts and
+// tables and, where pages move, a copy grid over their bytes that follows it as a dependent launch.
+//
+// Planning is one thread-block cluster of eight CTAs. The lowest-numbered free pages are found by
+// two passes over the counts, cut into eight pieces: every CTA counts the free pages of its piece,
+// the counts are exchanged through distributed shared memory, and the second pass (from cache)
+// numbers the free pages from there. The page with number g goes to the request whose range of the
+// needs' running sum holds g, so the result does not depend on the order in which threads run.
+#include <climits>
+#include <mutex>
+
+#include "../../include/nvfp4mla.h"
+#include "kv8.h"
+#include "ptx.cuh"
+
+namespace nvfp4mla {
+namespace {
+
+using namespace ptx;
+
+constexpr int kPlanCtas = 8;           // one portable cluster
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kCopyThreads = 256;
+constexpr int kChunkBytes = 16384;     // of a page that a copy block moves: four 16-byte loads a thread, all in flight
+constexpr unsigned kFull = 0xFFFFFFFFu;
+
+__device__ __forceinline__ void count_bad(int32_t* status, int word, int n = 1) {
+  if (status != nullptr) atomicAdd(status + word, n);
+}
+__device__ __forceinline__ void wait_for_planner() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// One chunk of one page, 16 bytes a load; page_bytes is a multiple of 16.
+__device__ __forceinline__ void copy_chunk(const PageStore& c, int64_t layer, int64_t from, int64_t to, int64_t chunk) {
+  const uint8_t* src = c.base + layer * c.layer_stride + from * c.page_bytes;
+  uint8_t* dst = c.base + layer * c.layer_stride + to * c.page_bytes;
+  constexpr int kLoads = kChunkBytes / (16 * kCopyThreads);
+  const int64_t at = chunk * kChunkBytes + (int64_t)threadIdx.x * 16;
+  uint4 v[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i)
+    if (at + i * kCopyThreads * 16 < c.page_bytes) v[i] = *reinterpret_cast<const uint4*>(src + at + i * kCopyThreads * 16);
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i)
+    if (at + i * kCopyThreads * 16 < c.page_bytes) *reinterpret_cast<uint4*>(dst + at + i * kCopyThreads * 16) = v[i];
+}
+__host__ __device__ __forceinline__ int64_t chunks_of(const PageStore& c) { return (c.page_bytes + kChunkBytes - 1) / kChunkBytes; }
+
+// ------------------------------------------------------------------ copy
+__global__ void __launch_bounds__(kCopyThreads)
+copy_kernel(const PageStore c, int64_t num_pages, const int32_t* src, const int32_t* dst, int32_t* status) {
+  const int64_t chunks = chunks_of(c), per = chunks * c.layers;
+  const int64_t i = blockIdx.x / per, rest = blockIdx.x % per;
+  const int64_t from = src[i], to = dst[i];
+  if (from == -1 || to == -1) return;
+  if (from < 0 || from >= num_pages || to < 0 || to >= num_pages) {
+    if (rest == 0 && threadIdx.x == 0) count_bad(status, NVFP4MLA_STAT_BAD_PAGE);
+    return;
+  }
+  if (from != to) copy_chunk(c, rest / chunks, from, to, rest % chunks);
+}
+
+// ------------------------------------------------------------------ free
+// Entries are taken out of the row by an exchange, so that a sequence listed twice gives each page
+// up once whichever of its blocks comes first.
+__global__ void __launch_bounds__(256) free_kernel(const PageState s, const int32_t* seqs) {
+  const int seq = seqs[blockIdx.x];
+  if (seq == -1) return;
+  if (seq < 0 || seq >= s.num_seqs) {
+    if (blockIdx.y == 0 && threadIdx.x == 0) count_bad(s.status, NVFP4MLA_STAT_BAD_SLOT);
+    return;
+  }
+  int32_t* row = s.table + (int64_t)seq * s.max_pages;
+  if (blockIdx.y == 0 && threadIdx.x == 0) s.lens[seq] = 0;
+  for (int64_t i = (int64_t)blockIdx.y * 256 + threadIdx.x; i < s.max_pages; i += (int64_t)gridDim.y * 256) {
+    if (row[i] == -1) continue;
+    const int32_t page = atomicExch(row + i, -1);
+    if (page == -1) continue;
+    if (page < 0 || page >= s.num_pages) {
+      count_bad(s.status, NVFP4MLA_STAT_BAD_PAGE);
+    } else if (atomicSub(s.refs + page, 1) <= 0) {
+      atomicAdd(s.refs + page, 1);
+      count_bad(s.status, NVFP4MLA_STAT_BAD_PAGE);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ planning
+struct PlanShared {
+  int64_t piece[kPlanCtas];    // this CTA's count, one slot a round, read by the others
+  int warp[kPlanWarps];
+  int64_t running;
+};
+
+// Sum of v over the block, in every thread.
+__device__ int block_sum(PlanShared* sh, int v) {
+  v = __reduce_add_sync(kFull, v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh->warp[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return __reduce_add_sync(kFull, sh->warp[threadIdx.x & 31]);
+}
+
+// Exclusive prefix over the block's warps of a per-warp value.
+__device__ int warp_prefix(PlanShared* sh, int v) {
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh->warp[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int w = sh->warp[threadIdx.x & 31];
+  return __reduce_add_sync(kFull, (int)(threadIdx.x & 31) < (int)(threadIdx.x >> 5) ? w : 0);
+}
+
+// Publishes this CTA's count and sums the others': before = those of the CTAs before it, all = of
+// all. Every thread of the cluster calls it; it orders global writes of the cluster too.
+__device__ void exchange(PlanShared* sh, int round, int64_t mine, int64_t& before, int64_t& all) {
+  if (threadIdx.x == 0) sh->piece[round] = mine;
+  __threadfence();
+  cluster_sync_all();
+  const uint32_t rank = cluster_ctarank();
+  before = all = 0;
+  for (uint32_t r = 0; r < kPlanCtas; ++r) {
+    const uint32_t at = map_shared_rank(smem_u32(&sh->piece[round]), r);
+    const int64_t v = (int64_t)(((uint64_t)ld_dsmem_u32(at + 4) << 32) | ld_dsmem_u32(at));
+    if (r < rank) before += v;
+    all += v;
+  }
+}
+
+// This CTA's piece of n items, and within it this warp's: multiples of 128, so that a lane's four
+// are one 16-byte load (refcounts are 16-byte aligned).
+__device__ __forceinline__ void piece_of(int64_t n, int64_t& lo, int64_t& hi) {
+  const int64_t per_warp = (n + kPlanCtas * kPlanWarps * 128 - 1) / (kPlanCtas * kPlanWarps * 128) * 128;
+  const int64_t w = (int64_t)cluster_ctarank() * kPlanWarps + (threadIdx.x >> 5);
+  lo = w * per_warp < n ? w * per_warp : n;
+  hi = lo + per_warp < n ? lo + per_warp : n;
+}
+
+// The four counts at i (items behind n read as `fill`).
+__device__ __forceinline__ int4 four_at(const int32_t* a, int64_t i, int64_t n, int fill) {
+  if (i + 3 < n) return *reinterpret_cast<const int4*>(a + i);
+  return make_int4(i < n ? a[i] : fill, i + 1 < n ? a[i + 1] : fill, i + 2 < n ? a[i + 2] : fill, fill);
+}
+
+// Items of [lo, hi) that `is` holds for, over the warp, in every lane.
+template <class F>
+__device__ int warp_count(const int32_t* a, int64_t lo, int64_t hi, int64_t n, int fill, F is) {
+  const int lane = threadIdx.x & 31;
+  int c = 0;
+#pragma unroll 4
+  for (int64_t i = lo; i < hi; i += 128) {
+    const int4 v = four_at(a, i + lane * 4, n, fill);
+    c += is(i + lane * 4, v.x) + is(i + lane * 4 + 1, v.y) + is(i + lane * 4 + 2, v.z) + is(i + lane * 4 + 3, v.w);
+  }
+  return __reduce_add_sync(kFull, c);
+}
+
+// do_(item, value, number) for every item of [lo, hi) that `is` holds for, numbered from `from`.
+template <class F, class G>
+__device__ void warp_number(const int32_t* a, int64_t lo, int64_t hi, int64_t n, int fill, int64_t from, int64_t stop, F is, G do_) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t i = lo; i < hi && from < stop; i += 128) {
+    const int64_t at = i + lane * 4;
+    const int4 v = four_at(a, at, n, fill);
+    const int vs[4] = {v.x, v.y, v.z, v.w};
+    int c = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c += is(at + k, vs[k]) ? 1 : 0;
+    int before = c;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(kFull, before, d);
+      if (lane >= d) before += o;
+    }
+    const int total = __shfl_sync(kFull, before, 31);
+    int64_t g = from + before - c;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (is(at + k, vs[k])) do_(at + k, vs[k], g++);
+    from += total;
+  }
+}
+
+// Running sums of the needs: sum[i] = those of the requests before i, sum[n] = all.
+template <class F>
+__device__ int64_t sum_needs(PlanShared* sh, int32_t* sum, int n, F need) {
+  if (threadIdx.x == 0) sh->running = 0;
+  __syncthreads();
+  for (int base = 0; base < n; base += kPlanThreads) {
+    const int i = base + threadIdx.x;
+    const int c = i < n ? need(i) : 0;
+    const int lane = threadIdx.x & 31;
+    int incl = c;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(kFull, incl, d);
+      if (lane >= d) incl += o;
+    }
+    const int64_t run = sh->running;
+    const int64_t ahead = run + warp_prefix(sh, __shfl_sync(kFull, incl, 31));
+    // a sum that leaves 32 bits stays at the top: there are fewer pages than that
+    const int64_t mine = ahead + incl - c;
+    if (i < n) sum[i] = (int32_t)(mine < INT_MAX ? mine : INT_MAX);
+    __syncthreads();
+    if (threadIdx.x == kPlanThreads - 1) sh->running = ahead + incl;
+    __syncthreads();
+  }
+  const int64_t all = sh->running;
+  if (threadIdx.x == 0) sum[n] = (int32_t)(all < INT_MAX ? all : INT_MAX);
+  __syncthreads();
+  return all;
+}
+
+// The request that the page with number g is for: the last whose running sum is at most g.
+__device__ __forceinline__ int owner_of(const int32_t* sum, int n, int64_t g) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sum[mid] <= g) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+struct IsFree {
+  __device__ bool operator()(int64_t, int v) const { return v == 0; }
+};
+
+// ------------------------------------------------------------------ fork
+// A claim on an empty sequence is kept where its length stands until the plan is done: INT_MIN + i,
+// so that the smallest i wins. Lengths that callers hold are not that small.
+constexpr int kClaim = INT_MIN;
+
+struct ForkArgs {
+  PageState s;
+  PageStore c;
+  const int32_t* src;
+  const int32_t* dst;
+  int n;
+  int32_t* new_pages;
+};
+
+__device__ __forceinline__ bool is_claim(int len) { return len < kClaim + NVFP4MLA_MAX_REQUESTS; }
+
+// The length that pair i would copy, or -1 when the pair is bad in itself.
+__device__ int fork_length(const ForkArgs& a, int i, bool& missing) {
+  const int src = a.src[i], dst = a.dst[i];
+  missing = false;
+  if (src < 0 || src >= a.s.num_seqs || dst < 0 || dst >= a.s.num_seqs || src == dst) return -1;
+  int len = __ldcg(a.s.lens + src);
+  if (is_claim(len)) len = 0;      // an empty source that is some pair's target
+  if (len < 0 || (len + (int64_t)kPageTokens - 1) / kPageTokens > a.s.max_pages) return -1;
+  if (len % kPageTokens != 0) {
+    const int page = a.s.table[(int64_t)src * a.s.max_pages + len / kPageTokens];
+    if (page < 0 || page >= a.s.num_pages) {
+      missing = true;
+      return -1;
+    }
+  }
+  return len;
+}
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs a) {
+  extern __shared__ int32_t sum[];   // [n + 1]
+  __shared__ PlanShared sh;
+  let_dependents_start();
+  const int rank = (int)cluster_ctarank();
+  // claims
+  for (int i = rank * kPlanThreads + threadIdx.x; i < a.n; i += kPlanCtas * kPlanThreads) {
+    bool missing;
+    const int len = fork_length(a, i, missing);
+    if (len < 0) {
+      count_bad(a.s.status, missing ? NVFP4MLA_STAT_BAD_PAGE : NVFP4MLA_STAT_BAD_SLOT);
+      continue;
+    }
+    int32_t* at = a.s.lens + a.dst[i];
+    const int there = __ldcg(at);
+    if (there == 0 || is_claim(there)) atomicMin(at, kClaim + i);
+  }
+  int64_t before, all;
+  exchange(&sh, 0, 0, before, all);
+  // who won, and what that needs
+  auto won = [&](int i, int& len) {
+    bool missing;
+    len = fork_length(a, i, missing);
+    return len >= 0 && __ldcg(a.s.lens + a.dst[i]) == kClaim + i;
+  };
+  const int64_t total = sum_needs(&sh, sum, a.n, [&](int i) {
+    int len;
+    return won(i, len) && len % kPageTokens != 0 ? 1 : 0;
+  });
+  // this thread's own pairs, read before any length is set
+  constexpr int kOwn = NVFP4MLA_MAX_REQUESTS / (kPlanCtas * kPlanThreads);
+  int own_len[kOwn];
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    const int i = (k * kPlanCtas + rank) * kPlanThreads + threadIdx.x;
+    int len = -1;
+    own_len[k] = i < a.n && won(i, len) ? len : -1;
+  }
+  int64_t lo, hi;
+  piece_of(a.s.num_pages, lo, hi);
+  const int c = warp_count(a.s.refs, lo, hi, a.s.num_pages, 1, IsFree());
+  const int cta = block_sum(&sh, (threadIdx.x & 31) == 0 ? c : 0);
+  exchange(&sh, 1, cta, before, all);
+  before += warp_prefix(&sh, c);
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    const int i = (k * kPlanCtas + rank) * kPlanThreads + threadIdx.x;
+    if (i >= a.n) continue;
+    const bool needs = sum[i + 1] > sum[i], refused = needs && sum[i] >= all;
+    if (own_len[k] >= 0) a.s.lens[a.dst[i]] = refused ? 0 : own_len[k];
+    if (own_len[k] < 0 || refused) a.new_pages[i] = -2;
+    else if (!needs) a.new_pages[i] = -1;
+  }
+  warp_number(a.s.refs, lo, hi, a.s.num_pages, 1, before, total, IsFree(), [&](int64_t page, int, int64_t g) {
+    if (g >= total) return;
+    a.s.refs[page] = 1;
+    a.new_pages[owner_of(sum, a.n, g)] = (int32_t)page;
+  });
+  cluster_sync_all();   // no CTA leaves while another may read its count
+}
+
+// Blocks (pair, chunk of a layer's page) move the part-full pages; the last blocks of a pair write
+// its row and count the shared pages.
+constexpr int kRowEntries = 1024;      // of a row that a block takes
+
+__global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(const ForkArgs a) {
+  wait_for_planner();
+  const int64_t chunks = chunks_of(a.c), copies = chunks * a.c.layers;
+  const int64_t per = copies + (a.s.max_pages + kRowEntries - 1) / kRowEntries;
+  const int64_t i = blockIdx.x / per, part = blockIdx.x % per;
+  const int fresh = a.new_pages[i];
+  if (fresh == -2) return;
+  const int src = a.src[i], dst = a.dst[i];
+  const int64_t full = a.s.lens[dst] / kPageTokens;
+  const int32_t* from = a.s.table + (int64_t)src * a.s.max_pages;
+  if (part < copies) {
+    if (fresh >= 0) copy_chunk(a.c, part / chunks, from[full], fresh, part % chunks);
+    return;
+  }
+  int32_t* to = a.s.table + (int64_t)dst * a.s.max_pages;
+  const int64_t lo = (part - copies) * kRowEntries;
+  for (int64_t k = lo + threadIdx.x; k < lo + kRowEntries && k < a.s.max_pages; k += kCopyThreads) {
+    int32_t page = -1;
+    if (k < full) {
+      page = from[k];
+      if (page < 0 || page >= a.s.num_pages) {
+        page = -1;
+        count_bad(a.s.status, NVFP4MLA_STAT_BAD_PAGE);
+      } else {
+        atomicAdd(a.s.refs + page, 1);
+      }
+    } else if (k == full && fresh >= 0) {
+      page = fresh;
+    }
+    to[k] = page;
+  }
+}
+
+// ------------------------------------------------------------------ extend
+struct ExtendArgs {
+  PageState s;
+  const int32_t* add;
+  int32_t* granted;
+};
+
+// Pages that sequence i lacks for its new length, or -1 when it cannot grow (bad: to be counted).
+__device__ int64_t extend_need(const ExtendArgs& a, int i, int64_t& have, bool& bad) {
+  const int64_t len = __ldcg(a.s.lens + i), add = a.add[i];
+  have = (len + kPageTokens - 1) / kPageTokens;
+  const int64_t want = (len + add + kPageTokens - 1) / kPageTokens;
+  bad = len < 0 || add < 0 || (add > 0 && want > a.s.max_pages) || len + add > INT_MAX;
+  return bad ? -1 : (want > have ? want - have : 0);
+}
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads) extend_kernel(const ExtendArgs a) {
+  extern __shared__ int32_t sum[];   // [num_seqs + 1]
+  __shared__ PlanShared sh;
+  const int rank = (int)cluster_ctarank();
+  const int n = a.s.num_seqs;
+  const int64_t total = sum_needs(&sh, sum, n, [&](int i) {
+    int64_t have;
+    bool bad;
+    const int64_t need = extend_need(a, i, have, bad);
+    return (int)(need > 0 ? need : 0);
+  });
+  int64_t lo, hi, before, all;
+  piece_of(a.s.num_pages, lo, hi);
+  const int c = warp_count(a.s.refs, lo, hi, a.s.num_pages, 1, IsFree());
+  const int cta = block_sum(&sh, (threadIdx.x & 31) == 0 ? c : 0);
+  exchange(&sh, 0, cta, before, all);
+  before += warp_prefix(&sh, c);
+  warp_number(a.s.refs, lo, hi, a.s.num_pages, 1, before, total, IsFree(), [&](int64_t page, int, int64_t g) {
+    if (g >= total) return;
+    const int i = owner_of(sum, n, g);
+    if (sum[i + 1] > all) return;    // refused: its pages stay free
+    int64_t have;
+    bool bad;
+    extend_need(a, i, have, bad);
+    a.s.refs[page] = 1;
+    a.s.table[(int64_t)i * a.s.max_pages + have + (g - sum[i])] = (int32_t)page;
+  });
+  const int64_t free_pages = all;
+  cluster_sync_all();   // the lengths change only when no CTA reads them any more, and no count is read after this
+  for (int i = rank * kPlanThreads + threadIdx.x; i < n; i += kPlanCtas * kPlanThreads) {
+    int64_t have;
+    bool bad;
+    const int64_t need = extend_need(a, i, have, bad);
+    const bool ok = !bad && (need == 0 || sum[i + 1] <= free_pages);
+    if (bad) count_bad(a.s.status, NVFP4MLA_STAT_BAD_SLOT);
+    if (ok) a.s.lens[i] += a.add[i];
+    if (a.granted != nullptr) a.granted[i] = ok ? 1 : 0;
+  }
+}
+
+// ------------------------------------------------------------------ compact
+// workspace: the free pages below the live ones' number, in order, then the live pages at or above
+// it, in order (each at most half of the pages), then how many.
+struct CompactArgs {
+  PageState s;
+  PageStore c;
+  int32_t* remap;
+  int32_t* num_live;
+  int32_t* holes;
+  int32_t* movers;
+  int32_t* num_moves;
+};
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactArgs a) {
+  __shared__ PlanShared sh;
+  let_dependents_start();
+  const int64_t n = a.s.num_pages;
+  const auto live = [](int64_t, int v) { return v > 0; };
+  int64_t lo, hi, before, num_live;
+  piece_of(n, lo, hi);
+  int c = warp_count(a.s.refs, lo, hi, n, 0, live);
+  int cta = block_sum(&sh, (threadIdx.x & 31) == 0 ? c : 0);
+  exchange(&sh, 0, cta, before, num_live);
+  // live pages behind the live ones' number, and free ones before it: equally many
+  const auto moves = [=](int64_t i, int v) { return v > 0 && i >= num_live; };
+  const auto hole = [=](int64_t i, int v) { return v <= 0 && i < num_live; };
+  const int cm = warp_count(a.s.refs, lo, hi, n, 0, moves), ch = warp_count(a.s.refs, lo, hi, n, 0, hole);
+  int64_t m_before, m_all, h_before, h_all;
+  cta = block_sum(&sh, (threadIdx.x & 31) == 0 ? cm : 0);
+  exchange(&sh, 1, cta, m_before, m_all);
+  m_before += warp_prefix(&sh, cm);
+  cta = block_sum(&sh, (threadIdx.x & 31) == 0 ? ch : 0);
+  exchange(&sh, 2, cta, h_before, h_all);
+  h_before += warp_prefix(&sh, ch);
+  warp_number(a.s.refs, lo, hi, n, 0, h_before, h_before + n, hole, [&](int64_t page, int, int64_t g) { a.holes[g] = (int32_t)page; });
+  for (int64_t i = lo + (threadIdx.x & 31); i < hi; i += 32) {
+    const int v = a.s.refs[i];
+    if (!moves(i, v)) a.remap[i] = v > 0 ? (int32_t)i : -1;
+  }
+  exchange(&sh, 3, 0, before, h_all);   // the holes are listed, and nobody reads a count below num_live any more
+  warp_number(a.s.refs, lo, hi, n, 0, m_before, m_before + n, moves, [&](int64_t page, int v, int64_t g) {
+    const int32_t to = __ldcg(a.holes + g);
+    a.movers[g] = (int32_t)page;
+    a.remap[page] = to;
+    a.s.refs[to] = v;
+    a.s.refs[page] = 0;
+  });
+  if (cluster_ctarank() == 0 && threadIdx.x == 0) {
+    *a.num_live = (int32_t)num_live;
+    *a.num_moves = (int32_t)m_all;
+  }
+  cluster_sync_all();   // no CTA leaves while another may read its count
+}
+
+__global__ void __launch_bounds__(kCopyThreads) compact_apply_kernel(const CompactArgs a, int table_blocks) {
+  wait_for_planner();
+  if ((int)blockIdx.x < table_blocks) {
+    const int64_t entries = (int64_t)a.s.num_seqs * a.s.max_pages;
+    for (int64_t i = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; i < entries; i += (int64_t)table_blocks * kCopyThreads) {
+      const int32_t page = a.s.table[i];
+      if (page == -1) continue;
+      const int32_t to = page >= 0 && page < a.s.num_pages ? a.remap[page] : -1;
+      if (to < 0) count_bad(a.s.status, NVFP4MLA_STAT_BAD_PAGE);
+      if (to != page) a.s.table[i] = to;
+    }
+    return;
+  }
+  const int64_t chunks = chunks_of(a.c), per = chunks * a.c.layers;
+  const int64_t items = *a.num_moves * per;
+  for (int64_t it = blockIdx.x - table_blocks; it < items; it += gridDim.x - table_blocks) {
+    const int64_t i = it / per, rest = it % per;
+    copy_chunk(a.c, rest / chunks, a.movers[i], a.holes[i], rest % chunks);
+  }
+}
+
+// A dependent launch: the grid may start while the planner runs and waits for it where it reads.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned blocks, unsigned threads, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Shared memory of the running sums (up to MAX_REQUESTS + 1 of them), allowed once per device.
+cudaError_t allow_sums(const void* kernel, int which) {
+  static std::mutex mu;
+  static bool done[2][64] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev < 64 && done[which][dev]) return cudaSuccess;
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (NVFP4MLA_MAX_REQUESTS + 1) * 4);
+  if (err == cudaSuccess && dev < 64) done[which][dev] = true;
+  return err;
+}
+
+}  // namespace
+
+int64_t pages_copy_blocks(const PageStore& c, int64_t n) { return n * c.layers * chunks_of(c); }
+
+cudaError_t launch_pages_copy(const PageStore& c, int64_t num_pages, const int32_t* src, const int32_t* dst, int64_t n,
+                              int32_t* status, cudaStream_t stream) {
+  copy_kernel<<<(unsigned)pages_copy_blocks(c, n), kCopyThreads, 0, stream>>>(c, num_pages, src, dst, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_free(const PageState& s, const int32_t* seqs, int n, cudaStream_t stream) {
+  const int64_t parts = (s.max_pages + 1023) / 1024;
+  free_kernel<<<dim3((unsigned)n, (unsigned)(parts < 64 ? parts : 64)), 256, 0, stream>>>(s, seqs);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_fork(const PageState& s, const PageStore& c, const int32_t* src, const int32_t* dst, int n,
+                              int32_t* new_pages, cudaStream_t stream) {
+  const ForkArgs a{s, c, src, dst, n, new_pages};
+  cudaError_t err = allow_sums(reinterpret_cast<const void*>(fork_plan_kernel), 0);
+  if (err != cudaSuccess) return err;
+  fork_plan_kernel<<<kPlanCtas, kPlanThreads, (size_t)(n + 1) * 4, stream>>>(a);
+  if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  const int64_t per = pages_copy_blocks(c, 1) + (s.max_pages + kRowEntries - 1) / kRowEntries;
+  return launch_after(fork_apply_kernel, (unsigned)(n * per), kCopyThreads, stream, a);
+}
+
+cudaError_t launch_pages_extend(const PageState& s, const int32_t* add, int32_t* granted, cudaStream_t stream) {
+  const ExtendArgs a{s, add, granted};
+  const cudaError_t err = allow_sums(reinterpret_cast<const void*>(extend_kernel), 1);
+  if (err != cudaSuccess) return err;
+  extend_kernel<<<kPlanCtas, kPlanThreads, (size_t)(s.num_seqs + 1) * 4, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_compact(const PageState& s, const PageStore& c, int32_t* remap, int32_t* num_live,
+                                 int32_t* workspace, cudaStream_t stream) {
+  const int64_t half = (s.num_pages / 2 + 4) / 4 * 4;
+  const CompactArgs a{s, c, remap, num_live, workspace, workspace + half, workspace + 2 * half};
+  compact_plan_kernel<<<kPlanCtas, kPlanThreads, 0, stream>>>(a);
+  const cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  const int64_t entries = (int64_t)s.num_seqs * s.max_pages;
+  int64_t table_blocks = (entries + 4 * kCopyThreads - 1) / (4 * kCopyThreads);
+  if (table_blocks > 1024) table_blocks = 1024;
+  int64_t copy_blocks = pages_copy_blocks(c, s.num_pages / 2 + 1);
+  const int64_t most = (int64_t)device_sm_count() * 8;     // every block resident: 2,048 threads an SM
+  if (copy_blocks > most) copy_blocks = most;
+  return launch_after(compact_apply_kernel, (unsigned)(table_blocks + copy_blocks), kCopyThreads, stream, a, (int)table_blocks);
+}
+
+}  // namespace nvfp4mla
