@@ -51,7 +51,14 @@ struct Kv8DecodeParams {
   uint16_t* out;                 // [B, Q, H, D]
   float* lse;                    // [B, Q, H]
   int32_t* status;
+  int ctas;                      // grid size
+  float* part_o;                 // [2 ctas, columns, D]: a CTA's first and last segment, where they are partial
+  float* part_ml;                // [2 ctas, columns, 2]: maximum (log2 units) and sum
+  uint64_t* arrived;             // [ctas]: this call's tag with the CTAs that have left their partials
+  uint64_t tag;                  // unique per call; its low 16 bits are the count's
+  uint32_t withhold;             // testing aid: 1 = no tile is ever loaded
 };
+int kv8_decode_columns(int Q, int group);                      // (query, head) columns of a CTA's tile
 cudaError_t launch_kv8_decode(const Kv8DecodeParams& p, int head_dim, bool fp16, cudaStream_t stream);
 
 // The three arrays of the page operators, and the caches whose pages they move.

@@ -75,6 +75,36 @@ int kv8_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, con
   return status_of(launch_kv8_append(p, head_dim, dtype == NVFP4MLA_FP16, static_cast<cudaStream_t>(stream)));
 }
 
+// Workspace: partial O [2 ctas, columns, D] f32 | partial (maximum, sum) [2 ctas, columns, 2] f32 |
+// arrival counts [ctas] u64; each part 256-byte aligned.
+struct Kv8Workspace {
+  size_t ml, arrived, total;
+};
+static size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+static Kv8Workspace decode_workspace(int columns, int head_dim, int ctas) {
+  Kv8Workspace w;
+  w.ml = align256((size_t)2 * ctas * columns * head_dim * sizeof(float));
+  w.arrived = w.ml + align256((size_t)2 * ctas * columns * 2 * sizeof(float));
+  w.total = w.arrived + align256((size_t)ctas * sizeof(uint64_t));
+  return w;
+}
+
+// The cache as a 4-D tensor of bytes: [pages][codes of a kind and head][64 tokens][head_dim]. One
+// box is the 64 rows of one kind and head of one page, swizzled as the tensor cores read them; a
+// page number behind the cache reads as zeros, from nowhere.
+static bool encode_pages_map(CUtensorMap* map, const void* cache, int64_t num_pages, int64_t page_bytes, int kv_heads,
+                             int head_dim) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)head_dim, kPageTokens, (cuuint64_t)(2 * kv_heads), (cuuint64_t)num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)head_dim, (cuuint64_t)(kPageTokens * head_dim), (cuuint64_t)page_bytes};
+  const cuuint32_t box[4] = {(cuuint32_t)head_dim, kPageTokens, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(cache), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 static bool decode_sizes_ok(int B, int Q, int H, int kv_heads, int head_dim) {
   if (!kv8_sizes_ok(kv_heads, head_dim) || B < 1 || Q < 1 || Q > 16 || H < 1 || H % kv_heads != 0) return false;
   return H / kv_heads <= kMaxGroup;
@@ -84,7 +114,7 @@ size_t kv8_decode_workspace_size(int B, int Q, int H, int kv_heads, int head_dim
   if (!decode_sizes_ok(B, Q, H, kv_heads, head_dim)) return 0;
   if (num_sms <= 0) num_sms = device_sm_count();
   if (num_sms <= 0) return 0;
-  return 256;
+  return decode_workspace(kv8_decode_columns(Q, H / kv_heads), head_dim, num_sms).total;
 }
 
 int kv8_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype, const void* cache,
@@ -108,6 +138,8 @@ int kv8_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, int
     return NVFP4MLA_ERR_INVALID_ARG;
   if ((int64_t)B * Q * H > INT32_MAX) return NVFP4MLA_ERR_UNSUPPORTED;
   Kv8DecodeParams p{};
+  if (!encode_pages_map(&p.cache_map, cache, num_pages, kv8_page_size(kv_heads, head_dim), kv_heads, head_dim))
+    return NVFP4MLA_ERR_CUDA;
   p.q = static_cast<const uint16_t*>(q);
   p.q_token_stride = q_token_stride;
   p.q_head_stride = q_head_stride;
@@ -127,7 +159,15 @@ int kv8_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, int
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.status = dev_status;
-  (void)flags;
+  const int sms = device_sm_count(), cap = (int)(flags & 0xFFFFu);
+  const Kv8Workspace w = decode_workspace(kv8_decode_columns(Q, p.group), head_dim, sms);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.ctas = cap > 0 && cap < sms ? cap : sms;
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + w.ml);
+  p.arrived = reinterpret_cast<uint64_t*>(ws + w.arrived);
+  p.tag = (next_call_tag() & ~(uint64_t)0xFFFF) | 0x10000u;
+  p.withhold = (flags & NVFP4MLA_FLAG_TEST_TIMEOUT) ? 1u : 0u;
   return status_of(launch_kv8_decode(p, head_dim, dtype == NVFP4MLA_FP16, static_cast<cudaStream_t>(stream)));
 }
 

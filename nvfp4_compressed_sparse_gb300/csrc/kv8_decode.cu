@@ -1,9 +1,38 @@
 // kv8_decode: attention of a step's queries over the 8-bit per-head cache.
 //
-// One block per (request, query, query head): the cached tokens in chunks of 128, thread = token
-// for the scores and thread = dim for the values, with the running maximum and sum of a softmax.
+// What it computes. For one request and key/value head, the columns c = (query, head of the group)
+// share every key and value row, so the step is two products over a 128-token tile:
+//   S[t, c] = K[t, :] . q_c            z = scale 2^(ek_t - 127) S        (ek, ev: scale bytes)
+//   O[d, c] += sum_t V[t, d] w[t, c]   w = 2^(z log2e + ev_t - 127 - M_c)
+// with M_c a running reference, at most 2^4 below the largest exponent so far, and beside it the
+// softmax's own running sum l_c = sum_t 2^(z log2e - m_c). A value's block scale goes into the
+// weight's exponent before the reference is taken, so that blocks with scales far apart lose nothing.
+//
+// What bounds it. A token costs 2 D + 0.5 bytes per head and 4 D operations per column: below some
+// 250 operations a byte the step is bound by memory, so the codes have to reach the tensor cores as
+// they lie in the cache, without a conversion in between. E4M3 x E4M3 products do that: K and V
+// are the A operands straight from where TMA put them (K K-major, V M-major), and the 16-bit
+// operands, q and w, are written as sums of E4M3 parts, each a sixteenth of the one before:
+//   x = x_0 + x_1/16 + x_2/256 (+ x_3/4096),   x_i = E4M3(what is left x 16^i)
+// A part takes four bits of the significand, so three hold an fp16 exactly and four hold a weight
+// to 16 bits. The parts are further columns of the B operand (their products land in columns of
+// their own and are added in fp32 afterwards), so that A is read from shared memory once.
+//
+// One CTA per SM, persistent. The tiles of all (request, key/value head, column tile) units form
+// one sequence, found by every CTA from the lengths, and each CTA takes one contiguous range of it.
+//   warp 0     producer: page numbers a group of 16 tiles ahead, then per tile four 64-row TMA boxes
+//              and the scale bytes into a ring of stages
+//   warp 1     issues S = K q;  warp 3: issues O += V w (two threads, so that neither waits for the other)
+//   warp 2     queries of the next unit: scaling by a power of two, parts, two buffers
+//   warps 4-7  softmax of the range's even tiles, warps 8-11 of the odd ones (thread = token): each
+//              stream has its own S, w and O, and keeps its own M, m, l; they are added at the unit's end
+// A unit that several CTAs share is joined by whichever of them finishes last: the others leave
+// (m, l, O) in the workspace and count themselves.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <cstddef>
+#include <mutex>
 
 #include "../../include/nvfp4mla.h"
 #include "kv8.h"
@@ -14,103 +43,891 @@ namespace {
 
 using namespace ptx;
 
-__device__ __forceinline__ float code_value(uint8_t c) {
-  const uint32_t h = e4m3x2_to_f16x2(c);
-  return __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu)));
+constexpr int kTile = 128;             // tokens per tile: two pages
+constexpr int kQParts = 3, kWParts = 4;
+constexpr int kThreads = 384;
+constexpr int kGroup = 16;             // tiles whose page numbers are read together
+constexpr int kMinTiles = 2;           // of a CTA: one for each stream
+constexpr float kHeadroom = 4.f;       // log2: how far above the reference a weight's exponent may come
+constexpr float kWeightScale = 4.f;    // log2: weights are held times 16, so that 2^4 above it is 256 <= 448
+constexpr float kSumHeadroom = 60.f;   // log2: the same for the sum, which fp32 holds
+constexpr unsigned kFull = 0xFFFFFFFFu;
+
+// Sizes of the instance with D dims and NC columns.
+template <int D, int NC>
+struct Shape {
+  static constexpr int kNS = (kQParts * NC + 15) / 16 * 16;     // columns of S
+  static constexpr int kNO = kWParts * NC;                      // columns of O, bytes of a row of w
+  static constexpr int kRowBytes = kTile * D;                   // K or V of a tile
+  static constexpr int kScaleOff = 2 * kRowBytes;
+  static constexpr int kStageBytes = 2 * kRowBytes;             // the scale bytes have an area of their own
+  static constexpr int kQBytes = (kNS * D + 1023) / 1024 * 1024;
+  static constexpr int kWBytes = kTile * kNO;
+  static constexpr int kBudget = 232448 - 1024 - 8192;          // less alignment and the control block
+  static constexpr int kFit = (kBudget - 2 * kQBytes - 2 * kWBytes) / kStageBytes;
+  static constexpr int kStages = kFit < 12 ? kFit : 12;
+  static constexpr int kUsed = 2 * kNS + 2 * kNO;               // TMEM columns
+  static constexpr uint32_t kTmem = kUsed <= 128 ? 128 : (kUsed <= 256 ? 256 : 512);
+  static constexpr uint32_t kSwK = D == 128 ? SW_128B : SW_64B;
+  static constexpr uint32_t kSwW = kNO == 128 ? SW_128B : (kNO == 64 ? SW_64B : SW_32B);
+  static_assert(kUsed <= 512 && kStages >= 3, "fits");
+};
+
+template <int NC, int kStages>
+struct Control {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], w_full[2];
+  uint64_t drain[2];
+  uint4 scales[kStages][2];            // per page: the scale bytes of two neighbouring heads
+  uint32_t pages_ok[kStages];          // bit per page: it is one
+  alignas(16) float f[2][NC];          // read four at a time, as M and m are: per query buffer: score of a column per unit of S, log2 units
+  int hi[2][NC], lo[2][NC];            // positions that a column attends to
+  alignas(16) float top_w[2][NC];      // per stream: M
+  alignas(16) float top_s[2][NC];      // m
+  float scale_o[2][NC], scale_l[2][NC];
+  float part_max[2][4][NC][2];
+  float part_l[2][4][NC];
+  uint32_t poison[2][NC][4];           // per stream and column: dims that a NaN value reaches
+  float join_m[NC], join_w0[NC], join_w1[NC], join_l[NC];
+  int any_poison[2];
+  int scan[kThreads / 32];
+  int64_t scan_sum[kThreads / 32];
+  int64_t start_before;                // tiles before request start_b
+  int start_b;
+  int last;
+  int abort;
+  uint32_t tmem_base;
+};
+
+// Tiles of one unit of a request with `len` tokens: [first, first + n). A unit has at least one, so
+// that a request without tokens is written too.
+__device__ __forceinline__ void unit_tiles(const Kv8DecodeParams& p, int len, int& first, int& n) {
+  const int64_t pages = min((int64_t)(len + (int64_t)kPageTokens - 1) / kPageTokens, p.max_pages);
+  int last = len > 0 ? (int)((pages + 1) / 2) : 1;
+  first = 0;
+  if (p.window > 0) {
+    const int64_t from = (int64_t)len - p.Q - p.window + 1;
+    if (from > 0) first = (int)(from / kTile);
+  }
+  if (first > last - 1) first = last - 1;
+  n = last - first;
 }
+
+// A walk over the segments of this CTA: per unit, the tiles of it that the CTA has.
+struct Walk {
+  int64_t left;          // tiles of the CTA's range from this segment on
+  int b, unit, units;    // request, unit inside it, units of a request
+  int len, first, n;     // the request's length and a unit's tiles
+  int at, count;         // this segment: tiles at .. at + count - 1 of the unit
+
+  __device__ __forceinline__ void load(const Kv8DecodeParams& p) {
+    len = __ldg(p.seq_lens + b);
+    if (len < 0) len = 0;
+    unit_tiles(p, len, first, n);
+  }
+  __device__ __forceinline__ void take() { count = (int)min((int64_t)(n - at), left); }
+  __device__ __forceinline__ void next(const Kv8DecodeParams& p) {
+    left -= count;
+    if (left <= 0) return;
+    at = 0;
+    if (++unit == units) {
+      unit = 0;
+      ++b;
+      load(p);
+    }
+    take();
+  }
+  __device__ __forceinline__ bool whole() const { return count == n; }
+};
+
+__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ bool bar_any(int id, int threads, bool v) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(v ? 1 : 0)
+      : "memory");
+  return r != 0;
+}
+
 template <bool kHalf>
-__device__ __forceinline__ float widen1(uint16_t x) {
-  if constexpr (kHalf) return __half2float(__ushort_as_half(x));
-  return __uint_as_float((uint32_t)x << 16);
+__device__ __forceinline__ float2 widen2(uint32_t w) {
+  if constexpr (kHalf) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// (a, b) as kParts pairs of E4M3 parts: part[i] holds two bytes, a's in the low one. |a|, |b| <= 448.
+template <int kParts>
+__device__ __forceinline__ void split_parts(float a, float b, uint32_t (&part)[kParts]) {
+  part[0] = f32x2_to_e4m3x2(a, b);
+  uint32_t h = e4m3x2_to_f16x2(part[0]);
+  const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  // what the first part leaves has at most 20 significant bits, of which the fp16 keeps 11: as much
+  // as the other parts hold
+  __half2 r = __floats2half2_rn(a - c.x, b - c.y);
+  const __half2 sixteen = __floats2half2_rn(16.f, 16.f);
+#pragma unroll
+  for (int i = 1; i < kParts; ++i) {
+    r = __hmul2(r, sixteen);
+    part[i] = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&r));
+    if (i + 1 < kParts) {
+      h = e4m3x2_to_f16x2(part[i]);
+      r = __hsub2(r, *reinterpret_cast<const __half2*>(&h));
+    }
+  }
+}
+
+// fp32 in an order-preserving signed integer.
+__device__ __forceinline__ int ordered(float x) {
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
+
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+// 2^(a - b), 1 for equal infinities.
+__device__ __forceinline__ float ratio(float a, float b) { return a == b ? 1.f : exp2f(a - b); }
+
+template <int D, int NC>
+struct Cta {
+  using S = Shape<D, NC>;
+  using Ctl = Control<NC, S::kStages>;
+  const Kv8DecodeParams& p;
+  uint8_t* stages;
+  uint8_t* qbuf;
+  uint8_t* wbuf;
+  Ctl* ctl;
+
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    if (mbar_wait(bar, parity, &ctl->abort, kWaitTimeoutNs)) return true;
+    if (atomicExch(&ctl->abort, 1) == 0 && p.status != nullptr) atomicAdd(p.status + NVFP4MLA_STAT_TIMEOUT, 1);
+    return false;
+  }
+  // First position that a query at `at` attends to.
+  __device__ __forceinline__ int window_start(int at) const { return p.window > 0 && at + 1 > p.window ? at + 1 - p.window : 0; }
+  __device__ __forceinline__ int col_tiles() const { return (p.Q * p.group + NC - 1) / NC; }
+
+  // ---------------------------------------------------------------- producer (warp 0)
+  // Page numbers of tiles i .. i + 15 of the segment: two lanes a tile. -1: not needed, or none.
+  __device__ __forceinline__ int load_pages(const Walk& w, int i, int ct, int kvh) {
+    const int lane = threadIdx.x & 31;
+    const int tile = i + (lane >> 1);
+    if (tile >= w.count) return -1;
+    const int64_t col = 2 * ((int64_t)w.first + w.at + tile) + (lane & 1);
+    const int64_t from = p.window > 0 ? (int64_t)w.len - p.Q - p.window + 1 : 0;
+    if (col * kPageTokens >= w.len || (col + 1) * kPageTokens <= from) return -1;
+    int page = -1;
+    if (col < p.max_pages) {
+      page = __ldg(p.page_table + (int64_t)w.b * p.max_pages + col);
+      if (page >= 0 && page < p.num_pages) return page;
+      page = -1;
+    } else {
+      return -1;                       // counted with the pages behind the table
+    }
+    if (ct == 0 && kvh == 0 && p.status != nullptr) atomicAdd(p.status + NVFP4MLA_STAT_BAD_PAGE, 1);
+    return page;
+  }
+
+  __device__ void producer(Walk w) {
+    const int lane = threadIdx.x & 31;
+    const int cts = col_tiles();
+    uint32_t g = 0;
+    if (p.withhold) return;
+    int pages = w.left > 0 ? load_pages(w, 0, w.unit % cts, w.unit / cts) : -1;
+    while (w.left > 0) {
+      const int kvh = w.unit / cts, ct = w.unit % cts;
+      if (kvh == 0 && ct == 0 && w.at + w.count == w.n && lane == 0 && p.status != nullptr) {
+        const int64_t need = ((int64_t)w.len + kPageTokens - 1) / kPageTokens;
+        int64_t from = p.window > 0 ? ((int64_t)w.len - p.Q - p.window + 1) / kPageTokens : 0;
+        if (from < p.max_pages) from = p.max_pages;
+        if (need > from) atomicAdd(p.status + NVFP4MLA_STAT_BAD_PAGE, (int)(need - from));
+      }
+      for (int i = 0; i < w.count; i += kGroup) {
+        const int mine = pages;
+        if (i + kGroup < w.count) {
+          pages = load_pages(w, i + kGroup, ct, kvh);
+        } else {
+          Walk nx = w;
+          nx.next(p);
+          pages = nx.left > 0 ? load_pages(nx, 0, nx.unit % cts, nx.unit / cts) : -1;
+        }
+        const int m = min(kGroup, w.count - i);
+        for (int k = 0; k < m; ++k, ++g) {
+          const int page0 = __shfl_sync(kFull, mine, 2 * k), page1 = __shfl_sync(kFull, mine, 2 * k + 1);
+          const uint32_t st = g % S::kStages, round = g / S::kStages;
+          bool ok = true;
+          if (lane == 0) {
+            ok = wait(&ctl->empty[st], (round & 1) ^ 1);
+            if (ok) {
+              uint8_t* kt = stages + st * S::kStageBytes;
+              uint8_t* vt = kt + S::kRowBytes;
+              ctl->pages_ok[st] = (page0 >= 0 ? 1u : 0u) | (page1 >= 0 ? 2u : 0u);
+              mbar_arrive_expect_tx(&ctl->full[st], 2 * S::kRowBytes + (page0 >= 0 ? 16 : 0) + (page1 >= 0 ? 16 : 0));
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int page = h == 0 ? page0 : page1;
+                const int at = page >= 0 ? page : (int)p.num_pages;      // behind the cache: zeros
+                if (page >= 0)
+                  bulk_g2s(&ctl->scales[st][h], p.cache + page * p.page_bytes + kv8_scales_off(p.kv_heads, D, kvh & ~1), 16, &ctl->full[st]);
+                tma_load_4d(kt + h * kPageTokens * D, &p.cache_map, 0, 0, kvh, at, &ctl->full[st]);
+                tma_load_4d(vt + h * kPageTokens * D, &p.cache_map, 0, 0, p.kv_heads + kvh, at, &ctl->full[st]);
+              }
+            }
+          }
+          if (__shfl_sync(kFull, ok ? 0 : 1, 0)) {
+            drain_copies(g);
+            return;
+          }
+        }
+      }
+      w.next(p);
+    }
+    if (ctl_aborted()) drain_copies(g);
+  }
+  __device__ __forceinline__ bool ctl_aborted() { return *reinterpret_cast<volatile int*>(&ctl->abort) != 0; }
+
+  // After a wait gave up: the copies of tiles before g that are still in flight land (bounded).
+  __device__ void drain_copies(uint32_t g) {
+    if ((threadIdx.x & 31) != 0) return;
+    const uint32_t n = g < (uint32_t)S::kStages ? g : (uint32_t)S::kStages;
+    for (uint32_t i = 0; i < n; ++i) {
+      const uint32_t t = g - 1 - i;
+      mbar_wait(&ctl->full[t % S::kStages], (t / S::kStages) & 1, nullptr, kWaitTimeoutNs);
+    }
+  }
+
+  // ---------------------------------------------------------------- S = K q (warp 1, one thread)
+  __device__ void issue_s(Walk w, uint32_t tmem) {
+    constexpr uint32_t kId = idesc_e4m3(128, S::kNS, false, false);
+    const uint64_t kd = sdesc(smem_u32(stages), 16, 8 * D, S::kSwK), qd = sdesc(smem_u32(qbuf), 16, 8 * D, S::kSwK);
+    uint32_t g = 0, uses[2] = {0, 0};
+    bool ok = true;
+    for (uint32_t seg = 0; ok && w.left > 0; ++seg, w.next(p)) {
+      const uint32_t buf = seg & 1;
+      ok = wait(&ctl->q_full[buf], (seg >> 1) & 1);
+      for (int i = 0; ok && i < w.count; ++i, ++g) {
+        const uint32_t st = g % S::kStages, stream = i & 1;
+        ok = wait(&ctl->full[st], (g / S::kStages) & 1);
+        // the stream's last S has been read once its weights are written
+        if (ok && uses[stream] > 0) ok = wait(&ctl->w_full[stream], (uses[stream] - 1) & 1);
+        if (!ok) break;
+        ++uses[stream];
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+          umma_f8_ss(tmem + stream * S::kNS, kd + ((st * S::kStageBytes + k * 32) >> 4), qd + ((buf * S::kQBytes + k * 32) >> 4), kId, k > 0);
+        umma_commit(&ctl->s_full[stream]);
+      }
+      if (ok) umma_commit(&ctl->q_empty[buf]);
+    }
+    umma_commit(&ctl->drain[0]);
+    mbar_wait(&ctl->drain[0], 0, nullptr, kWaitTimeoutNs);
+  }
+
+  // ---------------------------------------------------------------- O += V w (warp 3, one thread)
+  __device__ void issue_o(Walk w, uint32_t tmem) {
+    constexpr uint32_t kId = idesc_e4m3(D, S::kNO, true, true);
+    const uint64_t vd = sdesc(smem_u32(stages + S::kRowBytes), 16, 8 * D, S::kSwK), wd = sdesc(smem_u32(wbuf), 16, 8 * S::kNO, S::kSwW);
+    uint32_t g = 0, uses[2] = {0, 0};
+    bool ok = true;
+    for (; ok && w.left > 0; w.next(p)) {
+      for (int i = 0; ok && i < w.count; ++i, ++g) {
+        const uint32_t st = g % S::kStages, stream = i & 1;
+        ok = wait(&ctl->w_full[stream], uses[stream] & 1);
+        if (!ok) break;
+        ++uses[stream];
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kTile / 32; ++k)
+          umma_f8_ss(tmem + 2 * S::kNS + stream * S::kNO, vd + ((st * S::kStageBytes + k * 32 * D) >> 4),
+                     wd + ((stream * S::kWBytes + k * 32 * S::kNO) >> 4), kId, i > 1 || k > 0);
+        umma_commit(&ctl->empty[st]);
+      }
+    }
+    umma_commit(&ctl->drain[1]);
+    mbar_wait(&ctl->drain[1], 0, nullptr, kWaitTimeoutNs);
+  }
+
+  // ---------------------------------------------------------------- queries (warp 2)
+  template <bool kHalf>
+  __device__ void queries(Walk w) {
+    constexpr int kLanes = D / 8, kCols = 32 / kLanes;    // lanes a column, columns a round
+    const int lane = threadIdx.x & 31, sub = lane / kLanes, ch = lane % kLanes;
+    const int cts = col_tiles(), ncols = p.Q * p.group;
+    for (uint32_t seg = 0; w.left > 0; ++seg, w.next(p)) {
+      const uint32_t buf = seg & 1;
+      const int kvh = w.unit / cts, ct = w.unit % cts;
+      const bool ok = wait(&ctl->q_empty[buf], ((seg >> 1) & 1) ^ 1);
+      if (__any_sync(kFull, !ok)) return;
+      uint8_t* img = qbuf + buf * S::kQBytes;
+      constexpr int kRounds = NC / kCols, kBatch = kRounds < 4 ? kRounds : 4;
+      for (int r0 = 0; r0 < kRounds; r0 += kBatch) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) {
+          const int col = ct * NC + (r0 + r) * kCols + sub;
+          v[r] = make_uint4(0u, 0u, 0u, 0u);
+          if (col < ncols) {
+            const int j = col / p.group, h = kvh * p.group + col % p.group;
+            v[r] = __ldg(reinterpret_cast<const uint4*>(p.q + ((int64_t)w.b * p.Q + j) * p.q_token_stride + h * p.q_head_stride + ch * 8));
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) {
+          const int c = (r0 + r) * kCols + sub, col = ct * NC + c;
+          const uint32_t ws[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
+          uint32_t top = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = __vmaxu2(top, ws[k] & 0x7FFF7FFFu);
+          top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+          for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(kFull, top, d));
+          const bool finite = top < (kHalf ? 0x7C00u : 0x7F80u);
+          // the largest magnitude goes to [128, 256): a power of two, exact
+          const int e = (int)(__float_as_uint(widen2<kHalf>(top).x) >> 23) - 127;
+          const int sh = top == 0 || !finite ? 0 : min(7 - e, 126);
+          const float mul = finite ? __uint_as_float((uint32_t)(sh + 127) << 23) : 0.f;
+          uint32_t part[4][kQParts];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 x = widen2<kHalf>(ws[k]);
+            split_parts(finite ? x.x * mul : 0.f, finite ? x.y * mul : 0.f, part[k]);
+          }
+#pragma unroll
+          for (int i = 0; i < kQParts; ++i) {
+            const int n = i * NC + c;
+            const int chunk = D == 128 ? ((ch >> 1) ^ (n & 7)) : ((ch >> 1) ^ ((n >> 1) & 3));
+            *reinterpret_cast<uint2*>(img + n * D + chunk * 16 + (ch & 1) * 8) =
+                make_uint2(part[0][i] | (part[1][i] << 16), part[2][i] | (part[3][i] << 16));
+          }
+          if (ch == 0) {
+            const float back = __uint_as_float((uint32_t)(127 - sh) << 23);
+            ctl->f[buf][c] = col < ncols ? (finite ? p.scale_log2 * back : __int_as_float(0x7fc00000)) : 0.f;
+            const int at = w.len - p.Q + col / p.group;
+            ctl->hi[buf][c] = col < ncols ? at : -1;
+            ctl->lo[buf][c] = window_start(at);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->q_full[buf]);
+    }
+  }
+
+  // ---------------------------------------------------------------- softmax (warps 4-11)
+  // Rows of V that no column attends to become zeros (they may hold anything), and a NaN in a row
+  // that only some columns attend to is taken out and noted for those.
+  __device__ void clean_row(uint8_t* vt, int r, int t, bool page_ok, uint32_t buf, int stream, int cols) {
+    bool any = false, all = true;
+    for (int c = 0; c < cols; ++c) {
+      const bool in = page_ok && t <= ctl->hi[buf][c] && t >= ctl->lo[buf][c];
+      any |= in;
+      all &= in;
+    }
+    uint4* row = reinterpret_cast<uint4*>(vt + r * D);
+    if (!any) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
+    } else if (!all) {
+      for (int i = 0; i < D / 16; ++i) {
+        const uint4 x = row[i];
+        const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+        uint32_t nan = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) nan |= __vcmpeq4(ws[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        if (nan == 0) continue;
+        const int chunk = D == 128 ? (i ^ (r & 7)) : (i ^ ((r >> 1) & 3));
+        uint8_t* bytes = reinterpret_cast<uint8_t*>(row + i);
+        for (int k = 0; k < 16; ++k) {
+          if ((bytes[k] & 0x7F) != 0x7F) continue;
+          bytes[k] = 0;
+          const int d = chunk * 16 + k;
+          for (int c = 0; c < cols; ++c)
+            if (t <= ctl->hi[buf][c] && t >= ctl->lo[buf][c]) atomicOr(&ctl->poison[stream][c][d >> 5], 1u << (d & 31));
+          ctl->any_poison[stream] = 1;
+        }
+      }
+    }
+  }
+
+  // Leaves this CTA's partial results of a shared unit as counted; true for the last to come.
+  __device__ bool arrive(const Walk& w, int64_t base, int64_t total, int64_t ctas) {
+    const int64_t g0 = base, g1 = base + w.n - 1;
+    const int64_t c_lo = ((g0 + 1) * ctas - 1) / total, c_hi = ((g1 + 1) * ctas - 1) / total;
+    unsigned long long* at = reinterpret_cast<unsigned long long*>(p.arrived + c_lo);
+    const unsigned long long tag = p.tag;
+    unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(at);
+    for (;;) {
+      // a count of another call (or whatever the workspace held before) counts as none
+      const unsigned long long have = (old & ~0xFFFFull) == tag ? (old & 0xFFFF) : 0;
+      const bool last = (int64_t)have + 1 == c_hi - c_lo + 1;
+      const unsigned long long now = atomicCAS(at, old, last ? 0ull : (tag | (have + 1)));
+      if (now == old) return last;
+      old = now;
+    }
+  }
+
+  template <bool kHalf>
+  __device__ __forceinline__ void put(int64_t at, float v) {
+    if constexpr (kHalf) p.out[at] = __half_as_ushort(__float2half_rn(v));
+    else p.out[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  }
+
+  template <bool kHalf>
+  __device__ void softmax(Walk w, uint32_t tmem, int64_t t_begin, int64_t total, int64_t ctas) {
+    const int wg = (threadIdx.x >> 7) - 1;                // 0, 1: the stream
+    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, r = threadIdx.x & 127;
+    const uint32_t quarter = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t s_at = quarter + wg * S::kNS, o_at = quarter + 2 * S::kNS + wg * S::kNO;
+    const int cts = col_tiles(), ncols = p.Q * p.group;
+    const int64_t t_first = t_begin;
+    int64_t done = t_begin;                               // tiles of the whole sequence before this segment
+    uint32_t g = 0, uses = 0;
+    uint32_t last_tile = 0;
+    bool has_last = false;
+    float l[NC];
+    for (uint32_t seg = 0; w.left > 0; ++seg, w.next(p)) {
+      const uint32_t buf = seg & 1;
+      const int kvh = w.unit / cts, ct = w.unit % cts;
+      bool ok = wait(&ctl->q_full[buf], (seg >> 1) & 1);
+      // positions that every column attends to
+      const int j0 = ct * NC / p.group, j1 = (min(ct * NC + NC, ncols) - 1) / p.group;
+      const int at0 = w.len - p.Q + j0, at1 = w.len - p.Q + j1;
+      const int all_lo = window_start(at1);
+      const int cols = min(NC, ncols - ct * NC);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) l[c] = 0.f;
+      bool stop = false;
+      for (int i = wg; i < w.count; i += 2) {
+        const uint32_t gt = g + i, st = gt % S::kStages;
+        const int t0 = (w.first + w.at + i) * kTile, t = t0 + r;
+        ok = ok && wait(&ctl->s_full[wg], uses & 1);
+        ok = ok && wait(&ctl->full[st], (gt / S::kStages) & 1);
+        // the stream's weights before these have been read, and its O is at rest
+        if (has_last) ok = ok && wait(&ctl->empty[last_tile % S::kStages], (last_tile / S::kStages) & 1);
+        __syncwarp();
+        tc_fence_after();
+        ++uses;
+        const uint32_t pages = ctl->pages_ok[st];
+        const bool page_ok = (pages >> (r >> 6)) & 1;
+        const uint8_t* sc = reinterpret_cast<const uint8_t*>(&ctl->scales[st][r >> 6]) + (kvh & 1) * 8 + ((r & 63) >> 4);
+        const float ks = __uint_as_float((uint32_t)sc[0] << 23);
+        const float ev = (float)((int)sc[4] - 127);
+        const bool whole = pages == 3u && t0 + kTile - 1 <= at0 && t0 >= all_lo;
+        float z[NC];
+        bool raise = false;
+#pragma unroll
+        for (int c0 = 0; c0 < NC; c0 += 8) {
+          uint32_t a[8], b[8], d[8];
+          tmem_ld8(s_at + c0, a);
+          tmem_ld8(s_at + NC + c0, b);
+          tmem_ld8(s_at + 2 * NC + c0, d);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 8; k += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&ctl->f[buf][c0 + k]);
+            const float4 tw = *reinterpret_cast<const float4*>(&ctl->top_w[wg][c0 + k]);
+            const float4 ts = *reinterpret_cast<const float4*>(&ctl->top_s[wg][c0 + k]);
+            const float fs[4] = {f.x, f.y, f.z, f.w}, tws[4] = {tw.x, tw.y, tw.z, tw.w}, tss[4] = {ts.x, ts.y, ts.z, ts.w};
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const int q = k + n, c = c0 + q;
+              const float s = fmaf(__uint_as_float(d[q]), 1.f / 256.f, fmaf(__uint_as_float(b[q]), 1.f / 16.f, __uint_as_float(a[q])));
+              z[c] = s * (fs[n] * ks);
+              if (!whole && !(page_ok && t <= ctl->hi[buf][c] && t >= ctl->lo[buf][c])) z[c] = neg_inf();
+              raise |= z[c] + ev > tws[n] + kHeadroom || z[c] > tss[n] + kSumHeadroom;
+            }
+          }
+        }
+        uint8_t* vt = stages + st * S::kStageBytes + S::kRowBytes;
+        if (!whole && ok) clean_row(vt, r, t, page_ok, buf, wg, cols);
+        if (bar_any(1 + wg, 128, raise || !ok)) {
+          // rare after the first tiles: new references, the tile's own maxima where those are larger
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const int a = __reduce_max_sync(kFull, ordered(z[c] + ev)), b = __reduce_max_sync(kFull, ordered(z[c]));
+            if (lane == 0) {
+              ctl->part_max[wg][warp][c][0] = unordered(a);
+              ctl->part_max[wg][warp][c][1] = unordered(b);
+            }
+          }
+          if (bar_any(1 + wg, 128, !ok)) {
+            stop = true;
+            break;
+          }
+          if (r < NC) {
+            float a = ctl->top_w[wg][r], b = ctl->top_s[wg][r];
+            const float a0 = a, b0 = b;
+            for (int k = 0; k < 4; ++k) {
+              a = fmaxf(a, ctl->part_max[wg][k][r][0]);
+              b = fmaxf(b, ctl->part_max[wg][k][r][1]);
+            }
+            ctl->top_w[wg][r] = a;
+            ctl->top_s[wg][r] = b;
+            ctl->scale_o[wg][r] = ratio(a0, a);
+            ctl->scale_l[wg][r] = ratio(b0, b);
+          }
+          bar_sync(1 + wg, 128);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) l[c] *= ctl->scale_l[wg][c];
+          if (i > 1) {
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < S::kNO; n += 8) {
+              uint32_t o[8];
+              tmem_ld8(o_at + n, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * ctl->scale_o[wg][(n + k) % NC]);
+              tmem_st8(o_at + n, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        // weights, as parts, into the token's row of the B operand
+        uint8_t* wrow = wbuf + wg * S::kWBytes + r * S::kNO;
+        constexpr int kStep = NC < 16 ? NC : 16;
+#pragma unroll
+        for (int c0 = 0; c0 < NC; c0 += kStep) {
+          uint32_t out[kWParts][kStep / 4];
+#pragma unroll
+          for (int k = 0; k < kStep; k += 4) {
+            const float4 tw = *reinterpret_cast<const float4*>(&ctl->top_w[wg][c0 + k]);
+            const float4 ts = *reinterpret_cast<const float4*>(&ctl->top_s[wg][c0 + k]);
+            const float tws[4] = {tw.x, tw.y, tw.z, tw.w}, tss[4] = {ts.x, ts.y, ts.z, ts.w};
+            float e[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const int c = c0 + k + n;
+              const float mw = tws[n] == neg_inf() ? 0.f : tws[n] - kWeightScale, ms = tss[n] == neg_inf() ? 0.f : tss[n];
+              e[n] = ex2_approx(z[c] + ev - mw);
+              l[c] += ex2_approx(z[c] - ms);
+            }
+            uint32_t p01[kWParts], p23[kWParts];
+            split_parts(e[0], e[1], p01);
+            split_parts(e[2], e[3], p23);
+#pragma unroll
+            for (int n = 0; n < kWParts; ++n) out[n][k / 4] = p01[n] | (p23[n] << 16);
+          }
+          if constexpr (NC == 8) {
+            const int x = (r >> 2) & 1;
+            *reinterpret_cast<uint4*>(wrow + 16 * x) = make_uint4(out[0][0], out[0][1], out[1][0], out[1][1]);
+            *reinterpret_cast<uint4*>(wrow + 16 * (x ^ 1)) = make_uint4(out[2][0], out[2][1], out[3][0], out[3][1]);
+          } else {
+#pragma unroll
+            for (int n = 0; n < kWParts; ++n) {
+              const int chunk = (n * NC + c0) / 16;
+              const int x = NC == 16 ? chunk ^ ((r >> 1) & 3) : chunk ^ (r & 7);
+              *reinterpret_cast<uint4*>(wrow + 16 * x) = make_uint4(out[n][0], out[n][1], out[n][2], out[n][3]);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->w_full[wg]);
+        last_tile = gt;
+        has_last = true;
+      }
+      // ---- the segment's end: both streams, columns of this warpgroup
+      const int n = w.count;
+      if (!stop) {
+        const uint32_t a = g + (n - 1) / 2 * 2, b = g + (n >= 2 ? (n - 2) / 2 * 2 + 1 : 0);
+        ok = ok && wait(&ctl->empty[a % S::kStages], (a / S::kStages) & 1);
+        if (n >= 2) ok = ok && wait(&ctl->empty[b % S::kStages], (b / S::kStages) & 1);
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) l[c] += __shfl_xor_sync(kFull, l[c], d);
+          if (lane == 0) ctl->part_l[wg][warp][c] = l[c];
+        }
+      }
+      if (bar_any(3, 256, stop || !ok)) {
+        // gave up: the counts of the units that this CTA shares still come out even
+        if (wg == 0 && r == 0)
+          for (; w.left > 0; done += w.count, w.next(p))
+            if (!w.whole()) arrive(w, done - w.at, total, ctas);
+        return;
+      }
+      g += n;
+      constexpr int kHalfCols = NC / 2;
+      if (r < kHalfCols) {
+        const int c = wg * kHalfCols + r;
+        float l0 = 0.f, l1 = 0.f;
+        for (int k = 0; k < 4; ++k) {
+          l0 += ctl->part_l[0][k][c];
+          l1 += ctl->part_l[1][k][c];
+        }
+        const float m0 = ctl->top_s[0][c], m1 = ctl->top_s[1][c], m = fmaxf(m0, m1);
+        const float w0 = ctl->top_w[0][c], w1 = ctl->top_w[1][c];
+        ctl->join_m[c] = m;
+        ctl->join_l[c] = l0 * ratio(m0, m) + l1 * ratio(m1, m);
+        ctl->join_w0[c] = w0 == neg_inf() ? 0.f : exp2f(w0 - kWeightScale - m);
+        ctl->join_w1[c] = w1 == neg_inf() ? 0.f : exp2f(w1 - kWeightScale - m);
+      }
+      bar_sync(1 + wg, 128);
+      __syncwarp();
+      const int d = D == 128 ? r : (lane < 16 ? warp * 16 + lane : -1);     // M = 64 fills 16 lanes of each quarter
+      const bool full_unit = w.whole();
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (done == t_first ? 0 : 1);
+      const int64_t row0 = (int64_t)w.b * p.Q;
+      const bool poisoned = ctl->any_poison[0] | ctl->any_poison[1];
+#pragma unroll
+      for (int c0 = 0; c0 < kHalfCols; c0 += 4) {
+        float acc[4];
+#pragma unroll
+        for (int stream = 0; stream < 2; ++stream) {
+          if (stream == 1 && n < 2) break;
+          uint32_t o[kWParts][4];
+#pragma unroll
+          for (int k = 0; k < kWParts; ++k) tmem_ld4(quarter + 2 * S::kNS + stream * S::kNO + k * NC + wg * kHalfCols + c0, o[k]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int c = wg * kHalfCols + c0 + k;
+            float x = __uint_as_float(o[3][k]);
+            x = fmaf(x, 1.f / 16.f, __uint_as_float(o[2][k]));
+            x = fmaf(x, 1.f / 16.f, __uint_as_float(o[1][k]));
+            x = fmaf(x, 1.f / 16.f, __uint_as_float(o[0][k]));
+            if (poisoned && d >= 0 && ((ctl->poison[stream][c][d >> 5] >> (d & 31)) & 1)) x = __int_as_float(0x7fc00000);
+            acc[k] = stream == 0 ? x * ctl->join_w0[c] : fmaf(x, ctl->join_w1[c], acc[k]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = wg * kHalfCols + c0 + k, col = ct * NC + c;
+          if (d < 0 || col >= ncols) continue;
+          if (full_unit) {
+            const float sum = ctl->join_l[c];
+            const int64_t row = (row0 + col / p.group) * p.H + kvh * p.group + col % p.group;
+            put<kHalf>(row * D + d, sum == 0.f ? 0.f : acc[k] / sum);
+            if (d == 0) p.lse[row] = sum == 0.f ? neg_inf() : (ctl->join_m[c] + log2f(sum)) * 0.69314718055994530942f;
+          } else {
+            p.part_o[(slot * NC + c) * D + d] = acc[k];
+            if (d == 0) {
+              p.part_ml[(slot * NC + c) * 2] = ctl->join_m[c];
+              p.part_ml[(slot * NC + c) * 2 + 1] = ctl->join_l[c];
+            }
+          }
+        }
+      }
+      if (!full_unit) {
+        __threadfence();
+        bar_sync(3, 256);
+        if (wg == 0 && r == 0) {
+          ctl->last = arrive(w, done - w.at, total, ctas) ? 1 : 0;
+          __threadfence();
+        }
+        bar_sync(3, 256);
+        if (ctl->last) {
+          const int64_t base = done - w.at;
+          const int64_t c_lo = ((base + 1) * ctas - 1) / total, c_hi = ((base + w.n) * ctas - 1) / total;
+          const int64_t slot_lo = 2 * c_lo + (c_lo * total / ctas == base ? 0 : 1);
+          if (d >= 0) {
+            for (int c = wg * kHalfCols; c < wg * kHalfCols + kHalfCols && ct * NC + c < ncols; ++c) {
+              const int col = ct * NC + c;
+              float m = neg_inf(), sum = 0.f, acc = 0.f;
+              for (int64_t k = c_lo; k <= c_hi; ++k) {
+                const int64_t sl = k == c_lo ? slot_lo : 2 * k;
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (sl * NC + c) * 2));
+                const float o = __ldcg(p.part_o + (sl * NC + c) * D + d);
+                const float m_new = fmaxf(m, ml.x), keep = ratio(m, m_new), in = ratio(ml.x, m_new);
+                sum = sum * keep + ml.y * in;
+                acc = acc * keep + o * in;
+                m = m_new;
+              }
+              const int64_t row = (row0 + col / p.group) * p.H + kvh * p.group + col % p.group;
+              put<kHalf>(row * D + d, sum == 0.f ? 0.f : acc / sum);
+              if (d == 0) p.lse[row] = sum == 0.f ? neg_inf() : (m + log2f(sum)) * 0.69314718055994530942f;
+            }
+          }
+        }
+      }
+      // the next segment starts from nothing
+      bar_sync(3, 256);
+      if (r < NC) {
+        ctl->top_w[wg][r] = ctl->top_s[wg][r] = neg_inf();
+        if (poisoned)
+          for (int k = 0; k < 4; ++k) ctl->poison[wg][r][k] = 0;
+      }
+      if (r == 0) ctl->any_poison[wg] = 0;
+      bar_sync(1 + wg, 128);
+      if (lane == 0) mbar_arrive(&ctl->q_empty[buf]);
+      done += n;
+    }
+  }
+};
+
+template <int D, int NC, bool kHalf>
+__global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p) {
+  using S = Shape<D, NC>;
+  using Ctl = Control<NC, S::kStages>;
+  static_assert(offsetof(Ctl, scales) % 16 == 0 && offsetof(Ctl, f) % 16 == 0 && offsetof(Ctl, top_w) % 16 == 0 &&
+                offsetof(Ctl, top_s) % 16 == 0 && NC % 4 == 0, "vector accesses are aligned");
+  static_assert(sizeof(Ctl) <= 8192, "the control block fits its share");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* stages = base;
+  uint8_t* qbuf = stages + S::kStages * S::kStageBytes;
+  uint8_t* wbuf = qbuf + 2 * S::kQBytes;
+  Ctl* ctl = reinterpret_cast<Ctl*>(wbuf + 2 * S::kWBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    prefetch_tensormap(&p.cache_map);
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->q_full[i], 1);
+      mbar_init(&ctl->q_empty[i], 1 + 8);   // the issuer of S and the softmax warps
+      mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->w_full[i], 4);
+      mbar_init(&ctl->drain[i], 1);
+      ctl->any_poison[i] = 0;
+    }
+    ctl->abort = 0;
+    fence_barrier_init();
+  }
+  for (int i = tid; i < 2 * NC; i += kThreads) {
+    ctl->top_w[i / NC][i % NC] = ctl->top_s[i / NC][i % NC] = neg_inf();
+    for (int k = 0; k < 4; ++k) ctl->poison[i / NC][i % NC][k] = 0;
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem_base, S::kTmem);
+    tmem_relinquish();
+  }
+
+  // the whole sequence of tiles: every thread sums a run of requests
+  const int units = p.kv_heads * ((p.Q * p.group + NC - 1) / NC);
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  int64_t sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    int first, n;
+    unit_tiles(p, max(0, __ldg(p.seq_lens + b)), first, n);
+    sum += n;
+  }
+  int64_t incl = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(kFull, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) ctl->scan_sum[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int64_t before = 0, all = 0;
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) before += ctl->scan_sum[i];
+    all += ctl->scan_sum[i];
+  }
+  before += incl - sum;
+  const int64_t total = all * units;
+  // no CTA gets less than one tile for each of its two streams: joining costs more than a tile
+  const int64_t ctas = min((int64_t)gridDim.x, (total + kMinTiles - 1) / kMinTiles);
+  const int64_t cta = blockIdx.x;
+  const int64_t t_begin = cta < ctas ? cta * total / ctas : 0, t_end = cta < ctas ? (cta + 1) * total / ctas : 0;
+  if (t_begin < t_end && before * units <= t_begin && t_begin < (before + sum) * units) {
+    int b = b0;
+    int64_t at = before;
+    for (;; ++b) {
+      int first, n;
+      unit_tiles(p, max(0, __ldg(p.seq_lens + b)), first, n);
+      if (t_begin < (at + n) * units) break;
+      at += n;
+    }
+    ctl->start_b = b;
+    ctl->start_before = at * units;
+  }
+  __syncthreads();
+  Walk w{};
+  w.left = t_end - t_begin;
+  w.units = units;
+  if (w.left > 0) {
+    w.b = ctl->start_b;
+    w.load(p);
+    const int64_t in = t_begin - ctl->start_before;
+    w.unit = (int)(in / w.n);
+    w.at = (int)(in % w.n);
+    w.take();
+    const uint32_t tmem = ctl->tmem_base;
+    Cta<D, NC> c{p, stages, qbuf, wbuf, ctl};
+    if (warp == 0) {
+      c.producer(w);
+    } else if (warp == 1) {
+      if (lane == 0) c.issue_s(w, tmem);
+      __syncwarp();
+    } else if (warp == 2) {
+      c.template queries<kHalf>(w);
+    } else if (warp == 3) {
+      if (lane == 0) c.issue_o(w, tmem);
+      __syncwarp();
+    } else {
+      c.template softmax<kHalf>(w, tmem, t_begin, total, ctas);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(ctl->tmem_base, S::kTmem);
+  }
+}
+
+template <int D, int NC>
+constexpr size_t smem_bytes() {
+  using S = Shape<D, NC>;
+  return 1024 + (size_t)S::kStages * S::kStageBytes + 2 * S::kQBytes + 2 * S::kWBytes + sizeof(Control<NC, S::kStages>);
+}
+
+template <int D, int NC, bool kHalf>
+cudaError_t launch(const Kv8DecodeParams& p, cudaStream_t stream) {
+  constexpr size_t smem = smem_bytes<D, NC>();
+  static_assert(smem <= 232448, "exceeds the 227 KB shared-memory limit");
+  static std::mutex mu;
+  static bool allowed[64] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 64 || !allowed[dev]) {
+      err = cudaFuncSetAttribute(kv8_decode_kernel<D, NC, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (err != cudaSuccess) return err;
+      if (dev < 64) allowed[dev] = true;
+    }
+  }
+  kv8_decode_kernel<D, NC, kHalf><<<(unsigned)p.ctas, kThreads, smem, stream>>>(p);
+  return cudaGetLastError();
 }
 
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(128) decode_simple(const Kv8DecodeParams p) {
-  __shared__ float qs[D], ps[128], red[4];
-  __shared__ int64_t pages[2];
-  const int tid = threadIdx.x;
-  int64_t row = blockIdx.x;                       // (b, j, h)
-  const int h = (int)(row % p.H);
-  const int j = (int)(row / p.H % p.Q);
-  const int b = (int)(row / p.H / p.Q);
-  const int kvh = h / p.group;
-  const float kNegInf = __int_as_float(0xff800000);
-  if (tid < D) qs[tid] = widen1<kHalf>(p.q[((int64_t)b * p.Q + j) * p.q_token_stride + h * p.q_head_stride + tid]);
-  const int64_t len = p.seq_lens[b], at = len - p.Q + j;
-  const int64_t from = p.window > 0 && at - p.window + 1 > 0 ? at - p.window + 1 : 0;
-  const int64_t all_from = p.window > 0 && len - p.Q - p.window + 1 > 0 ? len - p.Q - p.window + 1 : 0;
-  float m = kNegInf, l = 0.f, o = 0.f;
-  for (int64_t t0 = all_from / 128 * 128; t0 < len; t0 += 128) {
-    __syncthreads();
-    if (tid < 2) {
-      const int64_t col = t0 / kPageTokens + tid;
-      int64_t page = col < p.max_pages ? p.page_table[(int64_t)b * p.max_pages + col] : -1;
-      if (page < 0 || page >= p.num_pages) {
-        page = -1;
-        if (h == 0 && j == 0 && col * kPageTokens < len && (col + 1) * kPageTokens > all_from && p.status != nullptr)
-          atomicAdd(p.status + NVFP4MLA_STAT_BAD_PAGE, 1);
-      }
-      pages[tid] = page;
-    }
-    __syncthreads();
-    const int64_t t = t0 + tid, page = pages[tid / kPageTokens];
-    const int r = tid % kPageTokens;
-    float z = kNegInf;
-    const bool ok = t >= from && t <= at && t < len && page >= 0;
-    if (ok) {
-      const uint8_t* base = p.cache + page * p.page_bytes;
-      const uint8_t* k = base + kv8_codes_off(p.kv_heads, D, 0, kvh) + r * D;
-      float s = 0.f;
-      for (int d = 0; d < D; ++d) s += qs[d] * code_value(k[d]);
-      z = s * __uint_as_float((uint32_t)base[kv8_scales_off(p.kv_heads, D, kvh) + r / kBlockTokens] << 23) * p.scale_log2;
-    }
-    float top = z;
-    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
-    if ((tid & 31) == 0) red[tid >> 5] = top;
-    __syncthreads();
-    const float m_new = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float base_m = m_new == kNegInf ? 0.f : m_new;
-    const float e = ok ? exp2f(z - base_m) : 0.f;
-    ps[tid] = e;
-    const float keep = exp2f((m == kNegInf ? base_m : m) - base_m);
-    __syncthreads();
-    float lc = 0.f, oc = 0.f;   // the chunk's own sums: a long run of small terms is not added one by one to a large one
-    for (int i = 0; i < 128; ++i) {
-      const int64_t pg = pages[i / kPageTokens];
-      if (pg < 0 || t0 + i < from || t0 + i > at || t0 + i >= len) continue;
-      lc += ps[i];
-      if (tid < D) {
-        const uint8_t* base = p.cache + pg * p.page_bytes;
-        const int ri = i % kPageTokens;
-        oc += ps[i] * (code_value(base[kv8_codes_off(p.kv_heads, D, 1, kvh) + ri * D + tid]) *
-                      __uint_as_float((uint32_t)base[kv8_scales_off(p.kv_heads, D, kvh) + kPageBlocks + ri / kBlockTokens] << 23));
-      }
-    }
-    l = l * keep + lc;
-    o = o * keep + oc;
-    m = m_new;
+cudaError_t launch_columns(const Kv8DecodeParams& p, cudaStream_t stream) {
+  switch (kv8_decode_columns(p.Q, p.group)) {
+    case 8: return launch<D, 8, kHalf>(p, stream);
+    case 16: return launch<D, 16, kHalf>(p, stream);
+    default: return launch<D, 32, kHalf>(p, stream);
   }
-  const bool empty = l == 0.f;
-  const float v = empty ? 0.f : o / l;
-  if (tid < D) {
-    if constexpr (kHalf) p.out[row * D + tid] = __half_as_ushort(__float2half_rn(v));
-    else p.out[row * D + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-  }
-  if (tid == 0) p.lse[row] = empty ? kNegInf : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
 }  // namespace
 
+// Columns of a tile: the softmax's work grows with them, and so does what a key is read for.
+int kv8_decode_columns(int Q, int group) {
+  const int n = Q * group;
+  return n <= 8 ? 8 : (n <= 16 ? 16 : 32);
+}
+
 cudaError_t launch_kv8_decode(const Kv8DecodeParams& p, int head_dim, bool fp16, cudaStream_t stream) {
-  const unsigned blocks = (unsigned)((int64_t)p.B * p.Q * p.H);
-  if (head_dim == 128) {
-    if (fp16) decode_simple<128, true><<<blocks, 128, 0, stream>>>(p);
-    else decode_simple<128, false><<<blocks, 128, 0, stream>>>(p);
-  } else {
-    if (fp16) decode_simple<64, true><<<blocks, 128, 0, stream>>>(p);
-    else decode_simple<64, false><<<blocks, 128, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  if (head_dim == 128) return fp16 ? launch_columns<128, true>(p, stream) : launch_columns<128, false>(p, stream);
+  return fp16 ? launch_columns<64, true>(p, stream) : launch_columns<64, false>(p, stream);
 }
 
 }  // namespace nvfp4mla

@@ -95,16 +95,29 @@ def rows(cache, page_row, length: int, kv_heads: int, head_dim: int):
     return k, v, have
 
 
+def value_scales(cache, page_row, length: int, kv_heads: int, head_dim: int):
+    """The values' scales float64 [Hk, length] (1 where there is no page)."""
+    _, scales = parts(cache, kv_heads, head_dim)
+    s = np.ones((kv_heads, length))
+    for t in range(0, length, BLOCK):
+        page = int(page_row[t // PAGE]) if t // PAGE < len(page_row) else -1
+        if 0 <= page < len(cache):
+            s[:, t:t + BLOCK] = 2.0 ** (scales[page, :, 1, t % PAGE // BLOCK].astype(np.float64) - 127)[:, None]
+    return s
+
+
 def decode(q, cache, page_table, seq_lens, kv_heads: int, scale: float, window: int = 0):
     """out float64 [B, Q, H, D] and lse [B, Q, H] for q float64 [B, Q, H, D], and what rounding bounds
-    are made of: mass = sum_t p_t |v_t| [B, Q, H, D], reach = max_t scale * sum_d |q_d k_td| [B, Q, H]."""
+    are made of: mass = sum_t p_t |v_t| [B, Q, H, D], reach = max_t scale * sum_d |q_d k_td| [B, Q, H],
+    and spread = max_t (p_t s_t) * sum_t |code_t| [B, Q, H, D], s_t and code_t a value's scale and code."""
     B, Q, H, D = q.shape
-    mass, reach = np.zeros(q.shape), np.zeros(q.shape[:3])
+    mass, reach, spread = np.zeros(q.shape), np.zeros(q.shape[:3]), np.zeros(q.shape)
     out = np.zeros(q.shape)
     lse = np.full(q.shape[:3], -np.inf)
     for b in range(B):
         length = max(0, int(seq_lens[b]))
         k, v, have = rows(cache, page_table[b], length, kv_heads, D)
+        s = value_scales(cache, page_table[b], length, kv_heads, D)
         for j in range(Q):
             p = length - Q + j
             t = np.arange(length)
@@ -121,7 +134,8 @@ def decode(q, cache, page_table, seq_lens, kv_heads: int, scale: float, window: 
                     lse[b, j, h] = m + np.log(e.sum())
                     mass[b, j, h] = (e[:, None] * np.abs(v[g][ok])).sum(0) / e.sum()
                     reach[b, j, h] = scale * (np.abs(k[g][ok]) @ np.abs(q[b, j, h])).max()
-    return out, lse, mass, reach
+                    spread[b, j, h] = (e * s[g][ok]).max() / e.sum() * (np.abs(v[g][ok]) / s[g][ok][:, None]).sum(0)
+    return out, lse, mass, reach, spread
 
 
 # ------------------------------------------------------------------ pages

@@ -62,8 +62,13 @@ def check(out, lse, ref, what=""):
     the scalings, by half a step of 2^-24). A weight is off by that, by the exponential's 2^-21, and by its own
     rounding to at least 16 bits (2^-16); the quotient of two such sums by twice as much. The output is then
     rounded once to its type: half a step.
+
+    The 16 bits hold for weights (times their value's scale) that are not far below the largest one. A weight x is
+    held as four E4M3 parts, each a sixteenth of the one before, in units in which the largest is 16 to 256: below
+    2^-6 a part has steps of 2^-9, so the last part's are 2^-9 / 16^3 = 2^-21, half of that is 2^-22, and that is
+    at most 2^-26 of the largest. So a code is added with a weight that is off by 2^-26 of the largest: 2^-26 spread.
     """
-    r_out, r_lse, mass, reach = ref
+    r_out, r_lse, mass, reach, spread = ref
     D = r_out.shape[-1]
     dz = (D + 8) * 2.0 ** -24 * reach
     dw = dz + 2.0 ** -21 + 2.0 ** -16
@@ -72,7 +77,7 @@ def check(out, lse, ref, what=""):
     got, got_lse = f64(out), f64(lse)
     nan = np.isnan(r_out)
     assert np.array_equal(np.isnan(got), nan), f"{what}: NaN in other places"
-    tol = half * np.abs(r_out) + (1 + half) * 2 * dw[..., None] * mass + tiny
+    tol = half * np.abs(r_out) + (1 + half) * (2 * dw[..., None] * mass + 2.0 ** -26 * spread) + tiny
     worst = np.nanmax(np.where(nan, 0, np.abs(got - r_out) / tol)) if got.size else 0
     assert worst <= 1, f"{what}: out off by {worst:.2f} of the bound"
     assert np.array_equal(np.isnan(got_lse), np.isnan(r_lse)), f"{what}: NaN lse in other places"

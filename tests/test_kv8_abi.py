@@ -142,12 +142,13 @@ def test_oracle_append_then_decode_is_plain_attention_of_the_rounded_rows():
     assert np.abs(kk - k.transpose(1, 0, 2)).max() <= 2.0 ** -4 * np.abs(k).max()
     assert np.all(np.abs(vv - v.transpose(1, 0, 2)) <= 2.0 ** -4 * np.abs(v.transpose(1, 0, 2)) + 2.0 ** -9 * np.abs(v).max() / 224)
     q = rng.standard_normal((1, 1, 4, D))
-    out, lse, mass, reach = kv8.decode(q, cache, np.array([[1, 0]]), [n], Hk, 0.125)
+    out, lse, mass, reach, spread = kv8.decode(q, cache, np.array([[1, 0]]), [n], Hk, 0.125)
     z = np.einsum("hd,hnd->hn", q[0, 0], kk.repeat(2, 0)) * 0.125
     p = np.exp(z) / np.exp(z).sum(1, keepdims=True)
     assert np.allclose(out[0, 0], np.einsum("hn,hnd->hd", p, vv.repeat(2, 0)), atol=1e-12)
     assert np.allclose(lse[0, 0], np.log(np.exp(z).sum(1)), atol=1e-12)
     assert (mass >= np.abs(out) - 1e-12).all() and (reach[0, 0] >= np.abs(z).max(1) - 1e-12).all()
+    assert (spread >= mass - 1e-12).all()
 
 
 def test_oracle_scale_byte():

@@ -259,7 +259,7 @@ def test_decode_non_finite_queries():
     ref = [x.copy() for x in c.reference()]
     for b, j, h in ((0, 0, 0), (0, 1, 1), (1, 0, 1)):
         ref[0][b, j, h] = ref[1][b, j, h] = np.nan
-        ref[2][b, j, h] = ref[3][b, j, h] = 0
+        ref[2][b, j, h] = ref[3][b, j, h] = ref[4][b, j, h] = 0
     check(out, lse, ref)
 
 
@@ -361,3 +361,25 @@ def test_decode_repeats_bit_for_bit():
     for _ in range(10):
         again = c.run()
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_decode_waits_are_bounded_and_the_next_calls_are_right():
+    """A step whose tiles never come (a testing flag) gives up after its limit, says so, and leaves workspace
+    and device fit for the next step, a replay of a captured one over the same workspace included."""
+    c = Case([3000, 200], 2, 64, Q=2, G=2, seed=22)
+    ws = torch.zeros(m.kv8_decode_workspace_size(2, 2, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    args = (c.q, dev(c.cache, torch.uint8), dev(c.table), dev(c.lens), 2, c.scale)
+    out, lse = m.kv8_decode(*args, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.kv8_decode(*args, out=out, lse=lse, workspace=ws)
+    status = dev(np.zeros(4))
+    m.kv8_decode(*args, workspace=ws, dev_status=status, test_timeout=True)
+    torch.cuda.synchronize()
+    assert status[2] > 0 and status[[0, 1, 3]].tolist() == [0, 0, 0]
+    for _ in range(2):
+        out.fill_(7)
+        g.replay()
+        check(out, lse, c.reference())
+    check(*m.kv8_decode(*args, workspace=ws), c.reference())
