@@ -90,10 +90,10 @@ struct Control {
   float part_l[2][4][NC];
   uint32_t poison[2][NC][4];           // per stream and column: dims that a NaN value reaches
   float join_m[NC], join_w0[NC], join_w1[NC], join_l[NC];
+  int row[NC];                         // of out and lse, -1: no column
   int any_poison[2];
-  int scan[kThreads / 32];
-  int64_t scan_sum[kThreads / 32];
-  int64_t start_before;                // tiles before request start_b
+  int scan_sum[kThreads / 32];
+  int start_before;                    // tiles before request start_b
   int start_b;
   int last;
   int abort;
@@ -114,9 +114,21 @@ __device__ __forceinline__ void unit_tiles(const Kv8DecodeParams& p, int len, in
   n = last - first;
 }
 
+// The ranges of the CTAs: the first `more` of them are one tile longer. (The host refuses sizes whose
+// tiles could leave 32 bits.)
+struct Ranges {
+  int ctas, each, more;
+  __device__ __forceinline__ Ranges(int total, int n) : ctas(n), each(total / n), more(total - total / n * n) {}
+  __device__ __forceinline__ int begin(int cta) const { return cta * each + min(cta, more); }
+  __device__ __forceinline__ int of(int tile) const {
+    const int longer = more * (each + 1);
+    return tile < longer ? tile / (each + 1) : more + (tile - longer) / each;
+  }
+};
+
 // A walk over the segments of this CTA: per unit, the tiles of it that the CTA has.
 struct Walk {
-  int64_t left;          // tiles of the CTA's range from this segment on
+  int left;              // tiles of the CTA's range from this segment on
   int b, unit, units;    // request, unit inside it, units of a request
   int len, first, n;     // the request's length and a unit's tiles
   int at, count;         // this segment: tiles at .. at + count - 1 of the unit
@@ -126,7 +138,7 @@ struct Walk {
     if (len < 0) len = 0;
     unit_tiles(p, len, first, n);
   }
-  __device__ __forceinline__ void take() { count = (int)min((int64_t)(n - at), left); }
+  __device__ __forceinline__ void take() { count = min(n - at, left); }
   __device__ __forceinline__ void next(const Kv8DecodeParams& p) {
     left -= count;
     if (left <= 0) return;
@@ -188,7 +200,7 @@ __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 // 2^(a - b), 1 for equal infinities.
-__device__ __forceinline__ float ratio(float a, float b) { return a == b ? 1.f : exp2f(a - b); }
+__device__ __forceinline__ float ratio(float a, float b) { return a == b ? 1.f : ex2_approx(a - b); }
 
 template <int D, int NC>
 struct Cta {
@@ -261,22 +273,25 @@ struct Cta {
           if (lane == 0) {
             ok = wait(&ctl->empty[st], (round & 1) ^ 1);
             if (ok) {
-              uint8_t* kt = stages + st * S::kStageBytes;
-              uint8_t* vt = kt + S::kRowBytes;
               ctl->pages_ok[st] = (page0 >= 0 ? 1u : 0u) | (page1 >= 0 ? 2u : 0u);
               mbar_arrive_expect_tx(&ctl->full[st], 2 * S::kRowBytes + (page0 >= 0 ? 16 : 0) + (page1 >= 0 ? 16 : 0));
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int page = h == 0 ? page0 : page1;
-                const int at = page >= 0 ? page : (int)p.num_pages;      // behind the cache: zeros
-                if (page >= 0)
-                  bulk_g2s(&ctl->scales[st][h], p.cache + page * p.page_bytes + kv8_scales_off(p.kv_heads, D, kvh & ~1), 16, &ctl->full[st]);
-                tma_load_4d(kt + h * kPageTokens * D, &p.cache_map, 0, 0, kvh, at, &ctl->full[st]);
-                tma_load_4d(vt + h * kPageTokens * D, &p.cache_map, 0, 0, p.kv_heads + kvh, at, &ctl->full[st]);
-              }
             }
           }
-          if (__shfl_sync(kFull, ok ? 0 : 1, 0)) {
+          ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+          // a lane a copy: keys and values of both pages (a page that is none reads from behind the
+          // cache: zeros), and their scale bytes
+          if (ok && lane < 6) {
+            const int h = lane & 1, page = h == 0 ? page0 : page1;
+            if (lane < 4) {
+              const int v = lane >> 1;
+              tma_load_4d(stages + st * S::kStageBytes + v * S::kRowBytes + h * kPageTokens * D, &p.cache_map, 0, 0,
+                          v * p.kv_heads + kvh, page >= 0 ? page : (int)p.num_pages, &ctl->full[st]);
+            } else if (page >= 0) {
+              bulk_g2s(&ctl->scales[st][h], p.cache + page * p.page_bytes + kv8_scales_off(p.kv_heads, D, kvh & ~1), 16, &ctl->full[st]);
+            }
+          }
+          __syncwarp();
+          if (!ok) {
             drain_copies(g);
             return;
           }
@@ -362,22 +377,26 @@ struct Cta {
       const bool ok = wait(&ctl->q_empty[buf], ((seg >> 1) & 1) ^ 1);
       if (__any_sync(kFull, !ok)) return;
       uint8_t* img = qbuf + buf * S::kQBytes;
-      constexpr int kRounds = NC / kCols, kBatch = kRounds < 4 ? kRounds : 4;
-      for (int r0 = 0; r0 < kRounds; r0 += kBatch) {
-        uint4 v[kBatch];
+      constexpr int kRounds = NC / kCols, kAhead = kRounds < 4 ? kRounds : 4;
+      auto load = [&](int round) {
+        const int col = ct * NC + round * kCols + sub;
+        if (round >= kRounds || col >= ncols) return make_uint4(0u, 0u, 0u, 0u);
+        const int j = col / p.group, h = kvh * p.group + col - j * p.group;
+        return __ldg(reinterpret_cast<const uint4*>(p.q + ((int64_t)w.b * p.Q + j) * p.q_token_stride + h * p.q_head_stride + ch * 8));
+      };
+      // four rounds' loads in flight, one round's code
+      uint4 v[kAhead];
 #pragma unroll
-        for (int r = 0; r < kBatch; ++r) {
-          const int col = ct * NC + (r0 + r) * kCols + sub;
-          v[r] = make_uint4(0u, 0u, 0u, 0u);
-          if (col < ncols) {
-            const int j = col / p.group, h = kvh * p.group + col % p.group;
-            v[r] = __ldg(reinterpret_cast<const uint4*>(p.q + ((int64_t)w.b * p.Q + j) * p.q_token_stride + h * p.q_head_stride + ch * 8));
-          }
-        }
+      for (int r = 0; r < kAhead; ++r) v[r] = load(r);
+#pragma unroll 1
+      for (int r = 0; r < kRounds; ++r) {
+        const uint4 x4 = v[0];
 #pragma unroll
-        for (int r = 0; r < kBatch; ++r) {
-          const int c = (r0 + r) * kCols + sub, col = ct * NC + c;
-          const uint32_t ws[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
+        for (int k = 0; k + 1 < kAhead; ++k) v[k] = v[k + 1];
+        v[kAhead - 1] = load(r + kAhead);
+        {
+          const int c = r * kCols + sub, col = ct * NC + c;
+          const uint32_t ws[4] = {x4.x, x4.y, x4.z, x4.w};
           uint32_t top = 0;
 #pragma unroll
           for (int k = 0; k < 4; ++k) top = __vmaxu2(top, ws[k] & 0x7FFF7FFFu);
@@ -454,16 +473,14 @@ struct Cta {
   }
 
   // Leaves this CTA's partial results of a shared unit as counted; true for the last to come.
-  __device__ bool arrive(const Walk& w, int64_t base, int64_t total, int64_t ctas) {
-    const int64_t g0 = base, g1 = base + w.n - 1;
-    const int64_t c_lo = ((g0 + 1) * ctas - 1) / total, c_hi = ((g1 + 1) * ctas - 1) / total;
+  __device__ bool arrive(int c_lo, int c_hi) {
     unsigned long long* at = reinterpret_cast<unsigned long long*>(p.arrived + c_lo);
     const unsigned long long tag = p.tag;
-    unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(at);
+    unsigned long long old = 0;          // what a finished call leaves: right for the first to come
     for (;;) {
       // a count of another call (or whatever the workspace held before) counts as none
-      const unsigned long long have = (old & ~0xFFFFull) == tag ? (old & 0xFFFF) : 0;
-      const bool last = (int64_t)have + 1 == c_hi - c_lo + 1;
+      const unsigned have = (old & ~0xFFFFull) == tag ? (unsigned)(old & 0xFFFF) : 0u;
+      const bool last = have + 1 == (unsigned)(c_hi - c_lo + 1);
       const unsigned long long now = atomicCAS(at, old, last ? 0ull : (tag | (have + 1)));
       if (now == old) return last;
       old = now;
@@ -476,15 +493,67 @@ struct Cta {
     else p.out[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
   }
 
+  // One column's result of dim d, from the maximum, the sum and the weighted sum.
   template <bool kHalf>
-  __device__ void softmax(Walk w, uint32_t tmem, int64_t t_begin, int64_t total, int64_t ctas) {
+  __device__ __forceinline__ void finish(int row, int d, float m, float sum, float acc) {
+    if (row < 0) return;
+    put<kHalf>((int64_t)row * D + d, sum == 0.f ? 0.f : acc / sum);
+    if (d == 0) p.lse[row] = sum == 0.f ? neg_inf() : (m + log2f(sum)) * 0.69314718055994530942f;
+  }
+
+  // Joins the partial results that CTAs c_lo .. c_hi left of a unit, for dim d of the columns from
+  // `from` on: four columns of four partial results at a time, every load of them in flight together.
+  template <bool kHalf>
+  __device__ void join(int from, int d, int c_lo, int c_hi, int first) {
+#pragma unroll 1
+    for (int c = from; c < from + NC / 2; c += 4) {
+      if (ctl->row[c] < 0) break;
+      float m[4], sum[4], acc[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        m[k] = neg_inf();
+        sum[k] = acc[k] = 0.f;
+      }
+#pragma unroll 1
+      for (int s0 = c_lo; s0 <= c_hi; s0 += 4) {
+        float o[4][4];
+        float4 ml[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (s0 + i > c_hi) break;
+          const int at = (2 * (s0 + i) + (s0 + i == c_lo ? first : 0)) * NC + c;
+          ml[i][0] = __ldcg(reinterpret_cast<const float4*>(p.part_ml + at * 2));
+          ml[i][1] = __ldcg(reinterpret_cast<const float4*>(p.part_ml + at * 2) + 1);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[i][k] = __ldcg(p.part_o + (int64_t)(at + k) * D + d);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (s0 + i > c_hi) break;
+          const float ms[4] = {ml[i][0].x, ml[i][0].z, ml[i][1].x, ml[i][1].z}, ls[4] = {ml[i][0].y, ml[i][0].w, ml[i][1].y, ml[i][1].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float m_new = fmaxf(m[k], ms[k]), keep = ratio(m[k], m_new), in = ratio(ms[k], m_new);
+            sum[k] = sum[k] * keep + ls[k] * in;
+            acc[k] = acc[k] * keep + o[i][k] * in;
+            m[k] = m_new;
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) finish<kHalf>(ctl->row[c + k], d, m[k], sum[k], acc[k]);
+    }
+  }
+
+  template <bool kHalf>
+  __device__ void softmax(Walk w, uint32_t tmem, const Ranges& ranges) {
     const int wg = (threadIdx.x >> 7) - 1;                // 0, 1: the stream
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, r = threadIdx.x & 127;
     const uint32_t quarter = tmem + ((uint32_t)(warp * 32) << 16);
     const uint32_t s_at = quarter + wg * S::kNS, o_at = quarter + 2 * S::kNS + wg * S::kNO;
     const int cts = col_tiles(), ncols = p.Q * p.group;
-    const int64_t t_first = t_begin;
-    int64_t done = t_begin;                               // tiles of the whole sequence before this segment
+    const int t_first = ranges.begin(blockIdx.x);
+    int done = t_first;                                   // tiles of the whole sequence before this segment
     uint32_t g = 0, uses = 0;
     uint32_t last_tile = 0;
     bool has_last = false;
@@ -639,18 +708,26 @@ struct Cta {
         ok = ok && wait(&ctl->empty[a % S::kStages], (a / S::kStages) & 1);
         if (n >= 2) ok = ok && wait(&ctl->empty[b % S::kStages], (b / S::kStages) & 1);
         tc_fence_after();
+        // sums over the warp's tokens: halves of the columns go to halves of the lanes, until a lane has one
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
+        for (int step = 0; step < 5; ++step) {
+          const int half = NC >> (step + 1), d = 16 >> step;
 #pragma unroll
-          for (int d = 16; d > 0; d >>= 1) l[c] += __shfl_xor_sync(kFull, l[c], d);
-          if (lane == 0) ctl->part_l[wg][warp][c] = l[c];
+          for (int c = 0; c < half; ++c) {
+            const bool up = (lane & d) != 0;
+            const float give = up ? l[c] : l[c + half], keep = up ? l[c + half] : l[c];
+            l[c] = keep + __shfl_xor_sync(kFull, give, d);
+          }
+          if (half == 0) l[0] += __shfl_xor_sync(kFull, l[0], d);
         }
+        // the lane's highest bits say which column: bit 4 halves NC, bit 3 a quarter, ...
+        if (NC == 32 || (lane & (32 / NC - 1)) == 0) ctl->part_l[wg][warp][NC == 32 ? lane : lane / (32 / NC)] = l[0];
       }
       if (bar_any(3, 256, stop || !ok)) {
         // gave up: the counts of the units that this CTA shares still come out even
         if (wg == 0 && r == 0)
           for (; w.left > 0; done += w.count, w.next(p))
-            if (!w.whole()) arrive(w, done - w.at, total, ctas);
+            if (!w.whole()) arrive(ranges.of(done - w.at), ranges.of(done - w.at + w.n - 1));
         return;
       }
       g += n;
@@ -668,84 +745,56 @@ struct Cta {
         ctl->join_l[c] = l0 * ratio(m0, m) + l1 * ratio(m1, m);
         ctl->join_w0[c] = w0 == neg_inf() ? 0.f : exp2f(w0 - kWeightScale - m);
         ctl->join_w1[c] = w1 == neg_inf() ? 0.f : exp2f(w1 - kWeightScale - m);
+        const int col = ct * NC + c, j = col / p.group;
+        ctl->row[c] = col < ncols ? (w.b * p.Q + j) * p.H + kvh * p.group + (col - j * p.group) : -1;
       }
       bar_sync(1 + wg, 128);
       __syncwarp();
       const int d = D == 128 ? r : (lane < 16 ? warp * 16 + lane : -1);     // M = 64 fills 16 lanes of each quarter
       const bool full_unit = w.whole();
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (done == t_first ? 0 : 1);
-      const int64_t row0 = (int64_t)w.b * p.Q;
+      const int slot = 2 * (int)blockIdx.x + (done == t_first ? 0 : 1);
       const bool poisoned = ctl->any_poison[0] | ctl->any_poison[1];
-#pragma unroll
-      for (int c0 = 0; c0 < kHalfCols; c0 += 4) {
-        float acc[4];
-#pragma unroll
-        for (int stream = 0; stream < 2; ++stream) {
-          if (stream == 1 && n < 2) break;
+      // four columns a round; kept as a loop, as code that runs once costs what its fetching costs
+#pragma unroll 1
+      for (int c = wg * kHalfCols; c < wg * kHalfCols + kHalfCols; c += 4) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int stream = 0; stream < min(n, 2); ++stream) {
           uint32_t o[kWParts][4];
 #pragma unroll
-          for (int k = 0; k < kWParts; ++k) tmem_ld4(quarter + 2 * S::kNS + stream * S::kNO + k * NC + wg * kHalfCols + c0, o[k]);
+          for (int k = 0; k < kWParts; ++k) tmem_ld4(quarter + 2 * S::kNS + stream * S::kNO + k * NC + c, o[k]);
           tmem_wait_ld();
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int c = wg * kHalfCols + c0 + k;
             float x = __uint_as_float(o[3][k]);
             x = fmaf(x, 1.f / 16.f, __uint_as_float(o[2][k]));
             x = fmaf(x, 1.f / 16.f, __uint_as_float(o[1][k]));
             x = fmaf(x, 1.f / 16.f, __uint_as_float(o[0][k]));
-            if (poisoned && d >= 0 && ((ctl->poison[stream][c][d >> 5] >> (d & 31)) & 1)) x = __int_as_float(0x7fc00000);
-            acc[k] = stream == 0 ? x * ctl->join_w0[c] : fmaf(x, ctl->join_w1[c], acc[k]);
+            if (poisoned && d >= 0 && ((ctl->poison[stream][c + k][d >> 5] >> (d & 31)) & 1)) x = __int_as_float(0x7fc00000);
+            acc[k] = fmaf(x, stream == 0 ? ctl->join_w0[c + k] : ctl->join_w1[c + k], acc[k]);
           }
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int c = wg * kHalfCols + c0 + k, col = ct * NC + c;
-          if (d < 0 || col >= ncols) continue;
-          if (full_unit) {
-            const float sum = ctl->join_l[c];
-            const int64_t row = (row0 + col / p.group) * p.H + kvh * p.group + col % p.group;
-            put<kHalf>(row * D + d, sum == 0.f ? 0.f : acc[k] / sum);
-            if (d == 0) p.lse[row] = sum == 0.f ? neg_inf() : (ctl->join_m[c] + log2f(sum)) * 0.69314718055994530942f;
-          } else {
-            p.part_o[(slot * NC + c) * D + d] = acc[k];
-            if (d == 0) {
-              p.part_ml[(slot * NC + c) * 2] = ctl->join_m[c];
-              p.part_ml[(slot * NC + c) * 2 + 1] = ctl->join_l[c];
-            }
-          }
+          if (d < 0) continue;
+          if (full_unit) finish<kHalf>(ctl->row[c + k], d, ctl->join_m[c + k], ctl->join_l[c + k], acc[k]);
+          else p.part_o[(int64_t)(slot * NC + c + k) * D + d] = acc[k];
         }
       }
       if (!full_unit) {
-        __threadfence();
+        if (r < kHalfCols) {
+          const int c = wg * kHalfCols + r;
+          *reinterpret_cast<float2*>(p.part_ml + (slot * NC + c) * 2) = make_float2(ctl->join_m[c], ctl->join_l[c]);
+        }
+        const int base = done - w.at, c_lo = ranges.of(base), c_hi = ranges.of(base + w.n - 1);
         bar_sync(3, 256);
         if (wg == 0 && r == 0) {
-          ctl->last = arrive(w, done - w.at, total, ctas) ? 1 : 0;
+          __threadfence();
+          ctl->last = arrive(c_lo, c_hi) ? 1 : 0;
           __threadfence();
         }
         bar_sync(3, 256);
-        if (ctl->last) {
-          const int64_t base = done - w.at;
-          const int64_t c_lo = ((base + 1) * ctas - 1) / total, c_hi = ((base + w.n) * ctas - 1) / total;
-          const int64_t slot_lo = 2 * c_lo + (c_lo * total / ctas == base ? 0 : 1);
-          if (d >= 0) {
-            for (int c = wg * kHalfCols; c < wg * kHalfCols + kHalfCols && ct * NC + c < ncols; ++c) {
-              const int col = ct * NC + c;
-              float m = neg_inf(), sum = 0.f, acc = 0.f;
-              for (int64_t k = c_lo; k <= c_hi; ++k) {
-                const int64_t sl = k == c_lo ? slot_lo : 2 * k;
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (sl * NC + c) * 2));
-                const float o = __ldcg(p.part_o + (sl * NC + c) * D + d);
-                const float m_new = fmaxf(m, ml.x), keep = ratio(m, m_new), in = ratio(ml.x, m_new);
-                sum = sum * keep + ml.y * in;
-                acc = acc * keep + o * in;
-                m = m_new;
-              }
-              const int64_t row = (row0 + col / p.group) * p.H + kvh * p.group + col % p.group;
-              put<kHalf>(row * D + d, sum == 0.f ? 0.f : acc / sum);
-              if (d == 0) p.lse[row] = sum == 0.f ? neg_inf() : (m + log2f(sum)) * 0.69314718055994530942f;
-            }
-          }
-        }
+        if (ctl->last && d >= 0) join<kHalf>(wg * kHalfCols, d, c_lo, c_hi, ranges.begin(c_lo) == base ? 0 : 1);
       }
       // the next segment starts from nothing
       bar_sync(3, 256);
@@ -807,36 +856,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const __grid_co
   const int units = p.kv_heads * ((p.Q * p.group + NC - 1) / NC);
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  int64_t sum = 0;
+  int sum = 0;
   for (int b = b0; b < b1; ++b) {
     int first, n;
     unit_tiles(p, max(0, __ldg(p.seq_lens + b)), first, n);
     sum += n;
   }
-  int64_t incl = sum;
+  int incl = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int64_t o = __shfl_up_sync(kFull, incl, d);
+    const int o = __shfl_up_sync(kFull, incl, d);
     if (lane >= d) incl += o;
   }
   if (lane == 31) ctl->scan_sum[warp] = incl;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int64_t before = 0, all = 0;
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) before += ctl->scan_sum[i];
-    all += ctl->scan_sum[i];
-  }
-  before += incl - sum;
-  const int64_t total = all * units;
+  const int of_warp = lane < kThreads / 32 ? ctl->scan_sum[lane] : 0;
+  const int before = __reduce_add_sync(kFull, lane < warp ? of_warp : 0) + incl - sum;
+  const int total = __reduce_add_sync(kFull, of_warp) * units;
   // no CTA gets less than one tile for each of its two streams: joining costs more than a tile
-  const int64_t ctas = min((int64_t)gridDim.x, (total + kMinTiles - 1) / kMinTiles);
-  const int64_t cta = blockIdx.x;
-  const int64_t t_begin = cta < ctas ? cta * total / ctas : 0, t_end = cta < ctas ? (cta + 1) * total / ctas : 0;
+  const Ranges ranges(total, min((int)gridDim.x, (total + kMinTiles - 1) / kMinTiles));
+  const int cta = blockIdx.x;
+  const int t_begin = ranges.begin(cta), t_end = cta < ranges.ctas ? ranges.begin(cta + 1) : t_begin;
   if (t_begin < t_end && before * units <= t_begin && t_begin < (before + sum) * units) {
-    int b = b0;
-    int64_t at = before;
+    int b = b0, at = before;
     for (;; ++b) {
       int first, n;
       unit_tiles(p, max(0, __ldg(p.seq_lens + b)), first, n);
@@ -853,9 +897,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const __grid_co
   if (w.left > 0) {
     w.b = ctl->start_b;
     w.load(p);
-    const int64_t in = t_begin - ctl->start_before;
-    w.unit = (int)(in / w.n);
-    w.at = (int)(in % w.n);
+    const int in = t_begin - ctl->start_before;
+    w.unit = in / w.n;
+    w.at = in - w.unit * w.n;
     w.take();
     const uint32_t tmem = ctl->tmem_base;
     Cta<D, NC> c{p, stages, qbuf, wbuf, ctl};
@@ -870,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const __grid_co
       if (lane == 0) c.issue_o(w, tmem);
       __syncwarp();
     } else {
-      c.template softmax<kHalf>(w, tmem, t_begin, total, ctas);
+      c.template softmax<kHalf>(w, tmem, ranges);
     }
   }
   tc_fence_before();
