@@ -20,12 +20,15 @@
 //
 // One CTA per SM, persistent. The tiles of all (request, key/value head, column tile) units form
 // one sequence, found by every CTA from the lengths, and each CTA takes one contiguous range of it.
-//   warp 0     producer: page numbers a group of 16 tiles ahead, then per tile four 64-row TMA boxes
-//              and the scale bytes into a ring of stages
+//   warp 0     producer: page numbers a group of tiles ahead, then per stage (128 rows of 128 bytes
+//              of K and of V) the TMA boxes of its pages and their scale bytes into a ring
 //   warp 1     issues S = K q;  warp 3: issues O += V w (two threads, so that neither waits for the other)
 //   warp 2     queries of the next unit: scaling by a power of two, parts, two buffers
-//   warps 4-7  softmax of the range's even tiles, warps 8-11 of the odd ones (thread = token): each
-//              stream has its own S, w and O, and keeps its own M, m, l; they are added at the unit's end
+//   warps 4-7  softmax of one stream of tiles, warps 8-11 of the other (thread = token): each stream
+//              has its own S, w and O, and keeps its own M, m, l; they are added at the unit's end
+// With 128 dims the streams take the stages in turn. With 64 dims a 128-byte row is two tokens (TMA
+// takes a cycle or so per row, and 64-byte rows would halve its rate): a stage is 256 tokens, the even
+// ones the one stream's and the odd ones the other's, whose operands start 64 bytes into the rows.
 // A unit that several CTAs share is joined by whichever of them finishes last: the others leave
 // (m, l, O) in the workspace and count themselves.
 #include <cuda_bf16.h>
@@ -43,11 +46,9 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kTile = 128;             // tokens per tile: two pages
+constexpr int kRows = 128;             // 128-byte rows of K or V in a stage: a token each, or two of 64 dims
 constexpr int kQParts = 3, kWParts = 4;
 constexpr int kThreads = 384;
-constexpr int kGroup = 16;             // tiles whose page numbers are read together
-constexpr int kMinTiles = 2;           // of a CTA: one for each stream
 constexpr float kHeadroom = 4.f;       // log2: how far above the reference a weight's exponent may come
 constexpr float kWeightScale = 4.f;    // log2: weights are held times 16, so that 2^4 above it is 256 <= 448
 constexpr float kSumHeadroom = 60.f;   // log2: the same for the sum, which fp32 holds
@@ -56,30 +57,38 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 // Sizes of the instance with D dims and NC columns.
 template <int D, int NC>
 struct Shape {
+  static constexpr bool kPair = D == 64;                        // a row is two tokens: one of each stream
+  static constexpr int kTile = kPair ? 256 : 128;               // tokens of a stage
+  static constexpr int kPages = kTile / kPageTokens;
+  static constexpr int kPageRows = kRows / kPages;
+  static constexpr int kGroup = 32 / kPages;                    // stages whose page numbers are read together
+  static constexpr int kMinTiles = kPair ? 1 : 2;               // of a CTA: work for both streams
   static constexpr int kNS = (kQParts * NC + 15) / 16 * 16;     // columns of S
   static constexpr int kNO = kWParts * NC;                      // columns of O, bytes of a row of w
-  static constexpr int kRowBytes = kTile * D;                   // K or V of a tile
-  static constexpr int kScaleOff = 2 * kRowBytes;
+  static constexpr int kRowBytes = kRows * 128;                 // K or V of a stage
   static constexpr int kStageBytes = 2 * kRowBytes;             // the scale bytes have an area of their own
   static constexpr int kQBytes = (kNS * D + 1023) / 1024 * 1024;
-  static constexpr int kWBytes = kTile * kNO;
+  static constexpr int kWBytes = kRows * kNO;
   static constexpr int kBudget = 232448 - 1024 - 8192;          // less alignment and the control block
   static constexpr int kFit = (kBudget - 2 * kQBytes - 2 * kWBytes) / kStageBytes;
   static constexpr int kStages = kFit < 12 ? kFit : 12;
-  static constexpr int kUsed = 2 * kNS + 2 * kNO;               // TMEM columns
+  static constexpr int kBufs = 4 * kNS + 2 * kNO <= 512 ? 2 : 1;   // S of the next tile while this one's is read
+  static constexpr int kOCol = 2 * kBufs * kNS;                 // TMEM columns: S of both streams, then O
+  static constexpr int kUsed = kOCol + 2 * kNO;
   static constexpr uint32_t kTmem = kUsed <= 128 ? 128 : (kUsed <= 256 ? 256 : 512);
-  static constexpr uint32_t kSwK = D == 128 ? SW_128B : SW_64B;
+  static constexpr uint32_t kSwQ = D == 128 ? SW_128B : SW_64B;
   static constexpr uint32_t kSwW = kNO == 128 ? SW_128B : (kNO == 64 ? SW_64B : SW_32B);
   static_assert(kUsed <= 512 && kStages >= 3, "fits");
 };
 
-template <int NC, int kStages>
+template <int NC, int kStages, int kPages>
 struct Control {
   uint64_t full[kStages], empty[kStages];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], w_full[2];
+  uint64_t s_full[2][2], w_full[2][2]; // per stream and buffer of S
+  uint64_t o_done[2];
   uint64_t drain[2];
-  uint4 scales[kStages][2];            // per page: the scale bytes of two neighbouring heads
+  uint4 scales[kStages][kPages];       // per page: the scale bytes of two neighbouring heads
   uint32_t pages_ok[kStages];          // bit per page: it is one
   alignas(16) float f[2][NC];          // read four at a time, as M and m are: per query buffer: score of a column per unit of S, log2 units
   int hi[2][NC], lo[2][NC];            // positions that a column attends to
@@ -102,9 +111,11 @@ struct Control {
 
 // Tiles of one unit of a request with `len` tokens: [first, first + n). A unit has at least one, so
 // that a request without tokens is written too.
+template <int kTile>
 __device__ __forceinline__ void unit_tiles(const Kv8DecodeParams& p, int len, int& first, int& n) {
+  constexpr int kPages = kTile / kPageTokens;
   const int64_t pages = min((int64_t)(len + (int64_t)kPageTokens - 1) / kPageTokens, p.max_pages);
-  int last = len > 0 ? (int)((pages + 1) / 2) : 1;
+  int last = len > 0 ? (int)((pages + kPages - 1) / kPages) : 1;
   first = 0;
   if (p.window > 0) {
     const int64_t from = (int64_t)len - p.Q - p.window + 1;
@@ -127,6 +138,7 @@ struct Ranges {
 };
 
 // A walk over the segments of this CTA: per unit, the tiles of it that the CTA has.
+template <int kTile>
 struct Walk {
   int left;              // tiles of the CTA's range from this segment on
   int b, unit, units;    // request, unit inside it, units of a request
@@ -136,7 +148,7 @@ struct Walk {
   __device__ __forceinline__ void load(const Kv8DecodeParams& p) {
     len = __ldg(p.seq_lens + b);
     if (len < 0) len = 0;
-    unit_tiles(p, len, first, n);
+    unit_tiles<kTile>(p, len, first, n);
   }
   __device__ __forceinline__ void take() { count = min(n - at, left); }
   __device__ __forceinline__ void next(const Kv8DecodeParams& p) {
@@ -205,7 +217,8 @@ __device__ __forceinline__ float ratio(float a, float b) { return a == b ? 1.f :
 template <int D, int NC>
 struct Cta {
   using S = Shape<D, NC>;
-  using Ctl = Control<NC, S::kStages>;
+  using Ctl = Control<NC, S::kStages, S::kPages>;
+  using Walk = ::nvfp4mla::Walk<S::kTile>;
   const Kv8DecodeParams& p;
   uint8_t* stages;
   uint8_t* qbuf;
@@ -222,12 +235,12 @@ struct Cta {
   __device__ __forceinline__ int col_tiles() const { return (p.Q * p.group + NC - 1) / NC; }
 
   // ---------------------------------------------------------------- producer (warp 0)
-  // Page numbers of tiles i .. i + 15 of the segment: two lanes a tile. -1: not needed, or none.
+  // Page numbers of a group of tiles from i on: a lane a page. -1: not needed, or none.
   __device__ __forceinline__ int load_pages(const Walk& w, int i, int ct, int kvh) {
     const int lane = threadIdx.x & 31;
-    const int tile = i + (lane >> 1);
+    const int tile = i + lane / S::kPages;
     if (tile >= w.count) return -1;
-    const int64_t col = 2 * ((int64_t)w.first + w.at + tile) + (lane & 1);
+    const int64_t col = S::kPages * ((int64_t)w.first + w.at + tile) + lane % S::kPages;
     const int64_t from = p.window > 0 ? (int64_t)w.len - p.Q - p.window + 1 : 0;
     if (col * kPageTokens >= w.len || (col + 1) * kPageTokens <= from) return -1;
     int page = -1;
@@ -256,40 +269,37 @@ struct Cta {
         if (from < p.max_pages) from = p.max_pages;
         if (need > from) atomicAdd(p.status + NVFP4MLA_STAT_BAD_PAGE, (int)(need - from));
       }
-      for (int i = 0; i < w.count; i += kGroup) {
+      for (int i = 0; i < w.count; i += S::kGroup) {
         const int mine = pages;
-        if (i + kGroup < w.count) {
-          pages = load_pages(w, i + kGroup, ct, kvh);
+        if (i + S::kGroup < w.count) {
+          pages = load_pages(w, i + S::kGroup, ct, kvh);
         } else {
           Walk nx = w;
           nx.next(p);
           pages = nx.left > 0 ? load_pages(nx, 0, nx.unit % cts, nx.unit / cts) : -1;
         }
-        const int m = min(kGroup, w.count - i);
+        const int m = min(S::kGroup, w.count - i);
         for (int k = 0; k < m; ++k, ++g) {
-          const int page0 = __shfl_sync(kFull, mine, 2 * k), page1 = __shfl_sync(kFull, mine, 2 * k + 1);
+          // a lane a copy: keys, values and scale bytes of every page (the codes of a page that is
+          // none read from behind the cache: zeros)
+          const int what = lane / S::kPages, h = lane % S::kPages;
+          const int page = __shfl_sync(kFull, mine, S::kPages * k + h);
+          const uint32_t have = __ballot_sync(kFull, page >= 0) & ((1u << S::kPages) - 1);
           const uint32_t st = g % S::kStages, round = g / S::kStages;
           bool ok = true;
           if (lane == 0) {
             ok = wait(&ctl->empty[st], (round & 1) ^ 1);
             if (ok) {
-              ctl->pages_ok[st] = (page0 >= 0 ? 1u : 0u) | (page1 >= 0 ? 2u : 0u);
-              mbar_arrive_expect_tx(&ctl->full[st], 2 * S::kRowBytes + (page0 >= 0 ? 16 : 0) + (page1 >= 0 ? 16 : 0));
+              ctl->pages_ok[st] = have;
+              mbar_arrive_expect_tx(&ctl->full[st], 2 * S::kRowBytes + 16 * __popc(have));
             }
           }
           ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
-          // a lane a copy: keys and values of both pages (a page that is none reads from behind the
-          // cache: zeros), and their scale bytes
-          if (ok && lane < 6) {
-            const int h = lane & 1, page = h == 0 ? page0 : page1;
-            if (lane < 4) {
-              const int v = lane >> 1;
-              tma_load_4d(stages + st * S::kStageBytes + v * S::kRowBytes + h * kPageTokens * D, &p.cache_map, 0, 0,
-                          v * p.kv_heads + kvh, page >= 0 ? page : (int)p.num_pages, &ctl->full[st]);
-            } else if (page >= 0) {
-              bulk_g2s(&ctl->scales[st][h], p.cache + page * p.page_bytes + kv8_scales_off(p.kv_heads, D, kvh & ~1), 16, &ctl->full[st]);
-            }
-          }
+          if (ok && what < 2)
+            tma_load_4d(stages + st * S::kStageBytes + what * S::kRowBytes + h * kPageTokens * D, &p.cache_map, 0, 0,
+                        what * p.kv_heads + kvh, page >= 0 ? page : (int)p.num_pages, &ctl->full[st]);
+          else if (ok && what == 2 && page >= 0)
+            bulk_g2s(&ctl->scales[st][h], p.cache + page * p.page_bytes + kv8_scales_off(p.kv_heads, D, kvh & ~1), 16, &ctl->full[st]);
           __syncwarp();
           if (!ok) {
             drain_copies(g);
@@ -316,24 +326,27 @@ struct Cta {
   // ---------------------------------------------------------------- S = K q (warp 1, one thread)
   __device__ void issue_s(Walk w, uint32_t tmem) {
     constexpr uint32_t kId = idesc_e4m3(128, S::kNS, false, false);
-    const uint64_t kd = sdesc(smem_u32(stages), 16, 8 * D, S::kSwK), qd = sdesc(smem_u32(qbuf), 16, 8 * D, S::kSwK);
+    const uint64_t kd = sdesc(smem_u32(stages), 16, 1024, SW_128B), qd = sdesc(smem_u32(qbuf), 16, 8 * D, S::kSwQ);
     uint32_t g = 0, uses[2] = {0, 0};
     bool ok = true;
     for (uint32_t seg = 0; ok && w.left > 0; ++seg, w.next(p)) {
       const uint32_t buf = seg & 1;
       ok = wait(&ctl->q_full[buf], (seg >> 1) & 1);
       for (int i = 0; ok && i < w.count; ++i, ++g) {
-        const uint32_t st = g % S::kStages, stream = i & 1;
+        const uint32_t st = g % S::kStages;
         ok = wait(&ctl->full[st], (g / S::kStages) & 1);
-        // the stream's last S has been read once its weights are written
-        if (ok && uses[stream] > 0) ok = wait(&ctl->w_full[stream], (uses[stream] - 1) & 1);
-        if (!ok) break;
-        ++uses[stream];
-        tc_fence_after();
+        for (int stream = S::kPair ? 0 : i & 1; ok && stream <= (S::kPair ? 1 : i & 1); ++stream) {
+          const uint32_t u = uses[stream]++, sb = u % S::kBufs, turn = u / S::kBufs;
+          // this buffer's last S has been read once its weights are written
+          if (turn > 0) ok = wait(&ctl->w_full[stream][sb], (turn - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t from = st * S::kStageBytes + (S::kPair ? stream * 64 : 0);   // a row's first or second token
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k)
-          umma_f8_ss(tmem + stream * S::kNS, kd + ((st * S::kStageBytes + k * 32) >> 4), qd + ((buf * S::kQBytes + k * 32) >> 4), kId, k > 0);
-        umma_commit(&ctl->s_full[stream]);
+          for (int k = 0; k < D / 32; ++k)
+            umma_f8_ss(tmem + (stream * S::kBufs + sb) * S::kNS, kd + ((from + k * 32) >> 4), qd + ((buf * S::kQBytes + k * 32) >> 4), kId, k > 0);
+          umma_commit(&ctl->s_full[stream][sb]);
+        }
       }
       if (ok) umma_commit(&ctl->q_empty[buf]);
     }
@@ -344,21 +357,25 @@ struct Cta {
   // ---------------------------------------------------------------- O += V w (warp 3, one thread)
   __device__ void issue_o(Walk w, uint32_t tmem) {
     constexpr uint32_t kId = idesc_e4m3(D, S::kNO, true, true);
-    const uint64_t vd = sdesc(smem_u32(stages + S::kRowBytes), 16, 8 * D, S::kSwK), wd = sdesc(smem_u32(wbuf), 16, 8 * S::kNO, S::kSwW);
+    const uint64_t vd = sdesc(smem_u32(stages + S::kRowBytes), 16, 1024, SW_128B), wd = sdesc(smem_u32(wbuf), 16, 8 * S::kNO, S::kSwW);
     uint32_t g = 0, uses[2] = {0, 0};
     bool ok = true;
     for (; ok && w.left > 0; w.next(p)) {
       for (int i = 0; ok && i < w.count; ++i, ++g) {
-        const uint32_t st = g % S::kStages, stream = i & 1;
-        ok = wait(&ctl->w_full[stream], uses[stream] & 1);
-        if (!ok) break;
-        ++uses[stream];
-        tc_fence_after();
+        const uint32_t st = g % S::kStages;
+        for (int stream = S::kPair ? 0 : i & 1; ok && stream <= (S::kPair ? 1 : i & 1); ++stream) {
+          const uint32_t u = uses[stream]++;
+          ok = wait(&ctl->w_full[stream][u % S::kBufs], (u / S::kBufs) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t from = st * S::kStageBytes + (S::kPair ? stream * 64 : 0);
 #pragma unroll
-        for (int k = 0; k < kTile / 32; ++k)
-          umma_f8_ss(tmem + 2 * S::kNS + stream * S::kNO, vd + ((st * S::kStageBytes + k * 32 * D) >> 4),
-                     wd + ((stream * S::kWBytes + k * 32 * S::kNO) >> 4), kId, i > 1 || k > 0);
-        umma_commit(&ctl->empty[st]);
+          for (int k = 0; k < kRows / 32; ++k)
+            umma_f8_ss(tmem + S::kOCol + stream * S::kNO, vd + ((from + k * 32 * 128) >> 4),
+                       wd + ((stream * S::kWBytes + k * 32 * S::kNO) >> 4), kId, i > (S::kPair ? 0 : 1) || k > 0);
+          umma_commit(&ctl->o_done[stream]);
+          umma_commit(&ctl->empty[st]);
+        }
       }
     }
     umma_commit(&ctl->drain[1]);
@@ -437,37 +454,31 @@ struct Cta {
   }
 
   // ---------------------------------------------------------------- softmax (warps 4-11)
-  // Rows of V that no column attends to become zeros (they may hold anything), and a NaN in a row
-  // that only some columns attend to is taken out and noted for those.
-  __device__ void clean_row(uint8_t* vt, int r, int t, bool page_ok, uint32_t buf, int stream, int cols) {
-    bool any = false, all = true;
-    for (int c = 0; c < cols; ++c) {
-      const bool in = page_ok && t <= ctl->hi[buf][c] && t >= ctl->lo[buf][c];
-      any |= in;
-      all &= in;
-    }
-    uint4* row = reinterpret_cast<uint4*>(vt + r * D);
-    if (!any) {
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
-    } else if (!all) {
-      for (int i = 0; i < D / 16; ++i) {
-        const uint4 x = row[i];
-        const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
-        uint32_t nan = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) nan |= __vcmpeq4(ws[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-        if (nan == 0) continue;
-        const int chunk = D == 128 ? (i ^ (r & 7)) : (i ^ ((r >> 1) & 3));
-        uint8_t* bytes = reinterpret_cast<uint8_t*>(row + i);
-        for (int k = 0; k < 16; ++k) {
-          if ((bytes[k] & 0x7F) != 0x7F) continue;
-          bytes[k] = 0;
-          const int d = chunk * 16 + k;
-          for (int c = 0; c < cols; ++c)
-            if (t <= ctl->hi[buf][c] && t >= ctl->lo[buf][c]) atomicOr(&ctl->poison[stream][c][d >> 5], 1u << (d & 31));
-          ctl->any_poison[stream] = 1;
-        }
+  // A token's row of V that no column attends to becomes zeros (it may hold anything), and a NaN in
+  // one that only some columns attend to is taken out and noted for those.
+  __device__ void clean_row(uint8_t* vt, int r, int t, bool any, uint32_t buf, int stream, int cols) {
+    uint8_t* row = vt + r * 128;
+    constexpr int kChunks = D / 16;
+    const int c0 = S::kPair ? stream * kChunks : 0;
+#pragma unroll 1
+    for (int i = 0; i < kChunks; ++i) {
+      uint4* at = reinterpret_cast<uint4*>(row + (((c0 + i) ^ (r & 7)) * 16));
+      if (!any) {
+        *at = make_uint4(0u, 0u, 0u, 0u);
+        continue;
+      }
+      const uint4 x = *at;
+      const uint32_t nan = __vcmpeq4(x.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(x.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                           __vcmpeq4(x.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(x.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+      if (nan == 0) continue;
+      uint8_t* bytes = reinterpret_cast<uint8_t*>(at);
+      for (int k = 0; k < 16; ++k) {
+        if ((bytes[k] & 0x7F) != 0x7F) continue;
+        bytes[k] = 0;
+        const int d = i * 16 + k;
+        for (int c = 0; c < cols; ++c)
+          if (t <= ctl->hi[buf][c] && t >= ctl->lo[buf][c]) atomicOr(&ctl->poison[stream][c][d >> 5], 1u << (d & 31));
+        ctl->any_poison[stream] = 1;
       }
     }
   }
@@ -550,13 +561,11 @@ struct Cta {
     const int wg = (threadIdx.x >> 7) - 1;                // 0, 1: the stream
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, r = threadIdx.x & 127;
     const uint32_t quarter = tmem + ((uint32_t)(warp * 32) << 16);
-    const uint32_t s_at = quarter + wg * S::kNS, o_at = quarter + 2 * S::kNS + wg * S::kNO;
+    const uint32_t s_at = quarter + wg * S::kBufs * S::kNS, o_at = quarter + S::kOCol + wg * S::kNO;
     const int cts = col_tiles(), ncols = p.Q * p.group;
     const int t_first = ranges.begin(blockIdx.x);
     int done = t_first;                                   // tiles of the whole sequence before this segment
-    uint32_t g = 0, uses = 0;
-    uint32_t last_tile = 0;
-    bool has_last = false;
+    uint32_t g = 0, uses = 0, uses_of[2] = {0, 0};        // tiles of this stream; of both, up to this segment
     float l[NC];
     for (uint32_t seg = 0; w.left > 0; ++seg, w.next(p)) {
       const uint32_t buf = seg & 1;
@@ -565,54 +574,66 @@ struct Cta {
       // positions that every column attends to
       const int j0 = ct * NC / p.group, j1 = (min(ct * NC + NC, ncols) - 1) / p.group;
       const int at0 = w.len - p.Q + j0, at1 = w.len - p.Q + j1;
-      const int all_lo = window_start(at1);
+      const int all_lo = window_start(at1), any_lo = window_start(at0);
       const int cols = min(NC, ncols - ct * NC);
 #pragma unroll
       for (int c = 0; c < NC; ++c) l[c] = 0.f;
       bool stop = false;
-      for (int i = wg; i < w.count; i += 2) {
-        const uint32_t gt = g + i, st = gt % S::kStages;
-        const int t0 = (w.first + w.at + i) * kTile, t = t0 + r;
-        ok = ok && wait(&ctl->s_full[wg], uses & 1);
+      for (int i = S::kPair ? 0 : wg; i < w.count; i += S::kPair ? 1 : 2) {
+        const uint32_t gt = g + i, st = gt % S::kStages, sb = uses % S::kBufs;
+        const int t0 = (w.first + w.at + i) * S::kTile, t = S::kPair ? t0 + 2 * r + wg : t0 + r;
+        const int h = r / S::kPageRows;
+        ok = ok && wait(&ctl->s_full[wg][sb], (uses / S::kBufs) & 1);
         ok = ok && wait(&ctl->full[st], (gt / S::kStages) & 1);
-        // the stream's weights before these have been read, and its O is at rest
-        if (has_last) ok = ok && wait(&ctl->empty[last_tile % S::kStages], (last_tile / S::kStages) & 1);
         __syncwarp();
         tc_fence_after();
-        ++uses;
         const uint32_t pages = ctl->pages_ok[st];
-        const bool page_ok = (pages >> (r >> 6)) & 1;
-        const uint8_t* sc = reinterpret_cast<const uint8_t*>(&ctl->scales[st][r >> 6]) + (kvh & 1) * 8 + ((r & 63) >> 4);
+        const uint8_t* sc = reinterpret_cast<const uint8_t*>(&ctl->scales[st][h]) + (kvh & 1) * 8 + (t % kPageTokens) / kBlockTokens;
         const float ks = __uint_as_float((uint32_t)sc[0] << 23);
         const float ev = (float)((int)sc[4] - 127);
-        const bool whole = pages == 3u && t0 + kTile - 1 <= at0 && t0 >= all_lo;
         float z[NC];
-        bool raise = false;
+        constexpr int kBatch = NC < 16 ? NC : 16;        // columns whose parts are loaded together
 #pragma unroll
-        for (int c0 = 0; c0 < NC; c0 += 8) {
-          uint32_t a[8], b[8], d[8];
-          tmem_ld8(s_at + c0, a);
-          tmem_ld8(s_at + NC + c0, b);
-          tmem_ld8(s_at + 2 * NC + c0, d);
+        for (int c0 = 0; c0 < NC; c0 += kBatch) {
+          uint32_t part[kQParts][kBatch];
+#pragma unroll
+          for (int k = 0; k < kQParts; ++k) tmem_ldn<kBatch>(s_at + sb * S::kNS + k * NC + c0, part[k]);
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 8; k += 4) {
+          for (int k = 0; k < kBatch; k += 4) {
             const float4 f = *reinterpret_cast<const float4*>(&ctl->f[buf][c0 + k]);
-            const float4 tw = *reinterpret_cast<const float4*>(&ctl->top_w[wg][c0 + k]);
-            const float4 ts = *reinterpret_cast<const float4*>(&ctl->top_s[wg][c0 + k]);
-            const float fs[4] = {f.x, f.y, f.z, f.w}, tws[4] = {tw.x, tw.y, tw.z, tw.w}, tss[4] = {ts.x, ts.y, ts.z, ts.w};
+            const float fs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const int q = k + n, c = c0 + q;
-              const float s = fmaf(__uint_as_float(d[q]), 1.f / 256.f, fmaf(__uint_as_float(b[q]), 1.f / 16.f, __uint_as_float(a[q])));
-              z[c] = s * (fs[n] * ks);
-              if (!whole && !(page_ok && t <= ctl->hi[buf][c] && t >= ctl->lo[buf][c])) z[c] = neg_inf();
-              raise |= z[c] + ev > tws[n] + kHeadroom || z[c] > tss[n] + kSumHeadroom;
-            }
+            for (int n = 0; n < 4; ++n)
+              z[c0 + k + n] = fmaf(__uint_as_float(part[2][k + n]), 1.f / 256.f,
+                                   fmaf(__uint_as_float(part[1][k + n]), 1.f / 16.f, __uint_as_float(part[0][k + n]))) * (fs[n] * ks);
           }
         }
-        uint8_t* vt = stages + st * S::kStageBytes + S::kRowBytes;
-        if (!whole && ok) clean_row(vt, r, t, page_ok, buf, wg, cols);
+        if (!(pages == (1u << S::kPages) - 1 && t0 + S::kTile - 1 <= at0 && t0 >= all_lo)) {
+          // the positions that columns attend to end or begin here: most rows are in for all of them or for none
+          const bool page_ok = (pages >> h) & 1;
+          const bool any = page_ok && t <= at1 && t >= any_lo, all = page_ok && t <= at0 && t >= all_lo;
+          if (!all) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if (!any || t > ctl->hi[buf][c] || t < ctl->lo[buf][c]) z[c] = neg_inf();
+            if (ok) clean_row(stages + st * S::kStageBytes + S::kRowBytes, r, t, any, buf, wg, cols);
+          }
+        }
+        bool raise = false;
+#pragma unroll
+        for (int k = 0; k < NC; k += 4) {
+          const float4 tw = *reinterpret_cast<const float4*>(&ctl->top_w[wg][k]);
+          const float4 ts = *reinterpret_cast<const float4*>(&ctl->top_s[wg][k]);
+          const float tws[4] = {tw.x, tw.y, tw.z, tw.w}, tss[4] = {ts.x, ts.y, ts.z, ts.w};
+#pragma unroll
+          for (int n = 0; n < 4; ++n) raise |= z[k + n] + ev > tws[n] + kHeadroom || z[k + n] > tss[n] + kSumHeadroom;
+        }
+        // the stream's weights before these have been read, and its O is at rest
+        if (uses > 0) ok = ok && wait(&ctl->o_done[wg], (uses - 1) & 1);
+        ++uses;
+        __syncwarp();
+        tc_fence_after();
         if (bar_any(1 + wg, 128, raise || !ok)) {
           // rare after the first tiles: new references, the tile's own maxima where those are larger
 #pragma unroll
@@ -642,7 +663,7 @@ struct Cta {
           bar_sync(1 + wg, 128);
 #pragma unroll
           for (int c = 0; c < NC; ++c) l[c] *= ctl->scale_l[wg][c];
-          if (i > 1) {
+          if (i > (S::kPair ? 0 : 1)) {
             __syncwarp();
 #pragma unroll
             for (int n = 0; n < S::kNO; n += 8) {
@@ -697,16 +718,17 @@ struct Cta {
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->w_full[wg]);
-        last_tile = gt;
-        has_last = true;
+        if (lane == 0) mbar_arrive(&ctl->w_full[wg][sb]);
       }
       // ---- the segment's end: both streams, columns of this warpgroup
       const int n = w.count;
       if (!stop) {
-        const uint32_t a = g + (n - 1) / 2 * 2, b = g + (n >= 2 ? (n - 2) / 2 * 2 + 1 : 0);
-        ok = ok && wait(&ctl->empty[a % S::kStages], (a / S::kStages) & 1);
-        if (n >= 2) ok = ok && wait(&ctl->empty[b % S::kStages], (b / S::kStages) & 1);
+        uses_of[0] += S::kPair ? n : (n + 1) / 2;
+        uses_of[1] += S::kPair ? n : n / 2;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (uses_of[k] > 0) ok = ok && wait(&ctl->o_done[k], (uses_of[k] - 1) & 1);
+        __syncwarp();
         tc_fence_after();
         // sums over the warp's tokens: halves of the columns go to halves of the lanes, until a lane has one
 #pragma unroll
@@ -759,10 +781,10 @@ struct Cta {
       for (int c = wg * kHalfCols; c < wg * kHalfCols + kHalfCols; c += 4) {
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-        for (int stream = 0; stream < min(n, 2); ++stream) {
+        for (int stream = 0; stream < (S::kPair || n > 1 ? 2 : 1); ++stream) {
           uint32_t o[kWParts][4];
 #pragma unroll
-          for (int k = 0; k < kWParts; ++k) tmem_ld4(quarter + 2 * S::kNS + stream * S::kNO + k * NC + c, o[k]);
+          for (int k = 0; k < kWParts; ++k) tmem_ld4(quarter + S::kOCol + stream * S::kNO + k * NC + c, o[k]);
           tmem_wait_ld();
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -814,7 +836,7 @@ struct Cta {
 template <int D, int NC, bool kHalf>
 __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p) {
   using S = Shape<D, NC>;
-  using Ctl = Control<NC, S::kStages>;
+  using Ctl = Control<NC, S::kStages, S::kPages>;
   static_assert(offsetof(Ctl, scales) % 16 == 0 && offsetof(Ctl, f) % 16 == 0 && offsetof(Ctl, top_w) % 16 == 0 &&
                 offsetof(Ctl, top_s) % 16 == 0 && NC % 4 == 0, "vector accesses are aligned");
   static_assert(sizeof(Ctl) <= 8192, "the control block fits its share");
@@ -830,13 +852,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const __grid_co
     prefetch_tensormap(&p.cache_map);
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&ctl->full[i], 1);
-      mbar_init(&ctl->empty[i], 1);
+      mbar_init(&ctl->empty[i], S::kPair ? 2 : 1);   // the streams that read it
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->q_full[i], 1);
       mbar_init(&ctl->q_empty[i], 1 + 8);   // the issuer of S and the softmax warps
-      mbar_init(&ctl->s_full[i], 1);
-      mbar_init(&ctl->w_full[i], 4);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(&ctl->s_full[i][k], 1);
+        mbar_init(&ctl->w_full[i][k], 4);
+      }
+      mbar_init(&ctl->o_done[i], 1);
       mbar_init(&ctl->drain[i], 1);
       ctl->any_poison[i] = 0;
     }
@@ -859,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const __grid_co
   int sum = 0;
   for (int b = b0; b < b1; ++b) {
     int first, n;
-    unit_tiles(p, max(0, __ldg(p.seq_lens + b)), first, n);
+    unit_tiles<S::kTile>(p, max(0, __ldg(p.seq_lens + b)), first, n);
     sum += n;
   }
   int incl = sum;
@@ -876,14 +901,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const __grid_co
   const int before = __reduce_add_sync(kFull, lane < warp ? of_warp : 0) + incl - sum;
   const int total = __reduce_add_sync(kFull, of_warp) * units;
   // no CTA gets less than one tile for each of its two streams: joining costs more than a tile
-  const Ranges ranges(total, min((int)gridDim.x, (total + kMinTiles - 1) / kMinTiles));
+  const Ranges ranges(total, min((int)gridDim.x, (total + S::kMinTiles - 1) / S::kMinTiles));
   const int cta = blockIdx.x;
   const int t_begin = ranges.begin(cta), t_end = cta < ranges.ctas ? ranges.begin(cta + 1) : t_begin;
   if (t_begin < t_end && before * units <= t_begin && t_begin < (before + sum) * units) {
     int b = b0, at = before;
     for (;; ++b) {
       int first, n;
-      unit_tiles(p, max(0, __ldg(p.seq_lens + b)), first, n);
+      unit_tiles<S::kTile>(p, max(0, __ldg(p.seq_lens + b)), first, n);
       if (t_begin < (at + n) * units) break;
       at += n;
     }
@@ -891,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const __grid_co
     ctl->start_before = at * units;
   }
   __syncthreads();
-  Walk w{};
+  Walk<S::kTile> w{};
   w.left = t_end - t_begin;
   w.units = units;
   if (w.left > 0) {
@@ -928,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const __grid_co
 template <int D, int NC>
 constexpr size_t smem_bytes() {
   using S = Shape<D, NC>;
-  return 1024 + (size_t)S::kStages * S::kStageBytes + 2 * S::kQBytes + 2 * S::kWBytes + sizeof(Control<NC, S::kStages>);
+  return 1024 + (size_t)S::kStages * S::kStageBytes + 2 * S::kQBytes + 2 * S::kWBytes + sizeof(Control<NC, S::kStages, S::kPages>);
 }
 
 template <int D, int NC, bool kHalf>
