@@ -24,8 +24,8 @@
 //              of K and of V) the TMA boxes of its pages and their scale bytes into a ring
 //   warp 1     issues S = K q;  warp 3: issues O += V w (two threads, so that neither waits for the other)
 //   warp 2     queries of the next unit: scaling by a power of two, parts, two buffers
-//   warps 4-7  softmax of one stream of tiles, warps 8-11 of the other (thread = token): each stream
-//              has its own S, w and O, and keeps its own M, m, l; they are added at the unit's end
+//   warps 4..  softmax: two streams of tiles, a warpgroup or two each (thread = token). Each stream has
+//              its own S, w and O, and keeps its own M, m, l; they are added at the unit's end
 // With 128 dims the streams take the stages in turn. With 64 dims a 128-byte row is two tokens (TMA
 // takes a cycle or so per row, and 64-byte rows would halve its rate): a stage is 256 tokens, the even
 // ones the one stream's and the odd ones the other's, whose operands start 64 bytes into the rows.
@@ -48,7 +48,6 @@ using namespace ptx;
 
 constexpr int kRows = 128;             // 128-byte rows of K or V in a stage: a token each, or two of 64 dims
 constexpr int kQParts = 3, kWParts = 4;
-constexpr int kThreads = 384;
 constexpr float kHeadroom = 4.f;       // log2: how far above the reference a weight's exponent may come
 constexpr float kWeightScale = 4.f;    // log2: weights are held times 16, so that 2^4 above it is 256 <= 448
 constexpr float kSumHeadroom = 60.f;   // log2: the same for the sum, which fp32 holds
@@ -58,6 +57,11 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 template <int D, int NC>
 struct Shape {
   static constexpr bool kPair = D == 64;                        // a row is two tokens: one of each stream
+  // A stream's softmax is one warpgroup, or two that halve the columns: it is bound by latency, and
+  // with 16 columns two took 0.6 of one's time.
+  static constexpr int kGroups = NC == 8 ? 1 : 2;
+  static constexpr int kCols = NC / kGroups;                    // columns of a warpgroup's softmax
+  static constexpr int kThreads = 128 + 2 * kGroups * 128;
   static constexpr int kTile = kPair ? 256 : 128;               // tokens of a stage
   static constexpr int kPages = kTile / kPageTokens;
   static constexpr int kPageRows = kRows / kPages;
@@ -81,7 +85,7 @@ struct Shape {
   static_assert(kUsed <= 512 && kStages >= 3, "fits");
 };
 
-template <int NC, int kStages, int kPages>
+template <int NC, int kStages, int kPages, int kWarps>
 struct Control {
   uint64_t full[kStages], empty[kStages];
   uint64_t q_full[2], q_empty[2];
@@ -101,7 +105,7 @@ struct Control {
   float join_m[NC], join_w0[NC], join_w1[NC], join_l[NC];
   int row[NC];                         // of out and lse, -1: no column
   int any_poison[2];
-  int scan_sum[kThreads / 32];
+  int scan_sum[kWarps];
   int start_before;                    // tiles before request start_b
   int start_b;
   int last;
@@ -217,7 +221,7 @@ __device__ __forceinline__ float ratio(float a, float b) { return a == b ? 1.f :
 template <int D, int NC>
 struct Cta {
   using S = Shape<D, NC>;
-  using Ctl = Control<NC, S::kStages, S::kPages>;
+  using Ctl = Control<NC, S::kStages, S::kPages, S::kThreads / 32>;
   using Walk = ::nvfp4mla::Walk<S::kTile>;
   const Kv8DecodeParams& p;
   uint8_t* stages;
@@ -291,15 +295,18 @@ struct Cta {
             ok = wait(&ctl->empty[st], (round & 1) ^ 1);
             if (ok) {
               ctl->pages_ok[st] = have;
-              mbar_arrive_expect_tx(&ctl->full[st], 2 * S::kRowBytes + 16 * __popc(have));
+              mbar_arrive_expect_tx(&ctl->full[st], 2 * S::kRowBytes);
             }
           }
           ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
           if (ok && what < 2)
             tma_load_4d(stages + st * S::kStageBytes + what * S::kRowBytes + h * kPageTokens * D, &p.cache_map, 0, 0,
                         what * p.kv_heads + kvh, page >= 0 ? page : (int)p.num_pages, &ctl->full[st]);
-          else if (ok && what == 2 && page >= 0)
-            bulk_g2s(&ctl->scales[st][h], p.cache + page * p.page_bytes + kv8_scales_off(p.kv_heads, D, kvh & ~1), 16, &ctl->full[st]);
+          if (ok && what == 0) {
+            // (a TMA copy takes the warp some 80 ns, a load-store copy by all lanes at once a few)
+            if (page >= 0) cp_async_16(&ctl->scales[st][h], p.cache + page * p.page_bytes + kv8_scales_off(p.kv_heads, D, kvh & ~1));
+            cp_async_arrive(&ctl->full[st]);
+          }
           __syncwarp();
           if (!ok) {
             drain_copies(g);
@@ -483,18 +490,21 @@ struct Cta {
     }
   }
 
-  // Leaves this CTA's partial results of a shared unit as counted; true for the last to come.
+  // Counts this CTA among those that have left their partial results of a unit; true for the last to
+  // come. A count of another call, or whatever the workspace held before, is replaced by the first to
+  // come; the last leaves this call's count at none, as a replay of a captured call expects it.
   __device__ bool arrive(int c_lo, int c_hi) {
-    unsigned long long* at = reinterpret_cast<unsigned long long*>(p.arrived + c_lo);
-    const unsigned long long tag = p.tag;
-    unsigned long long old = 0;          // what a finished call leaves: right for the first to come
+    uint64_t* at = p.arrived + c_lo;
+    uint64_t old = add_acq_rel_gpu_u64(at, 1);
     for (;;) {
-      // a count of another call (or whatever the workspace held before) counts as none
-      const unsigned have = (old & ~0xFFFFull) == tag ? (unsigned)(old & 0xFFFF) : 0u;
-      const bool last = have + 1 == (unsigned)(c_hi - c_lo + 1);
-      const unsigned long long now = atomicCAS(at, old, last ? 0ull : (tag | (have + 1)));
-      if (now == old) return last;
-      old = now;
+      if ((old & ~(uint64_t)0xFFFF) == p.tag) {
+        if ((int)(old & 0xFFFF) != c_hi - c_lo) return false;
+        st_relaxed_gpu_u64(at, p.tag);
+        return true;
+      }
+      const uint64_t now = cas_acq_rel_gpu_u64(at, old + 1, p.tag | 1);
+      if (now == old + 1) return false;      // two CTAs at least share a unit that is counted
+      old = (now & ~(uint64_t)0xFFFF) == p.tag ? add_acq_rel_gpu_u64(at, 1) : now - 1;
     }
   }
 
@@ -513,11 +523,12 @@ struct Cta {
   }
 
   // Joins the partial results that CTAs c_lo .. c_hi left of a unit, for dim d of the columns from
-  // `from` on: four columns of four partial results at a time, every load of them in flight together.
+  // `from` on: four columns of some partial results at a time, every load of them in flight together.
   template <bool kHalf>
   __device__ void join(int from, int d, int c_lo, int c_hi, int first) {
+    constexpr int kSlots = S::kGroups == 1 ? 8 : 4;
 #pragma unroll 1
-    for (int c = from; c < from + NC / 2; c += 4) {
+    for (int c = from; c < from + NC / (2 * S::kGroups); c += 4) {
       if (ctl->row[c] < 0) break;
       float m[4], sum[4], acc[4];
 #pragma unroll
@@ -526,11 +537,11 @@ struct Cta {
         sum[k] = acc[k] = 0.f;
       }
 #pragma unroll 1
-      for (int s0 = c_lo; s0 <= c_hi; s0 += 4) {
-        float o[4][4];
-        float4 ml[4][2];
+      for (int s0 = c_lo; s0 <= c_hi; s0 += kSlots) {
+        float o[kSlots][4];
+        float4 ml[kSlots][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
           if (s0 + i > c_hi) break;
           const int at = (2 * (s0 + i) + (s0 + i == c_lo ? first : 0)) * NC + c;
           ml[i][0] = __ldcg(reinterpret_cast<const float4*>(p.part_ml + at * 2));
@@ -539,7 +550,7 @@ struct Cta {
           for (int k = 0; k < 4; ++k) o[i][k] = __ldcg(p.part_o + (int64_t)(at + k) * D + d);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
           if (s0 + i > c_hi) break;
           const float ms[4] = {ml[i][0].x, ml[i][0].z, ml[i][1].x, ml[i][1].z}, ls[4] = {ml[i][0].y, ml[i][0].w, ml[i][1].y, ml[i][1].w};
 #pragma unroll
@@ -558,7 +569,11 @@ struct Cta {
 
   template <bool kHalf>
   __device__ void softmax(Walk w, uint32_t tmem, const Ranges& ranges) {
-    const int wg = (threadIdx.x >> 7) - 1;                // 0, 1: the stream
+    // the warpgroup's stream, and which of the columns are its own: own .. own + kCols - 1
+    constexpr int kCols = S::kCols;
+    const int wi = (threadIdx.x >> 7) - 1, wg = wi & 1, grp = wi >> 1, own = grp * kCols;
+    constexpr int kAll = 2 * S::kGroups * 128;            // threads of the softmax, and their barrier
+    constexpr int kAllBar = 2 * S::kGroups + 1;
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, r = threadIdx.x & 127;
     const uint32_t quarter = tmem + ((uint32_t)(warp * 32) << 16);
     const uint32_t s_at = quarter + wg * S::kBufs * S::kNS, o_at = quarter + S::kOCol + wg * S::kNO;
@@ -566,7 +581,7 @@ struct Cta {
     const int t_first = ranges.begin(blockIdx.x);
     int done = t_first;                                   // tiles of the whole sequence before this segment
     uint32_t g = 0, uses = 0, uses_of[2] = {0, 0};        // tiles of this stream; of both, up to this segment
-    float l[NC];
+    float l[kCols];
     for (uint32_t seg = 0; w.left > 0; ++seg, w.next(p)) {
       const uint32_t buf = seg & 1;
       const int kvh = w.unit / cts, ct = w.unit % cts;
@@ -577,31 +592,31 @@ struct Cta {
       const int all_lo = window_start(at1), any_lo = window_start(at0);
       const int cols = min(NC, ncols - ct * NC);
 #pragma unroll
-      for (int c = 0; c < NC; ++c) l[c] = 0.f;
+      for (int c = 0; c < kCols; ++c) l[c] = 0.f;
       bool stop = false;
       for (int i = S::kPair ? 0 : wg; i < w.count; i += S::kPair ? 1 : 2) {
         const uint32_t gt = g + i, st = gt % S::kStages, sb = uses % S::kBufs;
         const int t0 = (w.first + w.at + i) * S::kTile, t = S::kPair ? t0 + 2 * r + wg : t0 + r;
         const int h = r / S::kPageRows;
-        ok = ok && wait(&ctl->s_full[wg][sb], (uses / S::kBufs) & 1);
         ok = ok && wait(&ctl->full[st], (gt / S::kStages) & 1);
-        __syncwarp();
-        tc_fence_after();
         const uint32_t pages = ctl->pages_ok[st];
         const uint8_t* sc = reinterpret_cast<const uint8_t*>(&ctl->scales[st][h]) + (kvh & 1) * 8 + (t % kPageTokens) / kBlockTokens;
         const float ks = __uint_as_float((uint32_t)sc[0] << 23);
         const float ev = (float)((int)sc[4] - 127);
-        float z[NC];
-        constexpr int kBatch = NC < 16 ? NC : 16;        // columns whose parts are loaded together
+        ok = ok && wait(&ctl->s_full[wg][sb], (uses / S::kBufs) & 1);
+        __syncwarp();
+        tc_fence_after();
+        float z[kCols];
+        constexpr int kBatch = 8;        // columns whose parts are loaded together
 #pragma unroll
-        for (int c0 = 0; c0 < NC; c0 += kBatch) {
+        for (int c0 = 0; c0 < kCols; c0 += kBatch) {
           uint32_t part[kQParts][kBatch];
 #pragma unroll
-          for (int k = 0; k < kQParts; ++k) tmem_ldn<kBatch>(s_at + sb * S::kNS + k * NC + c0, part[k]);
+          for (int k = 0; k < kQParts; ++k) tmem_ldn<kBatch>(s_at + sb * S::kNS + k * NC + own + c0, part[k]);
           tmem_wait_ld();
 #pragma unroll
           for (int k = 0; k < kBatch; k += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(&ctl->f[buf][c0 + k]);
+            const float4 f = *reinterpret_cast<const float4*>(&ctl->f[buf][own + c0 + k]);
             const float fs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -615,16 +630,16 @@ struct Cta {
           const bool any = page_ok && t <= at1 && t >= any_lo, all = page_ok && t <= at0 && t >= all_lo;
           if (!all) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-              if (!any || t > ctl->hi[buf][c] || t < ctl->lo[buf][c]) z[c] = neg_inf();
-            if (ok) clean_row(stages + st * S::kStageBytes + S::kRowBytes, r, t, any, buf, wg, cols);
+            for (int c = 0; c < kCols; ++c)
+              if (!any || t > ctl->hi[buf][own + c] || t < ctl->lo[buf][own + c]) z[c] = neg_inf();
+            if (ok && grp == 0) clean_row(stages + st * S::kStageBytes + S::kRowBytes, r, t, any, buf, wg, cols);
           }
         }
         bool raise = false;
 #pragma unroll
-        for (int k = 0; k < NC; k += 4) {
-          const float4 tw = *reinterpret_cast<const float4*>(&ctl->top_w[wg][k]);
-          const float4 ts = *reinterpret_cast<const float4*>(&ctl->top_s[wg][k]);
+        for (int k = 0; k < kCols; k += 4) {
+          const float4 tw = *reinterpret_cast<const float4*>(&ctl->top_w[wg][own + k]);
+          const float4 ts = *reinterpret_cast<const float4*>(&ctl->top_s[wg][own + k]);
           const float tws[4] = {tw.x, tw.y, tw.z, tw.w}, tss[4] = {ts.x, ts.y, ts.z, ts.w};
 #pragma unroll
           for (int n = 0; n < 4; ++n) raise |= z[k + n] + ev > tws[n] + kHeadroom || z[k + n] > tss[n] + kSumHeadroom;
@@ -634,86 +649,86 @@ struct Cta {
         ++uses;
         __syncwarp();
         tc_fence_after();
-        if (bar_any(1 + wg, 128, raise || !ok)) {
+        if (bar_any(1 + wi, 128, raise || !ok)) {
           // rare after the first tiles: new references, the tile's own maxima where those are larger
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
+          for (int c = 0; c < kCols; ++c) {
             const int a = __reduce_max_sync(kFull, ordered(z[c] + ev)), b = __reduce_max_sync(kFull, ordered(z[c]));
             if (lane == 0) {
-              ctl->part_max[wg][warp][c][0] = unordered(a);
-              ctl->part_max[wg][warp][c][1] = unordered(b);
+              ctl->part_max[wg][warp][own + c][0] = unordered(a);
+              ctl->part_max[wg][warp][own + c][1] = unordered(b);
             }
           }
-          if (bar_any(1 + wg, 128, !ok)) {
+          if (bar_any(1 + wi, 128, !ok)) {
             stop = true;
             break;
           }
-          if (r < NC) {
-            float a = ctl->top_w[wg][r], b = ctl->top_s[wg][r];
+          if (r < kCols) {
+            const int c = own + r;
+            float a = ctl->top_w[wg][c], b = ctl->top_s[wg][c];
             const float a0 = a, b0 = b;
             for (int k = 0; k < 4; ++k) {
-              a = fmaxf(a, ctl->part_max[wg][k][r][0]);
-              b = fmaxf(b, ctl->part_max[wg][k][r][1]);
+              a = fmaxf(a, ctl->part_max[wg][k][c][0]);
+              b = fmaxf(b, ctl->part_max[wg][k][c][1]);
             }
-            ctl->top_w[wg][r] = a;
-            ctl->top_s[wg][r] = b;
-            ctl->scale_o[wg][r] = ratio(a0, a);
-            ctl->scale_l[wg][r] = ratio(b0, b);
+            ctl->top_w[wg][c] = a;
+            ctl->top_s[wg][c] = b;
+            ctl->scale_o[wg][c] = ratio(a0, a);
+            ctl->scale_l[wg][c] = ratio(b0, b);
           }
-          bar_sync(1 + wg, 128);
+          bar_sync(1 + wi, 128);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) l[c] *= ctl->scale_l[wg][c];
+          for (int c = 0; c < kCols; ++c) l[c] *= ctl->scale_l[wg][own + c];
           if (i > (S::kPair ? 0 : 1)) {
             __syncwarp();
-#pragma unroll
-            for (int n = 0; n < S::kNO; n += 8) {
+#pragma unroll 1
+            for (int n = 0; n < kWParts * kCols; n += 8) {
+              const int c = own + n % kCols, at = n / kCols * NC + c;
               uint32_t o[8];
-              tmem_ld8(o_at + n, o);
+              tmem_ld8(o_at + at, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * ctl->scale_o[wg][(n + k) % NC]);
-              tmem_st8(o_at + n, o);
+              for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * ctl->scale_o[wg][c + k]);
+              tmem_st8(o_at + at, o);
             }
             tmem_wait_st();
           }
         }
         // weights, as parts, into the token's row of the B operand
         uint8_t* wrow = wbuf + wg * S::kWBytes + r * S::kNO;
-        constexpr int kStep = NC < 16 ? NC : 16;
+        uint32_t out[kWParts][kCols / 4];
 #pragma unroll
-        for (int c0 = 0; c0 < NC; c0 += kStep) {
-          uint32_t out[kWParts][kStep / 4];
+        for (int k = 0; k < kCols; k += 4) {
+          const float4 tw = *reinterpret_cast<const float4*>(&ctl->top_w[wg][own + k]);
+          const float4 ts = *reinterpret_cast<const float4*>(&ctl->top_s[wg][own + k]);
+          const float tws[4] = {tw.x, tw.y, tw.z, tw.w}, tss[4] = {ts.x, ts.y, ts.z, ts.w};
+          float e[4];
 #pragma unroll
-          for (int k = 0; k < kStep; k += 4) {
-            const float4 tw = *reinterpret_cast<const float4*>(&ctl->top_w[wg][c0 + k]);
-            const float4 ts = *reinterpret_cast<const float4*>(&ctl->top_s[wg][c0 + k]);
-            const float tws[4] = {tw.x, tw.y, tw.z, tw.w}, tss[4] = {ts.x, ts.y, ts.z, ts.w};
-            float e[4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const int c = c0 + k + n;
-              const float mw = tws[n] == neg_inf() ? 0.f : tws[n] - kWeightScale, ms = tss[n] == neg_inf() ? 0.f : tss[n];
-              e[n] = ex2_approx(z[c] + ev - mw);
-              l[c] += ex2_approx(z[c] - ms);
-            }
-            uint32_t p01[kWParts], p23[kWParts];
-            split_parts(e[0], e[1], p01);
-            split_parts(e[2], e[3], p23);
-#pragma unroll
-            for (int n = 0; n < kWParts; ++n) out[n][k / 4] = p01[n] | (p23[n] << 16);
+          for (int n = 0; n < 4; ++n) {
+            const int c = k + n;
+            const float mw = tws[n] == neg_inf() ? 0.f : tws[n] - kWeightScale, ms = tss[n] == neg_inf() ? 0.f : tss[n];
+            e[n] = ex2_approx(z[c] + ev - mw);
+            l[c] += ex2_approx(z[c] - ms);
           }
-          if constexpr (NC == 8) {
-            const int x = (r >> 2) & 1;
-            *reinterpret_cast<uint4*>(wrow + 16 * x) = make_uint4(out[0][0], out[0][1], out[1][0], out[1][1]);
-            *reinterpret_cast<uint4*>(wrow + 16 * (x ^ 1)) = make_uint4(out[2][0], out[2][1], out[3][0], out[3][1]);
-          } else {
+          uint32_t p01[kWParts], p23[kWParts];
+          split_parts(e[0], e[1], p01);
+          split_parts(e[2], e[3], p23);
 #pragma unroll
-            for (int n = 0; n < kWParts; ++n) {
-              const int chunk = (n * NC + c0) / 16;
-              const int x = NC == 16 ? chunk ^ ((r >> 1) & 3) : chunk ^ (r & 7);
-              *reinterpret_cast<uint4*>(wrow + 16 * x) = make_uint4(out[n][0], out[n][1], out[n][2], out[n][3]);
-            }
-          }
+          for (int n = 0; n < kWParts; ++n) out[n][k / 4] = p01[n] | (p23[n] << 16);
+        }
+        // 16-byte chunks of the row, in the operand's swizzled order
+        if constexpr (NC == 8) {
+          const int x = (r >> 2) & 1;
+          *reinterpret_cast<uint4*>(wrow + 16 * x) = make_uint4(out[0][0], out[0][1], out[1][0], out[1][1]);
+          *reinterpret_cast<uint4*>(wrow + 16 * (x ^ 1)) = make_uint4(out[2][0], out[2][1], out[3][0], out[3][1]);
+        } else if constexpr (NC == 16) {
+#pragma unroll
+          for (int n = 0; n < kWParts; ++n)
+            *reinterpret_cast<uint2*>(wrow + 16 * (n ^ ((r >> 1) & 3)) + 8 * grp) = make_uint2(out[n][0], out[n][1]);
+        } else {
+#pragma unroll
+          for (int n = 0; n < kWParts; ++n)
+            *reinterpret_cast<uint4*>(wrow + 16 * ((2 * n + grp) ^ (r & 7))) = make_uint4(out[n][0], out[n][1], out[n][2], out[n][3]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -733,7 +748,7 @@ struct Cta {
         // sums over the warp's tokens: halves of the columns go to halves of the lanes, until a lane has one
 #pragma unroll
         for (int step = 0; step < 5; ++step) {
-          const int half = NC >> (step + 1), d = 16 >> step;
+          const int half = kCols >> (step + 1), d = 16 >> step;
 #pragma unroll
           for (int c = 0; c < half; ++c) {
             const bool up = (lane & d) != 0;
@@ -742,20 +757,20 @@ struct Cta {
           }
           if (half == 0) l[0] += __shfl_xor_sync(kFull, l[0], d);
         }
-        // the lane's highest bits say which column: bit 4 halves NC, bit 3 a quarter, ...
-        if (NC == 32 || (lane & (32 / NC - 1)) == 0) ctl->part_l[wg][warp][NC == 32 ? lane : lane / (32 / NC)] = l[0];
+        // the lane's highest bits say which column: bit 4 halves them, bit 3 quarters, ...
+        if (lane % (32 / kCols) == 0) ctl->part_l[wg][warp][own + lane / (32 / kCols)] = l[0];
       }
-      if (bar_any(3, 256, stop || !ok)) {
+      if (bar_any(kAllBar, kAll, stop || !ok)) {
         // gave up: the counts of the units that this CTA shares still come out even
-        if (wg == 0 && r == 0)
+        if (wi == 0 && r == 0)
           for (; w.left > 0; done += w.count, w.next(p))
             if (!w.whole()) arrive(ranges.of(done - w.at), ranges.of(done - w.at + w.n - 1));
         return;
       }
       g += n;
-      constexpr int kHalfCols = NC / 2;
-      if (r < kHalfCols) {
-        const int c = wg * kHalfCols + r;
+      constexpr int kWgCols = NC / (2 * S::kGroups);       // of the results, whose streams are added now
+      if (r < kWgCols) {
+        const int c = wi * kWgCols + r;
         float l0 = 0.f, l1 = 0.f;
         for (int k = 0; k < 4; ++k) {
           l0 += ctl->part_l[0][k][c];
@@ -770,7 +785,7 @@ struct Cta {
         const int col = ct * NC + c, j = col / p.group;
         ctl->row[c] = col < ncols ? (w.b * p.Q + j) * p.H + kvh * p.group + (col - j * p.group) : -1;
       }
-      bar_sync(1 + wg, 128);
+      bar_sync(1 + wi, 128);
       __syncwarp();
       const int d = D == 128 ? r : (lane < 16 ? warp * 16 + lane : -1);     // M = 64 fills 16 lanes of each quarter
       const bool full_unit = w.whole();
@@ -778,7 +793,7 @@ struct Cta {
       const bool poisoned = ctl->any_poison[0] | ctl->any_poison[1];
       // four columns a round; kept as a loop, as code that runs once costs what its fetching costs
 #pragma unroll 1
-      for (int c = wg * kHalfCols; c < wg * kHalfCols + kHalfCols; c += 4) {
+      for (int c = wi * kWgCols; c < wi * kWgCols + kWgCols; c += 4) {
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
         for (int stream = 0; stream < (S::kPair || n > 1 ? 2 : 1); ++stream) {
@@ -804,29 +819,25 @@ struct Cta {
         }
       }
       if (!full_unit) {
-        if (r < kHalfCols) {
-          const int c = wg * kHalfCols + r;
+        if (r < kWgCols) {
+          const int c = wi * kWgCols + r;
           *reinterpret_cast<float2*>(p.part_ml + (slot * NC + c) * 2) = make_float2(ctl->join_m[c], ctl->join_l[c]);
         }
         const int base = done - w.at, c_lo = ranges.of(base), c_hi = ranges.of(base + w.n - 1);
-        bar_sync(3, 256);
-        if (wg == 0 && r == 0) {
-          __threadfence();
-          ctl->last = arrive(c_lo, c_hi) ? 1 : 0;
-          __threadfence();
-        }
-        bar_sync(3, 256);
-        if (ctl->last && d >= 0) join<kHalf>(wg * kHalfCols, d, c_lo, c_hi, ranges.begin(c_lo) == base ? 0 : 1);
+        bar_sync(kAllBar, kAll);
+        if (wi == 0 && r == 0) ctl->last = arrive(c_lo, c_hi) ? 1 : 0;
+        bar_sync(kAllBar, kAll);
+        if (ctl->last && d >= 0) join<kHalf>(wi * kWgCols, d, c_lo, c_hi, ranges.begin(c_lo) == base ? 0 : 1);
       }
       // the next segment starts from nothing
-      bar_sync(3, 256);
-      if (r < NC) {
-        ctl->top_w[wg][r] = ctl->top_s[wg][r] = neg_inf();
+      bar_sync(kAllBar, kAll);
+      if (r < kCols) {
+        ctl->top_w[wg][own + r] = ctl->top_s[wg][own + r] = neg_inf();
         if (poisoned)
-          for (int k = 0; k < 4; ++k) ctl->poison[wg][r][k] = 0;
+          for (int k = 0; k < 4; ++k) ctl->poison[wg][own + r][k] = 0;
       }
-      if (r == 0) ctl->any_poison[wg] = 0;
-      bar_sync(1 + wg, 128);
+      if (r == 0 && grp == 0) ctl->any_poison[wg] = 0;
+      bar_sync(1 + wi, 128);
       if (lane == 0) mbar_arrive(&ctl->q_empty[buf]);
       done += n;
     }
@@ -834,9 +845,9 @@ struct Cta {
 };
 
 template <int D, int NC, bool kHalf>
-__global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p) {
+__global__ void __launch_bounds__(Shape<D, NC>::kThreads, 1) kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p) {
   using S = Shape<D, NC>;
-  using Ctl = Control<NC, S::kStages, S::kPages>;
+  using Ctl = Control<NC, S::kStages, S::kPages, S::kThreads / 32>;
   static_assert(offsetof(Ctl, scales) % 16 == 0 && offsetof(Ctl, f) % 16 == 0 && offsetof(Ctl, top_w) % 16 == 0 &&
                 offsetof(Ctl, top_s) % 16 == 0 && NC % 4 == 0, "vector accesses are aligned");
   static_assert(sizeof(Ctl) <= 8192, "the control block fits its share");
@@ -846,20 +857,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const __grid_co
   uint8_t* qbuf = stages + S::kStages * S::kStageBytes;
   uint8_t* wbuf = qbuf + 2 * S::kQBytes;
   Ctl* ctl = reinterpret_cast<Ctl*>(wbuf + 2 * S::kWBytes);
+  constexpr int kThreads = S::kThreads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  if (tid == 0) {
+  if (tid == 64) {
     prefetch_tensormap(&p.cache_map);
     for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->full[i], 1 + S::kPages);       // the codes' bytes, every page's scale bytes
       mbar_init(&ctl->empty[i], S::kPair ? 2 : 1);   // the streams that read it
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->q_full[i], 1);
-      mbar_init(&ctl->q_empty[i], 1 + 8);   // the issuer of S and the softmax warps
+      mbar_init(&ctl->q_empty[i], 1 + 8 * S::kGroups);   // the issuer of S and the softmax warps
       for (int k = 0; k < 2; ++k) {
         mbar_init(&ctl->s_full[i][k], 1);
-        mbar_init(&ctl->w_full[i][k], 4);
+        mbar_init(&ctl->w_full[i][k], 4 * S::kGroups);
       }
       mbar_init(&ctl->o_done[i], 1);
       mbar_init(&ctl->drain[i], 1);
@@ -953,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const __grid_co
 template <int D, int NC>
 constexpr size_t smem_bytes() {
   using S = Shape<D, NC>;
-  return 1024 + (size_t)S::kStages * S::kStageBytes + 2 * S::kQBytes + 2 * S::kWBytes + sizeof(Control<NC, S::kStages, S::kPages>);
+  return 1024 + (size_t)S::kStages * S::kStageBytes + 2 * S::kQBytes + 2 * S::kWBytes + sizeof(Control<NC, S::kStages, S::kPages, S::kThreads / 32>);
 }
 
 template <int D, int NC, bool kHalf>
@@ -973,7 +985,7 @@ cudaError_t launch(const Kv8DecodeParams& p, cudaStream_t stream) {
       if (dev < 64) allowed[dev] = true;
     }
   }
-  kv8_decode_kernel<D, NC, kHalf><<<(unsigned)p.ctas, kThreads, smem, stream>>>(p);
+  kv8_decode_kernel<D, NC, kHalf><<<(unsigned)p.ctas, Shape<D, NC>::kThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 

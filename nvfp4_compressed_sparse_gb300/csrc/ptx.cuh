@@ -56,6 +56,17 @@ __device__ __forceinline__ uint64_t ld_acquire_gpu_u64(const uint64_t* p) {
   asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
   return v;
 }
+// Read-modify-writes that order this thread's other accesses around them, at GPU scope.
+__device__ __forceinline__ uint64_t add_acq_rel_gpu_u64(uint64_t* p, uint64_t v) {
+  uint64_t r;
+  asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], %2;" : "=l"(r) : "l"(p), "l"(v) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint64_t cas_acq_rel_gpu_u64(uint64_t* p, uint64_t expected, uint64_t v) {
+  uint64_t r;
+  asm volatile("atom.cas.acq_rel.gpu.global.b64 %0, [%1], %2, %3;" : "=l"(r) : "l"(p), "l"(expected), "l"(v) : "memory");
+  return r;
+}
 __device__ __forceinline__ void st_relaxed_gpu_u64(uint64_t* p, uint64_t v) {
   asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
@@ -153,6 +164,14 @@ __device__ __forceinline__ void bulk_g2s_hint(void* dst_smem, const void* src, u
           smem_u32(dst_smem)),
       "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
+}
+// 16 bytes global -> this CTA's shared memory by the load-store unit, and an arrival on an mbarrier once
+// this thread's copies have landed (one of the arrivals that the barrier was set up for).
+__device__ __forceinline__ void cp_async_16(void* dst_smem, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst_smem)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ uint64_t policy_evict_first() {
   uint64_t p;
