@@ -538,7 +538,7 @@ size_t kv8_decode_workspace_size(int B, int Q, int H, int kv_heads, int head_dim
  *                     sparse_mla_decode)
  * All pointers: device memory of the current device. A step whose 128-token
  * tiles could number more than INT32_MAX (B x kv_heads x tiles of the page
- * table's width, times the groups of 32 query-head columns) returns
+ * table's width, times the groups of 16 query-head columns) returns
  * NVFP4MLA_ERR_UNSUPPORTED.
  */
 int kv8_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype, const void* cache,

@@ -57,54 +57,59 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 template <int D, int NC>
 struct Shape {
   static constexpr bool kPair = D == 64;                        // a row is two tokens: one of each stream
-  // A stream's softmax is one warpgroup, or two that halve the columns: it is bound by latency, and
-  // with 16 columns two took 0.6 of one's time.
-  static constexpr int kGroups = NC == 8 ? 1 : 2;
-  static constexpr int kCols = NC / kGroups;                    // columns of a warpgroup's softmax
-  static constexpr int kThreads = 128 + 2 * kGroups * 128;
+  // Two streams of tiles; a softmax warpgroup of a stream has eight columns (it is bound by latency, and
+  // with 16 columns two warpgroups took 0.6 of one's time).
+  static constexpr int kStreams = 2;
+  static constexpr int kGroups = NC / 8;
+  static constexpr int kSoftmax = 2 * kGroups * 128;            // its threads
+  static constexpr int kThreads = 128 + kSoftmax;
+  static constexpr int kStep = kPair ? 1 : 2;                   // a stream takes every kStep-th stage
+  static constexpr int kHalves = kPair ? 2 : 1;                 // streams that read a stage
   static constexpr int kTile = kPair ? 256 : 128;               // tokens of a stage
   static constexpr int kPages = kTile / kPageTokens;
   static constexpr int kPageRows = kRows / kPages;
   static constexpr int kGroup = 32 / kPages;                    // stages whose page numbers are read together
-  static constexpr int kMinTiles = kPair ? 1 : 2;               // of a CTA: work for both streams
+  static constexpr int kMinTiles = kStep;                       // of a CTA: work for every stream
   static constexpr int kNS = (kQParts * NC + 15) / 16 * 16;     // columns of S
   static constexpr int kNO = kWParts * NC;                      // columns of O, bytes of a row of w
   static constexpr int kRowBytes = kRows * 128;                 // K or V of a stage
   static constexpr int kStageBytes = 2 * kRowBytes;             // the scale bytes have an area of their own
   static constexpr int kQBytes = (kNS * D + 1023) / 1024 * 1024;
   static constexpr int kWBytes = kRows * kNO;
-  static constexpr int kBudget = 232448 - 1024 - 8192;          // less alignment and the control block
-  static constexpr int kFit = (kBudget - 2 * kQBytes - 2 * kWBytes) / kStageBytes;
-  static constexpr int kStages = kFit < 12 ? kFit : 12;
-  static constexpr int kBufs = 4 * kNS + 2 * kNO <= 512 ? 2 : 1;   // S of the next tile while this one's is read
-  static constexpr int kOCol = 2 * kBufs * kNS;                 // TMEM columns: S of both streams, then O
-  static constexpr int kUsed = kOCol + 2 * kNO;
-  static constexpr uint32_t kTmem = kUsed <= 128 ? 128 : (kUsed <= 256 ? 256 : 512);
+  static constexpr int kBudget = 232448 - 1024 - 6144;          // less alignment and the control block
+  static constexpr int kFit = (kBudget - 2 * kQBytes - kStreams * kWBytes) / kStageBytes;
+  static constexpr int kStages = kFit;
+  static constexpr int kBufs = 2;                               // S of the next tile while this one's is read
+  static constexpr int kOCol = kStreams * kBufs * kNS;          // TMEM columns: S of the streams, then O
+  static constexpr int kUsed = kOCol + kStreams * kNO;
+  static constexpr uint32_t kTmem = kUsed <= 256 ? 256 : 512;
   static constexpr uint32_t kSwQ = D == 128 ? SW_128B : SW_64B;
-  static constexpr uint32_t kSwW = kNO == 128 ? SW_128B : (kNO == 64 ? SW_64B : SW_32B);
+  static constexpr uint32_t kSwW = kNO == 64 ? SW_64B : SW_32B;
   static_assert(kUsed <= 512 && kStages >= 3, "fits");
 };
 
-template <int NC, int kStages, int kPages, int kWarps>
+template <int NC, int kStages, int kPages, int kHalves, int kWarps>
 struct Control {
-  uint64_t full[kStages], empty[kStages];
+  static constexpr int kStreams = 2;
+  uint64_t full[kStages], empty[kStages][kHalves];     // empty: a stream's product with V is complete
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2][2], w_full[2][2]; // per stream and buffer of S
-  uint64_t o_done[2];
+  uint64_t s_full[kStreams][2], w_full[kStreams][2];   // per buffer of S
   uint64_t drain[2];
   uint4 scales[kStages][kPages];       // per page: the scale bytes of two neighbouring heads
   uint32_t pages_ok[kStages];          // bit per page: it is one
-  alignas(16) float f[2][NC];          // read four at a time, as M and m are: per query buffer: score of a column per unit of S, log2 units
+  alignas(16) float f[2][NC];          // per query buffer: score of a column per unit of S, log2 units
   int hi[2][NC], lo[2][NC];            // positions that a column attends to
-  alignas(16) float top_w[2][NC];      // per stream: M
-  alignas(16) float top_s[2][NC];      // m
-  float scale_o[2][NC], scale_l[2][NC];
-  float part_max[2][4][NC][2];
-  float part_l[2][4][NC];
-  uint32_t poison[2][NC][4];           // per stream and column: dims that a NaN value reaches
-  float join_m[NC], join_w0[NC], join_w1[NC], join_l[NC];
-  int row[NC];                         // of out and lse, -1: no column
-  int any_poison[2];
+  int row[2][NC];                      // of out and lse, -1: no column
+  int at0[2], at1[2], cols[2];         // positions of the tile's first and last column; its columns
+  alignas(16) float top_w[kStreams][NC];   // M (these four are read four at a time)
+  alignas(16) float top_s[kStreams][NC];   // m
+  alignas(16) float scale_o[kStreams][NC];
+  alignas(16) float scale_l[kStreams][NC];
+  float part_max[kStreams][4][NC][2];
+  float part_l[kStreams][4][NC];
+  uint32_t poison[kStreams][NC][4];    // dims that a NaN value reaches
+  float join_m[NC], join_l[NC], join_w[kStreams][NC];
+  int any_poison[kStreams];
   int scan_sum[kWarps];
   int start_before;                    // tiles before request start_b
   int start_b;
@@ -141,30 +146,46 @@ struct Ranges {
   }
 };
 
-// A walk over the segments of this CTA: per unit, the tiles of it that the CTA has.
+// What starting and ending a unit costs, in tiles: ranges count a unit of n tiles as kUnitCost + n, so
+// that CTAs with many short units do not finish last.
+constexpr int kUnitCost = 4;
+
+// A walk over the segments of this CTA: per unit, the tiles of it that the CTA has. Units go by column
+// tile, request and key/value head; so the column tiles of one head's tokens run on different CTAs at
+// about the same time, and all but one of them read the codes from L2.
 template <int kTile>
 struct Walk {
-  int left;              // tiles of the CTA's range from this segment on
-  int b, unit, units;    // request, unit inside it, units of a request
+  int left;              // of the CTA's range, from this segment on
+  int ct, b, kvh;        // the unit
   int len, first, n;     // the request's length and a unit's tiles
   int at, count;         // this segment: tiles at .. at + count - 1 of the unit
+  int pos;               // of the unit's first tile, in the whole sequence
 
   __device__ __forceinline__ void load(const Kv8DecodeParams& p) {
     len = __ldg(p.seq_lens + b);
     if (len < 0) len = 0;
     unit_tiles<kTile>(p, len, first, n);
   }
-  __device__ __forceinline__ void take() { count = min(n - at, left); }
+  // From `in` of the unit on, of which the first kUnitCost are no tiles.
+  __device__ __forceinline__ void take(int in) {
+    const int skip = in < kUnitCost ? kUnitCost - in : 0;
+    left -= skip;
+    at = in + skip - kUnitCost;
+    count = min(n - at, left);
+  }
   __device__ __forceinline__ void next(const Kv8DecodeParams& p) {
     left -= count;
     if (left <= 0) return;
-    at = 0;
-    if (++unit == units) {
-      unit = 0;
-      ++b;
+    pos += n + kUnitCost;
+    if (++kvh == p.kv_heads) {
+      kvh = 0;
+      if (++b == p.B) {
+        b = 0;
+        ++ct;
+      }
       load(p);
     }
-    take();
+    take(0);
   }
   __device__ __forceinline__ bool whole() const { return count == n; }
 };
@@ -221,7 +242,7 @@ __device__ __forceinline__ float ratio(float a, float b) { return a == b ? 1.f :
 template <int D, int NC>
 struct Cta {
   using S = Shape<D, NC>;
-  using Ctl = Control<NC, S::kStages, S::kPages, S::kThreads / 32>;
+  using Ctl = Control<NC, S::kStages, S::kPages, S::kHalves, S::kThreads / 32>;
   using Walk = ::nvfp4mla::Walk<S::kTile>;
   const Kv8DecodeParams& p;
   uint8_t* stages;
@@ -236,11 +257,10 @@ struct Cta {
   }
   // First position that a query at `at` attends to.
   __device__ __forceinline__ int window_start(int at) const { return p.window > 0 && at + 1 > p.window ? at + 1 - p.window : 0; }
-  __device__ __forceinline__ int col_tiles() const { return (p.Q * p.group + NC - 1) / NC; }
 
   // ---------------------------------------------------------------- producer (warp 0)
   // Page numbers of a group of tiles from i on: a lane a page. -1: not needed, or none.
-  __device__ __forceinline__ int load_pages(const Walk& w, int i, int ct, int kvh) {
+  __device__ __forceinline__ int load_pages(const Walk& w, int i) {
     const int lane = threadIdx.x & 31;
     const int tile = i + lane / S::kPages;
     if (tile >= w.count) return -1;
@@ -255,19 +275,18 @@ struct Cta {
     } else {
       return -1;                       // counted with the pages behind the table
     }
-    if (ct == 0 && kvh == 0 && p.status != nullptr) atomicAdd(p.status + NVFP4MLA_STAT_BAD_PAGE, 1);
+    if (w.ct == 0 && w.kvh == 0 && p.status != nullptr) atomicAdd(p.status + NVFP4MLA_STAT_BAD_PAGE, 1);
     return page;
   }
 
   __device__ void producer(Walk w) {
     const int lane = threadIdx.x & 31;
-    const int cts = col_tiles();
     uint32_t g = 0;
     if (p.withhold) return;
-    int pages = w.left > 0 ? load_pages(w, 0, w.unit % cts, w.unit / cts) : -1;
+    int pages = w.left > 0 ? load_pages(w, 0) : -1;
     while (w.left > 0) {
-      const int kvh = w.unit / cts, ct = w.unit % cts;
-      if (kvh == 0 && ct == 0 && w.at + w.count == w.n && lane == 0 && p.status != nullptr) {
+      const int kvh = w.kvh;
+      if (w.kvh == 0 && w.ct == 0 && w.at + w.count == w.n && lane == 0 && p.status != nullptr) {
         const int64_t need = ((int64_t)w.len + kPageTokens - 1) / kPageTokens;
         int64_t from = p.window > 0 ? ((int64_t)w.len - p.Q - p.window + 1) / kPageTokens : 0;
         if (from < p.max_pages) from = p.max_pages;
@@ -276,11 +295,11 @@ struct Cta {
       for (int i = 0; i < w.count; i += S::kGroup) {
         const int mine = pages;
         if (i + S::kGroup < w.count) {
-          pages = load_pages(w, i + S::kGroup, ct, kvh);
+          pages = load_pages(w, i + S::kGroup);
         } else {
           Walk nx = w;
           nx.next(p);
-          pages = nx.left > 0 ? load_pages(nx, 0, nx.unit % cts, nx.unit / cts) : -1;
+          pages = nx.left > 0 ? load_pages(nx, 0) : -1;
         }
         const int m = min(S::kGroup, w.count - i);
         for (int k = 0; k < m; ++k, ++g) {
@@ -292,7 +311,7 @@ struct Cta {
           const uint32_t st = g % S::kStages, round = g / S::kStages;
           bool ok = true;
           if (lane == 0) {
-            ok = wait(&ctl->empty[st], (round & 1) ^ 1);
+            for (int k = 0; k < S::kHalves; ++k) ok = ok && wait(&ctl->empty[st][k], (round & 1) ^ 1);
             if (ok) {
               ctl->pages_ok[st] = have;
               mbar_arrive_expect_tx(&ctl->full[st], 2 * S::kRowBytes);
@@ -330,30 +349,50 @@ struct Cta {
     }
   }
 
+  // The two issuing threads. What bounds them is their own instructions (an MMA takes its issuer some
+  // 80 cycles, a commit as much), so each tile has one commit of each, descriptors differ in their low
+  // words alone, and stages and phases are counted instead of divided.
+  struct Ring {
+    uint32_t st = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+      if (++st == (uint32_t)S::kStages) {
+        st = 0;
+        phase ^= 1;
+      }
+    }
+  };
+
   // ---------------------------------------------------------------- S = K q (warp 1, one thread)
   __device__ void issue_s(Walk w, uint32_t tmem) {
     constexpr uint32_t kId = idesc_e4m3(128, S::kNS, false, false);
     const uint64_t kd = sdesc(smem_u32(stages), 16, 1024, SW_128B), qd = sdesc(smem_u32(qbuf), 16, 8 * D, S::kSwQ);
-    uint32_t g = 0, uses[2] = {0, 0};
+    Ring ring;
+    uint32_t uses[2] = {0, 0};
     bool ok = true;
     for (uint32_t seg = 0; ok && w.left > 0; ++seg, w.next(p)) {
       const uint32_t buf = seg & 1;
       ok = wait(&ctl->q_full[buf], (seg >> 1) & 1);
-      for (int i = 0; ok && i < w.count; ++i, ++g) {
-        const uint32_t st = g % S::kStages;
-        ok = wait(&ctl->full[st], (g / S::kStages) & 1);
-        for (int stream = S::kPair ? 0 : i & 1; ok && stream <= (S::kPair ? 1 : i & 1); ++stream) {
-          const uint32_t u = uses[stream]++, sb = u % S::kBufs, turn = u / S::kBufs;
-          // this buffer's last S has been read once its weights are written
-          if (turn > 0) ok = wait(&ctl->w_full[stream][sb], (turn - 1) & 1);
+      const uint32_t q_lo = (uint32_t)qd + ((buf * S::kQBytes) >> 4);
+      for (int i = 0; ok && i < w.count; ++i) {
+        ok = wait(&ctl->full[ring.st], ring.phase);
+#pragma unroll
+        for (int half = 0; half < S::kHalves; ++half) {
+          const int stream = S::kPair ? half : i & 1;
+          const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++, sb = u & 1;
+          // this buffer's last S has been read once its weights are written (before the first, parity
+          // 1 is that of the phase before any)
+          ok = ok && wait(&ctl->w_full[stream][sb], ((u >> 1) & 1) ^ 1);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t from = st * S::kStageBytes + (S::kPair ? stream * 64 : 0);   // a row's first or second token
+          const uint32_t d = tmem + (stream * S::kBufs + sb) * S::kNS;
+          const uint32_t k_lo = (uint32_t)kd + ((ring.st * S::kStageBytes + half * 64) >> 4);   // a row's first or second token
+          umma_f8_ss_w<0>(d, k_lo, (uint32_t)(kd >> 32), q_lo, (uint32_t)(qd >> 32), kId);
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k)
-            umma_f8_ss(tmem + (stream * S::kBufs + sb) * S::kNS, kd + ((from + k * 32) >> 4), qd + ((buf * S::kQBytes + k * 32) >> 4), kId, k > 0);
+          for (int k = 1; k < D / 32; ++k)
+            umma_f8_ss_w<1>(d, k_lo + 2 * k, (uint32_t)(kd >> 32), q_lo + 2 * k, (uint32_t)(qd >> 32), kId);
           umma_commit(&ctl->s_full[stream][sb]);
         }
+        ring.next();
       }
       if (ok) umma_commit(&ctl->q_empty[buf]);
     }
@@ -365,24 +404,27 @@ struct Cta {
   __device__ void issue_o(Walk w, uint32_t tmem) {
     constexpr uint32_t kId = idesc_e4m3(D, S::kNO, true, true);
     const uint64_t vd = sdesc(smem_u32(stages + S::kRowBytes), 16, 1024, SW_128B), wd = sdesc(smem_u32(wbuf), 16, 8 * S::kNO, S::kSwW);
-    uint32_t g = 0, uses[2] = {0, 0};
+    Ring ring;
+    uint32_t uses[2] = {0, 0};
     bool ok = true;
     for (; ok && w.left > 0; w.next(p)) {
-      for (int i = 0; ok && i < w.count; ++i, ++g) {
-        const uint32_t st = g % S::kStages;
-        for (int stream = S::kPair ? 0 : i & 1; ok && stream <= (S::kPair ? 1 : i & 1); ++stream) {
-          const uint32_t u = uses[stream]++;
-          ok = wait(&ctl->w_full[stream][u % S::kBufs], (u / S::kBufs) & 1);
+      for (int i = 0; ok && i < w.count; ++i) {
+#pragma unroll
+        for (int half = 0; half < S::kHalves; ++half) {
+          const int stream = S::kPair ? half : i & 1;
+          const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++;
+          ok = ok && wait(&ctl->w_full[stream][u & 1], (u >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t from = st * S::kStageBytes + (S::kPair ? stream * 64 : 0);
+          const uint32_t d = tmem + S::kOCol + stream * S::kNO;
+          const uint32_t v_lo = (uint32_t)vd + ((ring.st * S::kStageBytes + half * 64) >> 4), w_lo = (uint32_t)wd + ((stream * S::kWBytes) >> 4);
+          umma_f8_ss_w<-1>(d, v_lo, (uint32_t)(vd >> 32), w_lo, (uint32_t)(wd >> 32), kId, i >= S::kStep ? 1u : 0u);
 #pragma unroll
-          for (int k = 0; k < kRows / 32; ++k)
-            umma_f8_ss(tmem + S::kOCol + stream * S::kNO, vd + ((from + k * 32 * 128) >> 4),
-                       wd + ((stream * S::kWBytes + k * 32 * S::kNO) >> 4), kId, i > (S::kPair ? 0 : 1) || k > 0);
-          umma_commit(&ctl->o_done[stream]);
-          umma_commit(&ctl->empty[st]);
+          for (int k = 1; k < kRows / 32; ++k)
+            umma_f8_ss_w<1>(d, v_lo + k * 256, (uint32_t)(vd >> 32), w_lo + k * 2 * S::kNO, (uint32_t)(wd >> 32), kId);
+          umma_commit(&ctl->empty[ring.st][half]);
         }
+        ring.next();
       }
     }
     umma_commit(&ctl->drain[1]);
@@ -394,10 +436,10 @@ struct Cta {
   __device__ void queries(Walk w) {
     constexpr int kLanes = D / 8, kCols = 32 / kLanes;    // lanes a column, columns a round
     const int lane = threadIdx.x & 31, sub = lane / kLanes, ch = lane % kLanes;
-    const int cts = col_tiles(), ncols = p.Q * p.group;
+    const int ncols = p.Q * p.group;
     for (uint32_t seg = 0; w.left > 0; ++seg, w.next(p)) {
       const uint32_t buf = seg & 1;
-      const int kvh = w.unit / cts, ct = w.unit % cts;
+      const int kvh = w.kvh, ct = w.ct;
       const bool ok = wait(&ctl->q_empty[buf], ((seg >> 1) & 1) ^ 1);
       if (__any_sync(kFull, !ok)) return;
       uint8_t* img = qbuf + buf * S::kQBytes;
@@ -448,7 +490,14 @@ struct Cta {
           if (ch == 0) {
             const float back = __uint_as_float((uint32_t)(127 - sh) << 23);
             ctl->f[buf][c] = col < ncols ? (finite ? p.scale_log2 * back : __int_as_float(0x7fc00000)) : 0.f;
-            const int at = w.len - p.Q + col / p.group;
+            const int j = col / p.group, at = w.len - p.Q + j;
+            ctl->row[buf][c] = col < ncols ? (w.b * p.Q + j) * p.H + kvh * p.group + (col - j * p.group) : -1;
+            const int cols = min(NC, ncols - ct * NC);
+            if (c == 0) ctl->at0[buf] = at;
+            if (c == cols - 1) {
+              ctl->at1[buf] = at;
+              ctl->cols[buf] = cols;
+            }
             ctl->hi[buf][c] = col < ncols ? at : -1;
             ctl->lo[buf][c] = window_start(at);
           }
@@ -463,10 +512,10 @@ struct Cta {
   // ---------------------------------------------------------------- softmax (warps 4-11)
   // A token's row of V that no column attends to becomes zeros (it may hold anything), and a NaN in
   // one that only some columns attend to is taken out and noted for those.
-  __device__ void clean_row(uint8_t* vt, int r, int t, bool any, uint32_t buf, int stream, int cols) {
+  __device__ void clean_row(uint8_t* vt, int r, int half, int t, bool any, uint32_t buf, int stream) {
     uint8_t* row = vt + r * 128;
     constexpr int kChunks = D / 16;
-    const int c0 = S::kPair ? stream * kChunks : 0;
+    const int c0 = half * kChunks;
 #pragma unroll 1
     for (int i = 0; i < kChunks; ++i) {
       uint4* at = reinterpret_cast<uint4*>(row + (((c0 + i) ^ (r & 7)) * 16));
@@ -483,7 +532,7 @@ struct Cta {
         if ((bytes[k] & 0x7F) != 0x7F) continue;
         bytes[k] = 0;
         const int d = i * 16 + k;
-        for (int c = 0; c < cols; ++c)
+        for (int c = 0; c < ctl->cols[buf]; ++c)
           if (t <= ctl->hi[buf][c] && t >= ctl->lo[buf][c]) atomicOr(&ctl->poison[stream][c][d >> 5], 1u << (d & 31));
         ctl->any_poison[stream] = 1;
       }
@@ -508,6 +557,10 @@ struct Cta {
     }
   }
 
+  // A CTA's partial results go to its first slot for the unit that its range begins in, else to its
+  // second: there are at most two such units.
+  static __device__ __forceinline__ int second_slot(int begin, int pos) { return pos < begin ? 0 : 1; }
+
   template <bool kHalf>
   __device__ __forceinline__ void put(int64_t at, float v) {
     if constexpr (kHalf) p.out[at] = __half_as_ushort(__float2half_rn(v));
@@ -522,106 +575,95 @@ struct Cta {
     if (d == 0) p.lse[row] = sum == 0.f ? neg_inf() : (m + log2f(sum)) * 0.69314718055994530942f;
   }
 
-  // Joins the partial results that CTAs c_lo .. c_hi left of a unit, for dim d of the columns from
-  // `from` on: four columns of some partial results at a time, every load of them in flight together.
+  // Joins the partial results that CTAs c_lo .. c_hi left of a unit, for dim d of this warpgroup's
+  // columns: some partial results at a time, every load of them in flight together.
   template <bool kHalf>
-  __device__ void join(int from, int d, int c_lo, int c_hi, int first) {
-    constexpr int kSlots = S::kGroups == 1 ? 8 : 4;
-#pragma unroll 1
-    for (int c = from; c < from + NC / (2 * S::kGroups); c += 4) {
-      if (ctl->row[c] < 0) break;
-      float m[4], sum[4], acc[4];
+  __device__ void join(const int* row, int c, int d, int c_lo, int c_hi, int first) {
+    constexpr int kN = 4, kSlots = S::kGroups == 1 ? 8 : 4;
+    float m[kN], sum[kN], acc[kN];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        m[k] = neg_inf();
-        sum[k] = acc[k] = 0.f;
-      }
-#pragma unroll 1
-      for (int s0 = c_lo; s0 <= c_hi; s0 += kSlots) {
-        float o[kSlots][4];
-        float4 ml[kSlots][2];
-#pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
-          if (s0 + i > c_hi) break;
-          const int at = (2 * (s0 + i) + (s0 + i == c_lo ? first : 0)) * NC + c;
-          ml[i][0] = __ldcg(reinterpret_cast<const float4*>(p.part_ml + at * 2));
-          ml[i][1] = __ldcg(reinterpret_cast<const float4*>(p.part_ml + at * 2) + 1);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[i][k] = __ldcg(p.part_o + (int64_t)(at + k) * D + d);
-        }
-#pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
-          if (s0 + i > c_hi) break;
-          const float ms[4] = {ml[i][0].x, ml[i][0].z, ml[i][1].x, ml[i][1].z}, ls[4] = {ml[i][0].y, ml[i][0].w, ml[i][1].y, ml[i][1].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float m_new = fmaxf(m[k], ms[k]), keep = ratio(m[k], m_new), in = ratio(ms[k], m_new);
-            sum[k] = sum[k] * keep + ls[k] * in;
-            acc[k] = acc[k] * keep + o[i][k] * in;
-            m[k] = m_new;
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) finish<kHalf>(ctl->row[c + k], d, m[k], sum[k], acc[k]);
+    for (int k = 0; k < kN; ++k) {
+      m[k] = neg_inf();
+      sum[k] = acc[k] = 0.f;
     }
+#pragma unroll 1
+    for (int s0 = c_lo; s0 <= c_hi; s0 += kSlots) {
+      float o[kSlots][kN];
+      float2 ml[kSlots][kN];
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        if (s0 + i > c_hi) break;
+        const int at = (2 * (s0 + i) + (s0 + i == c_lo ? first : 0)) * NC + c;
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+          ml[i][k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at + k);
+          o[i][k] = __ldcg(p.part_o + (int64_t)(at + k) * D + d);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        if (s0 + i > c_hi) break;
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+          const float m_new = fmaxf(m[k], ml[i][k].x), keep = ratio(m[k], m_new), in = ratio(ml[i][k].x, m_new);
+          sum[k] = sum[k] * keep + ml[i][k].y * in;
+          acc[k] = acc[k] * keep + o[i][k] * in;
+          m[k] = m_new;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kN; ++k) finish<kHalf>(row[c + k], d, m[k], sum[k], acc[k]);
   }
 
   template <bool kHalf>
   __device__ void softmax(Walk w, uint32_t tmem, const Ranges& ranges) {
-    // the warpgroup's stream, and which of the columns are its own: own .. own + kCols - 1
-    constexpr int kCols = S::kCols;
-    const int wi = (threadIdx.x >> 7) - 1, wg = wi & 1, grp = wi >> 1, own = grp * kCols;
-    constexpr int kAll = 2 * S::kGroups * 128;            // threads of the softmax, and their barrier
-    constexpr int kAllBar = 2 * S::kGroups + 1;
+    // the warpgroup's stream, and which of the columns are its own: own .. own + 7
+    constexpr int kCols = 8, kStreams = S::kStreams;
+    const int wi = (threadIdx.x >> 7) - 1, stream = wi % kStreams, grp = wi / kStreams, own = grp * kCols;
+    constexpr int kAll = S::kSoftmax, kAllBar = 2 * S::kGroups + 1;   // threads of the softmax, and their barrier
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, r = threadIdx.x & 127;
     const uint32_t quarter = tmem + ((uint32_t)(warp * 32) << 16);
-    const uint32_t s_at = quarter + wg * S::kBufs * S::kNS, o_at = quarter + S::kOCol + wg * S::kNO;
-    const int cts = col_tiles(), ncols = p.Q * p.group;
+    const uint32_t s_at = quarter + stream * S::kBufs * S::kNS + own, o_at = quarter + S::kOCol + stream * S::kNO + own;
+    const int i0 = S::kPair ? 0 : stream, half = S::kPair ? stream : 0;
     const int t_first = ranges.begin(blockIdx.x);
-    int done = t_first;                                   // tiles of the whole sequence before this segment
-    uint32_t g = 0, uses = 0, uses_of[2] = {0, 0};        // tiles of this stream; of both, up to this segment
+    uint32_t g = 0, uses = 0;                             // stages before this segment; this stream's tiles
+    uint32_t prev = 0;                                    // the stage of this stream's tile before
     float l[kCols];
     for (uint32_t seg = 0; w.left > 0; ++seg, w.next(p)) {
       const uint32_t buf = seg & 1;
-      const int kvh = w.unit / cts, ct = w.unit % cts;
       bool ok = wait(&ctl->q_full[buf], (seg >> 1) & 1);
-      // positions that every column attends to
-      const int j0 = ct * NC / p.group, j1 = (min(ct * NC + NC, ncols) - 1) / p.group;
-      const int at0 = w.len - p.Q + j0, at1 = w.len - p.Q + j1;
-      const int all_lo = window_start(at1), any_lo = window_start(at0);
-      const int cols = min(NC, ncols - ct * NC);
+      // positions that every column attends to, and that any does
+      const int at0 = ctl->at0[buf], at1 = ctl->at1[buf], all_lo = window_start(at1), any_lo = window_start(at0);
 #pragma unroll
       for (int c = 0; c < kCols; ++c) l[c] = 0.f;
       bool stop = false;
-      for (int i = S::kPair ? 0 : wg; i < w.count; i += S::kPair ? 1 : 2) {
-        const uint32_t gt = g + i, st = gt % S::kStages, sb = uses % S::kBufs;
-        const int t0 = (w.first + w.at + i) * S::kTile, t = S::kPair ? t0 + 2 * r + wg : t0 + r;
+      for (int i = i0; i < w.count; i += S::kStep) {
+        const uint32_t gt = g + i, st = gt % S::kStages, sb = uses & 1;
+        const int t0 = (w.first + w.at + i) * S::kTile, t = S::kPair ? t0 + 2 * r + half : t0 + r;
         const int h = r / S::kPageRows;
         ok = ok && wait(&ctl->full[st], (gt / S::kStages) & 1);
         const uint32_t pages = ctl->pages_ok[st];
-        const uint8_t* sc = reinterpret_cast<const uint8_t*>(&ctl->scales[st][h]) + (kvh & 1) * 8 + (t % kPageTokens) / kBlockTokens;
+        const uint8_t* sc = reinterpret_cast<const uint8_t*>(&ctl->scales[st][h]) + (w.kvh & 1) * 8 + (t % kPageTokens) / kBlockTokens;
         const float ks = __uint_as_float((uint32_t)sc[0] << 23);
         const float ev = (float)((int)sc[4] - 127);
-        ok = ok && wait(&ctl->s_full[wg][sb], (uses / S::kBufs) & 1);
+        ok = ok && wait(&ctl->s_full[stream][sb], (uses >> 1) & 1);
         __syncwarp();
         tc_fence_after();
         float z[kCols];
-        constexpr int kBatch = 8;        // columns whose parts are loaded together
+        {
+          uint32_t part[kQParts][kCols];
 #pragma unroll
-        for (int c0 = 0; c0 < kCols; c0 += kBatch) {
-          uint32_t part[kQParts][kBatch];
-#pragma unroll
-          for (int k = 0; k < kQParts; ++k) tmem_ldn<kBatch>(s_at + sb * S::kNS + k * NC + own + c0, part[k]);
+          for (int k = 0; k < kQParts; ++k) tmem_ld8(s_at + sb * S::kNS + k * NC, part[k]);
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < kBatch; k += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(&ctl->f[buf][own + c0 + k]);
+          for (int k = 0; k < kCols; k += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&ctl->f[buf][own + k]);
             const float fs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
             for (int n = 0; n < 4; ++n)
-              z[c0 + k + n] = fmaf(__uint_as_float(part[2][k + n]), 1.f / 256.f,
-                                   fmaf(__uint_as_float(part[1][k + n]), 1.f / 16.f, __uint_as_float(part[0][k + n]))) * (fs[n] * ks);
+              z[k + n] = fmaf(__uint_as_float(part[2][k + n]), 1.f / 256.f,
+                              fmaf(__uint_as_float(part[1][k + n]), 1.f / 16.f, __uint_as_float(part[0][k + n]))) * (fs[n] * ks);
           }
         }
         if (!(pages == (1u << S::kPages) - 1 && t0 + S::kTile - 1 <= at0 && t0 >= all_lo)) {
@@ -632,21 +674,22 @@ struct Cta {
 #pragma unroll
             for (int c = 0; c < kCols; ++c)
               if (!any || t > ctl->hi[buf][own + c] || t < ctl->lo[buf][own + c]) z[c] = neg_inf();
-            if (ok && grp == 0) clean_row(stages + st * S::kStageBytes + S::kRowBytes, r, t, any, buf, wg, cols);
+            if (ok && grp == 0) clean_row(stages + st * S::kStageBytes + S::kRowBytes, r, half, t, any, buf, stream);
           }
         }
         bool raise = false;
 #pragma unroll
         for (int k = 0; k < kCols; k += 4) {
-          const float4 tw = *reinterpret_cast<const float4*>(&ctl->top_w[wg][own + k]);
-          const float4 ts = *reinterpret_cast<const float4*>(&ctl->top_s[wg][own + k]);
+          const float4 tw = *reinterpret_cast<const float4*>(&ctl->top_w[stream][own + k]);
+          const float4 ts = *reinterpret_cast<const float4*>(&ctl->top_s[stream][own + k]);
           const float tws[4] = {tw.x, tw.y, tw.z, tw.w}, tss[4] = {ts.x, ts.y, ts.z, ts.w};
 #pragma unroll
           for (int n = 0; n < 4; ++n) raise |= z[k + n] + ev > tws[n] + kHeadroom || z[k + n] > tss[n] + kSumHeadroom;
         }
         // the stream's weights before these have been read, and its O is at rest
-        if (uses > 0) ok = ok && wait(&ctl->o_done[wg], (uses - 1) & 1);
+        if (uses > 0) ok = ok && wait(&ctl->empty[prev % S::kStages][half], (prev / S::kStages) & 1);
         ++uses;
+        prev = gt;
         __syncwarp();
         tc_fence_after();
         if (bar_any(1 + wi, 128, raise || !ok)) {
@@ -655,8 +698,8 @@ struct Cta {
           for (int c = 0; c < kCols; ++c) {
             const int a = __reduce_max_sync(kFull, ordered(z[c] + ev)), b = __reduce_max_sync(kFull, ordered(z[c]));
             if (lane == 0) {
-              ctl->part_max[wg][warp][own + c][0] = unordered(a);
-              ctl->part_max[wg][warp][own + c][1] = unordered(b);
+              ctl->part_max[stream][warp][own + c][0] = unordered(a);
+              ctl->part_max[stream][warp][own + c][1] = unordered(b);
             }
           }
           if (bar_any(1 + wi, 128, !ok)) {
@@ -665,42 +708,41 @@ struct Cta {
           }
           if (r < kCols) {
             const int c = own + r;
-            float a = ctl->top_w[wg][c], b = ctl->top_s[wg][c];
-            const float a0 = a, b0 = b;
+            const float a0 = ctl->top_w[stream][c], b0 = ctl->top_s[stream][c];
+            float a = a0, b = b0;
             for (int k = 0; k < 4; ++k) {
-              a = fmaxf(a, ctl->part_max[wg][k][c][0]);
-              b = fmaxf(b, ctl->part_max[wg][k][c][1]);
+              a = fmaxf(a, ctl->part_max[stream][k][c][0]);
+              b = fmaxf(b, ctl->part_max[stream][k][c][1]);
             }
-            ctl->top_w[wg][c] = a;
-            ctl->top_s[wg][c] = b;
-            ctl->scale_o[wg][c] = ratio(a0, a);
-            ctl->scale_l[wg][c] = ratio(b0, b);
+            ctl->top_w[stream][c] = a;
+            ctl->top_s[stream][c] = b;
+            ctl->scale_o[stream][c] = ratio(a0, a);
+            ctl->scale_l[stream][c] = ratio(b0, b);
           }
           bar_sync(1 + wi, 128);
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) l[c] *= ctl->scale_l[wg][own + c];
-          if (i > (S::kPair ? 0 : 1)) {
+          for (int c = 0; c < kCols; ++c) l[c] *= ctl->scale_l[stream][own + c];
+          if (i >= S::kStep) {
             __syncwarp();
 #pragma unroll 1
-            for (int n = 0; n < kWParts * kCols; n += 8) {
-              const int c = own + n % kCols, at = n / kCols * NC + c;
-              uint32_t o[8];
-              tmem_ld8(o_at + at, o);
+            for (int k = 0; k < kWParts; ++k) {
+              uint32_t o[kCols];
+              tmem_ld8(o_at + k * NC, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * ctl->scale_o[wg][c + k]);
-              tmem_st8(o_at + at, o);
+              for (int c = 0; c < kCols; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * ctl->scale_o[stream][own + c]);
+              tmem_st8(o_at + k * NC, o);
             }
             tmem_wait_st();
           }
         }
         // weights, as parts, into the token's row of the B operand
-        uint8_t* wrow = wbuf + wg * S::kWBytes + r * S::kNO;
-        uint32_t out[kWParts][kCols / 4];
+        uint8_t* wrow = wbuf + stream * S::kWBytes + r * S::kNO;
+        uint32_t out[kWParts][2];
 #pragma unroll
         for (int k = 0; k < kCols; k += 4) {
-          const float4 tw = *reinterpret_cast<const float4*>(&ctl->top_w[wg][own + k]);
-          const float4 ts = *reinterpret_cast<const float4*>(&ctl->top_s[wg][own + k]);
+          const float4 tw = *reinterpret_cast<const float4*>(&ctl->top_w[stream][own + k]);
+          const float4 ts = *reinterpret_cast<const float4*>(&ctl->top_s[stream][own + k]);
           const float tws[4] = {tw.x, tw.y, tw.z, tw.w}, tss[4] = {ts.x, ts.y, ts.z, ts.w};
           float e[4];
 #pragma unroll
@@ -721,125 +763,118 @@ struct Cta {
           const int x = (r >> 2) & 1;
           *reinterpret_cast<uint4*>(wrow + 16 * x) = make_uint4(out[0][0], out[0][1], out[1][0], out[1][1]);
           *reinterpret_cast<uint4*>(wrow + 16 * (x ^ 1)) = make_uint4(out[2][0], out[2][1], out[3][0], out[3][1]);
-        } else if constexpr (NC == 16) {
-#pragma unroll
-          for (int n = 0; n < kWParts; ++n)
-            *reinterpret_cast<uint2*>(wrow + 16 * (n ^ ((r >> 1) & 3)) + 8 * grp) = make_uint2(out[n][0], out[n][1]);
         } else {
 #pragma unroll
           for (int n = 0; n < kWParts; ++n)
-            *reinterpret_cast<uint4*>(wrow + 16 * ((2 * n + grp) ^ (r & 7))) = make_uint4(out[n][0], out[n][1], out[n][2], out[n][3]);
+            *reinterpret_cast<uint2*>(wrow + 16 * (n ^ ((r >> 1) & 3)) + 8 * grp) = make_uint2(out[n][0], out[n][1]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->w_full[wg][sb]);
+        if (lane == 0) mbar_arrive(&ctl->w_full[stream][sb]);
       }
-      // ---- the segment's end: both streams, columns of this warpgroup
+      // ---- the segment's end: all streams, this warpgroup's share of the columns
       const int n = w.count;
       if (!stop) {
-        uses_of[0] += S::kPair ? n : (n + 1) / 2;
-        uses_of[1] += S::kPair ? n : n / 2;
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (uses_of[k] > 0) ok = ok && wait(&ctl->o_done[k], (uses_of[k] - 1) & 1);
+        for (int k = 0; k < kStreams; ++k) {
+          const uint32_t at = g + (S::kPair ? n - 1 : (n - 1 - k) / 2 * 2 + k);   // the stream's last stage
+          if (S::kPair || n > k) ok = ok && wait(&ctl->empty[at % S::kStages][S::kPair ? k : 0], (at / S::kStages) & 1);
+        }
         __syncwarp();
         tc_fence_after();
         // sums over the warp's tokens: halves of the columns go to halves of the lanes, until a lane has one
 #pragma unroll
         for (int step = 0; step < 5; ++step) {
-          const int half = kCols >> (step + 1), d = 16 >> step;
+          const int part = kCols >> (step + 1), d = 16 >> step;
 #pragma unroll
-          for (int c = 0; c < half; ++c) {
+          for (int c = 0; c < part; ++c) {
             const bool up = (lane & d) != 0;
-            const float give = up ? l[c] : l[c + half], keep = up ? l[c + half] : l[c];
+            const float give = up ? l[c] : l[c + part], keep = up ? l[c + part] : l[c];
             l[c] = keep + __shfl_xor_sync(kFull, give, d);
           }
-          if (half == 0) l[0] += __shfl_xor_sync(kFull, l[0], d);
+          if (part == 0) l[0] += __shfl_xor_sync(kFull, l[0], d);
         }
         // the lane's highest bits say which column: bit 4 halves them, bit 3 quarters, ...
-        if (lane % (32 / kCols) == 0) ctl->part_l[wg][warp][own + lane / (32 / kCols)] = l[0];
+        if (lane % (32 / kCols) == 0) ctl->part_l[stream][warp][own + lane / (32 / kCols)] = l[0];
       }
       if (bar_any(kAllBar, kAll, stop || !ok)) {
         // gave up: the counts of the units that this CTA shares still come out even
         if (wi == 0 && r == 0)
-          for (; w.left > 0; done += w.count, w.next(p))
-            if (!w.whole()) arrive(ranges.of(done - w.at), ranges.of(done - w.at + w.n - 1));
+          for (; w.left > 0; w.next(p))
+            if (!w.whole()) arrive(ranges.of(w.pos + kUnitCost), ranges.of(w.pos + kUnitCost + w.n - 1));
         return;
       }
       g += n;
-      constexpr int kWgCols = NC / (2 * S::kGroups);       // of the results, whose streams are added now
-      if (r < kWgCols) {
-        const int c = wi * kWgCols + r;
-        float l0 = 0.f, l1 = 0.f;
-        for (int k = 0; k < 4; ++k) {
-          l0 += ctl->part_l[0][k][c];
-          l1 += ctl->part_l[1][k][c];
+      constexpr int kN = 4;                               // columns whose streams this warpgroup adds
+      const int c0 = wi * kN;
+      if (r < kN) {
+        const int c = c0 + r;
+        float m = neg_inf(), sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kStreams; ++k) m = fmaxf(m, ctl->top_s[k][c]);
+#pragma unroll
+        for (int k = 0; k < kStreams; ++k) {
+          float part = 0.f;
+          for (int q = 0; q < 4; ++q) part += ctl->part_l[k][q][c];
+          sum += part * ratio(ctl->top_s[k][c], m);
+          const float tw = ctl->top_w[k][c];
+          ctl->join_w[k][c] = tw == neg_inf() ? 0.f : ex2_approx(tw - kWeightScale - m);
         }
-        const float m0 = ctl->top_s[0][c], m1 = ctl->top_s[1][c], m = fmaxf(m0, m1);
-        const float w0 = ctl->top_w[0][c], w1 = ctl->top_w[1][c];
         ctl->join_m[c] = m;
-        ctl->join_l[c] = l0 * ratio(m0, m) + l1 * ratio(m1, m);
-        ctl->join_w0[c] = w0 == neg_inf() ? 0.f : exp2f(w0 - kWeightScale - m);
-        ctl->join_w1[c] = w1 == neg_inf() ? 0.f : exp2f(w1 - kWeightScale - m);
-        const int col = ct * NC + c, j = col / p.group;
-        ctl->row[c] = col < ncols ? (w.b * p.Q + j) * p.H + kvh * p.group + (col - j * p.group) : -1;
+        ctl->join_l[c] = sum;
       }
       bar_sync(1 + wi, 128);
       __syncwarp();
       const int d = D == 128 ? r : (lane < 16 ? warp * 16 + lane : -1);     // M = 64 fills 16 lanes of each quarter
       const bool full_unit = w.whole();
-      const int slot = 2 * (int)blockIdx.x + (done == t_first ? 0 : 1);
-      const bool poisoned = ctl->any_poison[0] | ctl->any_poison[1];
-      // four columns a round; kept as a loop, as code that runs once costs what its fetching costs
+      const int slot = 2 * (int)blockIdx.x + second_slot(t_first, w.pos);
+      bool poisoned = false;
+#pragma unroll
+      for (int k = 0; k < kStreams; ++k) poisoned |= ctl->any_poison[k] != 0;
+      float acc[kN] = {};
+      // kept as a loop, as code that runs once costs what its fetching costs
 #pragma unroll 1
-      for (int c = wi * kWgCols; c < wi * kWgCols + kWgCols; c += 4) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-        for (int stream = 0; stream < (S::kPair || n > 1 ? 2 : 1); ++stream) {
-          uint32_t o[kWParts][4];
+      for (int k = 0; k < kStreams && (S::kPair || k < n); ++k) {
+        uint32_t o[kWParts][kN];
 #pragma unroll
-          for (int k = 0; k < kWParts; ++k) tmem_ld4(quarter + S::kOCol + stream * S::kNO + k * NC + c, o[k]);
-          tmem_wait_ld();
+        for (int q = 0; q < kWParts; ++q) tmem_ld4(quarter + S::kOCol + k * S::kNO + q * NC + c0, o[q]);
+        tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float x = __uint_as_float(o[3][k]);
-            x = fmaf(x, 1.f / 16.f, __uint_as_float(o[2][k]));
-            x = fmaf(x, 1.f / 16.f, __uint_as_float(o[1][k]));
-            x = fmaf(x, 1.f / 16.f, __uint_as_float(o[0][k]));
-            if (poisoned && d >= 0 && ((ctl->poison[stream][c + k][d >> 5] >> (d & 31)) & 1)) x = __int_as_float(0x7fc00000);
-            acc[k] = fmaf(x, stream == 0 ? ctl->join_w0[c + k] : ctl->join_w1[c + k], acc[k]);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (d < 0) continue;
-          if (full_unit) finish<kHalf>(ctl->row[c + k], d, ctl->join_m[c + k], ctl->join_l[c + k], acc[k]);
-          else p.part_o[(int64_t)(slot * NC + c + k) * D + d] = acc[k];
+        for (int c = 0; c < kN; ++c) {
+          float x = __uint_as_float(o[3][c]);
+          x = fmaf(x, 1.f / 16.f, __uint_as_float(o[2][c]));
+          x = fmaf(x, 1.f / 16.f, __uint_as_float(o[1][c]));
+          x = fmaf(x, 1.f / 16.f, __uint_as_float(o[0][c]));
+          if (poisoned && d >= 0 && ((ctl->poison[k][c0 + c][d >> 5] >> (d & 31)) & 1)) x = __int_as_float(0x7fc00000);
+          acc[c] = fmaf(x, ctl->join_w[k][c0 + c], acc[c]);
         }
       }
-      if (!full_unit) {
-        if (r < kWgCols) {
-          const int c = wi * kWgCols + r;
-          *reinterpret_cast<float2*>(p.part_ml + (slot * NC + c) * 2) = make_float2(ctl->join_m[c], ctl->join_l[c]);
-        }
-        const int base = done - w.at, c_lo = ranges.of(base), c_hi = ranges.of(base + w.n - 1);
+      if (full_unit) {
+#pragma unroll
+        for (int c = 0; c < kN; ++c)
+          if (d >= 0) finish<kHalf>(ctl->row[buf][c0 + c], d, ctl->join_m[c0 + c], ctl->join_l[c0 + c], acc[c]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < kN; ++c)
+          if (d >= 0) p.part_o[(int64_t)(slot * NC + c0 + c) * D + d] = acc[c];
+        if (r < kN) reinterpret_cast<float2*>(p.part_ml)[slot * NC + c0 + r] = make_float2(ctl->join_m[c0 + r], ctl->join_l[c0 + r]);
+        const int base = w.pos + kUnitCost, c_lo = ranges.of(base), c_hi = ranges.of(base + w.n - 1);
         bar_sync(kAllBar, kAll);
         if (wi == 0 && r == 0) ctl->last = arrive(c_lo, c_hi) ? 1 : 0;
         bar_sync(kAllBar, kAll);
-        if (ctl->last && d >= 0) join<kHalf>(wi * kWgCols, d, c_lo, c_hi, ranges.begin(c_lo) == base ? 0 : 1);
+        if (ctl->last && d >= 0) join<kHalf>(ctl->row[buf], c0, d, c_lo, c_hi, second_slot(ranges.begin(c_lo), w.pos));
       }
       // the next segment starts from nothing
       bar_sync(kAllBar, kAll);
       if (r < kCols) {
-        ctl->top_w[wg][own + r] = ctl->top_s[wg][own + r] = neg_inf();
+        ctl->top_w[stream][own + r] = ctl->top_s[stream][own + r] = neg_inf();
         if (poisoned)
-          for (int k = 0; k < 4; ++k) ctl->poison[wg][own + r][k] = 0;
+          for (int k = 0; k < 4; ++k) ctl->poison[stream][own + r][k] = 0;
       }
-      if (r == 0 && grp == 0) ctl->any_poison[wg] = 0;
+      if (r == 0 && grp == 0) ctl->any_poison[stream] = 0;
       bar_sync(1 + wi, 128);
       if (lane == 0) mbar_arrive(&ctl->q_empty[buf]);
-      done += n;
     }
   }
 };
@@ -847,16 +882,16 @@ struct Cta {
 template <int D, int NC, bool kHalf>
 __global__ void __launch_bounds__(Shape<D, NC>::kThreads, 1) kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p) {
   using S = Shape<D, NC>;
-  using Ctl = Control<NC, S::kStages, S::kPages, S::kThreads / 32>;
+  using Ctl = Control<NC, S::kStages, S::kPages, S::kHalves, S::kThreads / 32>;
   static_assert(offsetof(Ctl, scales) % 16 == 0 && offsetof(Ctl, f) % 16 == 0 && offsetof(Ctl, top_w) % 16 == 0 &&
-                offsetof(Ctl, top_s) % 16 == 0 && NC % 4 == 0, "vector accesses are aligned");
-  static_assert(sizeof(Ctl) <= 8192, "the control block fits its share");
+                offsetof(Ctl, top_s) % 16 == 0 && NC % 8 == 0, "vector accesses are aligned");
+  static_assert(sizeof(Ctl) <= 6144, "the control block fits its share");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stages = base;
   uint8_t* qbuf = stages + S::kStages * S::kStageBytes;
   uint8_t* wbuf = qbuf + 2 * S::kQBytes;
-  Ctl* ctl = reinterpret_cast<Ctl*>(wbuf + 2 * S::kWBytes);
+  Ctl* ctl = reinterpret_cast<Ctl*>(wbuf + S::kStreams * S::kWBytes);
   constexpr int kThreads = S::kThreads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -864,23 +899,24 @@ __global__ void __launch_bounds__(Shape<D, NC>::kThreads, 1) kv8_decode_kernel(c
     prefetch_tensormap(&p.cache_map);
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&ctl->full[i], 1 + S::kPages);       // the codes' bytes, every page's scale bytes
-      mbar_init(&ctl->empty[i], S::kPair ? 2 : 1);   // the streams that read it
+      for (int k = 0; k < S::kHalves; ++k) mbar_init(&ctl->empty[i][k], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->q_full[i], 1);
-      mbar_init(&ctl->q_empty[i], 1 + 8 * S::kGroups);   // the issuer of S and the softmax warps
+      mbar_init(&ctl->q_empty[i], 1 + S::kSoftmax / 32);           // the issuer of S and the softmax warps
+      mbar_init(&ctl->drain[i], 1);
+    }
+    for (int i = 0; i < S::kStreams; ++i) {
       for (int k = 0; k < 2; ++k) {
         mbar_init(&ctl->s_full[i][k], 1);
         mbar_init(&ctl->w_full[i][k], 4 * S::kGroups);
       }
-      mbar_init(&ctl->o_done[i], 1);
-      mbar_init(&ctl->drain[i], 1);
       ctl->any_poison[i] = 0;
     }
     ctl->abort = 0;
     fence_barrier_init();
   }
-  for (int i = tid; i < 2 * NC; i += kThreads) {
+  for (int i = tid; i < S::kStreams * NC; i += kThreads) {
     ctl->top_w[i / NC][i % NC] = ctl->top_s[i / NC][i % NC] = neg_inf();
     for (int k = 0; k < 4; ++k) ctl->poison[i / NC][i % NC][k] = 0;
   }
@@ -889,15 +925,15 @@ __global__ void __launch_bounds__(Shape<D, NC>::kThreads, 1) kv8_decode_kernel(c
     tmem_relinquish();
   }
 
-  // the whole sequence of tiles: every thread sums a run of requests
-  const int units = p.kv_heads * ((p.Q * p.group + NC - 1) / NC);
+  // the whole sequence: every thread sums a run of requests
+  const int cts = (p.Q * p.group + NC - 1) / NC;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   int sum = 0;
   for (int b = b0; b < b1; ++b) {
     int first, n;
     unit_tiles<S::kTile>(p, max(0, __ldg(p.seq_lens + b)), first, n);
-    sum += n;
+    sum += n + kUnitCost;
   }
   int incl = sum;
 #pragma unroll
@@ -910,34 +946,36 @@ __global__ void __launch_bounds__(Shape<D, NC>::kThreads, 1) kv8_decode_kernel(c
   __syncthreads();
   tc_fence_after();
   const int of_warp = lane < kThreads / 32 ? ctl->scan_sum[lane] : 0;
-  const int before = __reduce_add_sync(kFull, lane < warp ? of_warp : 0) + incl - sum;
-  const int total = __reduce_add_sync(kFull, of_warp) * units;
-  // no CTA gets less than one tile for each of its two streams: joining costs more than a tile
-  const Ranges ranges(total, min((int)gridDim.x, (total + S::kMinTiles - 1) / S::kMinTiles));
+  const int before = (__reduce_add_sync(kFull, lane < warp ? of_warp : 0) + incl - sum) * p.kv_heads;
+  const int all = __reduce_add_sync(kFull, of_warp) * p.kv_heads;      // of one column tile
+  // no CTA gets less than a tile for each of its streams: joining costs more than a tile
+  const int tiles = (all - kUnitCost * p.B * p.kv_heads) * cts;
+  const Ranges ranges(all * cts, min((int)gridDim.x, (tiles + S::kMinTiles - 1) / S::kMinTiles));
   const int cta = blockIdx.x;
   const int t_begin = ranges.begin(cta), t_end = cta < ranges.ctas ? ranges.begin(cta + 1) : t_begin;
-  if (t_begin < t_end && before * units <= t_begin && t_begin < (before + sum) * units) {
+  const int ct = t_begin / all, in_ct = t_begin - ct * all;
+  if (t_begin < t_end && before <= in_ct && in_ct < before + sum * p.kv_heads) {
     int b = b0, at = before;
     for (;; ++b) {
       int first, n;
       unit_tiles<S::kTile>(p, max(0, __ldg(p.seq_lens + b)), first, n);
-      if (t_begin < (at + n) * units) break;
-      at += n;
+      if (in_ct < at + (n + kUnitCost) * p.kv_heads) break;
+      at += (n + kUnitCost) * p.kv_heads;
     }
     ctl->start_b = b;
-    ctl->start_before = at * units;
+    ctl->start_before = at;
   }
   __syncthreads();
   Walk<S::kTile> w{};
   w.left = t_end - t_begin;
-  w.units = units;
   if (w.left > 0) {
+    w.ct = ct;
     w.b = ctl->start_b;
     w.load(p);
-    const int in = t_begin - ctl->start_before;
-    w.unit = in / w.n;
-    w.at = in - w.unit * w.n;
-    w.take();
+    const int in = in_ct - ctl->start_before, each = w.n + kUnitCost;
+    w.kvh = in / each;
+    w.pos = t_begin - (in - w.kvh * each);
+    w.take(in - w.kvh * each);
     const uint32_t tmem = ctl->tmem_base;
     Cta<D, NC> c{p, stages, qbuf, wbuf, ctl};
     if (warp == 0) {
@@ -965,7 +1003,7 @@ __global__ void __launch_bounds__(Shape<D, NC>::kThreads, 1) kv8_decode_kernel(c
 template <int D, int NC>
 constexpr size_t smem_bytes() {
   using S = Shape<D, NC>;
-  return 1024 + (size_t)S::kStages * S::kStageBytes + 2 * S::kQBytes + 2 * S::kWBytes + sizeof(Control<NC, S::kStages, S::kPages, S::kThreads / 32>);
+  return 1024 + (size_t)S::kStages * S::kStageBytes + 2 * S::kQBytes + S::kStreams * S::kWBytes + sizeof(Control<NC, S::kStages, S::kPages, S::kHalves, S::kThreads / 32>);
 }
 
 template <int D, int NC, bool kHalf>
@@ -991,19 +1029,15 @@ cudaError_t launch(const Kv8DecodeParams& p, cudaStream_t stream) {
 
 template <int D, bool kHalf>
 cudaError_t launch_columns(const Kv8DecodeParams& p, cudaStream_t stream) {
-  switch (kv8_decode_columns(p.Q, p.group)) {
-    case 8: return launch<D, 8, kHalf>(p, stream);
-    case 16: return launch<D, 16, kHalf>(p, stream);
-    default: return launch<D, 32, kHalf>(p, stream);
-  }
+  if (kv8_decode_columns(p.Q, p.group) == 8) return launch<D, 8, kHalf>(p, stream);
+  return launch<D, 16, kHalf>(p, stream);
 }
 
 }  // namespace
 
 // Columns of a tile: the softmax's work grows with them, and so does what a key is read for.
 int kv8_decode_columns(int Q, int group) {
-  const int n = Q * group;
-  return n <= 8 ? 8 : (n <= 16 ? 16 : 32);
+  return Q * group <= 8 ? 8 : 16;
 }
 
 cudaError_t launch_kv8_decode(const Kv8DecodeParams& p, int head_dim, bool fp16, cudaStream_t stream) {
