@@ -52,6 +52,8 @@ def lib_path() -> str:
 def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
     """Load (building first if needed) the CUDA library; raise if impossible."""
     global _LIB
+    if _LIB is not None:
+        return _LIB
     with _LOCK:
         if _LIB is not None:
             return _LIB
@@ -443,25 +445,38 @@ def sparse_mla_decode_shared(q, kv_cache, page_table, shared_indices, member_mas
 
 
 # ------------------------------------------------------------------ 8-bit per-head cache
+# A step's small calls are bound by what the host does for them, so these entry points take each
+# attribute of a tensor once and go to _check only for its message.
+def _ptr_of(t, name, dtype, index, ndim, contiguous=True):
+    """Address of t, which is a tensor of this type and number of axes on CUDA device `index`."""
+    if not (t.dtype is dtype and t.get_device() == index >= 0 and t.dim() == ndim and (not contiguous or t.is_contiguous())):
+        import torch
+        _check(t, name, dtype, torch.device("cuda", index) if index >= 0 else None, ndim, contiguous)
+    return t.data_ptr()
+
+
+def _optional_ptr(t, name, index):
+    import torch
+    return None if t is None else _ptr_of(t, name, torch.int32, index, 1)
+
+
+def _raw_stream(stream, index):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
 def _kv8_dtype(t, name) -> int:
     import torch
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return 0    # NVFP4MLA_BF16
-    if t.dtype == torch.float16:
+    if t.dtype is torch.float16:
         return 1    # NVFP4MLA_FP16
     raise TypeError(f"{name}: expected torch.bfloat16 or torch.float16, got {t.dtype}")
 
 
-def _kv8_cache_check(cache, kv_heads, head_dim):
-    import torch
-    _check(cache, "cache", torch.uint8, ndim=2)
-    if cache.shape[1] != kv8_page_bytes(kv_heads, head_dim):
-        raise ValueError("cache must be [num_pages, kv8_page_bytes(kv_heads, head_dim)]")
-
-
 def kv8_page_bytes(kv_heads: int, head_dim: int) -> int:
     """Bytes of one 64-token page of the 8-bit per-head cache (head_dim 64 or 128)."""
-    n = int(load_library().kv8_page_bytes(kv_heads, head_dim))
+    n = load_library().kv8_page_bytes(kv_heads, head_dim)
     if n == 0:
         raise ValueError("kv_heads must be 1..256 and head_dim 64 or 128")
     return n
@@ -473,29 +488,31 @@ def kv8_append(k, v, cu_tokens, seq_lens, page_table, cache, dev_status=None, st
     become its newest tokens; cu_tokens int32 [B+1], seq_lens int32 [B] with the new ones counted,
     page_table int32 [B, max_pages]."""
     import torch
+    lib, i32 = load_library(), torch.int32
     dt = _kv8_dtype(k, "k")
-    _check(k, "k", k.dtype, None, 3, contiguous=False)
-    dev = k.device
-    _check(v, "v", k.dtype, dev, 3, contiguous=False)
+    index = k.get_device()
+    kp, vp = _ptr_of(k, "k", k.dtype, index, 3, False), _ptr_of(v, "v", k.dtype, index, 3, False)
     n, hk, d = k.shape
     if v.shape != k.shape:
         raise ValueError("k and v must have the same shape")
-    if n and (k.stride(2) != 1 or v.stride(2) != 1):
+    (k0, k1, k2), (v0, v1, v2) = k.stride(), v.stride()
+    if n and (k2 != 1 or v2 != 1):
         raise ValueError("k and v must be contiguous along the feature axis")
-    _kv8_cache_check(cache, hk, d)
-    _check(cache, "cache", torch.uint8, dev)
-    _check(cu_tokens, "cu_tokens", torch.int32, dev, 1)
-    _check(seq_lens, "seq_lens", torch.int32, dev, 1)
-    _check(page_table, "page_table", torch.int32, dev, 2)
+    cp = _ptr_of(cache, "cache", torch.uint8, index, 2)
+    pages, page_bytes = cache.shape
+    if page_bytes != kv8_page_bytes(hk, d):
+        raise ValueError("cache must be [num_pages, kv8_page_bytes(kv_heads, head_dim)]")
+    cup, sp, pp = (_ptr_of(cu_tokens, "cu_tokens", i32, index, 1), _ptr_of(seq_lens, "seq_lens", i32, index, 1),
+                   _ptr_of(page_table, "page_table", i32, index, 2))
     B = seq_lens.shape[0]
     if cu_tokens.shape[0] != B + 1 or page_table.shape[0] != B:
         raise ValueError("shape mismatch")
-    if dev_status is not None:
-        _check(dev_status, "dev_status", torch.int32, dev, 1)
-    # the stride of an axis of one entry is never used and may be anything
-    ks, vs = ((t.stride(0) if n > 1 else 0, t.stride(1) if hk > 1 else 0) for t in (k, v))
-    rc = load_library().kv8_append(_ptr(k), *ks, _ptr(v), *vs, dt, n, _ptr(cu_tokens), _ptr(seq_lens),
-                                   _ptr(page_table), page_table.shape[1], B, hk, d, _ptr(cache), cache.shape[0], _ptr(dev_status), _stream_ptr(stream))
+    if n <= 1:      # the stride of an axis of one entry is never used and may be anything
+        k0 = v0 = 0
+    if hk == 1:
+        k1 = v1 = 0
+    rc = lib.kv8_append(kp, k0, k1, vp, v0, v1, dt, n, cup, sp, pp, page_table.shape[1], B, hk, d, cp, pages,
+                        _optional_ptr(dev_status, "dev_status", index), _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv8_append")
 
@@ -511,38 +528,35 @@ def kv8_decode(q, cache, page_table, seq_lens, kv_heads: int, softmax_scale, win
     [B, max_pages], seq_lens int32 [B]; window > 0: the newest `window` positions only. Returns (out as q's
     type [B, Q, H, head_dim], lse fp32 [B, Q, H])."""
     import torch
+    lib, i32 = load_library(), torch.int32
     dt = _kv8_dtype(q, "q")
-    _check(q, "q", q.dtype, None, 4, contiguous=False)
-    dev = q.device
-    B, Q, H, d = q.shape
+    index = q.get_device()
+    qp = _ptr_of(q, "q", q.dtype, index, 4, False)
+    shape = B, Q, H, d = q.shape
     s0, s1, s2, s3 = q.stride()
     if s3 != 1 or (B > 1 and Q > 1 and s0 != Q * s1):
         raise ValueError("q must be contiguous along the feature axis, and its batch stride Q times its query stride")
-    _kv8_cache_check(cache, kv_heads, d)
-    _check(cache, "cache", torch.uint8, dev)
-    _check(page_table, "page_table", torch.int32, dev, 2)
-    _check(seq_lens, "seq_lens", torch.int32, dev, 1)
-    if seq_lens.shape[0] != B or page_table.shape[0] != B:
+    cp = _ptr_of(cache, "cache", torch.uint8, index, 2)
+    pages, page_bytes = cache.shape
+    if page_bytes != kv8_page_bytes(kv_heads, d):
+        raise ValueError("cache must be [num_pages, kv8_page_bytes(kv_heads, head_dim)]")
+    pp, sp = _ptr_of(page_table, "page_table", i32, index, 2), _ptr_of(seq_lens, "seq_lens", i32, index, 1)
+    rows, max_pages = page_table.shape
+    if seq_lens.shape[0] != B or rows != B:
         raise ValueError("shape mismatch")
     if out is None:
-        out = torch.empty((B, Q, H, d), dtype=q.dtype, device=dev)
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
     if lse is None:
-        lse = torch.empty((B, Q, H), dtype=torch.float32, device=dev)
-    _check(out, "out", q.dtype, dev, 4)
-    _check(lse, "lse", torch.float32, dev, 3)
-    if out.shape != q.shape or lse.shape != q.shape[:3]:
+        lse = torch.empty((B, Q, H), dtype=torch.float32, device=q.device)
+    op, lp = _ptr_of(out, "out", q.dtype, index, 4), _ptr_of(lse, "lse", torch.float32, index, 3)
+    if out.shape != shape or lse.shape != shape[:3]:
         raise ValueError("out must be [B, Q, H, head_dim] and lse [B, Q, H]")
     if workspace is None:
-        workspace = torch.empty(max(kv8_decode_workspace_size(B, Q, H, kv_heads, d), 1), dtype=torch.uint8, device=dev)
-    if dev_status is not None:
-        _check(dev_status, "dev_status", torch.int32, dev, 1)
-    token_stride, head_stride = s1 if Q > 1 else s0 if B > 1 else 0, s2 if H > 1 else 0
-    rc = load_library().kv8_decode(_ptr(q), token_stride, head_stride, dt, _ptr(cache), cache.shape[0], _ptr(page_table),
-                                   page_table.shape[1], _ptr(seq_lens), B, Q, H, kv_heads, d, float(softmax_scale),
-                                   int(window), _ptr(out), _ptr(lse), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _ptr(dev_status),
-                                   (int(max_ctas) & 0xFFFF) | (FLAG_TEST_TIMEOUT if test_timeout else 0),
-                                   _stream_ptr(stream))
+        workspace = torch.empty(max(kv8_decode_workspace_size(B, Q, H, kv_heads, d), 1), dtype=torch.uint8, device=q.device)
+    rc = lib.kv8_decode(qp, s1 if Q > 1 else s0 if B > 1 else 0, s2 if H > 1 else 0, dt, cp, pages, pp, max_pages, sp,
+                        B, Q, H, kv_heads, d, softmax_scale, window, op, lp, workspace.data_ptr(), workspace.nbytes,
+                        _optional_ptr(dev_status, "dev_status", index),
+                        (max_ctas & 0xFFFF) | (FLAG_TEST_TIMEOUT if test_timeout else 0), _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv8_decode")
     return out, lse
@@ -550,57 +564,57 @@ def kv8_decode(q, cache, page_table, seq_lens, kv_heads: int, softmax_scale, win
 
 # ------------------------------------------------------------------ pages
 def _pages_of(cache, layered):
-    """(layers, layer stride in bytes, pages, bytes of a page) of a cache uint8 [P, ...], or [layers, P, ...]."""
+    """(address, layers, layer stride in bytes, pages, bytes of a page, device index) of a cache uint8
+    [P, ...], or [layers, P, ...]."""
     import torch
-    _check(cache, "cache", torch.uint8)
+    index, shape = cache.get_device(), cache.shape
+    cp = _ptr_of(cache, "cache", torch.uint8, index, len(shape))
     first = 1 if layered else 0
-    if cache.dim() < first + 2:
+    if len(shape) < first + 2:
         raise ValueError("cache must be [num_pages, ...]" if not layered else "cache must be [layers, num_pages, ...]")
-    pages = cache.shape[first]
-    each = cache.numel() // max(1, pages * (cache.shape[0] if layered else 1))
-    return (cache.shape[0], pages * each, pages, each) if layered else (1, 0, pages, each)
-
-
-def _page_state(page_table, refcounts, dev, seq_lens=None, dev_status=None):
-    import torch
-    _check(page_table, "page_table", torch.int32, dev, 2)
-    _check(refcounts, "refcounts", torch.int32, dev, 1)
-    if seq_lens is not None:
-        _check(seq_lens, "seq_lens", torch.int32, dev, 1)
-        if seq_lens.shape[0] != page_table.shape[0]:
-            raise ValueError("seq_lens and page_table must have one row per sequence")
-    if dev_status is not None:
-        _check(dev_status, "dev_status", torch.int32, dev, 1)
+    layers, pages = shape[0] if layered else 1, shape[first]
+    each = cache.numel() // max(1, pages * layers)
+    return cp, layers, pages * each if layered else 0, pages, each, index
 
 
 def kv_pages_copy(cache, src, dst, dev_status=None, stream=None, layered: bool = False) -> None:
     """Page dst[i] of the cache (uint8 [P, ...]; layered: [layers, P, ...]) becomes a copy of page src[i]
     (int32 [n], -1 = skip). No dst twice, and none that is another pair's src."""
     import torch
-    layers, stride, pages, each = _pages_of(cache, layered)
-    dev = cache.device
-    _check(src, "src", torch.int32, dev, 1)
-    _check(dst, "dst", torch.int32, dev, 1)
-    if src.shape != dst.shape:
+    lib, i32 = load_library(), torch.int32
+    cp, layers, stride, pages, each, index = _pages_of(cache, layered)
+    sp, dp = _ptr_of(src, "src", i32, index, 1), _ptr_of(dst, "dst", i32, index, 1)
+    n = src.shape[0]
+    if dst.shape[0] != n:
         raise ValueError("src and dst must have the same length")
-    if dev_status is not None:
-        _check(dev_status, "dev_status", torch.int32, dev, 1)
-    rc = load_library().kv_pages_copy(_ptr(cache), layers, stride, pages, each, _ptr(src), _ptr(dst), src.shape[0],
-                                      _ptr(dev_status), _stream_ptr(stream))
+    rc = lib.kv_pages_copy(cp, layers, stride, pages, each, sp, dp, n, _optional_ptr(dev_status, "dev_status", index),
+                           _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv_pages_copy")
+
+
+def _page_state(page_table, seq_lens, refcounts, index):
+    """Addresses and sizes of the page operators' state: table, its width, lengths, sequences, counts, pages."""
+    import torch
+    i32 = torch.int32
+    pp, rp = _ptr_of(page_table, "page_table", i32, index, 2), _ptr_of(refcounts, "refcounts", i32, index, 1)
+    seqs, width = page_table.shape
+    sp = None
+    if seq_lens is not None:
+        sp = _ptr_of(seq_lens, "seq_lens", i32, index, 1)
+        if seq_lens.shape[0] != seqs:
+            raise ValueError("seq_lens and page_table must have one row per sequence")
+    return pp, width, sp, seqs, rp, refcounts.shape[0]
 
 
 def kv_pages_free(page_table, seq_lens, refcounts, seqs, dev_status=None, stream=None) -> None:
     """Sequences seqs (int32 [n], -1 = skip) give up their pages: page_table int32 [S, max_pages], seq_lens
     int32 [S] and refcounts int32 [P] are updated in place."""
     import torch
-    dev = page_table.device
-    _page_state(page_table, refcounts, dev, seq_lens, dev_status)
-    _check(seqs, "seqs", torch.int32, dev, 1)
-    rc = load_library().kv_pages_free(_ptr(page_table), page_table.shape[1], _ptr(seq_lens), page_table.shape[0],
-                                      _ptr(refcounts), refcounts.shape[0], _ptr(seqs), seqs.shape[0],
-                                      _ptr(dev_status), _stream_ptr(stream))
+    index = page_table.get_device()
+    state = _page_state(page_table, seq_lens, refcounts, index)
+    rc = load_library().kv_pages_free(*state, _ptr_of(seqs, "seqs", torch.int32, index, 1), seqs.shape[0],
+                                      _optional_ptr(dev_status, "dev_status", index), _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv_pages_free")
 
@@ -611,21 +625,19 @@ def kv_pages_fork(cache, page_table, seq_lens, refcounts, src, dst, new_pages=No
     last page copied to a fresh one in the cache (uint8 [P, ...]; layered: [layers, P, ...]). Updates the
     tables in place; returns new_pages int32 [n]: the fresh page, -1 none needed, -2 refused."""
     import torch
-    layers, stride, pages, each = _pages_of(cache, layered)
-    dev = cache.device
-    _page_state(page_table, refcounts, dev, seq_lens, dev_status)
-    if refcounts.shape[0] != pages:
+    i32 = torch.int32
+    cp, layers, stride, pages, each, index = _pages_of(cache, layered)
+    pp, width, lp, seqs, rp, counts = _page_state(page_table, seq_lens, refcounts, index)
+    if counts != pages:
         raise ValueError("refcounts must have one entry per page of the cache")
-    _check(src, "src", torch.int32, dev, 1)
-    _check(dst, "dst", torch.int32, dev, 1)
+    sp, dp = _ptr_of(src, "src", i32, index, 1), _ptr_of(dst, "dst", i32, index, 1)
     if new_pages is None:
         new_pages = torch.empty_like(src)
-    _check(new_pages, "new_pages", torch.int32, dev, 1)
-    if src.shape != dst.shape or new_pages.shape != src.shape:
+    np_, n = _ptr_of(new_pages, "new_pages", i32, index, 1), src.shape[0]
+    if dst.shape[0] != n or new_pages.shape[0] != n:
         raise ValueError("src, dst and new_pages must have the same length")
-    rc = load_library().kv_pages_fork(_ptr(cache), layers, stride, pages, each, _ptr(page_table), page_table.shape[1],
-                                      _ptr(seq_lens), page_table.shape[0], _ptr(refcounts), _ptr(src), _ptr(dst),
-                                      src.shape[0], _ptr(new_pages), _ptr(dev_status), _stream_ptr(stream))
+    rc = load_library().kv_pages_fork(cp, layers, stride, pages, each, pp, width, lp, seqs, rp, sp, dp, n, np_,
+                                      _optional_ptr(dev_status, "dev_status", index), _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv_pages_fork")
     return new_pages
@@ -635,16 +647,13 @@ def kv_pages_extend(page_table, seq_lens, refcounts, add, granted=None, dev_stat
     """Sequence s grows by add[s] tokens (int32 [S]): fresh pages as needed, and the longer length. granted
     (int32 [S], optional): 1, or 0 for a sequence that was refused and left as it was."""
     import torch
-    dev = page_table.device
-    _page_state(page_table, refcounts, dev, seq_lens, dev_status)
-    for t, name in ((add, "add"), (granted, "granted")):
-        if t is not None:
-            _check(t, name, torch.int32, dev, 1)
-            if t.shape != seq_lens.shape:
-                raise ValueError(f"{name} must have one entry per sequence")
-    rc = load_library().kv_pages_extend(_ptr(page_table), page_table.shape[1], _ptr(seq_lens), page_table.shape[0],
-                                        _ptr(refcounts), refcounts.shape[0], _ptr(add), _ptr(granted),
-                                        _ptr(dev_status), _stream_ptr(stream))
+    index = page_table.get_device()
+    state = _page_state(page_table, seq_lens, refcounts, index)
+    ap, gp = _ptr_of(add, "add", torch.int32, index, 1), _optional_ptr(granted, "granted", index)
+    if add.shape[0] != state[3] or (granted is not None and granted.shape[0] != state[3]):
+        raise ValueError("add and granted must have one entry per sequence")
+    rc = load_library().kv_pages_extend(*state, ap, gp, _optional_ptr(dev_status, "dev_status", index),
+                                        _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv_pages_extend")
 
@@ -659,25 +668,23 @@ def kv_pages_compact(cache, page_table, refcounts, remap=None, num_live=None, wo
     counts follow in place. Returns (remap int32 [P]: where each page went, -1 for a free one; num_live int32
     [1]: how many are in use)."""
     import torch
-    layers, stride, pages, each = _pages_of(cache, layered)
-    dev = cache.device
-    _page_state(page_table, refcounts, dev, None, dev_status)
-    if refcounts.shape[0] != pages:
+    i32 = torch.int32
+    cp, layers, stride, pages, each, index = _pages_of(cache, layered)
+    pp, width, _, seqs, rp, counts = _page_state(page_table, None, refcounts, index)
+    if counts != pages:
         raise ValueError("refcounts must have one entry per page of the cache")
     if remap is None:
         remap = torch.empty_like(refcounts)
     if num_live is None:
-        num_live = torch.empty(1, dtype=torch.int32, device=dev)
-    _check(remap, "remap", torch.int32, dev, 1)
-    _check(num_live, "num_live", torch.int32, dev, 1)
-    if remap.shape != refcounts.shape or num_live.shape[0] < 1:
+        num_live = torch.empty(1, dtype=i32, device=cache.device)
+    mp, lp = _ptr_of(remap, "remap", i32, index, 1), _ptr_of(num_live, "num_live", i32, index, 1)
+    if remap.shape[0] != pages or num_live.shape[0] < 1:
         raise ValueError("remap must have one entry per page, num_live one")
     if workspace is None:
-        workspace = torch.empty(kv_pages_compact_workspace_size(pages), dtype=torch.uint8, device=dev)
-    rc = load_library().kv_pages_compact(_ptr(cache), layers, stride, pages, each, _ptr(page_table),
-                                         page_table.shape[1], page_table.shape[0], _ptr(refcounts), _ptr(remap),
-                                         _ptr(num_live), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                         _ptr(dev_status), _stream_ptr(stream))
+        workspace = torch.empty(kv_pages_compact_workspace_size(pages), dtype=torch.uint8, device=cache.device)
+    rc = load_library().kv_pages_compact(cp, layers, stride, pages, each, pp, width, seqs, rp, mp, lp,
+                                         workspace.data_ptr(), workspace.nbytes,
+                                         _optional_ptr(dev_status, "dev_status", index), _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv_pages_compact")
     return remap, num_live
