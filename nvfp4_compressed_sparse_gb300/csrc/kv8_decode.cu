@@ -13,9 +13,9 @@
 // they lie in the cache, without a conversion in between. E4M3 x E4M3 products do that: K and V
 // are the A operands straight from where TMA put them (K K-major, V M-major), and the 16-bit
 // operands, q and w, are written as sums of E4M3 parts, each a sixteenth of the one before:
-//   x = x_0 + x_1/16 + x_2/256 (+ x_3/4096),   x_i = E4M3(what is left x 16^i)
-// A part takes four bits of the significand, so three hold an fp16 exactly and four hold a weight
-// to 16 bits. The parts are further columns of the B operand (their products land in columns of
+//   x = x_0 + x_1/16 (+ x_2/256 (+ x_3/4096)),   x_i = E4M3(what is left x 16^i)
+// A part takes four bits of the significand, so two hold a bf16 exactly, three an fp16, and four hold
+// a weight to 16 bits. The parts are further columns of the B operand (their products land in columns of
 // their own and are added in fp32 afterwards), so that A is read from shared memory once.
 //
 // One CTA per SM, persistent. The tiles of all (request, key/value head, column tile) units form
@@ -47,28 +47,31 @@ namespace {
 using namespace ptx;
 
 constexpr int kRows = 128;             // 128-byte rows of K or V in a stage: a token each, or two of 64 dims
-constexpr int kQParts = 3, kWParts = 4;
+constexpr int kWParts = 4;
 constexpr float kHeadroom = 4.f;       // log2: how far above the reference a weight's exponent may come
 constexpr float kWeightScale = 4.f;    // log2: weights are held times 16, so that 2^4 above it is 256 <= 448
 constexpr float kSumHeadroom = 60.f;   // log2: the same for the sum, which fp32 holds
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
 // Sizes of the instance with D dims and NC columns.
-template <int D, int NC>
+template <int D, int NC, int kQ>
 struct Shape {
+  static constexpr int kQParts = kQ;                            // of a query element: 2 (bf16) or 3 (fp16)
   static constexpr bool kPair = D == 64;                        // a row is two tokens: one of each stream
-  // Two streams of tiles; a softmax warpgroup of a stream has eight columns (it is bound by latency, and
-  // with 16 columns two warpgroups took 0.6 of one's time).
-  static constexpr int kStreams = 2;
+  // A softmax warpgroup has eight columns (it is bound by latency: with 16 columns two warpgroups took
+  // 0.6 of one's time). Two streams of tiles keep up with memory at 128 dims (four measured 7 % slower:
+  // they end a unit later); at 64 dims half the bytes bring as many tokens, and it takes four.
+  static constexpr int kStreams = kPair && NC == 8 ? 4 : 2;
   static constexpr int kGroups = NC / 8;
-  static constexpr int kSoftmax = 2 * kGroups * 128;            // its threads
+  static constexpr int kSoftmax = kStreams * kGroups * 128;     // its threads
   static constexpr int kThreads = 128 + kSoftmax;
-  static constexpr int kStep = kPair ? 1 : 2;                   // a stream takes every kStep-th stage
+  static constexpr int kStep = kPair ? kStreams / 2 : kStreams; // a stream takes every kStep-th stage
   static constexpr int kHalves = kPair ? 2 : 1;                 // streams that read a stage
   static constexpr int kTile = kPair ? 256 : 128;               // tokens of a stage
   static constexpr int kPages = kTile / kPageTokens;
   static constexpr int kPageRows = kRows / kPages;
   static constexpr int kGroup = 32 / kPages;                    // stages whose page numbers are read together
+  static constexpr int kFewTiles = kPair ? 4 : 8;               // of a unit that is not worth splitting
   static constexpr int kMinTiles = kStep;                       // of a CTA: work for every stream
   static constexpr int kNS = (kQParts * NC + 15) / 16 * 16;     // columns of S
   static constexpr int kNO = kWParts * NC;                      // columns of O, bytes of a row of w
@@ -88,9 +91,8 @@ struct Shape {
   static_assert(kUsed <= 512 && kStages >= 3, "fits");
 };
 
-template <int NC, int kStages, int kPages, int kHalves, int kWarps>
+template <int NC, int kStages, int kPages, int kHalves, int kStreams, int kWarps>
 struct Control {
-  static constexpr int kStreams = 2;
   uint64_t full[kStages], empty[kStages][kHalves];     // empty: a stream's product with V is complete
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[kStreams][2], w_full[kStreams][2];   // per buffer of S
@@ -101,7 +103,8 @@ struct Control {
   int hi[2][NC], lo[2][NC];            // positions that a column attends to
   int row[2][NC];                      // of out and lse, -1: no column
   int at0[2], at1[2], cols[2];         // positions of the tile's first and last column; its columns
-  alignas(16) float top_w[kStreams][NC];   // M (these four are read four at a time)
+  alignas(16) float top_w[kStreams][NC];   // the weights' reference: M less kWeightScale (these four are
+                                           // read four at a time)
   alignas(16) float top_s[kStreams][NC];   // m
   alignas(16) float scale_o[kStreams][NC];
   alignas(16) float scale_l[kStreams][NC];
@@ -236,13 +239,17 @@ __device__ __forceinline__ int ordered(float x) {
 __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
-// 2^(a - b), 1 for equal infinities.
+// A reference before any position: far below every exponent, and finite, so that what is left out (an
+// exponent of -inf) stays 0 against it.
+constexpr float kNone = -1e30f;
+// 2^(a - b), 1 where the two are equal.
 __device__ __forceinline__ float ratio(float a, float b) { return a == b ? 1.f : ex2_approx(a - b); }
 
-template <int D, int NC>
+template <int D, int NC, int kQ>
 struct Cta {
-  using S = Shape<D, NC>;
-  using Ctl = Control<NC, S::kStages, S::kPages, S::kHalves, S::kThreads / 32>;
+  using S = Shape<D, NC, kQ>;
+  static constexpr int kQParts = kQ;
+  using Ctl = Control<NC, S::kStages, S::kPages, S::kHalves, S::kStreams, S::kThreads / 32>;
   using Walk = ::nvfp4mla::Walk<S::kTile>;
   const Kv8DecodeParams& p;
   uint8_t* stages;
@@ -367,7 +374,7 @@ struct Cta {
     constexpr uint32_t kId = idesc_e4m3(128, S::kNS, false, false);
     const uint64_t kd = sdesc(smem_u32(stages), 16, 1024, SW_128B), qd = sdesc(smem_u32(qbuf), 16, 8 * D, S::kSwQ);
     Ring ring;
-    uint32_t uses[2] = {0, 0};
+    uint32_t uses[2] = {0, 0};             // tiles that the streams of even and of odd stages have had
     bool ok = true;
     for (uint32_t seg = 0; ok && w.left > 0; ++seg, w.next(p)) {
       const uint32_t buf = seg & 1;
@@ -377,8 +384,8 @@ struct Cta {
         ok = wait(&ctl->full[ring.st], ring.phase);
 #pragma unroll
         for (int half = 0; half < S::kHalves; ++half) {
-          const int stream = S::kPair ? half : i & 1;
-          const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++, sb = u & 1;
+          const int turn = i & (S::kStep - 1), stream = S::kPair ? 2 * turn + half : turn;
+          const uint32_t u = turn == 0 ? uses[0] : uses[1], sb = u & 1;
           // this buffer's last S has been read once its weights are written (before the first, parity
           // 1 is that of the phase before any)
           ok = ok && wait(&ctl->w_full[stream][sb], ((u >> 1) & 1) ^ 1);
@@ -392,6 +399,7 @@ struct Cta {
             umma_f8_ss_w<1>(d, k_lo + 2 * k, (uint32_t)(kd >> 32), q_lo + 2 * k, (uint32_t)(qd >> 32), kId);
           umma_commit(&ctl->s_full[stream][sb]);
         }
+        ++(S::kStep == 1 || (i & 1) == 0 ? uses[0] : uses[1]);
         ring.next();
       }
       if (ok) umma_commit(&ctl->q_empty[buf]);
@@ -405,14 +413,14 @@ struct Cta {
     constexpr uint32_t kId = idesc_e4m3(D, S::kNO, true, true);
     const uint64_t vd = sdesc(smem_u32(stages + S::kRowBytes), 16, 1024, SW_128B), wd = sdesc(smem_u32(wbuf), 16, 8 * S::kNO, S::kSwW);
     Ring ring;
-    uint32_t uses[2] = {0, 0};
+    uint32_t uses[2] = {0, 0};             // tiles that the streams of even and of odd stages have had
     bool ok = true;
     for (; ok && w.left > 0; w.next(p)) {
       for (int i = 0; ok && i < w.count; ++i) {
 #pragma unroll
         for (int half = 0; half < S::kHalves; ++half) {
-          const int stream = S::kPair ? half : i & 1;
-          const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++;
+          const int turn = i & (S::kStep - 1), stream = S::kPair ? 2 * turn + half : turn;
+          const uint32_t u = turn == 0 ? uses[0] : uses[1];
           ok = ok && wait(&ctl->w_full[stream][u & 1], (u >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
@@ -424,6 +432,7 @@ struct Cta {
             umma_f8_ss_w<1>(d, v_lo + k * 256, (uint32_t)(vd >> 32), w_lo + k * 2 * S::kNO, (uint32_t)(wd >> 32), kId);
           umma_commit(&ctl->empty[ring.st][half]);
         }
+        ++(S::kStep == 1 || (i & 1) == 0 ? uses[0] : uses[1]);
         ring.next();
       }
     }
@@ -579,11 +588,11 @@ struct Cta {
   // columns: some partial results at a time, every load of them in flight together.
   template <bool kHalf>
   __device__ void join(const int* row, int c, int d, int c_lo, int c_hi, int first) {
-    constexpr int kN = 4, kSlots = S::kGroups == 1 ? 8 : 4;
+    constexpr int kN = NC / (S::kSoftmax / 128), kSlots = S::kThreads == 384 ? 8 : 16 / kN;
     float m[kN], sum[kN], acc[kN];
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-      m[k] = neg_inf();
+      m[k] = kNone;
       sum[k] = acc[k] = 0.f;
     }
 #pragma unroll 1
@@ -621,11 +630,11 @@ struct Cta {
     // the warpgroup's stream, and which of the columns are its own: own .. own + 7
     constexpr int kCols = 8, kStreams = S::kStreams;
     const int wi = (threadIdx.x >> 7) - 1, stream = wi % kStreams, grp = wi / kStreams, own = grp * kCols;
-    constexpr int kAll = S::kSoftmax, kAllBar = 2 * S::kGroups + 1;   // threads of the softmax, and their barrier
+    constexpr int kAll = S::kSoftmax, kAllBar = kAll / 128 + 1;   // threads of the softmax, and their barrier
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, r = threadIdx.x & 127;
     const uint32_t quarter = tmem + ((uint32_t)(warp * 32) << 16);
     const uint32_t s_at = quarter + stream * S::kBufs * S::kNS + own, o_at = quarter + S::kOCol + stream * S::kNO + own;
-    const int i0 = S::kPair ? 0 : stream, half = S::kPair ? stream : 0;
+    const int i0 = S::kPair ? stream >> 1 : stream, half = S::kPair ? stream & 1 : 0;
     const int t_first = ranges.begin(blockIdx.x);
     uint32_t g = 0, uses = 0;                             // stages before this segment; this stream's tiles
     uint32_t prev = 0;                                    // the stage of this stream's tile before
@@ -650,8 +659,12 @@ struct Cta {
         ok = ok && wait(&ctl->s_full[stream][sb], (uses >> 1) & 1);
         __syncwarp();
         tc_fence_after();
-        float z[kCols];
-        {
+        // the positions that columns attend to end or begin in some tiles: most rows are in for all of
+        // the columns or for none
+        const bool whole = pages == (1u << S::kPages) - 1 && t0 + S::kTile - 1 <= at0 && t0 >= all_lo;
+        const bool page_ok = (pages >> h) & 1;
+        const bool any = whole || (page_ok && t <= at1 && t >= any_lo), all = whole || (page_ok && t <= at0 && t >= all_lo);
+        auto scores = [&](float (&z)[kCols]) {
           uint32_t part[kQParts][kCols];
 #pragma unroll
           for (int k = 0; k < kQParts; ++k) tmem_ld8(s_at + sb * S::kNS + k * NC, part[k]);
@@ -661,30 +674,35 @@ struct Cta {
             const float4 f = *reinterpret_cast<const float4*>(&ctl->f[buf][own + k]);
             const float fs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-              z[k + n] = fmaf(__uint_as_float(part[2][k + n]), 1.f / 256.f,
-                              fmaf(__uint_as_float(part[1][k + n]), 1.f / 16.f, __uint_as_float(part[0][k + n]))) * (fs[n] * ks);
+            for (int n = 0; n < 4; ++n) {
+              float s = __uint_as_float(part[kQParts - 1][k + n]);
+#pragma unroll
+              for (int q = kQParts - 2; q >= 0; --q) s = fmaf(s, 1.f / 16.f, __uint_as_float(part[q][k + n]));
+              z[k + n] = s * (fs[n] * ks);
+            }
           }
-        }
-        if (!(pages == (1u << S::kPages) - 1 && t0 + S::kTile - 1 <= at0 && t0 >= all_lo)) {
-          // the positions that columns attend to end or begin here: most rows are in for all of them or for none
-          const bool page_ok = (pages >> h) & 1;
-          const bool any = page_ok && t <= at1 && t >= any_lo, all = page_ok && t <= at0 && t >= all_lo;
           if (!all) {
 #pragma unroll
             for (int c = 0; c < kCols; ++c)
               if (!any || t > ctl->hi[buf][own + c] || t < ctl->lo[buf][own + c]) z[c] = neg_inf();
-            if (ok && grp == 0) clean_row(stages + st * S::kStageBytes + S::kRowBytes, r, half, t, any, buf, stream);
           }
-        }
+        };
+        float a[kCols], b[kCols];
+        scores(b);
+        if (!all && ok && grp == 0) clean_row(stages + st * S::kStageBytes + S::kRowBytes, r, half, t, any, buf, stream);
+        // exponents against the references: of the weights, and of the sum
         bool raise = false;
 #pragma unroll
         for (int k = 0; k < kCols; k += 4) {
-          const float4 tw = *reinterpret_cast<const float4*>(&ctl->top_w[stream][own + k]);
-          const float4 ts = *reinterpret_cast<const float4*>(&ctl->top_s[stream][own + k]);
-          const float tws[4] = {tw.x, tw.y, tw.z, tw.w}, tss[4] = {ts.x, ts.y, ts.z, ts.w};
+          const float4 rw = *reinterpret_cast<const float4*>(&ctl->top_w[stream][own + k]);
+          const float4 rs = *reinterpret_cast<const float4*>(&ctl->top_s[stream][own + k]);
+          const float rws[4] = {rw.x, rw.y, rw.z, rw.w}, rss[4] = {rs.x, rs.y, rs.z, rs.w};
 #pragma unroll
-          for (int n = 0; n < 4; ++n) raise |= z[k + n] + ev > tws[n] + kHeadroom || z[k + n] > tss[n] + kSumHeadroom;
+          for (int n = 0; n < 4; ++n) {
+            a[k + n] = (b[k + n] + ev) - rws[n];
+            b[k + n] -= rss[n];
+            raise |= a[k + n] > kWeightScale + kHeadroom || b[k + n] > kSumHeadroom;
+          }
         }
         // the stream's weights before these have been read, and its O is at rest
         if (uses > 0) ok = ok && wait(&ctl->empty[prev % S::kStages][half], (prev / S::kStages) & 1);
@@ -693,13 +711,16 @@ struct Cta {
         __syncwarp();
         tc_fence_after();
         if (bar_any(1 + wi, 128, raise || !ok)) {
-          // rare after the first tiles: new references, the tile's own maxima where those are larger
+          // rare after the first tiles: new references, the tile's own maxima where those are larger (the
+          // scores are read again rather than kept in registers all the time)
+          float z[kCols];
+          scores(z);
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
-            const int a = __reduce_max_sync(kFull, ordered(z[c] + ev)), b = __reduce_max_sync(kFull, ordered(z[c]));
+            const int mw = __reduce_max_sync(kFull, ordered(z[c] + ev)), ms = __reduce_max_sync(kFull, ordered(z[c]));
             if (lane == 0) {
-              ctl->part_max[stream][warp][own + c][0] = unordered(a);
-              ctl->part_max[stream][warp][own + c][1] = unordered(b);
+              ctl->part_max[stream][warp][own + c][0] = unordered(mw);
+              ctl->part_max[stream][warp][own + c][1] = unordered(ms);
             }
           }
           if (bar_any(1 + wi, 128, !ok)) {
@@ -708,20 +729,25 @@ struct Cta {
           }
           if (r < kCols) {
             const int c = own + r;
-            const float a0 = ctl->top_w[stream][c], b0 = ctl->top_s[stream][c];
-            float a = a0, b = b0;
+            const float w0 = ctl->top_w[stream][c], s0 = ctl->top_s[stream][c];
+            float w1 = w0 + kWeightScale, s1 = s0;
             for (int k = 0; k < 4; ++k) {
-              a = fmaxf(a, ctl->part_max[stream][k][c][0]);
-              b = fmaxf(b, ctl->part_max[stream][k][c][1]);
+              w1 = fmaxf(w1, ctl->part_max[stream][k][c][0]);
+              s1 = fmaxf(s1, ctl->part_max[stream][k][c][1]);
             }
-            ctl->top_w[stream][c] = a;
-            ctl->top_s[stream][c] = b;
-            ctl->scale_o[stream][c] = ratio(a0, a);
-            ctl->scale_l[stream][c] = ratio(b0, b);
+            w1 = w1 > kNone / 2 ? w1 - kWeightScale : w0;
+            ctl->top_w[stream][c] = w1;
+            ctl->top_s[stream][c] = s1;
+            ctl->scale_o[stream][c] = ratio(w0, w1);
+            ctl->scale_l[stream][c] = ratio(s0, s1);
           }
           bar_sync(1 + wi, 128);
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) l[c] *= ctl->scale_l[stream][own + c];
+          for (int c = 0; c < kCols; ++c) {
+            l[c] *= ctl->scale_l[stream][own + c];
+            a[c] = (z[c] + ev) - ctl->top_w[stream][own + c];
+            b[c] = z[c] - ctl->top_s[stream][own + c];
+          }
           if (i >= S::kStep) {
             __syncwarp();
 #pragma unroll 1
@@ -741,16 +767,11 @@ struct Cta {
         uint32_t out[kWParts][2];
 #pragma unroll
         for (int k = 0; k < kCols; k += 4) {
-          const float4 tw = *reinterpret_cast<const float4*>(&ctl->top_w[stream][own + k]);
-          const float4 ts = *reinterpret_cast<const float4*>(&ctl->top_s[stream][own + k]);
-          const float tws[4] = {tw.x, tw.y, tw.z, tw.w}, tss[4] = {ts.x, ts.y, ts.z, ts.w};
           float e[4];
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
-            const int c = k + n;
-            const float mw = tws[n] == neg_inf() ? 0.f : tws[n] - kWeightScale, ms = tss[n] == neg_inf() ? 0.f : tss[n];
-            e[n] = ex2_approx(z[c] + ev - mw);
-            l[c] += ex2_approx(z[c] - ms);
+            e[n] = ex2_approx(a[k + n]);
+            l[k + n] += ex2_approx(b[k + n]);
           }
           uint32_t p01[kWParts], p23[kWParts];
           split_parts(e[0], e[1], p01);
@@ -778,8 +799,9 @@ struct Cta {
       if (!stop) {
 #pragma unroll
         for (int k = 0; k < kStreams; ++k) {
-          const uint32_t at = g + (S::kPair ? n - 1 : (n - 1 - k) / 2 * 2 + k);   // the stream's last stage
-          if (S::kPair || n > k) ok = ok && wait(&ctl->empty[at % S::kStages][S::kPair ? k : 0], (at / S::kStages) & 1);
+          const int from = S::kPair ? k >> 1 : k;
+          const uint32_t at = g + from + (n - 1 - from) / S::kStep * S::kStep;   // the stream's last stage
+          if (n > from) ok = ok && wait(&ctl->empty[at % S::kStages][S::kPair ? k & 1 : 0], (at / S::kStages) & 1);
         }
         __syncwarp();
         tc_fence_after();
@@ -806,11 +828,11 @@ struct Cta {
         return;
       }
       g += n;
-      constexpr int kN = 4;                               // columns whose streams this warpgroup adds
+      constexpr int kN = NC / (kAll / 128);               // columns whose streams this warpgroup adds
       const int c0 = wi * kN;
       if (r < kN) {
         const int c = c0 + r;
-        float m = neg_inf(), sum = 0.f;
+        float m = kNone, sum = 0.f;
 #pragma unroll
         for (int k = 0; k < kStreams; ++k) m = fmaxf(m, ctl->top_s[k][c]);
 #pragma unroll
@@ -818,8 +840,7 @@ struct Cta {
           float part = 0.f;
           for (int q = 0; q < 4; ++q) part += ctl->part_l[k][q][c];
           sum += part * ratio(ctl->top_s[k][c], m);
-          const float tw = ctl->top_w[k][c];
-          ctl->join_w[k][c] = tw == neg_inf() ? 0.f : ex2_approx(tw - kWeightScale - m);
+          ctl->join_w[k][c] = ex2_approx(ctl->top_w[k][c] - m);
         }
         ctl->join_m[c] = m;
         ctl->join_l[c] = sum;
@@ -835,10 +856,14 @@ struct Cta {
       float acc[kN] = {};
       // kept as a loop, as code that runs once costs what its fetching costs
 #pragma unroll 1
-      for (int k = 0; k < kStreams && (S::kPair || k < n); ++k) {
+      for (int k = 0; k < kStreams && (S::kPair ? k >> 1 : k) < n; ++k) {
         uint32_t o[kWParts][kN];
 #pragma unroll
-        for (int q = 0; q < kWParts; ++q) tmem_ld4(quarter + S::kOCol + k * S::kNO + q * NC + c0, o[q]);
+        for (int q = 0; q < kWParts; ++q) {
+          const uint32_t at = quarter + S::kOCol + k * S::kNO + q * NC + c0;
+          if constexpr (kN == 2) tmem_ld2(at, o[q]);
+          else tmem_ld4(at, o[q]);
+        }
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < kN; ++c) {
@@ -868,7 +893,7 @@ struct Cta {
       // the next segment starts from nothing
       bar_sync(kAllBar, kAll);
       if (r < kCols) {
-        ctl->top_w[stream][own + r] = ctl->top_s[stream][own + r] = neg_inf();
+        ctl->top_w[stream][own + r] = ctl->top_s[stream][own + r] = kNone;
         if (poisoned)
           for (int k = 0; k < 4; ++k) ctl->poison[stream][own + r][k] = 0;
       }
@@ -880,9 +905,9 @@ struct Cta {
 };
 
 template <int D, int NC, bool kHalf>
-__global__ void __launch_bounds__(Shape<D, NC>::kThreads, 1) kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p) {
-  using S = Shape<D, NC>;
-  using Ctl = Control<NC, S::kStages, S::kPages, S::kHalves, S::kThreads / 32>;
+__global__ void __launch_bounds__(Shape<D, NC, kHalf ? 3 : 2>::kThreads, 1) kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p) {
+  using S = Shape<D, NC, kHalf ? 3 : 2>;
+  using Ctl = Control<NC, S::kStages, S::kPages, S::kHalves, S::kStreams, S::kThreads / 32>;
   static_assert(offsetof(Ctl, scales) % 16 == 0 && offsetof(Ctl, f) % 16 == 0 && offsetof(Ctl, top_w) % 16 == 0 &&
                 offsetof(Ctl, top_s) % 16 == 0 && NC % 8 == 0, "vector accesses are aligned");
   static_assert(sizeof(Ctl) <= 6144, "the control block fits its share");
@@ -917,7 +942,7 @@ __global__ void __launch_bounds__(Shape<D, NC>::kThreads, 1) kv8_decode_kernel(c
     fence_barrier_init();
   }
   for (int i = tid; i < S::kStreams * NC; i += kThreads) {
-    ctl->top_w[i / NC][i % NC] = ctl->top_s[i / NC][i % NC] = neg_inf();
+    ctl->top_w[i / NC][i % NC] = ctl->top_s[i / NC][i % NC] = kNone;
     for (int k = 0; k < 4; ++k) ctl->poison[i / NC][i % NC][k] = 0;
   }
   if (warp == 1) {
@@ -925,6 +950,8 @@ __global__ void __launch_bounds__(Shape<D, NC>::kThreads, 1) kv8_decode_kernel(c
     tmem_relinquish();
   }
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // the whole sequence: every thread sums a run of requests
   const int cts = (p.Q * p.group + NC - 1) / NC;
   const int per = (p.B + kThreads - 1) / kThreads;
@@ -948,9 +975,11 @@ __global__ void __launch_bounds__(Shape<D, NC>::kThreads, 1) kv8_decode_kernel(c
   const int of_warp = lane < kThreads / 32 ? ctl->scan_sum[lane] : 0;
   const int before = (__reduce_add_sync(kFull, lane < warp ? of_warp : 0) + incl - sum) * p.kv_heads;
   const int all = __reduce_add_sync(kFull, of_warp) * p.kv_heads;      // of one column tile
-  // no CTA gets less than a tile for each of its streams: joining costs more than a tile
-  const int tiles = (all - kUnitCost * p.B * p.kv_heads) * cts;
-  const Ranges ranges(all * cts, min((int)gridDim.x, (tiles + S::kMinTiles - 1) / S::kMinTiles));
+  // no CTA gets less than a tile for each of its streams, and where units have few tiles, no less than
+  // an average unit: joining partial results costs some 4 us, a tile 0.6
+  const int units = p.B * p.kv_heads * cts, tiles = all * cts - kUnitCost * units;
+  const int most = tiles <= S::kFewTiles * units ? units : (tiles + S::kMinTiles - 1) / S::kMinTiles;
+  const Ranges ranges(all * cts, min((int)gridDim.x, most));
   const int cta = blockIdx.x;
   const int t_begin = ranges.begin(cta), t_end = cta < ranges.ctas ? ranges.begin(cta + 1) : t_begin;
   const int ct = t_begin / all, in_ct = t_begin - ct * all;
@@ -977,7 +1006,7 @@ __global__ void __launch_bounds__(Shape<D, NC>::kThreads, 1) kv8_decode_kernel(c
     w.pos = t_begin - (in - w.kvh * each);
     w.take(in - w.kvh * each);
     const uint32_t tmem = ctl->tmem_base;
-    Cta<D, NC> c{p, stages, qbuf, wbuf, ctl};
+    Cta<D, NC, kHalf ? 3 : 2> c{p, stages, qbuf, wbuf, ctl};
     if (warp == 0) {
       c.producer(w);
     } else if (warp == 1) {
@@ -1000,15 +1029,16 @@ __global__ void __launch_bounds__(Shape<D, NC>::kThreads, 1) kv8_decode_kernel(c
   }
 }
 
-template <int D, int NC>
+template <class S, int NC>
 constexpr size_t smem_bytes() {
-  using S = Shape<D, NC>;
-  return 1024 + (size_t)S::kStages * S::kStageBytes + 2 * S::kQBytes + S::kStreams * S::kWBytes + sizeof(Control<NC, S::kStages, S::kPages, S::kHalves, S::kThreads / 32>);
+  return 1024 + (size_t)S::kStages * S::kStageBytes + 2 * S::kQBytes + S::kStreams * S::kWBytes +
+         sizeof(Control<NC, S::kStages, S::kPages, S::kHalves, S::kStreams, S::kThreads / 32>);
 }
 
 template <int D, int NC, bool kHalf>
 cudaError_t launch(const Kv8DecodeParams& p, cudaStream_t stream) {
-  constexpr size_t smem = smem_bytes<D, NC>();
+  using S = Shape<D, NC, kHalf ? 3 : 2>;
+  constexpr size_t smem = smem_bytes<S, NC>();
   static_assert(smem <= 232448, "exceeds the 227 KB shared-memory limit");
   static std::mutex mu;
   static bool allowed[64] = {};
@@ -1023,8 +1053,19 @@ cudaError_t launch(const Kv8DecodeParams& p, cudaStream_t stream) {
       if (dev < 64) allowed[dev] = true;
     }
   }
-  kv8_decode_kernel<D, NC, kHalf><<<(unsigned)p.ctas, Shape<D, NC>::kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  // A dependent launch: a CTA sets itself up while the grid before it in the stream ends, and waits for
+  // all of that grid before it reads or writes memory.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.ctas, 1, 1);
+  cfg.blockDim = dim3(S::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv8_decode_kernel<D, NC, kHalf>, p);
 }
 
 template <int D, bool kHalf>
