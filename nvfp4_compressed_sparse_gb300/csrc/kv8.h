@@ -37,7 +37,7 @@ struct AppendParams {
 cudaError_t launch_kv8_append(const AppendParams& p, int head_dim, bool fp16, cudaStream_t stream);
 
 struct Kv8DecodeParams {
-  CUtensorMap cache_map;         // [pages][2 kv_heads][64 tokens][D bytes]
+  CUtensorMap cache_map;         // see encode_pages_map
   const uint16_t* q;
   int64_t q_token_stride, q_head_stride;
   const uint8_t* cache;

@@ -89,19 +89,21 @@ static Kv8Workspace decode_workspace(int columns, int head_dim, int ctas) {
   return w;
 }
 
-// The cache as a 4-D tensor of bytes: [pages][codes of a kind and head][rows][128]: a token a row, or
-// two of 64 dims. One box is the rows of one kind and head of one page, swizzled as the tensor cores
-// read them; a page number behind the cache reads as zeros, from nowhere.
+// The cache as a 5-D tensor of bytes: [pages][1 KB groups of a kind's heads][kinds][8 rows][128], a row
+// being a token, or two of 64 dims. One box is a head's keys and values of one page, eight rows of the
+// one beside eight of the other, so that the groups of either lie at one stride in shared memory, page
+// after page; swizzled as the tensor cores read them. A page number behind the cache reads as zeros,
+// from nowhere.
 static bool encode_pages_map(CUtensorMap* map, const void* cache, int64_t num_pages, int64_t page_bytes, int kv_heads,
                              int head_dim) {
   EncodeTiledFn fn = encode_tiled_fn();
   if (fn == nullptr) return false;
-  const cuuint64_t block = (cuuint64_t)kPageTokens * head_dim, rows = block / 128;
-  const cuuint64_t dims[4] = {128, rows, (cuuint64_t)(2 * kv_heads), (cuuint64_t)num_pages};
-  const cuuint64_t strides[3] = {128, block, (cuuint64_t)page_bytes};
-  const cuuint32_t box[4] = {128, (cuuint32_t)rows, 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(cache), dims, strides, box, estr,
+  const cuuint64_t block = (cuuint64_t)kPageTokens * head_dim, groups = block / 1024;
+  const cuuint64_t dims[5] = {128, 8, 2, groups * (cuuint64_t)kv_heads, (cuuint64_t)num_pages};
+  const cuuint64_t strides[4] = {128, block * (cuuint64_t)kv_heads, 1024, (cuuint64_t)page_bytes};
+  const cuuint32_t box[5] = {128, 8, 2, (cuuint32_t)groups, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(cache), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

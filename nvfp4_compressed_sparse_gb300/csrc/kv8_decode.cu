@@ -75,8 +75,7 @@ struct Shape {
   static constexpr int kMinTiles = kStep;                       // of a CTA: work for every stream
   static constexpr int kNS = (kQParts * NC + 15) / 16 * 16;     // columns of S
   static constexpr int kNO = kWParts * NC;                      // columns of O, bytes of a row of w
-  static constexpr int kRowBytes = kRows * 128;                 // K or V of a stage
-  static constexpr int kStageBytes = 2 * kRowBytes;             // the scale bytes have an area of their own
+  static constexpr int kStageBytes = 2 * kRows * 128;           // groups of 8 rows of K and of V in turn
   static constexpr int kQBytes = (kNS * D + 1023) / 1024 * 1024;
   static constexpr int kWBytes = kRows * kNO;
   static constexpr int kBudget = 232448 - 1024 - 6144;          // less alignment and the control block
@@ -310,10 +309,9 @@ struct Cta {
         }
         const int m = min(S::kGroup, w.count - i);
         for (int k = 0; k < m; ++k, ++g) {
-          // a lane a copy: keys, values and scale bytes of every page (the codes of a page that is
-          // none read from behind the cache: zeros)
-          const int what = lane / S::kPages, h = lane % S::kPages;
-          const int page = __shfl_sync(kFull, mine, S::kPages * k + h);
+          // a lane a page: one box of its codes (a page that is none reads from behind the cache:
+          // zeros) and its scale bytes
+          const int page = __shfl_sync(kFull, mine, S::kPages * k + lane % S::kPages);
           const uint32_t have = __ballot_sync(kFull, page >= 0) & ((1u << S::kPages) - 1);
           const uint32_t st = g % S::kStages, round = g / S::kStages;
           bool ok = true;
@@ -321,16 +319,15 @@ struct Cta {
             for (int k = 0; k < S::kHalves; ++k) ok = ok && wait(&ctl->empty[st][k], (round & 1) ^ 1);
             if (ok) {
               ctl->pages_ok[st] = have;
-              mbar_arrive_expect_tx(&ctl->full[st], 2 * S::kRowBytes);
+              mbar_arrive_expect_tx(&ctl->full[st], S::kStageBytes);
             }
           }
           ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
-          if (ok && what < 2)
-            tma_load_4d(stages + st * S::kStageBytes + what * S::kRowBytes + h * kPageTokens * D, &p.cache_map, 0, 0,
-                        what * p.kv_heads + kvh, page >= 0 ? page : (int)p.num_pages, &ctl->full[st]);
-          if (ok && what == 0) {
+          if (ok && lane < S::kPages) {
+            tma_load_5d(stages + st * S::kStageBytes + lane * 2 * kPageTokens * D, &p.cache_map, 0, 0, 0, kvh * (kPageTokens * D / 1024),
+                        page >= 0 ? page : (int)p.num_pages, &ctl->full[st]);
             // (a TMA copy takes the warp some 80 ns, a load-store copy by all lanes at once a few)
-            if (page >= 0) cp_async_16(&ctl->scales[st][h], p.cache + page * p.page_bytes + kv8_scales_off(p.kv_heads, D, kvh & ~1));
+            if (page >= 0) cp_async_16(&ctl->scales[st][lane], p.cache + page * p.page_bytes + kv8_scales_off(p.kv_heads, D, kvh & ~1));
             cp_async_arrive(&ctl->full[st]);
           }
           __syncwarp();
@@ -372,7 +369,7 @@ struct Cta {
   // ---------------------------------------------------------------- S = K q (warp 1, one thread)
   __device__ void issue_s(Walk w, uint32_t tmem) {
     constexpr uint32_t kId = idesc_e4m3(128, S::kNS, false, false);
-    const uint64_t kd = sdesc(smem_u32(stages), 16, 1024, SW_128B), qd = sdesc(smem_u32(qbuf), 16, 8 * D, S::kSwQ);
+    const uint64_t kd = sdesc(smem_u32(stages), 16, 2048, SW_128B), qd = sdesc(smem_u32(qbuf), 16, 8 * D, S::kSwQ);
     Ring ring;
     uint32_t uses[2] = {0, 0};             // tiles that the streams of even and of odd stages have had
     bool ok = true;
@@ -411,7 +408,7 @@ struct Cta {
   // ---------------------------------------------------------------- O += V w (warp 3, one thread)
   __device__ void issue_o(Walk w, uint32_t tmem) {
     constexpr uint32_t kId = idesc_e4m3(D, S::kNO, true, true);
-    const uint64_t vd = sdesc(smem_u32(stages + S::kRowBytes), 16, 1024, SW_128B), wd = sdesc(smem_u32(wbuf), 16, 8 * S::kNO, S::kSwW);
+    const uint64_t vd = sdesc(smem_u32(stages + 1024), 16, 2048, SW_128B), wd = sdesc(smem_u32(wbuf), 16, 8 * S::kNO, S::kSwW);
     Ring ring;
     uint32_t uses[2] = {0, 0};             // tiles that the streams of even and of odd stages have had
     bool ok = true;
@@ -429,7 +426,7 @@ struct Cta {
           umma_f8_ss_w<-1>(d, v_lo, (uint32_t)(vd >> 32), w_lo, (uint32_t)(wd >> 32), kId, i >= S::kStep ? 1u : 0u);
 #pragma unroll
           for (int k = 1; k < kRows / 32; ++k)
-            umma_f8_ss_w<1>(d, v_lo + k * 256, (uint32_t)(vd >> 32), w_lo + k * 2 * S::kNO, (uint32_t)(wd >> 32), kId);
+            umma_f8_ss_w<1>(d, v_lo + k * 512, (uint32_t)(vd >> 32), w_lo + k * 2 * S::kNO, (uint32_t)(wd >> 32), kId);
           umma_commit(&ctl->empty[ring.st][half]);
         }
         ++(S::kStep == 1 || (i & 1) == 0 ? uses[0] : uses[1]);
@@ -521,8 +518,7 @@ struct Cta {
   // ---------------------------------------------------------------- softmax (warps 4-11)
   // A token's row of V that no column attends to becomes zeros (it may hold anything), and a NaN in
   // one that only some columns attend to is taken out and noted for those.
-  __device__ void clean_row(uint8_t* vt, int r, int half, int t, bool any, uint32_t buf, int stream) {
-    uint8_t* row = vt + r * 128;
+  __device__ void clean_row(uint8_t* row, int r, int half, int t, bool any, uint32_t buf, int stream) {
     constexpr int kChunks = D / 16;
     const int c0 = half * kChunks;
 #pragma unroll 1
@@ -689,7 +685,7 @@ struct Cta {
         };
         float a[kCols], b[kCols];
         scores(b);
-        if (!all && ok && grp == 0) clean_row(stages + st * S::kStageBytes + S::kRowBytes, r, half, t, any, buf, stream);
+        if (!all && ok && grp == 0) clean_row(stages + st * S::kStageBytes + 1024 + (r >> 3) * 2048 + (r & 7) * 128, r, half, t, any, buf, stream);
         // exponents against the references: of the weights, and of the sum
         bool raise = false;
 #pragma unroll

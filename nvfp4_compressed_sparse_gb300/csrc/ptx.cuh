@@ -179,14 +179,14 @@ __device__ __forceinline__ uint64_t policy_evict_first() {
   return p;
 }
 
-// A box of a 4-D tensor map -> this CTA's shared memory. The innermost coordinate is 0 in every use
+// A box of a 5-D tensor map -> this CTA's shared memory. The innermost coordinate is 0 in every use
 // here, so that each copy starts on a 16-byte boundary; coordinates behind the tensor read as zeros.
-__device__ __forceinline__ void tma_load_4d(void* dst_smem, const void* map, int c0, int c1, int c2, int c3,
+__device__ __forceinline__ void tma_load_5d(void* dst_smem, const void* map, int c0, int c1, int c2, int c3, int c4,
                                             uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];" ::"r"(smem_u32(dst_smem)),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+      "%6}], [%7];" ::"r"(smem_u32(dst_smem)),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void prefetch_tensormap(const void* map) {
