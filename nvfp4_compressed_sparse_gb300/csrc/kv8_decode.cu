@@ -261,6 +261,11 @@ struct Cta {
     if (atomicExch(&ctl->abort, 1) == 0 && p.status != nullptr) atomicAdd(p.status + NVFP4MLA_STAT_TIMEOUT, 1);
     return false;
   }
+  // The product with V of the stage number g (and of a half of it) is complete. Not for a stage that may
+  // have been filled again and read since.
+  __device__ __forceinline__ bool product_done(uint32_t g, int half) {
+    return wait(&ctl->empty[g % S::kStages][half], (g / S::kStages) & 1);
+  }
   // First position that a query at `at` attends to.
   __device__ __forceinline__ int window_start(int at) const { return p.window > 0 && at + 1 > p.window ? at + 1 - p.window : 0; }
 
@@ -633,7 +638,6 @@ struct Cta {
     const int i0 = S::kPair ? stream >> 1 : stream, half = S::kPair ? stream & 1 : 0;
     const int t_first = ranges.begin(blockIdx.x);
     uint32_t g = 0, uses = 0;                             // stages before this segment; this stream's tiles
-    uint32_t prev = 0;                                    // the stage of this stream's tile before
     float l[kCols];
     for (uint32_t seg = 0; w.left > 0; ++seg, w.next(p)) {
       const uint32_t buf = seg & 1;
@@ -700,10 +704,9 @@ struct Cta {
             raise |= a[k + n] > kWeightScale + kHeadroom || b[k + n] > kSumHeadroom;
           }
         }
-        // the stream's weights before these have been read, and its O is at rest
-        if (uses > 0) ok = ok && wait(&ctl->empty[prev % S::kStages][half], (prev / S::kStages) & 1);
-        ++uses;
-        prev = gt;
+        // the stream's weights before these have been read, and its O is at rest (those of earlier segments
+        // are: a segment ends when all its products are complete, and the stages may have gone round since)
+        if (i >= S::kStep) ok = ok && product_done(gt - S::kStep, half);
         __syncwarp();
         tc_fence_after();
         if (bar_any(1 + wi, 128, raise || !ok)) {
@@ -759,6 +762,7 @@ struct Cta {
           }
         }
         // weights, as parts, into the token's row of the B operand
+        ++uses;
         uint8_t* wrow = wbuf + stream * S::kWBytes + r * S::kNO;
         uint32_t out[kWParts][2];
 #pragma unroll
@@ -797,7 +801,7 @@ struct Cta {
         for (int k = 0; k < kStreams; ++k) {
           const int from = S::kPair ? k >> 1 : k;
           const uint32_t at = g + from + (n - 1 - from) / S::kStep * S::kStep;   // the stream's last stage
-          if (n > from) ok = ok && wait(&ctl->empty[at % S::kStages][S::kPair ? k & 1 : 0], (at / S::kStages) & 1);
+          if (n > from) ok = ok && product_done(at, S::kPair ? k & 1 : 0);
         }
         __syncwarp();
         tc_fence_after();

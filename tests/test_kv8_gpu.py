@@ -205,6 +205,15 @@ def test_decode_any_split_gives_the_same_within_rounding(max_ctas):
     check(*c.run(max_ctas=max_ctas), c.reference())
 
 
+@pytest.mark.parametrize("D,Hk,G", [(64, 1, 2), (64, 2, 12), (128, 1, 4), (128, 3, 16)])
+@pytest.mark.parametrize("max_ctas", [0, 1, 3])
+def test_decode_many_requests_of_a_tile_or_two(D, Hk, G, max_ctas):
+    """Units of one tile leave one stream of tiles without work for many units in a row."""
+    lens = np.random.default_rng(D + G).choice([0, 1, 5, 100, 128, 129, 200, 256, 257, 300, 640], 90, p=[.1, .1, .1, .3, .1, .05, .05, .05, .05, .05, .05])
+    c = Case(lens, Hk, D, "fp16", G=G, seed=G)
+    check(*c.run(max_ctas=max_ctas), c.reference())
+
+
 def test_decode_scales_far_apart():
     """Blocks whose scales differ by up to 2^60, keys and values apart; and a block of zeros."""
     c = Case([300, 1200], 2, 128, "bf16", Q=2, G=4, seed=9)
