@@ -26,9 +26,8 @@
 //   warp 2     queries of the next unit: scaling by a power of two, parts, two buffers
 //   warps 4..  softmax: two streams of tiles, a warpgroup or two each (thread = token). Each stream has
 //              its own S, w and O, and keeps its own M, m, l; they are added at the unit's end
-// With 128 dims the streams take the stages in turn. With 64 dims a 128-byte row is two tokens (TMA
-// takes a cycle or so per row, and 64-byte rows would halve its rate): a stage is 256 tokens, the even
-// ones the one stream's and the odd ones the other's, whose operands start 64 bytes into the rows.
+// A stage is 128 rows of 128 bytes: a token each, or two tokens of 64 dims, which one softmax thread has
+// (TMA takes a cycle or so per row, and 64-byte rows would halve its rate).
 // A unit that several CTAs share is joined by whichever of them finishes last: the others leave
 // (m, l, O) in the workspace and count themselves.
 #include <cuda_bf16.h>
@@ -57,42 +56,43 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 template <int D, int NC, int kQ>
 struct Shape {
   static constexpr int kQParts = kQ;                            // of a query element: 2 (bf16) or 3 (fp16)
-  static constexpr bool kPair = D == 64;                        // a row is two tokens: one of each stream
-  // A softmax warpgroup has eight columns (it is bound by latency: with 16 columns two warpgroups took
-  // 0.6 of one's time). Two streams of tiles keep up with memory at 128 dims (four measured 7 % slower:
-  // they end a unit later); at 64 dims half the bytes bring as many tokens, and it takes four.
-  static constexpr int kStreams = kPair && NC == 8 ? 4 : 2;
+  static constexpr bool kPair = D == 64;                        // a row is two tokens
+  static constexpr int kHalves = kPair ? 2 : 1;                 // tokens of a row, and of a softmax thread
+  // Two streams, that take the stages in turn. A softmax warpgroup has eight columns: it is bound by
+  // latency, and with 16 columns two warpgroups took 0.6 of one's time.
+  static constexpr int kStreams = 2;
   static constexpr int kGroups = NC / 8;
   static constexpr int kSoftmax = kStreams * kGroups * 128;     // its threads
   static constexpr int kThreads = 128 + kSoftmax;
-  static constexpr int kStep = kPair ? kStreams / 2 : kStreams; // a stream takes every kStep-th stage
-  static constexpr int kHalves = kPair ? 2 : 1;                 // streams that read a stage
   static constexpr int kTile = kPair ? 256 : 128;               // tokens of a stage
   static constexpr int kPages = kTile / kPageTokens;
   static constexpr int kPageRows = kRows / kPages;
   static constexpr int kGroup = 32 / kPages;                    // stages whose page numbers are read together
   static constexpr int kFewTiles = kPair ? 4 : 8;               // of a unit that is not worth splitting
-  static constexpr int kMinTiles = kStep;                       // of a CTA: work for every stream
+  static constexpr int kMinTiles = kStreams;                    // of a CTA: work for every stream
   static constexpr int kNS = (kQParts * NC + 15) / 16 * 16;     // columns of S
-  static constexpr int kNO = kWParts * NC;                      // columns of O, bytes of a row of w
+  static constexpr int kNO = kWParts * NC;                      // columns of O of a half
+  static constexpr int kWRow = kHalves * kNO;                   // bytes of a row of w, columns of O
   static constexpr int kStageBytes = 2 * kRows * 128;           // groups of 8 rows of K and of V in turn
   static constexpr int kQBytes = (kNS * D + 1023) / 1024 * 1024;
-  static constexpr int kWBytes = kRows * kNO;
+  static constexpr int kWBytes = kRows * kWRow;
   static constexpr int kBudget = 232448 - 1024 - 6144;          // less alignment and the control block
   static constexpr int kFit = (kBudget - 2 * kQBytes - kStreams * kWBytes) / kStageBytes;
   static constexpr int kStages = kFit;
-  static constexpr int kBufs = 2;                               // S of the next tile while this one's is read
-  static constexpr int kOCol = kStreams * kBufs * kNS;          // TMEM columns: S of the streams, then O
-  static constexpr int kUsed = kOCol + kStreams * kNO;
+  // S of the next tile while this one's is read, where tensor memory holds it
+  static constexpr int kBufs = kStreams * (2 * kHalves * kNS + kWRow) <= 512 ? 2 : 1;
+  static constexpr int kSBuf = kHalves * kNS;                   // columns of a buffer of S
+  static constexpr int kOCol = kStreams * kBufs * kSBuf;        // TMEM columns: S of the streams, then O
+  static constexpr int kUsed = kOCol + kStreams * kWRow;
   static constexpr uint32_t kTmem = kUsed <= 256 ? 256 : 512;
   static constexpr uint32_t kSwQ = D == 128 ? SW_128B : SW_64B;
-  static constexpr uint32_t kSwW = kNO == 64 ? SW_64B : SW_32B;
+  static constexpr uint32_t kSwW = kWRow == 128 ? SW_128B : (kWRow == 64 ? SW_64B : SW_32B);
   static_assert(kUsed <= 512 && kStages >= 3, "fits");
 };
 
-template <int NC, int kStages, int kPages, int kHalves, int kStreams, int kWarps>
+template <int NC, int kStages, int kPages, int kStreams, int kWarps>
 struct Control {
-  uint64_t full[kStages], empty[kStages][kHalves];     // empty: a stream's product with V is complete
+  uint64_t full[kStages], empty[kStages];    // empty: the product with V is complete
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[kStreams][2], w_full[kStreams][2];   // per buffer of S
   uint64_t drain[2];
@@ -248,7 +248,7 @@ template <int D, int NC, int kQ>
 struct Cta {
   using S = Shape<D, NC, kQ>;
   static constexpr int kQParts = kQ;
-  using Ctl = Control<NC, S::kStages, S::kPages, S::kHalves, S::kStreams, S::kThreads / 32>;
+  using Ctl = Control<NC, S::kStages, S::kPages, S::kStreams, S::kThreads / 32>;
   using Walk = ::nvfp4mla::Walk<S::kTile>;
   const Kv8DecodeParams& p;
   uint8_t* stages;
@@ -261,11 +261,9 @@ struct Cta {
     if (atomicExch(&ctl->abort, 1) == 0 && p.status != nullptr) atomicAdd(p.status + NVFP4MLA_STAT_TIMEOUT, 1);
     return false;
   }
-  // The product with V of the stage number g (and of a half of it) is complete. Not for a stage that may
-  // have been filled again and read since.
-  __device__ __forceinline__ bool product_done(uint32_t g, int half) {
-    return wait(&ctl->empty[g % S::kStages][half], (g / S::kStages) & 1);
-  }
+  // The product with V of the stage number g is complete. Not for a stage that may have been filled
+  // again and read since.
+  __device__ __forceinline__ bool product_done(uint32_t g) { return wait(&ctl->empty[g % S::kStages], (g / S::kStages) & 1); }
   // First position that a query at `at` attends to.
   __device__ __forceinline__ int window_start(int at) const { return p.window > 0 && at + 1 > p.window ? at + 1 - p.window : 0; }
 
@@ -321,7 +319,7 @@ struct Cta {
           const uint32_t st = g % S::kStages, round = g / S::kStages;
           bool ok = true;
           if (lane == 0) {
-            for (int k = 0; k < S::kHalves; ++k) ok = ok && wait(&ctl->empty[st][k], (round & 1) ^ 1);
+            ok = wait(&ctl->empty[st], (round & 1) ^ 1);
             if (ok) {
               ctl->pages_ok[st] = have;
               mbar_arrive_expect_tx(&ctl->full[st], S::kStageBytes);
@@ -376,32 +374,31 @@ struct Cta {
     constexpr uint32_t kId = idesc_e4m3(128, S::kNS, false, false);
     const uint64_t kd = sdesc(smem_u32(stages), 16, 2048, SW_128B), qd = sdesc(smem_u32(qbuf), 16, 8 * D, S::kSwQ);
     Ring ring;
-    uint32_t uses[2] = {0, 0};             // tiles that the streams of even and of odd stages have had
+    uint32_t uses[2] = {0, 0};             // tiles that the streams have had
     bool ok = true;
     for (uint32_t seg = 0; ok && w.left > 0; ++seg, w.next(p)) {
       const uint32_t buf = seg & 1;
       ok = wait(&ctl->q_full[buf], (seg >> 1) & 1);
       const uint32_t q_lo = (uint32_t)qd + ((buf * S::kQBytes) >> 4);
       for (int i = 0; ok && i < w.count; ++i) {
+        const int stream = i & 1;
+        const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++, sb = u % S::kBufs;
         ok = wait(&ctl->full[ring.st], ring.phase);
+        // this buffer's last S has been read once its weights are written (before the first, parity 1 is
+        // that of the phase before any)
+        ok = ok && wait(&ctl->w_full[stream][sb], ((u / S::kBufs) & 1) ^ 1);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
         for (int half = 0; half < S::kHalves; ++half) {
-          const int turn = i & (S::kStep - 1), stream = S::kPair ? 2 * turn + half : turn;
-          const uint32_t u = turn == 0 ? uses[0] : uses[1], sb = u & 1;
-          // this buffer's last S has been read once its weights are written (before the first, parity
-          // 1 is that of the phase before any)
-          ok = ok && wait(&ctl->w_full[stream][sb], ((u >> 1) & 1) ^ 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = tmem + (stream * S::kBufs + sb) * S::kNS;
+          const uint32_t d = tmem + (stream * S::kBufs + sb) * S::kSBuf + half * S::kNS;
           const uint32_t k_lo = (uint32_t)kd + ((ring.st * S::kStageBytes + half * 64) >> 4);   // a row's first or second token
           umma_f8_ss_w<0>(d, k_lo, (uint32_t)(kd >> 32), q_lo, (uint32_t)(qd >> 32), kId);
 #pragma unroll
           for (int k = 1; k < D / 32; ++k)
             umma_f8_ss_w<1>(d, k_lo + 2 * k, (uint32_t)(kd >> 32), q_lo + 2 * k, (uint32_t)(qd >> 32), kId);
-          umma_commit(&ctl->s_full[stream][sb]);
         }
-        ++(S::kStep == 1 || (i & 1) == 0 ? uses[0] : uses[1]);
+        umma_commit(&ctl->s_full[stream][sb]);
         ring.next();
       }
       if (ok) umma_commit(&ctl->q_empty[buf]);
@@ -411,30 +408,30 @@ struct Cta {
   }
 
   // ---------------------------------------------------------------- O += V w (warp 3, one thread)
+  // With 64 dims the rows of V are 128 values, of two tokens, and those of w the weights of either: one
+  // product takes both. Of its 128 x 2 kNO results the even token's dims with the even token's weights
+  // are wanted, and the odd one's with the odd one's; the other half of the work costs less than twice
+  // as many instructions of this thread would.
   __device__ void issue_o(Walk w, uint32_t tmem) {
-    constexpr uint32_t kId = idesc_e4m3(D, S::kNO, true, true);
-    const uint64_t vd = sdesc(smem_u32(stages + 1024), 16, 2048, SW_128B), wd = sdesc(smem_u32(wbuf), 16, 8 * S::kNO, S::kSwW);
+    constexpr uint32_t kId = idesc_e4m3(128, S::kWRow, true, true);
+    const uint64_t vd = sdesc(smem_u32(stages + 1024), 16, 2048, SW_128B), wd = sdesc(smem_u32(wbuf), 16, 8 * S::kWRow, S::kSwW);
     Ring ring;
-    uint32_t uses[2] = {0, 0};             // tiles that the streams of even and of odd stages have had
+    uint32_t uses[2] = {0, 0};             // tiles that the streams have had
     bool ok = true;
     for (; ok && w.left > 0; w.next(p)) {
       for (int i = 0; ok && i < w.count; ++i) {
+        const int stream = i & 1;
+        const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++;
+        ok = wait(&ctl->w_full[stream][u % S::kBufs], (u / S::kBufs) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + S::kOCol + stream * S::kWRow;
+        const uint32_t v_lo = (uint32_t)vd + ((ring.st * S::kStageBytes) >> 4), w_lo = (uint32_t)wd + ((stream * S::kWBytes) >> 4);
+        umma_f8_ss_w<-1>(d, v_lo, (uint32_t)(vd >> 32), w_lo, (uint32_t)(wd >> 32), kId, i >= S::kStreams ? 1u : 0u);
 #pragma unroll
-        for (int half = 0; half < S::kHalves; ++half) {
-          const int turn = i & (S::kStep - 1), stream = S::kPair ? 2 * turn + half : turn;
-          const uint32_t u = turn == 0 ? uses[0] : uses[1];
-          ok = ok && wait(&ctl->w_full[stream][u & 1], (u >> 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = tmem + S::kOCol + stream * S::kNO;
-          const uint32_t v_lo = (uint32_t)vd + ((ring.st * S::kStageBytes + half * 64) >> 4), w_lo = (uint32_t)wd + ((stream * S::kWBytes) >> 4);
-          umma_f8_ss_w<-1>(d, v_lo, (uint32_t)(vd >> 32), w_lo, (uint32_t)(wd >> 32), kId, i >= S::kStep ? 1u : 0u);
-#pragma unroll
-          for (int k = 1; k < kRows / 32; ++k)
-            umma_f8_ss_w<1>(d, v_lo + k * 512, (uint32_t)(vd >> 32), w_lo + k * 2 * S::kNO, (uint32_t)(wd >> 32), kId);
-          umma_commit(&ctl->empty[ring.st][half]);
-        }
-        ++(S::kStep == 1 || (i & 1) == 0 ? uses[0] : uses[1]);
+        for (int k = 1; k < kRows / 32; ++k)
+          umma_f8_ss_w<1>(d, v_lo + k * 512, (uint32_t)(vd >> 32), w_lo + k * 2 * S::kWRow, (uint32_t)(wd >> 32), kId);
+        umma_commit(&ctl->empty[ring.st]);
         ring.next();
       }
     }
@@ -634,8 +631,9 @@ struct Cta {
     constexpr int kAll = S::kSoftmax, kAllBar = kAll / 128 + 1;   // threads of the softmax, and their barrier
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, r = threadIdx.x & 127;
     const uint32_t quarter = tmem + ((uint32_t)(warp * 32) << 16);
-    const uint32_t s_at = quarter + stream * S::kBufs * S::kNS + own, o_at = quarter + S::kOCol + stream * S::kNO + own;
-    const int i0 = S::kPair ? stream >> 1 : stream, half = S::kPair ? stream & 1 : 0;
+    // its own S and O; with 64 dims the lower lanes of O hold the even tokens' dims, the upper the odd ones'
+    const uint32_t s_at = quarter + stream * S::kBufs * S::kSBuf + own;
+    const uint32_t o_half = S::kPair && warp >= 2 ? S::kNO : 0, o_at = quarter + S::kOCol + stream * S::kWRow + o_half + own;
     const int t_first = ranges.begin(blockIdx.x);
     uint32_t g = 0, uses = 0;                             // stages before this segment; this stream's tiles
     float l[kCols];
@@ -647,27 +645,27 @@ struct Cta {
 #pragma unroll
       for (int c = 0; c < kCols; ++c) l[c] = 0.f;
       bool stop = false;
-      for (int i = i0; i < w.count; i += S::kStep) {
-        const uint32_t gt = g + i, st = gt % S::kStages, sb = uses & 1;
-        const int t0 = (w.first + w.at + i) * S::kTile, t = S::kPair ? t0 + 2 * r + half : t0 + r;
+      for (int i = stream; i < w.count; i += S::kStreams) {
+        const uint32_t gt = g + i, st = gt % S::kStages, sb = uses % S::kBufs;
+        const int t0 = (w.first + w.at + i) * S::kTile, t = t0 + S::kHalves * r;
         const int h = r / S::kPageRows;
         ok = ok && wait(&ctl->full[st], (gt / S::kStages) & 1);
         const uint32_t pages = ctl->pages_ok[st];
         const uint8_t* sc = reinterpret_cast<const uint8_t*>(&ctl->scales[st][h]) + (w.kvh & 1) * 8 + (t % kPageTokens) / kBlockTokens;
         const float ks = __uint_as_float((uint32_t)sc[0] << 23);
         const float ev = (float)((int)sc[4] - 127);
-        ok = ok && wait(&ctl->s_full[stream][sb], (uses >> 1) & 1);
+        ok = ok && wait(&ctl->s_full[stream][sb], (uses / S::kBufs) & 1);
         __syncwarp();
         tc_fence_after();
         // the positions that columns attend to end or begin in some tiles: most rows are in for all of
         // the columns or for none
         const bool whole = pages == (1u << S::kPages) - 1 && t0 + S::kTile - 1 <= at0 && t0 >= all_lo;
         const bool page_ok = (pages >> h) & 1;
-        const bool any = whole || (page_ok && t <= at1 && t >= any_lo), all = whole || (page_ok && t <= at0 && t >= all_lo);
-        auto scores = [&](float (&z)[kCols]) {
+        // exponents (log2 units) of the scores of a half's token
+        auto scores = [&](int half, float (&z)[kCols]) {
           uint32_t part[kQParts][kCols];
 #pragma unroll
-          for (int k = 0; k < kQParts; ++k) tmem_ld8(s_at + sb * S::kNS + k * NC, part[k]);
+          for (int k = 0; k < kQParts; ++k) tmem_ld8(s_at + sb * S::kSBuf + half * S::kNS + k * NC, part[k]);
           tmem_wait_ld();
 #pragma unroll
           for (int k = 0; k < kCols; k += 4) {
@@ -681,42 +679,60 @@ struct Cta {
               z[k + n] = s * (fs[n] * ks);
             }
           }
-          if (!all) {
+          if (!whole) {
 #pragma unroll
             for (int c = 0; c < kCols; ++c)
-              if (!any || t > ctl->hi[buf][own + c] || t < ctl->lo[buf][own + c]) z[c] = neg_inf();
+              if (!page_ok || t + half > ctl->hi[buf][own + c] || t + half < ctl->lo[buf][own + c]) z[c] = neg_inf();
           }
         };
-        float a[kCols], b[kCols];
-        scores(b);
-        if (!all && ok && grp == 0) clean_row(stages + st * S::kStageBytes + 1024 + (r >> 3) * 2048 + (r & 7) * 128, r, half, t, any, buf, stream);
-        // exponents against the references: of the weights, and of the sum
+        // and against the references: of the weights, and of the sum
+        float a[S::kHalves][kCols], b[S::kHalves][kCols];
+        auto against = [&](float (&a)[kCols], float (&b)[kCols]) {
+          bool raise = false;
+#pragma unroll
+          for (int k = 0; k < kCols; k += 4) {
+            const float4 rw = *reinterpret_cast<const float4*>(&ctl->top_w[stream][own + k]);
+            const float4 rs = *reinterpret_cast<const float4*>(&ctl->top_s[stream][own + k]);
+            const float rws[4] = {rw.x, rw.y, rw.z, rw.w}, rss[4] = {rs.x, rs.y, rs.z, rs.w};
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              a[k + n] = (b[k + n] + ev) - rws[n];
+              b[k + n] -= rss[n];
+              raise |= a[k + n] > kWeightScale + kHeadroom || b[k + n] > kSumHeadroom;
+            }
+          }
+          return raise;
+        };
         bool raise = false;
 #pragma unroll
-        for (int k = 0; k < kCols; k += 4) {
-          const float4 rw = *reinterpret_cast<const float4*>(&ctl->top_w[stream][own + k]);
-          const float4 rs = *reinterpret_cast<const float4*>(&ctl->top_s[stream][own + k]);
-          const float rws[4] = {rw.x, rw.y, rw.z, rw.w}, rss[4] = {rs.x, rs.y, rs.z, rs.w};
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            a[k + n] = (b[k + n] + ev) - rws[n];
-            b[k + n] -= rss[n];
-            raise |= a[k + n] > kWeightScale + kHeadroom || b[k + n] > kSumHeadroom;
+        for (int half = 0; half < S::kHalves; ++half) {
+          scores(half, b[half]);
+          raise |= against(a[half], b[half]);
+        }
+        if (!whole && ok && grp == 0) {
+          for (int half = 0; half < S::kHalves; ++half) {
+            const int at = t + half;
+            const bool any = page_ok && at <= at1 && at >= any_lo, all = page_ok && at <= at0 && at >= all_lo;
+            if (!all) clean_row(stages + st * S::kStageBytes + 1024 + (r >> 3) * 2048 + (r & 7) * 128, r, half, at, any, buf, stream);
           }
         }
         // the stream's weights before these have been read, and its O is at rest (those of earlier segments
         // are: a segment ends when all its products are complete, and the stages may have gone round since)
-        if (i >= S::kStep) ok = ok && product_done(gt - S::kStep, half);
+        if (i >= S::kStreams) ok = ok && product_done(gt - S::kStreams);
         __syncwarp();
         tc_fence_after();
         if (bar_any(1 + wi, 128, raise || !ok)) {
           // rare after the first tiles: new references, the tile's own maxima where those are larger (the
           // scores are read again rather than kept in registers all the time)
-          float z[kCols];
-          scores(z);
+#pragma unroll
+          for (int half = 0; half < S::kHalves; ++half) {
+            scores(half, b[half]);
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) a[0][c] = half == 0 ? b[0][c] : fmaxf(a[0][c], b[half][c]);
+          }
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
-            const int mw = __reduce_max_sync(kFull, ordered(z[c] + ev)), ms = __reduce_max_sync(kFull, ordered(z[c]));
+            const int ms = __reduce_max_sync(kFull, ordered(a[0][c])), mw = __reduce_max_sync(kFull, ordered(a[0][c] + ev));
             if (lane == 0) {
               ctl->part_max[stream][warp][own + c][0] = unordered(mw);
               ctl->part_max[stream][warp][own + c][1] = unordered(ms);
@@ -742,12 +758,10 @@ struct Cta {
           }
           bar_sync(1 + wi, 128);
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) {
-            l[c] *= ctl->scale_l[stream][own + c];
-            a[c] = (z[c] + ev) - ctl->top_w[stream][own + c];
-            b[c] = z[c] - ctl->top_s[stream][own + c];
-          }
-          if (i >= S::kStep) {
+          for (int c = 0; c < kCols; ++c) l[c] *= ctl->scale_l[stream][own + c];
+#pragma unroll
+          for (int half = 0; half < S::kHalves; ++half) against(a[half], b[half]);
+          if (i >= S::kStreams) {
             __syncwarp();
 #pragma unroll 1
             for (int k = 0; k < kWParts; ++k) {
@@ -761,33 +775,35 @@ struct Cta {
             tmem_wait_st();
           }
         }
-        // weights, as parts, into the token's row of the B operand
+        // weights, as parts, into the row of the B operand, whose 16-byte chunks are in swizzled order
         ++uses;
-        uint8_t* wrow = wbuf + stream * S::kWBytes + r * S::kNO;
-        uint32_t out[kWParts][2];
+        uint8_t* wrow = wbuf + stream * S::kWBytes + r * S::kWRow;
+        const int swizzle = S::kWRow == 128 ? r & 7 : (S::kWRow == 64 ? (r >> 1) & 3 : (r >> 2) & 1);
 #pragma unroll
-        for (int k = 0; k < kCols; k += 4) {
-          float e[4];
+        for (int half = 0; half < S::kHalves; ++half) {
+          uint32_t out[kWParts][2];
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            e[n] = ex2_approx(a[k + n]);
-            l[k + n] += ex2_approx(b[k + n]);
+          for (int k = 0; k < kCols; k += 4) {
+            float e[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              e[n] = ex2_approx(a[half][k + n]);
+              l[k + n] += ex2_approx(b[half][k + n]);
+            }
+            uint32_t p01[kWParts], p23[kWParts];
+            split_parts(e[0], e[1], p01);
+            split_parts(e[2], e[3], p23);
+#pragma unroll
+            for (int n = 0; n < kWParts; ++n) out[n][k / 4] = p01[n] | (p23[n] << 16);
           }
-          uint32_t p01[kWParts], p23[kWParts];
-          split_parts(e[0], e[1], p01);
-          split_parts(e[2], e[3], p23);
+          if constexpr (NC == 8) {
+            *reinterpret_cast<uint4*>(wrow + 16 * ((2 * half) ^ swizzle)) = make_uint4(out[0][0], out[0][1], out[1][0], out[1][1]);
+            *reinterpret_cast<uint4*>(wrow + 16 * ((2 * half + 1) ^ swizzle)) = make_uint4(out[2][0], out[2][1], out[3][0], out[3][1]);
+          } else {
 #pragma unroll
-          for (int n = 0; n < kWParts; ++n) out[n][k / 4] = p01[n] | (p23[n] << 16);
-        }
-        // 16-byte chunks of the row, in the operand's swizzled order
-        if constexpr (NC == 8) {
-          const int x = (r >> 2) & 1;
-          *reinterpret_cast<uint4*>(wrow + 16 * x) = make_uint4(out[0][0], out[0][1], out[1][0], out[1][1]);
-          *reinterpret_cast<uint4*>(wrow + 16 * (x ^ 1)) = make_uint4(out[2][0], out[2][1], out[3][0], out[3][1]);
-        } else {
-#pragma unroll
-          for (int n = 0; n < kWParts; ++n)
-            *reinterpret_cast<uint2*>(wrow + 16 * (n ^ ((r >> 1) & 3)) + 8 * grp) = make_uint2(out[n][0], out[n][1]);
+            for (int n = 0; n < kWParts; ++n)
+              *reinterpret_cast<uint2*>(wrow + 16 * ((4 * half + n) ^ swizzle) + 8 * grp) = make_uint2(out[n][0], out[n][1]);
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -799,9 +815,7 @@ struct Cta {
       if (!stop) {
 #pragma unroll
         for (int k = 0; k < kStreams; ++k) {
-          const int from = S::kPair ? k >> 1 : k;
-          const uint32_t at = g + from + (n - 1 - from) / S::kStep * S::kStep;   // the stream's last stage
-          if (n > from) ok = ok && product_done(at, S::kPair ? k & 1 : 0);
+          if (n > k) ok = ok && product_done(g + k + (n - 1 - k) / kStreams * kStreams);   // the stream's last stage
         }
         __syncwarp();
         tc_fence_after();
@@ -847,7 +861,7 @@ struct Cta {
       }
       bar_sync(1 + wi, 128);
       __syncwarp();
-      const int d = D == 128 ? r : (lane < 16 ? warp * 16 + lane : -1);     // M = 64 fills 16 lanes of each quarter
+      int d = S::kPair ? r & 63 : r;
       const bool full_unit = w.whole();
       const int slot = 2 * (int)blockIdx.x + second_slot(t_first, w.pos);
       bool poisoned = false;
@@ -856,13 +870,11 @@ struct Cta {
       float acc[kN] = {};
       // kept as a loop, as code that runs once costs what its fetching costs
 #pragma unroll 1
-      for (int k = 0; k < kStreams && (S::kPair ? k >> 1 : k) < n; ++k) {
+      for (int k = 0; k < min(kStreams, n); ++k) {
         uint32_t o[kWParts][kN];
 #pragma unroll
         for (int q = 0; q < kWParts; ++q) {
-          const uint32_t at = quarter + S::kOCol + k * S::kNO + q * NC + c0;
-          if constexpr (kN == 2) tmem_ld2(at, o[q]);
-          else tmem_ld4(at, o[q]);
+          tmem_ld4(quarter + S::kOCol + k * S::kWRow + o_half + q * NC + c0, o[q]);
         }
         tmem_wait_ld();
 #pragma unroll
@@ -871,8 +883,23 @@ struct Cta {
           x = fmaf(x, 1.f / 16.f, __uint_as_float(o[2][c]));
           x = fmaf(x, 1.f / 16.f, __uint_as_float(o[1][c]));
           x = fmaf(x, 1.f / 16.f, __uint_as_float(o[0][c]));
-          if (poisoned && d >= 0 && ((ctl->poison[k][c0 + c][d >> 5] >> (d & 31)) & 1)) x = __int_as_float(0x7fc00000);
+          if (poisoned && ((ctl->poison[k][c0 + c][d >> 5] >> (d & 31)) & 1)) x = __int_as_float(0x7fc00000);
           acc[c] = fmaf(x, ctl->join_w[k][c0 + c], acc[c]);
+        }
+      }
+      if constexpr (S::kPair) {
+        // the odd tokens' sums to the threads of the even ones', through the weights' memory, which is free
+        float* other = reinterpret_cast<float*>(wbuf) + (wi * 64 + d) * kN;
+        if (r >= 64) {
+#pragma unroll
+          for (int c = 0; c < kN; ++c) other[c] = acc[c];
+        }
+        bar_sync(1 + wi, 128);
+        if (r < 64) {
+#pragma unroll
+          for (int c = 0; c < kN; ++c) acc[c] += other[c];
+        } else {
+          d = -1;
         }
       }
       if (full_unit) {
@@ -907,7 +934,7 @@ struct Cta {
 template <int D, int NC, bool kHalf>
 __global__ void __launch_bounds__(Shape<D, NC, kHalf ? 3 : 2>::kThreads, 1) kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams p) {
   using S = Shape<D, NC, kHalf ? 3 : 2>;
-  using Ctl = Control<NC, S::kStages, S::kPages, S::kHalves, S::kStreams, S::kThreads / 32>;
+  using Ctl = Control<NC, S::kStages, S::kPages, S::kStreams, S::kThreads / 32>;
   static_assert(offsetof(Ctl, scales) % 16 == 0 && offsetof(Ctl, f) % 16 == 0 && offsetof(Ctl, top_w) % 16 == 0 &&
                 offsetof(Ctl, top_s) % 16 == 0 && NC % 8 == 0, "vector accesses are aligned");
   static_assert(sizeof(Ctl) <= 6144, "the control block fits its share");
@@ -924,7 +951,7 @@ __global__ void __launch_bounds__(Shape<D, NC, kHalf ? 3 : 2>::kThreads, 1) kv8_
     prefetch_tensormap(&p.cache_map);
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&ctl->full[i], 1 + S::kPages);       // the codes' bytes, every page's scale bytes
-      for (int k = 0; k < S::kHalves; ++k) mbar_init(&ctl->empty[i][k], 1);
+      mbar_init(&ctl->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->q_full[i], 1);
@@ -1032,7 +1059,7 @@ __global__ void __launch_bounds__(Shape<D, NC, kHalf ? 3 : 2>::kThreads, 1) kv8_
 template <class S, int NC>
 constexpr size_t smem_bytes() {
   return 1024 + (size_t)S::kStages * S::kStageBytes + 2 * S::kQBytes + S::kStreams * S::kWBytes +
-         sizeof(Control<NC, S::kStages, S::kPages, S::kHalves, S::kStreams, S::kThreads / 32>);
+         sizeof(Control<NC, S::kStages, S::kPages, S::kStreams, S::kThreads / 32>);
 }
 
 template <int D, int NC, bool kHalf>
