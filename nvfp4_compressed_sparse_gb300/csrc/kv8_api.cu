@@ -71,7 +71,7 @@ int kv8_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, con
   p.page_bytes = kv8_page_size(kv_heads, head_dim);
   p.slots = num_tokens / kBlockTokens + 2 * (int64_t)B;
   p.status = dev_status;
-  if (p.slots * 2 * kv_heads > (int64_t)INT32_MAX) return NVFP4MLA_ERR_UNSUPPORTED;
+  if (p.slots * kv_heads > (int64_t)INT32_MAX) return NVFP4MLA_ERR_UNSUPPORTED;
   return status_of(launch_kv8_append(p, head_dim, dtype == NVFP4MLA_FP16, static_cast<cudaStream_t>(stream)));
 }
 

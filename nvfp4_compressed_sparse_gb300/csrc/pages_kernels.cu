@@ -90,19 +90,12 @@ __global__ void __launch_bounds__(256) free_kernel(const PageState s, const int3
 
 // ------------------------------------------------------------------ planning
 struct PlanShared {
-  int64_t piece[kPlanCtas];    // this CTA's count, one slot a round, read by the others
+  int2 piece[2];               // this CTA's counts, by exchange, read by the others
+  int4 sums;                   // of an exchange: before, all; of the first count and of the second
   int warp[kPlanWarps];
+  int2 warp2[kPlanWarps];
   int64_t running;
 };
-
-// Sum of v over the block, in every thread.
-__device__ int block_sum(PlanShared* sh, int v) {
-  v = __reduce_add_sync(kFull, v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh->warp[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return __reduce_add_sync(kFull, sh->warp[threadIdx.x & 31]);
-}
 
 // Exclusive prefix over the block's warps of a per-warp value.
 __device__ int warp_prefix(PlanShared* sh, int v) {
@@ -113,26 +106,46 @@ __device__ int warp_prefix(PlanShared* sh, int v) {
   return __reduce_add_sync(kFull, (int)(threadIdx.x & 31) < (int)(threadIdx.x >> 5) ? w : 0);
 }
 
-// Publishes this CTA's count and sums the others': before = those of the CTAs before it, all = of
-// all. Every thread of the cluster calls it; it orders global writes of the cluster too.
-__device__ void exchange(PlanShared* sh, int round, int64_t mine, int64_t& before, int64_t& all) {
-  if (threadIdx.x == 0) sh->piece[round] = mine;
+// Two counts of every warp of the cluster: their sums over the warps before this one (of this and of
+// earlier CTAs) and over all. A warp of each CTA reads the others' sums; round: 0 and 1 in turn. Global
+// writes of the cluster before it are visible after it.
+struct Counts {
+  int before, all;
+};
+__device__ void exchange(PlanShared* sh, int round, int2 mine, Counts& first, Counts& second) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();
+  if (lane == 0) sh->warp2[warp] = mine;
+  __syncthreads();
+  const int2 w = sh->warp2[lane];
+  if (warp == 0) {
+    const int2 sum = make_int2(__reduce_add_sync(kFull, w.x), __reduce_add_sync(kFull, w.y));
+    if (lane == 0) sh->piece[round] = sum;
+  }
   __threadfence();
   cluster_sync_all();
-  const uint32_t rank = cluster_ctarank();
-  before = all = 0;
-  for (uint32_t r = 0; r < kPlanCtas; ++r) {
-    const uint32_t at = map_shared_rank(smem_u32(&sh->piece[round]), r);
-    const int64_t v = (int64_t)(((uint64_t)ld_dsmem_u32(at + 4) << 32) | ld_dsmem_u32(at));
-    if (r < rank) before += v;
-    all += v;
+  if (warp == 0) {
+    const int rank = (int)cluster_ctarank();
+    int2 v = make_int2(0, 0);
+    if (lane < kPlanCtas) {
+      const uint32_t at = map_shared_rank(smem_u32(&sh->piece[round]), (uint32_t)lane);
+      v = make_int2((int)ld_dsmem_u32(at), (int)ld_dsmem_u32(at + 4));
+    }
+    const int4 sums = make_int4(__reduce_add_sync(kFull, lane < rank ? v.x : 0), __reduce_add_sync(kFull, v.x),
+                                __reduce_add_sync(kFull, lane < rank ? v.y : 0), __reduce_add_sync(kFull, v.y));
+    if (lane == 0) sh->sums = sums;
   }
+  __syncthreads();
+  const int4 sums = sh->sums;
+  first = {sums.x + __reduce_add_sync(kFull, lane < warp ? w.x : 0), sums.y};
+  second = {sums.z + __reduce_add_sync(kFull, lane < warp ? w.y : 0), sums.w};
 }
 
 // This CTA's piece of n items, and within it this warp's: multiples of 128, so that a lane's four
 // are one 16-byte load (refcounts are 16-byte aligned).
 __device__ __forceinline__ void piece_of(int64_t n, int64_t& lo, int64_t& hi) {
-  const int64_t per_warp = (n + kPlanCtas * kPlanWarps * 128 - 1) / (kPlanCtas * kPlanWarps * 128) * 128;
+  constexpr int kAll = kPlanCtas * kPlanWarps * 128;
+  const int64_t per_warp = (n + kAll - 1) / kAll * 128;
   const int64_t w = (int64_t)cluster_ctarank() * kPlanWarps + (threadIdx.x >> 5);
   lo = w * per_warp < n ? w * per_warp : n;
   hi = lo + per_warp < n ? lo + per_warp : n;
@@ -279,8 +292,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     const int there = __ldcg(at);
     if (there == 0 || is_claim(there)) atomicMin(at, kClaim + i);
   }
-  int64_t before, all;
-  exchange(&sh, 0, 0, before, all);
+  cluster_sync_all();   // every claim is made
   // who won, and what that needs
   auto won = [&](int i, int& len) {
     bool missing;
@@ -302,10 +314,9 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   }
   int64_t lo, hi;
   piece_of(a.s.num_pages, lo, hi);
-  const int c = warp_count(a.s.refs, lo, hi, a.s.num_pages, 1, IsFree());
-  const int cta = block_sum(&sh, (threadIdx.x & 31) == 0 ? c : 0);
-  exchange(&sh, 1, cta, before, all);
-  before += warp_prefix(&sh, c);
+  Counts free_pages, unused;
+  exchange(&sh, 0, make_int2(warp_count(a.s.refs, lo, hi, a.s.num_pages, 1, IsFree()), 0), free_pages, unused);
+  const int64_t all = free_pages.all;
 #pragma unroll
   for (int k = 0; k < kOwn; ++k) {
     const int i = (k * kPlanCtas + rank) * kPlanThreads + threadIdx.x;
@@ -315,7 +326,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     if (own_len[k] < 0 || refused) a.new_pages[i] = -2;
     else if (!needs) a.new_pages[i] = -1;
   }
-  warp_number(a.s.refs, lo, hi, a.s.num_pages, 1, before, total, IsFree(), [&](int64_t page, int, int64_t g) {
+  warp_number(a.s.refs, lo, hi, a.s.num_pages, 1, free_pages.before, total, IsFree(), [&](int64_t page, int, int64_t g) {
     if (g >= total) return;
     a.s.refs[page] = 1;
     a.new_pages[owner_of(sum, a.n, g)] = (int32_t)page;
@@ -387,13 +398,12 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     const int64_t need = extend_need(a, i, have, bad);
     return (int)(need > 0 ? need : 0);
   });
-  int64_t lo, hi, before, all;
+  int64_t lo, hi;
   piece_of(a.s.num_pages, lo, hi);
-  const int c = warp_count(a.s.refs, lo, hi, a.s.num_pages, 1, IsFree());
-  const int cta = block_sum(&sh, (threadIdx.x & 31) == 0 ? c : 0);
-  exchange(&sh, 0, cta, before, all);
-  before += warp_prefix(&sh, c);
-  warp_number(a.s.refs, lo, hi, a.s.num_pages, 1, before, total, IsFree(), [&](int64_t page, int, int64_t g) {
+  Counts found, unused;
+  exchange(&sh, 0, make_int2(warp_count(a.s.refs, lo, hi, a.s.num_pages, 1, IsFree()), 0), found, unused);
+  const int64_t all = found.all;
+  warp_number(a.s.refs, lo, hi, a.s.num_pages, 1, found.before, total, IsFree(), [&](int64_t page, int, int64_t g) {
     if (g >= total) return;
     const int i = owner_of(sum, n, g);
     if (sum[i + 1] > all) return;    // refused: its pages stay free
@@ -434,29 +444,50 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   let_dependents_start();
   const int64_t n = a.s.num_pages;
   const auto live = [](int64_t, int v) { return v > 0; };
-  int64_t lo, hi, before, num_live;
+  int64_t lo, hi;
   piece_of(n, lo, hi);
-  int c = warp_count(a.s.refs, lo, hi, n, 0, live);
-  int cta = block_sum(&sh, (threadIdx.x & 31) == 0 ? c : 0);
-  exchange(&sh, 0, cta, before, num_live);
+  Counts live_pages, moved, holes;
+  exchange(&sh, 0, make_int2(warp_count(a.s.refs, lo, hi, n, 0, live), 0), live_pages, holes);
+  const int64_t num_live = live_pages.all;
   // live pages behind the live ones' number, and free ones before it: equally many
   const auto moves = [=](int64_t i, int v) { return v > 0 && i >= num_live; };
   const auto hole = [=](int64_t i, int v) { return v <= 0 && i < num_live; };
-  const int cm = warp_count(a.s.refs, lo, hi, n, 0, moves), ch = warp_count(a.s.refs, lo, hi, n, 0, hole);
-  int64_t m_before, m_all, h_before, h_all;
-  cta = block_sum(&sh, (threadIdx.x & 31) == 0 ? cm : 0);
-  exchange(&sh, 1, cta, m_before, m_all);
-  m_before += warp_prefix(&sh, cm);
-  cta = block_sum(&sh, (threadIdx.x & 31) == 0 ? ch : 0);
-  exchange(&sh, 2, cta, h_before, h_all);
-  h_before += warp_prefix(&sh, ch);
-  warp_number(a.s.refs, lo, hi, n, 0, h_before, h_before + n, hole, [&](int64_t page, int, int64_t g) { a.holes[g] = (int32_t)page; });
-  for (int64_t i = lo + (threadIdx.x & 31); i < hi; i += 32) {
-    const int v = a.s.refs[i];
-    if (!moves(i, v)) a.remap[i] = v > 0 ? (int32_t)i : -1;
+  const int lane = threadIdx.x & 31;
+  int2 c = make_int2(0, 0);
+#pragma unroll 4
+  for (int64_t i = lo; i < hi; i += 128) {
+    const int64_t at = i + lane * 4;
+    const int4 v = four_at(a.s.refs, at, n, 0);
+    c.x += moves(at, v.x) + moves(at + 1, v.y) + moves(at + 2, v.z) + moves(at + 3, v.w);
+    c.y += hole(at, v.x) + hole(at + 1, v.y) + hole(at + 2, v.z) + hole(at + 3, v.w);
   }
-  exchange(&sh, 3, 0, before, h_all);   // the holes are listed, and nobody reads a count below num_live any more
-  warp_number(a.s.refs, lo, hi, n, 0, m_before, m_before + n, moves, [&](int64_t page, int v, int64_t g) {
+  exchange(&sh, 1, make_int2(__reduce_add_sync(kFull, c.x), __reduce_add_sync(kFull, c.y)), moved, holes);
+  // list the free pages, and say where the pages that stay are
+#pragma unroll 2
+  for (int64_t i = lo; i < hi; i += 128) {
+    const int64_t at = i + lane * 4;
+    const int4 v = four_at(a.s.refs, at, n, 0);
+    const int vs[4] = {v.x, v.y, v.z, v.w};
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mine += hole(at + k, vs[k]) ? 1 : 0;
+    int incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(kFull, incl, d);
+      if (lane >= d) incl += o;
+    }
+    int g = holes.before + incl - mine;
+    holes.before += __shfl_sync(kFull, incl, 31);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (hole(at + k, vs[k])) a.holes[g++] = (int32_t)(at + k);
+      if (at + k < n && !moves(at + k, vs[k])) a.remap[at + k] = vs[k] > 0 ? (int32_t)(at + k) : -1;
+    }
+  }
+  __threadfence();
+  cluster_sync_all();   // the free pages are listed, and nobody reads a count below num_live any more
+  warp_number(a.s.refs, lo, hi, n, 0, moved.before, moved.before + n, moves, [&](int64_t page, int v, int64_t g) {
     const int32_t to = __ldcg(a.holes + g);
     a.movers[g] = (int32_t)page;
     a.remap[page] = to;
@@ -465,7 +496,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   });
   if (cluster_ctarank() == 0 && threadIdx.x == 0) {
     *a.num_live = (int32_t)num_live;
-    *a.num_moves = (int32_t)m_all;
+    *a.num_moves = moved.all;
   }
   cluster_sync_all();   // no CTA leaves while another may read its count
 }
