@@ -110,7 +110,7 @@ struct Control {
   float part_max[kStreams][4][NC][2];
   float part_l[kStreams][4][NC];
   uint32_t poison[kStreams][NC][4];    // dims that a NaN value reaches
-  float join_m[NC], join_l[NC], join_w[kStreams][NC];
+  float join_m[NC], join_l[NC], join_inv[NC], join_w[kStreams][NC];
   int any_poison[kStreams];
   int scan_sum[kWarps];
   int start_before;                    // tiles before request start_b
@@ -574,13 +574,11 @@ struct Cta {
     else p.out[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
   }
 
-  // One column's result of dim d, from the maximum, the sum and the weighted sum.
-  template <bool kHalf>
-  __device__ __forceinline__ void finish(int row, int d, float m, float sum, float acc) {
-    if (row < 0) return;
-    put<kHalf>((int64_t)row * D + d, sum == 0.f ? 0.f : acc / sum);
-    if (d == 0) p.lse[row] = sum == 0.f ? neg_inf() : (m + log2f(sum)) * 0.69314718055994530942f;
+  __device__ __forceinline__ void put_lse(int row, float m, float sum) {
+    if (row >= 0) p.lse[row] = sum == 0.f ? neg_inf() : (m + log2f(sum)) * 0.69314718055994530942f;
   }
+  // What a weighted sum is multiplied by: 0 where there was no position.
+  static __device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
 
   // Joins the partial results that CTAs c_lo .. c_hi left of a unit, for dim d of this warpgroup's
   // columns: some partial results at a time, every load of them in flight together.
@@ -620,7 +618,11 @@ struct Cta {
       }
     }
 #pragma unroll
-    for (int k = 0; k < kN; ++k) finish<kHalf>(row[c + k], d, m[k], sum[k], acc[k]);
+    for (int k = 0; k < kN; ++k) {
+      if (row[c + k] < 0) break;
+      put<kHalf>((int64_t)row[c + k] * D + d, acc[k] * inverse(sum[k]));
+      if (d == 0) put_lse(row[c + k], m[k], sum[k]);
+    }
   }
 
   template <bool kHalf>
@@ -858,6 +860,8 @@ struct Cta {
         }
         ctl->join_m[c] = m;
         ctl->join_l[c] = sum;
+        ctl->join_inv[c] = inverse(sum);
+        if (w.whole()) put_lse(ctl->row[buf][c], m, sum);
       }
       bar_sync(1 + wi, 128);
       __syncwarp();
@@ -905,7 +909,7 @@ struct Cta {
       if (full_unit) {
 #pragma unroll
         for (int c = 0; c < kN; ++c)
-          if (d >= 0) finish<kHalf>(ctl->row[buf][c0 + c], d, ctl->join_m[c0 + c], ctl->join_l[c0 + c], acc[c]);
+          if (d >= 0 && ctl->row[buf][c0 + c] >= 0) put<kHalf>((int64_t)ctl->row[buf][c0 + c] * D + d, acc[c] * ctl->join_inv[c0 + c]);
       } else {
 #pragma unroll
         for (int c = 0; c < kN; ++c)
