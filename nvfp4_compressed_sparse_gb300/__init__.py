@@ -465,6 +465,14 @@ def _raw_stream(stream, index):
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
+def _keep(stream, *tensors):
+    """Memory taken here, on the current stream, and used on `stream`: not to be reused before that is done."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _kv8_dtype(t, name) -> int:
     import torch
     if t.dtype is torch.bfloat16:
@@ -544,21 +552,25 @@ def kv8_decode(q, cache, page_table, seq_lens, kv_heads: int, softmax_scale, win
     rows, max_pages = page_table.shape
     if seq_lens.shape[0] != B or rows != B:
         raise ValueError("shape mismatch")
+    fresh = [None] * 3
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        out = fresh[0] = torch.empty(shape, dtype=q.dtype, device=q.device)
     if lse is None:
-        lse = torch.empty((B, Q, H), dtype=torch.float32, device=q.device)
+        lse = fresh[1] = torch.empty((B, Q, H), dtype=torch.float32, device=q.device)
     op, lp = _ptr_of(out, "out", q.dtype, index, 4), _ptr_of(lse, "lse", torch.float32, index, 3)
     if out.shape != shape or lse.shape != shape[:3]:
         raise ValueError("out must be [B, Q, H, head_dim] and lse [B, Q, H]")
     if workspace is None:
-        workspace = torch.empty(max(kv8_decode_workspace_size(B, Q, H, kv_heads, d), 1), dtype=torch.uint8, device=q.device)
+        workspace = fresh[2] = torch.empty(max(kv8_decode_workspace_size(B, Q, H, kv_heads, d), 1), dtype=torch.uint8,
+                                           device=q.device)
     rc = lib.kv8_decode(qp, s1 if Q > 1 else s0 if B > 1 else 0, s2 if H > 1 else 0, dt, cp, pages, pp, max_pages, sp,
-                        B, Q, H, kv_heads, d, softmax_scale, window, op, lp, workspace.data_ptr(), workspace.nbytes,
+                        B, Q, H, kv_heads, d, float(softmax_scale), int(window), op, lp, workspace.data_ptr(),
+                        workspace.nbytes,
                         _optional_ptr(dev_status, "dev_status", index),
-                        (max_ctas & 0xFFFF) | (FLAG_TEST_TIMEOUT if test_timeout else 0), _raw_stream(stream, index))
+                        (int(max_ctas) & 0xFFFF) | (FLAG_TEST_TIMEOUT if test_timeout else 0), _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv8_decode")
+    _keep(stream, *fresh)
     return out, lse
 
 
@@ -631,8 +643,9 @@ def kv_pages_fork(cache, page_table, seq_lens, refcounts, src, dst, new_pages=No
     if counts != pages:
         raise ValueError("refcounts must have one entry per page of the cache")
     sp, dp = _ptr_of(src, "src", i32, index, 1), _ptr_of(dst, "dst", i32, index, 1)
+    fresh = None
     if new_pages is None:
-        new_pages = torch.empty_like(src)
+        new_pages = fresh = torch.empty_like(src)
     np_, n = _ptr_of(new_pages, "new_pages", i32, index, 1), src.shape[0]
     if dst.shape[0] != n or new_pages.shape[0] != n:
         raise ValueError("src, dst and new_pages must have the same length")
@@ -640,6 +653,7 @@ def kv_pages_fork(cache, page_table, seq_lens, refcounts, src, dst, new_pages=No
                                       _optional_ptr(dev_status, "dev_status", index), _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv_pages_fork")
+    _keep(stream, fresh)
     return new_pages
 
 
@@ -673,18 +687,20 @@ def kv_pages_compact(cache, page_table, refcounts, remap=None, num_live=None, wo
     pp, width, _, seqs, rp, counts = _page_state(page_table, None, refcounts, index)
     if counts != pages:
         raise ValueError("refcounts must have one entry per page of the cache")
+    fresh = [None] * 3
     if remap is None:
-        remap = torch.empty_like(refcounts)
+        remap = fresh[0] = torch.empty_like(refcounts)
     if num_live is None:
-        num_live = torch.empty(1, dtype=i32, device=cache.device)
+        num_live = fresh[1] = torch.empty(1, dtype=i32, device=cache.device)
     mp, lp = _ptr_of(remap, "remap", i32, index, 1), _ptr_of(num_live, "num_live", i32, index, 1)
     if remap.shape[0] != pages or num_live.shape[0] < 1:
         raise ValueError("remap must have one entry per page, num_live one")
     if workspace is None:
-        workspace = torch.empty(kv_pages_compact_workspace_size(pages), dtype=torch.uint8, device=cache.device)
+        workspace = fresh[2] = torch.empty(kv_pages_compact_workspace_size(pages), dtype=torch.uint8, device=cache.device)
     rc = load_library().kv_pages_compact(cp, layers, stride, pages, each, pp, width, seqs, rp, mp, lp,
                                          workspace.data_ptr(), workspace.nbytes,
                                          _optional_ptr(dev_status, "dev_status", index), _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv_pages_compact")
+    _keep(stream, *fresh)
     return remap, num_live

@@ -143,7 +143,7 @@ int kv8_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, int
   const int columns = kv8_decode_columns(Q, H / kv_heads);
   const int64_t units = (int64_t)kv_heads * ((Q * (H / kv_heads) + columns - 1) / columns);
   if ((int64_t)B * Q * H > INT32_MAX || max_pages_per_seq > INT32_MAX) return NVFP4MLA_ERR_UNSUPPORTED;
-  if (max_pages_per_seq / 2 + 8 > INT32_MAX / (B * units)) return NVFP4MLA_ERR_UNSUPPORTED;
+  if (max_pages_per_seq / 2 + 16 > INT32_MAX / (B * units)) return NVFP4MLA_ERR_UNSUPPORTED;
   Kv8DecodeParams p{};
   if (!encode_pages_map(&p.cache_map, cache, num_pages, kv8_page_size(kv_heads, head_dim), kv_heads, head_dim))
     return NVFP4MLA_ERR_CUDA;

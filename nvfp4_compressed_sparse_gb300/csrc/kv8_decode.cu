@@ -26,10 +26,16 @@
 //   warp 2     queries of the next unit: scaling by a power of two, parts, two buffers
 //   warps 4..  softmax: two streams of tiles, a warpgroup or two each (thread = token). Each stream has
 //              its own S, w and O, and keeps its own M, m, l; they are added at the unit's end
-// A stage is 128 rows of 128 bytes: a token each, or two tokens of 64 dims, which one softmax thread has
-// (TMA takes a cycle or so per row, and 64-byte rows would halve its rate).
+// A stage is 128 rows of 128 bytes: a token each, or two tokens of 64 dims, which one softmax thread has.
 // A unit that several CTAs share is joined by whichever of them finishes last: the others leave
 // (m, l, O) in the workspace and count themselves.
+//
+// Measured (device time, inputs beyond L2, 152 SMs): 8 columns and 128 dims run at the memory's pace:
+// 16 requests of 20-90K tokens, 8 key/value heads: 1.38 GB in 210 us, 6.57 TB/s, 97 % of the measured
+// copy bandwidth; one request of 131K tokens: 269 MB in 53 us (74 %: 5 us until the first product, 7
+// from the last to the joined result). With 64 dims a byte brings twice the softmax work: 64 requests
+// of 4-30K tokens: 871 MB in 161 us (80 %). With 16 columns the softmax sets the pace: 1.0 us a stage
+// at 128 dims, 1.8 at 64, issue slots 60 % taken (32 requests of 4-16K, two queries of 8 heads: 72 %).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -149,8 +155,10 @@ struct Ranges {
 };
 
 // What starting and ending a unit costs, in tiles: ranges count a unit of n tiles as kUnitCost + n, so
-// that CTAs with many short units do not finish last.
-constexpr int kUnitCost = 4;
+// that CTAs with many short units do not finish last. Measured with 0, 4, 8, 12 and 16: 256 requests of
+// 200-1,500 tokens 161, 127, 123, 125 and 126 us; 64 of 4-30K with 64 dims 188, 169, 161, 163 and 169;
+// 16 of 20-90K 211.5, 210, 210.5, 210.5 and 212.
+constexpr int kUnitCost = 8;
 
 // A walk over the segments of this CTA: per unit, the tiles of it that the CTA has. Units go by column
 // tile, request and key/value head; so the column tiles of one head's tokens run on different CTAs at
@@ -164,7 +172,7 @@ struct Walk {
   int pos;               // of the unit's first tile, in the whole sequence
 
   __device__ __forceinline__ void load(const Kv8DecodeParams& p) {
-    len = __ldg(p.seq_lens + b);
+    len = p.seq_lens[b];
     if (len < 0) len = 0;
     unit_tiles<kTile>(p, len, first, n);
   }
@@ -278,7 +286,7 @@ struct Cta {
     if (col * kPageTokens >= w.len || (col + 1) * kPageTokens <= from) return -1;
     int page = -1;
     if (col < p.max_pages) {
-      page = __ldg(p.page_table + (int64_t)w.b * p.max_pages + col);
+      page = p.page_table[(int64_t)w.b * p.max_pages + col];
       if (page >= 0 && page < p.num_pages) return page;
       page = -1;
     } else {
@@ -456,7 +464,7 @@ struct Cta {
         const int col = ct * NC + round * kCols + sub;
         if (round >= kRounds || col >= ncols) return make_uint4(0u, 0u, 0u, 0u);
         const int j = col / p.group, h = kvh * p.group + col - j * p.group;
-        return __ldg(reinterpret_cast<const uint4*>(p.q + ((int64_t)w.b * p.Q + j) * p.q_token_stride + h * p.q_head_stride + ch * 8));
+        return *reinterpret_cast<const uint4*>(p.q + ((int64_t)w.b * p.Q + j) * p.q_token_stride + h * p.q_head_stride + ch * 8);
       };
       // four rounds' loads in flight, one round's code
       uint4 v[kAhead];
@@ -990,7 +998,7 @@ __global__ void __launch_bounds__(Shape<D, NC, kHalf ? 3 : 2>::kThreads, 1) kv8_
   int sum = 0;
   for (int b = b0; b < b1; ++b) {
     int first, n;
-    unit_tiles<S::kTile>(p, max(0, __ldg(p.seq_lens + b)), first, n);
+    unit_tiles<S::kTile>(p, max(0, p.seq_lens[b]), first, n);
     sum += n + kUnitCost;
   }
   int incl = sum;
@@ -1007,7 +1015,8 @@ __global__ void __launch_bounds__(Shape<D, NC, kHalf ? 3 : 2>::kThreads, 1) kv8_
   const int before = (__reduce_add_sync(kFull, lane < warp ? of_warp : 0) + incl - sum) * p.kv_heads;
   const int all = __reduce_add_sync(kFull, of_warp) * p.kv_heads;      // of one column tile
   // no CTA gets less than a tile for each of its streams, and where units have few tiles, no less than
-  // an average unit: joining partial results costs some 4 us, a tile 0.6
+  // an average unit: joining partial results costs some 4 us, a tile 0.6 (one request of 1,000 tokens:
+  // 11.3 us, and 12.8 when its eight units are split)
   const int units = p.B * p.kv_heads * cts, tiles = all * cts - kUnitCost * units;
   const int most = tiles <= S::kFewTiles * units ? units : (tiles + S::kMinTiles - 1) / S::kMinTiles;
   const Ranges ranges(all * cts, min((int)gridDim.x, most));
@@ -1018,7 +1027,7 @@ __global__ void __launch_bounds__(Shape<D, NC, kHalf ? 3 : 2>::kThreads, 1) kv8_
     int b = b0, at = before;
     for (;; ++b) {
       int first, n;
-      unit_tiles<S::kTile>(p, max(0, __ldg(p.seq_lens + b)), first, n);
+      unit_tiles<S::kTile>(p, max(0, p.seq_lens[b]), first, n);
       if (in_ct < at + (n + kUnitCost) * p.kv_heads) break;
       at += (n + kUnitCost) * p.kv_heads;
     }
@@ -1107,7 +1116,11 @@ cudaError_t launch_columns(const Kv8DecodeParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-// Columns of a tile: the softmax's work grows with them, and so does what a key is read for.
+// Columns of a tile. 8 where they hold all of a key/value head's: with 16 such steps took 229 us instead
+// of 210 (16 requests of 20-90K tokens, 128 dims) and 295 instead of 169 (64 of 4-30K, 64 dims), as the
+// softmax's work grows with them. From 9 columns on 16: two tiles of 8 would read every key twice and
+// take as many instructions. (32 columns in one tile spilled registers, and took 82 ns a column and
+// tile where 16 took 62.)
 int kv8_decode_columns(int Q, int group) {
   return Q * group <= 8 ? 8 : 16;
 }

@@ -392,3 +392,32 @@ def test_decode_waits_are_bounded_and_the_next_calls_are_right():
         g.replay()
         check(out, lse, c.reference())
     check(*m.kv8_decode(*args, workspace=ws), c.reference())
+
+
+def test_decode_on_a_stream_of_its_own_keeps_what_it_took():
+    """out, lse and workspace taken by the call itself, on the current stream, while the step waits on another:
+    what is taken from the allocator next must not be theirs."""
+    c = Case([2000, 900], 2, 128, Q=1, G=4, seed=23)
+    args = (c.q, dev(c.cache, torch.uint8), dev(c.table), dev(c.lens), 2, c.scale)
+    want = m.kv8_decode(*args)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    x = torch.randn((4096, 4096), device="cuda")
+    size = m.kv8_decode_workspace_size(2, 1, 8, 2, 128)
+    for _ in range(3):
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                x = x @ x * 1e-3            # some milliseconds before the step
+        out, lse = m.kv8_decode(*args, stream=s)
+        for _ in range(8):
+            torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        s.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_decode_of_expanded_and_one_entry_axes():
+    """Axes of one entry may have any stride; a batch axis that repeats one query row (stride 0)."""
+    c = Case([100, 77], 1, 64, Q=1, G=1, seed=24)
+    wide = torch.randn((2, 1, 1, 100), device="cuda").to(torch.bfloat16)
+    q = wide.as_strided((2, 1, 1, 64), (0, 7, 13, 1))
+    check(*c.run(q=q), c.reference(q=q))
