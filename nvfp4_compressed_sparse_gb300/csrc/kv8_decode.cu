@@ -34,8 +34,9 @@
 // 16 requests of 20-90K tokens, 8 key/value heads: 1.38 GB in 210 us, 6.57 TB/s, 97 % of the measured
 // copy bandwidth; one request of 131K tokens: 269 MB in 53 us (74 %: 5 us until the first product, 7
 // from the last to the joined result). With 64 dims a byte brings twice the softmax work: 64 requests
-// of 4-30K tokens: 871 MB in 161 us (80 %). With 16 columns the softmax sets the pace: 1.0 us a stage
-// at 128 dims, 1.8 at 64, issue slots 60 % taken (32 requests of 4-16K, two queries of 8 heads: 72 %).
+// of 4-30K tokens: 871 MB in 158 us (81 %). With 16 columns the softmax sets the pace: 0.95 us a stage
+// at 128 dims, 1.7 at 64, issue slots 60 % taken (32 requests of 4-16K, two queries of 8 heads: 595 MB
+// in 117 us, 75 %; four queries, whose two column tiles read the codes twice, 202 us, 44 %).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -264,9 +265,17 @@ struct Cta {
   uint8_t* wbuf;
   Ctl* ctl;
 
+  // The waiting, its limit and the error are a function of their own: the loops of five roles run from
+  // one instruction cache, and with the long wait inlined at each call, and the rare branches of the
+  // softmax in line, the 16-column steps took 6 to 8 % longer (32 requests of 4-16K, two queries of 8
+  // heads: 117 us against 124) and 256 short requests 111 us against 123.
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return wait_long(ctl, p.status, bar, parity);
+  }
+  static __device__ __noinline__ bool wait_long(Ctl* ctl, int32_t* status, uint64_t* bar, uint32_t parity) {
     if (mbar_wait(bar, parity, &ctl->abort, kWaitTimeoutNs)) return true;
-    if (atomicExch(&ctl->abort, 1) == 0 && p.status != nullptr) atomicAdd(p.status + NVFP4MLA_STAT_TIMEOUT, 1);
+    if (atomicExch(&ctl->abort, 1) == 0 && status != nullptr) atomicAdd(status + NVFP4MLA_STAT_TIMEOUT, 1);
     return false;
   }
   // The product with V of the stage number g is complete. Not for a stage that may have been filled
@@ -689,7 +698,7 @@ struct Cta {
               z[k + n] = s * (fs[n] * ks);
             }
           }
-          if (!whole) {
+          if (__builtin_expect(!whole, 0)) {
 #pragma unroll
             for (int c = 0; c < kCols; ++c)
               if (!page_ok || t + half > ctl->hi[buf][own + c] || t + half < ctl->lo[buf][own + c]) z[c] = neg_inf();
@@ -719,7 +728,7 @@ struct Cta {
           scores(half, b[half]);
           raise |= against(a[half], b[half]);
         }
-        if (!whole && ok && grp == 0) {
+        if (__builtin_expect(!whole && ok && grp == 0, 0)) {
           for (int half = 0; half < S::kHalves; ++half) {
             const int at = t + half;
             const bool any = page_ok && at <= at1 && at >= any_lo, all = page_ok && at <= at0 && at >= all_lo;
@@ -731,7 +740,7 @@ struct Cta {
         if (i >= S::kStreams) ok = ok && product_done(gt - S::kStreams);
         __syncwarp();
         tc_fence_after();
-        if (bar_any(1 + wi, 128, raise || !ok)) {
+        if (__builtin_expect(bar_any(1 + wi, 128, raise || !ok), 0)) {
           // rare after the first tiles: new references, the tile's own maxima where those are larger (the
           // scores are read again rather than kept in registers all the time)
 #pragma unroll
