@@ -257,7 +257,7 @@ int kv_pages_extend(int32_t* page_table, int64_t max_pages_per_seq, int32_t* seq
 
 size_t kv_pages_compact_workspace_size(int64_t num_pages) {
   if (num_pages < 1 || num_pages > INT32_MAX) return 0;
-  return ((size_t)(2 * ((num_pages / 2 + 4) / 4 * 4) + 1) * 4 + 255) / 256 * 256;
+  return ((size_t)(2 * ((num_pages / 2 + 4) / 4 * 4) + 4) * 4 + 255) / 256 * 256;
 }
 
 int kv_pages_compact(void* cache, int64_t layers, int64_t layer_stride, int64_t num_pages, int64_t page_bytes,

@@ -122,7 +122,6 @@ __device__ void exchange(PlanShared* sh, int round, int2 mine, Counts& first, Co
     const int2 sum = make_int2(__reduce_add_sync(kFull, w.x), __reduce_add_sync(kFull, w.y));
     if (lane == 0) sh->piece[round] = sum;
   }
-  __threadfence();
   cluster_sync_all();
   if (warp == 0) {
     const int rank = (int)cluster_ctarank();
@@ -428,7 +427,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 
 // ------------------------------------------------------------------ compact
 // workspace: the free pages below the live ones' number, in order, then the live pages at or above
-// it, in order (each at most half of the pages), then how many.
+// it, in order (each at most half of the pages), then how many, and the next item of the copy.
 struct CompactArgs {
   PageState s;
   PageStore c;
@@ -437,7 +436,12 @@ struct CompactArgs {
   int32_t* holes;
   int32_t* movers;
   int32_t* num_moves;
+  unsigned long long* next;
 };
+
+// remap of the g-th page that moves, until its new place is looked up in `holes`.
+__device__ __forceinline__ int32_t moving(int64_t g) { return (int32_t)(-2 - g); }
+__device__ __forceinline__ int32_t move_of(int32_t mark) { return -2 - mark; }
 
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactArgs a) {
   __shared__ PlanShared sh;
@@ -462,63 +466,80 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     c.y += hole(at, v.x) + hole(at + 1, v.y) + hole(at + 2, v.z) + hole(at + 3, v.w);
   }
   exchange(&sh, 1, make_int2(__reduce_add_sync(kFull, c.x), __reduce_add_sync(kFull, c.y)), moved, holes);
-  // list the free pages, and say where the pages that stay are
+  // list both, and say where each page goes. (What a move does to the counts, and the places of the
+  // pages that move, is left to the grid that follows: done here, it took 8 of this kernel's 18 us at 40,000 pages.)
 #pragma unroll 2
   for (int64_t i = lo; i < hi; i += 128) {
     const int64_t at = i + lane * 4;
     const int4 v = four_at(a.s.refs, at, n, 0);
     const int vs[4] = {v.x, v.y, v.z, v.w};
-    int mine = 0;
+    int mine = 0;                      // free pages below, live pages above in the upper half
 #pragma unroll
-    for (int k = 0; k < 4; ++k) mine += hole(at + k, vs[k]) ? 1 : 0;
+    for (int k = 0; k < 4; ++k) mine += (hole(at + k, vs[k]) ? 1 : 0) + (moves(at + k, vs[k]) ? 1 << 16 : 0);
     int incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(kFull, incl, d);
       if (lane >= d) incl += o;
     }
-    int g = holes.before + incl - mine;
-    holes.before += __shfl_sync(kFull, incl, 31);
+    const int all = __shfl_sync(kFull, incl, 31), before = incl - mine;
+    int g = holes.before + (before & 0xFFFF), m = moved.before + (before >> 16);
+    holes.before += all & 0xFFFF;
+    moved.before += all >> 16;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (hole(at + k, vs[k])) a.holes[g++] = (int32_t)(at + k);
-      if (at + k < n && !moves(at + k, vs[k])) a.remap[at + k] = vs[k] > 0 ? (int32_t)(at + k) : -1;
+      const int32_t page = (int32_t)(at + k);
+      if (hole(page, vs[k])) a.holes[g++] = page;
+      if (page < n) a.remap[page] = moves(page, vs[k]) ? moving(m) : (vs[k] > 0 ? page : -1);
+      if (moves(page, vs[k])) a.movers[m++] = page;
     }
   }
-  __threadfence();
-  cluster_sync_all();   // the free pages are listed, and nobody reads a count below num_live any more
-  warp_number(a.s.refs, lo, hi, n, 0, moved.before, moved.before + n, moves, [&](int64_t page, int v, int64_t g) {
-    const int32_t to = __ldcg(a.holes + g);
-    a.movers[g] = (int32_t)page;
-    a.remap[page] = to;
-    a.s.refs[to] = v;
-    a.s.refs[page] = 0;
-  });
   if (cluster_ctarank() == 0 && threadIdx.x == 0) {
     *a.num_live = (int32_t)num_live;
     *a.num_moves = moved.all;
+    *a.next = 0;
   }
   cluster_sync_all();   // no CTA leaves while another may read its count
 }
 
+// The first blocks write the tables, the counts and the places of the pages that move; the others copy
+// pages. A page's place is read by table blocks while another writes it over its mark: both say the same.
 __global__ void __launch_bounds__(kCopyThreads) compact_apply_kernel(const CompactArgs a, int table_blocks) {
   wait_for_planner();
+  const int64_t moves = *a.num_moves;
   if ((int)blockIdx.x < table_blocks) {
-    const int64_t entries = (int64_t)a.s.num_seqs * a.s.max_pages;
-    for (int64_t i = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; i < entries; i += (int64_t)table_blocks * kCopyThreads) {
+    const int64_t entries = (int64_t)a.s.num_seqs * a.s.max_pages, step = (int64_t)table_blocks * kCopyThreads;
+    for (int64_t i = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; i < entries; i += step) {
       const int32_t page = a.s.table[i];
       if (page == -1) continue;
-      const int32_t to = page >= 0 && page < a.s.num_pages ? a.remap[page] : -1;
+      int32_t to = -1;
+      if (page >= 0 && page < a.s.num_pages) {
+        to = *static_cast<volatile const int32_t*>(a.remap + page);
+        if (to < -1) to = a.holes[move_of(to)];
+      }
       if (to < 0) count_bad(a.s.status, NVFP4MLA_STAT_BAD_PAGE);
       if (to != page) a.s.table[i] = to;
     }
+    for (int64_t i = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; i < moves; i += step) {
+      const int32_t from = a.movers[i], to = a.holes[i];
+      a.s.refs[to] = a.s.refs[from];
+      a.s.refs[from] = 0;
+      a.remap[from] = to;
+    }
     return;
   }
-  const int64_t chunks = chunks_of(a.c), per = chunks * a.c.layers;
-  const int64_t items = *a.num_moves * per;
-  for (int64_t it = blockIdx.x - table_blocks; it < items; it += gridDim.x - table_blocks) {
+  // Items (page, chunk of a layer's page) are taken from a counter, the next one while this one's bytes
+  // move: with a fixed share each, blocks ended between 46 and 78 us after the start.
+  __shared__ int64_t taken[2];
+  const int64_t chunks = chunks_of(a.c), per = chunks * a.c.layers, items = moves * per;
+  int64_t it = blockIdx.x - table_blocks;
+  const int64_t others = gridDim.x - table_blocks;
+  for (int round = 0; it < items; round ^= 1) {
+    if (threadIdx.x == 0) taken[round] = others + (int64_t)atomicAdd(a.next, 1ull);
     const int64_t i = it / per, rest = it % per;
     copy_chunk(a.c, rest / chunks, a.movers[i], a.holes[i], rest % chunks);
+    __syncthreads();
+    it = taken[round];
   }
 }
 
@@ -589,14 +610,16 @@ cudaError_t launch_pages_extend(const PageState& s, const int32_t* add, int32_t*
 cudaError_t launch_pages_compact(const PageState& s, const PageStore& c, int32_t* remap, int32_t* num_live,
                                  int32_t* workspace, cudaStream_t stream) {
   const int64_t half = (s.num_pages / 2 + 4) / 4 * 4;
-  const CompactArgs a{s, c, remap, num_live, workspace, workspace + half, workspace + 2 * half};
+  const CompactArgs a{s, c, remap, num_live, workspace, workspace + half, workspace + 2 * half,
+                      reinterpret_cast<unsigned long long*>(workspace + 2 * half + 2)};
   compact_plan_kernel<<<kPlanCtas, kPlanThreads, 0, stream>>>(a);
   const cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
-  const int64_t entries = (int64_t)s.num_seqs * s.max_pages;
-  int64_t table_blocks = (entries + 4 * kCopyThreads - 1) / (4 * kCopyThreads);
+  const int64_t entries = (int64_t)s.num_seqs * s.max_pages, words = entries > s.num_pages / 2 ? entries : s.num_pages / 2;
+  int64_t table_blocks = (words + 4 * kCopyThreads - 1) / (4 * kCopyThreads);
   if (table_blocks > 1024) table_blocks = 1024;
   int64_t copy_blocks = pages_copy_blocks(c, s.num_pages / 2 + 1);
+  if (table_blocks < 1) table_blocks = 1;
   const int64_t most = (int64_t)device_sm_count() * 8;     // every block resident: 2,048 threads an SM
   if (copy_blocks > most) copy_blocks = most;
   return launch_after(compact_apply_kernel, (unsigned)(table_blocks + copy_blocks), kCopyThreads, stream, a, (int)table_blocks);
