@@ -7,6 +7,11 @@
 //
 // The floor is the traffic, three bytes per value (two in, one out). Consecutive warps take
 // consecutive heads of the same tokens, so that a token's row of all heads is read in one piece.
+//
+// Measured (device time): 12 prompts of 300-9,000 tokens, 8 heads of 128: 213 MB in 36.9 us, 5.8 TB/s,
+// 85 % of the measured copy bandwidth, ALU pipe 55 % busy (it makes the codes); 64 requests of one token:
+// 4.2 us, a launch and one chain of loads. Keys and values by one warp instead of two took 64 to 62 us,
+// the path for finite blocks 62 to 40.
 #include <cuda_fp16.h>
 
 #include "../../include/nvfp4mla.h"
@@ -18,7 +23,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kAppendThreads = 128;
+constexpr int kAppendThreads = 128;    // five such blocks an SM: 37 us (a row above), three of 256 threads 40
 
 // Two 16-bit elements (low half first) -> fp32.
 template <bool kHalf>

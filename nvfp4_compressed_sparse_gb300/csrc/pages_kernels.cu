@@ -8,6 +8,12 @@
 // the counts are exchanged through distributed shared memory, and the second pass (from cache)
 // numbers the free pages from there. The page with number g goes to the request whose range of the
 // needs' running sum holds g, so the result does not depend on the order in which threads run.
+//
+// Copies are bound by memory, planning by the latency of a few dependent passes and exchanges (1.5 us
+// each; one CTA alone took 22 us for a plan that eight take 17 for, and 10 since moves are left to the
+// copy grid). Measured (device time): 3,001 pages of 131 KB 787 MB in 117 us, 99 % of the measured copy
+// bandwidth; compaction of 40,000 pages of 22.5 KB, 9,600 of which move: 85 us, of which the copy's 432 MB
+// 70; free, fork and extend of 64 sequences over 4,096 pages together 16 us.
 #include <climits>
 #include <mutex>
 

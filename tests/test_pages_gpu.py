@@ -205,6 +205,14 @@ def test_compact_of_a_large_pool():
     s.same()
 
 
+@pytest.mark.parametrize("lens,layers,page_bytes", [([64 * 900], 2, 33008), ([0, 64 * 300, 5, 64 * 700 + 1], 3, 16400), ([64 * 9000], 1, 16)])
+def test_compact_of_more_chunks_than_blocks(lens, layers, page_bytes):
+    # several items a copy block, whose layers and chunks differ; a table much shorter than the pool
+    s = State(lens, 30000 if page_bytes == 16 else 2000, page_bytes, layers, seed=13)
+    s.compact()
+    s.same()
+
+
 def test_a_captured_step_replays_on_the_state_it_finds():
     s = State([100, 64, 1, 0, 0, 0], 40, seed=12)
     ended, src, dst, add = dev([-1]), dev([0]), dev([3]), dev(np.ones(6))
