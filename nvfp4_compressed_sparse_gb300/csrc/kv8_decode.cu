@@ -34,9 +34,11 @@
 // 16 requests of 20-90K tokens, 8 key/value heads: 1.38 GB in 210 us, 6.57 TB/s, 97 % of the measured
 // copy bandwidth; one request of 131K tokens: 269 MB in 53 us (74 %: 5 us until the first product, 7
 // from the last to the joined result). With 64 dims a byte brings twice the softmax work: 64 requests
-// of 4-30K tokens: 871 MB in 158 us (81 %). With 16 columns the softmax sets the pace: 0.95 us a stage
-// at 128 dims, 1.7 at 64, issue slots 60 % taken (32 requests of 4-16K, two queries of 8 heads: 595 MB
-// in 117 us, 75 %; four queries, whose two column tiles read the codes twice, 202 us, 44 %).
+// of 4-30K tokens: 871 MB in 154 us (83 %). With 16 columns the softmax sets the pace, some 0.9 us a
+// stage at 128 dims and 1.3 at 64 (32 requests of 4-16K, two queries of 8 heads: 595 MB in 115 us, 76 %;
+// four queries, whose two column tiles read the codes twice, 198 us, 44 %). Its instructions are what
+// there is to save: pairs of columns in one instruction took those from 117, 202 and, at 64 dims, 147
+// to 130 us, then keeping fewer values in registers to 121.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -69,6 +71,11 @@ struct Shape {
   // latency, and with 16 columns two warpgroups took 0.6 of one's time.
   static constexpr int kStreams = 2;
   static constexpr int kGroups = NC / 8;
+  // Whether a thread keeps its exponents from their check to their use, or takes them from the scores
+  // again, which are half as many registers: with 16 columns and 128 dims keeping took 98 us instead of
+  // 104 (one key/value head, 64 query heads); with 64 dims 130 instead of 120, as more than the 96
+  // registers of 640 threads were live; with 8 columns 103 instead of 101 (256 short requests).
+  static constexpr bool kKeep = kGroups > 1 && !kPair;
   static constexpr int kSoftmax = kStreams * kGroups * 128;     // its threads
   static constexpr int kThreads = 128 + kSoftmax;
   static constexpr int kTile = kPair ? 256 : 128;               // tokens of a stage
@@ -226,7 +233,8 @@ __device__ __forceinline__ void split_parts(float a, float b, uint32_t (&part)[k
   const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&h));
   // what the first part leaves has at most 20 significant bits, of which the fp16 keeps 11: as much
   // as the other parts hold
-  __half2 r = __floats2half2_rn(a - c.x, b - c.y);
+  const float2 left = __ffma2_rn(c, make_float2(-1.f, -1.f), make_float2(a, b));
+  __half2 r = __floats2half2_rn(left.x, left.y);
   const __half2 sixteen = __floats2half2_rn(16.f, 16.f);
 #pragma unroll
   for (int i = 1; i < kParts; ++i) {
@@ -246,6 +254,16 @@ __device__ __forceinline__ int ordered(float x) {
 }
 __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
 
+// The largest of three; a NaN counts as none.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ float2 pair_of(const uint32_t (&v)[N], int i) {
+  return make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+}
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 // A reference before any position: far below every exponent, and finite, so that what is left out (an
 // exponent of -inf) stays 0 against it.
@@ -537,28 +555,44 @@ struct Cta {
   // ---------------------------------------------------------------- softmax (warps 4-11)
   // A token's row of V that no column attends to becomes zeros (it may hold anything), and a NaN in
   // one that only some columns attend to is taken out and noted for those.
+  static __device__ __forceinline__ uint32_t nans_in(const uint4& x) {
+    return __vcmpeq4(x.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(x.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+           __vcmpeq4(x.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(x.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  }
+  __device__ __forceinline__ void take_out(uint8_t* bytes, int d0, int t, uint32_t buf, int stream) {
+    for (int k = 0; k < 16; ++k) {
+      if ((bytes[k] & 0x7F) != 0x7F) continue;
+      bytes[k] = 0;
+      const int d = d0 + k;
+      for (int c = 0; c < ctl->cols[buf]; ++c)
+        if (t <= ctl->hi[buf][c] && t >= ctl->lo[buf][c]) atomicOr(&ctl->poison[stream][c][d >> 5], 1u << (d & 31));
+      ctl->any_poison[stream] = 1;
+    }
+  }
   __device__ void clean_row(uint8_t* row, int r, int half, int t, bool any, uint32_t buf, int stream) {
     constexpr int kChunks = D / 16;
-    const int c0 = half * kChunks;
-#pragma unroll 1
-    for (int i = 0; i < kChunks; ++i) {
-      uint4* at = reinterpret_cast<uint4*>(row + (((c0 + i) ^ (r & 7)) * 16));
-      if (!any) {
-        *at = make_uint4(0u, 0u, 0u, 0u);
-        continue;
+    auto chunk = [&](int i) { return reinterpret_cast<uint4*>(row + (((half * kChunks + i) ^ (r & 7)) * 16)); };
+    if constexpr (S::kPair) {
+      // the loads of a row of 64 dims all in flight: 32 requests' four queries in a window 58 us instead of
+      // 60 (with 128 dims, more code than it saves: 256 short requests 108 instead of 102)
+      uint4 x[kChunks];
+      uint32_t nan = 0;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (any) x[i] = *chunk(i);
+        else *chunk(i) = x[i];
       }
-      const uint4 x = *at;
-      const uint32_t nan = __vcmpeq4(x.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(x.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
-                           __vcmpeq4(x.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(x.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-      if (nan == 0) continue;
-      uint8_t* bytes = reinterpret_cast<uint8_t*>(at);
-      for (int k = 0; k < 16; ++k) {
-        if ((bytes[k] & 0x7F) != 0x7F) continue;
-        bytes[k] = 0;
-        const int d = i * 16 + k;
-        for (int c = 0; c < ctl->cols[buf]; ++c)
-          if (t <= ctl->hi[buf][c] && t >= ctl->lo[buf][c]) atomicOr(&ctl->poison[stream][c][d >> 5], 1u << (d & 31));
-        ctl->any_poison[stream] = 1;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) nan |= nans_in(x[i]);
+      if (nan == 0) return;
+#pragma unroll 1
+      for (int i = 0; i < kChunks; ++i) take_out(reinterpret_cast<uint8_t*>(chunk(i)), i * 16, t, buf, stream);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kChunks; ++i) {
+        if (!any) *chunk(i) = make_uint4(0u, 0u, 0u, 0u);
+        else if (nans_in(*chunk(i)) != 0) take_out(reinterpret_cast<uint8_t*>(chunk(i)), i * 16, t, buf, stream);
       }
     }
   }
@@ -680,22 +714,25 @@ struct Cta {
         // the columns or for none
         const bool whole = pages == (1u << S::kPages) - 1 && t0 + S::kTile - 1 <= at0 && t0 >= all_lo;
         const bool page_ok = (pages >> h) & 1;
-        // exponents (log2 units) of the scores of a half's token
+        // exponents (log2 units) of the scores of a half's token; two columns an instruction here and below,
+        // and four columns' parts at a time, as registers are short (eight: 63 us instead of 60, as above)
         auto scores = [&](int half, float (&z)[kCols]) {
-          uint32_t part[kQParts][kCols];
-#pragma unroll
-          for (int k = 0; k < kQParts; ++k) tmem_ld8(s_at + sb * S::kSBuf + half * S::kNS + k * NC, part[k]);
-          tmem_wait_ld();
 #pragma unroll
           for (int k = 0; k < kCols; k += 4) {
+            uint32_t part[kQParts][4];
+#pragma unroll
+            for (int q = 0; q < kQParts; ++q) tmem_ld4(s_at + sb * S::kSBuf + half * S::kNS + q * NC + k, part[q]);
+            tmem_wait_ld();
             const float4 f = *reinterpret_cast<const float4*>(&ctl->f[buf][own + k]);
-            const float fs[4] = {f.x, f.y, f.z, f.w};
+            const float2 fs[2] = {make_float2(f.x, f.y), make_float2(f.z, f.w)};
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              float s = __uint_as_float(part[kQParts - 1][k + n]);
+            for (int n = 0; n < 2; ++n) {
+              float2 s = pair_of(part[kQParts - 1], 2 * n);
 #pragma unroll
-              for (int q = kQParts - 2; q >= 0; --q) s = fmaf(s, 1.f / 16.f, __uint_as_float(part[q][k + n]));
-              z[k + n] = s * (fs[n] * ks);
+              for (int q = kQParts - 2; q >= 0; --q) s = __ffma2_rn(s, make_float2(1.f / 16.f, 1.f / 16.f), pair_of(part[q], 2 * n));
+              s = __fmul2_rn(s, __fmul2_rn(fs[n], make_float2(ks, ks)));
+              z[k + 2 * n] = s.x;
+              z[k + 2 * n + 1] = s.y;
             }
           }
           if (__builtin_expect(!whole, 0)) {
@@ -705,28 +742,44 @@ struct Cta {
           }
         };
         // and against the references: of the weights, and of the sum
-        float a[S::kHalves][kCols], b[S::kHalves][kCols];
-        auto against = [&](float (&a)[kCols], float (&b)[kCols]) {
-          bool raise = false;
+        auto refs = [&](const float* top, int k, float2 (&r)[2]) {
+          const float4 t = *reinterpret_cast<const float4*>(top + own + k);
+          r[0] = make_float2(t.x, t.y);
+          r[1] = make_float2(t.z, t.w);
+        };
+        auto less = [&](float2 z, float2 r) { return __ffma2_rn(r, make_float2(-1.f, -1.f), z); };
+        auto plus_ev = [&](float2 z) { return __fadd2_rn(z, make_float2(ev, ev)); };
+        float z[S::kHalves][kCols], kept[kCols];
+        // whether an exponent is too far above; kKeep: z and kept become the exponents
+        auto above = [&](float (&z)[kCols]) {
+          float most_w = neg_inf(), most_s = neg_inf();
 #pragma unroll
           for (int k = 0; k < kCols; k += 4) {
-            const float4 rw = *reinterpret_cast<const float4*>(&ctl->top_w[stream][own + k]);
-            const float4 rs = *reinterpret_cast<const float4*>(&ctl->top_s[stream][own + k]);
-            const float rws[4] = {rw.x, rw.y, rw.z, rw.w}, rss[4] = {rs.x, rs.y, rs.z, rs.w};
+            float2 rw[2], rs[2];
+            refs(ctl->top_w[stream], k, rw);
+            refs(ctl->top_s[stream], k, rs);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              a[k + n] = (b[k + n] + ev) - rws[n];
-              b[k + n] -= rss[n];
-              raise |= a[k + n] > kWeightScale + kHeadroom || b[k + n] > kSumHeadroom;
+            for (int n = 0; n < 2; ++n) {
+              const int c = k + 2 * n;
+              const float2 x = make_float2(z[c], z[c + 1]);
+              const float2 w = less(S::kKeep ? plus_ev(x) : x, rw[n]), s = less(x, rs[n]);
+              if constexpr (S::kKeep) {
+                kept[c] = w.x;
+                kept[c + 1] = w.y;
+                z[c] = s.x;
+                z[c + 1] = s.y;
+              }
+              most_w = max3(most_w, w.x, w.y);
+              most_s = max3(most_s, s.x, s.y);
             }
           }
-          return raise;
+          return (S::kKeep ? most_w : most_w + ev) > kWeightScale + kHeadroom || most_s > kSumHeadroom;
         };
         bool raise = false;
 #pragma unroll
         for (int half = 0; half < S::kHalves; ++half) {
-          scores(half, b[half]);
-          raise |= against(a[half], b[half]);
+          scores(half, z[half]);
+          raise |= above(z[half]);
         }
         if (__builtin_expect(!whole && ok && grp == 0, 0)) {
           for (int half = 0; half < S::kHalves; ++half) {
@@ -743,15 +796,16 @@ struct Cta {
         if (__builtin_expect(bar_any(1 + wi, 128, raise || !ok), 0)) {
           // rare after the first tiles: new references, the tile's own maxima where those are larger (the
           // scores are read again rather than kept in registers all the time)
+          float top[kCols];
 #pragma unroll
           for (int half = 0; half < S::kHalves; ++half) {
-            scores(half, b[half]);
+            scores(half, z[half]);
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) a[0][c] = half == 0 ? b[0][c] : fmaxf(a[0][c], b[half][c]);
+            for (int c = 0; c < kCols; ++c) top[c] = half == 0 ? z[0][c] : fmaxf(top[c], z[half][c]);
           }
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
-            const int ms = __reduce_max_sync(kFull, ordered(a[0][c])), mw = __reduce_max_sync(kFull, ordered(a[0][c] + ev));
+            const int ms = __reduce_max_sync(kFull, ordered(top[c])), mw = __reduce_max_sync(kFull, ordered(top[c] + ev));
             if (lane == 0) {
               ctl->part_max[stream][warp][own + c][0] = unordered(mw);
               ctl->part_max[stream][warp][own + c][1] = unordered(ms);
@@ -778,8 +832,7 @@ struct Cta {
           bar_sync(1 + wi, 128);
 #pragma unroll
           for (int c = 0; c < kCols; ++c) l[c] *= ctl->scale_l[stream][own + c];
-#pragma unroll
-          for (int half = 0; half < S::kHalves; ++half) against(a[half], b[half]);
+          if constexpr (S::kKeep) above(z[0]);
           if (i >= S::kStreams) {
             __syncwarp();
 #pragma unroll 1
@@ -804,10 +857,26 @@ struct Cta {
 #pragma unroll
           for (int k = 0; k < kCols; k += 4) {
             float e[4];
+            float2 rw[2], rs[2];
+            if constexpr (!S::kKeep) {
+              refs(ctl->top_w[stream], k, rw);
+              refs(ctl->top_s[stream], k, rs);
+            }
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              e[n] = ex2_approx(a[half][k + n]);
-              l[k + n] += ex2_approx(b[half][k + n]);
+            for (int n = 0; n < 4; n += 2) {
+              const int c = k + n;
+              float2 w, s = make_float2(z[half][c], z[half][c + 1]);
+              if constexpr (S::kKeep) {
+                w = make_float2(kept[c], kept[c + 1]);
+              } else {
+                w = less(plus_ev(s), rw[n / 2]);
+                s = less(s, rs[n / 2]);
+              }
+              e[n] = ex2_approx(w.x);
+              e[n + 1] = ex2_approx(w.y);
+              const float2 sum = __fadd2_rn(make_float2(l[c], l[c + 1]), make_float2(ex2_approx(s.x), ex2_approx(s.y)));
+              l[c] = sum.x;
+              l[c + 1] = sum.y;
             }
             uint32_t p01[kWParts], p23[kWParts];
             split_parts(e[0], e[1], p01);
