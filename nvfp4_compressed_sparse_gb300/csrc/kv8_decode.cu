@@ -247,17 +247,16 @@ __device__ __forceinline__ void split_parts(float a, float b, uint32_t (&part)[k
   }
 }
 
-// fp32 in an order-preserving signed integer.
-__device__ __forceinline__ int ordered(float x) {
-  const int i = __float_as_int(x);
-  return i ^ ((i >> 31) & 0x7FFFFFFF);
-}
-__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
-
 // The largest of three; a NaN counts as none.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// The largest over the warp; a NaN counts as none.
+__device__ __forceinline__ float redux_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
 template <int N>
@@ -805,11 +804,8 @@ struct Cta {
           }
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
-            const int ms = __reduce_max_sync(kFull, ordered(top[c])), mw = __reduce_max_sync(kFull, ordered(top[c] + ev));
-            if (lane == 0) {
-              ctl->part_max[stream][warp][own + c][0] = unordered(mw);
-              ctl->part_max[stream][warp][own + c][1] = unordered(ms);
-            }
+            const float ms = redux_max(top[c]), mw = redux_max(top[c] + ev);
+            if (lane == 0) *reinterpret_cast<float2*>(ctl->part_max[stream][warp][own + c]) = make_float2(mw, ms);
           }
           if (bar_any(1 + wi, 128, !ok)) {
             stop = true;
@@ -820,8 +816,9 @@ struct Cta {
             const float w0 = ctl->top_w[stream][c], s0 = ctl->top_s[stream][c];
             float w1 = w0 + kWeightScale, s1 = s0;
             for (int k = 0; k < 4; ++k) {
-              w1 = fmaxf(w1, ctl->part_max[stream][k][c][0]);
-              s1 = fmaxf(s1, ctl->part_max[stream][k][c][1]);
+              const float2 most = *reinterpret_cast<const float2*>(ctl->part_max[stream][k][c]);
+              w1 = fmaxf(w1, most.x);
+              s1 = fmaxf(s1, most.y);
             }
             w1 = w1 > kNone / 2 ? w1 - kWeightScale : w0;
             ctl->top_w[stream][c] = w1;
@@ -1026,7 +1023,7 @@ __global__ void __launch_bounds__(Shape<D, NC, kHalf ? 3 : 2>::kThreads, 1) kv8_
   using S = Shape<D, NC, kHalf ? 3 : 2>;
   using Ctl = Control<NC, S::kStages, S::kPages, S::kStreams, S::kThreads / 32>;
   static_assert(offsetof(Ctl, scales) % 16 == 0 && offsetof(Ctl, f) % 16 == 0 && offsetof(Ctl, top_w) % 16 == 0 &&
-                offsetof(Ctl, top_s) % 16 == 0 && NC % 8 == 0, "vector accesses are aligned");
+                offsetof(Ctl, top_s) % 16 == 0 && offsetof(Ctl, part_max) % 8 == 0 && NC % 8 == 0, "vector accesses are aligned");
   static_assert(sizeof(Ctl) <= 6144, "the control block fits its share");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
