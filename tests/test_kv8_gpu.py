@@ -214,6 +214,32 @@ def test_decode_many_requests_of_a_tile_or_two(D, Hk, G, max_ctas):
     check(*c.run(max_ctas=max_ctas), c.reference())
 
 
+@pytest.mark.parametrize("D,Hk,G,Q,dtype", [(64, 2, 2, 1, "bf16"), (64, 3, 12, 1, "fp16"), (128, 8, 4, 2, "bf16"), (128, 2, 16, 3, "fp16"),
+                                            (64, 4, 5, 4, "bf16"), (128, 1, 1, 1, "fp16")])
+@pytest.mark.parametrize("max_ctas", [0, 2, 7])
+def test_decode_of_short_requests_only(D, Hk, G, Q, dtype, max_ctas):
+    """Every unit has a tile or two: the streams take units in turn."""
+    top = 256 if D == 128 else 512
+    lens = np.random.default_rng(D + G + Q).choice([0, 1, 7, 64, top // 2 - 1, top // 2, top // 2 + 1, top - 1, top], 170)
+    c = Case(lens, Hk, D, dtype, G=G, Q=Q, seed=G)
+    check(*c.run(max_ctas=max_ctas), c.reference())
+
+
+@pytest.mark.parametrize("D,G", [(64, 4), (64, 16), (128, 4), (128, 16)])
+def test_decode_of_short_requests_with_nan_and_windows(D, G):
+    """As above, with NaN in values that some queries attend to, a window, and pages that are none."""
+    lens = np.random.default_rng(D + G).integers(1, 256, 120)
+    c = Case(lens, 2, D, "bf16", G=G, Q=3, seed=G)
+    codes, _ = kv8.parts(c.cache, 2, D)
+    for b in range(0, 120, 7):
+        t = int(lens[b]) - 1 - b % 3                        # the newest positions: some queries see them
+        if t >= 0:
+            codes[c.table[b, t // 64], 1, b % 2, t % 64, b % D] = 0x7F
+    c.table[3::11, 0] = -1
+    for window in (0, 70):
+        check(*c.run(window, max_ctas=5), c.reference(window))
+
+
 def test_decode_scales_far_apart():
     """Blocks whose scales differ by up to 2^60, keys and values apart; and a block of zeros."""
     c = Case([300, 1200], 2, 128, "bf16", Q=2, G=4, seed=9)
