@@ -460,6 +460,12 @@ def _optional_ptr(t, name, index):
     return None if t is None else _ptr_of(t, name, torch.int32, index, 1)
 
 
+def _status_ptr(t, index):
+    if t is not None and t.shape[0] < 4:     # NVFP4MLA_STATUS_WORDS
+        raise ValueError("dev_status: must have 4 words")
+    return _optional_ptr(t, "dev_status", index)
+
+
 def _raw_stream(stream, index):
     import torch
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
@@ -520,7 +526,7 @@ def kv8_append(k, v, cu_tokens, seq_lens, page_table, cache, dev_status=None, st
     if hk == 1:
         k1 = v1 = 0
     rc = lib.kv8_append(kp, k0, k1, vp, v0, v1, dt, n, cup, sp, pp, page_table.shape[1], B, hk, d, cp, pages,
-                        _optional_ptr(dev_status, "dev_status", index), _raw_stream(stream, index))
+                        _status_ptr(dev_status, index), _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv8_append")
 
@@ -563,10 +569,14 @@ def kv8_decode(q, cache, page_table, seq_lens, kv_heads: int, softmax_scale, win
     if workspace is None:
         workspace = fresh[2] = torch.empty(max(kv8_decode_workspace_size(B, Q, H, kv_heads, d), 1), dtype=torch.uint8,
                                            device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    if not 0 <= window < 1 << 31:
+        raise ValueError("window must be 0 (none) or a number of positions below 2^31")
     rc = lib.kv8_decode(qp, s1 if Q > 1 else s0 if B > 1 else 0, s2 if H > 1 else 0, dt, cp, pages, pp, max_pages, sp,
                         B, Q, H, kv_heads, d, float(softmax_scale), int(window), op, lp, workspace.data_ptr(),
                         workspace.nbytes,
-                        _optional_ptr(dev_status, "dev_status", index),
+                        _status_ptr(dev_status, index),
                         (int(max_ctas) & 0xFFFF) | (FLAG_TEST_TIMEOUT if test_timeout else 0), _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv8_decode")
@@ -599,7 +609,7 @@ def kv_pages_copy(cache, src, dst, dev_status=None, stream=None, layered: bool =
     n = src.shape[0]
     if dst.shape[0] != n:
         raise ValueError("src and dst must have the same length")
-    rc = lib.kv_pages_copy(cp, layers, stride, pages, each, sp, dp, n, _optional_ptr(dev_status, "dev_status", index),
+    rc = lib.kv_pages_copy(cp, layers, stride, pages, each, sp, dp, n, _status_ptr(dev_status, index),
                            _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv_pages_copy")
@@ -626,7 +636,7 @@ def kv_pages_free(page_table, seq_lens, refcounts, seqs, dev_status=None, stream
     index = page_table.get_device()
     state = _page_state(page_table, seq_lens, refcounts, index)
     rc = load_library().kv_pages_free(*state, _ptr_of(seqs, "seqs", torch.int32, index, 1), seqs.shape[0],
-                                      _optional_ptr(dev_status, "dev_status", index), _raw_stream(stream, index))
+                                      _status_ptr(dev_status, index), _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv_pages_free")
 
@@ -650,7 +660,7 @@ def kv_pages_fork(cache, page_table, seq_lens, refcounts, src, dst, new_pages=No
     if dst.shape[0] != n or new_pages.shape[0] != n:
         raise ValueError("src, dst and new_pages must have the same length")
     rc = load_library().kv_pages_fork(cp, layers, stride, pages, each, pp, width, lp, seqs, rp, sp, dp, n, np_,
-                                      _optional_ptr(dev_status, "dev_status", index), _raw_stream(stream, index))
+                                      _status_ptr(dev_status, index), _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv_pages_fork")
     _keep(stream, fresh)
@@ -666,7 +676,7 @@ def kv_pages_extend(page_table, seq_lens, refcounts, add, granted=None, dev_stat
     ap, gp = _ptr_of(add, "add", torch.int32, index, 1), _optional_ptr(granted, "granted", index)
     if add.shape[0] != state[3] or (granted is not None and granted.shape[0] != state[3]):
         raise ValueError("add and granted must have one entry per sequence")
-    rc = load_library().kv_pages_extend(*state, ap, gp, _optional_ptr(dev_status, "dev_status", index),
+    rc = load_library().kv_pages_extend(*state, ap, gp, _status_ptr(dev_status, index),
                                         _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv_pages_extend")
@@ -697,9 +707,11 @@ def kv_pages_compact(cache, page_table, refcounts, remap=None, num_live=None, wo
         raise ValueError("remap must have one entry per page, num_live one")
     if workspace is None:
         workspace = fresh[2] = torch.empty(kv_pages_compact_workspace_size(pages), dtype=torch.uint8, device=cache.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
     rc = load_library().kv_pages_compact(cp, layers, stride, pages, each, pp, width, seqs, rp, mp, lp,
                                          workspace.data_ptr(), workspace.nbytes,
-                                         _optional_ptr(dev_status, "dev_status", index), _raw_stream(stream, index))
+                                         _status_ptr(dev_status, index), _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv_pages_compact")
     _keep(stream, *fresh)

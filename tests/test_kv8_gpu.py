@@ -447,3 +447,29 @@ def test_decode_of_expanded_and_one_entry_axes():
     wide = torch.randn((2, 1, 1, 100), device="cuda").to(torch.bfloat16)
     q = wide.as_strided((2, 1, 1, 64), (0, 7, 13, 1))
     check(*c.run(q=q), c.reference(q=q))
+
+
+def test_refusals():
+    c = Case([100, 30], 2, 64, "bf16", G=2, seed=30)
+    cache, table, lens, short = dev(c.cache, torch.uint8), dev(c.table), dev(c.lens), dev(np.zeros(3))
+    k, cu = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda"), dev([0, 1, 2])
+    ws = torch.empty(2 * m.kv8_decode_workspace_size(2, 1, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    before = cache.clone()
+    odd = torch.zeros(2, 2, 65, dtype=torch.bfloat16, device="cuda")[:, :, :64]      # strides that are no multiples of 8
+    decodes = [dict(window=-1), dict(window=1 << 31), dict(window=(1 << 32) + 5), dict(dev_status=short), dict(workspace=ws[::2]),
+               dict(workspace=ws[:256]), dict(workspace=ws[4:]), dict(q=c.q.cpu()), dict(q=c.q.float()), dict(q=c.q[..., ::2]),
+               dict(q=c.q[:1]), dict(out=torch.empty_like(c.q).half()), dict(lse=torch.empty(2, 1, 3, device="cuda"))]
+    calls = [lambda kw=kw: m.kv8_decode(kw.pop("q", c.q), cache, table, lens, 2, c.scale, **kw) for kw in decodes]
+    calls += [lambda: m.kv8_decode(c.q, cache, table, lens, 2, 0.0), lambda: m.kv8_decode(c.q, cache, table, lens, 3, c.scale),
+              lambda: m.kv8_decode(c.q, cache[:, :-1], table, lens, 2, c.scale),
+              lambda: m.kv8_append(k, k, cu, lens, table, cache, dev_status=short), lambda: m.kv8_append(odd, k, cu, lens, table, cache),
+              lambda: m.kv8_append(k, k.half(), cu, lens, table, cache), lambda: m.kv8_append(k, k[:1], cu, lens, table, cache),
+              lambda: m.kv8_append(k, k, cu[:2], lens, table, cache), lambda: m.kv8_append(k, k, cu, lens, table, cache.cpu()),
+              lambda: m.kv8_append(k[:, :1], k[:, :1], cu, lens, table, cache)]
+    for i, call in enumerate(calls):
+        with pytest.raises((ValueError, TypeError, m.NvFp4MlaError)):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    torch.cuda.synchronize()
+    assert torch.equal(cache, before)
+    check(*c.run(), c.reference())

@@ -248,6 +248,37 @@ def test_a_captured_step_replays_on_the_state_it_finds():
         s.same()
 
 
+def test_refusals_leave_everything_as_it_was():
+    s = State([100, 64, 0], 40, seed=20)
+    seqs, short = dev([0]), dev(np.zeros(3))
+    misaligned = torch.zeros(41, dtype=torch.int32, device="cuda")[1:]
+    ws = torch.empty(2 * m.kv_pages_compact_workspace_size(40), dtype=torch.uint8, device="cuda")
+    calls = [lambda: m.kv_pages_copy(s.d_cache, seqs, seqs, dev_status=short, layered=True),
+             lambda: m.kv_pages_copy(s.d_cache, seqs, seqs[:0], layered=True),
+             lambda: m.kv_pages_copy(s.d_cache[:, ::2], seqs, seqs, layered=True),
+             lambda: m.kv_pages_free(s.d_table, s.d_lens, s.d_refs, seqs, dev_status=short),
+             lambda: m.kv_pages_free(s.d_table, s.d_lens[:2], s.d_refs, seqs),
+             lambda: m.kv_pages_free(s.d_table, s.d_lens, misaligned, seqs),
+             lambda: m.kv_pages_free(s.d_table.cpu(), s.d_lens, s.d_refs, seqs),
+             lambda: m.kv_pages_fork(s.d_cache, s.d_table, s.d_lens, s.d_refs, seqs, seqs, dev_status=short, layered=True),
+             lambda: m.kv_pages_fork(s.d_cache, s.d_table, s.d_lens, s.d_refs[:20], seqs, seqs, layered=True),
+             lambda: m.kv_pages_fork(s.d_cache, s.d_table, s.d_lens, s.d_refs, seqs, dev([0, 1]), layered=True),
+             lambda: m.kv_pages_extend(s.d_table, s.d_lens, s.d_refs, dev([1, 1, 1]), dev_status=short),
+             lambda: m.kv_pages_extend(s.d_table, s.d_lens, s.d_refs, dev([1, 1])),
+             lambda: m.kv_pages_extend(s.d_table, s.d_lens, s.d_refs, dev([1, 1, 1]), granted=dev([0])),
+             lambda: m.kv_pages_compact(s.d_cache, s.d_table, s.d_refs, dev_status=short, layered=True),
+             lambda: m.kv_pages_compact(s.d_cache, s.d_table, s.d_refs, workspace=ws[::2], layered=True),
+             lambda: m.kv_pages_compact(s.d_cache, s.d_table, s.d_refs, workspace=ws[:100], layered=True),
+             lambda: m.kv_pages_compact(s.d_cache, s.d_table, s.d_refs, workspace=ws[1:], layered=True),
+             lambda: m.kv_pages_compact(s.d_cache, s.d_table, s.d_refs, remap=dev([0]), layered=True)]
+    for i, call in enumerate(calls):
+        with pytest.raises((ValueError, TypeError, m.NvFp4MlaError)):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    torch.cuda.synchronize()
+    s.same()
+
+
 @pytest.mark.parametrize("D,dtype", [(64, torch.float16), (128, torch.bfloat16)])
 def test_a_server_runs_on_the_operators_alone(D, dtype):
     """Prompts, decode steps, forks that share pages, endings and a compaction: after each, the attention over
