@@ -281,16 +281,19 @@ __device__ int fork_length(const ForkArgs& a, int i, bool& missing) {
 }
 
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs a) {
-  extern __shared__ int32_t sum[];   // [n + 1]
+  extern __shared__ int32_t sum[];   // [n + 1], then per pair the length that it copies, -1: none
   __shared__ PlanShared sh;
+  int32_t* copies = sum + a.n + 1;   // (each is only its own thread's, pair i's thread i mod kPlanThreads)
   let_dependents_start();
   const int rank = (int)cluster_ctarank();
-  // claims
-  for (int i = rank * kPlanThreads + threadIdx.x; i < a.n; i += kPlanCtas * kPlanThreads) {
+  const auto owns = [=](int i) { return i / kPlanThreads % kPlanCtas == rank; };
+  // claims: every CTA makes all of them, as it needs the lengths, and once is as good as eight times
+  for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
     bool missing;
     const int len = fork_length(a, i, missing);
+    copies[i] = len;
     if (len < 0) {
-      count_bad(a.s.status, missing ? NVFP4MLA_STAT_BAD_PAGE : NVFP4MLA_STAT_BAD_SLOT);
+      if (owns(i)) count_bad(a.s.status, missing ? NVFP4MLA_STAT_BAD_PAGE : NVFP4MLA_STAT_BAD_SLOT);
       continue;
     }
     int32_t* at = a.s.lens + a.dst[i];
@@ -299,36 +302,25 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   }
   cluster_sync_all();   // every claim is made
   // who won, and what that needs
-  auto won = [&](int i, int& len) {
-    bool missing;
-    len = fork_length(a, i, missing);
-    return len >= 0 && __ldcg(a.s.lens + a.dst[i]) == kClaim + i;
-  };
   const int64_t total = sum_needs(&sh, sum, a.n, [&](int i) {
-    int len;
-    return won(i, len) && len % kPageTokens != 0 ? 1 : 0;
+    const int len = copies[i];
+    if (len < 0 || __ldcg(a.s.lens + a.dst[i]) != kClaim + i) {
+      copies[i] = -1;
+      return 0;
+    }
+    return len % kPageTokens != 0 ? 1 : 0;
   });
-  // this thread's own pairs, read before any length is set
-  constexpr int kOwn = NVFP4MLA_MAX_REQUESTS / (kPlanCtas * kPlanThreads);
-  int own_len[kOwn];
-#pragma unroll
-  for (int k = 0; k < kOwn; ++k) {
-    const int i = (k * kPlanCtas + rank) * kPlanThreads + threadIdx.x;
-    int len = -1;
-    own_len[k] = i < a.n && won(i, len) ? len : -1;
-  }
   int64_t lo, hi;
   piece_of(a.s.num_pages, lo, hi);
   Counts free_pages, unused;
   exchange(&sh, 0, make_int2(warp_count(a.s.refs, lo, hi, a.s.num_pages, 1, IsFree()), 0), free_pages, unused);
   const int64_t all = free_pages.all;
-#pragma unroll
-  for (int k = 0; k < kOwn; ++k) {
-    const int i = (k * kPlanCtas + rank) * kPlanThreads + threadIdx.x;
-    if (i >= a.n) continue;
+  // (every CTA has read the lengths: they may change)
+  for (int i = rank * kPlanThreads + threadIdx.x; i < a.n; i += kPlanCtas * kPlanThreads) {
+    const int len = copies[i];
     const bool needs = sum[i + 1] > sum[i], refused = needs && sum[i] >= all;
-    if (own_len[k] >= 0) a.s.lens[a.dst[i]] = refused ? 0 : own_len[k];
-    if (own_len[k] < 0 || refused) a.new_pages[i] = -2;
+    if (len >= 0) a.s.lens[a.dst[i]] = refused ? 0 : len;
+    if (len < 0 || refused) a.new_pages[i] = -2;
     else if (!needs) a.new_pages[i] = -1;
   }
   warp_number(a.s.refs, lo, hi, a.s.num_pages, 1, free_pages.before, total, IsFree(), [&](int64_t page, int, int64_t g) {
@@ -564,7 +556,7 @@ cudaError_t launch_after(void (*kernel)(P...), unsigned blocks, unsigned threads
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Shared memory of the running sums (up to MAX_REQUESTS + 1 of them), allowed once per device.
+// Shared memory of the running sums (up to MAX_REQUESTS + 1 of them) and lengths, allowed once per device.
 cudaError_t allow_sums(const void* kernel, int which) {
   static std::mutex mu;
   static bool done[2][64] = {};
@@ -573,7 +565,7 @@ cudaError_t allow_sums(const void* kernel, int which) {
   if (err != cudaSuccess) return err;
   std::lock_guard<std::mutex> lock(mu);
   if (dev < 64 && done[which][dev]) return cudaSuccess;
-  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (NVFP4MLA_MAX_REQUESTS + 1) * 4);
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (2 * NVFP4MLA_MAX_REQUESTS + 1) * 4);
   if (err == cudaSuccess && dev < 64) done[which][dev] = true;
   return err;
 }
@@ -599,7 +591,7 @@ cudaError_t launch_pages_fork(const PageState& s, const PageStore& c, const int3
   const ForkArgs a{s, c, src, dst, n, new_pages};
   cudaError_t err = allow_sums(reinterpret_cast<const void*>(fork_plan_kernel), 0);
   if (err != cudaSuccess) return err;
-  fork_plan_kernel<<<kPlanCtas, kPlanThreads, (size_t)(n + 1) * 4, stream>>>(a);
+  fork_plan_kernel<<<kPlanCtas, kPlanThreads, (size_t)(2 * n + 1) * 4, stream>>>(a);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
   const int64_t per = pages_copy_blocks(c, 1) + (s.max_pages + kRowEntries - 1) / kRowEntries;
   return launch_after(fork_apply_kernel, (unsigned)(n * per), kCopyThreads, stream, a);
