@@ -71,11 +71,6 @@ struct Shape {
   // latency, and with 16 columns two warpgroups took 0.6 of one's time.
   static constexpr int kStreams = 2;
   static constexpr int kGroups = NC / 8;
-  // Whether a thread keeps its exponents from their check to their use, or takes them from the scores
-  // again, which are half as many registers: with 16 columns and 128 dims keeping took 98 us instead of
-  // 104 (one key/value head, 64 query heads); with 64 dims 130 instead of 120, as more than the 96
-  // registers of 640 threads were live; with 8 columns 103 instead of 101 (256 short requests).
-  static constexpr bool kKeep = kGroups > 1 && !kPair;
   static constexpr int kSoftmax = kStreams * kGroups * 128;     // its threads
   static constexpr int kThreads = 128 + kSoftmax;
   static constexpr int kTile = kPair ? 256 : 128;               // tokens of a stage
@@ -631,40 +626,56 @@ struct Cta {
   static __device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
 
   // Joins the partial results that CTAs c_lo .. c_hi left of a unit, for dim d of this warpgroup's
-  // columns: some partial results at a time, every load of them in flight together.
+  // columns, 32 at a time: a lane has the maxima and sums of one, and the outputs of kSlots are in flight
+  // together, the first of them beside the maxima. (It has few registers on purpose: with every part's
+  // maxima and sums in each thread, the tile loop's values were spilled: with 16 columns 197 us instead of
+  // 178, 32 requests of 4-16K, four queries of 8 heads, and 120 instead of 106 with 64 dims.)
   template <bool kHalf>
   __device__ void join(const int* row, int c, int d, int c_lo, int c_hi, int first) {
-    constexpr int kN = NC / (S::kSoftmax / 128), kSlots = S::kThreads == 384 ? 8 : 16 / kN;
+    constexpr int kN = NC / (S::kSoftmax / 128), kSlots = S::kThreads == 384 ? 8 : 4;
+    const int lane = threadIdx.x & 31;
     float m[kN], sum[kN], acc[kN];
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
       m[k] = kNone;
       sum[k] = acc[k] = 0.f;
     }
+    auto at = [&](int cta) { return (2 * cta + (cta == c_lo ? first : 0)) * NC + c; };
 #pragma unroll 1
-    for (int s0 = c_lo; s0 <= c_hi; s0 += kSlots) {
-      float o[kSlots][kN];
-      float2 ml[kSlots][kN];
+    for (int s0 = c_lo; s0 <= c_hi; s0 += 32) {
+      const int n = min(32, c_hi - s0 + 1);
+      float o[kSlots][kN], w[kN], l[kN];
+      auto load = [&](int from) {
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        if (s0 + i > c_hi) break;
-        const int at = (2 * (s0 + i) + (s0 + i == c_lo ? first : 0)) * NC + c;
+        for (int i = 0; i < kSlots; ++i)
 #pragma unroll
-        for (int k = 0; k < kN; ++k) {
-          ml[i][k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at + k);
-          o[i][k] = __ldcg(p.part_o + (int64_t)(at + k) * D + d);
-        }
+          for (int k = 0; k < kN; ++k) o[i][k] = from + i < n ? __ldcg(p.part_o + (int64_t)(at(s0 + from + i) + k) * D + d) : 0.f;
+      };
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        const float2 ml = lane < n ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at(s0 + lane) + k) : make_float2(kNone, 0.f);
+        w[k] = ml.x;
+        l[k] = ml.y;
       }
+      load(0);
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        if (s0 + i > c_hi) break;
+      for (int k = 0; k < kN; ++k) {
+        const float m_new = fmaxf(m[k], redux_max(w[k])), keep = ratio(m[k], m_new);
+        w[k] = ratio(w[k], m_new);
+        l[k] *= w[k];
 #pragma unroll
-        for (int k = 0; k < kN; ++k) {
-          const float m_new = fmaxf(m[k], ml[i][k].x), keep = ratio(m[k], m_new), in = ratio(ml[i][k].x, m_new);
-          sum[k] = sum[k] * keep + ml[i][k].y * in;
-          acc[k] = acc[k] * keep + o[i][k] * in;
-          m[k] = m_new;
-        }
+        for (int x = 16; x > 0; x >>= 1) l[k] += __shfl_xor_sync(kFull, l[k], x);
+        sum[k] = sum[k] * keep + l[k];
+        acc[k] *= keep;
+        m[k] = m_new;
+      }
+#pragma unroll 1
+      for (int from = 0; from < n; from += kSlots) {
+        if (from > 0) load(from);
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i)
+#pragma unroll
+          for (int k = 0; k < kN; ++k) acc[k] = fmaf(o[i][k], __shfl_sync(kFull, w[k], (from + i) & 31), acc[k]);
       }
     }
 #pragma unroll
@@ -747,10 +758,10 @@ struct Cta {
           r[1] = make_float2(t.z, t.w);
         };
         auto less = [&](float2 z, float2 r) { return __ffma2_rn(r, make_float2(-1.f, -1.f), z); };
-        auto plus_ev = [&](float2 z) { return __fadd2_rn(z, make_float2(ev, ev)); };
-        float z[S::kHalves][kCols], kept[kCols];
-        // whether an exponent is too far above; kKeep: z and kept become the exponents
-        auto above = [&](float (&z)[kCols]) {
+        // (z becomes the sum's; taking both from the scores again later, for fewer registers, took 182 us
+        // instead of 178 with 16 columns, four queries of 8 heads)
+        float z[S::kHalves][kCols], zw[S::kHalves][kCols];
+        auto against = [&](float (&zw)[kCols], float (&z)[kCols]) {
           float most_w = neg_inf(), most_s = neg_inf();
 #pragma unroll
           for (int k = 0; k < kCols; k += 4) {
@@ -761,24 +772,22 @@ struct Cta {
             for (int n = 0; n < 2; ++n) {
               const int c = k + 2 * n;
               const float2 x = make_float2(z[c], z[c + 1]);
-              const float2 w = less(S::kKeep ? plus_ev(x) : x, rw[n]), s = less(x, rs[n]);
-              if constexpr (S::kKeep) {
-                kept[c] = w.x;
-                kept[c + 1] = w.y;
-                z[c] = s.x;
-                z[c + 1] = s.y;
-              }
+              const float2 w = less(__fadd2_rn(x, make_float2(ev, ev)), rw[n]), s = less(x, rs[n]);
+              zw[c] = w.x;
+              zw[c + 1] = w.y;
+              z[c] = s.x;
+              z[c + 1] = s.y;
               most_w = max3(most_w, w.x, w.y);
               most_s = max3(most_s, s.x, s.y);
             }
           }
-          return (S::kKeep ? most_w : most_w + ev) > kWeightScale + kHeadroom || most_s > kSumHeadroom;
+          return most_w > kWeightScale + kHeadroom || most_s > kSumHeadroom;
         };
         bool raise = false;
 #pragma unroll
         for (int half = 0; half < S::kHalves; ++half) {
           scores(half, z[half]);
-          raise |= above(z[half]);
+          raise |= against(zw[half], z[half]);
         }
         if (__builtin_expect(!whole && ok && grp == 0, 0)) {
           for (int half = 0; half < S::kHalves; ++half) {
@@ -829,7 +838,8 @@ struct Cta {
           bar_sync(1 + wi, 128);
 #pragma unroll
           for (int c = 0; c < kCols; ++c) l[c] *= ctl->scale_l[stream][own + c];
-          if constexpr (S::kKeep) above(z[0]);
+#pragma unroll
+          for (int half = 0; half < S::kHalves; ++half) against(zw[half], z[half]);
           if (i >= S::kStreams) {
             __syncwarp();
 #pragma unroll 1
@@ -854,24 +864,12 @@ struct Cta {
 #pragma unroll
           for (int k = 0; k < kCols; k += 4) {
             float e[4];
-            float2 rw[2], rs[2];
-            if constexpr (!S::kKeep) {
-              refs(ctl->top_w[stream], k, rw);
-              refs(ctl->top_s[stream], k, rs);
-            }
 #pragma unroll
             for (int n = 0; n < 4; n += 2) {
               const int c = k + n;
-              float2 w, s = make_float2(z[half][c], z[half][c + 1]);
-              if constexpr (S::kKeep) {
-                w = make_float2(kept[c], kept[c + 1]);
-              } else {
-                w = less(plus_ev(s), rw[n / 2]);
-                s = less(s, rs[n / 2]);
-              }
-              e[n] = ex2_approx(w.x);
-              e[n + 1] = ex2_approx(w.y);
-              const float2 sum = __fadd2_rn(make_float2(l[c], l[c + 1]), make_float2(ex2_approx(s.x), ex2_approx(s.y)));
+              e[n] = ex2_approx(zw[half][c]);
+              e[n + 1] = ex2_approx(zw[half][c + 1]);
+              const float2 sum = __fadd2_rn(make_float2(l[c], l[c + 1]), make_float2(ex2_approx(z[half][c]), ex2_approx(z[half][c + 1])));
               l[c] = sum.x;
               l[c + 1] = sum.y;
             }
