@@ -16,6 +16,7 @@ kv_pages_compact_workspace_size, kv_pages_compact, nvfp4mla_status_string.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -488,6 +489,7 @@ def _kv8_dtype(t, name) -> int:
     raise TypeError(f"{name}: expected torch.bfloat16 or torch.float16, got {t.dtype}")
 
 
+@functools.lru_cache(maxsize=None)
 def kv8_page_bytes(kv_heads: int, head_dim: int) -> int:
     """Bytes of one 64-token page of the 8-bit per-head cache (head_dim 64 or 128)."""
     n = load_library().kv8_page_bytes(kv_heads, head_dim)

@@ -31,14 +31,15 @@
 // (m, l, O) in the workspace and count themselves.
 //
 // Measured (device time, inputs beyond L2, 152 SMs): 8 columns and 128 dims run at the memory's pace:
-// 16 requests of 20-90K tokens, 8 key/value heads: 1.38 GB in 210 us, 6.57 TB/s, 97 % of the measured
-// copy bandwidth; one request of 131K tokens: 269 MB in 53 us (74 %: 5 us until the first product, 7
-// from the last to the joined result). With 64 dims a byte brings twice the softmax work: 64 requests
-// of 4-30K tokens: 871 MB in 154 us (83 %). With 16 columns the softmax sets the pace, some 0.9 us a
-// stage at 128 dims and 1.3 at 64 (32 requests of 4-16K, two queries of 8 heads: 595 MB in 115 us, 76 %;
-// four queries, whose two column tiles read the codes twice, 198 us, 44 %). Its instructions are what
-// there is to save: pairs of columns in one instruction took those from 117, 202 and, at 64 dims, 147
-// to 130 us, then keeping fewer values in registers to 121.
+// 16 requests of 20-90K tokens, 8 key/value heads: 1.38 GB in 210 us, 6.6 TB/s, 97 % of the measured copy
+// bandwidth; one request of 131K tokens: 269 MB in 51.5 us (77 %: 5 us until the first product, 5 from the
+// last to the joined result). With 64 dims a byte brings twice the softmax work: 64 requests of 4-30K
+// tokens: 871 MB in 151 us (85 %). With 16 columns the softmax sets the pace, some 0.8 us a stage at 128
+// dims and 1.1 at 64 (32 requests of 4-16K, two queries of 8 heads: 595 MB in 109 us, 81 %; four queries,
+// whose two column tiles read the codes twice, 179 us, 49 %). Its instructions and registers are what
+// there is to save: pairs of columns in one instruction took those from 117 and 202 to 115 and 198 us
+// (and 147 to 130 with 64 dims, four queries of 4 heads), tile loops without spilled registers to 109 and
+// 179 (103).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -158,9 +159,9 @@ struct Ranges {
 };
 
 // What starting and ending a unit costs, in tiles: ranges count a unit of n tiles as kUnitCost + n, so
-// that CTAs with many short units do not finish last. Measured with 0, 4, 8, 12 and 16: 256 requests of
-// 200-1,500 tokens 161, 127, 123, 125 and 126 us; 64 of 4-30K with 64 dims 188, 169, 161, 163 and 169;
-// 16 of 20-90K 211.5, 210, 210.5, 210.5 and 212.
+// that CTAs with many short units do not finish last. Measured with 0, 4, 8 and 12: 256 requests of
+// 200-1,500 tokens 133, 99, 95 and 100 us; 64 of 4-30K with 64 dims 164, 148, 150 and 153; 32 of 900-9,000,
+// four queries in a window, 59, 49, 50 and 52; 16 of 20-90K 208, 206, 206 and 207.
 constexpr int kUnitCost = 8;
 
 // A walk over the segments of this CTA: per unit, the tiles of it that the CTA has. Units go by column
@@ -568,7 +569,7 @@ struct Cta {
     auto chunk = [&](int i) { return reinterpret_cast<uint4*>(row + (((half * kChunks + i) ^ (r & 7)) * 16)); };
     if constexpr (S::kPair) {
       // the loads of a row of 64 dims all in flight: 32 requests' four queries in a window 58 us instead of
-      // 60 (with 128 dims, more code than it saves: 256 short requests 108 instead of 102)
+      // 60 (with 128 dims, more code than it saves: 256 short requests 99 instead of 95)
       uint4 x[kChunks];
       uint32_t nan = 0;
 #pragma unroll
@@ -725,7 +726,7 @@ struct Cta {
         const bool whole = pages == (1u << S::kPages) - 1 && t0 + S::kTile - 1 <= at0 && t0 >= all_lo;
         const bool page_ok = (pages >> h) & 1;
         // exponents (log2 units) of the scores of a half's token; two columns an instruction here and below,
-        // and four columns' parts at a time, as registers are short (eight: 63 us instead of 60, as above)
+        // and four columns' parts at a time, as registers are short (eight: 182 us instead of 179, as below)
         auto scores = [&](int half, float (&z)[kCols]) {
 #pragma unroll
           for (int k = 0; k < kCols; k += 4) {
@@ -759,7 +760,7 @@ struct Cta {
         };
         auto less = [&](float2 z, float2 r) { return __ffma2_rn(r, make_float2(-1.f, -1.f), z); };
         // (z becomes the sum's; taking both from the scores again later, for fewer registers, took 182 us
-        // instead of 178 with 16 columns, four queries of 8 heads)
+        // instead of 179: 32 requests of 4-16K, four queries of 8 heads)
         float z[S::kHalves][kCols], zw[S::kHalves][kCols];
         auto against = [&](float (&zw)[kCols], float (&z)[kCols]) {
           float most_w = neg_inf(), most_s = neg_inf();
@@ -1089,12 +1090,12 @@ __global__ void __launch_bounds__(Shape<D, NC, kHalf ? 3 : 2>::kThreads, 1) kv8_
   const int all = __reduce_add_sync(kFull, of_warp) * p.kv_heads;      // of one column tile
   // no CTA gets less than a tile for each of its streams, and where units have few tiles, no less than
   // an average unit: joining partial results costs some 4 us, a tile 0.6 (one request of 1,000 tokens:
-  // 11.3 us, and 12.8 when its eight units are split)
+  // 10.6 us, and 12.7 when its eight units are split)
   const int units = p.B * p.kv_heads * cts, tiles = all * cts - kUnitCost * units;
   // Where a unit would be cut into very many, a part less saves more of the joining (some 0.1 us each) than
   // it adds to the others' tiles: of t tiles, 2 sqrt(t) parts at most (one request, one key/value head of 8
-  // query heads: 16K tokens 16.5 us instead of 22, 32K 17.3 instead of 31; with sqrt(t) parts 16.0 and 18.5,
-  // but 2K tokens 12.9 instead of 11.9)
+  // query heads: 16K tokens 15 us, 32K 15; with the join as it was then 16.5 and 17.3 instead of 22 and 31;
+  // with sqrt(t) parts 16.0 and 18.5, but 2K tokens 12.9 instead of 11.9)
   const int parts = (int)ceilf(2.f * sqrtf((float)tiles / (float)units)), grid = (int)gridDim.x;
   const int most = tiles <= S::kFewTiles * units ? units
                                                  : min((tiles + S::kMinTiles - 1) / S::kMinTiles, min(units, grid) * min(parts, grid));
@@ -1195,8 +1196,8 @@ cudaError_t launch_columns(const Kv8DecodeParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-// Columns of a tile. 8 where they hold all of a key/value head's: with 16 such steps took 229 us instead
-// of 210 (16 requests of 20-90K tokens, 128 dims) and 295 instead of 169 (64 of 4-30K, 64 dims), as the
+// Columns of a tile. 8 where they hold all of a key/value head's: with 16 such steps took 219 us instead
+// of 210 (16 requests of 20-90K tokens, 128 dims) and 187 instead of 151 (64 of 4-30K, 64 dims), as the
 // softmax's work grows with them. From 9 columns on 16: two tiles of 8 would read every key twice and
 // take as many instructions. (32 columns in one tile spilled registers, and took 82 ns a column and
 // tile where 16 took 62.)
