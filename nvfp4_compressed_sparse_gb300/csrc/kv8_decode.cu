@@ -1005,11 +1005,11 @@ struct Cta {
       }
       // the next segment starts from nothing
       bar_sync(kAllBar, kAll);
-      if (r < kCols) {
-        ctl->top_w[stream][own + r] = ctl->top_s[stream][own + r] = kNone;
-        if (poisoned)
-          for (int k = 0; k < 4; ++k) ctl->poison[stream][own + r][k] = 0;
-      }
+      if (r < kCols) ctl->top_w[stream][own + r] = ctl->top_s[stream][own + r] = kNone;
+      // (a stream's notes of NaN, of all columns, by the warpgroup that makes them: no barrier of both its
+      // warpgroups comes before the next segment's first)
+      if (poisoned && grp == 0 && r < NC)
+        for (int k = 0; k < 4; ++k) ctl->poison[stream][r][k] = 0;
       if (r == 0 && grp == 0) ctl->any_poison[stream] = 0;
       bar_sync(1 + wi, 128);
       if (lane == 0) mbar_arrive(&ctl->q_empty[buf]);

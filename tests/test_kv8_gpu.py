@@ -282,6 +282,25 @@ def test_decode_nan_reaches_only_who_attends_to_it():
         check(*c.run(window), c.reference(window))
 
 
+@pytest.mark.parametrize("D,Hk,G,Q,dtype", [(128, 3, 8, 2, "bf16"), (64, 2, 4, 4, "fp16"), (128, 1, 16, 2, "fp16")])
+@pytest.mark.parametrize("max_ctas", [1, 3])
+def test_decode_nan_of_some_columns_in_one_unit_after_the_other(D, Hk, G, Q, dtype, max_ctas):
+    """More than eight columns (two warpgroups a stream), units of a tile or two, and in every unit a NaN in values
+    that the later queries alone attend to: what one unit notes of it is gone, and only that, when the next begins."""
+    lens = np.random.default_rng(G).integers(Q, 2 * (128 if D == 128 else 256), 150)
+    c = Case(lens, Hk, D, dtype, G=G, Q=Q, seed=G)
+    codes, _ = kv8.parts(c.cache, Hk, D)
+    for b in range(150):
+        t = int(lens[b]) - 1                                # the newest position: the last query's
+        codes[c.table[b, t // 64], 1, :, t % 64, b % D] = 0x7F
+        if b % 3 == 0:
+            codes[c.table[b, (t - 1) // 64], 1, 0, (t - 1) % 64, (b + 17) % D] = 0xFF
+    ref = c.reference()
+    assert np.isnan(ref[0][:, -1]).any() and not np.isnan(ref[0][1::3, 0]).any()
+    for _ in range(5):
+        check(*c.run(max_ctas=max_ctas), ref)
+
+
 def test_decode_non_finite_queries():
     c = Case([200, 64, 0], 1, 64, "fp16", Q=2, G=2, seed=12)
     c.q[0, 0, 0, 3] = float("inf")
