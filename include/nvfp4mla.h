@@ -518,6 +518,14 @@ size_t kv8_decode_workspace_size(int B, int Q, int H, int kv_heads, int head_dim
  * in positions not attended to reaches none. A query row with an infinity or
  * a NaN gives NaN.
  *
+ * Scores, maxima and sums are held in fp32. Two operands are held in fewer bits:
+ *   queries  a bf16 row's elements are exact from 2^-13 of its largest magnitude
+ *            on, and below that off by at most 2^-21 of it (fp16: 2^-14, 2^-25)
+ *   weights  what a value's code is multiplied by, exp(z_t - m) times the block's
+ *            scale, is off by at most 2^-15 of itself, or 2^-40 of the largest
+ *            such product of the head's attended positions if that is more; the
+ *            sum that divides is one of unrounded exponentials
+ *
  *   q                 dtype [B, Q, H, head_dim], 16-byte aligned; element
  *                     strides q_token_stride (of b*Q + j) and q_head_stride,
  *                     multiples of 8

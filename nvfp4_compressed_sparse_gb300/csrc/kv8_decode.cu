@@ -6,17 +6,24 @@
 //   O[d, c] += sum_t V[t, d] w[t, c]   w = 2^(z log2e + ev_t - 127 - M_c)
 // with M_c a running reference, at most 2^4 below the largest exponent so far, and beside it the
 // softmax's own running sum l_c = sum_t 2^(z log2e - m_c). A value's block scale goes into the
-// weight's exponent before the reference is taken, so that blocks with scales far apart lose nothing.
+// weight's exponent before the reference is taken.
 //
 // What bounds it. A token costs 2 D + 0.5 bytes per head and 4 D operations per column: below some
 // 250 operations a byte the step is bound by memory, so the codes have to reach the tensor cores as
-// they lie in the cache, without a conversion in between. E4M3 x E4M3 products do that: K and V
-// are the A operands straight from where TMA put them (K K-major, V M-major), and the 16-bit
-// operands, q and w, are written as sums of E4M3 parts, each a sixteenth of the one before:
-//   x = x_0 + x_1/16 (+ x_2/256 (+ x_3/4096)),   x_i = E4M3(what is left x 16^i)
-// A part takes four bits of the significand, so two hold a bf16 exactly, three an fp16, and four hold
-// a weight to 16 bits. The parts are further columns of the B operand (their products land in columns of
-// their own and are added in fp32 afterwards), so that A is read from shared memory once.
+// they lie in the cache, without a conversion in between. 8-bit products do that: K and V are the A
+// operands straight from where TMA put them (K K-major, V M-major), and the other operands, q and w,
+// are written as sums of 8-bit parts, each a sixteenth of the one before:
+//   x = x_0 + x_1/16 (+ x_2/256 (+ x_3/4096)),   x_i = 8 bits of (what is left x 16^i)
+// The parts are further columns of the B operand (their products land in columns of their own and are
+// added in fp32 afterwards), so that A is read from shared memory once.
+//   q: E4M3. Two parts hold a bf16, three an fp16, with its row's largest element at 2^7 to 2^8, down to
+//     the last part's half step: 2^-14 for two, 2^-18 for three. So an element is off by at most 2^-21
+//     (2^-25) of its row's largest, and exact from 2^-13 of that on for bf16, 2^-14 for fp16.
+//   w: E5M2, four parts: 2^-15 of the weight, whose largest is 2^11 to 2^15; the last part's half step is
+//     2^-17/4096, 2^-40 of the largest. E4M3 parts hold one bit more of a weight near the largest, but
+//     have 2^-26 in the place of that 2^-40, and what is below adds to l and not to O: one key as heavy
+//     as 100,000 others together, whose value block had a scale 2^10 times theirs, took all of the
+//     others' share.
 //
 // One CTA per SM, persistent. The tiles of all (request, key/value head, column tile) units form
 // one sequence, found by every CTA from the lengths, and each CTA takes one contiguous range of it.
@@ -58,7 +65,7 @@ using namespace ptx;
 constexpr int kRows = 128;             // 128-byte rows of K or V in a stage: a token each, or two of 64 dims
 constexpr int kWParts = 4;
 constexpr float kHeadroom = 4.f;       // log2: how far above the reference a weight's exponent may come
-constexpr float kWeightScale = 4.f;    // log2: weights are held times 16, so that 2^4 above it is 256 <= 448
+constexpr float kWeightScale = 11.f;   // log2: weights are held times 2^11: 2^4 above it, a part is at most 2^15 (E5M2: 57,344)
 constexpr float kSumHeadroom = 60.f;   // log2: the same for the sum, which fp32 holds
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
@@ -241,6 +248,26 @@ __device__ __forceinline__ void split_parts(float a, float b, uint32_t (&part)[k
       r = __hsub2(r, *reinterpret_cast<const __half2*>(&h));
     }
   }
+}
+
+// (a, b) as four pairs of E5M2 parts, 0 <= a, b <= 2^15. A part leaves at most 2^-3 of the power of two below
+// its value, the next ones 2^-4 each: 2^-15 after four. The first two are taken off in fp32 (exactly); of what they
+// leave the fp16 keeps 11 bits, more than the others hold.
+__device__ __forceinline__ void split_weight(float a, float b, uint32_t (&part)[kWParts]) {
+  auto wide = [](uint32_t two) {
+    const uint32_t h = e5m2x2_to_f16x2(two);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+  };
+  const float2 minus = make_float2(-1.f, -1.f), sixteen = make_float2(16.f, 16.f);
+  part[0] = f32x2_to_e5m2x2(a, b);
+  float2 left = __fmul2_rn(__ffma2_rn(wide(part[0]), minus, make_float2(a, b)), sixteen);
+  part[1] = f32x2_to_e5m2x2(left.x, left.y);
+  left = __fmul2_rn(__ffma2_rn(wide(part[1]), minus, left), sixteen);
+  const __half2 r = __floats2half2_rn(left.x, left.y);
+  part[2] = f16x2_to_e5m2x2(*reinterpret_cast<const uint32_t*>(&r));
+  const uint32_t h = e5m2x2_to_f16x2(part[2]);
+  const __half2 last = __hmul2(__hsub2(r, *reinterpret_cast<const __half2*>(&h)), __floats2half2_rn(16.f, 16.f));
+  part[3] = f16x2_to_e5m2x2(*reinterpret_cast<const uint32_t*>(&last));
 }
 
 // The largest of three; a NaN counts as none.
@@ -443,7 +470,7 @@ struct Cta {
   // are wanted, and the odd one's with the odd one's; the other half of the work costs less than twice
   // as many instructions of this thread would.
   __device__ void issue_o(Walk w, uint32_t tmem) {
-    constexpr uint32_t kId = idesc_e4m3(128, S::kWRow, true, true);
+    constexpr uint32_t kId = idesc_e4m3(128, S::kWRow, true, true, true);
     const uint64_t vd = sdesc(smem_u32(stages + 1024), 16, 2048, SW_128B), wd = sdesc(smem_u32(wbuf), 16, 8 * S::kWRow, S::kSwW);
     Ring ring;
     uint32_t uses[2] = {0, 0};             // tiles that the streams have had
@@ -875,8 +902,8 @@ struct Cta {
               l[c + 1] = sum.y;
             }
             uint32_t p01[kWParts], p23[kWParts];
-            split_parts(e[0], e[1], p01);
-            split_parts(e[2], e[3], p23);
+            split_weight(e[0], e[1], p01);
+            split_weight(e[2], e[3], p23);
 #pragma unroll
             for (int n = 0; n < kWParts; ++n) out[n][k / 4] = p01[n] | (p23[n] << 16);
           }

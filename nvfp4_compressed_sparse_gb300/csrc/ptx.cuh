@@ -314,10 +314,10 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, 
          ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Instruction descriptor, kind::f8f6f4, E4M3 x E4M3 with fp32 accumulate (both type fields 0).
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major, bool b_mn_major) {
-  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor, kind::f8f6f4, A E4M3 (type 0) and B E4M3 or E5M2 (type 1), fp32 accumulate.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major, bool b_mn_major, bool b_e5m2 = false) {
+  return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // TMEM loads/stores, 32 lanes x 32 bits, 32 consecutive columns per thread.
@@ -423,6 +423,19 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float a, float b) {
 __device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h2) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+  return r;
+}
+// Two E5M2 bytes (low byte = first) -> f16x2, exact: an E5M2 number is an fp16's upper byte.
+__device__ __forceinline__ uint32_t e5m2x2_to_f16x2(uint32_t two_bytes) { return __byte_perm(two_bytes, 0u, 0x1404); }
+// (a, b) fp32, and f16x2 -> E5M2 pair, as the E4M3 conversions above (saturating to +-57344).
+__device__ __forceinline__ uint32_t f32x2_to_e5m2x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_to_e5m2x2(uint32_t h2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
   return r;
 }
 // Two bf16 values (low half first) -> E4M3 pair: nearest even, saturating to +-448, and a NaN

@@ -86,3 +86,22 @@ def check(out, lse, ref, what=""):
     fine = ~empty & ~np.isnan(r_lse)
     tol = (dw + 2.0 ** -22 * np.maximum(1, np.abs(np.where(fine, r_lse, 0))))[fine]
     assert np.all(np.abs(got_lse[fine] - r_lse[fine]) <= tol), f"{what}: lse"
+
+
+def check_small_weights(out, ref, adds, what=""):
+    """Outputs against the oracle's, with what weights far below the largest one may lose.
+
+    A weight is held as four E5M2 parts, each a sixteenth of the one before, with the largest at 2^11 to 2^15. A part
+    has three bits: it leaves at most 2^-3 of the power of two below its value, which is itself at least the power of
+    two above what is left, so that the next ones leave 2^-4 each: 2^-3-4-4-4 = 2^-15. Below 2^-14 a part has steps of
+    2^-16, so the last one leaves 2^-17 / 16^3 = 2^-29, 2^-40 of the largest weight times its value's scale. The sum
+    is made of `adds` additions in 32 bits, each off by at most a step (2^-23) of what it has reached. Scores and
+    exponentials as in check(); the sum that divides is of unrounded weights."""
+    r_out, _, mass, reach, spread = ref
+    dz = (r_out.shape[-1] + 8) * 2.0 ** -24 * reach
+    dw = 2 * (dz + 2.0 ** -21) + 2.0 ** -15 + adds * 2.0 ** -23
+    half = torch.finfo(out.dtype).eps / 2
+    tiny = torch.finfo(out.dtype).smallest_normal * half
+    tol = half * np.abs(r_out) + (1 + half) * (dw[..., None] * mass + 2.0 ** -40 * spread) + tiny
+    worst = np.max(np.abs(f64(out) - r_out) / tol)
+    assert worst <= 1, f"{what}: out off by {worst:.2f} of the bound"

@@ -5,7 +5,7 @@ import torch
 
 import nvfp4_compressed_sparse_gb300 as m
 from oracle import kv8
-from tests.kv8_util import DTYPES, Case, check, dev, f64
+from tests.kv8_util import DTYPES, Case, check, check_small_weights, dev, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -270,6 +270,52 @@ def test_decode_one_weight_over_many_small_ones(dtype):
         codes[page[at], 0, 0, row[at], 0] = 0x38                              # the one key: 1
         codes[page[at], 1, 0, row[at]] = 0xB8                                 # its value: -1
         check(*c.run(), c.reference())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,log2_scale,at", [(10007, 10, 0), (100003, 10, 50000), (100003, 0, 77), (131000, 0, 130999), (131000, 6, 9)])
+def test_decode_one_key_as_heavy_as_all_others_together(n, log2_scale, at, D, dtype):
+    """One weight that equals the sum of n - 1 equal others, whose value has a block scale 2^log2_scale times theirs and
+    is 0 in all dims but one: in those the result is the others' share alone. On one CTA, so that nothing is split."""
+    c = Case([n], 1, D, dtype, G=2, seed=n)
+    codes, scales = kv8.parts(c.cache, 1, D)
+    c.q = torch.zeros((1, 1, 2, D), dtype=DTYPES[dtype], device="cuda")
+    c.q[..., 0] = 1.0
+    c.scale = float(np.log(n - 1))
+    t = np.arange(n)
+    page, row = c.table[0][t // 64], t % 64
+    codes[page, 0, 0, row] = 0
+    codes[page, 1, 0, row] = 0x38 + c.rng.integers(0, 8, (n, D))              # 1 .. 1.875
+    scales[page, 0, :, row // 16] = 127
+    block = at // 16 * 16 + np.arange(16)
+    block = block[block < n]
+    codes[page[block], 1, 0, row[block]] = 0                                  # (the scale is its whole block's)
+    scales[page[at], 0, 1, row[at] // 16] = 127 + log2_scale
+    codes[page[at], 0, 0, row[at], 0] = 0x38
+    codes[page[at], 1, 0, row[at], D - 1] = 0xB8                              # -1
+    out, lse = c.run(max_ctas=1)
+    ref = c.reference()
+    check_small_weights(out, ref, n / 64)                                     # two streams, 32 tokens an addition
+    check(out, lse, ref)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_decode_a_key_far_above_a_million_others(dtype):
+    """The others' weights are e^-15.9 of the one key's, and all their sum is an eighth of it."""
+    n = 1 << 20
+    c = Case([n], 1, 64, dtype, G=1, seed=3)
+    codes, scales = kv8.parts(c.cache, 1, 64)
+    c.q = torch.zeros((1, 1, 1, 64), dtype=DTYPES[dtype], device="cuda")
+    c.q[..., 0] = 1.0
+    c.scale = 15.9
+    codes[:] = 0
+    scales[:] = 127
+    codes[:, 1] = 0x38 + c.rng.integers(0, 8, codes[:, 1].shape)
+    codes[c.table[0, 700], 0, 0, 5, 0] = 0x38
+    codes[c.table[0, 700], 1, 0, 5] = 0
+    out, _ = c.run(max_ctas=1)
+    check_small_weights(out, c.reference(), n / 64)
 
 
 def test_decode_nan_reaches_only_who_attends_to_it():
