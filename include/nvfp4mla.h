@@ -518,7 +518,8 @@ size_t kv8_decode_workspace_size(int B, int Q, int H, int kv_heads, int head_dim
  * in positions not attended to reaches none. A query row with an infinity or
  * a NaN gives NaN.
  *
- * Scores, maxima and sums are held in fp32. Two operands are held in fewer bits:
+ * Scores, maxima and sums are held in fp32; a row's largest |q| x softmax_scale x
+ * a key block's scale has to be below 2^120. Two operands are held in fewer bits:
  *   queries  a bf16 row's elements are exact from 2^-13 of its largest magnitude
  *            on, and below that off by at most 2^-21 of it (fp16: 2^-14, 2^-25)
  *   weights  what a value's code is multiplied by, exp(z_t - m) times the block's

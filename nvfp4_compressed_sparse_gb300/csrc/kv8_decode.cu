@@ -119,15 +119,16 @@ struct Control {
   int hi[2][NC], lo[2][NC];            // positions that a column attends to
   int row[2][NC];                      // of out and lse, -1: no column
   int at0[2], at1[2], cols[2];         // positions of the tile's first and last column; its columns
-  alignas(16) float top_w[kStreams][NC];   // the weights' reference: M less kWeightScale (these four are
-                                           // read four at a time)
+  alignas(16) float top_w[kStreams][NC];   // the weights' reference: M less kWeightScale, less m (these four
+                                           // are read four at a time)
   alignas(16) float top_s[kStreams][NC];   // m
   alignas(16) float scale_o[kStreams][NC];
   alignas(16) float scale_l[kStreams][NC];
-  float part_max[kStreams][4][NC][2];
+  float part_max[kStreams][4][NC][2];  // of a warp: the largest score, and weight against that
   float part_l[kStreams][4][NC];
   uint32_t poison[kStreams][NC][4];    // dims that a NaN value reaches
-  float join_m[NC], join_l[NC], join_inv[NC], join_w[kStreams][NC];
+  float join_m[NC], join_l[NC];
+  alignas(8) float join_w[kStreams][NC][2];       // O's factor, in two
   int any_poison[kStreams];
   int scan_sum[kWarps];
   int start_before;                    // tiles before request start_b
@@ -287,9 +288,9 @@ __device__ __forceinline__ float2 pair_of(const uint32_t (&v)[N], int i) {
   return make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
 }
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
-// A reference before any position: far below every exponent, and finite, so that what is left out (an
-// exponent of -inf) stays 0 against it.
-constexpr float kNone = -1e30f;
+// A reference before any position: below every exponent that fp32 holds but the last few, and finite, so that
+// what is left out (an exponent of -inf) stays 0 against it.
+constexpr float kNone = -3e38f;
 // 2^(a - b), 1 where the two are equal.
 __device__ __forceinline__ float ratio(float a, float b) { return a == b ? 1.f : ex2_approx(a - b); }
 
@@ -650,10 +651,10 @@ struct Cta {
   __device__ __forceinline__ void put_lse(int row, float m, float sum) {
     if (row >= 0) p.lse[row] = sum == 0.f ? neg_inf() : (m + log2f(sum)) * 0.69314718055994530942f;
   }
-  // What a weighted sum is multiplied by: 0 where there was no position.
-  static __device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+  // 1 / sum (to 2^-23), 0 where there was no position. A sum is 0, or at least 1 and far from fp32's end.
+  static __device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : rcp_approx(sum); }
 
-  // Joins the partial results that CTAs c_lo .. c_hi left of a unit, for dim d of this warpgroup's
+  // Joins the partial means that CTAs c_lo .. c_hi left of a unit, for dim d of this warpgroup's
   // columns, 32 at a time: a lane has the maxima and sums of one, and the outputs of kSlots are in flight
   // together, the first of them beside the maxima. (It has few registers on purpose: with every part's
   // maxima and sums in each thread, the tile loop's values were spilled: with 16 columns 197 us instead of
@@ -689,12 +690,15 @@ struct Cta {
 #pragma unroll
       for (int k = 0; k < kN; ++k) {
         const float m_new = fmaxf(m[k], redux_max(w[k])), keep = ratio(m[k], m_new);
-        w[k] = ratio(w[k], m_new);
-        l[k] *= w[k];
+        w[k] = l[k] * ratio(w[k], m_new);
+        float all = w[k];
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) l[k] += __shfl_xor_sync(kFull, l[k], x);
-        sum[k] = sum[k] * keep + l[k];
-        acc[k] *= keep;
+        for (int x = 16; x > 0; x >>= 1) all += __shfl_xor_sync(kFull, all, x);
+        all += sum[k] * keep;
+        const float inv = inverse(all);      // acc, too, is a mean all the way
+        acc[k] *= sum[k] * keep * inv;
+        w[k] *= inv;
+        sum[k] = all;
         m[k] = m_new;
       }
 #pragma unroll 1
@@ -709,7 +713,7 @@ struct Cta {
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
       if (row[c + k] < 0) break;
-      put<kHalf>((int64_t)row[c + k] * D + d, acc[k] * inverse(sum[k]));
+      put<kHalf>((int64_t)row[c + k] * D + d, acc[k]);
       if (d == 0) put_lse(row[c + k], m[k], sum[k]);
     }
   }
@@ -779,7 +783,8 @@ struct Cta {
               if (!page_ok || t + half > ctl->hi[buf][own + c] || t + half < ctl->lo[buf][own + c]) z[c] = neg_inf();
           }
         };
-        // and against the references: of the weights, and of the sum
+        // and against the references: of the sum, and from there of the weights (scores may be so large that a
+        // block's scale added to one would be rounded away)
         auto refs = [&](const float* top, int k, float2 (&r)[2]) {
           const float4 t = *reinterpret_cast<const float4*>(top + own + k);
           r[0] = make_float2(t.x, t.y);
@@ -800,7 +805,7 @@ struct Cta {
             for (int n = 0; n < 2; ++n) {
               const int c = k + 2 * n;
               const float2 x = make_float2(z[c], z[c + 1]);
-              const float2 w = less(__fadd2_rn(x, make_float2(ev, ev)), rw[n]), s = less(x, rs[n]);
+              const float2 s = less(x, rs[n]), w = __fadd2_rn(s, less(make_float2(ev, ev), rw[n]));
               zw[c] = w.x;
               zw[c + 1] = w.y;
               z[c] = s.x;
@@ -841,8 +846,8 @@ struct Cta {
           }
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
-            const float ms = redux_max(top[c]), mw = redux_max(top[c] + ev);
-            if (lane == 0) *reinterpret_cast<float2*>(ctl->part_max[stream][warp][own + c]) = make_float2(mw, ms);
+            const float ms = fmaxf(redux_max(top[c]), kNone), mw = redux_max(top[c] - ms + ev);
+            if (lane == 0) *reinterpret_cast<float2*>(ctl->part_max[stream][warp][own + c]) = make_float2(ms, mw);
           }
           if (bar_any(1 + wi, 128, !ok)) {
             stop = true;
@@ -851,16 +856,16 @@ struct Cta {
           if (r < kCols) {
             const int c = own + r;
             const float w0 = ctl->top_w[stream][c], s0 = ctl->top_s[stream][c];
-            float w1 = w0 + kWeightScale, s1 = s0;
+            float s1 = s0;
+            for (int k = 0; k < 4; ++k) s1 = fmaxf(s1, ctl->part_max[stream][k][c][0]);
+            float w1 = s0 - s1 + w0;
             for (int k = 0; k < 4; ++k) {
               const float2 most = *reinterpret_cast<const float2*>(ctl->part_max[stream][k][c]);
-              w1 = fmaxf(w1, most.x);
-              s1 = fmaxf(s1, most.y);
+              w1 = fmaxf(w1, most.x - s1 + most.y - kWeightScale);
             }
-            w1 = w1 > kNone / 2 ? w1 - kWeightScale : w0;
             ctl->top_w[stream][c] = w1;
             ctl->top_s[stream][c] = s1;
-            ctl->scale_o[stream][c] = ratio(w0, w1);
+            ctl->scale_o[stream][c] = ex2_approx(s0 - s1 + w0 - w1);
             ctl->scale_l[stream][c] = ratio(s0, s1);
           }
           bar_sync(1 + wi, 128);
@@ -965,11 +970,19 @@ struct Cta {
           float part = 0.f;
           for (int q = 0; q < 4; ++q) part += ctl->part_l[k][q][c];
           sum += part * ratio(ctl->top_s[k][c], m);
-          ctl->join_w[k][c] = ex2_approx(ctl->top_w[k][c] - m);
+        }
+        // What O is multiplied by makes it the weighted mean at once, which fp32 holds wherever it holds the
+        // values (m may lie 2^60 below the largest weight, so that the weighted sum need not fit). It is
+        // taken in two factors beside 1 / (the sum's 1 to 2), which stay far from fp32's ends.
+        const int up = max(0, min(126, (int)((__float_as_uint(sum) >> 23) & 0xFFu) - 127));
+        const float inv = inverse(sum * __uint_as_float((uint32_t)(127 - up) << 23));
+#pragma unroll
+        for (int k = 0; k < kStreams; ++k) {
+          const float half = ex2_approx(0.5f * (ctl->top_s[k][c] - m + ctl->top_w[k][c] - (float)up));
+          *reinterpret_cast<float2*>(ctl->join_w[k][c]) = make_float2(half * inv, half);
         }
         ctl->join_m[c] = m;
         ctl->join_l[c] = sum;
-        ctl->join_inv[c] = inverse(sum);
         if (w.whole()) put_lse(ctl->row[buf][c], m, sum);
       }
       bar_sync(1 + wi, 128);
@@ -997,7 +1010,8 @@ struct Cta {
           x = fmaf(x, 1.f / 16.f, __uint_as_float(o[1][c]));
           x = fmaf(x, 1.f / 16.f, __uint_as_float(o[0][c]));
           if (poisoned && ((ctl->poison[k][c0 + c][d >> 5] >> (d & 31)) & 1)) x = __int_as_float(0x7fc00000);
-          acc[c] = fmaf(x, ctl->join_w[k][c0 + c], acc[c]);
+          const float2 f = *reinterpret_cast<const float2*>(ctl->join_w[k][c0 + c]);
+          acc[c] = fmaf(x * f.x, f.y, acc[c]);
         }
       }
       if constexpr (S::kPair) {
@@ -1018,7 +1032,7 @@ struct Cta {
       if (full_unit) {
 #pragma unroll
         for (int c = 0; c < kN; ++c)
-          if (d >= 0 && ctl->row[buf][c0 + c] >= 0) put<kHalf>((int64_t)ctl->row[buf][c0 + c] * D + d, acc[c] * ctl->join_inv[c0 + c]);
+          if (d >= 0 && ctl->row[buf][c0 + c] >= 0) put<kHalf>((int64_t)ctl->row[buf][c0 + c] * D + d, acc[c]);
       } else {
 #pragma unroll
         for (int c = 0; c < kN; ++c)
@@ -1032,7 +1046,10 @@ struct Cta {
       }
       // the next segment starts from nothing
       bar_sync(kAllBar, kAll);
-      if (r < kCols) ctl->top_w[stream][own + r] = ctl->top_s[stream][own + r] = kNone;
+      if (r < kCols) {
+        ctl->top_w[stream][own + r] = 0.f;
+        ctl->top_s[stream][own + r] = kNone;
+      }
       // (a stream's notes of NaN, of all columns, by the warpgroup that makes them: no barrier of both its
       // warpgroups comes before the next segment's first)
       if (poisoned && grp == 0 && r < NC)
@@ -1049,7 +1066,7 @@ __global__ void __launch_bounds__(Shape<D, NC, kHalf ? 3 : 2>::kThreads, 1) kv8_
   using S = Shape<D, NC, kHalf ? 3 : 2>;
   using Ctl = Control<NC, S::kStages, S::kPages, S::kStreams, S::kThreads / 32>;
   static_assert(offsetof(Ctl, scales) % 16 == 0 && offsetof(Ctl, f) % 16 == 0 && offsetof(Ctl, top_w) % 16 == 0 &&
-                offsetof(Ctl, top_s) % 16 == 0 && offsetof(Ctl, part_max) % 8 == 0 && NC % 8 == 0, "vector accesses are aligned");
+                offsetof(Ctl, top_s) % 16 == 0 && offsetof(Ctl, part_max) % 8 == 0 && offsetof(Ctl, join_w) % 8 == 0 && NC % 8 == 0, "vector accesses are aligned");
   static_assert(sizeof(Ctl) <= 6144, "the control block fits its share");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1082,7 +1099,8 @@ __global__ void __launch_bounds__(Shape<D, NC, kHalf ? 3 : 2>::kThreads, 1) kv8_
     fence_barrier_init();
   }
   for (int i = tid; i < S::kStreams * NC; i += kThreads) {
-    ctl->top_w[i / NC][i % NC] = ctl->top_s[i / NC][i % NC] = kNone;
+    ctl->top_w[i / NC][i % NC] = 0.f;
+    ctl->top_s[i / NC][i % NC] = kNone;
     for (int k = 0; k < 4; ++k) ctl->poison[i / NC][i % NC][k] = 0;
   }
   if (warp == 1) {

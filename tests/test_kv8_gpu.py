@@ -272,6 +272,64 @@ def test_decode_one_weight_over_many_small_ones(dtype):
         check(*c.run(), c.reference())
 
 
+@pytest.mark.parametrize("low,high", [(252, 253), (1, 2), (1, 253), (190, 253)])
+@pytest.mark.parametrize("D,G,Q", [(128, 4, 1), (64, 3, 1), (128, 4, 4), (64, 8, 2)])
+@pytest.mark.parametrize("max_ctas", [0, 1, 5])
+def test_decode_values_at_the_ends_of_the_range(low, high, D, G, Q, max_ctas):
+    """Block scales of values from 2^-126 to 2^126, with scores that rise by 2^-50 to 2^50 from block to block."""
+    c = Case([1000, 130, 40, 5], 2, D, "bf16", Q=Q, G=G, seed=low + G)
+    codes, scales = kv8.parts(c.cache, 2, D)
+    used = scales[:, :, 1] != 0xFF
+    scales[:, :, 1][used] = c.rng.integers(low, high + 1, used.sum())
+    codes[:, 1] = np.where(codes[:, 1] == 0xFF, 0xFF, codes[:, 1] & 0xBF)     # values below 2
+    c.scale *= 4
+    check(*c.run(max_ctas=max_ctas), c.reference())
+
+
+@pytest.mark.parametrize("log2_step", [13, 25, 29])
+@pytest.mark.parametrize("D,Q", [(128, 1), (64, 4)])
+def test_decode_of_scores_that_rise_slowly(D, Q, log2_step):
+    """Every 128 tokens the weights are 2^log2_step times those before: the sum's reference, which is raised by factors
+    of more than 2^60, lies far below the largest, and the values are near fp32's end."""
+    c = Case([1500, 257], 1, D, "bf16", Q=Q, G=4, seed=2)
+    codes, scales = kv8.parts(c.cache, 1, D)
+    c.q = torch.zeros((2, Q, 4, D), dtype=torch.bfloat16, device="cuda")
+    c.q[..., 0] = 1.0
+    c.scale = log2_step * float(np.log(2))
+    for b, n in enumerate(c.lens):
+        t = np.arange(n)
+        page, row = c.table[b, t // 64], t % 64
+        codes[page, 0, 0, row] = 0
+        codes[page, 0, 0, row, 0] = kv8.e4m3_encode(t // 128.0)
+        scales[page, 0, 0, row // 16] = 127
+        codes[page, 1, 0, row] = 0x38 + c.rng.integers(0, 8, (n, D))
+        scales[page, 0, 1, row // 16] = 253
+    for ctas in (0, 1, 3):
+        check(*c.run(max_ctas=ctas), c.reference())
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("D,Q,G", [(64, 1, 2), (128, 2, 8)])
+def test_decode_of_large_scores_that_are_all_equal(sign, D, Q, G):
+    """Scores of +-2^106: the result is the mean of the values, and lse the score."""
+    c = Case([700, 3], 1, D, "bf16", Q=Q, G=G, seed=7)
+    codes, scales = kv8.parts(c.cache, 1, D)
+    codes[:, 0] = 0
+    codes[:, 0, :, :, 5] = 0x38
+    scales[:, :, 0] = 127 + 50
+    c.q = torch.zeros(c.q.shape, dtype=torch.bfloat16, device="cuda")
+    c.q[..., 5] = sign * 2.0 ** 56
+    c.scale = 1.0
+    out, lse = c.run()
+    v = kv8.rows(c.cache, c.table[0], 700, 1, D)[1][0]
+    half, steps = 2.0 ** -8, 2.0 ** -14
+    for j in range(Q):
+        seen = v[:700 - Q + 1 + j]
+        want, mass = seen.mean(0), np.abs(seen).mean(0)
+        assert np.all(np.abs(f64(out[0, j]) - want) <= half * np.abs(want) + (1 + half) * steps * mass)
+    assert np.all(np.abs(f64(lse) - sign * 2.0 ** 106) <= 2.0 ** (106 - 21))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("n,log2_scale,at", [(10007, 10, 0), (100003, 10, 50000), (100003, 0, 77), (131000, 0, 130999), (131000, 6, 9)])
