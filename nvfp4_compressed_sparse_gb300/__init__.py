@@ -16,6 +16,7 @@ kv_pages_compact_workspace_size, kv_pages_compact, nvfp4mla_status_string.
 from __future__ import annotations
 
 import ctypes
+import contextlib
 import functools
 import os
 import threading
@@ -472,12 +473,23 @@ def _raw_stream(stream, index):
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
+_AS_IT_IS = contextlib.nullcontext()
+
+
+def _taken_on(stream):
+    """Where a call takes memory of its own: on the stream that it runs on. A block that the allocator has back from the
+    current stream may still be in use there, by work that `stream` does not wait for."""
+    import torch
+    return _AS_IT_IS if stream is None else torch.cuda.stream(stream)
+
+
 def _keep(stream, *tensors):
-    """Memory taken here, on the current stream, and used on `stream`: not to be reused before that is done."""
+    """Results that were taken on `stream`, and that the caller uses on its current one: not to be reused before that is done."""
+    import torch
     if stream is not None:
         for t in tensors:
             if t is not None:
-                t.record_stream(stream)
+                t.record_stream(torch.cuda.current_stream(t.device))
 
 
 def _kv8_dtype(t, name) -> int:
@@ -560,19 +572,19 @@ def kv8_decode(q, cache, page_table, seq_lens, kv_heads: int, softmax_scale, win
     rows, max_pages = page_table.shape
     if seq_lens.shape[0] != B or rows != B:
         raise ValueError("shape mismatch")
-    fresh = [None] * 3
-    if out is None:
-        out = fresh[0] = torch.empty(shape, dtype=q.dtype, device=q.device)
-    if lse is None:
-        lse = fresh[1] = torch.empty((B, Q, H), dtype=torch.float32, device=q.device)
+    fresh = [None] * 2
+    with _taken_on(stream):
+        if out is None:
+            out = fresh[0] = torch.empty(shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = fresh[1] = torch.empty((B, Q, H), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(max(kv8_decode_workspace_size(B, Q, H, kv_heads, d), 1), dtype=torch.uint8, device=q.device)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace: must be contiguous")
     op, lp = _ptr_of(out, "out", q.dtype, index, 4), _ptr_of(lse, "lse", torch.float32, index, 3)
     if out.shape != shape or lse.shape != shape[:3]:
         raise ValueError("out must be [B, Q, H, head_dim] and lse [B, Q, H]")
-    if workspace is None:
-        workspace = fresh[2] = torch.empty(max(kv8_decode_workspace_size(B, Q, H, kv_heads, d), 1), dtype=torch.uint8,
-                                           device=q.device)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace: must be contiguous")
     if not 0 <= window < 1 << 31:
         raise ValueError("window must be 0 (none) or a number of positions below 2^31")
     rc = lib.kv8_decode(qp, s1 if Q > 1 else s0 if B > 1 else 0, s2 if H > 1 else 0, dt, cp, pages, pp, max_pages, sp,
@@ -657,7 +669,8 @@ def kv_pages_fork(cache, page_table, seq_lens, refcounts, src, dst, new_pages=No
     sp, dp = _ptr_of(src, "src", i32, index, 1), _ptr_of(dst, "dst", i32, index, 1)
     fresh = None
     if new_pages is None:
-        new_pages = fresh = torch.empty_like(src)
+        with _taken_on(stream):
+            new_pages = fresh = torch.empty_like(src)
     np_, n = _ptr_of(new_pages, "new_pages", i32, index, 1), src.shape[0]
     if dst.shape[0] != n or new_pages.shape[0] != n:
         raise ValueError("src, dst and new_pages must have the same length")
@@ -699,18 +712,19 @@ def kv_pages_compact(cache, page_table, refcounts, remap=None, num_live=None, wo
     pp, width, _, seqs, rp, counts = _page_state(page_table, None, refcounts, index)
     if counts != pages:
         raise ValueError("refcounts must have one entry per page of the cache")
-    fresh = [None] * 3
-    if remap is None:
-        remap = fresh[0] = torch.empty_like(refcounts)
-    if num_live is None:
-        num_live = fresh[1] = torch.empty(1, dtype=i32, device=cache.device)
+    fresh = [None] * 2
+    with _taken_on(stream):
+        if remap is None:
+            remap = fresh[0] = torch.empty_like(refcounts)
+        if num_live is None:
+            num_live = fresh[1] = torch.empty(1, dtype=i32, device=cache.device)
+        if workspace is None:
+            workspace = torch.empty(kv_pages_compact_workspace_size(pages), dtype=torch.uint8, device=cache.device)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace: must be contiguous")
     mp, lp = _ptr_of(remap, "remap", i32, index, 1), _ptr_of(num_live, "num_live", i32, index, 1)
     if remap.shape[0] != pages or num_live.shape[0] < 1:
         raise ValueError("remap must have one entry per page, num_live one")
-    if workspace is None:
-        workspace = fresh[2] = torch.empty(kv_pages_compact_workspace_size(pages), dtype=torch.uint8, device=cache.device)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace: must be contiguous")
     rc = load_library().kv_pages_compact(cp, layers, stride, pages, each, pp, width, seqs, rp, mp, lp,
                                          workspace.data_ptr(), workspace.nbytes,
                                          _status_ptr(dev_status, index), _raw_stream(stream, index))

@@ -5,7 +5,7 @@ import torch
 
 import nvfp4_compressed_sparse_gb300 as m
 from oracle import kv8
-from tests.kv8_util import check, dev, f64
+from tests.kv8_util import Case, check, dev, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -246,6 +246,45 @@ def test_a_captured_step_replays_on_the_state_it_finds():
         g.replay()
         oracle(e, a, b)
         s.same()
+
+
+@pytest.mark.parametrize("call", ["decode", "fork", "compact"])
+def test_what_a_call_takes_on_another_stream_is_free_there(call):
+    """A call on an idle stream, while the current one still has to write memory that it gave back before: neither
+    results nor workspace of the call are that memory. Everything that the call could take is given back beforehand."""
+    c = Case([2000, 900], 2, 128, Q=1, G=4, seed=31)
+    args = (c.q, dev(c.cache, torch.uint8), dev(c.table), dev(c.lens), 2, c.scale)
+    size = m.kv8_decode_workspace_size(2, 1, 8, 2, 128)
+    want = m.kv8_decode(*args)
+    x = torch.randn((4096, 4096), device="cuda")
+    s = torch.cuda.Stream()
+    src, dst = dev([0, 1]), dev([3, 4])
+    for turn in range(3):
+        p = State([100, 64, 1, 0, 0], 300, 4096, 2, seed=turn)
+        torch.cuda.synchronize()
+        blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in (c.q.numel() * 2, c.q.numel(), size, 8, 1200, 4, 512, 2048) for _ in range(4)]
+        for _ in range(20):
+            x = x @ x * 1e-3                # some milliseconds before the blocks are written
+        for block in blocks:
+            block.fill_(255)
+        del blocks, block
+        if call == "decode":
+            got = m.kv8_decode(*args, stream=s)
+        elif call == "fork":
+            got = m.kv_pages_fork(p.d_cache, p.d_table, p.d_lens, p.d_refs, src, dst, layered=True, stream=s)
+        else:
+            got = m.kv_pages_compact(p.d_cache, p.d_table, p.d_refs, layered=True, stream=s)
+        s.synchronize()
+        torch.cuda.synchronize()
+        if call == "decode":
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            continue
+        if call == "fork":
+            assert got.tolist() == kv8.fork(p.cache, p.table, p.lens, p.refs, [0, 1], [3, 4])
+        else:
+            remap, n = kv8.compact(p.cache, p.table, p.refs)
+            assert np.array_equal(got[0].cpu().numpy(), remap) and got[1].item() == n
+        p.same()
 
 
 def test_refusals_leave_everything_as_it_was():
