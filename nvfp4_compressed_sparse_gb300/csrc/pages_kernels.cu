@@ -103,13 +103,13 @@ struct PlanShared {
   int64_t running;
 };
 
-// Exclusive prefix over the block's warps of a per-warp value.
-__device__ int warp_prefix(PlanShared* sh, int v) {
+// Exclusive prefix over the block's warps of a per-warp value, which is not negative (32 of which may leave 32 bits).
+__device__ int64_t warp_prefix(PlanShared* sh, int v) {
   __syncthreads();
   if ((threadIdx.x & 31) == 0) sh->warp[threadIdx.x >> 5] = v;
   __syncthreads();
-  const int w = sh->warp[threadIdx.x & 31];
-  return __reduce_add_sync(kFull, (int)(threadIdx.x & 31) < (int)(threadIdx.x >> 5) ? w : 0);
+  const int w = (int)(threadIdx.x & 31) < (int)(threadIdx.x >> 5) ? sh->warp[threadIdx.x & 31] : 0;
+  return ((int64_t)__reduce_add_sync(kFull, w >> 16) << 16) + __reduce_add_sync(kFull, w & 0xFFFF);
 }
 
 // Two counts of every warp of the cluster: their sums over the warps before this one (of this and of
@@ -201,7 +201,8 @@ __device__ void warp_number(const int32_t* a, int64_t lo, int64_t hi, int64_t n,
   }
 }
 
-// Running sums of the needs: sum[i] = those of the requests before i, sum[n] = all.
+// Running sums of the needs: sum[i] = those of the requests before i, sum[n] = all. (A need is at most the pages
+// of 2^31 tokens, 2^25, so a warp's sum is one of 32 bits.)
 template <class F>
 __device__ int64_t sum_needs(PlanShared* sh, int32_t* sum, int n, F need) {
   if (threadIdx.x == 0) sh->running = 0;

@@ -166,6 +166,22 @@ def test_extend_of_many_sequences_and_pages():
     s.same()
 
 
+def test_extend_of_needs_that_add_up_beyond_32_bits():
+    """1,100 sequences in rows of 2^21 pages, of which all but two ask for a whole row: 2.3e9 pages."""
+    n, width = 1100, 1 << 21
+    table = torch.full((n, width), -1, dtype=torch.int32, device="cuda")
+    lens, refs, granted = dev(np.zeros(n)), dev(np.zeros(100)), dev(np.full(n, 9))
+    refs[[0, 3]] = 1
+    add = np.full(n, width * 64)
+    add[[0, 1]] = 65, 1
+    m.kv_pages_extend(table, lens, refs, dev(add), granted=granted)
+    assert granted.tolist() == [1, 1] + [0] * (n - 2) and lens.tolist() == [65, 1] + [0] * (n - 2)
+    assert torch.nonzero(refs).flatten().tolist() == [0, 1, 2, 3, 4]
+    assert table[0, :3].tolist() == [1, 2, -1] and table[1, :2].tolist() == [4, -1]
+    table[0, :2] = table[1, 0] = -1
+    assert int(table.max()) == int(table.min()) == -1
+
+
 @pytest.mark.parametrize("layers,page_bytes", [(1, 16), (2, 33008)])
 @pytest.mark.parametrize("pages", [7, 129, 700])
 def test_compact(pages, layers, page_bytes):
