@@ -607,10 +607,10 @@ int kv_pages_fork(void* cache, int64_t layers, int64_t layer_stride, int64_t num
 /* kv_pages_extend: sequence s grows by add[s] >= 0 tokens: fresh pages
  * are added to its row until it holds seq_lens[s] + add[s] tokens and its
  * length becomes that. granted[s] is 1, or 0
- * when it was refused and left as it was: too few free pages, or (counted) a
- * row too short for the new length, a negative add or a negative length. The
- * pages that a refused sequence would have got stay free. granted may be NULL.
- * num_seqs <= NVFP4MLA_MAX_REQUESTS. */
+ * when it was refused and left as it was: it needs more pages than are free once
+ * the sequences before it have theirs, or (counted) a row too short for the new
+ * length, a negative add or a negative length. A refused sequence takes nothing
+ * from those after it. granted may be NULL. num_seqs <= NVFP4MLA_MAX_REQUESTS. */
 int kv_pages_extend(int32_t* page_table, int64_t max_pages_per_seq, int32_t* seq_lens, int num_seqs,
                     int32_t* refcounts, int64_t num_pages, const int32_t* add, int32_t* granted,
                     int32_t* dev_status, void* stream);

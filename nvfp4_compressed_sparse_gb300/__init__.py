@@ -684,7 +684,8 @@ def kv_pages_fork(cache, page_table, seq_lens, refcounts, src, dst, new_pages=No
 
 def kv_pages_extend(page_table, seq_lens, refcounts, add, granted=None, dev_status=None, stream=None) -> None:
     """Sequence s grows by add[s] tokens (int32 [S]): fresh pages as needed, and the longer length. granted
-    (int32 [S], optional): 1, or 0 for a sequence that was refused and left as it was."""
+    (int32 [S], optional): 1, or 0 for a sequence that was refused and left as it was, as when it needs more
+    pages than are free once the sequences before it have theirs; those after it may still be granted."""
     import torch
     index = page_table.get_device()
     state = _page_state(page_table, seq_lens, refcounts, index)

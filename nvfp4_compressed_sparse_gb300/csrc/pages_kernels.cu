@@ -385,12 +385,67 @@ __device__ int64_t extend_need(const ExtendArgs& a, int i, int64_t& have, bool& 
   return bad ? -1 : (want > have ? want - have : 0);
 }
 
+// When there are fewer pages than needs: the sequences in order, each granted if its need fits what those before
+// it left, else passed over. sum[i] = the pages granted before sequence i; returns all that are granted. One warp,
+// 32 sequences at a time: those whose need alone is too large are passed over at once, and the first whose
+// running sum is too large where that happens. (Every CTA does the same; the others of its warps wait.)
+__device__ int64_t settle(const ExtendArgs& a, PlanShared* sh, int32_t* sum, int n, int64_t free_pages) {
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+    int64_t have;
+    bool bad;
+    const int64_t need = extend_need(a, i, have, bad);
+    sum[i] = (int32_t)(need > 0 ? need : 0);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int64_t given = 0;
+    for (int base = 0; base < n; base += 32) {
+      const int need = base + lane < n ? sum[base + lane] : 0;
+      int64_t left = free_pages - given;
+      unsigned open = __ballot_sync(kFull, need > 0), granted = 0;
+      while (open != 0) {
+        open &= __ballot_sync(kFull, need <= left);
+        const int mine = (open >> lane) & 1 ? need : 0;
+        int incl = mine;                   // (32 needs of at most 2^25)
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(kFull, incl, d);
+          if (lane >= d) incl += o;
+        }
+        const unsigned over = __ballot_sync(kFull, incl > left) & open;
+        const int stop = over != 0 ? __ffs(over) - 1 : 32;             // passed over, those before it granted
+        const unsigned now = over != 0 ? open & ((1u << stop) - 1) : open;
+        left -= __reduce_add_sync(kFull, (now >> lane) & 1 ? need : 0);
+        granted |= now;
+        open = over != 0 ? open & ~((2u << stop) - 1) : 0u;
+      }
+      const int mine = (granted >> lane) & 1 ? need : 0;
+      int incl = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kFull, incl, d);
+        if (lane >= d) incl += o;
+      }
+      if (base + lane < n) sum[base + lane] = (int32_t)(given + incl - mine);
+      given = free_pages - left;
+    }
+    if (lane == 0) {
+      sum[n] = (int32_t)given;
+      sh->running = given;
+    }
+  }
+  __syncthreads();
+  return sh->running;
+}
+
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads) extend_kernel(const ExtendArgs a) {
   extern __shared__ int32_t sum[];   // [num_seqs + 1]
   __shared__ PlanShared sh;
   const int rank = (int)cluster_ctarank();
   const int n = a.s.num_seqs;
-  const int64_t total = sum_needs(&sh, sum, n, [&](int i) {
+  int64_t total = sum_needs(&sh, sum, n, [&](int i) {
     int64_t have;
     bool bad;
     const int64_t need = extend_need(a, i, have, bad);
@@ -400,24 +455,22 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   piece_of(a.s.num_pages, lo, hi);
   Counts found, unused;
   exchange(&sh, 0, make_int2(warp_count(a.s.refs, lo, hi, a.s.num_pages, 1, IsFree()), 0), found, unused);
-  const int64_t all = found.all;
+  if (total > found.all) total = settle(a, &sh, sum, n, found.all);
   warp_number(a.s.refs, lo, hi, a.s.num_pages, 1, found.before, total, IsFree(), [&](int64_t page, int, int64_t g) {
     if (g >= total) return;
     const int i = owner_of(sum, n, g);
-    if (sum[i + 1] > all) return;    // refused: its pages stay free
     int64_t have;
     bool bad;
     extend_need(a, i, have, bad);
     a.s.refs[page] = 1;
     a.s.table[(int64_t)i * a.s.max_pages + have + (g - sum[i])] = (int32_t)page;
   });
-  const int64_t free_pages = all;
   cluster_sync_all();   // the lengths change only when no CTA reads them any more, and no count is read after this
   for (int i = rank * kPlanThreads + threadIdx.x; i < n; i += kPlanCtas * kPlanThreads) {
     int64_t have;
     bool bad;
     const int64_t need = extend_need(a, i, have, bad);
-    const bool ok = !bad && (need == 0 || sum[i + 1] <= free_pages);
+    const bool ok = !bad && (need == 0 || sum[i + 1] > sum[i]);
     if (bad) count_bad(a.s.status, NVFP4MLA_STAT_BAD_SLOT);
     if (ok) a.s.lens[i] += a.add[i];
     if (a.granted != nullptr) a.granted[i] = ok ? 1 : 0;

@@ -217,13 +217,13 @@ def extend(table, lens, refs, add) -> list:
         if lens[s] < 0 or add[s] < 0 or (add[s] > 0 and want > table.shape[1]):
             granted.append(0)
             continue
-        first, at = at, at + want - have
-        if want > have and at > len(pages):
+        if want - have > len(pages) - at:
             granted.append(0)
             continue
-        for i, p in enumerate(pages[first:at]):
-            table[s, have + i] = p
-            refs[p] = 1
+        for i in range(want - have):
+            table[s, have + i] = pages[at + i]
+            refs[pages[at + i]] = 1
+        at += max(0, want - have)
         lens[s] += add[s]
         granted.append(1)
     return granted

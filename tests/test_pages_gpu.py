@@ -150,6 +150,24 @@ def test_extend(pages, seed):
         s.same()
 
 
+def test_extend_passes_over_what_does_not_fit():
+    """A sequence that asks for more than there is left takes nothing from those behind it."""
+    s = State([64] * 6, 16, width=40, seed=14)                         # 10 free
+    s.extend([64 * 20, 64 * 3, 64 * 8, 64 * 7, 1, 0])
+    assert s.lens.tolist() == [64, 256, 64, 512, 64, 64] and not (s.refs == 0).any()
+    s.same()
+
+
+@pytest.mark.parametrize("n,pages", [(5, 12), (33, 100), (1500, 3000), (16384, 30000), (16384, 16400)])
+def test_extend_when_pages_run_out(n, pages):
+    rng = np.random.default_rng(n)
+    s = State(rng.integers(0, 65, n), pages, page_bytes=16, width=300, seed=n)
+    for _ in range(3):
+        s.extend(rng.integers(0, 2, n) * rng.choice([1, 60, 300, 2000, 17000], n, p=[.4, .3, .2, .05, .05]))
+        s.same()
+    assert (s.refs == 0).sum() < 5
+
+
 def test_extend_refuses():
     s = State([10, 20, 30, 64, 0], 100, width=2, seed=7)
     s.d_lens[4], s.lens[4] = -3, -3
