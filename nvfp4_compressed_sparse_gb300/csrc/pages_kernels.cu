@@ -540,10 +540,10 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     moved.before += all >> 16;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int32_t page = (int32_t)(at + k);
-      if (hole(page, vs[k])) a.holes[g++] = page;
-      if (page < n) a.remap[page] = moves(page, vs[k]) ? moving(m) : (vs[k] > 0 ? page : -1);
-      if (moves(page, vs[k])) a.movers[m++] = page;
+      const int64_t page = at + k;         // behind n it may leave 32 bits
+      if (hole(page, vs[k])) a.holes[g++] = (int32_t)page;
+      if (page < n) a.remap[page] = moves(page, vs[k]) ? moving(m) : (vs[k] > 0 ? (int32_t)page : -1);
+      if (moves(page, vs[k])) a.movers[m++] = (int32_t)page;
     }
   }
   if (cluster_ctarank() == 0 && threadIdx.x == 0) {

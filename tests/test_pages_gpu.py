@@ -247,6 +247,35 @@ def test_compact_of_more_chunks_than_blocks(lens, layers, page_bytes):
     s.same()
 
 
+def test_page_numbers_up_to_the_largest():
+    """A pool of 2^31 - 1 pages of 16 bytes (34 GB): its last pages are found, moved and given out like any others."""
+    n = (1 << 31) - 1
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB")
+    cache = torch.empty((n, 16), dtype=torch.uint8, device="cuda")
+    refs = torch.zeros(n, dtype=torch.int32, device="cuda")
+    held = [5, 7, n - 130, n - 129, n - 3, n - 1]
+    for i, p in enumerate(held):
+        refs[p] = 1
+        cache[p] = i + 1
+    table, lens = dev(np.array([held + [-1], [-1] * 7])), dev([6 * 64 - 1, 0])
+    remap, live = m.kv_pages_compact(cache, table, refs)
+    assert live.item() == 6 and table[0].tolist() == [5, 0, 1, 2, 3, 4, -1]
+    assert [cache[int(p), 0].item() for p in table[0, :6]] == [1, 2, 3, 4, 5, 6]
+    assert remap[torch.tensor([5, 6, 7, n - 130, n - 129, n - 3, n - 2, n - 1], device="cuda")].tolist() == [5, -1, 0, 1, 2, 3, -1, 4]
+    assert torch.nonzero(refs[:100]).flatten().tolist() == [0, 1, 2, 3, 4, 5] and not refs[n - 200:].any()
+    del remap
+    refs.fill_(1)
+    refs[n - 1] = refs[n - 2] = 0
+    new = m.kv_pages_fork(cache, table, lens, refs, dev([0]), dev([1]))
+    assert new.tolist() == [n - 2] and cache[n - 2, 0] == 6 and refs[n - 2] == 1
+    granted = dev([9, 9])
+    m.kv_pages_extend(table, lens, refs, dev([1, 2]), granted=granted)
+    assert granted.tolist() == [1, 1] and table[1].tolist() == [5, 0, 1, 2, 3, n - 2, n - 1] and lens.tolist() == [384, 385]
+    del cache, refs
+    torch.cuda.empty_cache()
+
+
 def test_a_captured_step_replays_on_the_state_it_finds():
     s = State([100, 64, 1, 0, 0, 0], 40, seed=12)
     ended, src, dst, add = dev([-1]), dev([0]), dev([3]), dev(np.ones(6))
