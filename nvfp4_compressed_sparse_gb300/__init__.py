@@ -554,7 +554,7 @@ def kv8_decode(q, cache, page_table, seq_lens, kv_heads: int, softmax_scale, win
     """Attention of each request's Q newest tokens over its cached tokens: q bf16 or fp16 [B, Q, H, head_dim]
     (batch and query axes of one stride, any head stride), cache uint8 [P, kv8_page_bytes], page_table int32
     [B, max_pages], seq_lens int32 [B]; window > 0: the newest `window` positions only. Returns (out as q's
-    type [B, Q, H, head_dim], lse fp32 [B, Q, H])."""
+    type [B, Q, H, head_dim], lse fp32 [B, Q, H]). A step of no requests (B = 0) enqueues nothing."""
     import torch
     lib, i32 = load_library(), torch.int32
     dt = _kv8_dtype(q, "q")
@@ -587,6 +587,8 @@ def kv8_decode(q, cache, page_table, seq_lens, kv_heads: int, softmax_scale, win
         raise ValueError("out must be [B, Q, H, head_dim] and lse [B, Q, H]")
     if not 0 <= window < 1 << 31:
         raise ValueError("window must be 0 (none) or a number of positions below 2^31")
+    if B == 0:
+        return out, lse
     rc = lib.kv8_decode(qp, s1 if Q > 1 else s0 if B > 1 else 0, s2 if H > 1 else 0, dt, cp, pages, pp, max_pages, sp,
                         B, Q, H, kv_heads, d, float(softmax_scale), int(window), op, lp, workspace.data_ptr(),
                         workspace.nbytes,

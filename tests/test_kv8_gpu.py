@@ -158,6 +158,17 @@ def test_append_of_nothing():
     assert bool((d == 7).all())
 
 
+def test_decode_of_no_requests():
+    """A step that has none is as good as any, as it is for kv8_append; what it is given is checked all the same."""
+    cache = torch.zeros((2, m.kv8_page_bytes(2, 64)), dtype=torch.uint8, device="cuda")
+    q, table, lens = torch.zeros((0, 3, 4, 64), dtype=torch.float16, device="cuda"), dev(np.zeros((0, 5))), dev(np.zeros(0))
+    out, lse = m.kv8_decode(q, cache, table, lens, 2, 0.125)
+    assert out.shape == (0, 3, 4, 64) and out.dtype == torch.float16 and lse.shape == (0, 3, 4) and lse.dtype == torch.float32
+    for bad in (dict(page_table=dev(np.zeros((1, 5)))), dict(cache=cache[:, 1:]), dict(window=-1)):
+        with pytest.raises(ValueError):
+            m.kv8_decode(**(dict(q=q, cache=cache, page_table=table, seq_lens=lens, kv_heads=2, softmax_scale=0.125) | bad))
+
+
 # ------------------------------------------------------------------ decode
 LENS = [1, 0, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 191, 300, 1000]
 
