@@ -188,6 +188,13 @@ def test_decode_window(window, Q):
     check(*c.run(window), c.reference(window))
 
 
+@pytest.mark.parametrize("window", [1, 2, 16, 63, 64, 65, 128, 200, 5000])
+@pytest.mark.parametrize("Q,G,dtype", [(1, 4, "bf16"), (5, 3, "fp16"), (4, 8, "bf16")])
+def test_decode_window_at_128_dims(window, Q, G, dtype):
+    c = Case(LENS, 2, 128, dtype, Q=Q, G=G, seed=window)
+    check(*c.run(window), c.reference(window))
+
+
 def test_decode_rows_that_masks_leave_empty():
     """More new tokens than cached ones, lengths of zero and below: out 0, lse -inf."""
     c = Case([0, 1, 3, 7, 8, 64], 2, 128, Q=8, G=2)
