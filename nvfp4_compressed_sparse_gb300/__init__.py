@@ -573,7 +573,7 @@ def kv8_decode(q, cache, page_table, seq_lens, kv_heads: int, softmax_scale, win
     if seq_lens.shape[0] != B or rows != B:
         raise ValueError("shape mismatch")
     fresh = [None] * 2
-    with _taken_on(stream):
+    with _taken_on(stream if out is None or lse is None or workspace is None else None):
         if out is None:
             out = fresh[0] = torch.empty(shape, dtype=q.dtype, device=q.device)
         if lse is None:
@@ -716,7 +716,7 @@ def kv_pages_compact(cache, page_table, refcounts, remap=None, num_live=None, wo
     if counts != pages:
         raise ValueError("refcounts must have one entry per page of the cache")
     fresh = [None] * 2
-    with _taken_on(stream):
+    with _taken_on(stream if remap is None or num_live is None or workspace is None else None):
         if remap is None:
             remap = fresh[0] = torch.empty_like(refcounts)
         if num_live is None:
