@@ -96,7 +96,8 @@ def check_small_weights(out, ref, adds, what=""):
     two above what is left, so that the next ones leave 2^-4 each: 2^-3-4-4-4 = 2^-15. Below 2^-14 a part has steps of
     2^-16, so the last one leaves 2^-17 / 16^3 = 2^-29, 2^-40 of the largest weight times its value's scale. The sum
     is made of `adds` additions in 32 bits, each off by at most a step (2^-23) of what it has reached. Scores and
-    exponentials as in check(); the sum that divides is of unrounded weights."""
+    exponentials as in check(); the sum that divides is of unrounded weights. (check() was derived for four E4M3 parts:
+    it has 2^-16 twice, as if the divisor were rounded too, which covers 2^-15 once, and 2^-26 of spread.)"""
     r_out, _, mass, reach, spread = ref
     dz = (r_out.shape[-1] + 8) * 2.0 ** -24 * reach
     dw = 2 * (dz + 2.0 ** -21) + 2.0 ** -15 + adds * 2.0 ** -23

@@ -377,6 +377,20 @@ def test_decode_one_key_as_heavy_as_all_others_together(n, log2_scale, at, D, dt
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D,G,Q", [(128, 4, 1), (64, 3, 2), (128, 4, 4), (64, 16, 1), (128, 11, 3)])
+@pytest.mark.parametrize("max_ctas", [0, 1, 4])
+def test_decode_within_the_bound_of_what_weights_lose(D, G, Q, dtype, max_ctas):
+    """Scores and block scales of a wide spread, cut into units of one and of several CTAs."""
+    c = Case([3000, 700, 129, 1], 2, D, dtype, Q=Q, G=G, seed=D + G)
+    _, scales = kv8.parts(c.cache, 2, D)
+    used = scales[:, :, 1] != 0xFF
+    low, high = (112, 138) if dtype == "bf16" else (112, 131)
+    scales[:, :, 1][used] = c.rng.integers(low, high, used.sum())
+    c.scale *= 2
+    check_small_weights(c.run(max_ctas=max_ctas)[0], c.reference(), 3000 / 32)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_decode_a_key_far_above_a_million_others(dtype):
     """The others' weights are e^-15.9 of the one key's, and all their sum is an eighth of it."""
     n = 1 << 20
