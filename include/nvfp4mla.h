@@ -476,11 +476,15 @@ size_t kv8_page_bytes(int kv_heads, int head_dim);
  *          with its sign bit
  *   the codes of the block's tokens from before become E4M3(value / 2^(e-127))
  * Nothing else of the cache changes: not the rows behind the last new token.
+ * A block's scale never shrinks while it holds tokens from before: a token that
+ * is dropped again (a rejected draft) leaves the scale that it called for, and
+ * bits that its block's other tokens lost to that scale are not brought back.
  *
  *   k, v              dtype [num_tokens, kv_heads, head_dim], 16-byte aligned;
  *                     token and head strides in elements, multiples of 8
  *   dtype             NVFP4MLA_BF16 or NVFP4MLA_FP16
- *   cu_tokens         int32 [B + 1], not decreasing, cu_tokens[B] <= num_tokens
+ *   cu_tokens         int32 [B + 1], not decreasing (where it does, tokens of any
+ *                     request may be left out), cu_tokens[B] <= num_tokens
  *   seq_lens          int32 [B]: cached tokens of request b with the new ones
  *   page_table        int32 [B, max_pages_per_seq] contiguous; a page that gets
  *                     new tokens must belong to one request only
@@ -560,10 +564,14 @@ int kv8_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, int
  * with them, as they know pages by their bytes only (22,528 for the NVFP4
  * cache, kv8_page_bytes for the 8-bit one). The state is three device arrays:
  *   page_table   int32 [num_seqs, max_pages_per_seq], -1 = none
- *   seq_lens     int32 [num_seqs], 0 = the sequence is empty
+ *   seq_lens     int32 [num_seqs], 0 = the sequence is empty (a negative one is
+ *                no length; kv_pages_fork keeps those below -2^31 + 16384 for itself)
  *   refcounts    int32 [num_pages], 16-byte aligned: how many table entries
  *                hold the page; 0 = the page is free
  * A row's entries behind ceil(seq_lens / 64) are -1: these calls keep it so.
+ * No call shortens a sequence: whoever lowers a length (rejected draft tokens)
+ * first gives back, in table and counts, the pages behind the new end, or
+ * kv_pages_extend writes over their entries and their counts never return to 0.
  * Fresh pages are the lowest-numbered free ones, in the requests' order, so
  * the results are the same on every run. Nothing is read back by the host.
  * layers caches of num_pages pages each, layer_stride bytes apart, share the

@@ -41,12 +41,14 @@
 // 16 requests of 20-90K tokens, 8 key/value heads: 1.38 GB in 210 us, 6.6 TB/s, 97 % of the measured copy
 // bandwidth; one request of 131K tokens: 269 MB in 51.5 us (77 %: 5 us until the first product, 5 from the
 // last to the joined result). With 64 dims a byte brings twice the softmax work: 64 requests of 4-30K
-// tokens: 871 MB in 151 us (85 %). With 16 columns the softmax sets the pace, some 0.8 us a stage at 128
-// dims and 1.1 at 64 (32 requests of 4-16K, two queries of 8 heads: 595 MB in 109 us, 81 %; four queries,
-// whose two column tiles read the codes twice, 179 us, 49 %). Its instructions and registers are what
-// there is to save: pairs of columns in one instruction took those from 117 and 202 to 115 and 198 us
-// (and 147 to 130 with 64 dims, four queries of 4 heads), tile loops without spilled registers to 109 and
-// 179 (103).
+// tokens: 871 MB in 152 us (85 %). With 16 columns the softmax's chain of a tile sets the pace, some 0.8 us
+// a stage at 128 dims and 1.1 at 64 (32 requests of 4-16K, two queries of 8 heads: 595 MB in 109 us, 81 %;
+// four queries, whose two column tiles read the codes twice, 181 us, 49 %; with 64 dims, four queries of 4
+// heads, 105, 62 %). It is latency more than issue: in the four queries' step 57 % of the issue slots are
+// taken, and loads (tensor memory's among them) are the largest stall. Fewer instructions and registers
+// shorten it all the same: pairs of columns in one instruction took the first two from 117 and 202 to 115
+// and 198 us, a join with few registers, beside which the compiler kept the tile loop's values in
+// registers, to 109 and 179.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -86,7 +88,7 @@ struct Shape {
   static constexpr int kPageRows = kRows / kPages;
   static constexpr int kGroup = 32 / kPages;                    // stages whose page numbers are read together
   static constexpr int kFewTiles = kPair ? 4 : 8;               // of a unit that is not worth splitting
-  static constexpr int kMinTiles = kStreams;                    // of a CTA: work for every stream
+  static constexpr int kMinTiles = kStreams;                    // of a CTA, on average: work for every stream
   static constexpr int kNS = (kQParts * NC + 15) / 16 * 16;     // columns of S
   static constexpr int kNO = kWParts * NC;                      // columns of O of a half
   static constexpr int kWRow = kHalves * kNO;                   // bytes of a row of w, columns of O
@@ -235,8 +237,8 @@ __device__ __forceinline__ void split_parts(float a, float b, uint32_t (&part)[k
   part[0] = f32x2_to_e4m3x2(a, b);
   uint32_t h = e4m3x2_to_f16x2(part[0]);
   const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  // what the first part leaves has at most 20 significant bits, of which the fp16 keeps 11: as much
-  // as the other parts hold
+  // (an element of q has at most 11 significant bits: what the first part leaves is an fp16, but for its last
+  // subnormal bits, below what the other parts hold)
   const float2 left = __ffma2_rn(c, make_float2(-1.f, -1.f), make_float2(a, b));
   __half2 r = __floats2half2_rn(left.x, left.y);
   const __half2 sixteen = __floats2half2_rn(16.f, 16.f);
@@ -575,7 +577,7 @@ struct Cta {
     }
   }
 
-  // ---------------------------------------------------------------- softmax (warps 4-11)
+  // ---------------------------------------------------------------- softmax (warps 4-11, with 16 columns 4-19)
   // A token's row of V that no column attends to becomes zeros (it may hold anything), and a NaN in
   // one that only some columns attend to is taken out and noted for those.
   static __device__ __forceinline__ uint32_t nans_in(const uint4& x) {
@@ -657,8 +659,9 @@ struct Cta {
   // Joins the partial means that CTAs c_lo .. c_hi left of a unit, for dim d of this warpgroup's
   // columns, 32 at a time: a lane has the maxima and sums of one, and the outputs of kSlots are in flight
   // together, the first of them beside the maxima. (It has few registers on purpose: with every part's
-  // maxima and sums in each thread, the tile loop's values were spilled: with 16 columns 197 us instead of
-  // 178, 32 requests of 4-16K, four queries of 8 heads, and 120 instead of 106 with 64 dims.)
+  // maxima and sums in each thread, the compiler spilled: with 16 columns 197 us instead of 178, 32 requests
+  // of 4-16K, four queries of 8 heads, and 120 instead of 106 with 64 dims. Of the eight instances one still
+  // spills, 4 bytes: 64 dims, 16 columns, fp16.)
   template <bool kHalf>
   __device__ void join(const int* row, int c, int d, int c_lo, int c_hi, int first) {
     constexpr int kN = NC / (S::kSoftmax / 128), kSlots = S::kThreads == 384 ? 8 : 4;
@@ -1133,9 +1136,11 @@ __global__ void __launch_bounds__(Shape<D, NC, kHalf ? 3 : 2>::kThreads, 1) kv8_
   const int of_warp = lane < kThreads / 32 ? ctl->scan_sum[lane] : 0;
   const int before = (__reduce_add_sync(kFull, lane < warp ? of_warp : 0) + incl - sum) * p.kv_heads;
   const int all = __reduce_add_sync(kFull, of_warp) * p.kv_heads;      // of one column tile
-  // no CTA gets less than a tile for each of its streams, and where units have few tiles, no less than
-  // an average unit: joining partial results costs some 4 us, a tile 0.6 (one request of 1,000 tokens:
-  // 10.6 us, and 12.7 when its eight units are split)
+  // no more CTAs than leave each a tile for each of its streams on average, and where units have few tiles, no
+  // more than units: joining partial results costs some 4 us, a tile 0.6 (one request of 1,000 tokens: 10.6
+  // us, and 12.7 when its eight units are split). Ranges divide positions, of which a unit's first kUnitCost
+  // are no tiles, so where few CTAs share one unit the first may have no tile and the others more than that
+  // average: of 16 tiles of one unit, cut in eight, two have none, one has one, and five have three.
   const int units = p.B * p.kv_heads * cts, tiles = all * cts - kUnitCost * units;
   // Where a unit would be cut into very many, a part less saves more of the joining (some 0.1 us each) than
   // it adds to the others' tiles: of t tiles, 2 sqrt(t) parts at most (one request, one key/value head of 8
