@@ -455,7 +455,8 @@ int sparse_mla_decode_fp8_token(const void* q, const void* kv_cache_tok, int64_t
  * scale has to grow: only codes that become subnormal are rounded again.
  */
 #define NVFP4MLA_BLOCK_TOKENS 16  /* tokens per scale of the 8-bit cache         */
-enum { NVFP4MLA_BF16 = 0, NVFP4MLA_FP16 = 1 }; /* element types of k, v, q, out   */
+enum { NVFP4MLA_BF16 = 0, NVFP4MLA_FP16 = 1, NVFP4MLA_FP32 = 2 }; /* element types: k, v, q and out
+                                    bf16 or fp16, spec_verify's logits any of them */
 
 /* Bytes of one page: 1 <= kv_heads <= 256, head_dim 64 or 128; 0 otherwise. */
 size_t kv8_page_bytes(int kv_heads, int head_dim);
@@ -502,6 +503,44 @@ int kv8_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, con
                int64_t v_head_stride, int dtype, int64_t num_tokens, const int32_t* cu_tokens,
                const int32_t* seq_lens, const int32_t* page_table, int64_t max_pages_per_seq, int B, int kv_heads,
                int head_dim, void* cache, int64_t num_pages, int32_t* dev_status, void* stream);
+
+/*
+ * kv8_append_rope: kv8_append of keys that are normalised and rotated on the way, and the queries of the
+ * same tokens beside them: what stands between a layer's projections and kv8_decode.
+ *
+ * Of each row x of a query or key head (head_dim values), in fp32:
+ *   y = x w / sqrt(mean(x^2) + eps), where that kind has a weight; else y = x
+ *   pair i of rotary_dim / 2, by the cosine c and sine s of its token's position:
+ *     (a, b) -> (a c - b s, b c + a s),  a = y[i], b = y[i + rotary_dim / 2], or, interleaved,
+ *     a = y[2i], b = y[2i + 1];  what lies behind rotary_dim is not turned
+ * A query is rounded once, to dtype, into q_out; a key once, to its block's code, whose scale is that of
+ * the turned keys. Values, blocks and scales as kv8_append. A NaN key that this arithmetic makes is stored
+ * as 0x7F.
+ *
+ *   q                 dtype [num_tokens, heads, head_dim], strides as k's
+ *   q_out             the same shape, strides of its own; it may be q itself, and must not otherwise
+ *                     overlap q, k or v. Rows of no request, or of one that is left out, are not written
+ *   heads             >= 1 (any number beside kv_heads, <= 32,768)
+ *   q_weight, k_weight  dtype [head_dim], 16-byte aligned, or NULL: no norm of that kind
+ *   eps               >= 0, finite
+ *   cos_sin           fp32 [max_positions, rotary_dim]: a position's cosines of all pairs, then its sines
+ *   rotary_dim        a multiple of 16, <= head_dim
+ *   positions         int32 [axes, num_tokens], axis_stride elements from axis to axis, or NULL (axes 1):
+ *                     a token's place in its sequence
+ *   sections          HOST int32 [axes]: the first sections[0] pairs go by axis 0, and so on; their sum is
+ *                     rotary_dim / 2. Not read when axes is 1.  axes  1 .. 4
+ *   everything else   as kv8_append
+ * A token with a position outside of the table is counted (NVFP4MLA_STAT_BAD_INDEX), and what the
+ * position turns of its query and key becomes NaN.
+ */
+int kv8_append_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k, int64_t k_token_stride,
+                    int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride, int dtype,
+                    int64_t num_tokens, const int32_t* cu_tokens, const int32_t* seq_lens, const int32_t* page_table,
+                    int64_t max_pages_per_seq, int B, int heads, int kv_heads, int head_dim, const void* q_weight,
+                    const void* k_weight, float eps, const float* cos_sin, int64_t max_positions, int rotary_dim,
+                    int interleaved, const int32_t* positions, int64_t axis_stride, const int32_t* sections, int axes,
+                    void* q_out, int64_t out_token_stride, int64_t out_head_stride, void* cache, int64_t num_pages,
+                    int32_t* dev_status, void* stream);
 
 /* Bytes of workspace that kv8_decode needs for these sizes on a GPU with
  * num_sms SMs (num_sms <= 0: the current device); 0 for invalid sizes. */
@@ -560,6 +599,108 @@ int kv8_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, int
                void* workspace, size_t workspace_bytes, int32_t* dev_status, uint32_t flags, void* stream);
 
 /*
+ * A speculative step over the 8-bit cache. Each request's Q newest places hold the nodes of a tree: node 0
+ * the newest token that is certain, the others drafts, each with a parent of a smaller number. The step:
+ * kv_pages_extend and kv8_append_rope (with the nodes' places in the text as positions) make room for and
+ * write them, kv8_decode_tree attends, spec_verify says which drafts stand, kv8_keep and kv_pages_trim
+ * take the others out.
+ */
+#define NVFP4MLA_MAX_NODES 64     /* nodes of a tree, node 0 among them           */
+
+/* As kv8_decode_workspace_size, for kv8_decode_tree. */
+size_t kv8_decode_tree_workspace_size(int B, int Q, int H, int kv_heads, int head_dim, int num_sms);
+
+/*
+ * kv8_decode_tree: kv8_decode for trees. With base = seq_lens[b] - Q, node j of request b attends to the
+ * positions t >= 0 with
+ *   t < base, and t > place - window when window > 0, place = base + (bits of its mask) - 1 being its place
+ *   in the text; or t = base + i, i < Q, with bit i of masks[b, j] set (its ancestors and itself)
+ * A mask of 0 is padding: such a node attends to nothing, its out is 0 and its lse -inf. Bits from Q on are
+ * not looked at, but a mask of those alone is not 0.
+ *
+ *   masks             uint64 [B, Q], 8-byte aligned
+ *   Q                 1 .. NVFP4MLA_MAX_NODES
+ *   window            0 (none), or >= Q (else NVFP4MLA_ERR_UNSUPPORTED): drafts are never outside of it
+ *   everything else   as kv8_decode
+ */
+int kv8_decode_tree(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype, const void* cache,
+                    int64_t num_pages, const int32_t* page_table, int64_t max_pages_per_seq, const int32_t* seq_lens,
+                    const uint64_t* masks, int B, int Q, int H, int kv_heads, int head_dim, float softmax_scale, int window,
+                    void* out, float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status, uint32_t flags,
+                    void* stream);
+
+/* Bytes of workspace that spec_verify needs; 0 for invalid sizes. */
+#define NVFP4MLA_MAX_VOCABULARY (1 << 24)
+size_t spec_verify_workspace_size(int B, int Q, int64_t V);
+
+/*
+ * spec_verify: which drafts of each request's tree the target's distribution accepts, and the token that
+ * follows them, from given random numbers.
+ *
+ * p_j: softmax of logits[b, j, :] / temperature, the target's distribution behind node j. From node 0 on, the
+ * children of the current node c are tried in the order of their numbers, with r = p_c and s = 1 at first:
+ *   child j with token x is accepted, and becomes the current node, when uniforms[b, j] q(x) s < r(x);
+ *   else r becomes max(r - s q, 0), and s the sum of r
+ * where q = draft_probs[b, c, :], from which all children of c were drawn, or, without draft_probs, 1 at x and
+ * 0 elsewhere. When no child is left, the next token is the first whose running sum of r exceeds
+ * uniforms[b, 0] times the sum of r (of p_c, should nothing be left of r). So the tokens are distributed as
+ * the target's own. Greedy, temperature 0: a child is accepted when its token is the smallest of those with
+ * the largest logit, which is the next token too.
+ *
+ * Logits may be -inf (never drawn, and so is a NaN). Of a row with +inf those are equally likely, and the
+ * only ones. Where a row has nothing else but -inf, none of its children is accepted and the next token is -1
+ * (counted). A decision or a draw that is nearer to a border than the rounding of exponentials and sums in
+ * fp32 (some 1e-7 of the probability) may fall to either side, the same on every run.
+ *
+ *   logits            dtype [B, Q, V]; row (b, j) begins (b*Q + j) * logits_row_stride elements in; aligned to
+ *                     its elements
+ *   dtype             NVFP4MLA_BF16, NVFP4MLA_FP16 or NVFP4MLA_FP32
+ *   draft_probs       fp32 [B, Q, V], rows probs_row_stride elements apart, or NULL; rows of leaves are not read
+ *   drafts            int32 [B, Q]: the nodes' tokens (node 0's is not read)
+ *   parents           int32 [B, Q]: a smaller node, or -1: no node (node 0's is not read). A draft with another
+ *                     number for a parent, or a token outside of 0 .. V-1, is left out and counted
+ *                     (NVFP4MLA_STAT_BAD_INDEX)
+ *   uniforms          fp32 [B, Q], of [0, 1); below is 0, a NaN or 1 and more refuse, or draw the last token
+ *                     that has a probability
+ *   temperatures      fp32 [B], or NULL: 1. What is not above 0 is greedy
+ *   B, Q, V           B >= 1, 1 <= Q <= NVFP4MLA_MAX_NODES, 1 <= V <= NVFP4MLA_MAX_VOCABULARY
+ *   tokens            int32 [B, Q]: the accepted drafts' tokens, the next token, -1
+ *   path              int32 [B, Q]: the accepted nodes, -1 behind them
+ *   accepted          int32 [B]: how many
+ *   workspace         device scratch, 256-byte aligned, spec_verify_workspace_size bytes; contents need no
+ *                     initialisation. Calls that share one must be ordered.
+ * All pointers: device memory of the current device. More than INT32_MAX chunks of 1,024 logits return
+ * NVFP4MLA_ERR_UNSUPPORTED.
+ */
+int spec_verify(const void* logits, int64_t logits_row_stride, int dtype, const float* draft_probs, int64_t probs_row_stride,
+                const int32_t* drafts, const int32_t* parents, const float* uniforms, const float* temperatures, int B,
+                int Q, int64_t V, int32_t* tokens, int32_t* path, int32_t* accepted, void* workspace, size_t workspace_bytes,
+                int32_t* dev_status, void* stream);
+
+/*
+ * kv8_keep: the accepted nodes' keys and values move up behind node 0, in every layer. With base =
+ * seq_lens[b] - Q, node path[b, i], i < accepted[b], goes to place base + 1 + i. A block of 16 places that
+ * gets a node from another place takes the largest scale byte of the blocks whose tokens it then holds; the
+ * codes of those with a smaller one become E4M3(value / 2^(e - 127)) (a NaN stays). Nothing else of the cache
+ * changes; seq_lens and the page table stay as they are.
+ *
+ *   path              int32 [B, Q]; 0 < path[b, 0] < path[b, 1] < ... < Q
+ *   accepted          int32 [B]; < 0: leave the request out
+ *   new_lens          int32 [B] (output): base + 1 + accepted[b], for kv_pages_trim; seq_lens[b] of a request that
+ *                     is left out, or refused (and counted, NVFP4MLA_STAT_BAD_SLOT): another path than that, or
+ *                     fewer than Q tokens
+ *   layers, layer_stride  caches of num_pages pages each, layer_stride bytes apart (a multiple of 16; not read
+ *                     when layers is 1), that share the table
+ *   everything else   as kv8_append. A place whose table entry is no page of the cache is not read or not
+ *                     written, and counted (NVFP4MLA_STAT_BAD_PAGE). Pages that get nodes must belong to one
+ *                     request only
+ * B of 0 enqueues nothing.
+ */
+int kv8_keep(void* cache, int64_t layers, int64_t layer_stride, int64_t num_pages, const int32_t* page_table,
+             int64_t max_pages_per_seq, const int32_t* seq_lens, const int32_t* path, const int32_t* accepted, int B, int Q,
+             int kv_heads, int head_dim, int32_t* new_lens, int32_t* dev_status, void* stream);
+
+/*
  * Pages of a cache: who holds which. Every paged cache of this library works
  * with them, as they know pages by their bytes only (22,528 for the NVFP4
  * cache, kv8_page_bytes for the 8-bit one). The state is three device arrays:
@@ -569,7 +710,7 @@ int kv8_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, int
  *   refcounts    int32 [num_pages], 16-byte aligned: how many table entries
  *                hold the page; 0 = the page is free
  * A row's entries behind ceil(seq_lens / 64) are -1: these calls keep it so.
- * No call shortens a sequence: whoever lowers a length (rejected draft tokens)
+ * kv_pages_trim alone shortens a sequence: whoever lowers a length otherwise
  * first gives back, in table and counts, the pages behind the new end, or
  * kv_pages_extend writes over their entries and their counts never return to 0.
  * Fresh pages are the lowest-numbered free ones, in the requests' order, so
@@ -595,6 +736,11 @@ int kv_pages_copy(void* cache, int64_t layers, int64_t layer_stride, int64_t num
 int kv_pages_free(int32_t* page_table, int64_t max_pages_per_seq, int32_t* seq_lens, int num_seqs,
                   int32_t* refcounts, int64_t num_pages, const int32_t* seqs, int n, int32_t* dev_status,
                   void* stream);
+
+/* kv_pages_trim: sequence s is cut to new_lens[s] tokens (int32 [num_seqs]): the entries behind become -1, their
+ * pages' counts go down by one. A new length below 0 or above seq_lens[s] is refused and counted. */
+int kv_pages_trim(int32_t* page_table, int64_t max_pages_per_seq, int32_t* seq_lens, int num_seqs, int32_t* refcounts,
+                  int64_t num_pages, const int32_t* new_lens, int32_t* dev_status, void* stream);
 
 /* kv_pages_fork: sequence dst[i], empty before, becomes a copy of sequence
  * src[i]: its full pages are shared (counted once more), its part-full last

@@ -9,8 +9,10 @@ C entry points (see include/nvfp4mla.h): mla_kv_pack,
 sparse_mla_decode_workspace_size, sparse_mla_decode, sparse_mla_decode_plan,
 sparse_mla_decode_noalloc, indexer_topk, fp8_kv_pack, nvfp4_stage_fp8,
 sparse_mla_decode_fp8, fp8_token_kv_pack, sparse_mla_decode_fp8_token,
-sparse_mla_decode_shared, kv8_page_bytes, kv8_append, kv8_decode_workspace_size,
-kv8_decode, kv_pages_copy, kv_pages_free, kv_pages_fork, kv_pages_extend,
+sparse_mla_decode_shared, kv8_page_bytes, kv8_append, kv8_append_rope,
+kv8_decode_workspace_size, kv8_decode, kv8_decode_tree_workspace_size,
+kv8_decode_tree, spec_verify_workspace_size, spec_verify, kv8_keep,
+kv_pages_copy, kv_pages_free, kv_pages_trim, kv_pages_fork, kv_pages_extend,
 kv_pages_compact_workspace_size, kv_pages_compact, nvfp4mla_status_string.
 """
 from __future__ import annotations
@@ -101,6 +103,23 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.kv8_decode.argtypes = [vp, i64, i64, i32, vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, ctypes.c_float,
                                    i32, vp, vp, vp, sz, vp, u32, vp]
         lib.kv8_decode.restype = i32
+        f32 = ctypes.c_float
+        lib.kv8_append_rope.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, i64, vp, vp, vp, i64, i32, i32, i32, i32,
+                                        vp, vp, f32, vp, i64, i32, i32, vp, i64, vp, i32, vp, i64, i64, vp, i64, vp, vp]
+        lib.kv8_append_rope.restype = i32
+        lib.kv8_decode_tree_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+        lib.kv8_decode_tree_workspace_size.restype = sz
+        lib.kv8_decode_tree.argtypes = [vp, i64, i64, i32, vp, i64, vp, i64, vp, vp, i32, i32, i32, i32, i32, f32, i32, vp, vp,
+                                        vp, sz, vp, u32, vp]
+        lib.kv8_decode_tree.restype = i32
+        lib.spec_verify_workspace_size.argtypes = [i32, i32, i64]
+        lib.spec_verify_workspace_size.restype = sz
+        lib.spec_verify.argtypes = [vp, i64, i32, vp, i64, vp, vp, vp, vp, i32, i32, i64, vp, vp, vp, vp, sz, vp, vp]
+        lib.spec_verify.restype = i32
+        lib.kv8_keep.argtypes = [vp, i64, i64, i64, vp, i64, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp]
+        lib.kv8_keep.restype = i32
+        lib.kv_pages_trim.argtypes = [vp, i64, vp, i32, vp, i64, vp, vp, vp]
+        lib.kv_pages_trim.restype = i32
         lib.kv_pages_copy.argtypes = [vp, i64, i64, i64, i64, vp, vp, i64, vp, vp]
         lib.kv_pages_copy.restype = i32
         lib.kv_pages_free.argtypes = [vp, i64, vp, i32, vp, i64, vp, i32, vp, vp]
@@ -545,18 +564,86 @@ def kv8_append(k, v, cu_tokens, seq_lens, page_table, cache, dev_status=None, st
         raise NvFp4MlaError(rc, "kv8_append")
 
 
+def _rows(t, n):
+    """Token and head strides of t [N, heads, D] (n tokens): the stride of an axis of one entry is never used and may be anything."""
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and t.numel():
+        raise ValueError("q, k, v and q_out must be contiguous along the feature axis")
+    return (s0 if n > 1 else 0), (s1 if t.shape[1] > 1 else 0)
+
+
+@functools.lru_cache(maxsize=64)
+def _int_array(values: tuple):
+    return (ctypes.c_int32 * len(values))(*values)
+
+
+def kv8_append_rope(q, k, v, cos_sin, cu_tokens, seq_lens, page_table, cache, q_weight=None, k_weight=None, eps: float = 1e-6,
+                    positions=None, sections=None, interleaved: bool = False, q_out=None, dev_status=None, stream=None):
+    """kv8_append of keys that are normalised (where k_weight [head_dim] is given) and rotated on the way, and the queries
+    q [N, heads, head_dim] of the same tokens beside them (q_weight): returns q_out of q's shape and type (q itself may be
+    given). cos_sin fp32 [max_positions, rotary_dim]: the cosines of a position's pairs, then their sines; pairs are
+    halves' dims, or neighbours when interleaved. positions int32 [N] (default: a token's place in its sequence), or
+    [axes, N] with sections, the numbers of pairs that go by each axis."""
+    import torch
+    lib, i32 = load_library(), torch.int32
+    dt = _kv8_dtype(q, "q")
+    index = q.get_device()
+    qp, kp, vp = (_ptr_of(t, name, q.dtype, index, 3, False) for t, name in ((q, "q"), (k, "k"), (v, "v")))
+    n, heads, d = q.shape
+    hk = k.shape[1]
+    if v.shape != k.shape or k.shape[0] != n or k.shape[2] != d:
+        raise ValueError("k and v must have the same shape, and q's tokens and dims")
+    cp = _ptr_of(cache, "cache", torch.uint8, index, 2)
+    pages, page_bytes = cache.shape
+    if page_bytes != kv8_page_bytes(hk, d):
+        raise ValueError("cache must be [num_pages, kv8_page_bytes(kv_heads, head_dim)]")
+    cup, sp, pp = (_ptr_of(cu_tokens, "cu_tokens", i32, index, 1), _ptr_of(seq_lens, "seq_lens", i32, index, 1),
+                   _ptr_of(page_table, "page_table", i32, index, 2))
+    B = seq_lens.shape[0]
+    if cu_tokens.shape[0] != B + 1 or page_table.shape[0] != B:
+        raise ValueError("shape mismatch")
+    sheet = _ptr_of(cos_sin, "cos_sin", torch.float32, index, 2)
+    weights = []
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        weights.append(None if t is None else _ptr_of(t, name, q.dtype, index, 1))
+        if t is not None and t.shape[0] != d:
+            raise ValueError(f"{name} must have head_dim entries")
+    axes, at, step, parts = 1, None, 0, None
+    if positions is not None:
+        at = _ptr_of(positions, "positions", i32, index, positions.dim(), False)
+        if positions.dim() not in (1, 2) or positions.shape[-1] != n or (n > 1 and positions.stride(-1) != 1):
+            raise ValueError("positions must be [N] or [axes, N], its last axis contiguous")
+        if positions.dim() == 2:
+            axes, step = positions.shape[0], positions.stride(0) if positions.shape[0] > 1 else 0
+    if axes > 1:
+        if sections is None or len(sections) != axes:
+            raise ValueError("sections must have one entry per axis of positions")
+        parts = _int_array(tuple(int(x) for x in sections))
+    fresh = None
+    if q_out is None:
+        with _taken_on(stream):
+            q_out = fresh = torch.empty((n, heads, d), dtype=q.dtype, device=q.device)
+    op = _ptr_of(q_out, "q_out", q.dtype, index, 3, False)
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    (q0, q1), (k0, k1), (v0, v1), (o0, o1) = (_rows(t, n) for t in (q, k, v, q_out))
+    rc = lib.kv8_append_rope(qp, q0, q1, kp, k0, k1, vp, v0, v1, dt, n, cup, sp, pp, page_table.shape[1], B, heads, hk, d, *weights,
+                             float(eps), sheet, *cos_sin.shape, 1 if interleaved else 0, at, step, parts, axes, op, o0, o1, cp,
+                             pages, _status_ptr(dev_status, index), _raw_stream(stream, index))
+    if rc != 0:
+        raise NvFp4MlaError(rc, "kv8_append_rope")
+    _keep(stream, fresh)
+    return q_out
+
+
 def kv8_decode_workspace_size(B: int, Q: int, H: int, kv_heads: int, head_dim: int, num_sms: int = 0) -> int:
     return int(load_library().kv8_decode_workspace_size(B, Q, H, kv_heads, head_dim, num_sms))
 
 
-def kv8_decode(q, cache, page_table, seq_lens, kv_heads: int, softmax_scale, window: int = 0, out=None, lse=None,
-               workspace=None, dev_status=None, max_ctas: int = 0, stream=None, test_timeout: bool = False):
-    """Attention of each request's Q newest tokens over its cached tokens: q bf16 or fp16 [B, Q, H, head_dim]
-    (batch and query axes of one stride, any head stride), cache uint8 [P, kv8_page_bytes], page_table int32
-    [B, max_pages], seq_lens int32 [B]; window > 0: the newest `window` positions only. Returns (out as q's
-    type [B, Q, H, head_dim], lse fp32 [B, Q, H]). A step of no requests (B = 0) enqueues nothing."""
+def _decode(name, call, size_of, q, cache, page_table, seq_lens, masks, kv_heads, softmax_scale, window, out, lse, workspace,
+            dev_status, max_ctas, stream, test_timeout):
     import torch
-    lib, i32 = load_library(), torch.int32
+    i32 = torch.int32
     dt = _kv8_dtype(q, "q")
     index = q.get_device()
     qp = _ptr_of(q, "q", q.dtype, index, 4, False)
@@ -579,7 +666,7 @@ def kv8_decode(q, cache, page_table, seq_lens, kv_heads: int, softmax_scale, win
         if lse is None:
             lse = fresh[1] = torch.empty((B, Q, H), dtype=torch.float32, device=q.device)
         if workspace is None:
-            workspace = torch.empty(max(kv8_decode_workspace_size(B, Q, H, kv_heads, d), 1), dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(max(size_of(B, Q, H, kv_heads, d), 1), dtype=torch.uint8, device=q.device)
         elif not workspace.is_contiguous():
             raise ValueError("workspace: must be contiguous")
     op, lp = _ptr_of(out, "out", q.dtype, index, 4), _ptr_of(lse, "lse", torch.float32, index, 3)
@@ -587,17 +674,132 @@ def kv8_decode(q, cache, page_table, seq_lens, kv_heads: int, softmax_scale, win
         raise ValueError("out must be [B, Q, H, head_dim] and lse [B, Q, H]")
     if not 0 <= window < 1 << 31:
         raise ValueError("window must be 0 (none) or a number of positions below 2^31")
+    more = ()
+    if masks is not None:
+        more = (_ptr_of(masks, "masks", torch.int64, index, 2),)
+        if masks.shape != shape[:2]:
+            raise ValueError("masks must be [B, Q]")
     if B == 0:
         return out, lse
-    rc = lib.kv8_decode(qp, s1 if Q > 1 else s0 if B > 1 else 0, s2 if H > 1 else 0, dt, cp, pages, pp, max_pages, sp,
-                        B, Q, H, kv_heads, d, float(softmax_scale), int(window), op, lp, workspace.data_ptr(),
-                        workspace.nbytes,
-                        _status_ptr(dev_status, index),
-                        (int(max_ctas) & 0xFFFF) | (FLAG_TEST_TIMEOUT if test_timeout else 0), _raw_stream(stream, index))
+    rc = call(qp, s1 if Q > 1 else s0 if B > 1 else 0, s2 if H > 1 else 0, dt, cp, pages, pp, max_pages, sp, *more,
+              B, Q, H, kv_heads, d, float(softmax_scale), int(window), op, lp, workspace.data_ptr(), workspace.nbytes,
+              _status_ptr(dev_status, index),
+              (int(max_ctas) & 0xFFFF) | (FLAG_TEST_TIMEOUT if test_timeout else 0), _raw_stream(stream, index))
     if rc != 0:
-        raise NvFp4MlaError(rc, "kv8_decode")
+        raise NvFp4MlaError(rc, name)
     _keep(stream, *fresh)
     return out, lse
+
+
+def kv8_decode(q, cache, page_table, seq_lens, kv_heads: int, softmax_scale, window: int = 0, out=None, lse=None,
+               workspace=None, dev_status=None, max_ctas: int = 0, stream=None, test_timeout: bool = False):
+    """Attention of each request's Q newest tokens over its cached tokens: q bf16 or fp16 [B, Q, H, head_dim]
+    (batch and query axes of one stride, any head stride), cache uint8 [P, kv8_page_bytes], page_table int32
+    [B, max_pages], seq_lens int32 [B]; window > 0: the newest `window` positions only. Returns (out as q's
+    type [B, Q, H, head_dim], lse fp32 [B, Q, H]). A step of no requests (B = 0) enqueues nothing."""
+    return _decode("kv8_decode", load_library().kv8_decode, kv8_decode_workspace_size, q, cache, page_table, seq_lens, None, kv_heads,
+                   softmax_scale, window, out, lse, workspace, dev_status, max_ctas, stream, test_timeout)
+
+
+# ------------------------------------------------------------------ a speculative step over the 8-bit cache
+def kv8_decode_tree_workspace_size(B: int, Q: int, H: int, kv_heads: int, head_dim: int, num_sms: int = 0) -> int:
+    return int(load_library().kv8_decode_tree_workspace_size(B, Q, H, kv_heads, head_dim, num_sms))
+
+
+def kv8_decode_tree(q, cache, page_table, seq_lens, masks, kv_heads: int, softmax_scale, window: int = 0, out=None, lse=None,
+                    workspace=None, dev_status=None, max_ctas: int = 0, stream=None, test_timeout: bool = False):
+    """kv8_decode for trees of up to 64 nodes, the Q newest tokens of each request: masks int64 [B, Q], bit i of node j's:
+    it attends to node i (its ancestors and itself; 0: padding, out 0 and lse -inf). All nodes attend to what lies before
+    the tree; window (0, or at least Q): as far back as the node's place in the text allows."""
+    return _decode("kv8_decode_tree", load_library().kv8_decode_tree, kv8_decode_tree_workspace_size, q, cache, page_table, seq_lens,
+                   masks, kv_heads, softmax_scale, window, out, lse, workspace, dev_status, max_ctas, stream, test_timeout)
+
+
+def spec_verify_workspace_size(B: int, Q: int, V: int) -> int:
+    return int(load_library().spec_verify_workspace_size(B, Q, V))
+
+
+def spec_verify(logits, drafts, parents, uniforms, temperatures=None, draft_probs=None, tokens=None, path=None, accepted=None,
+                workspace=None, dev_status=None, stream=None):
+    """Which drafts the target accepts: logits bf16, fp16 or fp32 [B, Q, V] (any row stride), drafts and parents int32
+    [B, Q] (-1: no node), uniforms fp32 [B, Q], temperatures fp32 [B] (0: greedy; default 1), draft_probs fp32
+    [B, Q, V]: what a node's children were drawn from (default: drafts that were chosen, not drawn). Returns int32 tokens
+    [B, Q] (the accepted drafts' and the next token, then -1), path [B, Q] (the accepted nodes, then -1) and
+    accepted [B]. A step of no requests (B = 0) enqueues nothing."""
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    types = {torch.bfloat16: 0, torch.float16: 1, f32: 2}     # NVFP4MLA_BF16, _FP16, _FP32
+    if logits.dtype not in types:
+        raise TypeError(f"logits: expected torch.bfloat16, torch.float16 or torch.float32, got {logits.dtype}")
+    index = logits.get_device()
+    lp = _ptr_of(logits, "logits", logits.dtype, index, 3, False)
+    pp = None if draft_probs is None else _ptr_of(draft_probs, "draft_probs", f32, index, 3, False)
+    B, Q, V = logits.shape
+    if draft_probs is not None and draft_probs.shape != logits.shape:
+        raise ValueError("draft_probs must have logits' shape")
+    steps = []
+    for t in (logits, draft_probs):
+        s0, s1, s2 = (0, 0, 1) if t is None else t.stride()
+        if (V > 1 and s2 != 1) or (B > 1 and Q > 1 and s0 != Q * s1):
+            raise ValueError("logits and draft_probs must be contiguous along the vocabulary, and their batch stride Q times their node stride")
+        steps.append(s1 if Q > 1 else s0 if B > 1 else 0)
+    dp, up, np_ = (_ptr_of(drafts, "drafts", i32, index, 2), _ptr_of(uniforms, "uniforms", f32, index, 2),
+                   _ptr_of(parents, "parents", i32, index, 2))
+    tp = None if temperatures is None else _ptr_of(temperatures, "temperatures", f32, index, 1)
+    if not drafts.shape == parents.shape == uniforms.shape == (B, Q) or (temperatures is not None and temperatures.shape[0] != B):
+        raise ValueError("drafts, parents and uniforms must be [B, Q], temperatures [B]")
+    fresh = [None] * 3
+    with _taken_on(stream if tokens is None or path is None or accepted is None or workspace is None else None):
+        if tokens is None:
+            tokens = fresh[0] = torch.empty((B, Q), dtype=i32, device=logits.device)
+        if path is None:
+            path = fresh[1] = torch.empty((B, Q), dtype=i32, device=logits.device)
+        if accepted is None:
+            accepted = fresh[2] = torch.empty(B, dtype=i32, device=logits.device)
+        if workspace is None:
+            workspace = torch.empty(max(spec_verify_workspace_size(B, Q, V), 1), dtype=torch.uint8, device=logits.device)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace: must be contiguous")
+    outs = [_ptr_of(tokens, "tokens", i32, index, 2), _ptr_of(path, "path", i32, index, 2), _ptr_of(accepted, "accepted", i32, index, 1)]
+    if tokens.shape != (B, Q) or path.shape != (B, Q) or accepted.shape[0] != B:
+        raise ValueError("tokens and path must be [B, Q], accepted [B]")
+    if B == 0:
+        return tokens, path, accepted
+    rc = load_library().spec_verify(lp, steps[0], types[logits.dtype], pp, steps[1], dp, np_, up, tp, B, Q, V, *outs,
+                                    workspace.data_ptr(), workspace.nbytes, _status_ptr(dev_status, index),
+                                    _raw_stream(stream, index))
+    if rc != 0:
+        raise NvFp4MlaError(rc, "spec_verify")
+    _keep(stream, *fresh)
+    return tokens, path, accepted
+
+
+def kv8_keep(cache, page_table, seq_lens, path, accepted, kv_heads: int, head_dim: int, new_lens=None, dev_status=None,
+             stream=None, layered: bool = False):
+    """After a verify step over trees of Q nodes, path int32 [B, Q]: the accepted nodes' keys and values (path[b, i],
+    i < accepted[b]) move up behind node 0, in the cache uint8 [P, kv8_page_bytes] (layered: [layers, P, ...]). accepted
+    int32 [B], below 0: left out. Returns new_lens int32 [B] for kv_pages_trim."""
+    import torch
+    i32 = torch.int32
+    cp, layers, stride, pages, each, index = _pages_of(cache, layered)
+    if each != kv8_page_bytes(kv_heads, head_dim):
+        raise ValueError("cache must be [num_pages, kv8_page_bytes(kv_heads, head_dim)]")
+    pp, sp = _ptr_of(page_table, "page_table", i32, index, 2), _ptr_of(seq_lens, "seq_lens", i32, index, 1)
+    hp, ap = _ptr_of(path, "path", i32, index, 2), _ptr_of(accepted, "accepted", i32, index, 1)
+    B, Q = path.shape
+    fresh = None
+    if new_lens is None:
+        with _taken_on(stream):
+            new_lens = fresh = torch.empty(B, dtype=i32, device=cache.device)
+    np_ = _ptr_of(new_lens, "new_lens", i32, index, 1)
+    if not page_table.shape[0] == seq_lens.shape[0] == accepted.shape[0] == new_lens.shape[0] == B:
+        raise ValueError("page_table, seq_lens, path, accepted and new_lens must have one row per request")
+    rc = load_library().kv8_keep(cp, layers, stride, pages, pp, page_table.shape[1], sp, hp, ap, B, Q, kv_heads, head_dim, np_,
+                                 _status_ptr(dev_status, index), _raw_stream(stream, index))
+    if rc != 0:
+        raise NvFp4MlaError(rc, "kv8_keep")
+    _keep(stream, fresh)
+    return new_lens
 
 
 # ------------------------------------------------------------------ pages
@@ -655,6 +857,20 @@ def kv_pages_free(page_table, seq_lens, refcounts, seqs, dev_status=None, stream
                                       _status_ptr(dev_status, index), _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv_pages_free")
+
+
+def kv_pages_trim(page_table, seq_lens, refcounts, new_lens, dev_status=None, stream=None) -> None:
+    """Sequence s is cut to new_lens[s] tokens (int32 [S]): the pages behind are given back; the tables are updated in
+    place. A new length below 0 or above the present one is refused and counted."""
+    import torch
+    index = page_table.get_device()
+    state = _page_state(page_table, seq_lens, refcounts, index)
+    np_ = _ptr_of(new_lens, "new_lens", torch.int32, index, 1)
+    if new_lens.shape[0] != state[3]:
+        raise ValueError("new_lens must have one entry per sequence")
+    rc = load_library().kv_pages_trim(*state, np_, _status_ptr(dev_status, index), _raw_stream(stream, index))
+    if rc != 0:
+        raise NvFp4MlaError(rc, "kv_pages_trim")
 
 
 def kv_pages_fork(cache, page_table, seq_lens, refcounts, src, dst, new_pages=None, dev_status=None, stream=None,

@@ -1,4 +1,4 @@
-// Internal declarations of the 8-bit per-head cache and of the page operators.
+// Internal declarations of the 8-bit per-head cache, of the speculative step over it and of the page operators.
 #pragma once
 #include "internal.h"
 
@@ -36,6 +36,24 @@ struct AppendParams {
 };
 cudaError_t launch_kv8_append(const AppendParams& p, int head_dim, bool fp16, cudaStream_t stream);
 
+constexpr int kMaxAxes = 4;
+struct RopeParams : AppendParams {
+  const uint16_t* q;
+  int64_t q_token_stride, q_head_stride;
+  uint16_t* q_out;
+  int64_t out_token_stride, out_head_stride;
+  int heads;                     // of q
+  const uint16_t* weight[2];     // of queries' and keys' norms, [D], or null: none
+  float eps;
+  const float* cos_sin;          // [max_positions, rot]: the pairs' cosines, then their sines
+  int64_t max_positions;
+  int rot;                       // dims that are rotated
+  const int32_t* positions;      // [axes, num_tokens], or null: a token's place in its sequence
+  int64_t axis_stride;
+  int axes, ends[kMaxAxes];      // pairs up to ends[a] go by axis a
+};
+cudaError_t launch_kv8_append_rope(const RopeParams& p, int head_dim, bool fp16, bool interleaved, cudaStream_t stream);
+
 struct Kv8DecodeParams {
   CUtensorMap cache_map;         // see encode_pages_map
   const uint16_t* q;
@@ -61,6 +79,47 @@ struct Kv8DecodeParams {
 int kv8_decode_columns(int Q, int group);                      // (query, head) columns of a CTA's tile
 cudaError_t launch_kv8_decode(const Kv8DecodeParams& p, int head_dim, bool fp16, cudaStream_t stream);
 
+struct Kv8TreeParams : Kv8DecodeParams {
+  const uint64_t* masks;         // [B, Q]
+};
+int kv8_tree_columns(int Q, int group);
+cudaError_t launch_kv8_decode_tree(const Kv8TreeParams& p, int head_dim, bool fp16, cudaStream_t stream);
+
+struct KeepParams {
+  uint8_t* cache;
+  int64_t layers, layer_stride, num_pages, page_bytes;
+  const int32_t* page_table;     // [B, max_pages]
+  int64_t max_pages;
+  const int32_t* seq_lens;       // [B]
+  const int32_t* path;           // [B, Q]
+  const int32_t* accepted;       // [B]
+  int B, Q, kv_heads;
+  int32_t* new_lens;             // [B]
+  int32_t* status;
+};
+cudaError_t launch_kv8_keep(const KeepParams& p, int head_dim, cudaStream_t stream);
+
+struct VerifyParams {
+  const void* logits;            // [B, Q, V], rows row_stride elements apart
+  int64_t row_stride;
+  const float* probs;            // [B, Q, V], or null
+  int64_t probs_stride;
+  const int32_t* drafts;         // [B, Q]
+  const int32_t* parents;        // [B, Q]
+  const float* uniforms;         // [B, Q]
+  const float* temperatures;     // [B], or null: 1
+  int B, Q, V;
+  int32_t *tokens, *path;        // [B, Q]
+  int32_t* accepted;             // [B]
+  int32_t* status;
+  int chunks;                    // of a row, at most
+  float2* chunk_ms;              // [B Q, chunks]: largest logit of a chunk, sum of exponentials against it
+  int32_t* chunk_at;             // [B Q, chunks]: where the largest is
+  double* chunk_sum;             // [B, chunks]
+};
+int verify_chunks(int64_t V);
+cudaError_t launch_spec_verify(const VerifyParams& p, int type, cudaStream_t stream);   // type: NVFP4MLA_BF16, _FP16 or _FP32
+
 // The three arrays of the page operators, and the caches whose pages they move.
 struct PageState {
   int32_t* table;                // [num_seqs, max_pages]
@@ -78,6 +137,7 @@ struct PageStore {
 cudaError_t launch_pages_copy(const PageStore& c, int64_t num_pages, const int32_t* src, const int32_t* dst, int64_t n,
                               int32_t* status, cudaStream_t stream);
 cudaError_t launch_pages_free(const PageState& s, const int32_t* seqs, int n, cudaStream_t stream);
+cudaError_t launch_pages_trim(const PageState& s, const int32_t* new_lens, cudaStream_t stream);
 cudaError_t launch_pages_fork(const PageState& s, const PageStore& c, const int32_t* src, const int32_t* dst, int n,
                               int32_t* new_pages, cudaStream_t stream);
 cudaError_t launch_pages_extend(const PageState& s, const int32_t* add, int32_t* granted, cudaStream_t stream);

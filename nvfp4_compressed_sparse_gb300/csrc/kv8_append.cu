@@ -12,10 +12,9 @@
 // 85 % of the measured copy bandwidth, ALU pipe 55 % busy (it makes the codes); 64 requests of one token:
 // 4.2 us, a launch and one chain of loads. Keys and values by one warp instead of two took 64 to 62 us,
 // the path for finite blocks 62 to 40.
-#include <cuda_fp16.h>
-
 #include "../../include/nvfp4mla.h"
 #include "kv8.h"
+#include "kv8_codes.cuh"
 #include "ptx.cuh"
 
 namespace nvfp4mla {
@@ -24,64 +23,6 @@ namespace {
 using namespace ptx;
 
 constexpr int kAppendThreads = 128;    // five such blocks an SM: 37 us (a row above), three of 256 threads 40
-
-// Two 16-bit elements (low half first) -> fp32.
-template <bool kHalf>
-__device__ __forceinline__ float2 widen(uint32_t w) {
-  if constexpr (kHalf) return __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-
-// Two elements as E4M3 of x * mul: nearest even, saturating; kNan: a NaN as 0x7F with its own sign.
-template <bool kHalf, bool kNan>
-__device__ __forceinline__ uint32_t encode2(uint32_t w, float mul) {
-  const float2 x = widen<kHalf>(w);
-  uint32_t r = f32x2_to_e4m3x2(x.x * mul, x.y * mul);
-  if constexpr (kNan) {
-    constexpr uint32_t kInf = kHalf ? 0x7C00u : 0x7F80u;
-    const uint32_t lo = w & 0xFFFFu, hi = w >> 16;
-    if ((lo & 0x7FFFu) > kInf) r = (r & 0xFF00u) | 0x7Fu | ((lo >> 8) & 0x80u);
-    if ((hi & 0x7FFFu) > kInf) r = (r & 0x00FFu) | ((0x7Fu | ((hi >> 8) & 0x80u)) << 8);
-  }
-  return r;
-}
-template <bool kHalf, bool kNan>
-__device__ __forceinline__ uint2 encode8(const uint4& x, float mul) {
-  return make_uint2(__byte_perm(encode2<kHalf, kNan>(x.x, mul), encode2<kHalf, kNan>(x.y, mul), 0x5410),
-                    __byte_perm(encode2<kHalf, kNan>(x.z, mul), encode2<kHalf, kNan>(x.w, mul), 0x5410));
-}
-
-// Largest magnitude (its 16 bits) of four pairs; kFinite: of the finite ones. Magnitudes order as their
-// bits do, infinities and NaN above all.
-template <bool kHalf, bool kFinite>
-__device__ __forceinline__ uint32_t top8(const uint4& x, uint32_t top) {
-  constexpr uint32_t kInf2 = kHalf ? 0x7C007C00u : 0x7F807F80u;
-  const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t a = ws[k] & 0x7FFF7FFFu;
-    if constexpr (kFinite) a &= __vcmpltu2(a, kInf2);
-    top = __vmaxu2(top, a);
-  }
-  return top;
-}
-
-// Two codes times mul (a power of two of at most 1), as codes; NaN codes stay.
-__device__ __forceinline__ uint32_t shrink2(uint32_t two, float mul) {
-  const uint32_t h = e4m3x2_to_f16x2(two);
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  uint32_t r = f32x2_to_e4m3x2(x.x * mul, x.y * mul);
-  if ((two & 0x7Fu) == 0x7Fu) r = (r & 0xFF00u) | (two & 0xFFu);
-  if ((two & 0x7F00u) == 0x7F00u) r = (r & 0x00FFu) | (two & 0xFF00u);
-  return r;
-}
-
-// First block slot of request b: the slots of requests do not overlap, as a request of n tokens
-// touches at most floor((n + 30) / 16) blocks and gets at least floor(n / 16) + 2 slots.
-__device__ __forceinline__ int first_slot(const AppendParams& p, int b) {
-  const int c = __ldg(p.cu + b);
-  return (c < 0 ? 0 : (c > (int)p.num_tokens ? (int)p.num_tokens : c)) / kBlockTokens + 2 * b;
-}
 
 template <int D, bool kHalf>
 __global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const AppendParams p) {
@@ -93,17 +34,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const AppendP
   const int slot = (int)(item / (unsigned)p.kv_heads), head = (int)(item - (unsigned)slot * (unsigned)p.kv_heads);
   if (slot >= p.slots) return;
 
-  // the last request whose first slot is not behind this one: 32 probes a round
-  int lo = 0, hi = p.B;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) >> 5;
-    const int at = lo + lane * step;
-    const unsigned yes = __ballot_sync(0xFFFFFFFFu, at < hi && first_slot(p, at) <= slot) | 1u;
-    const int k = 31 - __clz(yes);
-    lo += k * step;
-    hi = min(hi, lo + step);
-  }
-  const int b = lo;
+  const int b = request_of(p, slot);
   const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), len = __ldg(p.seq_lens + b);
   const int nth = slot - first_slot(p, b);
   const int64_t n = (int64_t)c1 - c0, p0 = len - n;
@@ -144,40 +75,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const AppendP
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     uint8_t* codes = base + kv8_codes_off(p.kv_heads, D, which, head) + quarter * kBlockTokens * D + col8;
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) top = top8<kHalf, false>(w[which][i], top);
-    top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16));
-    // blocks with an infinity or a NaN are rare, and cost three times the instructions
-    const bool finite = top < (kHalf ? 0x7C00u : 0x7F80u);
-    if (!finite) {
-      top = 0;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) top = top8<kHalf, true>(w[which][i], top);
-      top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16));
-    }
-    // amax = m 2^t, 1 <= m < 2, and 448 = 1.75 x 2^8
-    const uint32_t bits = __float_as_uint(widen<kHalf>(top).x);
-    const int t = (int)(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    const uint32_t e = max((uint32_t)max(t, 1), before[which]);
-    const float mul = __uint_as_float((254u - e) << 23);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int row = i * kRows + row0;
-      if (row >= first && row < behind)
-        *reinterpret_cast<uint2*>(codes + row * D) = finite ? encode8<kHalf, false>(w[which][i], mul) : encode8<kHalf, true>(w[which][i], mul);
-    }
-    if (first > 0 && e > before[which]) {
-      const float less = __uint_as_float((127u - min(e - before[which], 126u)) << 23);
-#pragma unroll 1
-      for (int row = row0; row < first; row += kRows) {
-        uint2* at = reinterpret_cast<uint2*>(codes + row * D);
-        const uint2 c = *at;
-        *at = make_uint2(shrink2(c.x & 0xFFFFu, less) | (shrink2(c.x >> 16, less) << 16),
-                         shrink2(c.y & 0xFFFFu, less) | (shrink2(c.y >> 16, less) << 16));
-      }
-    }
-    if (lane == 0) scales[which * kPageBlocks] = (uint8_t)e;
+    put_block<D, kHalf>(w[which], row0, first, behind, before[which], codes, scales + which * kPageBlocks);
   }
 }
 

@@ -1,4 +1,4 @@
-// Page operators: copy, free, fork, extend and compact the pages of a paged cache.
+// Page operators: copy, free, trim, fork, extend and compact the pages of a paged cache.
 //
 // The tables are small and the pages large, so each call is a planning kernel over the counts and
 // tables and, where pages move, a copy grid over their bytes that follows it as a dependent launch.
@@ -85,6 +85,32 @@ __global__ void __launch_bounds__(256) free_kernel(const PageState s, const int3
     if (row[i] == -1) continue;
     const int32_t page = atomicExch(row + i, -1);
     if (page == -1) continue;
+    if (page < 0 || page >= s.num_pages) {
+      count_bad(s.status, NVFP4MLA_STAT_BAD_PAGE);
+    } else if (atomicSub(s.refs + page, 1) <= 0) {
+      atomicAdd(s.refs + page, 1);
+      count_bad(s.status, NVFP4MLA_STAT_BAD_PAGE);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ trim
+// A block a sequence, whose thread reads the one entry that most trims give back, if any.
+__global__ void __launch_bounds__(32) trim_kernel(const PageState s, const int32_t* new_lens) {
+  const int seq = blockIdx.x;
+  const int len = s.lens[seq], now = new_lens[seq];
+  if (now < 0 || now > len) {
+    if (threadIdx.x == 0) count_bad(s.status, NVFP4MLA_STAT_BAD_SLOT);
+    return;
+  }
+  if (now == len) return;
+  __syncwarp();                        // (new_lens may be lens itself)
+  if (threadIdx.x == 0) s.lens[seq] = now;
+  int32_t* row = s.table + (int64_t)seq * s.max_pages;
+  const int64_t end = min(((int64_t)len + kPageTokens - 1) / kPageTokens, s.max_pages);
+  for (int64_t i = ((int64_t)now + kPageTokens - 1) / kPageTokens + threadIdx.x; i < end; i += 32) {
+    const int32_t page = row[i];
+    row[i] = -1;
     if (page < 0 || page >= s.num_pages) {
       count_bad(s.status, NVFP4MLA_STAT_BAD_PAGE);
     } else if (atomicSub(s.refs + page, 1) <= 0) {
@@ -643,6 +669,11 @@ cudaError_t launch_pages_copy(const PageStore& c, int64_t num_pages, const int32
 cudaError_t launch_pages_free(const PageState& s, const int32_t* seqs, int n, cudaStream_t stream) {
   const int64_t parts = (s.max_pages + 1023) / 1024;
   free_kernel<<<dim3((unsigned)n, (unsigned)(parts < 64 ? parts : 64)), 256, 0, stream>>>(s, seqs);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_trim(const PageState& s, const int32_t* new_lens, cudaStream_t stream) {
+  trim_kernel<<<(unsigned)s.num_seqs, 32, 0, stream>>>(s, new_lens);
   return cudaGetLastError();
 }
 
