@@ -614,7 +614,7 @@ size_t kv8_decode_tree_workspace_size(int B, int Q, int H, int kv_heads, int hea
  * kv8_decode_tree: kv8_decode for trees. With base = seq_lens[b] - Q, node j of request b attends to the
  * positions t >= 0 with
  *   t < base, and t > place - window when window > 0, place = base + (bits of its mask) - 1 being its place
- *   in the text; or t = base + i, i < Q, with bit i of masks[b, j] set (its ancestors and itself)
+ *   in the text (base at least); or t = base + i, i < Q, with bit i of masks[b, j] set (its ancestors and itself)
  * A mask of 0 is padding: such a node attends to nothing, its out is 0 and its lse -inf. Bits from Q on are
  * not looked at, but a mask of those alone is not 0.
  *

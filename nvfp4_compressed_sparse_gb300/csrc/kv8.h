@@ -82,7 +82,7 @@ cudaError_t launch_kv8_decode(const Kv8DecodeParams& p, int head_dim, bool fp16,
 struct Kv8TreeParams : Kv8DecodeParams {
   const uint64_t* masks;         // [B, Q]
 };
-int kv8_tree_columns(int Q, int group);
+int kv8_tree_columns();                                         // (node, head) columns of a CTA's tile
 cudaError_t launch_kv8_decode_tree(const Kv8TreeParams& p, int head_dim, bool fp16, cudaStream_t stream);
 
 struct KeepParams {

@@ -141,16 +141,16 @@ int kv8_append_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride
 }
 
 // Workspace: partial O [2 ctas, columns, D] f32 | partial (maximum, sum) [2 ctas, columns, 2] f32 |
-// arrival counts [ctas] u64; each part 256-byte aligned.
+// arrival counts [ctas] u64, or three words a CTA that say what is to be joined; each part 256-byte aligned.
 struct Kv8Workspace {
   size_t ml, arrived, total;
 };
 static size_t align256(size_t x) { return (x + 255) / 256 * 256; }
-static Kv8Workspace decode_workspace(int columns, int head_dim, int ctas) {
+static Kv8Workspace decode_workspace(int columns, int head_dim, int ctas, int words = 1) {
   Kv8Workspace w;
   w.ml = align256((size_t)2 * ctas * columns * head_dim * sizeof(float));
   w.arrived = w.ml + align256((size_t)2 * ctas * columns * 2 * sizeof(float));
-  w.total = w.arrived + align256((size_t)ctas * sizeof(uint64_t));
+  w.total = w.arrived + align256((size_t)ctas * words * sizeof(uint64_t));
   return w;
 }
 
@@ -173,6 +173,21 @@ static bool encode_pages_map(CUtensorMap* map, const void* cache, int64_t num_pa
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The cache as rows of head_dim bytes: [pages][heads of keys, then of values][64 tokens]. One box is a head's keys of one
+// page, swizzled as the tensor cores read rows of that size.
+static bool encode_rows_map(CUtensorMap* map, const void* cache, int64_t num_pages, int64_t page_bytes, int kv_heads,
+                            int head_dim) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)2 * kv_heads * kPageTokens, (cuuint64_t)num_pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)head_dim, (cuuint64_t)page_bytes};
+  const cuuint32_t box[3] = {(cuuint32_t)head_dim, (cuuint32_t)kPageTokens, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(cache), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 static bool decode_sizes_ok(int B, int Q, int H, int kv_heads, int head_dim) {
   if (!kv8_sizes_ok(kv_heads, head_dim) || B < 1 || Q < 1 || Q > 16 || H < 1 || H % kv_heads != 0) return false;
   return H / kv_heads <= kMaxGroup;
@@ -185,12 +200,13 @@ size_t kv8_decode_workspace_size(int B, int Q, int H, int kv_heads, int head_dim
   return decode_workspace(kv8_decode_columns(Q, H / kv_heads), head_dim, num_sms).total;
 }
 
-// What kv8_decode and kv8_decode_tree have in common, their sizes checked before. columns: of a tile.
+// What kv8_decode and kv8_decode_tree have in common, their sizes checked before: columns and pages of a tile, words of the
+// workspace for each CTA.
 static int check_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype, const void* cache,
                         int64_t num_pages, const int32_t* page_table, int64_t max_pages_per_seq, const int32_t* seq_lens, int B,
                         int Q, int H, int kv_heads, int head_dim, float softmax_scale, int window, void* out, float* lse,
                         void* workspace, size_t workspace_bytes, int32_t* dev_status, uint32_t flags, int columns,
-                        Kv8DecodeParams* to) {
+                        int tile_pages, int words, Kv8DecodeParams* to) {
   if (dtype != NVFP4MLA_BF16 && dtype != NVFP4MLA_FP16) return NVFP4MLA_ERR_INVALID_ARG;
   if (num_pages < 1 || num_pages >= INT32_MAX || max_pages_per_seq < 1 || window < 0) return NVFP4MLA_ERR_INVALID_ARG;
   if (q_token_stride < 0 || q_head_stride < 0) return NVFP4MLA_ERR_INVALID_ARG;
@@ -201,7 +217,7 @@ static int check_decode(const void* q, int64_t q_token_stride, int64_t q_head_st
     return NVFP4MLA_ERR_ALIGNMENT;
   const int sms = device_sm_count();
   if (sms <= 0) return NVFP4MLA_ERR_CUDA;
-  const Kv8Workspace w = decode_workspace(columns, head_dim, sms);
+  const Kv8Workspace w = decode_workspace(columns, head_dim, sms, words);
   if (workspace == nullptr || workspace_bytes < w.total) return NVFP4MLA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return NVFP4MLA_ERR_ALIGNMENT;
   if (!all_device({q, cache, page_table, seq_lens, out, lse, workspace}) || !optional_ok(dev_status))
@@ -209,10 +225,8 @@ static int check_decode(const void* q, int64_t q_token_stride, int64_t q_head_st
   // 32-bit row numbers, and tile numbers of the whole step
   const int64_t units = (int64_t)kv_heads * ((Q * (H / kv_heads) + columns - 1) / columns);
   if ((int64_t)B * Q * H > INT32_MAX || max_pages_per_seq > INT32_MAX) return NVFP4MLA_ERR_UNSUPPORTED;
-  if (max_pages_per_seq / 2 + 16 > INT32_MAX / (B * units)) return NVFP4MLA_ERR_UNSUPPORTED;
+  if (max_pages_per_seq / tile_pages + 16 > INT32_MAX / (B * units)) return NVFP4MLA_ERR_UNSUPPORTED;
   Kv8DecodeParams& p = *to;
-  if (!encode_pages_map(&p.cache_map, cache, num_pages, kv8_page_size(kv_heads, head_dim), kv_heads, head_dim))
-    return NVFP4MLA_ERR_CUDA;
   p.q = static_cast<const uint16_t*>(q);
   p.q_token_stride = q_token_stride;
   p.q_head_stride = q_head_stride;
@@ -251,11 +265,13 @@ int kv8_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, int
   Kv8DecodeParams p{};
   const int rc = check_decode(q, q_token_stride, q_head_stride, dtype, cache, num_pages, page_table, max_pages_per_seq, seq_lens, B, Q, H,
                               kv_heads, head_dim, softmax_scale, window, out, lse, workspace, workspace_bytes, dev_status, flags,
-                              kv8_decode_columns(Q, H / kv_heads), &p);
+                              kv8_decode_columns(Q, H / kv_heads), 2, 1, &p);
   if (rc != NVFP4MLA_OK) return rc;
+  if (!encode_pages_map(&p.cache_map, cache, num_pages, p.page_bytes, kv_heads, head_dim)) return NVFP4MLA_ERR_CUDA;
   return status_of(launch_kv8_decode(p, head_dim, dtype == NVFP4MLA_FP16, static_cast<cudaStream_t>(stream)));
 }
 
+constexpr int kTreeWords = 3;
 static bool tree_sizes_ok(int B, int Q, int H, int kv_heads, int head_dim) {
   if (!kv8_sizes_ok(kv_heads, head_dim) || B < 1 || Q < 1 || Q > NVFP4MLA_MAX_NODES || H < 1 || H % kv_heads != 0) return false;
   return H / kv_heads <= kMaxGroup;
@@ -265,7 +281,7 @@ size_t kv8_decode_tree_workspace_size(int B, int Q, int H, int kv_heads, int hea
   if (!tree_sizes_ok(B, Q, H, kv_heads, head_dim)) return 0;
   if (num_sms <= 0) num_sms = device_sm_count();
   if (num_sms <= 0) return 0;
-  return decode_workspace(kv8_tree_columns(Q, H / kv_heads), head_dim, num_sms).total;
+  return decode_workspace(kv8_tree_columns(), head_dim, num_sms, kTreeWords).total;
 }
 
 int kv8_decode_tree(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype, const void* cache,
@@ -279,9 +295,10 @@ int kv8_decode_tree(const void* q, int64_t q_token_stride, int64_t q_head_stride
   Kv8TreeParams p{};
   const int rc = check_decode(q, q_token_stride, q_head_stride, dtype, cache, num_pages, page_table, max_pages_per_seq, seq_lens, B, Q, H,
                               kv_heads, head_dim, softmax_scale, window, out, lse, workspace, workspace_bytes, dev_status, flags,
-                              kv8_tree_columns(Q, H / kv_heads), &p);
+                              kv8_tree_columns(), 1, kTreeWords, &p);
   if (rc != NVFP4MLA_OK) return rc;
   if (!all_device({masks})) return NVFP4MLA_ERR_INVALID_ARG;
+  if (!encode_rows_map(&p.cache_map, cache, num_pages, p.page_bytes, kv_heads, head_dim)) return NVFP4MLA_ERR_CUDA;
   p.masks = masks;
   return status_of(launch_kv8_decode_tree(p, head_dim, dtype == NVFP4MLA_FP16, static_cast<cudaStream_t>(stream)));
 }

@@ -1,13 +1,42 @@
 // kv8_decode_tree: attention of a tree of drafted tokens over the 8-bit per-head cache.
 //
-// A CTA takes one node and query head: its warps take positions in turn, a lane holding D / 32 dims, each warp with
-// a running maximum, sum and weighted values of its own, which are joined at the end.
+// What it computes. For one request and key/value head the columns (node, head of the group) share every key
+// and value row. 128 of them are the rows of two products over a page of 64 tokens:
+//   S[c, t] = q_c . K[t, :]            z = scale 2^(ek_t - 127) S        (ek, ev: scale bytes)
+//   O[c, d] += sum_t w[c, t] V[t, d]   w = 2^(z log2e - m_c + ev_t - 127 - W_c)
+// with running references m_c of the scores and W_c of the weights, whole numbers, so that raising one scales what
+// has been summed by a power of two, exactly. The softmax's own sum l_c = sum_t 2^(z log2e - m_c) is made of the
+// same exponentials: within a block of 16 tokens they differ from w by one power of two.
+//
+// What bounds it. A tree has some ten times the columns of a plain step: 16 nodes of 8 heads are 128, at which a
+// token costs 2 D bytes and 512 D operations, near the ratio of the tensor cores' rate to the memory's. So:
+//   S  8-bit products, as in kv8_decode: keys are used as they lie in the cache, and a query is a sum of E4M3
+//      numbers (two of a bf16, three of an fp16, the row's largest element at 2^7 to 2^8): what is left after them is
+//      half of E4M3's smallest step, 2^-10, 2^-17 of the largest. The parts are further steps along K: one sum.
+//   O  fp16 products of weights in fp16 and codes, which an fp16 holds exactly. A weight's largest is 2^11 to 2^15,
+//      so half a step is 2^-12 of it, and at the lower end 2^-25 in those units: 2^-40 of the largest. (Weights as
+//      8-bit parts, as kv8_decode has them, need four for that range: twice the tensor time, and some thirty
+//      instructions for a pair of weights where a conversion is one. There the codes need no conversion instead,
+//      which is 2 D a token and does not grow with the columns.)
+//
+// One CTA per SM, persistent; the pages of all (request, key/value head, column tile) units form one sequence, cut
+// into one contiguous range a CTA. Its warps:
+//   0        producer: page numbers, then each page's keys (TMA, swizzled), values (as they lie) and scale bytes
+//   1        issues S = q K;  3: issues O += w V (two threads, so that neither waits for the other)
+//   4-7      feeders: the unit's queries as parts, then each page's values as fp16
+//   8-15     softmax: two streams, which take the pages in turn, a warpgroup each (thread = column, so that maxima
+//            and sums need no exchange). A stream has two buffers of S, w in the place of its S, and its own O, m, W, l
+// A unit that several CTAs share leaves means and sums in the workspace, which join_kernel adds up.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <climits>
+#include <cstddef>
+#include <mutex>
+
 #include "../../include/nvfp4mla.h"
 #include "kv8.h"
-#include "kv8_codes.cuh"
+#include "kv8_units.cuh"
 #include "ptx.cuh"
 
 namespace nvfp4mla {
@@ -15,106 +44,891 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kTreeWarps = 4;
+constexpr int kCols = 128;             // of a unit: (node, head)
+constexpr int kTile = kPageTokens;     // tokens of a stage
+constexpr int kStreams = 2;
+constexpr int kTreeThreads = 512;
+constexpr int kFeeders = 128;          // threads
+constexpr int kSoftmaxThreads = 256;
+constexpr int kUnitCost = 8;           // of a unit, in pages
+constexpr int kMinPages = 4;           // of a CTA, on average
+constexpr float kHeadroom = 4.f;       // log2: how far above the reference a weight's exponent may come
+constexpr float kWeightScale = 11.f;   // log2: weights are held times 2^11: 2^4 above it, one is 2^15 (fp16: 65,504)
+constexpr float kSumHeadroom = 60.f;   // log2: the same for the sum, which fp32 holds
 constexpr unsigned kFull = 0xFFFFFFFFu;
+enum { kBarFeeders = 1, kBarSoftmax = 2 };
 
-__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+template <int D, int kQ>
+struct Shape {
+  static constexpr int kQParts = kQ;
+  static constexpr int kQImage = kCols * D;                     // bytes of a part
+  static constexpr int kQBytes = kQ * kQImage;
+  static constexpr int kCodes = kTile * D;                      // bytes of a page's keys, or values
+  static constexpr int kStageBytes = 2 * kCodes;
+  static constexpr int kVBytes = 2 * kCodes;                    // values as fp16
+  static constexpr int kVBufs = 4;
+  static constexpr int kControl = 13312;
+  static constexpr int kFit = (232448 - 1024 - kControl - kQBytes - kVBufs * kVBytes) / kStageBytes;
+  static constexpr int kStages = kFit < 16 ? kFit : 16;
+  static constexpr uint32_t kSw = D == 128 ? SW_128B : SW_64B;  // of rows of D bytes
+  static constexpr int kOCol = kStreams * 2 * kTile;            // TMEM columns: buffers of S, then O
+  static constexpr uint32_t kTmem = 512;
+  static_assert(kOCol + kStreams * D <= 512 && kStages >= 4, "fits");
+};
+
+template <int kStages, int kVBufs>
+struct Control {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t q_full[2], q_empty, done[2];                // done: softmax has ended a segment
+  uint64_t s_full[kStreams][2], w_full[kStreams][2], o_done[kStreams][2];
+  uint64_t v_full[kVBufs], v_empty[kVBufs];
+  uint64_t drain[2];
+  alignas(16) uint4 scales[kStages];                   // the scale bytes of two neighbouring heads
+  int page_ok[kStages];
+  alignas(16) float f[2][kCols];                       // per segment parity: score of a column per unit of S, log2 units
+  uint64_t mask[2][kCols];
+  int lo[2][kCols];                                    // first position before the tree that a column attends to
+  int row[2][kCols];                                   // of out and lse, -1: no column
+  uint64_t any_mask[2], all_mask[2];                   // nodes that some, and that all of the tree attend to
+  int any_lo[2], all_lo[2];
+  uint32_t poison[2][kCols][4];                        // dims that a NaN value reaches
+  int any_poison[2];
+  float m[kStreams][kCols], w[kStreams][kCols], l[kStreams][kCols];
+  int scan_sum[kTreeThreads / 32];
+  int start_before, start_b;
+  int abort;
+  uint32_t tmem_base;
+};
+
+// What join_kernel is to add up, by the CTA that has a shared unit's first pages.
+struct Shared {
+  int last;                            // CTA, -1: none
+  int slot;                            // of its own part: 0 or 1
+  int b, kvh, ct;
+};
+
+template <bool kHalf>
+__device__ __forceinline__ float2 widen2(uint32_t w) {
+  if constexpr (kHalf) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <bool kHalf>
+__device__ __forceinline__ uint32_t narrow2(float a, float b) {
+  if constexpr (kHalf) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Four E4M3 codes -> two pairs of fp16.
+__device__ __forceinline__ uint2 codes4(uint32_t w) {
+  uint2 r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(w));
+  return r;
+}
+// (a, b) as kParts pairs of E4M3 numbers whose sum they are, but for the last one's rounding. |a|, |b| < 256.
+template <int kParts>
+__device__ __forceinline__ void split(float a, float b, uint32_t (&part)[kParts]) {
+  float2 left = make_float2(a, b);
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) {
+    part[i] = f32x2_to_e4m3x2(left.x, left.y);
+    const uint32_t h = e4m3x2_to_f16x2(part[i]);
+    left = __ffma2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h)), make_float2(-1.f, -1.f), left);
+  }
+}
+// bits lo .. hi - 1 of 64, none if there are none
+__device__ __forceinline__ uint64_t bits(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 64);
+  return lo >= hi ? 0ull : (hi - lo == 64 ? ~0ull : ((1ull << (hi - lo)) - 1) << lo);
+}
+// a tree's nodes, the first of which is position `base`, among the 64 positions from t0 on
+__device__ __forceinline__ uint64_t nodes_at(uint64_t mask, int base, int t0) {
+  const int d = base - t0;
+  return d >= 64 || d <= -64 ? 0ull : (d >= 0 ? mask << d : mask >> -d);
+}
+__device__ __forceinline__ int second_slot(int begin, int pos) { return pos < begin ? 0 : 1; }
+__device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : rcp_approx(sum); }
+
+template <int D, int kQ>
+struct Cta {
+  using S = Shape<D, kQ>;
+  using Ctl = Control<S::kStages, S::kVBufs>;
+  using Walk = ::nvfp4mla::Walk<kTile, kUnitCost>;
+  const Kv8TreeParams& p;
+  uint8_t* stages;
+  uint8_t* qimg;
+  uint8_t* vimg;
+  Ctl* ctl;
+
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return wait_long(ctl, p.status, bar, parity);
+  }
+  static __device__ __noinline__ bool wait_long(Ctl* ctl, int32_t* status, uint64_t* bar, uint32_t parity) {
+    if (mbar_wait(bar, parity, &ctl->abort, kWaitTimeoutNs)) return true;
+    if (atomicExch(&ctl->abort, 1) == 0 && status != nullptr) atomicAdd(status + NVFP4MLA_STAT_TIMEOUT, 1);
+    return false;
+  }
+  __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) { return __all_sync(kFull, wait(bar, parity)); }
+
+  // Counts up to n and round again, with the phase that goes with it.
+  template <int n>
+  struct Ring {
+    uint32_t st = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+      if (++st == (uint32_t)n) {
+        st = 0;
+        phase ^= 1;
+      }
+    }
+  };
+
+  // ---------------------------------------------------------------- producer (warp 0)
+  __device__ __forceinline__ int load_pages(const Walk& w, int i) {
+    const int lane = threadIdx.x & 31;
+    if (i + lane >= w.count) return -1;
+    const int64_t col = (int64_t)w.first + w.at + i + lane;
+    if (col * kPageTokens >= w.len || col >= p.max_pages) return -1;   // behind the table: counted together
+    const int page = p.page_table[(int64_t)w.b * p.max_pages + col];
+    if (page >= 0 && page < p.num_pages) return page;
+    if (w.ct == 0 && w.kvh == 0 && p.status != nullptr) atomicAdd(p.status + NVFP4MLA_STAT_BAD_PAGE, 1);
+    return -1;
+  }
+
+  __device__ void producer(Walk w) {
+    const int lane = threadIdx.x & 31;
+    if (p.withhold) return;
+    Ring<S::kStages> ring;
+    uint32_t g = 0;
+    int pages = w.left > 0 ? load_pages(w, 0) : -1;
+    bool ok = true;
+    while (ok && w.left > 0) {
+      const int kvh = w.kvh;
+      if (w.kvh == 0 && w.ct == 0 && w.at + w.count == w.n && lane == 0 && p.status != nullptr) {
+        const int64_t need = ((int64_t)w.len + kPageTokens - 1) / kPageTokens;
+        const int64_t from = max((int64_t)w.first, p.max_pages);
+        if (need > from) atomicAdd(p.status + NVFP4MLA_STAT_BAD_PAGE, (int)(need - from));
+      }
+      for (int i = 0; ok && i < w.count; i += 32) {
+        const int mine = pages;
+        if (i + 32 < w.count) {
+          pages = load_pages(w, i + 32);
+        } else {
+          Walk nx = w;
+          nx.next(p);
+          pages = nx.left > 0 ? load_pages(nx, 0) : -1;
+        }
+        const int m = min(32, w.count - i);
+        for (int k = 0; ok && k < m; ++k) {
+          const int page = __shfl_sync(kFull, mine, k);
+          if (lane == 0) {
+            ok = wait(&ctl->empty[ring.st], ring.phase ^ 1);
+            if (ok) {
+              uint8_t* to = stages + ring.st * S::kStageBytes;
+              ctl->page_ok[ring.st] = page >= 0;
+              mbar_arrive_expect_tx(&ctl->full[ring.st], page >= 0 ? S::kStageBytes : 0);
+              if (page >= 0) {
+                const uint8_t* at = p.cache + page * p.page_bytes;
+                tma_load_3d(to, &p.cache_map, 0, kvh * kPageTokens, page, &ctl->full[ring.st]);
+                bulk_g2s(to + S::kCodes, at + kv8_codes_off(p.kv_heads, D, 1, kvh), S::kCodes, &ctl->full[ring.st]);
+                cp_async_16(&ctl->scales[ring.st], at + kv8_scales_off(p.kv_heads, D, kvh & ~1));
+              }
+              cp_async_arrive(&ctl->full[ring.st]);
+            }
+          }
+          ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+          if (ok) {
+            ring.next();
+            ++g;
+          }
+        }
+      }
+      if (ok) w.next(p);
+    }
+    if (lane == 0 && (!ok || *reinterpret_cast<volatile int*>(&ctl->abort) != 0)) {
+      // a wait gave up: the copies that are still in flight land (bounded)
+      const uint32_t n = min(g, (uint32_t)S::kStages);
+      for (uint32_t i = 0; i < n; ++i) {
+        const uint32_t t = g - 1 - i;
+        mbar_wait(&ctl->full[t % S::kStages], (t / S::kStages) & 1, nullptr, kWaitTimeoutNs);
+      }
+    }
+    __syncwarp();
+  }
+
+  // ---------------------------------------------------------------- S = q K (warp 1, one thread)
+  __device__ void issue_s(Walk w, uint32_t tmem) {
+    constexpr uint32_t kId = idesc_e4m3(kCols, kTile, false, false);
+    const uint64_t kd = sdesc(smem_u32(stages), 16, 8 * D, S::kSw), qd = sdesc(smem_u32(qimg), 16, 8 * D, S::kSw);
+    Ring<S::kStages> ring;
+    uint32_t uses[kStreams] = {0, 0};
+    bool ok = true;
+    for (uint32_t seg = 0; ok && w.left > 0; ++seg, w.next(p)) {
+      ok = wait(&ctl->q_full[seg & 1], (seg >> 1) & 1);
+      for (int i = 0; ok && i < w.count; ++i) {
+        const int stream = i & 1;
+        const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++, sb = u & 1;
+        ok = wait(&ctl->full[ring.st], ring.phase);
+        ok = ok && wait(&ctl->o_done[stream][sb], ((u >> 1) & 1) ^ 1);   // the buffer's last weights have been used
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (stream * 2 + sb) * kTile, k_lo = (uint32_t)kd + ((ring.st * S::kStageBytes) >> 4);
+#pragma unroll
+        for (int part = 0; part < kQ; ++part)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            const uint32_t q_lo = (uint32_t)qd + ((part * S::kQImage) >> 4) + 2 * k;
+            if (part == 0 && k == 0) umma_f8_ss_w<0>(d, q_lo, (uint32_t)(qd >> 32), k_lo + 2 * k, (uint32_t)(kd >> 32), kId);
+            else umma_f8_ss_w<1>(d, q_lo, (uint32_t)(qd >> 32), k_lo + 2 * k, (uint32_t)(kd >> 32), kId);
+          }
+        umma_commit(&ctl->s_full[stream][sb]);
+        umma_commit(&ctl->empty[ring.st]);
+        ring.next();
+      }
+      if (ok) umma_commit(&ctl->q_empty);
+    }
+    umma_commit(&ctl->drain[0]);
+    mbar_wait(&ctl->drain[0], 0, nullptr, kWaitTimeoutNs);
+  }
+
+  // ---------------------------------------------------------------- O += w V (warp 3, one thread)
+  __device__ void issue_o(Walk w, uint32_t tmem) {
+    constexpr uint32_t kId = idesc_f16(kCols, D, false, true, false);
+    const uint64_t vd = sdesc(smem_u32(vimg), kTile * 128, 1024, SW_128B);
+    Ring<S::kVBufs> ring;
+    uint32_t uses[kStreams] = {0, 0};
+    bool ok = true;
+    for (; ok && w.left > 0; w.next(p)) {
+      for (int i = 0; ok && i < w.count; ++i) {
+        const int stream = i & 1;
+        const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++, sb = u & 1;
+        ok = wait(&ctl->v_full[ring.st], ring.phase);
+        ok = ok && wait(&ctl->w_full[stream][sb], (u >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + S::kOCol + stream * D, a = tmem + (stream * 2 + sb) * kTile;
+        const uint32_t v_lo = (uint32_t)vd + ((ring.st * S::kVBytes) >> 4);
+        umma_ts_w<-1>(d, a, v_lo, (uint32_t)(vd >> 32), kId, i >= kStreams ? 1u : 0u);
+#pragma unroll
+        for (int k = 1; k < kTile / 16; ++k) umma_ts_w<1>(d, a + 8 * k, v_lo + k * 128, (uint32_t)(vd >> 32), kId);
+        umma_commit(&ctl->o_done[stream][sb]);
+        umma_commit(&ctl->v_empty[ring.st]);
+        ring.next();
+      }
+    }
+    umma_commit(&ctl->drain[1]);
+    mbar_wait(&ctl->drain[1], 0, nullptr, kWaitTimeoutNs);
+  }
+
+  // ---------------------------------------------------------------- feeders (warps 4-7)
+  // The unit's queries, and what its columns attend to.
+  template <bool kHalf>
+  __device__ void queries(const Walk& w, uint32_t buf) {
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = 32 / kAtOnce, kAhead = 4;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, sub = lane / kLanes, ch = lane % kLanes;
+    const int ncols = p.Q * p.group, base = w.len - p.Q;
+    auto load = [&](int round) {
+      const int col = w.ct * kCols + warp * 32 + round * kAtOnce + sub;
+      if (round >= kRounds || col >= ncols) return make_uint4(0u, 0u, 0u, 0u);
+      const int j = col / p.group, h = w.kvh * p.group + col - j * p.group;
+      return *reinterpret_cast<const uint4*>(p.q + ((int64_t)w.b * p.Q + j) * p.q_token_stride + h * p.q_head_stride + ch * 8);
+    };
+    const uint64_t* masks = p.masks + (int64_t)w.b * p.Q;
+    const uint64_t bits_of = p.Q == 64 ? ~0ull : (1ull << p.Q) - 1;
+    uint4 v[kAhead];
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) v[r] = load(r);
+    {
+      // a lane a column: what it attends to
+      const int c = warp * 32 + lane, col = w.ct * kCols + c, j = col / p.group;
+      const uint64_t mask = col < ncols ? masks[j] : 0;
+      const int place = base + max(1, __popcll(mask & bits_of)) - 1;
+      ctl->mask[buf][c] = mask & bits_of;
+      ctl->lo[buf][c] = mask == 0 ? INT_MAX : (p.window > 0 ? max(0, place - p.window + 1) : 0);
+      ctl->row[buf][c] = col < ncols ? (w.b * p.Q + j) * p.H + w.kvh * p.group + (col - j * p.group) : -1;
+    }
+    if (warp == 0) {
+      uint64_t some = 0, all = ~0ull;
+      int first = INT_MAX, last = 0;
+      for (int j = lane; j < p.Q; j += 32) {
+        const uint64_t mask = masks[j];
+        if (mask == 0) continue;
+        some |= mask & bits_of;
+        all &= mask & bits_of;
+        const int lo = p.window > 0 ? max(0, base + max(1, __popcll(mask & bits_of)) - p.window) : 0;
+        first = min(first, lo);
+        last = max(last, lo);
+      }
+      const uint32_t some0 = __reduce_or_sync(kFull, (uint32_t)some), some1 = __reduce_or_sync(kFull, (uint32_t)(some >> 32));
+      const uint32_t all0 = __reduce_and_sync(kFull, (uint32_t)all), all1 = __reduce_and_sync(kFull, (uint32_t)(all >> 32));
+      first = __reduce_min_sync(kFull, first);
+      last = __reduce_max_sync(kFull, last);
+      if (lane == 0) {
+        ctl->any_mask[buf] = (uint64_t)some1 << 32 | some0;
+        ctl->all_mask[buf] = ((uint64_t)all1 << 32 | all0) & bits_of;
+        ctl->any_lo[buf] = first;
+        ctl->all_lo[buf] = last;
+      }
+    }
+#pragma unroll 1
+    for (int r = 0; r < kRounds; ++r) {
+      const uint4 x4 = v[0];
+#pragma unroll
+      for (int k = 0; k + 1 < kAhead; ++k) v[k] = v[k + 1];
+      v[kAhead - 1] = load(r + kAhead);
+      const int n = warp * 32 + r * kAtOnce + sub;
+      const uint32_t ws[4] = {x4.x, x4.y, x4.z, x4.w};
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = __vmaxu2(top, ws[k] & 0x7FFF7FFFu);
+      top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+      for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(kFull, top, d));
+      const bool finite = top < (kHalf ? 0x7C00u : 0x7F80u);
+      // the largest magnitude goes to [128, 256): a power of two, exact
+      const int e = (int)(__float_as_uint(widen2<kHalf>(top).x) >> 23) - 127;
+      const int sh = top == 0 || !finite ? 0 : min(7 - e, 126);
+      const float mul = finite ? __uint_as_float((uint32_t)(sh + 127) << 23) : 0.f;
+      uint32_t part[4][kQ];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = widen2<kHalf>(ws[k]);
+        split(finite ? x.x * mul : 0.f, finite ? x.y * mul : 0.f, part[k]);
+      }
+      const int chunk = D == 128 ? ((ch >> 1) ^ (n & 7)) : ((ch >> 1) ^ ((n >> 1) & 3));
+#pragma unroll
+      for (int i = 0; i < kQ; ++i)
+        *reinterpret_cast<uint2*>(qimg + i * S::kQImage + n * D + chunk * 16 + (ch & 1) * 8) =
+            make_uint2(part[0][i] | (part[1][i] << 16), part[2][i] | (part[3][i] << 16));
+      if (ch == 0) ctl->f[buf][n] = finite ? p.scale_log2 * __uint_as_float((uint32_t)(127 - sh) << 23) : __int_as_float(0x7fc00000);
+    }
+  }
+
+  // 16 codes of token t (row r of its page), dims 16 c .. 16 c + 15, as fp16 into the image.
+  __device__ __forceinline__ void put_values(uint8_t* img, const uint4& x, int r, int c) {
+    const uint2 a = codes4(x.x), b = codes4(x.y), d = codes4(x.z), e = codes4(x.w);
+    const uint4 first = make_uint4(a.x, a.y, b.x, b.y), second = make_uint4(d.x, d.y, e.x, e.y);
+    uint8_t* row = img + (c >> 2) * (kTile * 128) + r * 128;
+    const int at = (c & 3) * 2, swap = (c >> 2) & 1;           // (the halves of 64 dims in turn, for the banks' sake)
+    *reinterpret_cast<uint4*>(row + (((at + swap) ^ (r & 7)) << 4)) = swap ? second : first;
+    *reinterpret_cast<uint4*>(row + (((at + 1 - swap) ^ (r & 7)) << 4)) = swap ? first : second;
+  }
+
+  // Row r of a page that not all columns attend to: zeros where none does (it may hold anything), and a NaN is taken out
+  // and noted for those that do.
+  __device__ __noinline__ void clean(uint4& x, int t, int c, bool any, uint32_t buf, int base) {
+    uint8_t* byte = reinterpret_cast<uint8_t*>(&x);
+    if (!any) {
+      x = make_uint4(0u, 0u, 0u, 0u);
+      return;
+    }
+    for (int k = 0; k < 16; ++k) {
+      if ((byte[k] & 0x7F) != 0x7F) continue;
+      byte[k] = 0;
+      const int d = c * 16 + k;
+      for (int n = 0; n < kCols; ++n) {
+        const bool attends = t < base ? t >= ctl->lo[buf][n] : t - base < 64 && ((ctl->mask[buf][n] >> (t - base)) & 1) != 0;
+        if (attends) atomicOr(&ctl->poison[buf][n][d >> 5], 1u << (d & 31));
+      }
+      ctl->any_poison[buf] = 1;
+    }
+  }
+
+  template <bool kHalf>
+  __device__ void feed(Walk w) {
+    constexpr int kChunks = D / 16, kLoads = kTile * kChunks / kFeeders;
+    const int tid = threadIdx.x & 127, lane = threadIdx.x & 31;
+    Ring<S::kStages> ring;
+    Ring<S::kVBufs> vring;
+    bool ok = true;
+    for (uint32_t seg = 0; w.left > 0; ++seg, w.next(p)) {
+      const uint32_t buf = seg & 1;
+      ok = ok && wait_warp(&ctl->q_empty, (seg & 1) ^ 1);              // the products with the last unit's queries are complete
+      ok = ok && wait_warp(&ctl->done[buf], ((seg >> 1) & 1) ^ 1);     // and the unit's before that is written
+      if (ok) {
+        queries<kHalf>(w, buf);
+        fence_proxy_async_smem();
+      }
+      if (bar_any(kBarFeeders, kFeeders, !ok)) return;
+      if (lane == 0) mbar_arrive(&ctl->q_full[buf]);
+      const int base = w.len - p.Q, all_lo = ctl->all_lo[buf], any_lo = ctl->any_lo[buf];
+      for (int i = 0; i < w.count; ++i) {
+        const int t0 = (w.first + w.at + i) * kTile;
+        ok = ok && wait_warp(&ctl->full[ring.st], ring.phase);
+        ok = ok && wait_warp(&ctl->v_empty[vring.st], vring.phase ^ 1);
+        if (!ok) break;
+        const uint8_t* from = stages + ring.st * S::kStageBytes + S::kCodes;
+        uint8_t* img = vimg + vring.st * S::kVBytes;
+        const bool page_ok = ctl->page_ok[ring.st] != 0;
+        uint4 x[kLoads];
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) x[k] = *reinterpret_cast<const uint4*>(from + (tid + k * kFeeders) * 16);
+        if (!(page_ok && t0 >= all_lo && t0 + kTile <= base)) {
+          const uint64_t any = page_ok ? bits(any_lo - t0, base - t0) | nodes_at(ctl->any_mask[buf], base, t0) : 0;
+          const uint64_t all = page_ok ? bits(all_lo - t0, base - t0) | nodes_at(ctl->all_mask[buf], base, t0) : 0;
+#pragma unroll 1
+          for (int k = 0; k < kLoads; ++k) {
+            const int r = (tid + k * kFeeders) / kChunks, c = (tid + k * kFeeders) % kChunks;
+            uint4 y = *reinterpret_cast<const uint4*>(from + (tid + k * kFeeders) * 16);
+            if (((all >> r) & 1) == 0) clean(y, t0 + r, c, ((any >> r) & 1) != 0, buf, base);
+            put_values(img, y, r, c);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kLoads; ++k) put_values(img, x[k], (tid + k * kFeeders) / kChunks, (tid + k * kFeeders) % kChunks);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ctl->v_full[vring.st]);
+          mbar_arrive(&ctl->empty[ring.st]);
+        }
+        ring.next();
+        vring.next();
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- softmax (warps 8-15)
+  template <bool kHalf>
+  __device__ void softmax(Walk w, uint32_t tmem, const Ranges& ranges, Shared* shared) {
+    const int stream = (threadIdx.x >> 7) - 2, warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, r = threadIdx.x & 127;
+    const uint32_t quarter = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t o_at = quarter + S::kOCol + stream * D;
+    const int t_first = ranges.begin(blockIdx.x);
+    uint32_t g = 0, u = 0;                               // stages before this segment; this stream's pages
+    for (uint32_t seg = 0; w.left > 0; ++seg, w.next(p)) {
+      const uint32_t buf = seg & 1;
+      bool ok = wait_warp(&ctl->q_full[buf], (seg >> 1) & 1);
+      const int base = w.len - p.Q, all_lo = ctl->all_lo[buf];
+      const float f = ctl->f[buf][r];
+      const int row = ctl->row[buf][r], lo = ctl->lo[buf][r];
+      const bool idle = __all_sync(kFull, row < 0);      // no column of this warp
+      float m = 0.f, top_w = 0.f, l = 0.f;
+      bool any = false;
+      for (int i = stream; i < w.count; i += kStreams) {
+        const uint32_t gt = g + i, st = gt % S::kStages, sb = u & 1;
+        const int t0 = (w.first + w.at + i) * kTile;
+        ok = ok && wait_warp(&ctl->full[st], (gt / S::kStages) & 1);
+        ok = ok && wait_warp(&ctl->s_full[stream][sb], (u >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const bool page_ok = ctl->page_ok[st] != 0;
+        const uint2 sc = reinterpret_cast<const uint2*>(&ctl->scales[st])[w.kvh & 1];
+        const uint32_t s_at = quarter + (stream * 2 + sb) * kTile;
+        if (!idle) {
+          uint32_t s[2][32];
+          tmem_ld32(s_at, s[0]);
+          tmem_ld32(s_at + 32, s[1]);
+          tmem_wait_ld();
+          const bool whole = page_ok && t0 >= all_lo && t0 + kTile <= base;
+          uint64_t mine = ~0ull;
+          if (!whole) {
+            mine = page_ok ? bits(lo == INT_MAX ? 64 : lo - t0, base - t0) | nodes_at(ctl->mask[buf][r], base, t0) : 0;
+#pragma unroll
+            for (int k = 0; k < kTile; ++k)
+              if (((k < 32 ? (uint32_t)mine : (uint32_t)(mine >> 32)) >> (k & 31) & 1) == 0) s[k >> 5][k & 31] = 0xff800000u;
+          }
+          // the blocks' largest scores, and with their values' scales
+          float c[4], ev[4], z[4], mz = neg_inf(), mw = neg_inf(), ev_min;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            c[b] = f * __uint_as_float(((sc.x >> (8 * b)) & 0xFFu) << 23);
+            ev[b] = (float)((int)((sc.y >> (8 * b)) & 0xFFu) - 127);
+            float x = neg_inf();
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) x = max3(x, __uint_as_float(s[b >> 1][(b & 1) * 16 + k]), __uint_as_float(s[b >> 1][(b & 1) * 16 + k + 1]));
+            z[b] = x == neg_inf() ? x : x * c[b];
+            mz = fmaxf(mz, z[b]);
+            mw = fmaxf(mw, (z[b] - m) + ev[b]);
+          }
+          ev_min = fminf(fminf(ev[0], ev[1]), fminf(ev[2], ev[3]));
+          const bool raise = any ? mw > top_w + kHeadroom || mz > m + kSumHeadroom : mz > neg_inf();
+          if (__any_sync(kFull, raise)) {
+            // rare after the first pages: new references, this page's own where those are larger
+            float scale_o = 1.f;
+            if (raise) {
+              const float m1 = any ? fmaxf(m, ceilf(mz)) : ceilf(mz);
+              float w1 = neg_inf();
+#pragma unroll
+              for (int b = 0; b < 4; ++b) w1 = fmaxf(w1, ceilf((z[b] - m1) + ev[b]));
+              if (any) {
+                w1 = fmaxf(w1, top_w + (m - m1));
+                scale_o = ex2_approx((m - m1) + (top_w - w1));
+                l *= ex2_approx(m - m1);
+              }
+              m = m1;
+              top_w = w1;
+              any = true;
+            }
+            if (i >= kStreams && __any_sync(kFull, scale_o != 1.f)) {
+              // O is at rest once the product before is complete
+              ok = wait_warp(&ctl->o_done[stream][sb ^ 1], ((u - 1) >> 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int k = 0; k < D; k += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_at + k, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * scale_o);
+                tmem_st16(o_at + k, o);
+              }
+              tmem_wait_st();
+            }
+          }
+          uint32_t out[32];
+          // One exponential serves w and l where fp32 holds the one beside the other: the smallest that matters to l,
+          // 2^-40, has a weight above 2^-120.
+          if (__builtin_expect(whole && !__any_sync(kFull, fabsf(m) >= 1048576.f || top_w - ev_min > 80.f), 1)) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const float2 cc = make_float2(c[b], c[b]);
+              const float k0 = (ev[b] - top_w + kWeightScale) - m;     // whole numbers: exact
+              const float2 kk = make_float2(k0, k0);
+              float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                const float2 a = __ffma2_rn(pair_of(s[b >> 1], (b & 1) * 16 + k), cc, kk);
+                const float2 e = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+                sum = __fadd2_rn(sum, e);
+                out[b * 8 + k / 2] = narrow2<true>(e.x, e.y);
+              }
+              l = fmaf(sum.x + sum.y, ex2_approx(top_w - kWeightScale - ev[b]), l);
+            }
+          } else {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                float e[2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                  const int at = b * 16 + k + n;
+                  const bool in = ((at < 32 ? (uint32_t)mine : (uint32_t)(mine >> 32)) >> (at & 31) & 1) != 0;
+                  const float d = __fadd_rn(__fmul_rn(__uint_as_float(s[at >> 5][at & 31]), c[b]), -m);
+                  l += in ? ex2_approx(d) : 0.f;
+                  e[n] = in ? ex2_approx(d + (ev[b] - top_w + kWeightScale)) : 0.f;
+                }
+                out[b * 8 + k / 2] = narrow2<true>(e[0], e[1]);
+              }
+            }
+          }
+          tmem_st32(s_at, out);
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ctl->empty[st]);
+          mbar_arrive(&ctl->w_full[stream][sb]);
+        }
+        ++u;
+      }
+      // ---- the segment's end: both streams' columns, half of the dims each
+      const int n = w.count;
+      if (ok && n > stream) ok = wait_warp(&ctl->o_done[stream][(u - 1) & 1], ((u - 1) >> 1) & 1);
+      ctl->m[stream][r] = any ? m : kNone;
+      ctl->w[stream][r] = top_w - kWeightScale;
+      ctl->l[stream][r] = l;
+      tc_fence_before();
+      if (bar_any(kBarSoftmax, kSoftmaxThreads, !ok)) return;
+      tc_fence_after();
+      g += n;
+      const bool pad = row < 0 || lo == INT_MAX;         // a padding node's column: whatever was summed is not wanted
+      float top = kNone, sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kStreams; ++k) top = fmaxf(top, ctl->m[k][r]);
+#pragma unroll
+      for (int k = 0; k < kStreams; ++k) sum += ctl->l[k][r] * ratio(ctl->m[k][r], top);
+      if (pad) {
+        top = kNone;
+        sum = 0.f;
+      }
+      // what O is multiplied by makes it the weighted mean at once, in two factors that stay far from fp32's ends
+      const int up = max(0, min(126, (int)((__float_as_uint(sum) >> 23) & 0xFFu) - 127));
+      const float inv = inverse(sum * __uint_as_float((uint32_t)(127 - up) << 23));
+      float2 factor[kStreams];
+#pragma unroll
+      for (int k = 0; k < kStreams; ++k) {
+        const float half = ex2_approx(0.5f * ((ctl->m[k][r] - top) + ctl->w[k][r] - (float)up));
+        factor[k] = make_float2(half * inv, half);
+      }
+      const bool poisoned = ctl->any_poison[buf] != 0, full_unit = w.whole();
+      const int slot = 2 * (int)blockIdx.x + second_slot(t_first, w.pos);
+      if (!idle) {
+#pragma unroll 1
+        for (int k0 = 0; k0 < D / 2; k0 += 16) {
+          const int d0 = stream * (D / 2) + k0;
+          uint32_t a[16], b[16];
+          tmem_ld16(quarter + S::kOCol + d0, a);
+          if (n > 1) tmem_ld16(quarter + S::kOCol + D + d0, b);
+          tmem_wait_ld();
+          float o[16];
+          const uint32_t bad = poisoned ? ctl->poison[buf][r][d0 >> 5] >> (d0 & 31) : 0u;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            o[k] = __uint_as_float(a[k]) * factor[0].x * factor[0].y;
+            if (n > 1) o[k] = fmaf(__uint_as_float(b[k]) * factor[1].x, factor[1].y, o[k]);
+            if (pad) o[k] = 0.f;
+            if ((bad >> k) & 1) o[k] = __int_as_float(0x7fc00000);
+          }
+          if (row >= 0) {
+            if (full_unit) {
+              uint4* to = reinterpret_cast<uint4*>(p.out + (int64_t)row * D + d0);
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                to[k] = make_uint4(narrow2<kHalf>(o[8 * k], o[8 * k + 1]), narrow2<kHalf>(o[8 * k + 2], o[8 * k + 3]),
+                                   narrow2<kHalf>(o[8 * k + 4], o[8 * k + 5]), narrow2<kHalf>(o[8 * k + 6], o[8 * k + 7]));
+            } else {
+              float4* to = reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * kCols + r) * D + d0);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            }
+          }
+        }
+        if (stream == 0 && row >= 0) {
+          if (full_unit) p.lse[row] = sum == 0.f ? neg_inf() : (top + log2f(sum)) * 0.69314718055994530942f;
+          else reinterpret_cast<float2*>(p.part_ml)[slot * kCols + r] = make_float2(top, sum);
+        }
+      }
+      if (!full_unit && w.at == 0 && threadIdx.x == 256)
+        *shared = Shared{ranges.of(w.pos + kUnitCost + w.n - 1), second_slot(t_first, w.pos), w.b, w.kvh, w.ct};
+      tc_fence_before();
+      bar_sync(kBarSoftmax, kSoftmaxThreads);            // all have read O, the notes of NaN and each other's sums
+      if (poisoned) {
+        if (stream == 0)
+          for (int k = 0; k < 4; ++k) ctl->poison[buf][r][k] = 0;
+        if (threadIdx.x == 256) ctl->any_poison[buf] = 0;
+        bar_sync(kBarSoftmax, kSoftmaxThreads);
+      }
+      if (lane == 0) mbar_arrive(&ctl->done[buf]);
+    }
+  }
+};
 
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(kTreeWarps * 32) tree_kernel(const __grid_constant__ Kv8TreeParams p) {
-  constexpr int kN = D / 32;
-  __shared__ float acc_of[kTreeWarps][D], m_of[kTreeWarps], l_of[kTreeWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = blockIdx.x;
-  const int h = (int)(row % p.H), kvh = h / p.group;
-  const int64_t node = row / p.H;
-  const int b = (int)(node / p.Q);
-  const int len = max(0, p.seq_lens[b]), base = len - p.Q;
-  const uint64_t mask = p.masks[node], used = p.Q == 64 ? mask : mask & ((1ull << p.Q) - 1);
-  const int place = base + __popcll(used) - 1;
-  const int64_t from = p.window > 0 ? (int64_t)place - p.window + 1 : 0;
-  float q[kN];
-  bool finite = true;
-#pragma unroll
-  for (int k = 0; k < kN; ++k) {
-    const uint16_t x = p.q[node * p.q_token_stride + h * p.q_head_stride + lane * kN + k];
-    q[k] = widen<kHalf>(x).x;
-    finite = finite && fabsf(q[k]) < __int_as_float(0x7f800000);
-  }
-  finite = __all_sync(kFull, finite);
-  float m = neg_inf(), l = 0.f, acc[kN] = {};
-  for (int t = warp; t < len; t += kTreeWarps) {
-    if (mask == 0 || (t < base ? t < from : ((used >> (t - base)) & 1) == 0)) continue;
-    const int col = t / kPageTokens, r = t % kPageTokens;
-    const int page = col < p.max_pages ? p.page_table[(int64_t)b * p.max_pages + col] : -1;
-    if (page < 0 || page >= p.num_pages) continue;
-    const uint8_t* at = p.cache + page * p.page_bytes;
-    const uint8_t* sc = at + kv8_scales_off(p.kv_heads, D, kvh) + r / kBlockTokens;
-    const float ks = __uint_as_float((uint32_t)sc[0] << 23), vs = __uint_as_float((uint32_t)sc[4] << 23);
-    const uint8_t* kc = at + kv8_codes_off(p.kv_heads, D, 0, kvh) + r * D + lane * kN;
-    const uint8_t* vc = at + kv8_codes_off(p.kv_heads, D, 1, kvh) + r * D + lane * kN;
-    float z = 0.f, v[kN];
-#pragma unroll
-    for (int k = 0; k < kN; k += 2) {
-      const uint32_t kh = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(kc + k)), vh = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(vc + k));
-      const float2 a = widen<true>(kh), c = widen<true>(vh);
-      z = fmaf(a.x, q[k], fmaf(a.y, q[k + 1], z));
-      v[k] = c.x;
-      v[k + 1] = c.y;
+__global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_constant__ Kv8TreeParams p) {
+  constexpr int kQ = kHalf ? 3 : 2;
+  using S = Shape<D, kQ>;
+  using Ctl = Control<S::kStages, S::kVBufs>;
+  static_assert(sizeof(Ctl) <= S::kControl, "the control block fits its share");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qimg = stages + S::kStages * S::kStageBytes;
+  uint8_t* vimg = qimg + S::kQBytes;
+  Ctl* ctl = reinterpret_cast<Ctl*>(vimg + S::kVBufs * S::kVBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 64) {
+    prefetch_tensormap(&p.cache_map);
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&ctl->full[i], 2);                     // the codes' bytes, the scale bytes
+      mbar_init(&ctl->empty[i], 1 + 4 + 4);            // S, the feeders, the stream's softmax
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(kFull, z, d);
-    z = finite ? z * (p.scale_log2 * ks) : __int_as_float(0x7fc00000);
-    const float now = fmaxf(m, z);
-    const float keep = m == now ? 1.f : ex2_approx(m - now), w = z == now ? 1.f : ex2_approx(z - now);
-    l = l * keep + w;
-#pragma unroll
-    for (int k = 0; k < kN; ++k) acc[k] = acc[k] * keep + w * (v[k] * vs);
-    m = now;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->q_full[i], 4);
+      mbar_init(&ctl->done[i], kSoftmaxThreads / 32);
+      mbar_init(&ctl->drain[i], 1);
+      ctl->any_poison[i] = 0;
+    }
+    mbar_init(&ctl->q_empty, 1);
+    for (int i = 0; i < kStreams; ++i)
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(&ctl->s_full[i][k], 1);
+        mbar_init(&ctl->w_full[i][k], 4);
+        mbar_init(&ctl->o_done[i][k], 1);
+      }
+    for (int i = 0; i < S::kVBufs; ++i) {
+      mbar_init(&ctl->v_full[i], 4);
+      mbar_init(&ctl->v_empty[i], 1);
+    }
+    ctl->abort = 0;
+    fence_barrier_init();
   }
+  for (int i = tid; i < 2 * kCols * 4; i += kTreeThreads) (&ctl->poison[0][0][0])[i] = 0;
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem_base, S::kTmem);
+    tmem_relinquish();
+  }
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  Shared* shared = reinterpret_cast<Shared*>(p.arrived) + blockIdx.x;
+  if (tid == 0) shared->last = -1;
+  // the whole sequence: every thread sums a run of requests
+  const int cts = (p.Q * p.group + kCols - 1) / kCols;
+  const int per = (p.B + kTreeThreads - 1) / kTreeThreads;
+  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    int first, n;
+    unit_tiles<kTile>(p, max(0, p.seq_lens[b]), first, n);
+    sum += n + kUnitCost;
+  }
+  int incl = sum;
 #pragma unroll
-  for (int k = 0; k < kN; ++k) acc_of[warp][lane * kN + k] = acc[k];
-  if (lane == 0) {
-    m_of[warp] = m;
-    l_of[warp] = l;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(kFull, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) ctl->scan_sum[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const int of_warp = lane < kTreeThreads / 32 ? ctl->scan_sum[lane] : 0;
+  const int before = (__reduce_add_sync(kFull, lane < warp ? of_warp : 0) + incl - sum) * p.kv_heads;
+  const int all = __reduce_add_sync(kFull, of_warp) * p.kv_heads;      // of one column tile
+  const int units = p.B * p.kv_heads * cts, tiles = all * cts - kUnitCost * units;
+  const Ranges ranges(all * cts, min((int)gridDim.x, max(units, (tiles + kMinPages - 1) / kMinPages)));
+  const int cta = blockIdx.x;
+  const int t_begin = ranges.begin(cta), t_end = cta < ranges.ctas ? ranges.begin(cta + 1) : t_begin;
+  const int ct = t_begin / all, in_ct = t_begin - ct * all;
+  if (t_begin < t_end && before <= in_ct && in_ct < before + sum * p.kv_heads) {
+    int b = b0, at = before;
+    for (;; ++b) {
+      int first, n;
+      unit_tiles<kTile>(p, max(0, p.seq_lens[b]), first, n);
+      if (in_ct < at + (n + kUnitCost) * p.kv_heads) break;
+      at += (n + kUnitCost) * p.kv_heads;
+    }
+    ctl->start_b = b;
+    ctl->start_before = at;
   }
   __syncthreads();
-  float top = neg_inf(), sum = 0.f;
-  for (int w = 0; w < kTreeWarps; ++w) top = fmaxf(top, m_of[w]);
-  for (int w = 0; w < kTreeWarps; ++w) sum += m_of[w] == top ? l_of[w] : l_of[w] * ex2_approx(m_of[w] - top);
-  const bool none = !(sum != 0.f);
-  for (int d = threadIdx.x; d < D; d += kTreeWarps * 32) {
-    float o = 0.f;
-    for (int w = 0; w < kTreeWarps; ++w) o += acc_of[w][d] * (m_of[w] == top ? 1.f : ex2_approx(m_of[w] - top));
-    o = none ? 0.f : o / sum;
-    p.out[row * D + d] = kHalf ? __half_as_ushort(__float2half_rn(o)) : __bfloat16_as_ushort(__float2bfloat16_rn(o));
-  }
-  if (threadIdx.x == 0) p.lse[row] = none ? neg_inf() : (top + log2f(sum)) * 0.69314718055994530942f;
-  // pages that are none, once
-  if (h == 0 && node % p.Q == 0 && p.status != nullptr) {
-    const int64_t cols = ((int64_t)len + kPageTokens - 1) / kPageTokens;
-    const int64_t first = p.window > 0 ? max((int64_t)0, (int64_t)base - p.window + 1) / kPageTokens : 0;
-    for (int64_t col = first + threadIdx.x; col < cols; col += kTreeWarps * 32) {
-      const int page = col < p.max_pages ? p.page_table[(int64_t)b * p.max_pages + col] : -1;
-      if (page < 0 || page >= p.num_pages) atomicAdd(p.status + NVFP4MLA_STAT_BAD_PAGE, 1);
+  Walk<kTile, kUnitCost> w{};
+  w.left = t_end - t_begin;
+  if (w.left > 0) {
+    w.ct = ct;
+    w.b = ctl->start_b;
+    w.load(p);
+    const int in = in_ct - ctl->start_before, each = w.n + kUnitCost;
+    w.kvh = in / each;
+    w.pos = t_begin - (in - w.kvh * each);
+    w.take(in - w.kvh * each);
+    const uint32_t tmem = ctl->tmem_base;
+    Cta<D, kQ> c{p, stages, qimg, vimg, ctl};
+    if (warp == 0) {
+      c.producer(w);
+    } else if (warp == 1) {
+      if (lane == 0) c.issue_s(w, tmem);
+      __syncwarp();
+    } else if (warp == 3) {
+      if (lane == 0) c.issue_o(w, tmem);
+      __syncwarp();
+    } else if (warp >= 8) {
+      c.template softmax<kHalf>(w, tmem, ranges, shared);
+    } else if (warp >= 4) {
+      c.template feed<kHalf>(w);
     }
   }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(ctl->tmem_base, S::kTmem);
+  }
+}
+
+// Means of a shared unit's parts, added by the sums that they are of: a warp a column, D / 32 dims a lane.
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Kv8TreeParams p) {
+  constexpr int kN = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, first = blockIdx.x, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const Shared s = reinterpret_cast<const Shared*>(p.arrived)[first];
+  if (s.last < 0) return;
+  const int col = s.ct * kCols + r, j = col / p.group;
+  if (col >= p.Q * p.group) return;
+  const int64_t row = ((int64_t)s.b * p.Q + j) * p.H + s.kvh * p.group + (col - j * p.group);
+  auto at = [&](int cta) { return (int64_t)(2 * cta + (cta == first ? s.slot : 0)) * kCols + r; };
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  float m = kNone, sum = 0.f;
+  for (int c = first + lane; c <= s.last; c += 32) m = fmaxf(m, ml[at(c)].x);
+  m = redux_max(m);
+  for (int c = first + lane; c <= s.last; c += 32) {
+    const float2 x = ml[at(c)];
+    sum += x.y * ratio(x.x, m);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  float o[kN] = {};
+#pragma unroll 4
+  for (int c = first; c <= s.last; ++c) {
+    const float2 x = ml[at(c)];
+    const float f = x.y * ratio(x.x, m) * inv;
+    const float* part = p.part_o + at(c) * D + lane * kN;
+    if constexpr (kN == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(part);
+      o[0] = fmaf(v.x, f, o[0]);
+      o[1] = fmaf(v.y, f, o[1]);
+      o[2] = fmaf(v.z, f, o[2]);
+      o[3] = fmaf(v.w, f, o[3]);
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(part);
+      o[0] = fmaf(v.x, f, o[0]);
+      o[1] = fmaf(v.y, f, o[1]);
+    }
+  }
+  uint32_t* to = reinterpret_cast<uint32_t*>(p.out + row * D + lane * kN);
+#pragma unroll
+  for (int k = 0; k < kN / 2; ++k) to[k] = narrow2<kHalf>(o[2 * k], o[2 * k + 1]);
+  if (lane == 0) p.lse[row] = sum == 0.f ? neg_inf() : (m + log2f(sum)) * 0.69314718055994530942f;
+}
+
+template <int D, bool kHalf>
+cudaError_t launch(const Kv8TreeParams& p, cudaStream_t stream) {
+  using S = Shape<D, kHalf ? 3 : 2>;
+  constexpr size_t smem = 1024 + (size_t)S::kStages * S::kStageBytes + S::kQBytes + S::kVBufs * S::kVBytes + S::kControl;
+  static_assert(smem <= 232448, "exceeds the 227 KB shared-memory limit");
+  static std::mutex mu;
+  static bool allowed[64] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 64 || !allowed[dev]) {
+      err = cudaFuncSetAttribute(tree_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (err != cudaSuccess) return err;
+      if (dev < 64) allowed[dev] = true;
+    }
+  }
+  // Dependent launches: a CTA sets itself up while the grid before it in the stream ends, and waits for all of that grid
+  // before it reads or writes memory.
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.ctas, 1, 1);
+  cfg.blockDim = dim3(kTreeThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, tree_kernel<D, kHalf>, p);
+  if (err != cudaSuccess) return err;
+  cfg.gridDim = dim3((unsigned)p.ctas, kCols / 8, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, kHalf>, p);
 }
 
 }  // namespace
 
-int kv8_tree_columns(int Q, int group) { return 128; }
+static_assert(sizeof(Shared) <= 3 * sizeof(uint64_t), "the workspace holds three words a CTA");
+int kv8_tree_columns() { return kCols; }
 
 cudaError_t launch_kv8_decode_tree(const Kv8TreeParams& p, int head_dim, bool fp16, cudaStream_t stream) {
-  const unsigned blocks = (unsigned)((int64_t)p.B * p.Q * p.H);
-  if (head_dim == 128) {
-    if (fp16) tree_kernel<128, true><<<blocks, kTreeWarps * 32, 0, stream>>>(p);
-    else tree_kernel<128, false><<<blocks, kTreeWarps * 32, 0, stream>>>(p);
-  } else {
-    if (fp16) tree_kernel<64, true><<<blocks, kTreeWarps * 32, 0, stream>>>(p);
-    else tree_kernel<64, false><<<blocks, kTreeWarps * 32, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  if (head_dim == 128) return fp16 ? launch<128, true>(p, stream) : launch<128, false>(p, stream);
+  return fp16 ? launch<64, true>(p, stream) : launch<64, false>(p, stream);
 }
 
 }  // namespace nvfp4mla

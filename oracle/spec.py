@@ -63,7 +63,7 @@ def decode_tree(q, cache, page_table, seq_lens, masks, kv_heads: int, scale: flo
             if int(masks[b, j]) == 0:
                 continue
             nodes = bits(masks[b, j], Q)
-            place = base + len(nodes) - 1
+            place = base + max(1, len(nodes)) - 1
             ok = np.zeros(length, bool)
             ok[max(0, place - window + 1) if window else 0:max(0, base)] = True
             for i in nodes:
