@@ -618,6 +618,11 @@ size_t kv8_decode_tree_workspace_size(int B, int Q, int H, int kv_heads, int hea
  * A mask of 0 is padding: such a node attends to nothing, its out is 0 and its lse -inf. Bits from Q on are
  * not looked at, but a mask of those alone is not 0.
  *
+ * NaN, infinities and the sizes of scores as kv8_decode. The two operands that are held in fewer bits:
+ *   queries  off by at most 2^-17 of the row's largest magnitude (bf16: exact from 2^-9 of it on, fp16: 2^-6)
+ *   weights  off by at most 2^-12 of itself, or 2^-34 of the largest such product of the row's attended positions
+ *            if that is more; the sum that divides is one of unrounded exponentials
+ *
  *   masks             uint64 [B, Q], 8-byte aligned
  *   Q                 1 .. NVFP4MLA_MAX_NODES
  *   window            0 (none), or >= Q (else NVFP4MLA_ERR_UNSUPPORTED): drafts are never outside of it

@@ -13,9 +13,9 @@
 //   S  8-bit products, as in kv8_decode: keys are used as they lie in the cache, and a query is a sum of E4M3
 //      numbers (two of a bf16, three of an fp16, the row's largest element at 2^7 to 2^8): what is left after them is
 //      half of E4M3's smallest step, 2^-10, 2^-17 of the largest. The parts are further steps along K: one sum.
-//   O  fp16 products of weights in fp16 and codes, which an fp16 holds exactly. A weight's largest is 2^11 to 2^15,
-//      so half a step is 2^-12 of it, and at the lower end 2^-25 in those units: 2^-40 of the largest. (Weights as
-//      8-bit parts, as kv8_decode has them, need four for that range: twice the tensor time, and some thirty
+//   O  fp16 products of weights in fp16 and codes, which an fp16 holds exactly. A column's largest is 2^9 to 2^16,
+//      so half a step is 2^-12 of it, and at the lower end 2^-25 in those units: 2^-34 of the largest. (Weights as
+//      8-bit parts, as kv8_decode has them, need four for such a range: twice the tensor time, and some thirty
 //      instructions for a pair of weights where a conversion is one. There the codes need no conversion instead,
 //      which is 2 D a token and does not grow with the columns.)
 //
@@ -52,9 +52,9 @@ constexpr int kFeeders = 128;          // threads
 constexpr int kSoftmaxThreads = 256;
 constexpr int kUnitCost = 8;           // of a unit, in pages
 constexpr int kMinPages = 4;           // of a CTA, on average
-constexpr float kHeadroom = 4.f;       // log2: how far above the reference a weight's exponent may come
-constexpr float kWeightScale = 11.f;   // log2: weights are held times 2^11: 2^4 above it, one is 2^15 (fp16: 65,504)
-constexpr float kSumHeadroom = 60.f;   // log2: the same for the sum, which fp32 holds
+constexpr float kWeightScale = 9.f;    // log2: a weight at its reference is held as 2^9
+constexpr float kMostWeights = 64512.f;   // of 16 weights together, so that an fp16 holds each (65,504)
+constexpr float kSumHeadroom = 60.f;   // log2: how far above its reference a score may come, for the sum's sake
 constexpr unsigned kFull = 0xFFFFFFFFu;
 enum { kBarFeeders = 1, kBarSoftmax = 2 };
 
@@ -66,7 +66,7 @@ struct Shape {
   static constexpr int kCodes = kTile * D;                      // bytes of a page's keys, or values
   static constexpr int kStageBytes = 2 * kCodes;
   static constexpr int kVBytes = 2 * kCodes;                    // values as fp16
-  static constexpr int kVBufs = 4;
+  static constexpr int kVBufs = 2 * kStreams;                   // one beside each buffer of S
   static constexpr int kControl = 13312;
   static constexpr int kFit = (232448 - 1024 - kControl - kQBytes - kVBufs * kVBytes) / kStageBytes;
   static constexpr int kStages = kFit < 16 ? kFit : 16;
@@ -76,12 +76,12 @@ struct Shape {
   static_assert(kOCol + kStreams * D <= 512 && kStages >= 4, "fits");
 };
 
-template <int kStages, int kVBufs>
+template <int kStages>
 struct Control {
   uint64_t full[kStages], empty[kStages];
   uint64_t q_full[2], q_empty, done[2];                // done: softmax has ended a segment
-  uint64_t s_full[kStreams][2], w_full[kStreams][2], o_done[kStreams][2];
-  uint64_t v_full[kVBufs], v_empty[kVBufs];
+  uint64_t s_full[kStreams][2], v_full[kStreams][2], w_full[kStreams][2];
+  uint64_t o_done[kStreams][2];                        // the product is complete: weights and values are used, O is at rest
   uint64_t drain[2];
   alignas(16) uint4 scales[kStages];                   // the scale bytes of two neighbouring heads
   int page_ok[kStages];
@@ -157,7 +157,7 @@ __device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : 
 template <int D, int kQ>
 struct Cta {
   using S = Shape<D, kQ>;
-  using Ctl = Control<S::kStages, S::kVBufs>;
+  using Ctl = Control<S::kStages>;
   using Walk = ::nvfp4mla::Walk<kTile, kUnitCost>;
   const Kv8TreeParams& p;
   uint8_t* stages;
@@ -286,8 +286,7 @@ struct Cta {
             if (part == 0 && k == 0) umma_f8_ss_w<0>(d, q_lo, (uint32_t)(qd >> 32), k_lo + 2 * k, (uint32_t)(kd >> 32), kId);
             else umma_f8_ss_w<1>(d, q_lo, (uint32_t)(qd >> 32), k_lo + 2 * k, (uint32_t)(kd >> 32), kId);
           }
-        umma_commit(&ctl->s_full[stream][sb]);
-        umma_commit(&ctl->empty[ring.st]);
+        umma_commit(&ctl->s_full[stream][sb]);           // (the stage is given back by the softmax, which waits for this)
         ring.next();
       }
       if (ok) umma_commit(&ctl->q_empty);
@@ -300,25 +299,22 @@ struct Cta {
   __device__ void issue_o(Walk w, uint32_t tmem) {
     constexpr uint32_t kId = idesc_f16(kCols, D, false, true, false);
     const uint64_t vd = sdesc(smem_u32(vimg), kTile * 128, 1024, SW_128B);
-    Ring<S::kVBufs> ring;
     uint32_t uses[kStreams] = {0, 0};
     bool ok = true;
     for (; ok && w.left > 0; w.next(p)) {
       for (int i = 0; ok && i < w.count; ++i) {
         const int stream = i & 1;
         const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++, sb = u & 1;
-        ok = wait(&ctl->v_full[ring.st], ring.phase);
+        ok = wait(&ctl->v_full[stream][sb], (u >> 1) & 1);
         ok = ok && wait(&ctl->w_full[stream][sb], (u >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + S::kOCol + stream * D, a = tmem + (stream * 2 + sb) * kTile;
-        const uint32_t v_lo = (uint32_t)vd + ((ring.st * S::kVBytes) >> 4);
+        const uint32_t v_lo = (uint32_t)vd + (((stream * 2 + sb) * S::kVBytes) >> 4);
         umma_ts_w<-1>(d, a, v_lo, (uint32_t)(vd >> 32), kId, i >= kStreams ? 1u : 0u);
 #pragma unroll
         for (int k = 1; k < kTile / 16; ++k) umma_ts_w<1>(d, a + 8 * k, v_lo + k * 128, (uint32_t)(vd >> 32), kId);
         umma_commit(&ctl->o_done[stream][sb]);
-        umma_commit(&ctl->v_empty[ring.st]);
-        ring.next();
       }
     }
     umma_commit(&ctl->drain[1]);
@@ -329,7 +325,7 @@ struct Cta {
   // The unit's queries, and what its columns attend to.
   template <bool kHalf>
   __device__ void queries(const Walk& w, uint32_t buf) {
-    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = 32 / kAtOnce, kAhead = 4;
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = 32 / kAtOnce, kAhead = 4;    // rounds whose loads, and chains, are under way together
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, sub = lane / kLanes, ch = lane % kLanes;
     const int ncols = p.Q * p.group, base = w.len - p.Q;
     auto load = [&](int round) {
@@ -376,36 +372,42 @@ struct Cta {
       }
     }
 #pragma unroll 1
-    for (int r = 0; r < kRounds; ++r) {
-      const uint4 x4 = v[0];
+    for (int r0 = 0; r0 < kRounds; r0 += kAhead) {
+      uint4 x[kAhead];
+      uint32_t top[kAhead];
 #pragma unroll
-      for (int k = 0; k + 1 < kAhead; ++k) v[k] = v[k + 1];
-      v[kAhead - 1] = load(r + kAhead);
-      const int n = warp * 32 + r * kAtOnce + sub;
-      const uint32_t ws[4] = {x4.x, x4.y, x4.z, x4.w};
-      uint32_t top = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) top = __vmaxu2(top, ws[k] & 0x7FFF7FFFu);
-      top = max(top & 0xFFFFu, top >> 16);
-#pragma unroll
-      for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(kFull, top, d));
-      const bool finite = top < (kHalf ? 0x7C00u : 0x7F80u);
-      // the largest magnitude goes to [128, 256): a power of two, exact
-      const int e = (int)(__float_as_uint(widen2<kHalf>(top).x) >> 23) - 127;
-      const int sh = top == 0 || !finite ? 0 : min(7 - e, 126);
-      const float mul = finite ? __uint_as_float((uint32_t)(sh + 127) << 23) : 0.f;
-      uint32_t part[4][kQ];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 x = widen2<kHalf>(ws[k]);
-        split(finite ? x.x * mul : 0.f, finite ? x.y * mul : 0.f, part[k]);
+      for (int i = 0; i < kAhead; ++i) {
+        x[i] = v[i];
+        v[i] = load(r0 + kAhead + i);
+        top[i] = __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu), __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
+        top[i] = max(top[i] & 0xFFFFu, top[i] >> 16);
       }
-      const int chunk = D == 128 ? ((ch >> 1) ^ (n & 7)) : ((ch >> 1) ^ ((n >> 1) & 3));
 #pragma unroll
-      for (int i = 0; i < kQ; ++i)
-        *reinterpret_cast<uint2*>(qimg + i * S::kQImage + n * D + chunk * 16 + (ch & 1) * 8) =
-            make_uint2(part[0][i] | (part[1][i] << 16), part[2][i] | (part[3][i] << 16));
-      if (ch == 0) ctl->f[buf][n] = finite ? p.scale_log2 * __uint_as_float((uint32_t)(127 - sh) << 23) : __int_as_float(0x7fc00000);
+      for (int d = 1; d < kLanes; d <<= 1)
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) top[i] = max(top[i], __shfl_xor_sync(kFull, top[i], d));
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int n = warp * 32 + (r0 + i) * kAtOnce + sub;
+        const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        const bool finite = top[i] < (kHalf ? 0x7C00u : 0x7F80u);
+        // the largest magnitude goes to [128, 256): a power of two, exact
+        const int e = (int)(__float_as_uint(widen2<kHalf>(top[i]).x) >> 23) - 127;
+        const int sh = top[i] == 0 || !finite ? 0 : min(7 - e, 126);
+        const float mul = finite ? __uint_as_float((uint32_t)(sh + 127) << 23) : 0.f;
+        uint32_t part[4][kQ];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 y = widen2<kHalf>(ws[k]);
+          split(finite ? y.x * mul : 0.f, finite ? y.y * mul : 0.f, part[k]);
+        }
+        const int chunk = D == 128 ? ((ch >> 1) ^ (n & 7)) : ((ch >> 1) ^ ((n >> 1) & 3));
+#pragma unroll
+        for (int q = 0; q < kQ; ++q)
+          *reinterpret_cast<uint2*>(qimg + q * S::kQImage + n * D + chunk * 16 + (ch & 1) * 8) =
+              make_uint2(part[0][q] | (part[1][q] << 16), part[2][q] | (part[3][q] << 16));
+        if (ch == 0) ctl->f[buf][n] = finite ? p.scale_log2 * __uint_as_float((uint32_t)(127 - sh) << 23) : __int_as_float(0x7fc00000);
+      }
     }
   }
 
@@ -444,7 +446,7 @@ struct Cta {
     constexpr int kChunks = D / 16, kLoads = kTile * kChunks / kFeeders;
     const int tid = threadIdx.x & 127, lane = threadIdx.x & 31;
     Ring<S::kStages> ring;
-    Ring<S::kVBufs> vring;
+    uint32_t uses[kStreams] = {0, 0};
     bool ok = true;
     for (uint32_t seg = 0; w.left > 0; ++seg, w.next(p)) {
       const uint32_t buf = seg & 1;
@@ -458,12 +460,13 @@ struct Cta {
       if (lane == 0) mbar_arrive(&ctl->q_full[buf]);
       const int base = w.len - p.Q, all_lo = ctl->all_lo[buf], any_lo = ctl->any_lo[buf];
       for (int i = 0; i < w.count; ++i) {
-        const int t0 = (w.first + w.at + i) * kTile;
+        const int t0 = (w.first + w.at + i) * kTile, stream = i & 1;
+        const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++, sb = u & 1;
         ok = ok && wait_warp(&ctl->full[ring.st], ring.phase);
-        ok = ok && wait_warp(&ctl->v_empty[vring.st], vring.phase ^ 1);
+        ok = ok && wait_warp(&ctl->o_done[stream][sb], ((u >> 1) & 1) ^ 1);
         if (!ok) break;
         const uint8_t* from = stages + ring.st * S::kStageBytes + S::kCodes;
-        uint8_t* img = vimg + vring.st * S::kVBytes;
+        uint8_t* img = vimg + (stream * 2 + sb) * S::kVBytes;
         const bool page_ok = ctl->page_ok[ring.st] != 0;
         uint4 x[kLoads];
 #pragma unroll
@@ -485,16 +488,97 @@ struct Cta {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&ctl->v_full[vring.st]);
+          mbar_arrive(&ctl->v_full[stream][sb]);
           mbar_arrive(&ctl->empty[ring.st]);
         }
         ring.next();
-        vring.next();
       }
     }
   }
 
   // ---------------------------------------------------------------- softmax (warps 8-15)
+  struct Refs {
+    float m, w, l;                       // references of the scores, and of the weights from there; the sum
+    bool any;                            // a position has been seen
+    bool gave_up;
+  };
+  // A page's weights in the place of its scores, with whatever is rare: positions that the column does not attend to,
+  // new references, and scores or scales so wide that sum and weights need an exponential each.
+  __device__ __noinline__ Refs careful(Refs t, uint32_t s_at, float f, uint2 sc, uint64_t mine, uint64_t* rest, uint32_t parity, uint32_t o_at) {
+    float c[4], ev[4], z[4], mz = neg_inf(), mw = neg_inf();
+    auto scores = [&](int b, uint32_t (&s)[16]) {
+      tmem_ld16(s_at + 16 * b, s);
+      tmem_wait_ld();
+    };
+    auto in = [&](int b, int k) { return (((b < 2 ? (uint32_t)mine : (uint32_t)(mine >> 32)) >> ((b & 1) * 16 + k)) & 1) != 0; };
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      c[b] = f * __uint_as_float(((sc.x >> (8 * b)) & 0xFFu) << 23);
+      ev[b] = (float)((int)((sc.y >> (8 * b)) & 0xFFu) - 127);
+      uint32_t s[16];
+      scores(b, s);
+      float x = neg_inf();
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x = fmaxf(x, in(b, k) ? __uint_as_float(s[k]) : neg_inf());
+      z[b] = x == neg_inf() ? x : x * c[b];
+      mz = fmaxf(mz, z[b]);
+      mw = fmaxf(mw, (z[b] - t.m) + ev[b]);
+    }
+    // (16 weights at the reference are 2^(9 + 4); the page's own are at most 2^2 above it)
+    const bool raise = t.any ? mw > t.w + 2.f || mz > t.m + kSumHeadroom : mz > neg_inf();
+    float scale_o = 1.f;
+    if (raise) {
+      const float m1 = t.any ? fmaxf(t.m, ceilf(mz)) : ceilf(mz);
+      float w1 = neg_inf();
+#pragma unroll
+      for (int b = 0; b < 4; ++b) w1 = fmaxf(w1, ceilf((z[b] - m1) + ev[b]));
+      if (t.any) {
+        w1 = fmaxf(w1, t.w + (t.m - m1));
+        scale_o = ex2_approx((t.m - m1) + (t.w - w1));
+        t.l *= ex2_approx(t.m - m1);
+      }
+      t.m = m1;
+      t.w = w1;
+      t.any = true;
+    }
+    t.gave_up = false;
+    if (rest != nullptr && __any_sync(kFull, scale_o != 1.f)) {
+      // O is at rest once the product before is complete
+      if (!wait_warp(rest, parity)) {
+        t.gave_up = true;
+        return t;
+      }
+      tc_fence_after();
+#pragma unroll 1
+      for (int k = 0; k < D; k += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_at + k, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * scale_o);
+        tmem_st32(o_at + k, o);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      uint32_t s[16], out[8];
+      scores(b, s);
+#pragma unroll
+      for (int k = 0; k < 16; k += 2) {
+        float e[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float d = __fadd_rn(__fmul_rn(__uint_as_float(s[k + n]), c[b]), -t.m);
+          t.l += in(b, k + n) ? ex2_approx(d) : 0.f;
+          e[n] = in(b, k + n) ? ex2_approx(d + (ev[b] - t.w + kWeightScale)) : 0.f;
+        }
+        out[k / 2] = narrow2<true>(e[0], e[1]);
+      }
+      tmem_st8(s_at + 8 * b, out);       // (in the place of scores that have been read)
+    }
+    return t;
+  }
+
   template <bool kHalf>
   __device__ void softmax(Walk w, uint32_t tmem, const Ranges& ranges, Shared* shared) {
     const int stream = (threadIdx.x >> 7) - 2, warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, r = threadIdx.x & 127;
@@ -510,7 +594,11 @@ struct Cta {
       const int row = ctl->row[buf][r], lo = ctl->lo[buf][r];
       const bool idle = __all_sync(kFull, row < 0);      // no column of this warp
       float m = 0.f, top_w = 0.f, l = 0.f;
-      bool any = false;
+      bool any = false, fits = false;
+      // of the references: what a weight's exponent has beside its score and scale, what takes a block's weights to the
+      // sum's units, and the smallest byte of a values' scale that one exponential will do for (256: none)
+      float offset = 0.f, back = 0.f;
+      int least_ev = 256;
       for (int i = stream; i < w.count; i += kStreams) {
         const uint32_t gt = g + i, st = gt % S::kStages, sb = u & 1;
         const int t0 = (w.first + w.at + i) * kTile;
@@ -522,76 +610,22 @@ struct Cta {
         const uint2 sc = reinterpret_cast<const uint2*>(&ctl->scales[st])[w.kvh & 1];
         const uint32_t s_at = quarter + (stream * 2 + sb) * kTile;
         if (!idle) {
-          uint32_t s[2][32];
-          tmem_ld32(s_at, s[0]);
-          tmem_ld32(s_at + 32, s[1]);
-          tmem_wait_ld();
           const bool whole = page_ok && t0 >= all_lo && t0 + kTile <= base;
-          uint64_t mine = ~0ull;
-          if (!whole) {
-            mine = page_ok ? bits(lo == INT_MAX ? 64 : lo - t0, base - t0) | nodes_at(ctl->mask[buf][r], base, t0) : 0;
-#pragma unroll
-            for (int k = 0; k < kTile; ++k)
-              if (((k < 32 ? (uint32_t)mine : (uint32_t)(mine >> 32)) >> (k & 31) & 1) == 0) s[k >> 5][k & 31] = 0xff800000u;
-          }
-          // the blocks' largest scores, and with their values' scales
-          float c[4], ev[4], z[4], mz = neg_inf(), mw = neg_inf(), ev_min;
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            c[b] = f * __uint_as_float(((sc.x >> (8 * b)) & 0xFFu) << 23);
-            ev[b] = (float)((int)((sc.y >> (8 * b)) & 0xFFu) - 127);
-            float x = neg_inf();
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) x = max3(x, __uint_as_float(s[b >> 1][(b & 1) * 16 + k]), __uint_as_float(s[b >> 1][(b & 1) * 16 + k + 1]));
-            z[b] = x == neg_inf() ? x : x * c[b];
-            mz = fmaxf(mz, z[b]);
-            mw = fmaxf(mw, (z[b] - m) + ev[b]);
-          }
-          ev_min = fminf(fminf(ev[0], ev[1]), fminf(ev[2], ev[3]));
-          const bool raise = any ? mw > top_w + kHeadroom || mz > m + kSumHeadroom : mz > neg_inf();
-          if (__any_sync(kFull, raise)) {
-            // rare after the first pages: new references, this page's own where those are larger
-            float scale_o = 1.f;
-            if (raise) {
-              const float m1 = any ? fmaxf(m, ceilf(mz)) : ceilf(mz);
-              float w1 = neg_inf();
-#pragma unroll
-              for (int b = 0; b < 4; ++b) w1 = fmaxf(w1, ceilf((z[b] - m1) + ev[b]));
-              if (any) {
-                w1 = fmaxf(w1, top_w + (m - m1));
-                scale_o = ex2_approx((m - m1) + (top_w - w1));
-                l *= ex2_approx(m - m1);
-              }
-              m = m1;
-              top_w = w1;
-              any = true;
-            }
-            if (i >= kStreams && __any_sync(kFull, scale_o != 1.f)) {
-              // O is at rest once the product before is complete
-              ok = wait_warp(&ctl->o_done[stream][sb ^ 1], ((u - 1) >> 1) & 1);
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int k = 0; k < D; k += 16) {
-                uint32_t o[16];
-                tmem_ld16(o_at + k, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * scale_o);
-                tmem_st16(o_at + k, o);
-              }
-              tmem_wait_st();
-            }
-          }
-          uint32_t out[32];
+          const uint32_t e01 = __vminu2(__byte_perm(sc.y, 0u, 0x4140), __byte_perm(sc.y, 0u, 0x4342));
           // One exponential serves w and l where fp32 holds the one beside the other: the smallest that matters to l,
           // 2^-40, has a weight above 2^-120.
-          if (__builtin_expect(whole && !__any_sync(kFull, fabsf(m) >= 1048576.f || top_w - ev_min > 80.f), 1)) {
+          if (whole && (int)min(e01 & 0xFFu, e01 >> 16) >= least_ev) {
+            uint32_t s[2][32], out[32];
+            tmem_ld32(s_at, s[0]);
+            tmem_ld32(s_at + 32, s[1]);
+            tmem_wait_ld();
+            float more = 0.f, most = 0.f;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-              const float2 cc = make_float2(c[b], c[b]);
-              const float k0 = (ev[b] - top_w + kWeightScale) - m;     // whole numbers: exact
-              const float2 kk = make_float2(k0, k0);
+              const uint32_t kb = (sc.x >> (8 * b)) & 0xFFu, vb = (sc.y >> (8 * b)) & 0xFFu;
+              const float c = f * __uint_as_float(kb << 23);
+              const float k0 = (__uint_as_float(0x4B000000u | vb) - 8388735.f) + offset;     // whole numbers: exact
+              const float2 cc = make_float2(c, c), kk = make_float2(k0, k0);
               float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
               for (int k = 0; k < 16; k += 2) {
@@ -600,27 +634,37 @@ struct Cta {
                 sum = __fadd2_rn(sum, e);
                 out[b * 8 + k / 2] = narrow2<true>(e.x, e.y);
               }
-              l = fmaf(sum.x + sum.y, ex2_approx(top_w - kWeightScale - ev[b]), l);
+              const float both = sum.x + sum.y;
+              most = fmaxf(most, both);
+              more = fmaf(both * back, __uint_as_float((254u - vb) << 23), more);
+            }
+            if (__any_sync(kFull, most > kMostWeights)) {
+              fits = false;
+            } else {
+              l += more;
+              tmem_st32(s_at, out);
+              fits = true;
             }
           } else {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-#pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                float e[2];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                  const int at = b * 16 + k + n;
-                  const bool in = ((at < 32 ? (uint32_t)mine : (uint32_t)(mine >> 32)) >> (at & 31) & 1) != 0;
-                  const float d = __fadd_rn(__fmul_rn(__uint_as_float(s[at >> 5][at & 31]), c[b]), -m);
-                  l += in ? ex2_approx(d) : 0.f;
-                  e[n] = in ? ex2_approx(d + (ev[b] - top_w + kWeightScale)) : 0.f;
-                }
-                out[b * 8 + k / 2] = narrow2<true>(e[0], e[1]);
-              }
-            }
+            fits = false;
           }
-          tmem_st32(s_at, out);
+          if (!fits) {
+            const uint64_t mine = whole ? ~0ull : (page_ok ? bits(lo == INT_MAX ? 64 : lo - t0, base - t0) | nodes_at(ctl->mask[buf][r], base, t0) : 0);
+            const Refs now = careful(Refs{m, top_w, l, any}, s_at, f, sc, mine, i >= kStreams ? &ctl->o_done[stream][sb ^ 1] : nullptr, ((u - 1) >> 1) & 1, o_at);
+            m = now.m;
+            top_w = now.w;
+            l = now.l;
+            any = now.any;
+            if (__any_sync(kFull, now.gave_up)) {
+              ok = false;
+              break;
+            }
+            offset = kWeightScale - top_w - m;
+            back = ex2_approx(top_w - kWeightScale);
+            const float highest = redux_max(top_w);
+            const bool plain = fabsf(m) < 1048576.f && fabsf(top_w) < 100.f && any;
+            least_ev = __all_sync(kFull, plain) ? (int)highest - 80 + 127 : 256;
+          }
           tmem_wait_st();
           tc_fence_before();
         }
@@ -717,7 +761,7 @@ template <int D, bool kHalf>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_constant__ Kv8TreeParams p) {
   constexpr int kQ = kHalf ? 3 : 2;
   using S = Shape<D, kQ>;
-  using Ctl = Control<S::kStages, S::kVBufs>;
+  using Ctl = Control<S::kStages>;
   static_assert(sizeof(Ctl) <= S::kControl, "the control block fits its share");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -730,7 +774,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     prefetch_tensormap(&p.cache_map);
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&ctl->full[i], 2);                     // the codes' bytes, the scale bytes
-      mbar_init(&ctl->empty[i], 1 + 4 + 4);            // S, the feeders, the stream's softmax
+      mbar_init(&ctl->empty[i], 4 + 4);                // the feeders, the stream's softmax
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->q_full[i], 4);
@@ -742,13 +786,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     for (int i = 0; i < kStreams; ++i)
       for (int k = 0; k < 2; ++k) {
         mbar_init(&ctl->s_full[i][k], 1);
+        mbar_init(&ctl->v_full[i][k], 4);
         mbar_init(&ctl->w_full[i][k], 4);
         mbar_init(&ctl->o_done[i][k], 1);
       }
-    for (int i = 0; i < S::kVBufs; ++i) {
-      mbar_init(&ctl->v_full[i], 4);
-      mbar_init(&ctl->v_empty[i], 1);
-    }
     ctl->abort = 0;
     fence_barrier_init();
   }

@@ -216,9 +216,9 @@ def check_tree(out, lse, ref, adds, what=""):
     """Outputs against the oracle's.
 
     A score is a sum of D products in fp32, off by at most (D + 8) 2^-24 of reach; a query's elements are held to 2^-17 of the row's
-    largest: 2^-17 of span. A weight is off by that, by the exponential's 2^-21, by its rounding to fp16 (half a step, 2^-12), or
-    2^-40 of the largest such product of the head; the sum that divides is one of unrounded weights; both sums are made of `adds`
-    additions in 32 bits, each off by at most a step of what it has reached. The output is rounded once to its type; one that
+    largest: 2^-17 of span. A weight is off by that, by the exponential's 2^-21, and by its rounding to fp16: half a step, 2^-12, or,
+    below 2^-14, half of 2^-24; as the column's largest such product is held at 2^9 at least, that is 2^-25 / 2^9 = 2^-34 of it. The
+    sum that divides is one of unrounded weights; both sums are made of `adds` additions in 32 bits, each off by at most a step of what it has reached. The output is rounded once to its type; one that
     the type does not hold becomes an infinity."""
     r_out, r_lse, mass, reach, spread, span = ref
     dz = (r_out.shape[-1] + 8) * 2.0 ** -24 * reach + 2.0 ** -17 * span
@@ -228,7 +228,7 @@ def check_tree(out, lse, ref, adds, what=""):
     got, got_lse = f64(out), f64(lse)
     nan = np.isnan(r_out)
     assert np.array_equal(np.isnan(got), nan), f"{what}: NaN in other places"
-    tol = half * np.abs(r_out) + (1 + half) * (dw[..., None] * mass + 2.0 ** -40 * spread) + tiny
+    tol = half * np.abs(r_out) + (1 + half) * (dw[..., None] * mass + 2.0 ** -34 * spread) + tiny
     most = torch.finfo(out.dtype).max * (1 + half)           # what is nearer to it than to the largest number
     with np.errstate(invalid="ignore"):
         got = np.where((got == np.copysign(np.inf, r_out)) & (np.abs(r_out) + tol >= most), r_out, got)
