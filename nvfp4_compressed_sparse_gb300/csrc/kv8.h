@@ -81,6 +81,7 @@ cudaError_t launch_kv8_decode(const Kv8DecodeParams& p, int head_dim, bool fp16,
 
 struct Kv8TreeParams : Kv8DecodeParams {
   const uint64_t* masks;         // [B, Q]
+  uint32_t group_inverse;        // 2^24 / group + 1: (c x that) >> 24 = c / group for c < 2^14, as group <= 128
 };
 int kv8_tree_columns();                                         // (node, head) columns of a CTA's tile
 cudaError_t launch_kv8_decode_tree(const Kv8TreeParams& p, int head_dim, bool fp16, cudaStream_t stream);

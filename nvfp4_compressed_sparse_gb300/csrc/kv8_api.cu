@@ -295,11 +295,12 @@ int kv8_decode_tree(const void* q, int64_t q_token_stride, int64_t q_head_stride
   Kv8TreeParams p{};
   const int rc = check_decode(q, q_token_stride, q_head_stride, dtype, cache, num_pages, page_table, max_pages_per_seq, seq_lens, B, Q, H,
                               kv_heads, head_dim, softmax_scale, window, out, lse, workspace, workspace_bytes, dev_status, flags,
-                              kv8_tree_columns(), 1, kTreeWords, &p);
+                              kv8_tree_columns(), 2, kTreeWords, &p);
   if (rc != NVFP4MLA_OK) return rc;
   if (!all_device({masks})) return NVFP4MLA_ERR_INVALID_ARG;
   if (!encode_rows_map(&p.cache_map, cache, num_pages, p.page_bytes, kv_heads, head_dim)) return NVFP4MLA_ERR_CUDA;
   p.masks = masks;
+  p.group_inverse = (1u << 24) / (uint32_t)p.group + 1;
   return status_of(launch_kv8_decode_tree(p, head_dim, dtype == NVFP4MLA_FP16, static_cast<cudaStream_t>(stream)));
 }
 

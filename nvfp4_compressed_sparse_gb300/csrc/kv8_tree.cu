@@ -45,13 +45,14 @@ namespace {
 using namespace ptx;
 
 constexpr int kCols = 128;             // of a unit: (node, head)
-constexpr int kTile = kPageTokens;     // tokens of a stage
+constexpr int kTile = 2 * kPageTokens; // tokens of a stage: two pages, which one product with the queries takes
+constexpr int kHalves = 2;
 constexpr int kStreams = 2;
 constexpr int kTreeThreads = 512;
 constexpr int kFeeders = 128;          // threads
 constexpr int kSoftmaxThreads = 256;
-constexpr int kUnitCost = 8;           // of a unit, in pages
-constexpr int kMinPages = 4;           // of a CTA, on average
+constexpr int kUnitCost = 4;           // of a unit, in tiles
+constexpr int kMinTiles = 2;           // of a CTA, on average
 constexpr float kWeightScale = 9.f;    // log2: a weight at its reference is held as 2^9
 constexpr float kMostWeights = 64512.f;   // of 16 weights together, so that an fp16 holds each (65,504)
 constexpr float kSumHeadroom = 60.f;   // log2: how far above its reference a score may come, for the sum's sake
@@ -63,28 +64,28 @@ struct Shape {
   static constexpr int kQParts = kQ;
   static constexpr int kQImage = kCols * D;                     // bytes of a part
   static constexpr int kQBytes = kQ * kQImage;
-  static constexpr int kCodes = kTile * D;                      // bytes of a page's keys, or values
-  static constexpr int kStageBytes = 2 * kCodes;
-  static constexpr int kVBytes = 2 * kCodes;                    // values as fp16
-  static constexpr int kVBufs = 2 * kStreams;                   // one beside each buffer of S
+  static constexpr int kCodes = kPageTokens * D;                // bytes of a page's keys, or values
+  static constexpr int kStageBytes = 2 * kHalves * kCodes;      // keys of both pages, then values
+  static constexpr int kVBytes = 2 * kCodes;                    // a page's values as fp16
+  static constexpr int kVBufs = kStreams * kHalves;
   static constexpr int kControl = 13312;
   static constexpr int kFit = (232448 - 1024 - kControl - kQBytes - kVBufs * kVBytes) / kStageBytes;
   static constexpr int kStages = kFit < 16 ? kFit : 16;
   static constexpr uint32_t kSw = D == 128 ? SW_128B : SW_64B;  // of rows of D bytes
-  static constexpr int kOCol = kStreams * 2 * kTile;            // TMEM columns: buffers of S, then O
+  static constexpr int kOCol = kStreams * kTile;                // TMEM columns: S of the streams, then O
   static constexpr uint32_t kTmem = 512;
-  static_assert(kOCol + kStreams * D <= 512 && kStages >= 4, "fits");
+  static_assert(kOCol + kStreams * D <= 512 && kStages >= 3, "fits");
 };
 
 template <int kStages>
 struct Control {
   uint64_t full[kStages], empty[kStages];
   uint64_t q_full[2], q_empty, done[2];                // done: softmax has ended a segment
-  uint64_t s_full[kStreams][2], v_full[kStreams][2], w_full[kStreams][2];
-  uint64_t o_done[kStreams][2];                        // the product is complete: weights and values are used, O is at rest
+  uint64_t s_full[kStreams], v_full[kStreams][kHalves], w_full[kStreams][kHalves];
+  uint64_t o_done[kStreams][kHalves];                  // the product is complete: weights and values are used, O is at rest
   uint64_t drain[2];
-  alignas(16) uint4 scales[kStages];                   // the scale bytes of two neighbouring heads
-  int page_ok[kStages];
+  alignas(16) uint4 scales[kStages][kHalves];          // the scale bytes of two neighbouring heads
+  int pages_ok[kStages];                               // bit per page: it is one
   alignas(16) float f[2][kCols];                       // per segment parity: score of a column per unit of S, log2 units
   uint64_t mask[2][kCols];
   int lo[2][kCols];                                    // first position before the tree that a column attends to
@@ -189,10 +190,11 @@ struct Cta {
   };
 
   // ---------------------------------------------------------------- producer (warp 0)
+  // Page numbers of 16 tiles from i on, a lane a page. -1: not needed, or none.
   __device__ __forceinline__ int load_pages(const Walk& w, int i) {
     const int lane = threadIdx.x & 31;
-    if (i + lane >= w.count) return -1;
-    const int64_t col = (int64_t)w.first + w.at + i + lane;
+    if (i + lane / kHalves >= w.count) return -1;
+    const int64_t col = kHalves * ((int64_t)w.first + w.at + i) + lane;
     if (col * kPageTokens >= w.len || col >= p.max_pages) return -1;   // behind the table: counted together
     const int page = p.page_table[(int64_t)w.b * p.max_pages + col];
     if (page >= 0 && page < p.num_pages) return page;
@@ -211,37 +213,41 @@ struct Cta {
       const int kvh = w.kvh;
       if (w.kvh == 0 && w.ct == 0 && w.at + w.count == w.n && lane == 0 && p.status != nullptr) {
         const int64_t need = ((int64_t)w.len + kPageTokens - 1) / kPageTokens;
-        const int64_t from = max((int64_t)w.first, p.max_pages);
+        const int64_t from = max((int64_t)kHalves * w.first, p.max_pages);
         if (need > from) atomicAdd(p.status + NVFP4MLA_STAT_BAD_PAGE, (int)(need - from));
       }
-      for (int i = 0; ok && i < w.count; i += 32) {
+      for (int i = 0; ok && i < w.count; i += 16) {
         const int mine = pages;
-        if (i + 32 < w.count) {
-          pages = load_pages(w, i + 32);
+        if (i + 16 < w.count) {
+          pages = load_pages(w, i + 16);
         } else {
           Walk nx = w;
           nx.next(p);
           pages = nx.left > 0 ? load_pages(nx, 0) : -1;
         }
-        const int m = min(32, w.count - i);
+        const int m = min(16, w.count - i);
         for (int k = 0; ok && k < m; ++k) {
-          const int page = __shfl_sync(kFull, mine, k);
+          const int page = __shfl_sync(kFull, mine, kHalves * k + (lane & 1));
+          const uint32_t have = __ballot_sync(kFull, page >= 0) & 3u;
           if (lane == 0) {
             ok = wait(&ctl->empty[ring.st], ring.phase ^ 1);
             if (ok) {
-              uint8_t* to = stages + ring.st * S::kStageBytes;
-              ctl->page_ok[ring.st] = page >= 0;
-              mbar_arrive_expect_tx(&ctl->full[ring.st], page >= 0 ? S::kStageBytes : 0);
-              if (page >= 0) {
-                const uint8_t* at = p.cache + page * p.page_bytes;
-                tma_load_3d(to, &p.cache_map, 0, kvh * kPageTokens, page, &ctl->full[ring.st]);
-                bulk_g2s(to + S::kCodes, at + kv8_codes_off(p.kv_heads, D, 1, kvh), S::kCodes, &ctl->full[ring.st]);
-                cp_async_16(&ctl->scales[ring.st], at + kv8_scales_off(p.kv_heads, D, kvh & ~1));
-              }
-              cp_async_arrive(&ctl->full[ring.st]);
+              ctl->pages_ok[ring.st] = (int)have;
+              mbar_arrive_expect_tx(&ctl->full[ring.st], __popc(have) * 2 * S::kCodes);
             }
           }
           ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+          if (ok && lane < kHalves) {
+            if (page >= 0) {
+              uint8_t* to = stages + ring.st * S::kStageBytes + lane * S::kCodes;
+              const uint8_t* at = p.cache + page * p.page_bytes;
+              tma_load_3d(to, &p.cache_map, 0, kvh * kPageTokens, page, &ctl->full[ring.st]);
+              bulk_g2s(to + kHalves * S::kCodes, at + kv8_codes_off(p.kv_heads, D, 1, kvh), S::kCodes, &ctl->full[ring.st]);
+              cp_async_16(&ctl->scales[ring.st][lane], at + kv8_scales_off(p.kv_heads, D, kvh & ~1));
+            }
+            cp_async_arrive(&ctl->full[ring.st]);
+          }
+          __syncwarp();
           if (ok) {
             ring.next();
             ++g;
@@ -272,12 +278,12 @@ struct Cta {
       ok = wait(&ctl->q_full[seg & 1], (seg >> 1) & 1);
       for (int i = 0; ok && i < w.count; ++i) {
         const int stream = i & 1;
-        const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++, sb = u & 1;
+        const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++;
         ok = wait(&ctl->full[ring.st], ring.phase);
-        ok = ok && wait(&ctl->o_done[stream][sb], ((u >> 1) & 1) ^ 1);   // the buffer's last weights have been used
+        ok = ok && wait(&ctl->o_done[stream][1], (u & 1) ^ 1);           // the weights of the tile before have been used
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + (stream * 2 + sb) * kTile, k_lo = (uint32_t)kd + ((ring.st * S::kStageBytes) >> 4);
+        const uint32_t d = tmem + stream * kTile, k_lo = (uint32_t)kd + ((ring.st * S::kStageBytes) >> 4);
 #pragma unroll
         for (int part = 0; part < kQ; ++part)
 #pragma unroll
@@ -286,7 +292,7 @@ struct Cta {
             if (part == 0 && k == 0) umma_f8_ss_w<0>(d, q_lo, (uint32_t)(qd >> 32), k_lo + 2 * k, (uint32_t)(kd >> 32), kId);
             else umma_f8_ss_w<1>(d, q_lo, (uint32_t)(qd >> 32), k_lo + 2 * k, (uint32_t)(kd >> 32), kId);
           }
-        umma_commit(&ctl->s_full[stream][sb]);           // (the stage is given back by the softmax, which waits for this)
+        umma_commit(&ctl->s_full[stream]);               // (the stage is given back by the softmax, which waits for this)
         ring.next();
       }
       if (ok) umma_commit(&ctl->q_empty);
@@ -298,23 +304,27 @@ struct Cta {
   // ---------------------------------------------------------------- O += w V (warp 3, one thread)
   __device__ void issue_o(Walk w, uint32_t tmem) {
     constexpr uint32_t kId = idesc_f16(kCols, D, false, true, false);
-    const uint64_t vd = sdesc(smem_u32(vimg), kTile * 128, 1024, SW_128B);
+    const uint64_t vd = sdesc(smem_u32(vimg), kPageTokens * 128, 1024, SW_128B);
     uint32_t uses[kStreams] = {0, 0};
     bool ok = true;
     for (; ok && w.left > 0; w.next(p)) {
       for (int i = 0; ok && i < w.count; ++i) {
         const int stream = i & 1;
-        const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++, sb = u & 1;
-        ok = wait(&ctl->v_full[stream][sb], (u >> 1) & 1);
-        ok = ok && wait(&ctl->w_full[stream][sb], (u >> 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t d = tmem + S::kOCol + stream * D, a = tmem + (stream * 2 + sb) * kTile;
-        const uint32_t v_lo = (uint32_t)vd + (((stream * 2 + sb) * S::kVBytes) >> 4);
-        umma_ts_w<-1>(d, a, v_lo, (uint32_t)(vd >> 32), kId, i >= kStreams ? 1u : 0u);
+        const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++;
+        const uint32_t d = tmem + S::kOCol + stream * D;
 #pragma unroll
-        for (int k = 1; k < kTile / 16; ++k) umma_ts_w<1>(d, a + 8 * k, v_lo + k * 128, (uint32_t)(vd >> 32), kId);
-        umma_commit(&ctl->o_done[stream][sb]);
+        for (int half = 0; half < kHalves; ++half) {
+          ok = ok && wait(&ctl->v_full[stream][half], u & 1);
+          ok = ok && wait(&ctl->w_full[stream][half], u & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = tmem + stream * kTile + half * kPageTokens, v_lo = (uint32_t)vd + (((stream * kHalves + half) * S::kVBytes) >> 4);
+          if (half == 0) umma_ts_w<-1>(d, a, v_lo, (uint32_t)(vd >> 32), kId, i >= kStreams ? 1u : 0u);
+          else umma_ts_w<1>(d, a, v_lo, (uint32_t)(vd >> 32), kId);
+#pragma unroll
+          for (int k = 1; k < kPageTokens / 16; ++k) umma_ts_w<1>(d, a + 8 * k, v_lo + k * 128, (uint32_t)(vd >> 32), kId);
+          umma_commit(&ctl->o_done[stream][half]);
+        }
       }
     }
     umma_commit(&ctl->drain[1]);
@@ -325,13 +335,14 @@ struct Cta {
   // The unit's queries, and what its columns attend to.
   template <bool kHalf>
   __device__ void queries(const Walk& w, uint32_t buf) {
-    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = 32 / kAtOnce, kAhead = 4;    // rounds whose loads, and chains, are under way together
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = 32 / kAtOnce, kTogether = 4, kAhead = kRounds < 12 ? kRounds : 12;    // rounds whose chains, and loads, are under way together
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, sub = lane / kLanes, ch = lane % kLanes;
     const int ncols = p.Q * p.group, base = w.len - p.Q;
+    auto node_of = [&](int col) { return (int)(((uint64_t)(uint32_t)col * p.group_inverse) >> 24); };   // col / group
     auto load = [&](int round) {
       const int col = w.ct * kCols + warp * 32 + round * kAtOnce + sub;
       if (round >= kRounds || col >= ncols) return make_uint4(0u, 0u, 0u, 0u);
-      const int j = col / p.group, h = w.kvh * p.group + col - j * p.group;
+      const int j = node_of(col), h = w.kvh * p.group + col - j * p.group;
       return *reinterpret_cast<const uint4*>(p.q + ((int64_t)w.b * p.Q + j) * p.q_token_stride + h * p.q_head_stride + ch * 8);
     };
     const uint64_t* masks = p.masks + (int64_t)w.b * p.Q;
@@ -341,7 +352,7 @@ struct Cta {
     for (int r = 0; r < kAhead; ++r) v[r] = load(r);
     {
       // a lane a column: what it attends to
-      const int c = warp * 32 + lane, col = w.ct * kCols + c, j = col / p.group;
+      const int c = warp * 32 + lane, col = w.ct * kCols + c, j = node_of(col);
       const uint64_t mask = col < ncols ? masks[j] : 0;
       const int place = base + max(1, __popcll(mask & bits_of)) - 1;
       ctl->mask[buf][c] = mask & bits_of;
@@ -372,22 +383,25 @@ struct Cta {
       }
     }
 #pragma unroll 1
-    for (int r0 = 0; r0 < kRounds; r0 += kAhead) {
-      uint4 x[kAhead];
-      uint32_t top[kAhead];
+    for (int r0 = 0; r0 < kRounds; r0 += kTogether) {
+      uint4 x[kTogether];
+      uint32_t top[kTogether];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
+      for (int i = 0; i < kTogether; ++i) {
         x[i] = v[i];
-        v[i] = load(r0 + kAhead + i);
         top[i] = __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu), __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
         top[i] = max(top[i] & 0xFFFFu, top[i] >> 16);
       }
 #pragma unroll
+      for (int i = 0; i + kTogether < kAhead; ++i) v[i] = v[i + kTogether];
+#pragma unroll
+      for (int i = 0; i < kTogether; ++i) v[kAhead - kTogether + i] = load(r0 + kAhead + i);
+#pragma unroll
       for (int d = 1; d < kLanes; d <<= 1)
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) top[i] = max(top[i], __shfl_xor_sync(kFull, top[i], d));
+        for (int i = 0; i < kTogether; ++i) top[i] = max(top[i], __shfl_xor_sync(kFull, top[i], d));
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
+      for (int i = 0; i < kTogether; ++i) {
         const int n = warp * 32 + (r0 + i) * kAtOnce + sub;
         const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
         const bool finite = top[i] < (kHalf ? 0x7C00u : 0x7F80u);
@@ -415,35 +429,36 @@ struct Cta {
   __device__ __forceinline__ void put_values(uint8_t* img, const uint4& x, int r, int c) {
     const uint2 a = codes4(x.x), b = codes4(x.y), d = codes4(x.z), e = codes4(x.w);
     const uint4 first = make_uint4(a.x, a.y, b.x, b.y), second = make_uint4(d.x, d.y, e.x, e.y);
-    uint8_t* row = img + (c >> 2) * (kTile * 128) + r * 128;
+    uint8_t* row = img + (c >> 2) * (kPageTokens * 128) + r * 128;
     const int at = (c & 3) * 2, swap = (c >> 2) & 1;           // (the halves of 64 dims in turn, for the banks' sake)
     *reinterpret_cast<uint4*>(row + (((at + swap) ^ (r & 7)) << 4)) = swap ? second : first;
     *reinterpret_cast<uint4*>(row + (((at + 1 - swap) ^ (r & 7)) << 4)) = swap ? first : second;
   }
 
-  // Row r of a page that not all columns attend to: zeros where none does (it may hold anything), and a NaN is taken out
-  // and noted for those that do.
-  __device__ __noinline__ void clean(uint4& x, int t, int c, bool any, uint32_t buf, int base) {
+  // Values of a row that only some columns attend to: a NaN is taken out and noted for those. (A row that none attends
+  // to may hold anything, and becomes zeros.)
+  static __device__ __forceinline__ bool nans_in(const uint4& x) {
+    return (__vcmpeq4(x.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(x.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+            __vcmpeq4(x.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(x.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu)) != 0;
+  }
+  __device__ __noinline__ uint4 without_nans(uint4 x, int t, int c, uint32_t buf, int base) {
     uint8_t* byte = reinterpret_cast<uint8_t*>(&x);
-    if (!any) {
-      x = make_uint4(0u, 0u, 0u, 0u);
-      return;
-    }
     for (int k = 0; k < 16; ++k) {
       if ((byte[k] & 0x7F) != 0x7F) continue;
       byte[k] = 0;
       const int d = c * 16 + k;
       for (int n = 0; n < kCols; ++n) {
-        const bool attends = t < base ? t >= ctl->lo[buf][n] : t - base < 64 && ((ctl->mask[buf][n] >> (t - base)) & 1) != 0;
+        const bool attends = t < base ? t >= ctl->lo[buf][n] : ((ctl->mask[buf][n] >> (t - base)) & 1) != 0;
         if (attends) atomicOr(&ctl->poison[buf][n][d >> 5], 1u << (d & 31));
       }
       ctl->any_poison[buf] = 1;
     }
+    return x;
   }
 
   template <bool kHalf>
   __device__ void feed(Walk w) {
-    constexpr int kChunks = D / 16, kLoads = kTile * kChunks / kFeeders;
+    constexpr int kChunks = D / 16, kLoads = kPageTokens * kChunks / kFeeders;
     const int tid = threadIdx.x & 127, lane = threadIdx.x & 31;
     Ring<S::kStages> ring;
     uint32_t uses[kStreams] = {0, 0};
@@ -459,38 +474,43 @@ struct Cta {
       if (bar_any(kBarFeeders, kFeeders, !ok)) return;
       if (lane == 0) mbar_arrive(&ctl->q_full[buf]);
       const int base = w.len - p.Q, all_lo = ctl->all_lo[buf], any_lo = ctl->any_lo[buf];
-      for (int i = 0; i < w.count; ++i) {
-        const int t0 = (w.first + w.at + i) * kTile, stream = i & 1;
-        const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++, sb = u & 1;
-        ok = ok && wait_warp(&ctl->full[ring.st], ring.phase);
-        ok = ok && wait_warp(&ctl->o_done[stream][sb], ((u >> 1) & 1) ^ 1);
-        if (!ok) break;
-        const uint8_t* from = stages + ring.st * S::kStageBytes + S::kCodes;
-        uint8_t* img = vimg + (stream * 2 + sb) * S::kVBytes;
-        const bool page_ok = ctl->page_ok[ring.st] != 0;
-        uint4 x[kLoads];
+      for (int i = 0; ok && i < w.count; ++i) {
+        const int stream = i & 1;
+        const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++;
+        ok = wait_warp(&ctl->full[ring.st], ring.phase);
+        for (int half = 0; half < kHalves; ++half) {
+          const int t0 = (w.first + w.at + i) * kTile + half * kPageTokens;
+          ok = ok && wait_warp(&ctl->o_done[stream][half], (u & 1) ^ 1);
+          if (!ok) break;
+          const uint8_t* from = stages + ring.st * S::kStageBytes + (kHalves + half) * S::kCodes;
+          uint8_t* img = vimg + (stream * kHalves + half) * S::kVBytes;
+          const bool page_ok = ((ctl->pages_ok[ring.st] >> half) & 1) != 0;
+          if (page_ok && t0 >= all_lo && t0 + kPageTokens <= base) {
+            uint4 x[kLoads];
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k) x[k] = *reinterpret_cast<const uint4*>(from + (tid + k * kFeeders) * 16);
-        if (!(page_ok && t0 >= all_lo && t0 + kTile <= base)) {
-          const uint64_t any = page_ok ? bits(any_lo - t0, base - t0) | nodes_at(ctl->any_mask[buf], base, t0) : 0;
-          const uint64_t all = page_ok ? bits(all_lo - t0, base - t0) | nodes_at(ctl->all_mask[buf], base, t0) : 0;
+            for (int k = 0; k < kLoads; ++k) x[k] = *reinterpret_cast<const uint4*>(from + (tid + k * kFeeders) * 16);
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) put_values(img, x[k], (tid + k * kFeeders) / kChunks, (tid + k * kFeeders) % kChunks);
+          } else {
+            const uint64_t any = page_ok ? bits(any_lo - t0, base - t0) | nodes_at(ctl->any_mask[buf], base, t0) : 0;
+            const uint64_t all = page_ok ? bits(all_lo - t0, base - t0) | nodes_at(ctl->all_mask[buf], base, t0) : 0;
 #pragma unroll 1
-          for (int k = 0; k < kLoads; ++k) {
-            const int r = (tid + k * kFeeders) / kChunks, c = (tid + k * kFeeders) % kChunks;
-            uint4 y = *reinterpret_cast<const uint4*>(from + (tid + k * kFeeders) * 16);
-            if (((all >> r) & 1) == 0) clean(y, t0 + r, c, ((any >> r) & 1) != 0, buf, base);
-            put_values(img, y, r, c);
+            for (int k = 0; k < kLoads; ++k) {
+              const int r = (tid + k * kFeeders) / kChunks, c = (tid + k * kFeeders) % kChunks;
+              uint4 y = make_uint4(0u, 0u, 0u, 0u);
+              if ((any >> r) & 1) {
+                y = *reinterpret_cast<const uint4*>(from + (tid + k * kFeeders) * 16);
+                if (((all >> r) & 1) == 0 && nans_in(y)) y = without_nans(y, t0 + r, c, buf, base);
+              }
+              put_values(img, y, r, c);
+            }
           }
-        } else {
-#pragma unroll
-          for (int k = 0; k < kLoads; ++k) put_values(img, x[k], (tid + k * kFeeders) / kChunks, (tid + k * kFeeders) % kChunks);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->v_full[stream][half]);
         }
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ctl->v_full[stream][sb]);
-          mbar_arrive(&ctl->empty[ring.st]);
-        }
+        if (ok && lane == 0) mbar_arrive(&ctl->empty[ring.st]);
         ring.next();
       }
     }
@@ -505,24 +525,27 @@ struct Cta {
   // A page's weights in the place of its scores, with whatever is rare: positions that the column does not attend to,
   // new references, and scores or scales so wide that sum and weights need an exponential each.
   __device__ __noinline__ Refs careful(Refs t, uint32_t s_at, float f, uint2 sc, uint64_t mine, uint64_t* rest, uint32_t parity, uint32_t o_at) {
-    float c[4], ev[4], z[4], mz = neg_inf(), mw = neg_inf();
-    auto scores = [&](int b, uint32_t (&s)[16]) {
-      tmem_ld16(s_at + 16 * b, s);
-      tmem_wait_ld();
-    };
-    auto in = [&](int b, int k) { return (((b < 2 ? (uint32_t)mine : (uint32_t)(mine >> 32)) >> ((b & 1) * 16 + k)) & 1) != 0; };
+    float z[4], mz = neg_inf(), mw = neg_inf();
+    t.gave_up = false;
+    if (!__any_sync(kFull, mine != 0)) {
+      uint32_t none[32] = {};
+      tmem_st32(s_at, none);
+      return t;
+    }
+    auto key_scale = [&](int b) { return f * __uint_as_float(((sc.x >> (8 * b)) & 0xFFu) << 23); };
+    auto value_scale = [&](int b) { return (float)((int)((sc.y >> (8 * b)) & 0xFFu) - 127); };
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      c[b] = f * __uint_as_float(((sc.x >> (8 * b)) & 0xFFu) << 23);
-      ev[b] = (float)((int)((sc.y >> (8 * b)) & 0xFFu) - 127);
       uint32_t s[16];
-      scores(b, s);
+      tmem_ld16(s_at + 16 * b, s);
+      tmem_wait_ld();
+      const uint32_t in = (uint32_t)(mine >> (16 * b));
       float x = neg_inf();
 #pragma unroll
-      for (int k = 0; k < 16; ++k) x = fmaxf(x, in(b, k) ? __uint_as_float(s[k]) : neg_inf());
-      z[b] = x == neg_inf() ? x : x * c[b];
+      for (int k = 0; k < 16; ++k) x = fmaxf(x, (in >> k) & 1 ? __uint_as_float(s[k]) : neg_inf());
+      z[b] = x == neg_inf() ? x : x * key_scale(b);
       mz = fmaxf(mz, z[b]);
-      mw = fmaxf(mw, (z[b] - t.m) + ev[b]);
+      mw = fmaxf(mw, (z[b] - t.m) + value_scale(b));
     }
     // (16 weights at the reference are 2^(9 + 4); the page's own are at most 2^2 above it)
     const bool raise = t.any ? mw > t.w + 2.f || mz > t.m + kSumHeadroom : mz > neg_inf();
@@ -531,7 +554,7 @@ struct Cta {
       const float m1 = t.any ? fmaxf(t.m, ceilf(mz)) : ceilf(mz);
       float w1 = neg_inf();
 #pragma unroll
-      for (int b = 0; b < 4; ++b) w1 = fmaxf(w1, ceilf((z[b] - m1) + ev[b]));
+      for (int b = 0; b < 4; ++b) w1 = fmaxf(w1, ceilf((z[b] - m1) + value_scale(b)));
       if (t.any) {
         w1 = fmaxf(w1, t.w + (t.m - m1));
         scale_o = ex2_approx((t.m - m1) + (t.w - w1));
@@ -541,7 +564,6 @@ struct Cta {
       t.w = w1;
       t.any = true;
     }
-    t.gave_up = false;
     if (rest != nullptr && __any_sync(kFull, scale_o != 1.f)) {
       // O is at rest once the product before is complete
       if (!wait_warp(rest, parity)) {
@@ -559,21 +581,28 @@ struct Cta {
         tmem_st32(o_at + k, o);
       }
     }
-#pragma unroll
+    // (kept as a loop: code that runs a few times costs what its fetching costs)
+#pragma unroll 1
     for (int b = 0; b < 4; ++b) {
       uint32_t s[16], out[8];
-      scores(b, s);
+      tmem_ld16(s_at + 16 * b, s);
+      tmem_wait_ld();
+      const uint32_t in = (uint32_t)(mine >> (16 * b));
+      const float c = key_scale(b), less = value_scale(b) - t.w + kWeightScale;
+      float sum[2] = {0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < 16; k += 2) {
         float e[2];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const float d = __fadd_rn(__fmul_rn(__uint_as_float(s[k + n]), c[b]), -t.m);
-          t.l += in(b, k + n) ? ex2_approx(d) : 0.f;
-          e[n] = in(b, k + n) ? ex2_approx(d + (ev[b] - t.w + kWeightScale)) : 0.f;
+          const float d = __fadd_rn(__fmul_rn(__uint_as_float(s[k + n]), c), -t.m);
+          const bool is_in = ((in >> (k + n)) & 1) != 0;
+          sum[n] += is_in ? ex2_approx(d) : 0.f;
+          e[n] = is_in ? ex2_approx(d + less) : 0.f;
         }
         out[k / 2] = narrow2<true>(e[0], e[1]);
       }
+      t.l += sum[0] + sum[1];
       tmem_st8(s_at + 8 * b, out);       // (in the place of scores that have been read)
     }
     return t;
@@ -585,7 +614,7 @@ struct Cta {
     const uint32_t quarter = tmem + ((uint32_t)(warp * 32) << 16);
     const uint32_t o_at = quarter + S::kOCol + stream * D;
     const int t_first = ranges.begin(blockIdx.x);
-    uint32_t g = 0, u = 0;                               // stages before this segment; this stream's pages
+    uint32_t g = 0, u = 0;                               // stages before this segment; this stream's tiles
     for (uint32_t seg = 0; w.left > 0; ++seg, w.next(p)) {
       const uint32_t buf = seg & 1;
       bool ok = wait_warp(&ctl->q_full[buf], (seg >> 1) & 1);
@@ -600,17 +629,20 @@ struct Cta {
       float offset = 0.f, back = 0.f;
       int least_ev = 256;
       for (int i = stream; i < w.count; i += kStreams) {
-        const uint32_t gt = g + i, st = gt % S::kStages, sb = u & 1;
-        const int t0 = (w.first + w.at + i) * kTile;
+        const uint32_t gt = g + i, st = gt % S::kStages;
         ok = ok && wait_warp(&ctl->full[st], (gt / S::kStages) & 1);
-        ok = ok && wait_warp(&ctl->s_full[stream][sb], (u >> 1) & 1);
+        ok = ok && wait_warp(&ctl->s_full[stream], u & 1);
         if (!ok) break;
         tc_fence_after();
-        const bool page_ok = ctl->page_ok[st] != 0;
-        const uint2 sc = reinterpret_cast<const uint2*>(&ctl->scales[st])[w.kvh & 1];
-        const uint32_t s_at = quarter + (stream * 2 + sb) * kTile;
+        const int pages_ok = ctl->pages_ok[st];
+#pragma unroll 1
+        for (int half = 0; half < kHalves; ++half) {
+        const int t0 = (w.first + w.at + i) * kTile + half * kPageTokens;
+        const bool page_ok = ((pages_ok >> half) & 1) != 0;
+        const uint2 sc = reinterpret_cast<const uint2*>(&ctl->scales[st][half])[w.kvh & 1];
+        const uint32_t s_at = quarter + stream * kTile + half * kPageTokens;
         if (!idle) {
-          const bool whole = page_ok && t0 >= all_lo && t0 + kTile <= base;
+          const bool whole = page_ok && t0 >= all_lo && t0 + kPageTokens <= base;
           const uint32_t e01 = __vminu2(__byte_perm(sc.y, 0u, 0x4140), __byte_perm(sc.y, 0u, 0x4342));
           // One exponential serves w and l where fp32 holds the one beside the other: the smallest that matters to l,
           // 2^-40, has a weight above 2^-120.
@@ -650,7 +682,9 @@ struct Cta {
           }
           if (!fits) {
             const uint64_t mine = whole ? ~0ull : (page_ok ? bits(lo == INT_MAX ? 64 : lo - t0, base - t0) | nodes_at(ctl->mask[buf][r], base, t0) : 0);
-            const Refs now = careful(Refs{m, top_w, l, any}, s_at, f, sc, mine, i >= kStreams ? &ctl->o_done[stream][sb ^ 1] : nullptr, ((u - 1) >> 1) & 1, o_at);
+            // the product before this page's: the other half's, of this tile or the one before
+            uint64_t* rest = half == 1 || i >= kStreams ? &ctl->o_done[stream][half ^ 1] : nullptr;
+            const Refs now = careful(Refs{m, top_w, l, any, false}, s_at, f, sc, mine, rest, half == 1 ? u & 1 : (u & 1) ^ 1, o_at);
             m = now.m;
             top_w = now.w;
             l = now.l;
@@ -669,15 +703,15 @@ struct Cta {
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ctl->empty[st]);
-          mbar_arrive(&ctl->w_full[stream][sb]);
+        if (lane == 0) mbar_arrive(&ctl->w_full[stream][half]);
         }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(&ctl->empty[st]);
         ++u;
       }
       // ---- the segment's end: both streams' columns, half of the dims each
       const int n = w.count;
-      if (ok && n > stream) ok = wait_warp(&ctl->o_done[stream][(u - 1) & 1], ((u - 1) >> 1) & 1);
+      if (ok && n > stream) ok = wait_warp(&ctl->o_done[stream][1], (u - 1) & 1);
       ctl->m[stream][r] = any ? m : kNone;
       ctl->w[stream][r] = top_w - kWeightScale;
       ctl->l[stream][r] = l;
@@ -773,7 +807,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   if (tid == 64) {
     prefetch_tensormap(&p.cache_map);
     for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&ctl->full[i], 2);                     // the codes' bytes, the scale bytes
+      mbar_init(&ctl->full[i], 1 + kHalves);           // the codes' bytes, every page's scale bytes
       mbar_init(&ctl->empty[i], 4 + 4);                // the feeders, the stream's softmax
     }
     for (int i = 0; i < 2; ++i) {
@@ -783,13 +817,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       ctl->any_poison[i] = 0;
     }
     mbar_init(&ctl->q_empty, 1);
-    for (int i = 0; i < kStreams; ++i)
-      for (int k = 0; k < 2; ++k) {
-        mbar_init(&ctl->s_full[i][k], 1);
+    for (int i = 0; i < kStreams; ++i) {
+      mbar_init(&ctl->s_full[i], 1);
+      for (int k = 0; k < kHalves; ++k) {
         mbar_init(&ctl->v_full[i][k], 4);
         mbar_init(&ctl->w_full[i][k], 4);
         mbar_init(&ctl->o_done[i][k], 1);
       }
+    }
     ctl->abort = 0;
     fence_barrier_init();
   }
@@ -827,7 +862,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   const int before = (__reduce_add_sync(kFull, lane < warp ? of_warp : 0) + incl - sum) * p.kv_heads;
   const int all = __reduce_add_sync(kFull, of_warp) * p.kv_heads;      // of one column tile
   const int units = p.B * p.kv_heads * cts, tiles = all * cts - kUnitCost * units;
-  const Ranges ranges(all * cts, min((int)gridDim.x, max(units, (tiles + kMinPages - 1) / kMinPages)));
+  const Ranges ranges(all * cts, min((int)gridDim.x, max(units, (tiles + kMinTiles - 1) / kMinTiles)));
   const int cta = blockIdx.x;
   const int t_begin = ranges.begin(cta), t_end = cta < ranges.ctas ? ranges.begin(cta + 1) : t_begin;
   const int ct = t_begin / all, in_ct = t_begin - ct * all;
@@ -885,7 +920,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Kv8Tr
   const int lane = threadIdx.x & 31, first = blockIdx.x, r = blockIdx.y * 8 + (threadIdx.x >> 5);
   const Shared s = reinterpret_cast<const Shared*>(p.arrived)[first];
   if (s.last < 0) return;
-  const int col = s.ct * kCols + r, j = col / p.group;
+  const int col = s.ct * kCols + r, j = (int)(((uint64_t)(uint32_t)col * p.group_inverse) >> 24);
   if (col >= p.Q * p.group) return;
   const int64_t row = ((int64_t)s.b * p.Q + j) * p.H + s.kvh * p.group + (col - j * p.group);
   auto at = [&](int cta) { return (int64_t)(2 * cta + (cta == first ? s.slot : 0)) * kCols + r; };
