@@ -47,7 +47,7 @@ using namespace ptx;
 constexpr int kCols = 128;             // of a unit: (node, head)
 constexpr int kTile = 2 * kPageTokens; // tokens of a stage: two pages, which one product with the queries takes
 constexpr int kHalves = 2;
-constexpr int kStreams = 2;
+constexpr int kBufs = 3;               // tiles whose scores, or weights in their place, tensor memory holds
 constexpr int kTreeThreads = 512;
 constexpr int kFeeders = 128;          // threads
 constexpr int kSoftmaxThreads = 256;
@@ -57,7 +57,7 @@ constexpr float kWeightScale = 9.f;    // log2: a weight at its reference is hel
 constexpr float kMostWeights = 64512.f;   // of 16 weights together, so that an fp16 holds each (65,504)
 constexpr float kSumHeadroom = 60.f;   // log2: how far above its reference a score may come, for the sum's sake
 constexpr unsigned kFull = 0xFFFFFFFFu;
-enum { kBarFeeders = 1, kBarSoftmax = 2 };
+enum { kBarFeeders = 1, kBarSoftmax = 2, kBarQuarter = 3 };   // (one for each quarter of the columns)
 
 template <int D, int kQ>
 struct Shape {
@@ -67,22 +67,22 @@ struct Shape {
   static constexpr int kCodes = kPageTokens * D;                // bytes of a page's keys, or values
   static constexpr int kStageBytes = 2 * kHalves * kCodes;      // keys of both pages, then values
   static constexpr int kVBytes = 2 * kCodes;                    // a page's values as fp16
-  static constexpr int kVBufs = kStreams * kHalves;
+  static constexpr int kVBufs = 2 * kHalves;                    // of two tiles
   static constexpr int kControl = 13312;
   static constexpr int kFit = (232448 - 1024 - kControl - kQBytes - kVBufs * kVBytes) / kStageBytes;
   static constexpr int kStages = kFit < 16 ? kFit : 16;
   static constexpr uint32_t kSw = D == 128 ? SW_128B : SW_64B;  // of rows of D bytes
-  static constexpr int kOCol = kStreams * kTile;                // TMEM columns: S of the streams, then O
+  static constexpr int kOCol = kBufs * kTile;                   // TMEM columns: buffers of S, then O
   static constexpr uint32_t kTmem = 512;
-  static_assert(kOCol + kStreams * D <= 512 && kStages >= 3, "fits");
+  static_assert(kOCol + D <= 512 && kStages >= 3, "fits");
 };
 
 template <int kStages>
 struct Control {
   uint64_t full[kStages], empty[kStages];
   uint64_t q_full[2], q_empty, done[2];                // done: softmax has ended a segment
-  uint64_t s_full[kStreams], v_full[kStreams][kHalves], w_full[kStreams][kHalves];
-  uint64_t o_done[kStreams][kHalves];                  // the product is complete: weights and values are used, O is at rest
+  uint64_t s_full[kBufs], w_full[kBufs], v_full[2];
+  uint64_t o_done[kBufs];                              // the product is complete: weights and values are used, O is at rest
   uint64_t drain[2];
   alignas(16) uint4 scales[kStages][kHalves];          // the scale bytes of two neighbouring heads
   int pages_ok[kStages];                               // bit per page: it is one
@@ -94,7 +94,8 @@ struct Control {
   int any_lo[2], all_lo[2];
   uint32_t poison[2][kCols][4];                        // dims that a NaN value reaches
   int any_poison[2];
-  float m[kStreams][kCols], w[kStreams][kCols], l[kStreams][kCols];
+  alignas(8) float2 most[kHalves][kCols];              // of a half: the largest score, and weight
+  float l[kHalves][kCols];                             // at a segment's end: the sum of a half's weights
   int scan_sum[kTreeThreads / 32];
   int start_before, start_b;
   int abort;
@@ -188,7 +189,6 @@ struct Cta {
       }
     }
   };
-
   // ---------------------------------------------------------------- producer (warp 0)
   // Page numbers of 16 tiles from i on, a lane a page. -1: not needed, or none.
   __device__ __forceinline__ int load_pages(const Walk& w, int i) {
@@ -272,18 +272,16 @@ struct Cta {
     constexpr uint32_t kId = idesc_e4m3(kCols, kTile, false, false);
     const uint64_t kd = sdesc(smem_u32(stages), 16, 8 * D, S::kSw), qd = sdesc(smem_u32(qimg), 16, 8 * D, S::kSw);
     Ring<S::kStages> ring;
-    uint32_t uses[kStreams] = {0, 0};
+    Ring<kBufs> buf;
     bool ok = true;
     for (uint32_t seg = 0; ok && w.left > 0; ++seg, w.next(p)) {
       ok = wait(&ctl->q_full[seg & 1], (seg >> 1) & 1);
       for (int i = 0; ok && i < w.count; ++i) {
-        const int stream = i & 1;
-        const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++;
         ok = wait(&ctl->full[ring.st], ring.phase);
-        ok = ok && wait(&ctl->o_done[stream][1], (u & 1) ^ 1);           // the weights of the tile before have been used
+        ok = ok && wait(&ctl->o_done[buf.st], buf.phase ^ 1);            // the buffer's last weights have been used
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + stream * kTile, k_lo = (uint32_t)kd + ((ring.st * S::kStageBytes) >> 4);
+        const uint32_t d = tmem + buf.st * kTile, k_lo = (uint32_t)kd + ((ring.st * S::kStageBytes) >> 4);
 #pragma unroll
         for (int part = 0; part < kQ; ++part)
 #pragma unroll
@@ -292,8 +290,9 @@ struct Cta {
             if (part == 0 && k == 0) umma_f8_ss_w<0>(d, q_lo, (uint32_t)(qd >> 32), k_lo + 2 * k, (uint32_t)(kd >> 32), kId);
             else umma_f8_ss_w<1>(d, q_lo, (uint32_t)(qd >> 32), k_lo + 2 * k, (uint32_t)(kd >> 32), kId);
           }
-        umma_commit(&ctl->s_full[stream]);               // (the stage is given back by the softmax, which waits for this)
+        umma_commit(&ctl->s_full[buf.st]);               // (the stage is given back by the softmax, which waits for this)
         ring.next();
+        buf.next();
       }
       if (ok) umma_commit(&ctl->q_empty);
     }
@@ -305,26 +304,26 @@ struct Cta {
   __device__ void issue_o(Walk w, uint32_t tmem) {
     constexpr uint32_t kId = idesc_f16(kCols, D, false, true, false);
     const uint64_t vd = sdesc(smem_u32(vimg), kPageTokens * 128, 1024, SW_128B);
-    uint32_t uses[kStreams] = {0, 0};
+    Ring<kBufs> buf;
+    Ring<2> vbuf;
     bool ok = true;
     for (; ok && w.left > 0; w.next(p)) {
       for (int i = 0; ok && i < w.count; ++i) {
-        const int stream = i & 1;
-        const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++;
-        const uint32_t d = tmem + S::kOCol + stream * D;
+        ok = wait(&ctl->v_full[vbuf.st], vbuf.phase);
+        ok = ok && wait(&ctl->w_full[buf.st], buf.phase);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + S::kOCol, a = tmem + buf.st * kTile, v_lo = (uint32_t)vd + ((vbuf.st * kHalves * S::kVBytes) >> 4);
 #pragma unroll
-        for (int half = 0; half < kHalves; ++half) {
-          ok = ok && wait(&ctl->v_full[stream][half], u & 1);
-          ok = ok && wait(&ctl->w_full[stream][half], u & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t a = tmem + stream * kTile + half * kPageTokens, v_lo = (uint32_t)vd + (((stream * kHalves + half) * S::kVBytes) >> 4);
-          if (half == 0) umma_ts_w<-1>(d, a, v_lo, (uint32_t)(vd >> 32), kId, i >= kStreams ? 1u : 0u);
-          else umma_ts_w<1>(d, a, v_lo, (uint32_t)(vd >> 32), kId);
-#pragma unroll
-          for (int k = 1; k < kPageTokens / 16; ++k) umma_ts_w<1>(d, a + 8 * k, v_lo + k * 128, (uint32_t)(vd >> 32), kId);
-          umma_commit(&ctl->o_done[stream][half]);
+        for (int k = 0; k < kTile / 16; ++k) {
+          // (a page's weights lie in the first half of its scores' place)
+          const uint32_t a_k = a + (k / 4) * kPageTokens + (k % 4) * 8, v_k = v_lo + (k / 4) * (S::kVBytes >> 4) + (k % 4) * 128;
+          if (k == 0) umma_ts_w<-1>(d, a_k, v_k, (uint32_t)(vd >> 32), kId, i > 0 ? 1u : 0u);
+          else umma_ts_w<1>(d, a_k, v_k, (uint32_t)(vd >> 32), kId);
         }
+        umma_commit(&ctl->o_done[buf.st]);
+        buf.next();
+        vbuf.next();
       }
     }
     umma_commit(&ctl->drain[1]);
@@ -461,7 +460,9 @@ struct Cta {
     constexpr int kChunks = D / 16, kLoads = kPageTokens * kChunks / kFeeders;
     const int tid = threadIdx.x & 127, lane = threadIdx.x & 31;
     Ring<S::kStages> ring;
-    uint32_t uses[kStreams] = {0, 0};
+    Ring<kBufs> used;                    // the tile before the last: its values' buffers are this one's
+    Ring<2> vbuf;
+    uint32_t t = 0;
     bool ok = true;
     for (uint32_t seg = 0; w.left > 0; ++seg, w.next(p)) {
       const uint32_t buf = seg & 1;
@@ -474,16 +475,14 @@ struct Cta {
       if (bar_any(kBarFeeders, kFeeders, !ok)) return;
       if (lane == 0) mbar_arrive(&ctl->q_full[buf]);
       const int base = w.len - p.Q, all_lo = ctl->all_lo[buf], any_lo = ctl->any_lo[buf];
-      for (int i = 0; ok && i < w.count; ++i) {
-        const int stream = i & 1;
-        const uint32_t u = stream == 0 ? uses[0]++ : uses[1]++;
+      for (int i = 0; ok && i < w.count; ++i, ++t) {
         ok = wait_warp(&ctl->full[ring.st], ring.phase);
+        if (t >= 2) ok = ok && wait_warp(&ctl->o_done[used.st], used.phase);
+        if (!ok) break;
         for (int half = 0; half < kHalves; ++half) {
           const int t0 = (w.first + w.at + i) * kTile + half * kPageTokens;
-          ok = ok && wait_warp(&ctl->o_done[stream][half], (u & 1) ^ 1);
-          if (!ok) break;
           const uint8_t* from = stages + ring.st * S::kStageBytes + (kHalves + half) * S::kCodes;
-          uint8_t* img = vimg + (stream * kHalves + half) * S::kVBytes;
+          uint8_t* img = vimg + (vbuf.st * kHalves + half) * S::kVBytes;
           const bool page_ok = ((ctl->pages_ok[ring.st] >> half) & 1) != 0;
           if (page_ok && t0 >= all_lo && t0 + kPageTokens <= base) {
             uint4 x[kLoads];
@@ -505,35 +504,41 @@ struct Cta {
               put_values(img, y, r, c);
             }
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->v_full[stream][half]);
         }
+        fence_proxy_async_smem();
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&ctl->empty[ring.st]);
+        if (lane == 0) {
+          mbar_arrive(&ctl->v_full[vbuf.st]);
+          mbar_arrive(&ctl->empty[ring.st]);
+        }
         ring.next();
+        vbuf.next();
+        if (t >= 2) used.next();
       }
     }
   }
 
   // ---------------------------------------------------------------- softmax (warps 8-15)
+  // References of a column's scores, and of its weights from there, and the sum that this thread has against the former.
   struct Refs {
-    float m, w, l;                       // references of the scores, and of the weights from there; the sum
-    bool any;                            // a position has been seen
-    bool gave_up;
+    float m, w, l;
+    __device__ __forceinline__ bool none() const { return w == kNone; }
   };
   // A page's weights in the place of its scores, with whatever is rare: positions that the column does not attend to,
-  // new references, and scores or scales so wide that sum and weights need an exponential each.
-  __device__ __noinline__ Refs careful(Refs t, uint32_t s_at, float f, uint2 sc, uint64_t mine, uint64_t* rest, uint32_t parity, uint32_t o_at) {
-    float z[4], mz = neg_inf(), mw = neg_inf();
-    t.gave_up = false;
-    if (!__any_sync(kFull, mine != 0)) {
-      uint32_t none[32] = {};
-      tmem_st32(s_at, none);
-      return t;
-    }
+  // new references, and scores or scales so wide that sum and weights need an exponential each. Both halves' threads of
+  // a quarter of the columns come here together. (at_rest: the barrier of the product before, or null; false: a wait gave up.)
+  __device__ __noinline__ bool careful(Refs& refs, int half, uint32_t s_at, float f, uint2 sc, uint64_t mine, uint64_t* at_rest, uint32_t parity, uint32_t o_at) {
+    Refs t = refs;
+    const int warp = (threadIdx.x >> 5) & 3, r = threadIdx.x & 127;
+    float z[4], mz = neg_inf();
     auto key_scale = [&](int b) { return f * __uint_as_float(((sc.x >> (8 * b)) & 0xFFu) << 23); };
     auto value_scale = [&](int b) { return (float)((int)((sc.y >> (8 * b)) & 0xFFu) - 127); };
+    auto largest = [&](float m) {          // of the weights, against m
+      float w = neg_inf();
+#pragma unroll
+      for (int b = 0; b < 4; ++b) w = fmaxf(w, (z[b] - m) + value_scale(b));
+      return w;
+    };
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       uint32_t s[16];
@@ -545,40 +550,40 @@ struct Cta {
       for (int k = 0; k < 16; ++k) x = fmaxf(x, (in >> k) & 1 ? __uint_as_float(s[k]) : neg_inf());
       z[b] = x == neg_inf() ? x : x * key_scale(b);
       mz = fmaxf(mz, z[b]);
-      mw = fmaxf(mw, (z[b] - t.m) + value_scale(b));
     }
-    // (16 weights at the reference are 2^(9 + 4); the page's own are at most 2^2 above it)
-    const bool raise = t.any ? mw > t.w + 2.f || mz > t.m + kSumHeadroom : mz > neg_inf();
+    ctl->most[half][r] = make_float2(mz, largest(t.m));
+    bar_sync(kBarQuarter + warp, 64);
+    const float2 other = ctl->most[half ^ 1][r];
+    const float mz2 = fmaxf(mz, other.x), mw2 = fmaxf(largest(t.m), other.y);
+    // (16 weights at the reference are 2^(9 + 4); the tile's own are at most 2^2 above it)
+    const bool raise = t.none() ? mz2 > neg_inf() : mw2 > t.w + 2.f || mz2 > t.m + kSumHeadroom;
     float scale_o = 1.f;
-    if (raise) {
-      const float m1 = t.any ? fmaxf(t.m, ceilf(mz)) : ceilf(mz);
-      float w1 = neg_inf();
-#pragma unroll
-      for (int b = 0; b < 4; ++b) w1 = fmaxf(w1, ceilf((z[b] - m1) + value_scale(b)));
-      if (t.any) {
-        w1 = fmaxf(w1, t.w + (t.m - m1));
-        scale_o = ex2_approx((t.m - m1) + (t.w - w1));
-        t.l *= ex2_approx(t.m - m1);
+    if (bar_any(kBarQuarter + warp, 64, raise)) {
+      const float m1 = !raise ? t.m : (t.none() ? ceilf(mz2) : fmaxf(t.m, ceilf(mz2)));
+      ctl->most[half][r].y = largest(m1);
+      bar_sync(kBarQuarter + warp, 64);
+      if (raise) {
+        float w1 = ceilf(fmaxf(largest(m1), ctl->most[half ^ 1][r].y));
+        if (!t.none()) {
+          w1 = fmaxf(w1, t.w + (t.m - m1));
+          scale_o = ex2_approx((t.m - m1) + (t.w - w1));
+          t.l *= ratio(t.m, m1);
+        }
+        t.m = m1;
+        t.w = w1;
       }
-      t.m = m1;
-      t.w = w1;
-      t.any = true;
-    }
-    if (rest != nullptr && __any_sync(kFull, scale_o != 1.f)) {
-      // O is at rest once the product before is complete
-      if (!wait_warp(rest, parity)) {
-        t.gave_up = true;
-        return t;
-      }
-      tc_fence_after();
+      if (at_rest != nullptr && __any_sync(kFull, scale_o != 1.f)) {
+        if (!wait_warp(at_rest, parity)) return false;
+        tc_fence_after();
 #pragma unroll 1
-      for (int k = 0; k < D; k += 32) {
-        uint32_t o[32];
-        tmem_ld32(o_at + k, o);
-        tmem_wait_ld();
+        for (int k = half * (D / 2); k < (half + 1) * (D / 2); k += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_at + k, o);
+          tmem_wait_ld();
 #pragma unroll
-        for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * scale_o);
-        tmem_st32(o_at + k, o);
+          for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * scale_o);
+          tmem_st32(o_at + k, o);
+        }
       }
     }
     // (kept as a loop: code that runs a few times costs what its fetching costs)
@@ -605,16 +610,21 @@ struct Cta {
       t.l += sum[0] + sum[1];
       tmem_st8(s_at + 8 * b, out);       // (in the place of scores that have been read)
     }
-    return t;
+    refs = t;
+    return true;
   }
 
+  // A warpgroup a page of each tile. The two threads of a column have the same references, and agree on every tile whether
+  // those will do.
   template <bool kHalf>
   __device__ void softmax(Walk w, uint32_t tmem, const Ranges& ranges, Shared* shared) {
-    const int stream = (threadIdx.x >> 7) - 2, warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, r = threadIdx.x & 127;
-    const uint32_t quarter = tmem + ((uint32_t)(warp * 32) << 16);
-    const uint32_t o_at = quarter + S::kOCol + stream * D;
+    const int half = (threadIdx.x >> 7) - 2, warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, r = threadIdx.x & 127;
+    const uint32_t quarter = tmem + ((uint32_t)(warp * 32) << 16), o_at = quarter + S::kOCol;
     const int t_first = ranges.begin(blockIdx.x);
-    uint32_t g = 0, u = 0;                               // stages before this segment; this stream's tiles
+    Ring<S::kStages> ring;
+    Ring<kBufs> at;
+    uint64_t* at_rest = nullptr;                         // the barrier of the product before
+    uint32_t rest_phase = 0;
     for (uint32_t seg = 0; w.left > 0; ++seg, w.next(p)) {
       const uint32_t buf = seg & 1;
       bool ok = wait_warp(&ctl->q_full[buf], (seg >> 1) & 1);
@@ -622,36 +632,30 @@ struct Cta {
       const float f = ctl->f[buf][r];
       const int row = ctl->row[buf][r], lo = ctl->lo[buf][r];
       const bool idle = __all_sync(kFull, row < 0);      // no column of this warp
-      float m = 0.f, top_w = 0.f, l = 0.f;
-      bool any = false, fits = false;
+      Refs refs{0.f, kNone, 0.f};
       // of the references: what a weight's exponent has beside its score and scale, what takes a block's weights to the
       // sum's units, and the smallest byte of a values' scale that one exponential will do for (256: none)
       float offset = 0.f, back = 0.f;
       int least_ev = 256;
-      for (int i = stream; i < w.count; i += kStreams) {
-        const uint32_t gt = g + i, st = gt % S::kStages;
-        ok = ok && wait_warp(&ctl->full[st], (gt / S::kStages) & 1);
-        ok = ok && wait_warp(&ctl->s_full[stream], u & 1);
-        if (!ok) break;
-        tc_fence_after();
-        const int pages_ok = ctl->pages_ok[st];
-#pragma unroll 1
-        for (int half = 0; half < kHalves; ++half) {
+      for (int i = 0; ok && i < w.count; ++i) {
+        ok = wait_warp(&ctl->full[ring.st], ring.phase) && wait_warp(&ctl->s_full[at.st], at.phase);
         const int t0 = (w.first + w.at + i) * kTile + half * kPageTokens;
-        const bool page_ok = ((pages_ok >> half) & 1) != 0;
-        const uint2 sc = reinterpret_cast<const uint2*>(&ctl->scales[st][half])[w.kvh & 1];
-        const uint32_t s_at = quarter + stream * kTile + half * kPageTokens;
+        const bool page_ok = ((ctl->pages_ok[ring.st] >> half) & 1) != 0, whole = page_ok && t0 >= all_lo && t0 + kPageTokens <= base;
+        const uint2 sc = reinterpret_cast<const uint2*>(&ctl->scales[ring.st][half])[w.kvh & 1];
+        const uint32_t s_at = quarter + at.st * kTile + half * kPageTokens;
+        tc_fence_after();
         if (!idle) {
-          const bool whole = page_ok && t0 >= all_lo && t0 + kPageTokens <= base;
-          const uint32_t e01 = __vminu2(__byte_perm(sc.y, 0u, 0x4140), __byte_perm(sc.y, 0u, 0x4342));
+          const uint32_t ev2 = __vminu2(__byte_perm(sc.y, 0u, 0x4140), __byte_perm(sc.y, 0u, 0x4342));
+          uint32_t out[32];
+          float more = 0.f, most = 0.f;
+          bool fits = ok && whole && (int)min(ev2 & 0xFFu, ev2 >> 16) >= least_ev;
           // One exponential serves w and l where fp32 holds the one beside the other: the smallest that matters to l,
           // 2^-40, has a weight above 2^-120.
-          if (whole && (int)min(e01 & 0xFFu, e01 >> 16) >= least_ev) {
-            uint32_t s[2][32], out[32];
+          if (fits) {
+            uint32_t s[2][32];
             tmem_ld32(s_at, s[0]);
             tmem_ld32(s_at + 32, s[1]);
             tmem_wait_ld();
-            float more = 0.f, most = 0.f;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
               const uint32_t kb = (sc.x >> (8 * b)) & 0xFFu, vb = (sc.y >> (8 * b)) & 0xFFu;
@@ -670,91 +674,62 @@ struct Cta {
               most = fmaxf(most, both);
               more = fmaf(both * back, __uint_as_float((254u - vb) << 23), more);
             }
-            if (__any_sync(kFull, most > kMostWeights)) {
-              fits = false;
-            } else {
-              l += more;
-              tmem_st32(s_at, out);
-              fits = true;
-            }
-          } else {
-            fits = false;
           }
-          if (!fits) {
+          if (__builtin_expect(!bar_any(kBarQuarter + warp, 64, !fits || most > kMostWeights), 1)) {
+            refs.l += more;
+            tmem_st32(s_at, out);
+          } else if (bar_any(kBarQuarter + warp, 64, !ok)) {
+            ok = false;
+            break;
+          } else {
             const uint64_t mine = whole ? ~0ull : (page_ok ? bits(lo == INT_MAX ? 64 : lo - t0, base - t0) | nodes_at(ctl->mask[buf][r], base, t0) : 0);
-            // the product before this page's: the other half's, of this tile or the one before
-            uint64_t* rest = half == 1 || i >= kStreams ? &ctl->o_done[stream][half ^ 1] : nullptr;
-            const Refs now = careful(Refs{m, top_w, l, any, false}, s_at, f, sc, mine, rest, half == 1 ? u & 1 : (u & 1) ^ 1, o_at);
-            m = now.m;
-            top_w = now.w;
-            l = now.l;
-            any = now.any;
-            if (__any_sync(kFull, now.gave_up)) {
-              ok = false;
-              break;
-            }
-            offset = kWeightScale - top_w - m;
-            back = ex2_approx(top_w - kWeightScale);
-            const float highest = redux_max(top_w);
-            const bool plain = fabsf(m) < 1048576.f && fabsf(top_w) < 100.f && any;
+            // (both halves' warps of a quarter go on together, or give up together)
+            ok = !bar_any(kBarQuarter + warp, 64, !careful(refs, half, s_at, f, sc, mine, i > 0 ? at_rest : nullptr, rest_phase, o_at));
+            offset = kWeightScale - refs.w - refs.m;
+            back = ex2_approx(refs.w - kWeightScale);
+            const bool plain = fabsf(refs.m) < 1048576.f && fabsf(refs.w) < 100.f;
+            const float highest = redux_max(refs.w);
             least_ev = __all_sync(kFull, plain) ? (int)highest - 80 + 127 : 256;
           }
           tmem_wait_st();
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->w_full[stream][half]);
+        if (ok && lane == 0) {
+          mbar_arrive(&ctl->w_full[at.st]);
+          mbar_arrive(&ctl->empty[ring.st]);
         }
-        if (!ok) break;
-        if (lane == 0) mbar_arrive(&ctl->empty[st]);
-        ++u;
+        at_rest = &ctl->o_done[at.st];
+        rest_phase = at.phase;
+        ring.next();
+        at.next();
       }
-      // ---- the segment's end: both streams' columns, half of the dims each
-      const int n = w.count;
-      if (ok && n > stream) ok = wait_warp(&ctl->o_done[stream][1], (u - 1) & 1);
-      ctl->m[stream][r] = any ? m : kNone;
-      ctl->w[stream][r] = top_w - kWeightScale;
-      ctl->l[stream][r] = l;
+      // ---- the segment's end: half of the dims each
+      ok = ok && wait_warp(at_rest, rest_phase);
+      ctl->l[half][r] = refs.l;
       tc_fence_before();
       if (bar_any(kBarSoftmax, kSoftmaxThreads, !ok)) return;
       tc_fence_after();
-      g += n;
       const bool pad = row < 0 || lo == INT_MAX;         // a padding node's column: whatever was summed is not wanted
-      float top = kNone, sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < kStreams; ++k) top = fmaxf(top, ctl->m[k][r]);
-#pragma unroll
-      for (int k = 0; k < kStreams; ++k) sum += ctl->l[k][r] * ratio(ctl->m[k][r], top);
-      if (pad) {
-        top = kNone;
-        sum = 0.f;
-      }
+      const float top = refs.none() || pad ? kNone : refs.m, sum = pad ? 0.f : ctl->l[0][r] + ctl->l[1][r];
       // what O is multiplied by makes it the weighted mean at once, in two factors that stay far from fp32's ends
       const int up = max(0, min(126, (int)((__float_as_uint(sum) >> 23) & 0xFFu) - 127));
       const float inv = inverse(sum * __uint_as_float((uint32_t)(127 - up) << 23));
-      float2 factor[kStreams];
-#pragma unroll
-      for (int k = 0; k < kStreams; ++k) {
-        const float half = ex2_approx(0.5f * ((ctl->m[k][r] - top) + ctl->w[k][r] - (float)up));
-        factor[k] = make_float2(half * inv, half);
-      }
+      const float factor = ex2_approx(0.5f * ((refs.none() ? 0.f : refs.w) - kWeightScale - (float)up)), first = factor * inv;
       const bool poisoned = ctl->any_poison[buf] != 0, full_unit = w.whole();
       const int slot = 2 * (int)blockIdx.x + second_slot(t_first, w.pos);
       if (!idle) {
 #pragma unroll 1
         for (int k0 = 0; k0 < D / 2; k0 += 16) {
-          const int d0 = stream * (D / 2) + k0;
-          uint32_t a[16], b[16];
-          tmem_ld16(quarter + S::kOCol + d0, a);
-          if (n > 1) tmem_ld16(quarter + S::kOCol + D + d0, b);
+          const int d0 = half * (D / 2) + k0;
+          uint32_t a[16];
+          tmem_ld16(o_at + d0, a);
           tmem_wait_ld();
           float o[16];
           const uint32_t bad = poisoned ? ctl->poison[buf][r][d0 >> 5] >> (d0 & 31) : 0u;
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            o[k] = __uint_as_float(a[k]) * factor[0].x * factor[0].y;
-            if (n > 1) o[k] = fmaf(__uint_as_float(b[k]) * factor[1].x, factor[1].y, o[k]);
-            if (pad) o[k] = 0.f;
+            o[k] = pad ? 0.f : __uint_as_float(a[k]) * first * factor;
             if ((bad >> k) & 1) o[k] = __int_as_float(0x7fc00000);
           }
           if (row >= 0) {
@@ -765,13 +740,14 @@ struct Cta {
                 to[k] = make_uint4(narrow2<kHalf>(o[8 * k], o[8 * k + 1]), narrow2<kHalf>(o[8 * k + 2], o[8 * k + 3]),
                                    narrow2<kHalf>(o[8 * k + 4], o[8 * k + 5]), narrow2<kHalf>(o[8 * k + 6], o[8 * k + 7]));
             } else {
-              float4* to = reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * kCols + r) * D + d0);
+              // four dims of all columns side by side: a warp writes 512 bytes in one piece
+              float4* to = reinterpret_cast<float4*>(p.part_o) + ((int64_t)slot * (D / 4) + d0 / 4) * kCols + r;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              for (int k = 0; k < 4; ++k) to[k * kCols] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
             }
           }
         }
-        if (stream == 0 && row >= 0) {
+        if (half == 0 && row >= 0) {
           if (full_unit) p.lse[row] = sum == 0.f ? neg_inf() : (top + log2f(sum)) * 0.69314718055994530942f;
           else reinterpret_cast<float2*>(p.part_ml)[slot * kCols + r] = make_float2(top, sum);
         }
@@ -781,7 +757,7 @@ struct Cta {
       tc_fence_before();
       bar_sync(kBarSoftmax, kSoftmaxThreads);            // all have read O, the notes of NaN and each other's sums
       if (poisoned) {
-        if (stream == 0)
+        if (half == 0)
           for (int k = 0; k < 4; ++k) ctl->poison[buf][r][k] = 0;
         if (threadIdx.x == 256) ctl->any_poison[buf] = 0;
         bar_sync(kBarSoftmax, kSoftmaxThreads);
@@ -808,7 +784,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     prefetch_tensormap(&p.cache_map);
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&ctl->full[i], 1 + kHalves);           // the codes' bytes, every page's scale bytes
-      mbar_init(&ctl->empty[i], 4 + 4);                // the feeders, the stream's softmax
+      mbar_init(&ctl->empty[i], (kFeeders + kSoftmaxThreads) / 32);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->q_full[i], 4);
@@ -817,14 +793,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       ctl->any_poison[i] = 0;
     }
     mbar_init(&ctl->q_empty, 1);
-    for (int i = 0; i < kStreams; ++i) {
+    for (int i = 0; i < kBufs; ++i) {
       mbar_init(&ctl->s_full[i], 1);
-      for (int k = 0; k < kHalves; ++k) {
-        mbar_init(&ctl->v_full[i][k], 4);
-        mbar_init(&ctl->w_full[i][k], 4);
-        mbar_init(&ctl->o_done[i][k], 1);
-      }
+      mbar_init(&ctl->w_full[i], kSoftmaxThreads / 32);
+      mbar_init(&ctl->o_done[i], 1);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&ctl->v_full[i], kFeeders / 32);
     ctl->abort = 0;
     fence_barrier_init();
   }
@@ -912,51 +886,45 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   }
 }
 
-// Means of a shared unit's parts, added by the sums that they are of: a warp a column, D / 32 dims a lane.
+// Means of a shared unit's parts, added by the sums that they are of: a lane a column, D / 8 dims a warp.
 template <int D, bool kHalf>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Kv8TreeParams p) {
-  constexpr int kN = D / 32;
+  constexpr int kN = D / 32;                             // four dims each
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, first = blockIdx.x, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = blockIdx.x, r = blockIdx.y * 32 + lane;
   const Shared s = reinterpret_cast<const Shared*>(p.arrived)[first];
-  if (s.last < 0) return;
   const int col = s.ct * kCols + r, j = (int)(((uint64_t)(uint32_t)col * p.group_inverse) >> 24);
-  if (col >= p.Q * p.group) return;
+  if (s.last < 0 || col >= p.Q * p.group) return;
   const int64_t row = ((int64_t)s.b * p.Q + j) * p.H + s.kvh * p.group + (col - j * p.group);
-  auto at = [&](int cta) { return (int64_t)(2 * cta + (cta == first ? s.slot : 0)) * kCols + r; };
+  auto slot = [&](int cta) { return (int64_t)(2 * cta + (cta == first ? s.slot : 0)); };
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
   float m = kNone, sum = 0.f;
-  for (int c = first + lane; c <= s.last; c += 32) m = fmaxf(m, ml[at(c)].x);
-  m = redux_max(m);
-  for (int c = first + lane; c <= s.last; c += 32) {
-    const float2 x = ml[at(c)];
+#pragma unroll 8
+  for (int c = first; c <= s.last; ++c) m = fmaxf(m, ml[slot(c) * kCols + r].x);
+#pragma unroll 8
+  for (int c = first; c <= s.last; ++c) {
+    const float2 x = ml[slot(c) * kCols + r];
     sum += x.y * ratio(x.x, m);
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  float o[kN] = {};
+  float4 o[kN] = {};
 #pragma unroll 4
   for (int c = first; c <= s.last; ++c) {
-    const float2 x = ml[at(c)];
+    const float2 x = ml[slot(c) * kCols + r];
     const float f = x.y * ratio(x.x, m) * inv;
-    const float* part = p.part_o + at(c) * D + lane * kN;
-    if constexpr (kN == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(part);
-      o[0] = fmaf(v.x, f, o[0]);
-      o[1] = fmaf(v.y, f, o[1]);
-      o[2] = fmaf(v.z, f, o[2]);
-      o[3] = fmaf(v.w, f, o[3]);
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(part);
-      o[0] = fmaf(v.x, f, o[0]);
-      o[1] = fmaf(v.y, f, o[1]);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const float4 v = reinterpret_cast<const float4*>(p.part_o)[(slot(c) * (D / 4) + warp * kN + k) * kCols + r];
+      o[k].x = fmaf(v.x, f, o[k].x);
+      o[k].y = fmaf(v.y, f, o[k].y);
+      o[k].z = fmaf(v.z, f, o[k].z);
+      o[k].w = fmaf(v.w, f, o[k].w);
     }
   }
-  uint32_t* to = reinterpret_cast<uint32_t*>(p.out + row * D + lane * kN);
+  uint2* to = reinterpret_cast<uint2*>(p.out + row * D + warp * kN * 4);
 #pragma unroll
-  for (int k = 0; k < kN / 2; ++k) to[k] = narrow2<kHalf>(o[2 * k], o[2 * k + 1]);
-  if (lane == 0) p.lse[row] = sum == 0.f ? neg_inf() : (m + log2f(sum)) * 0.69314718055994530942f;
+  for (int k = 0; k < kN; ++k) to[k] = make_uint2(narrow2<kHalf>(o[k].x, o[k].y), narrow2<kHalf>(o[k].z, o[k].w));
+  if (warp == 0) p.lse[row] = sum == 0.f ? neg_inf() : (m + log2f(sum)) * 0.69314718055994530942f;
 }
 
 template <int D, bool kHalf>
@@ -991,7 +959,7 @@ cudaError_t launch(const Kv8TreeParams& p, cudaStream_t stream) {
   cfg.numAttrs = 1;
   err = cudaLaunchKernelEx(&cfg, tree_kernel<D, kHalf>, p);
   if (err != cudaSuccess) return err;
-  cfg.gridDim = dim3((unsigned)p.ctas, kCols / 8, 1);
+  cfg.gridDim = dim3((unsigned)p.ctas, kCols / 32, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join_kernel<D, kHalf>, p);
