@@ -61,7 +61,6 @@ enum { kBarFeeders = 1, kBarSoftmax = 2, kBarQuarter = 3 };   // (one for each q
 
 template <int D, int kQ>
 struct Shape {
-  static constexpr int kQParts = kQ;
   static constexpr int kQImage = kCols * D;                     // bytes of a part
   static constexpr int kQBytes = kQ * kQImage;
   static constexpr int kCodes = kPageTokens * D;                // bytes of a page's keys, or values
@@ -334,7 +333,7 @@ struct Cta {
   // The unit's queries, and what its columns attend to.
   template <bool kHalf>
   __device__ void queries(const Walk& w, uint32_t buf) {
-    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = 32 / kAtOnce, kTogether = 4, kAhead = kRounds < 12 ? kRounds : 12;    // rounds whose chains, and loads, are under way together
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = 32 / kAtOnce, kTogether = 2, kAhead = 8;    // rounds whose chains, and loads, are under way together (little code: it is fetched once a unit)
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, sub = lane / kLanes, ch = lane % kLanes;
     const int ncols = p.Q * p.group, base = w.len - p.Q;
     auto node_of = [&](int col) { return (int)(((uint64_t)(uint32_t)col * p.group_inverse) >> 24); };   // col / group
@@ -524,13 +523,40 @@ struct Cta {
     float m, w, l;
     __device__ __forceinline__ bool none() const { return w == kNone; }
   };
+  // The first references of columns that have none, from a tile whose pages all columns attend to.
+  __device__ __forceinline__ void start(Refs& refs, int half, uint32_t s_at, float f, uint2 sc) {
+    const int warp = (threadIdx.x >> 5) & 3, r = threadIdx.x & 127;
+    float mz = neg_inf(), mw = neg_inf();
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+      uint32_t s[16];
+      tmem_ld16(s_at + 16 * b, s);
+      tmem_wait_ld();
+      float x = neg_inf();
+#pragma unroll
+      for (int k = 0; k < 16; k += 2) x = max3(x, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+      const float z = x == neg_inf() ? x : x * (f * __uint_as_float(((sc.x >> (8 * b)) & 0xFFu) << 23));
+      mz = fmaxf(mz, z);
+      mw = fmaxf(mw, z + (float)((int)((sc.y >> (8 * b)) & 0xFFu) - 127));
+    }
+    ctl->most[half][r] = make_float2(mz, mw);
+    bar_sync(kBarQuarter + warp, 64);
+    const float2 other = ctl->most[half ^ 1][r];
+    const float top = fmaxf(mz, other.x);
+    if (refs.none() && fabsf(top) < 1048576.f) {       // (none to speak of, or one beside which a scale would be rounded away: careful())
+      refs.m = ceilf(top);
+      refs.w = ceilf(fmaxf(mw, other.y)) - refs.m;
+    }
+    bar_sync(kBarQuarter + warp, 64);
+  }
+
   // A page's weights in the place of its scores, with whatever is rare: positions that the column does not attend to,
   // new references, and scores or scales so wide that sum and weights need an exponential each. Both halves' threads of
   // a quarter of the columns come here together. (at_rest: the barrier of the product before, or null; false: a wait gave up.)
   __device__ __noinline__ bool careful(Refs& refs, int half, uint32_t s_at, float f, uint2 sc, uint64_t mine, uint64_t* at_rest, uint32_t parity, uint32_t o_at) {
     Refs t = refs;
     const int warp = (threadIdx.x >> 5) & 3, r = threadIdx.x & 127;
-    float z[4], mz = neg_inf();
+    float z[4] = {}, mz = neg_inf();
     auto key_scale = [&](int b) { return f * __uint_as_float(((sc.x >> (8 * b)) & 0xFFu) << 23); };
     auto value_scale = [&](int b) { return (float)((int)((sc.y >> (8 * b)) & 0xFFu) - 127); };
     auto largest = [&](float m) {          // of the weights, against m
@@ -539,7 +565,8 @@ struct Cta {
       for (int b = 0; b < 4; ++b) w = fmaxf(w, (z[b] - m) + value_scale(b));
       return w;
     };
-#pragma unroll
+    // (kept as loops: code that runs a few times costs what its fetching costs)
+#pragma unroll 1
     for (int b = 0; b < 4; ++b) {
       uint32_t s[16];
       tmem_ld16(s_at + 16 * b, s);
@@ -548,8 +575,12 @@ struct Cta {
       float x = neg_inf();
 #pragma unroll
       for (int k = 0; k < 16; ++k) x = fmaxf(x, (in >> k) & 1 ? __uint_as_float(s[k]) : neg_inf());
-      z[b] = x == neg_inf() ? x : x * key_scale(b);
-      mz = fmaxf(mz, z[b]);
+      x = x == neg_inf() ? x : x * key_scale(b);
+      z[0] = b == 0 ? x : z[0];
+      z[1] = b == 1 ? x : z[1];
+      z[2] = b == 2 ? x : z[2];
+      z[3] = b == 3 ? x : z[3];
+      mz = fmaxf(mz, x);
     }
     ctl->most[half][r] = make_float2(mz, largest(t.m));
     bar_sync(kBarQuarter + warp, 64);
@@ -586,7 +617,6 @@ struct Cta {
         }
       }
     }
-    // (kept as a loop: code that runs a few times costs what its fetching costs)
 #pragma unroll 1
     for (int b = 0; b < 4; ++b) {
       uint32_t s[16], out[8];
@@ -637,18 +667,29 @@ struct Cta {
       // sum's units, and the smallest byte of a values' scale that one exponential will do for (256: none)
       float offset = 0.f, back = 0.f;
       int least_ev = 256;
-      for (int i = 0; ok && i < w.count; ++i) {
+      auto known = [&]() {
+        offset = kWeightScale - refs.w - refs.m;
+        back = ex2_approx(refs.w - kWeightScale);
+        const bool plain = fabsf(refs.m) < 1048576.f && fabsf(refs.w) < 100.f;
+        const float highest = redux_max(refs.w);
+        least_ev = __all_sync(kFull, plain) ? (int)highest - 80 + 127 : 256;
+      };
+      int t0 = (w.first + w.at) * kTile + half * kPageTokens;
+      for (int i = 0; ok && i < w.count; ++i, t0 += kTile) {
         ok = wait_warp(&ctl->full[ring.st], ring.phase) && wait_warp(&ctl->s_full[at.st], at.phase);
-        const int t0 = (w.first + w.at + i) * kTile + half * kPageTokens;
-        const bool page_ok = ((ctl->pages_ok[ring.st] >> half) & 1) != 0, whole = page_ok && t0 >= all_lo && t0 + kPageTokens <= base;
-        const uint2 sc = reinterpret_cast<const uint2*>(&ctl->scales[ring.st][half])[w.kvh & 1];
-        const uint32_t s_at = quarter + at.st * kTile + half * kPageTokens;
         tc_fence_after();
         if (!idle) {
+          const bool page_ok = ((ctl->pages_ok[ring.st] >> half) & 1) != 0, whole = ok && page_ok && t0 >= all_lo && t0 + kPageTokens <= base;
+          const uint2 sc = reinterpret_cast<const uint2*>(&ctl->scales[ring.st][half])[w.kvh & 1];
+          const uint32_t s_at = quarter + at.st * kTile + half * kPageTokens;
+          if (__builtin_expect(least_ev > 255, 0) && !bar_any(kBarQuarter + warp, 64, !whole)) {
+            start(refs, half, s_at, f, sc);
+            known();
+          }
           const uint32_t ev2 = __vminu2(__byte_perm(sc.y, 0u, 0x4140), __byte_perm(sc.y, 0u, 0x4342));
           uint32_t out[32];
           float more = 0.f, most = 0.f;
-          bool fits = ok && whole && (int)min(ev2 & 0xFFu, ev2 >> 16) >= least_ev;
+          const bool fits = whole && (int)min(ev2 & 0xFFu, ev2 >> 16) >= least_ev;
           // One exponential serves w and l where fp32 holds the one beside the other: the smallest that matters to l,
           // 2^-40, has a weight above 2^-120.
           if (fits) {
@@ -685,11 +726,7 @@ struct Cta {
             const uint64_t mine = whole ? ~0ull : (page_ok ? bits(lo == INT_MAX ? 64 : lo - t0, base - t0) | nodes_at(ctl->mask[buf][r], base, t0) : 0);
             // (both halves' warps of a quarter go on together, or give up together)
             ok = !bar_any(kBarQuarter + warp, 64, !careful(refs, half, s_at, f, sc, mine, i > 0 ? at_rest : nullptr, rest_phase, o_at));
-            offset = kWeightScale - refs.w - refs.m;
-            back = ex2_approx(refs.w - kWeightScale);
-            const bool plain = fabsf(refs.m) < 1048576.f && fabsf(refs.w) < 100.f;
-            const float highest = redux_max(refs.w);
-            least_ev = __all_sync(kFull, plain) ? (int)highest - 80 + 127 : 256;
+            known();
           }
           tmem_wait_st();
           tc_fence_before();
@@ -752,8 +789,6 @@ struct Cta {
           else reinterpret_cast<float2*>(p.part_ml)[slot * kCols + r] = make_float2(top, sum);
         }
       }
-      if (!full_unit && w.at == 0 && threadIdx.x == 256)
-        *shared = Shared{ranges.of(w.pos + kUnitCost + w.n - 1), second_slot(t_first, w.pos), w.b, w.kvh, w.ct};
       tc_fence_before();
       bar_sync(kBarSoftmax, kSoftmaxThreads);            // all have read O, the notes of NaN and each other's sums
       if (poisoned) {
@@ -763,6 +798,8 @@ struct Cta {
         bar_sync(kBarSoftmax, kSoftmaxThreads);
       }
       if (lane == 0) mbar_arrive(&ctl->done[buf]);
+      if (!full_unit && w.at == 0 && threadIdx.x == 256)
+        *shared = Shared{ranges.of(w.pos + kUnitCost + w.n - 1), second_slot(t_first, w.pos), w.b, w.kvh, w.ct};
     }
   }
 };
