@@ -7,11 +7,11 @@
 // r.) When no child is taken, the next token is drawn from r by its running sum.
 //
 // What bounds it. Every row of logits is read once, for its largest value and its sum of exponentials.
-// stats_kernel does that by chunks of 1,024 logits, a warp each, whose values stay in registers; the chunks'
-// sums are kept, since with them a token can be drawn by reading a single chunk again. walk_kernel has a CTA
-// a request (with draft distributions a cluster of eight, since what a refusal leaves is a sum over the
-// vocabulary): all nodes' probabilities are found at once, so that the walk itself is a few comparisons.
-// Sums over chunks, and what is compared, are in 64 bits: the results are whole numbers.
+// stats_kernel does that by chunks of 4 KB, a warp each, whose values stay in registers; the chunks' sums are
+// kept, since with them a token can be drawn by reading a single chunk again. walk_kernel has a CTA a request
+// (with draft distributions a cluster of eight, since what a refusal leaves is a sum over the vocabulary): all
+// nodes' probabilities are found at once, so that the walk itself is a few comparisons. Sums over chunks, and
+// what is compared, are in 64 bits: the results are whole numbers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -26,26 +26,48 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kChunk = 1024;           // logits
+constexpr int kChunkBytes = 4096;      // of a row that a warp takes: eight 16-byte loads a lane, all in flight
 constexpr int kStatsThreads = 256;
-constexpr int kWalkThreads = 256, kWalkWarps = kWalkThreads / 32;
 constexpr int kWalkCtas = 8;           // of a request, with draft distributions
 constexpr int kMaxNodes = 64;
 constexpr unsigned kFull = 0xFFFFFFFFu;
+
+template <typename T>
+struct Vec {
+  static constexpr int kN = 16 / (int)sizeof(T);           // logits of a load
+  static constexpr int kChunk = kChunkBytes / (int)sizeof(T);
+  static constexpr int kLoads = kChunkBytes / (32 * 16);
+};
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-// A NaN is no candidate.
-template <typename T>
-__device__ __forceinline__ float logit(T x) {
-  const float v = as_float(x);
-  return v != v ? neg_inf() : v;
+// The logits of a load as they are.
+__device__ __forceinline__ void widen(const uint4& w, float (&x)[4], const float*) {
+  x[0] = __uint_as_float(w.x);
+  x[1] = __uint_as_float(w.y);
+  x[2] = __uint_as_float(w.z);
+  x[3] = __uint_as_float(w.w);
 }
+template <typename T>
+__device__ __forceinline__ void widen(const uint4& w, float (&x)[8], const T*) {
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float2 two;
+    if constexpr (sizeof(T) == 2 && __is_same(T, __half)) two = __half22float2(*reinterpret_cast<const __half2*>(&ws[k]));
+    else two = make_float2(__uint_as_float(ws[k] << 16), __uint_as_float(ws[k] & 0xFFFF0000u));
+    x[2 * k] = two.x;
+    x[2 * k + 1] = two.y;
+  }
+}
+// A NaN is no candidate.
+__device__ __forceinline__ float clean(float v) { return v != v ? neg_inf() : v; }
 
 // log2(e) / temperature as hi + lo: rounded to one fp32, its error would grow with a logit's distance from the
-// largest. hi < 0: greedy, which is asked for by 0 (and by what is no temperature).
+// largest. lo > 0, so that an infinite distance stays one. hi < 0: greedy, which is asked for by 0 (and by what is no
+// temperature).
 struct Rate {
   float hi, lo;
 };
@@ -53,9 +75,10 @@ __device__ __forceinline__ Rate rate_of(const VerifyParams& p, int b) {
   const float t = p.temperatures != nullptr ? p.temperatures[b] : 1.f;
   if (!(t > 0.f)) return Rate{-1.f, 0.f};
   constexpr float kHi = 1.4426950408889634f, kLo = (float)(1.4426950408889634 - (double)kHi);
-  const float hi = kHi / t;
-  if (!(hi < 3e38f)) return Rate{3e38f, 0.f};
-  return Rate{hi, (fmaf(-hi, t, kHi) + kLo) / t};
+  float hi = kHi / t;
+  if (!(hi < 3e38f)) return Rate{3e38f, 1e-38f};
+  if (hi > 1e-30f) hi = __uint_as_float(__float_as_uint(hi) - 1);        // at or below the quotient
+  return Rate{hi, fmaxf((fmaf(-hi, t, kHi) + kLo) / t, 1e-38f)};
 }
 // exp((x - m) / T) for x <= m; 0 for x = -inf, 1 for x = m whatever they are.
 __device__ __forceinline__ float weight(float x, float m, Rate rate) {
@@ -63,86 +86,113 @@ __device__ __forceinline__ float weight(float x, float m, Rate rate) {
   return x == neg_inf() ? 0.f : (x == m ? 1.f : ex2_approx(fmaf(d, rate.hi, d * rate.lo)));
 }
 
-template <typename T>
-struct Vec {
-  static constexpr int kN = 16 / (int)sizeof(T);
-};
-
 // A row's chunks begin at 16-byte boundaries, so that the first may begin before the row.
 template <typename T>
 __device__ __forceinline__ int lead_of(const T* row) {
   return (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
 }
-// The kN logits from `at` on, -inf outside of the row.
 template <typename T>
-__device__ __forceinline__ void load_vec(const T* row, int64_t at, int64_t V, float (&x)[Vec<T>::kN]) {
-  constexpr int kN = Vec<T>::kN;
-  if (at >= 0 && at + kN <= V) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + at));
-    const T* t = reinterpret_cast<const T*>(&w);
-#pragma unroll
-    for (int k = 0; k < kN; ++k) x[k] = logit(t[k]);
-  } else {
-#pragma unroll
-    for (int k = 0; k < kN; ++k) x[k] = at + k >= 0 && at + k < V ? logit(row[at + k]) : neg_inf();
-  }
+__device__ __forceinline__ int chunks_of(const T* row, int V) {
+  return (int)(((int64_t)V + lead_of(row) + Vec<T>::kChunk - 1) / Vec<T>::kChunk);
+}
+// The load from logit `at` on, -inf outside of the row.
+template <typename T>
+__device__ __forceinline__ uint4 load_vec(const T* row, int64_t at, int64_t V) {
+  if (at >= 0 && at + Vec<T>::kN <= V) return __ldg(reinterpret_cast<const uint4*>(row + at));
+  constexpr uint32_t kInf = sizeof(T) == 4 ? 0xff800000u : (__is_same(T, __half) ? 0xfc00fc00u : 0xff80ff80u);
+  uint4 w = make_uint4(kInf, kInf, kInf, kInf);
+  T* t = reinterpret_cast<T*>(&w);
+  for (int k = 0; k < Vec<T>::kN; ++k)
+    if (at + k >= 0 && at + k < V) t[k] = row[at + k];
+  return w;
 }
 
-__device__ __forceinline__ bool is_node(const VerifyParams& p, int64_t row) {
-  const int j = (int)(row % p.Q);
+__device__ __forceinline__ bool is_node(const VerifyParams& p, int row) {
+  const int j = row % p.Q;
   if (j == 0) return true;
   const int up = p.parents[row];
   return up >= 0 && up < j;
 }
 
+// The largest, whatever a NaN beside it.
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// A chunk's largest logit, and the sum of its exponentials against that; greedy: where the largest is first.
 template <typename T>
-__global__ void __launch_bounds__(kStatsThreads) stats_kernel(const VerifyParams p) {
-  constexpr int kN = Vec<T>::kN, kLoads = kChunk / (32 * kN);
+__global__ void __launch_bounds__(kStatsThreads) stats_kernel(const __grid_constant__ VerifyParams p) {
+  using V = Vec<T>;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * (kStatsThreads / 32) + (threadIdx.x >> 5);
-  const int64_t r = item / p.chunks;
-  const int chunk = (int)(item - r * p.chunks);
-  if (r >= (int64_t)p.B * p.Q || !is_node(p, r)) return;
-  const T* row = static_cast<const T*>(p.logits) + r * p.row_stride;
-  const int64_t at = (int64_t)chunk * kChunk - lead_of(row);
-  if (at >= p.V) return;
-  float x[kLoads][kN];
+  const int r = blockIdx.x, chunk = blockIdx.y * (kStatsThreads / 32) + (threadIdx.x >> 5);
+  const T* row = static_cast<const T*>(p.logits) + (int64_t)r * p.row_stride;
+  const int64_t at = (int64_t)chunk * V::kChunk - lead_of(row);
+  if (at >= p.V || !is_node(p, r)) return;
+  uint4 w[V::kLoads];
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) load_vec(row, at + (i * 32 + lane) * kN, p.V, x[i]);
-  const Rate rate = rate_of(p, (int)(r / p.Q));
+  for (int i = 0; i < V::kLoads; ++i) w[i] = load_vec(row, at + (i * 32 + lane) * V::kN, p.V);
+  const Rate rate = rate_of(p, r / p.Q);
   float m = neg_inf();
-  int where = INT_MAX;
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i)
+  for (int i = 0; i < V::kLoads; ++i) {
+    float x[V::kN];
+    widen(w[i], x, row);
 #pragma unroll
-    for (int k = 0; k < kN; ++k)
-      if (x[i][k] > m) {
-        m = x[i][k];
-        where = (int)(at + (i * 32 + lane) * kN + k);
-      }
+    for (int k = 0; k < V::kN; ++k) m = fmaxf(m, x[k]);
+  }
+  m = warp_max(m);
+  const int64_t to = (int64_t)r * p.chunks + chunk;
+  if (rate.hi < 0.f) {
+    int where = INT_MAX;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    const float om = __shfl_xor_sync(kFull, m, d);
-    const int ow = __shfl_xor_sync(kFull, where, d);
-    if (om > m || (om == m && ow < where)) {
-      m = om;
-      where = ow;
+    for (int i = V::kLoads - 1; i >= 0; --i) {
+      float x[V::kN];
+      widen(w[i], x, row);
+#pragma unroll
+      for (int k = V::kN - 1; k >= 0; --k) where = x[k] == m ? (int)(at + (i * 32 + lane) * V::kN + k) : where;
     }
+    where = __reduce_min_sync(kFull, where);
+    if (lane == 0) {
+      p.chunk_ms[to] = make_float2(m, 0.f);
+      p.chunk_at[to] = where;
+    }
+    return;
   }
   float sum = 0.f;
-  if (rate.hi >= 0.f) {
+  if (fabsf(m) < __int_as_float(0x7f800000)) {
+    const float2 less = make_float2(-m, -m), hi = make_float2(rate.hi, rate.hi), lo = make_float2(rate.lo, rate.lo);
+    float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
+    for (int i = 0; i < V::kLoads; ++i) {
+      float x[V::kN];
+      widen(w[i], x, row);
 #pragma unroll
-      for (int k = 0; k < kN; ++k) sum += weight(x[i][k], m, rate);
+      for (int k = 0; k < V::kN; k += 2) {
+        const float2 d = __fadd2_rn(make_float2(x[k], x[k + 1]), less);
+        const float2 e = __ffma2_rn(d, hi, __fmul2_rn(d, lo));
+        part[(k >> 1) & 1] = __fadd2_rn(part[(k >> 1) & 1], make_float2(ex2_approx(e.x), ex2_approx(e.y)));
+      }
+    }
+    sum = (part[0].x + part[0].y) + (part[1].x + part[1].y);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
   }
-  if (lane == 0) {
-    p.chunk_ms[r * p.chunks + chunk] = make_float2(m, sum);
-    p.chunk_at[r * p.chunks + chunk] = where;
+  if (!(sum > 0.f) || !(fabsf(m) < __int_as_float(0x7f800000))) {
+    // a NaN, or infinities
+    sum = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < V::kLoads; ++i) {
+      float x[V::kN];
+      widen(load_vec(row, at + (i * 32 + lane) * V::kN, p.V), x, row);
+      for (int k = 0; k < V::kN; ++k) sum += weight(clean(x[k]), m, rate);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
   }
+  if (lane == 0) p.chunk_ms[to] = make_float2(m, sum);
 }
 
 struct WalkShared {
@@ -155,12 +205,15 @@ struct WalkShared {
   float u[kMaxNodes];
   double left[kMaxNodes];              // s before each refusal at the current node
   int out[kMaxNodes];                  // tokens that were refused there
-  double sum;
-  int pick;
+  double sum;                          // of what is left
+  // the walk
+  int at, count, refused, next_node, ends;
 };
 
-template <typename T, bool kProbs>
+template <typename T, bool kProbs, int kThreads>
 struct Walker {
+  using V = Vec<T>;
+  static constexpr int kWarps = kThreads / 32;
   const VerifyParams& p;
   WalkShared& sh;
   int b, rank, ctas;
@@ -168,173 +221,259 @@ struct Walker {
 
   __device__ const T* row_of(int j) const { return static_cast<const T*>(p.logits) + ((int64_t)b * p.Q + j) * p.row_stride; }
   __device__ const float* probs_of(int j) const { return p.probs + ((int64_t)b * p.Q + j) * p.probs_stride; }
-  __device__ int chunks_of(int j) const { return (int)((p.V + lead_of(row_of(j)) + kChunk - 1) / kChunk); }
 
-  // What is left of node j's probability of a token after `refused` refusals, times the node's sum of exponentials
-  // without draft distributions (an order of magnitude that a draw does not need).
-  __device__ float rest(int j, float w, int64_t at, float inv, int refused) const {
+  // A load's worth of what is left at node j, from logit `at` on: with draft distributions r after `refused` refusals,
+  // else the exponentials, but for the refused tokens'.
+  __device__ __forceinline__ void rest(int j, const uint4& w, int64_t at, float m, float inv, int refused, float (&x)[V::kN]) const {
+    widen(w, x, static_cast<const T*>(nullptr));
+#pragma unroll
+    for (int k = 0; k < V::kN; ++k) x[k] = weight(clean(x[k]), m, rate);
     if constexpr (kProbs) {
-      float r = w * inv;
-      if (refused > 0 && at >= 0 && at < p.V) {
-        const float q = __ldg(probs_of(j) + at);
-        for (int i = 0; i < refused; ++i) r = fmaxf(r - (float)sh.left[i] * q, 0.f);
+#pragma unroll
+      for (int k = 0; k < V::kN; ++k) x[k] *= inv;
+      if (refused == 0) return;
+      float q[V::kN];
+      const float* from = probs_of(j) + at;
+      if (at >= 0 && at + V::kN <= p.V && (reinterpret_cast<uintptr_t>(from) & 15) == 0) {
+#pragma unroll
+        for (int k = 0; k < V::kN; k += 4) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(from + k));
+          q[k] = v.x;
+          q[k + 1] = v.y;
+          q[k + 2] = v.z;
+          q[k + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < V::kN; ++k) q[k] = at + k >= 0 && at + k < p.V ? __ldg(from + k) : 0.f;
       }
-      return r;
+#pragma unroll 1
+      for (int i = 0; i < refused; ++i) {
+        const float s = (float)sh.left[i];
+#pragma unroll
+        for (int k = 0; k < V::kN; ++k) x[k] = fmaxf(x[k] - s * q[k], 0.f);
+      }
     } else {
-      for (int i = 0; i < refused; ++i) w = sh.out[i] == at ? 0.f : w;
-      return w;
+#pragma unroll 1
+      for (int i = 0; i < refused; ++i) {
+        const int64_t k0 = sh.out[i] - at;
+#pragma unroll
+        for (int k = 0; k < V::kN; ++k) x[k] = k0 == k ? 0.f : x[k];
+      }
     }
   }
 
-  // A chunk's rest by one warp, lane by lane; the sum in every lane.
+  // A chunk's rest by one warp, all of its loads in flight; the sum in every lane.
   __device__ double chunk_rest(int j, int chunk, float m, float inv, int refused) const {
-    constexpr int kN = Vec<T>::kN, kLoads = kChunk / (32 * kN);
     const int lane = threadIdx.x & 31;
     const T* row = row_of(j);
-    const int64_t at = (int64_t)chunk * kChunk - lead_of(row);
-    double sum = 0.;
-    for (int i = 0; i < kLoads; ++i) {
-      float x[kN], part = 0.f;
-      const int64_t from = at + (i * 32 + lane) * kN;
-      load_vec(row, from, p.V, x);
+    const int64_t at = (int64_t)chunk * V::kChunk - lead_of(row) + lane * V::kN;
+    uint4 w[V::kLoads];
 #pragma unroll
-      for (int k = 0; k < kN; ++k) part += rest(j, weight(x[k], m, rate), from + k, inv, refused);
+    for (int i = 0; i < V::kLoads; ++i) w[i] = load_vec(row, at + i * 32 * V::kN, p.V);
+    float sum = 0.f;
+#pragma unroll 2
+    for (int i = 0; i < V::kLoads; ++i) {
+      float x[V::kN];
+      uint4 v = w[0];
+#pragma unroll
+      for (int n = 1; n < V::kLoads; ++n) v = n == i ? w[n] : v;
+      rest(j, v, at + i * 32 * V::kN, m, inv, refused, x);
+      float part = 0.f;
+#pragma unroll
+      for (int k = 0; k < V::kN; ++k) part += x[k];
       sum += part;
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
-    return sum;
+    return (double)sum;
   }
 
   __device__ void everyone() const {
-    __syncthreads();
     if (ctas > 1) cluster_sync_all();
+    else __syncthreads();
   }
 
-  // Sums of the chunks of what is left at node j, into chunk_sum; their sum, the same in every CTA.
-  __device__ double sums(int j, int refused) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chunks = chunks_of(j);
+  // Sums of the chunks of what is left at node j, into chunk_sum, and their sum into sh.sum: the same in every CTA.
+  __device__ void sums(int j, int refused) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const T* row = row_of(j);
+    const int chunks = chunks_of(row, p.V);
     double* to = p.chunk_sum + (int64_t)b * p.chunks;
     const float m = sh.top[j], inv = (float)(1. / sh.total[j]);
     if (kProbs && refused > 0) {
-      for (int c = rank * kWalkWarps + warp; c < chunks; c += ctas * kWalkWarps) {
+      for (int c = rank * kWarps + warp; c < chunks; c += ctas * kWarps) {
         const double s = chunk_rest(j, c, m, inv, refused);
         if (lane == 0) to[c] = s;
       }
-    } else {
+    } else if (rank == 0) {
       // the chunks' sums, and again where a refused token lies
       const int64_t first = ((int64_t)b * p.Q + j) * p.chunks;
       const float scale = kProbs ? inv : 1.f;
-      if (rank == 0) {
-        for (int c = threadIdx.x; c < chunks; c += kWalkThreads) {
-          const float2 ms = __ldcg(p.chunk_ms + first + c);
-          to[c] = (double)(ms.y * weight(ms.x, m, rate)) * scale;
-        }
-        if (!kProbs) {
-          __syncthreads();
-          const int lead = lead_of(row_of(j));
-          for (int i = warp; i < refused; i += kWalkWarps) {
-            const int c = (sh.out[i] + lead) / kChunk;
-            const double s = chunk_rest(j, c, m, inv, refused);     // (two refused tokens of a chunk: the same sum twice)
-            if (lane == 0) to[c] = s;
-          }
+      for (int c = threadIdx.x; c < chunks; c += kThreads) {
+        const float2 ms = __ldcg(p.chunk_ms + first + c);
+        to[c] = (double)(ms.y * weight(ms.x, m, rate) * scale);
+      }
+      if (!kProbs && refused > 0) {
+        __syncthreads();
+        const int lead = lead_of(row);
+        for (int i = warp; i < refused; i += kWarps) {
+          const int c = (sh.out[i] + lead) / V::kChunk;
+          const double s = chunk_rest(j, c, m, inv, refused);     // (two refused tokens of a chunk: the same sum twice)
+          if (lane == 0) to[c] = s;
         }
       }
     }
     everyone();
     if (warp == 0) {
       double s = 0.;
-      for (int c = lane; c < chunks; c += 32) s += __ldcg(to + c);
+      const int per = (chunks + 31) / 32;
+#pragma unroll 4
+      for (int i = 0; i < per; ++i) s += lane * per + i < chunks ? __ldcg(to + lane * per + i) : 0.;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
       if (lane == 0) sh.sum = s;
     }
-    __syncthreads();
-    const double s = sh.sum;
     everyone();                          // nobody writes the sums again before all have read them
-    return s;
   }
 
-  // The first token whose running sum of what is left at node j exceeds `share` of it all: warp 0 of the first CTA.
+  // An inclusive sum over the lanes.
+  static __device__ __forceinline__ double scan(double x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const double o = __shfl_up_sync(kFull, x, d);
+      if (lane >= d) x += o;
+    }
+    return x;
+  }
+
+  // The first token whose running sum of what is left at node j exceeds `share` of it all: one warp.
   __device__ int draw(int j, double share, double total, int refused) {
-    constexpr int kN = Vec<T>::kN, kLoads = kChunk / (32 * kN);
-    const int lane = threadIdx.x & 31, chunks = chunks_of(j);
+    const int lane = threadIdx.x & 31;
+    const T* row = row_of(j);
+    const int chunks = chunks_of(row, p.V), per = (chunks + 31) / 32;
     const double* of = p.chunk_sum + (int64_t)b * p.chunks;
     const double want = share * total;
-    double before = 0.;
-    int chunk = -1, last = -1;
-    double last_before = 0.;
-    for (int c0 = 0; c0 < chunks && chunk < 0; c0 += 32) {
-      const double mine = c0 + lane < chunks ? __ldcg(of + c0 + lane) : 0.;
-      double incl = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const double o = __shfl_up_sync(kFull, incl, d);
-        if (lane >= d) incl += o;
+    // a lane a run of chunks, then the run's chunks one by one; where none is past it, the last that has anything
+    double mine = 0.;
+#pragma unroll 4
+    for (int i = 0; i < per; ++i) mine += lane * per + i < chunks ? __ldcg(of + lane * per + i) : 0.;
+    const double incl = scan(mine);
+    unsigned past = __ballot_sync(kFull, mine > 0. && incl > want);
+    const unsigned some = __ballot_sync(kFull, mine > 0.);
+    if (some == 0) return -1;
+    const int who = past != 0 ? __ffs(past) - 1 : 31 - __clz(some);
+    double before = incl - mine, at_before = 0.;
+    int chunk = -1;
+    for (int i = 0; i < per; ++i) {
+      const double s = lane * per + i < chunks ? __ldcg(of + lane * per + i) : 0.;
+      if (s > 0. && (chunk < 0 || !(at_before > want))) {
+        // (at_before: up to the end of the chunk that is held)
+        chunk = lane * per + i;
+        at_before = before + s;
       }
-      const unsigned some = __ballot_sync(kFull, mine > 0.), past = __ballot_sync(kFull, mine > 0. && before + incl > want);
-      const int at = past != 0 ? __ffs(past) - 1 : (some != 0 ? 31 - __clz(some) : -1);
-      if (at >= 0) {
-        const double upto = __shfl_sync(kFull, incl - mine, at);
-        last = c0 + at;
-        last_before = before + upto;
-        if (past != 0) chunk = last;
-      }
-      before += __shfl_sync(kFull, incl, 31);
+      before += s;
     }
-    chunk = last;                        // (none past it: the last that has anything)
-    if (chunk < 0) return -1;
-    const T* row = row_of(j);
-    const int64_t at = (int64_t)chunk * kChunk - lead_of(row);
+    chunk = __shfl_sync(kFull, chunk, who);
+    // what lies before the chunk, as the scan has it
+    double upto = 0.;
+    for (int i = 0; i < per; ++i) upto += lane * per + i < chunk ? __ldcg(of + lane * per + i) : 0.;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) upto += __shfl_xor_sync(kFull, upto, d);
+
+    const int64_t at = (int64_t)chunk * V::kChunk - lead_of(row) + lane * V::kN;
     const float m = sh.top[j], inv = (float)(1. / sh.total[j]);
-    before = last_before;
+    uint4 w[V::kLoads];
+#pragma unroll
+    for (int i = 0; i < V::kLoads; ++i) w[i] = load_vec(row, at + i * 32 * V::kN, p.V);
     int found = -1;
-    for (int i = 0; i < kLoads; ++i) {
-      float x[kN];
-      const int64_t from = at + (i * 32 + lane) * kN;
-      load_vec(row, from, p.V, x);
+#pragma unroll 1
+    for (int i = 0; i < V::kLoads; ++i) {
+      float x[V::kN];
+      uint4 v = w[0];
+#pragma unroll
+      for (int n = 1; n < V::kLoads; ++n) v = n == i ? w[n] : v;
+      const int64_t from = at + i * 32 * V::kN;
+      rest(j, v, from, m, inv, refused, x);
       double part = 0.;
 #pragma unroll
-      for (int k = 0; k < kN; ++k) {
-        x[k] = rest(j, weight(x[k], m, rate), from + k, inv, refused);
-        part += x[k];
-      }
-      double incl = part;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const double o = __shfl_up_sync(kFull, incl, d);
-        if (lane >= d) incl += o;
-      }
+      for (int k = 0; k < V::kN; ++k) part += (double)x[k];
+      const double upto_here = scan(part);
       // this lane's first token past `want`, else its last that has anything
-      double run = before + incl - part;
-      int mine = -1;
-      bool past = false;
+      double run = upto + upto_here - part;
+      int token = -1;
+      bool is_past = false;
 #pragma unroll
-      for (int k = 0; k < kN; ++k) {
-        run += x[k];
-        if (x[k] > 0.f && !past) {
-          mine = (int)(from + k);
-          past = run > want;
+      for (int k = 0; k < V::kN; ++k) {
+        run += (double)x[k];
+        if (x[k] > 0.f && !is_past) {
+          token = (int)(from + k);
+          is_past = run > want;
         }
       }
-      const unsigned some = __ballot_sync(kFull, mine >= 0), hit = __ballot_sync(kFull, past);
-      if (some != 0) found = __shfl_sync(kFull, mine, hit != 0 ? __ffs(hit) - 1 : 31 - __clz(some));
+      const unsigned any = __ballot_sync(kFull, token >= 0), hit = __ballot_sync(kFull, is_past);
+      if (any != 0) found = __shfl_sync(kFull, token, hit != 0 ? __ffs(hit) - 1 : 31 - __clz(any));
       if (hit != 0) break;
-      before += __shfl_sync(kFull, incl, 31);
+      upto += __shfl_sync(kFull, upto_here, 31);
     }
     return found;
   }
+
+  // From where the walk stands to its end, or to a refusal behind which a sum is needed: one thread. left: s of what is left.
+  __device__ void walk(bool greedy, double left) {
+    int at = sh.at, count = sh.count, refused = sh.refused, j = sh.next_node;
+    for (; j < p.Q; ++j) {
+      if (sh.parent[j] != at) continue;
+      bool yes;
+      if (greedy) {
+        yes = sh.best[at] == sh.token[j];
+      } else {
+        if (kProbs && left < 0.) break;      // another child after a refusal: s is that of what is left
+        double r = sh.have[j];
+        const double q = sh.drawn[j];
+        for (int i = 0; i < refused; ++i) {
+          if (kProbs) r = fmax(r - sh.left[i] * q, 0.);
+          else if (sh.out[i] == sh.token[j]) r = 0.;
+        }
+        yes = (double)sh.u[j] * q * left < r;
+        if (!yes) {
+          sh.left[refused] = left;
+          sh.out[refused++] = sh.token[j];
+          left = kProbs ? -1. : left - r;
+        }
+      }
+      if (yes) {
+        if (rank == 0) {
+          p.path[(int64_t)b * p.Q + count] = j;
+          p.tokens[(int64_t)b * p.Q + count] = sh.token[j];
+        }
+        ++count;
+        at = j;
+        refused = 0;
+        left = 1.;
+      }
+    }
+    sh.at = at;
+    sh.count = count;
+    sh.refused = refused;
+    sh.next_node = j;
+    sh.ends = j >= p.Q;
+  }
 };
 
-template <typename T, bool kProbs>
-__global__ void __launch_bounds__(kWalkThreads) walk_kernel(const VerifyParams p) {
+template <typename T, bool kProbs, int kThreads>
+__global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ VerifyParams p) {
+  constexpr int kWarps = kThreads / 32;
   __shared__ WalkShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ctas = kProbs ? kWalkCtas : 1, b = blockIdx.x / ctas, rank = kProbs ? (int)cluster_ctarank() : 0;
   const int Q = p.Q;
   const Rate rate = rate_of(p, b);
   const bool greedy = rate.hi < 0.f;
+  Walker<T, kProbs, kThreads> w{p, sh, b, rank, ctas, rate};
   bool bad = false;
+  float logit = 0.f;
   if (tid < Q) {
     const int64_t r = (int64_t)b * Q + tid;
     int up = tid == 0 ? -1 : p.parents[r];
@@ -345,115 +484,79 @@ __global__ void __launch_bounds__(kWalkThreads) walk_kernel(const VerifyParams p
     }
     sh.parent[tid] = up;
     sh.token[tid] = x;
-    sh.u[tid] = fmaxf(p.uniforms[r], 0.f);
-    if (!(p.uniforms[r] == p.uniforms[r])) sh.u[tid] = __int_as_float(0x7f800000);
+    const float u = p.uniforms[r];
+    sh.u[tid] = u == u ? fmaxf(u, 0.f) : __int_as_float(0x7f800000);
+    sh.drawn[tid] = kProbs && up >= 0 ? __ldg(w.probs_of(up) + x) : 1.f;
+    if (up >= 0) logit = clean(as_float(w.row_of(up)[x]));
+  }
+  if (tid == 0) {
+    sh.at = sh.count = sh.refused = 0;
+    sh.next_node = 1;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // nodes' largest logits and sums, a warp a node
-  for (int j = warp; j < Q; j += kWalkWarps) {
-    if (!is_node(p, (int64_t)b * Q + j)) continue;
+  for (int j = warp; j < Q; j += kWarps) {
+    if (!is_node(p, b * Q + j)) continue;
     const int64_t first = ((int64_t)b * Q + j) * p.chunks;
-    const T* row = static_cast<const T*>(p.logits) + ((int64_t)b * Q + j) * p.row_stride;
-    const int chunks = (int)((p.V + lead_of(row) + kChunk - 1) / kChunk);
+    const int chunks = chunks_of(w.row_of(j), p.V);
     float m = neg_inf();
-    int where = INT_MAX;
-    for (int c = lane; c < chunks; c += 32) {
-      const float2 ms = __ldcg(p.chunk_ms + first + c);
-      if (ms.x > m) {
-        m = ms.x;
-        where = __ldcg(p.chunk_at + first + c);
-      }
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      const float om = __shfl_xor_sync(kFull, m, d);
-      const int ow = __shfl_xor_sync(kFull, where, d);
-      if (om > m || (om == m && ow < where)) {
-        m = om;
-        where = ow;
-      }
-    }
     double sum = 0.;
-    if (!greedy)
-      for (int c = lane; c < chunks; c += 32) {
-        const float2 ms = __ldcg(p.chunk_ms + first + c);
-        sum += ms.y * weight(ms.x, m, rate);
+    int where = INT_MAX;
+    for (int c0 = 0; c0 < chunks; c0 += 128) {           // four loads in flight
+      float2 ms[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ms[i] = c0 + i * 32 + lane < chunks ? __ldcg(p.chunk_ms + first + c0 + i * 32 + lane) : make_float2(neg_inf(), 0.f);
+      const float now = warp_max(fmaxf(fmaxf(m, fmaxf(ms[0].x, ms[1].x)), fmaxf(ms[2].x, ms[3].x)));
+      if (greedy) {
+        if (now > m) {
+#pragma unroll
+          for (int i = 3; i >= 0; --i) where = ms[i].x == now ? c0 + i * 32 + lane : where;
+          where = __reduce_min_sync(kFull, ms[0].x == now || ms[1].x == now || ms[2].x == now || ms[3].x == now ? where : INT_MAX);
+        }
+      } else {
+        float part = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part += ms[i].y * weight(ms[i].x, now, rate);
+        sum = sum * (double)weight(m, now, rate) + (double)part;
       }
+      m = now;
+    }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
     if (lane == 0) {
       sh.top[j] = m;
       sh.total[j] = sum;
-      sh.best[j] = m == neg_inf() ? -1 : where;
+      sh.best[j] = greedy && m != neg_inf() ? __ldcg(p.chunk_at + first + where) : -1;
     }
   }
   __syncthreads();
-  Walker<T, kProbs> w{p, sh, b, rank, ctas, rate};
-  if (tid < Q && sh.parent[tid] >= 0) {
-    const int up = sh.parent[tid], x = sh.token[tid];
-    const float l = logit(w.row_of(up)[x]), m = sh.top[up];
-    double have = 0.;
-    if (!greedy && l != neg_inf()) have = (l == m ? 1. : exp2(((double)l - (double)m) * ((double)rate.hi + (double)rate.lo))) / sh.total[up];
-    sh.have[tid] = have;
-    sh.drawn[tid] = kProbs ? __ldg(w.probs_of(up) + x) : 1.f;
+  if (tid < Q && sh.parent[tid] >= 0 && !greedy) {
+    const int up = sh.parent[tid];
+    const float m = sh.top[up], d = logit - m, a = d * rate.hi;
+    // exp2 of a, and of what rounding took from it
+    double have = logit == neg_inf() ? 0. : (logit == m ? 1. : (double)exp2f(a) * (1. + 0.6931471805599453 * (double)(fmaf(d, rate.hi, -a) + d * rate.lo)));
+    sh.have[tid] = have / sh.total[up];
   }
   __syncthreads();
-
-  // the walk, the same in every thread
-  int at = 0, count = 0, refused = 0;
-  double left = 1.;
-  bool known = true;                     // left is that of what is left now
-  for (int j = 1; j < Q; ++j) {
-    if (sh.parent[j] != at) continue;
-    bool yes;
-    if (greedy) {
-      yes = sh.best[at] == sh.token[j];
-    } else {
-      if constexpr (kProbs) {
-        if (!known) {
-          left = w.sums(at, refused);
-          known = true;
-        }
-      }
-      double r = sh.have[j];
-      const double q = sh.drawn[j];
-      for (int i = 0; i < refused; ++i) {
-        if (kProbs) r = fmax(r - sh.left[i] * q, 0.);
-        else if (sh.out[i] == sh.token[j]) r = 0.;
-      }
-      yes = (double)sh.u[j] * q * left < r;
-      if (!yes) {
-        __syncthreads();                 // (the lists below have been read)
-        if (tid == 0) {
-          sh.left[refused] = left;
-          sh.out[refused] = sh.token[j];
-        }
-        __syncthreads();
-        ++refused;
-        if (kProbs) known = false;
-        else left -= r;
-      }
-    }
-    if (yes) {
-      if (rank == 0 && tid == 0) {
-        p.path[(int64_t)b * Q + count] = j;
-        p.tokens[(int64_t)b * Q + count] = sh.token[j];
-      }
-      ++count;
-      at = j;
-      refused = 0;
-      left = 1.;
-      known = true;
+  if (tid == 0) w.walk(greedy, 1.);
+  __syncthreads();
+  if constexpr (kProbs) {
+    while (!sh.ends) {
+      const int at = sh.at, refused = sh.refused;
+      w.sums(at, refused);
+      if (tid == 0) w.walk(greedy, sh.sum);
+      __syncthreads();
     }
   }
-  int next = greedy ? sh.best[at] : -1;
+  const int at = sh.at, count = sh.count;
+  int refused = sh.refused, next = greedy ? sh.best[at] : -1;
   if (!greedy && sh.top[at] != neg_inf()) {
-    double total = w.sums(at, refused);
-    if (!(total > 0.) && refused > 0) {  // nothing is left: from the target's own
+    w.sums(at, refused);
+    if (!(sh.sum > 0.) && refused > 0) {   // nothing is left: from the target's own
       refused = 0;
-      total = w.sums(at, 0);
+      w.sums(at, 0);
     }
-    if (warp == 0 && rank == 0) next = w.draw(at, (double)sh.u[0], total, refused);
+    if (warp == 0 && rank == 0) next = w.draw(at, (double)sh.u[0], sh.sum, refused);
   }
   if (rank == 0) {
     if (tid == 0) {
@@ -469,16 +572,11 @@ __global__ void __launch_bounds__(kWalkThreads) walk_kernel(const VerifyParams p
   }
 }
 
-template <typename T>
-cudaError_t launch(const VerifyParams& p, cudaStream_t stream) {
-  const int64_t warps = (int64_t)p.B * p.Q * p.chunks;
-  stats_kernel<T><<<(unsigned)((warps + kStatsThreads / 32 - 1) / (kStatsThreads / 32)), kStatsThreads, 0, stream>>>(p);
-  cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
-  const bool probs = p.probs != nullptr;
+template <typename T, bool kProbs, int kThreads>
+cudaError_t launch_walk(const VerifyParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.B * (probs ? kWalkCtas : 1)), 1, 1);
-  cfg.blockDim = dim3(kWalkThreads, 1, 1);
+  cfg.gridDim = dim3((unsigned)(p.B * (kProbs ? kWalkCtas : 1)), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -488,13 +586,23 @@ cudaError_t launch(const VerifyParams& p, cudaStream_t stream) {
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = probs ? 2 : 1;
-  return probs ? cudaLaunchKernelEx(&cfg, walk_kernel<T, true>, p) : cudaLaunchKernelEx(&cfg, walk_kernel<T, false>, p);
+  cfg.numAttrs = kProbs ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, walk_kernel<T, kProbs, kThreads>, p);
+}
+
+template <typename T>
+cudaError_t launch(VerifyParams p, cudaStream_t stream) {
+  p.chunks = (p.V + Vec<T>::kN - 1) / Vec<T>::kChunk + 1;
+  const dim3 grid((unsigned)(p.B * p.Q), (unsigned)((p.chunks + kStatsThreads / 32 - 1) / (kStatsThreads / 32)));
+  stats_kernel<T><<<grid, kStatsThreads, 0, stream>>>(p);
+  const cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  return p.probs != nullptr ? launch_walk<T, true, 256>(p, stream) : launch_walk<T, false, 512>(p, stream);
 }
 
 }  // namespace
 
-int verify_chunks(int64_t V) { return (int)((V + 7) / kChunk + 1); }
+int verify_chunks(int64_t V) { return (int)((V + 7) / (kChunkBytes / 4) + 1); }
 
 cudaError_t launch_spec_verify(const VerifyParams& p, int type, cudaStream_t stream) {
   if (type == NVFP4MLA_FP32) return launch<float>(p, stream);
