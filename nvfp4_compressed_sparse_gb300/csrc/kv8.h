@@ -116,9 +116,10 @@ struct VerifyParams {
   int chunks;                    // of a row, at most
   float2* chunk_ms;              // [B Q, chunks]: largest logit of a chunk, sum of exponentials against it
   int32_t* chunk_at;             // [B Q, chunks]: where the largest is
-  double* chunk_sum;             // [B, chunks]
+  double* entry_sum;             // [B, entries]: sums of what a walk has left, by chunks or finer
 };
 int verify_chunks(int64_t V);
+int verify_entries(int64_t V);
 cudaError_t launch_spec_verify(const VerifyParams& p, int type, cudaStream_t stream);   // type: NVFP4MLA_BF16, _FP16 or _FP32
 
 // The three arrays of the page operators, and the caches whose pages they move.

@@ -331,7 +331,7 @@ static VerifyWorkspace verify_workspace(int B, int Q, int64_t V) {
   const size_t chunks = (size_t)verify_chunks(V);
   VerifyWorkspace w;
   w.sums = align256((size_t)B * Q * chunks * sizeof(float2));
-  w.at = w.sums + align256((size_t)B * chunks * sizeof(double));
+  w.at = w.sums + align256((size_t)B * verify_entries(V) * sizeof(double));
   w.total = w.at + align256((size_t)B * Q * chunks * sizeof(int32_t));
   return w;
 }
@@ -374,7 +374,7 @@ int spec_verify(const void* logits, int64_t logits_row_stride, int dtype, const 
   p.accepted = accepted;
   p.status = dev_status;
   p.chunk_ms = reinterpret_cast<float2*>(ws);
-  p.chunk_sum = reinterpret_cast<double*>(ws + w.sums);
+  p.entry_sum = reinterpret_cast<double*>(ws + w.sums);
   p.chunk_at = reinterpret_cast<int32_t*>(ws + w.at);
   return status_of(launch_spec_verify(p, dtype, static_cast<cudaStream_t>(stream)));
 }

@@ -30,6 +30,7 @@ constexpr int kChunkBytes = 4096;      // of a row that a warp takes: eight 16-b
 constexpr int kStatsThreads = 256;
 constexpr int kWalkCtas = 8;           // of a request, with draft distributions
 constexpr int kMaxNodes = 64;
+constexpr int kFine = 8;               // warps' loads of a chunk
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
 template <typename T>
@@ -123,7 +124,7 @@ __device__ __forceinline__ float warp_max(float x) {
 
 // A chunk's largest logit, and the sum of its exponentials against that; greedy: where the largest is first.
 template <typename T>
-__global__ void __launch_bounds__(kStatsThreads) stats_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(kStatsThreads, 4) stats_kernel(const __grid_constant__ VerifyParams p) {
   using V = Vec<T>;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
@@ -205,7 +206,11 @@ struct WalkShared {
   float u[kMaxNodes];
   double left[kMaxNodes];              // s before each refusal at the current node
   int out[kMaxNodes];                  // tokens that were refused there
+  float inverse[kMaxNodes];            // 1 / total
   double sum;                          // of what is left
+  double warp_sum[16];
+  float part[16], need;
+  int pick, last;
   // the walk
   int at, count, refused, next_node, ends;
 };
@@ -222,202 +227,192 @@ struct Walker {
   __device__ const T* row_of(int j) const { return static_cast<const T*>(p.logits) + ((int64_t)b * p.Q + j) * p.row_stride; }
   __device__ const float* probs_of(int j) const { return p.probs + ((int64_t)b * p.Q + j) * p.probs_stride; }
 
-  // A load's worth of what is left at node j, from logit `at` on: with draft distributions r after `refused` refusals,
-  // else the exponentials, but for the refused tokens'.
-  __device__ __forceinline__ void rest(int j, const uint4& w, int64_t at, float m, float inv, int refused, float (&x)[V::kN]) const {
-    widen(w, x, static_cast<const T*>(nullptr));
-#pragma unroll
-    for (int k = 0; k < V::kN; ++k) x[k] = weight(clean(x[k]), m, rate);
-    if constexpr (kProbs) {
-#pragma unroll
-      for (int k = 0; k < V::kN; ++k) x[k] *= inv;
-      if (refused == 0) return;
-      float q[V::kN];
+  // Code that a CTA runs once costs what its fetching costs, some 16 cycles an instruction: so every thread has one load
+  // of a chunk, and the loops are loops.
+  struct Load {
+    float x[V::kN];
+  };
+  // What is left, after `refused` refusals at node j, of the tokens of the load from `at` on: of their probabilities (with
+  // draft distributions), or of their exponentials.
+  __device__ __noinline__ Load rest(int j, int64_t at, int refused) const {
+    const T* row = row_of(j);
+    const float m = sh.top[j], inv = kProbs ? sh.inverse[j] : 1.f;
+    const uint4 w = load_vec(row, at, p.V);
+    Load q;
+    if (kProbs && refused > 0) {
       const float* from = probs_of(j) + at;
       if (at >= 0 && at + V::kN <= p.V && (reinterpret_cast<uintptr_t>(from) & 15) == 0) {
 #pragma unroll
-        for (int k = 0; k < V::kN; k += 4) {
-          const float4 v = __ldg(reinterpret_cast<const float4*>(from + k));
-          q[k] = v.x;
-          q[k + 1] = v.y;
-          q[k + 2] = v.z;
-          q[k + 3] = v.w;
-        }
+        for (int k = 0; k < V::kN; k += 4) *reinterpret_cast<float4*>(q.x + k) = __ldg(reinterpret_cast<const float4*>(from + k));
       } else {
 #pragma unroll
-        for (int k = 0; k < V::kN; ++k) q[k] = at + k >= 0 && at + k < p.V ? __ldg(from + k) : 0.f;
-      }
-#pragma unroll 1
-      for (int i = 0; i < refused; ++i) {
-        const float s = (float)sh.left[i];
-#pragma unroll
-        for (int k = 0; k < V::kN; ++k) x[k] = fmaxf(x[k] - s * q[k], 0.f);
-      }
-    } else {
-#pragma unroll 1
-      for (int i = 0; i < refused; ++i) {
-        const int64_t k0 = sh.out[i] - at;
-#pragma unroll
-        for (int k = 0; k < V::kN; ++k) x[k] = k0 == k ? 0.f : x[k];
+        for (int k = 0; k < V::kN; ++k) q.x[k] = at + k >= 0 && at + k < p.V ? __ldg(from + k) : 0.f;
       }
     }
-  }
-
-  // A chunk's rest by one warp, all of its loads in flight; the sum in every lane.
-  __device__ double chunk_rest(int j, int chunk, float m, float inv, int refused) const {
-    const int lane = threadIdx.x & 31;
-    const T* row = row_of(j);
-    const int64_t at = (int64_t)chunk * V::kChunk - lead_of(row) + lane * V::kN;
-    uint4 w[V::kLoads];
+    Load r;
+    widen(w, r.x, row);
 #pragma unroll
-    for (int i = 0; i < V::kLoads; ++i) w[i] = load_vec(row, at + i * 32 * V::kN, p.V);
-    float sum = 0.f;
-#pragma unroll 2
-    for (int i = 0; i < V::kLoads; ++i) {
-      float x[V::kN];
-      uint4 v = w[0];
+    for (int k = 0; k < V::kN; ++k) r.x[k] = weight(clean(r.x[k]), m, rate) * inv;
+#pragma unroll 1
+    for (int i = 0; i < refused; ++i) {
+      const float s = (float)sh.left[i];
+      const int64_t out = sh.out[i] - at;
 #pragma unroll
-      for (int n = 1; n < V::kLoads; ++n) v = n == i ? w[n] : v;
-      rest(j, v, at + i * 32 * V::kN, m, inv, refused, x);
-      float part = 0.f;
-#pragma unroll
-      for (int k = 0; k < V::kN; ++k) part += x[k];
-      sum += part;
+      for (int k = 0; k < V::kN; ++k) r.x[k] = kProbs ? fmaxf(r.x[k] - s * q.x[k], 0.f) : (out == k ? 0.f : r.x[k]);
     }
+    return r;
+  }
+  static __device__ __forceinline__ float add_up(const Load& r) {
+    float s = 0.f;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
-    return (double)sum;
+    for (int k = 0; k < V::kN; ++k) s += r.x[k];
+    return s;
+  }
+  static __device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(kFull, x, d);
+    return x;
   }
 
-  __device__ void everyone() const {
-    if (ctas > 1) cluster_sync_all();
-    else __syncthreads();
+  // What is left at node j, summed by entries: a warp's loads, where a distribution has been taken off, else chunks.
+  __device__ __forceinline__ bool fine(int refused) const { return kProbs && refused > 0; }
+  __device__ __forceinline__ int entry_tokens(int refused) const { return fine(refused) ? 32 * V::kN : V::kChunk; }
+  __device__ int entries(int j, int refused) const {
+    return (p.V + lead_of(row_of(j)) + entry_tokens(refused) - 1) / entry_tokens(refused);
   }
 
-  // Sums of the chunks of what is left at node j, into chunk_sum, and their sum into sh.sum: the same in every CTA.
-  __device__ void sums(int j, int refused) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const T* row = row_of(j);
-    const int chunks = chunks_of(row, p.V);
-    double* to = p.chunk_sum + (int64_t)b * p.chunks;
-    const float m = sh.top[j], inv = (float)(1. / sh.total[j]);
-    if (kProbs && refused > 0) {
-      for (int c = rank * kWarps + warp; c < chunks; c += ctas * kWarps) {
-        const double s = chunk_rest(j, c, m, inv, refused);
-        if (lane == 0) to[c] = s;
+  // The entries' sums, and from there of all: sh.sum, the same in every CTA. Returns the sum of the entries before this
+  // thread's, of which it has a run of sh.per. again: not the first time.
+  __device__ double sums(int j, int refused, bool again) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = entries(j, refused);
+    double* to = p.entry_sum + (int64_t)b * p.chunks * kFine;
+    if (again) {                         // (all have read the sums before these)
+      if (ctas > 1) cluster_sync_all();
+      else __syncthreads();
+    }
+    const int64_t start = -(int64_t)lead_of(row_of(j));
+    if (fine(refused)) {
+#pragma unroll 1
+      for (int c = rank * kWarps + warp; c < n; c += ctas * kWarps) {
+        const float s = warp_sum(add_up(rest(j, start + ((int64_t)c * 32 + lane) * V::kN, refused)));
+        if (lane == 0) to[c] = (double)s;
       }
     } else if (rank == 0) {
-      // the chunks' sums, and again where a refused token lies
       const int64_t first = ((int64_t)b * p.Q + j) * p.chunks;
-      const float scale = kProbs ? inv : 1.f;
-      for (int c = threadIdx.x; c < chunks; c += kThreads) {
+      const float m = sh.top[j], scale = kProbs ? sh.inverse[j] : 1.f;
+#pragma unroll 1
+      for (int c = threadIdx.x; c < n; c += kThreads) {
         const float2 ms = __ldcg(p.chunk_ms + first + c);
         to[c] = (double)(ms.y * weight(ms.x, m, rate) * scale);
       }
       if (!kProbs && refused > 0) {
+        // again, where a refused token lies: all warps a chunk, whose parts one thread adds up
         __syncthreads();
-        const int lead = lead_of(row);
-        for (int i = warp; i < refused; i += kWarps) {
-          const int c = (sh.out[i] + lead) / V::kChunk;
-          const double s = chunk_rest(j, c, m, inv, refused);     // (two refused tokens of a chunk: the same sum twice)
-          if (lane == 0) to[c] = s;
+#pragma unroll 1
+        for (int i = 0; i < refused; ++i) {
+          const int c = (int)((sh.out[i] - start) / V::kChunk);
+          if (threadIdx.x < V::kChunk / V::kN) {
+            const float s = warp_sum(add_up(rest(j, start + (int64_t)c * V::kChunk + threadIdx.x * V::kN, refused)));
+            if (lane == 0) sh.part[warp] = s;
+          }
+          __syncthreads();
+          if (threadIdx.x == 0) {
+            float s = 0.f;
+            for (int k = 0; k < V::kChunk / V::kN / 32; ++k) s += sh.part[k];
+            to[c] = (double)s;
+          }
+          __syncthreads();
         }
       }
     }
-    everyone();
-    if (warp == 0) {
-      double s = 0.;
-      const int per = (chunks + 31) / 32;
-#pragma unroll 4
-      for (int i = 0; i < per; ++i) s += lane * per + i < chunks ? __ldcg(to + lane * per + i) : 0.;
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-      if (lane == 0) sh.sum = s;
-    }
-    everyone();                          // nobody writes the sums again before all have read them
-  }
-
-  // An inclusive sum over the lanes.
-  static __device__ __forceinline__ double scan(double x) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const double o = __shfl_up_sync(kFull, x, d);
-      if (lane >= d) x += o;
-    }
-    return x;
-  }
-
-  // The first token whose running sum of what is left at node j exceeds `share` of it all: one warp.
-  __device__ int draw(int j, double share, double total, int refused) {
-    const int lane = threadIdx.x & 31;
-    const T* row = row_of(j);
-    const int chunks = chunks_of(row, p.V), per = (chunks + 31) / 32;
-    const double* of = p.chunk_sum + (int64_t)b * p.chunks;
-    const double want = share * total;
-    // a lane a run of chunks, then the run's chunks one by one; where none is past it, the last that has anything
+    if (ctas > 1) cluster_sync_all();
+    else __syncthreads();
+    const int per = (n + kThreads - 1) / kThreads;
     double mine = 0.;
-#pragma unroll 4
-    for (int i = 0; i < per; ++i) mine += lane * per + i < chunks ? __ldcg(of + lane * per + i) : 0.;
-    const double incl = scan(mine);
-    unsigned past = __ballot_sync(kFull, mine > 0. && incl > want);
-    const unsigned some = __ballot_sync(kFull, mine > 0.);
-    if (some == 0) return -1;
-    const int who = past != 0 ? __ffs(past) - 1 : 31 - __clz(some);
-    double before = incl - mine, at_before = 0.;
-    int chunk = -1;
-    for (int i = 0; i < per; ++i) {
-      const double s = lane * per + i < chunks ? __ldcg(of + lane * per + i) : 0.;
-      if (s > 0. && (chunk < 0 || !(at_before > want))) {
-        // (at_before: up to the end of the chunk that is held)
-        chunk = lane * per + i;
-        at_before = before + s;
+#pragma unroll 1
+    for (int i = threadIdx.x * per; i < min(n, ((int)threadIdx.x + 1) * per); ++i) mine += __ldcg(to + i);
+    double incl = mine;
+#pragma unroll 1
+    for (int d = 1; d < 32; d <<= 1) {
+      const double o = __shfl_up_sync(kFull, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) sh.warp_sum[warp] = incl;
+    __syncthreads();
+    double before = 0., all = 0.;
+#pragma unroll 1
+    for (int k = 0; k < kWarps; ++k) {
+      if (k == warp) before = all;
+      all += sh.warp_sum[k];
+    }
+    if (threadIdx.x == 0) {
+      sh.sum = all;
+      sh.pick = INT_MAX;
+      sh.last = -1;
+    }
+    __syncthreads();
+    return before + incl - mine;
+  }
+
+  // The first token whose running sum of what is left at node j exceeds `share` of it all, else the last that has
+  // anything: the threads of one CTA, behind sums(), whose result is `before`.
+  __device__ int draw(int j, double share, double before, int refused) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = entries(j, refused), per = (n + kThreads - 1) / kThreads;
+    const double* of = p.entry_sum + (int64_t)b * p.chunks * kFine;
+    const double want = share * sh.sum;
+#pragma unroll 1
+    for (int i = threadIdx.x * per; i < min(n, ((int)threadIdx.x + 1) * per); ++i) {
+      const double s = __ldcg(of + i);
+      if (s > 0.) {
+        atomicMax(&sh.last, i);
+        if (before + s > want) atomicMin(&sh.pick, i);
       }
       before += s;
     }
-    chunk = __shfl_sync(kFull, chunk, who);
-    // what lies before the chunk, as the scan has it
-    double upto = 0.;
-    for (int i = 0; i < per; ++i) upto += lane * per + i < chunk ? __ldcg(of + lane * per + i) : 0.;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) upto += __shfl_xor_sync(kFull, upto, d);
-
-    const int64_t at = (int64_t)chunk * V::kChunk - lead_of(row) + lane * V::kN;
-    const float m = sh.top[j], inv = (float)(1. / sh.total[j]);
-    uint4 w[V::kLoads];
-#pragma unroll
-    for (int i = 0; i < V::kLoads; ++i) w[i] = load_vec(row, at + i * 32 * V::kN, p.V);
-    int found = -1;
+    __syncthreads();
+    const int entry = sh.pick != INT_MAX ? sh.pick : sh.last;
+    if (entry < 0) return -1;
+    // the entry's thread knows what lies before it
+    if (entry / per == (int)threadIdx.x) {
 #pragma unroll 1
-    for (int i = 0; i < V::kLoads; ++i) {
-      float x[V::kN];
-      uint4 v = w[0];
-#pragma unroll
-      for (int n = 1; n < V::kLoads; ++n) v = n == i ? w[n] : v;
-      const int64_t from = at + i * 32 * V::kN;
-      rest(j, v, from, m, inv, refused, x);
-      double part = 0.;
-#pragma unroll
-      for (int k = 0; k < V::kN; ++k) part += (double)x[k];
-      const double upto_here = scan(part);
-      // this lane's first token past `want`, else its last that has anything
-      double run = upto + upto_here - part;
-      int token = -1;
-      bool is_past = false;
+      for (int i = entry; i < min(n, ((int)threadIdx.x + 1) * per); ++i) before -= __ldcg(of + i);
+      sh.need = (float)(want - before);
+    }
+    __syncthreads();
+    const bool in = (int)threadIdx.x < entry_tokens(refused) / V::kN;
+    const int64_t at = (int64_t)entry * entry_tokens(refused) - lead_of(row_of(j)) + threadIdx.x * V::kN;
+    Load r;
+    float sum = 0.f, incl = 0.f;
+    if (warp * 32 < entry_tokens(refused) / V::kN) {
+      r = rest(j, at, refused);
+      incl = sum = add_up(r);
+#pragma unroll 1
+      for (int d = 1; d < 32; d <<= 1) {
+        const float o = __shfl_up_sync(kFull, incl, d);
+        if (lane >= d) incl += o;
+      }
+    }
+    if (lane == 31) sh.part[warp] = incl;
+    if (threadIdx.x == 0) {
+      sh.pick = INT_MAX;
+      sh.last = -1;
+    }
+    __syncthreads();
+    if (in) {
+      float run = incl - sum;
+#pragma unroll 1
+      for (int k = 0; k < warp; ++k) run += sh.part[k];
 #pragma unroll
       for (int k = 0; k < V::kN; ++k) {
-        run += (double)x[k];
-        if (x[k] > 0.f && !is_past) {
-          token = (int)(from + k);
-          is_past = run > want;
+        run += r.x[k];
+        if (r.x[k] > 0.f) {
+          atomicMax(&sh.last, (int)(at + k));
+          if (run > sh.need) atomicMin(&sh.pick, (int)(at + k));
         }
       }
-      const unsigned any = __ballot_sync(kFull, token >= 0), hit = __ballot_sync(kFull, is_past);
-      if (any != 0) found = __shfl_sync(kFull, token, hit != 0 ? __ffs(hit) - 1 : 31 - __clz(any));
-      if (hit != 0) break;
-      upto += __shfl_sync(kFull, upto_here, 31);
     }
-    return found;
+    __syncthreads();
+    return sh.pick != INT_MAX ? sh.pick : sh.last;
   }
 
   // From where the walk stands to its end, or to a refusal behind which a sum is needed: one thread. left: s of what is left.
@@ -526,6 +521,7 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
     if (lane == 0) {
       sh.top[j] = m;
       sh.total[j] = sum;
+      sh.inverse[j] = sum > 0. ? 1.f / (float)sum : 0.f;
       sh.best[j] = greedy && m != neg_inf() ? __ldcg(p.chunk_at + first + where) : -1;
     }
   }
@@ -534,16 +530,18 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
     const int up = sh.parent[tid];
     const float m = sh.top[up], d = logit - m, a = d * rate.hi;
     // exp2 of a, and of what rounding took from it
-    double have = logit == neg_inf() ? 0. : (logit == m ? 1. : (double)exp2f(a) * (1. + 0.6931471805599453 * (double)(fmaf(d, rate.hi, -a) + d * rate.lo)));
-    sh.have[tid] = have / sh.total[up];
+    const float e = exp2f(a), have = logit == neg_inf() ? 0.f : (logit == m ? 1.f : fmaf(e, 0.69314718f * (fmaf(d, rate.hi, -a) + d * rate.lo), e));
+    sh.have[tid] = (double)(have * sh.inverse[up]);
   }
   __syncthreads();
   if (tid == 0) w.walk(greedy, 1.);
   __syncthreads();
+  bool again = false;
   if constexpr (kProbs) {
     while (!sh.ends) {
       const int at = sh.at, refused = sh.refused;
-      w.sums(at, refused);
+      w.sums(at, refused, again);
+      again = true;
       if (tid == 0) w.walk(greedy, sh.sum);
       __syncthreads();
     }
@@ -551,12 +549,12 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
   const int at = sh.at, count = sh.count;
   int refused = sh.refused, next = greedy ? sh.best[at] : -1;
   if (!greedy && sh.top[at] != neg_inf()) {
-    w.sums(at, refused);
+    double before = w.sums(at, refused, again);
     if (!(sh.sum > 0.) && refused > 0) {   // nothing is left: from the target's own
       refused = 0;
-      w.sums(at, 0);
+      before = w.sums(at, 0, true);
     }
-    if (warp == 0 && rank == 0) next = w.draw(at, (double)sh.u[0], sh.sum, refused);
+    if (rank == 0) next = w.draw(at, (double)sh.u[0], before, refused);
   }
   if (rank == 0) {
     if (tid == 0) {
@@ -603,6 +601,7 @@ cudaError_t launch(VerifyParams p, cudaStream_t stream) {
 }  // namespace
 
 int verify_chunks(int64_t V) { return (int)((V + 7) / (kChunkBytes / 4) + 1); }
+int verify_entries(int64_t V) { return verify_chunks(V) * kFine; }
 
 cudaError_t launch_spec_verify(const VerifyParams& p, int type, cudaStream_t stream) {
   if (type == NVFP4MLA_FP32) return launch<float>(p, stream);
