@@ -10,8 +10,8 @@
 // stats_kernel does that by chunks of 4 KB, a warp each, whose values stay in registers; the chunks' sums are
 // kept, since with them a token can be drawn by reading a single chunk again. walk_kernel has a CTA a request
 // (with draft distributions a cluster of eight, since what a refusal leaves is a sum over the vocabulary): all
-// nodes' probabilities are found at once, so that the walk itself is a few comparisons. Sums over chunks, and
-// what is compared, are in 64 bits: the results are whole numbers.
+// nodes' probabilities are found at once, so that the walk itself is a few comparisons. Running sums over chunks
+// are in 64 bits: what is drawn changes where they cross a border between tokens.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -124,7 +124,7 @@ __device__ __forceinline__ float warp_max(float x) {
 
 // A chunk's largest logit, and the sum of its exponentials against that; greedy: where the largest is first.
 template <typename T>
-__global__ void __launch_bounds__(kStatsThreads, 4) stats_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(kStatsThreads) stats_kernel(const __grid_constant__ VerifyParams p) {
   using V = Vec<T>;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
@@ -198,19 +198,17 @@ __global__ void __launch_bounds__(kStatsThreads, 4) stats_kernel(const __grid_co
 
 struct WalkShared {
   float top[kMaxNodes];                // a node's largest logit
-  double total[kMaxNodes];             // its sum of exponentials against that
+  float inverse[kMaxNodes];            // 1 / its sum of exponentials against that
   int best[kMaxNodes];
-  double have[kMaxNodes];              // probability of a draft's token under its parent
+  float have[kMaxNodes];               // probability of a draft's token under its parent
   float drawn[kMaxNodes];              // and under what it was drawn from
   int parent[kMaxNodes], token[kMaxNodes];
   float u[kMaxNodes];
-  double left[kMaxNodes];              // s before each refusal at the current node
+  float left[kMaxNodes];               // s before each refusal at the current node
   int out[kMaxNodes];                  // tokens that were refused there
-  float inverse[kMaxNodes];            // 1 / total
   double sum;                          // of what is left
-  double warp_sum[16];
-  float part[16], need;
-  int pick, last;
+  float part[2][kFine], need;
+  int entry, pick, last;
   // the walk
   int at, count, refused, next_node, ends;
 };
@@ -234,7 +232,7 @@ struct Walker {
   };
   // What is left, after `refused` refusals at node j, of the tokens of the load from `at` on: of their probabilities (with
   // draft distributions), or of their exponentials.
-  __device__ __noinline__ Load rest(int j, int64_t at, int refused) const {
+  __device__ __forceinline__ Load rest(int j, int64_t at, int refused) const {
     const T* row = row_of(j);
     const float m = sh.top[j], inv = kProbs ? sh.inverse[j] : 1.f;
     const uint4 w = load_vec(row, at, p.V);
@@ -251,14 +249,22 @@ struct Walker {
     }
     Load r;
     widen(w, r.x, row);
+    if (fabsf(m) < __int_as_float(0x7f800000)) {
 #pragma unroll
-    for (int k = 0; k < V::kN; ++k) r.x[k] = weight(clean(r.x[k]), m, rate) * inv;
+      for (int k = 0; k < V::kN; ++k) {
+        const float d = fmaxf(r.x[k], neg_inf()) - m;      // (a NaN is no candidate)
+        r.x[k] = ex2_approx(fmaf(d, rate.hi, d * rate.lo)) * inv;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < V::kN; ++k) r.x[k] = r.x[k] == m && m != neg_inf() ? inv : 0.f;
+    }
 #pragma unroll 1
     for (int i = 0; i < refused; ++i) {
-      const float s = (float)sh.left[i];
+      const float s = sh.left[i];
       const int64_t out = sh.out[i] - at;
 #pragma unroll
-      for (int k = 0; k < V::kN; ++k) r.x[k] = kProbs ? fmaxf(r.x[k] - s * q.x[k], 0.f) : (out == k ? 0.f : r.x[k]);
+      for (int k = 0; k < V::kN; ++k) r.x[k] = kProbs ? fmaxf(fmaf(-s, q.x[k], r.x[k]), 0.f) : (out == k ? 0.f : r.x[k]);
     }
     return r;
   }
@@ -274,18 +280,21 @@ struct Walker {
     return x;
   }
 
-  // What is left at node j, summed by entries: a warp's loads, where a distribution has been taken off, else chunks.
+  __device__ __noinline__ float rest_of_warp(int j, int64_t at, int refused) const { return warp_sum(add_up(rest(j, at, refused))); }
+
+  // What is left at node j is summed by entries: a warp's loads, where a distribution has been taken off, else chunks.
   __device__ __forceinline__ bool fine(int refused) const { return kProbs && refused > 0; }
   __device__ __forceinline__ int entry_tokens(int refused) const { return fine(refused) ? 32 * V::kN : V::kChunk; }
   __device__ int entries(int j, int refused) const {
     return (p.V + lead_of(row_of(j)) + entry_tokens(refused) - 1) / entry_tokens(refused);
   }
+  __device__ __forceinline__ double* entry_sums() const { return p.entry_sum + (int64_t)b * p.chunks * kFine; }
 
-  // The entries' sums, and from there of all: sh.sum, the same in every CTA. Returns the sum of the entries before this
-  // thread's, of which it has a run of sh.per. again: not the first time.
+  // The entries' sums, and from there of all: sh.sum, the same in every CTA. A lane of warp 0 has a run of them; returns
+  // what lies before it. again: not the first time.
   __device__ double sums(int j, int refused, bool again) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = entries(j, refused);
-    double* to = p.entry_sum + (int64_t)b * p.chunks * kFine;
+    double* to = entry_sums();
     if (again) {                         // (all have read the sums before these)
       if (ctas > 1) cluster_sync_all();
       else __syncthreads();
@@ -294,7 +303,7 @@ struct Walker {
     if (fine(refused)) {
 #pragma unroll 1
       for (int c = rank * kWarps + warp; c < n; c += ctas * kWarps) {
-        const float s = warp_sum(add_up(rest(j, start + ((int64_t)c * 32 + lane) * V::kN, refused)));
+        const float s = rest_of_warp(j, start + ((int64_t)c * 32 + lane) * V::kN, refused);
         if (lane == 0) to[c] = (double)s;
       }
     } else if (rank == 0) {
@@ -306,20 +315,23 @@ struct Walker {
         to[c] = (double)(ms.y * weight(ms.x, m, rate) * scale);
       }
       if (!kProbs && refused > 0) {
-        // again, where a refused token lies: all warps a chunk, whose parts one thread adds up
+        // again, where a refused token lies: eight warps a chunk
         __syncthreads();
+        constexpr int kGroups = kWarps / kFine;
 #pragma unroll 1
-        for (int i = 0; i < refused; ++i) {
-          const int c = (int)((sh.out[i] - start) / V::kChunk);
-          if (threadIdx.x < V::kChunk / V::kN) {
-            const float s = warp_sum(add_up(rest(j, start + (int64_t)c * V::kChunk + threadIdx.x * V::kN, refused)));
-            if (lane == 0) sh.part[warp] = s;
+        for (int i0 = 0; i0 < refused; i0 += kGroups) {
+          const int group = warp / kFine, i = i0 + group;
+          const int c = i < refused ? (int)((sh.out[i] - start) / V::kChunk) : 0;
+          if (i < refused) {
+            const float s = rest_of_warp(j, start + (int64_t)c * V::kChunk + (threadIdx.x & 255) * V::kN, refused);
+            if (lane == 0) sh.part[group][warp % kFine] = s;
           }
           __syncthreads();
-          if (threadIdx.x == 0) {
+          if (i < refused && (threadIdx.x & 255) == 0) {
             float s = 0.f;
-            for (int k = 0; k < V::kChunk / V::kN / 32; ++k) s += sh.part[k];
-            to[c] = (double)s;
+#pragma unroll 1
+            for (int k = 0; k < kFine; ++k) s += sh.part[group][k];
+            to[c] = (double)s;           // (two refused tokens of a chunk: the same sum twice)
           }
           __syncthreads();
         }
@@ -327,63 +339,63 @@ struct Walker {
     }
     if (ctas > 1) cluster_sync_all();
     else __syncthreads();
-    const int per = (n + kThreads - 1) / kThreads;
-    double mine = 0.;
+    double mine = 0., incl = 0.;
+    if (warp == 0) {
+      const int per = (n + 31) / 32;
+#pragma unroll 4
+      for (int i = 0; i < per; ++i) mine += lane * per + i < n ? __ldcg(to + lane * per + i) : 0.;
+      incl = mine;
 #pragma unroll 1
-    for (int i = threadIdx.x * per; i < min(n, ((int)threadIdx.x + 1) * per); ++i) mine += __ldcg(to + i);
-    double incl = mine;
-#pragma unroll 1
-    for (int d = 1; d < 32; d <<= 1) {
-      const double o = __shfl_up_sync(kFull, incl, d);
-      if (lane >= d) incl += o;
-    }
-    if (lane == 31) sh.warp_sum[warp] = incl;
-    __syncthreads();
-    double before = 0., all = 0.;
-#pragma unroll 1
-    for (int k = 0; k < kWarps; ++k) {
-      if (k == warp) before = all;
-      all += sh.warp_sum[k];
-    }
-    if (threadIdx.x == 0) {
-      sh.sum = all;
-      sh.pick = INT_MAX;
-      sh.last = -1;
+      for (int d = 1; d < 32; d <<= 1) {
+        const double o = __shfl_up_sync(kFull, incl, d);
+        if (lane >= d) incl += o;
+      }
+      if (lane == 31) sh.sum = incl;
+      if (lane == 0) {
+        sh.entry = sh.pick = INT_MAX;
+        sh.last = -1;
+      }
     }
     __syncthreads();
-    return before + incl - mine;
+    return incl - mine;
   }
 
   // The first token whose running sum of what is left at node j exceeds `share` of it all, else the last that has
   // anything: the threads of one CTA, behind sums(), whose result is `before`.
-  __device__ int draw(int j, double share, double before, int refused) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = entries(j, refused), per = (n + kThreads - 1) / kThreads;
-    const double* of = p.entry_sum + (int64_t)b * p.chunks * kFine;
-    const double want = share * sh.sum;
+  __device__ int draw(int j, float share, double before, int refused) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = entries(j, refused);
+    if (warp == 0) {
+      const double* of = entry_sums();
+      const double want = (double)share * sh.sum;
+      const int per = (n + 31) / 32;
+      int first = -1, last = -1;
+      double at_first = 0., at_last = 0.;
 #pragma unroll 1
-    for (int i = threadIdx.x * per; i < min(n, ((int)threadIdx.x + 1) * per); ++i) {
-      const double s = __ldcg(of + i);
-      if (s > 0.) {
-        atomicMax(&sh.last, i);
-        if (before + s > want) atomicMin(&sh.pick, i);
+      for (int i = lane * per; i < min(n, (lane + 1) * per); ++i) {
+        const double s = __ldcg(of + i);
+        if (s > 0.) {
+          last = i;
+          at_last = before;
+          if (first < 0 && before + s > want) {
+            first = i;
+            at_first = before;
+          }
+        }
+        before += s;
       }
-      before += s;
+      const unsigned past = __ballot_sync(kFull, first >= 0), some = __ballot_sync(kFull, last >= 0);
+      if (past != 0 ? lane == __ffs(past) - 1 : (some != 0 && lane == 31 - __clz(some))) {
+        sh.entry = past != 0 ? first : last;
+        sh.need = (float)(want - (past != 0 ? at_first : at_last));
+      }
     }
     __syncthreads();
-    const int entry = sh.pick != INT_MAX ? sh.pick : sh.last;
-    if (entry < 0) return -1;
-    // the entry's thread knows what lies before it
-    if (entry / per == (int)threadIdx.x) {
-#pragma unroll 1
-      for (int i = entry; i < min(n, ((int)threadIdx.x + 1) * per); ++i) before -= __ldcg(of + i);
-      sh.need = (float)(want - before);
-    }
-    __syncthreads();
-    const bool in = (int)threadIdx.x < entry_tokens(refused) / V::kN;
+    const int entry = sh.entry, loads = entry_tokens(refused) / V::kN;
+    if (entry == INT_MAX) return -1;
     const int64_t at = (int64_t)entry * entry_tokens(refused) - lead_of(row_of(j)) + threadIdx.x * V::kN;
     Load r;
     float sum = 0.f, incl = 0.f;
-    if (warp * 32 < entry_tokens(refused) / V::kN) {
+    if (warp * 32 < loads) {
       r = rest(j, at, refused);
       incl = sum = add_up(r);
 #pragma unroll 1
@@ -391,17 +403,13 @@ struct Walker {
         const float o = __shfl_up_sync(kFull, incl, d);
         if (lane >= d) incl += o;
       }
-    }
-    if (lane == 31) sh.part[warp] = incl;
-    if (threadIdx.x == 0) {
-      sh.pick = INT_MAX;
-      sh.last = -1;
+      if (lane == 31) sh.part[0][warp] = incl;
     }
     __syncthreads();
-    if (in) {
+    if (warp * 32 < loads) {
       float run = incl - sum;
 #pragma unroll 1
-      for (int k = 0; k < warp; ++k) run += sh.part[k];
+      for (int k = 0; k < warp; ++k) run += sh.part[0][k];
 #pragma unroll
       for (int k = 0; k < V::kN; ++k) {
         run += r.x[k];
@@ -415,45 +423,66 @@ struct Walker {
     return sh.pick != INT_MAX ? sh.pick : sh.last;
   }
 
-  // From where the walk stands to its end, or to a refusal behind which a sum is needed: one thread. left: s of what is left.
-  __device__ void walk(bool greedy, double left) {
-    int at = sh.at, count = sh.count, refused = sh.refused, j = sh.next_node;
-    for (; j < p.Q; ++j) {
-      if (sh.parent[j] != at) continue;
+  // From where the walk stands to its end, or to a refusal behind which a sum is needed: warp 0. left: s of what is left,
+  // below 0 where it is not known.
+  __device__ void walk(bool greedy, float left) {
+    const int lane = threadIdx.x & 31;
+    const int up0 = lane < p.Q ? sh.parent[lane] : -1, up1 = 32 + lane < p.Q ? sh.parent[32 + lane] : -1;
+    int at = sh.at, count = sh.count, refused = sh.refused, from = sh.next_node;
+    bool ends = true;
+    __syncwarp();
+    for (;;) {
+      // the next child of the current node
+      const uint64_t children = ((uint64_t)__ballot_sync(kFull, up1 == at) << 32 | __ballot_sync(kFull, up0 == at)) & (from < 64 ? ~0ull << from : 0ull);
+      if (children == 0) break;
+      const int j = __ffsll((long long)children) - 1;
+      from = j + 1;
       bool yes;
       if (greedy) {
         yes = sh.best[at] == sh.token[j];
       } else {
-        if (kProbs && left < 0.) break;      // another child after a refusal: s is that of what is left
-        double r = sh.have[j];
-        const double q = sh.drawn[j];
-        for (int i = 0; i < refused; ++i) {
-          if (kProbs) r = fmax(r - sh.left[i] * q, 0.);
-          else if (sh.out[i] == sh.token[j]) r = 0.;
+        if (kProbs && left < 0.f) {      // another child after a refusal
+          from = j;
+          ends = false;
+          break;
         }
-        yes = (double)sh.u[j] * q * left < r;
+        float r = sh.have[j];
+        const float q = sh.drawn[j];
+#pragma unroll 1
+        for (int i = 0; i < refused; ++i) {
+          if (kProbs) r = fmaxf(fmaf(-sh.left[i], q, r), 0.f);
+          else if (sh.out[i] == sh.token[j]) r = 0.f;
+        }
+        yes = sh.u[j] * q * left < r;
         if (!yes) {
-          sh.left[refused] = left;
-          sh.out[refused++] = sh.token[j];
-          left = kProbs ? -1. : left - r;
+          __syncwarp();
+          if (lane == 0) {
+            sh.left[refused] = left;
+            sh.out[refused] = sh.token[j];
+          }
+          __syncwarp();
+          ++refused;
+          left = kProbs ? -1.f : left - r;
         }
       }
       if (yes) {
-        if (rank == 0) {
+        if (rank == 0 && lane == 0) {
           p.path[(int64_t)b * p.Q + count] = j;
           p.tokens[(int64_t)b * p.Q + count] = sh.token[j];
         }
         ++count;
         at = j;
         refused = 0;
-        left = 1.;
+        left = 1.f;
       }
     }
-    sh.at = at;
-    sh.count = count;
-    sh.refused = refused;
-    sh.next_node = j;
-    sh.ends = j >= p.Q;
+    if (lane == 0) {
+      sh.at = at;
+      sh.count = count;
+      sh.refused = refused;
+      sh.next_node = from;
+      sh.ends = ends;
+    }
   }
 };
 
@@ -488,15 +517,17 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
     sh.at = sh.count = sh.refused = 0;
     sh.next_node = 1;
   }
+  __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // nodes' largest logits and sums, a warp a node
+#pragma unroll 1
   for (int j = warp; j < Q; j += kWarps) {
-    if (!is_node(p, b * Q + j)) continue;
+    if (j > 0 && sh.parent[j] < 0) continue;
     const int64_t first = ((int64_t)b * Q + j) * p.chunks;
     const int chunks = chunks_of(w.row_of(j), p.V);
-    float m = neg_inf();
-    double sum = 0.;
+    float m = neg_inf(), sum = 0.f;
     int where = INT_MAX;
+#pragma unroll 1
     for (int c0 = 0; c0 < chunks; c0 += 128) {           // four loads in flight
       float2 ms[4];
 #pragma unroll
@@ -512,16 +543,14 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
         float part = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) part += ms[i].y * weight(ms[i].x, now, rate);
-        sum = sum * (double)weight(m, now, rate) + (double)part;
+        sum = fmaf(sum, weight(m, now, rate), part);
       }
       m = now;
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
+    sum = w.warp_sum(sum);
     if (lane == 0) {
       sh.top[j] = m;
-      sh.total[j] = sum;
-      sh.inverse[j] = sum > 0. ? 1.f / (float)sum : 0.f;
+      sh.inverse[j] = sum > 0.f ? 1.f / sum : 0.f;
       sh.best[j] = greedy && m != neg_inf() ? __ldcg(p.chunk_at + first + where) : -1;
     }
   }
@@ -531,10 +560,10 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
     const float m = sh.top[up], d = logit - m, a = d * rate.hi;
     // exp2 of a, and of what rounding took from it
     const float e = exp2f(a), have = logit == neg_inf() ? 0.f : (logit == m ? 1.f : fmaf(e, 0.69314718f * (fmaf(d, rate.hi, -a) + d * rate.lo), e));
-    sh.have[tid] = (double)(have * sh.inverse[up]);
+    sh.have[tid] = have * sh.inverse[up];
   }
   __syncthreads();
-  if (tid == 0) w.walk(greedy, 1.);
+  if (warp == 0) w.walk(greedy, 1.f);
   __syncthreads();
   bool again = false;
   if constexpr (kProbs) {
@@ -542,7 +571,7 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
       const int at = sh.at, refused = sh.refused;
       w.sums(at, refused, again);
       again = true;
-      if (tid == 0) w.walk(greedy, sh.sum);
+      if (warp == 0) w.walk(greedy, (float)sh.sum);
       __syncthreads();
     }
   }
@@ -554,7 +583,7 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
       refused = 0;
       before = w.sums(at, 0, true);
     }
-    if (rank == 0) next = w.draw(at, (double)sh.u[0], before, refused);
+    if (rank == 0) next = w.draw(at, sh.u[0], before, refused);
   }
   if (rank == 0) {
     if (tid == 0) {
