@@ -280,7 +280,7 @@ struct Walker {
     return x;
   }
 
-  __device__ __noinline__ float rest_of_warp(int j, int64_t at, int refused) const { return warp_sum(add_up(rest(j, at, refused))); }
+  __device__ __forceinline__ float rest_of_warp(int j, int64_t at, int refused) const { return warp_sum(add_up(rest(j, at, refused))); }
 
   // What is left at node j is summed by entries: a warp's loads, where a distribution has been taken off, else chunks.
   __device__ __forceinline__ bool fine(int refused) const { return kProbs && refused > 0; }
