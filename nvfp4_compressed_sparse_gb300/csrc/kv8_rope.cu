@@ -8,8 +8,7 @@
 // What bounds it: memory, four bytes a query's value and three a key's or value's, once a row costs few enough
 // instructions: some 60 for two rows. A lane has four pairs: two runs of four dims, half the turned dims apart, or eight
 // dims side by side where pairs are neighbours, so that nothing but the sum of squares crosses lanes; behind the turned
-// dims it has eight dims of its own. A key is turned twice, for its block's scale and for its code, as holding 16 turned
-// rows would leave too few warps.
+// dims it has eight dims of its own.
 //
 // A CTA takes a block of 16 tokens of one request and a share of its rows' heads: it stages the cosines and
 // sines of its tokens once, then each warp takes a head at a time.
@@ -124,12 +123,13 @@ struct Lane {
   }
   __device__ __forceinline__ bool is_new(int i) const { return (rows >> i) & 1; }
   __device__ __forceinline__ bool is_step(int i) const { return (steps >> i) & 1; }
-  // Rows of one head, x at the lane's row 0; zeros where a row is not new.
-  __device__ __forceinline__ void load(const uint16_t* x, int64_t stride, uint4 (&w)[R::kLoads]) const {
+  // Rows of one head, from load i0 on, x at the lane's row of that; zeros where a row is not new.
+  template <int kN>
+  __device__ __forceinline__ void load(const uint16_t* x, int64_t stride, int i0, uint4 (&w)[kN]) const {
 #pragma unroll
-    for (int i = 0; i < R::kLoads; ++i) {
+    for (int i = 0; i < kN; ++i) {
       w[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (is_new(i)) {
+      if (is_new(i0 + i)) {
         if constexpr (kInter) {
           w[i] = *reinterpret_cast<const uint4*>(x + at_a);
         } else {
@@ -152,7 +152,7 @@ __device__ __forceinline__ void queries(const RopeParams& p, const Block& b, con
 #pragma unroll 1
   for (; head < end; head += kRopeWarps) {
     uint4 w[R::kLoads];
-    lane.load(p.q + (b.token + lane.row0) * p.q_token_stride + head * p.q_head_stride, p.q_token_stride, w);
+    lane.load(p.q + (b.token + lane.row0) * p.q_token_stride + head * p.q_head_stride, p.q_token_stride, 0, w);
     uint16_t* to = p.q_out + (b.token + lane.row0) * p.out_token_stride + head * p.out_head_stride;
 #pragma unroll
     for (int i = 0; i < R::kLoads; ++i) {
@@ -175,65 +175,72 @@ __device__ __forceinline__ void queries(const RopeParams& p, const Block& b, con
   }
 }
 
+// Two warps a head, half of the block's rows each, so that the turned rows stay in registers until the scale is known.
 template <int D, bool kHalf, bool kInter>
-__device__ __forceinline__ void keys(const RopeParams& p, const Block& b, const float (*sheets)[D], int head, int end) {
+__device__ __forceinline__ void keys(const RopeParams& p, const Block& b, const float (*sheets)[D], int first_head, int end) {
   using R = Rows<D>;
+  constexpr int kN = R::kLoads / 2;
+  __shared__ uint32_t tops[2][kRopeWarps];
   const Lane<D, kInter> lane(b, p.rot);
   const bool norm = p.weight[1] != nullptr;
+  const int warp = threadIdx.x >> 5, i0 = (warp & 1) * kN;
   Eight g = {};
   if (norm) g = widen8<kHalf>(__ldg(reinterpret_cast<const uint2*>(p.weight[1] + lane.at_a)), __ldg(reinterpret_cast<const uint2*>(p.weight[1] + lane.at_b)));
+  // the larger of this warp's and the other's
+  auto exchange = [&](int round, uint32_t bits) {
+    bits = __reduce_max_sync(kFull, bits);
+    if ((threadIdx.x & 31) == 0) tops[round][warp] = bits;
+    asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
+    return max(bits, tops[round][warp ^ 1]);
+  };
 #pragma unroll 1
-  for (; head < end; head += kRopeWarps) {
-    uint4 w[R::kLoads];
-    lane.load(p.x[0] + (b.token + lane.row0) * p.token_stride[0] + head * p.head_stride[0], p.token_stride[0], w);
+  for (int head = first_head + (warp >> 1); head < end; head += kRopeWarps / 2) {
+    const int64_t row = b.token + i0 * R::kAtOnce + lane.row0;
+    uint4 w[kN];
+    lane.load(p.x[0] + row * p.token_stride[0] + head * p.head_stride[0], p.token_stride[0], i0, w);
     uint8_t* codes = b.page + kv8_codes_off(p.kv_heads, D, 0, head) + b.quarter * kBlockTokens * D;
     uint8_t* scale = b.page + kv8_scales_off(p.kv_heads, D, head) + b.quarter;
     const uint32_t before = b.first > 0 ? min((uint32_t)*scale, 253u) : 0u;
-    __syncwarp();
-    auto turned = [&](int i) {
-      Eight y = widen8<kHalf>(make_uint2(w[i].x, w[i].y), make_uint2(w[i].z, w[i].w));
-      turn<D, kInter>(y, norm, g, p.eps, lane.turns, sheets[i * R::kAtOnce + lane.row0] + 4 * lane.l, p.rot / 2);
-      return y;
-    };
-    // the largest; of the finite ones, once there is an infinity (a NaN is never the larger)
+    Eight y[kN];
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < R::kLoads; ++i) {
-      if (!lane.is_step(i)) continue;
-      const Eight y = turned(i);
-      const float most = fmaxf(fmaxf(fmaxf(fabsf(y.a[0].x), fabsf(y.a[0].y)), fmaxf(fabsf(y.a[1].x), fabsf(y.a[1].y))),
-                               fmaxf(fmaxf(fabsf(y.b[0].x), fabsf(y.b[0].y)), fmaxf(fabsf(y.b[1].x), fabsf(y.b[1].y))));
-      if (lane.is_new(i)) top = fmaxf(top, most);
+    for (int i = 0; i < kN; ++i) {
+      y[i] = widen8<kHalf>(make_uint2(w[i].x, w[i].y), make_uint2(w[i].z, w[i].w));
+      turn<D, kInter>(y[i], norm, g, p.eps, lane.turns, sheets[(i0 + i) * R::kAtOnce + lane.row0] + 4 * lane.l, p.rot / 2);
+      const float most = fmaxf(fmaxf(fmaxf(fabsf(y[i].a[0].x), fabsf(y[i].a[0].y)), fmaxf(fabsf(y[i].a[1].x), fabsf(y[i].a[1].y))),
+                               fmaxf(fmaxf(fabsf(y[i].b[0].x), fabsf(y[i].b[0].y)), fmaxf(fabsf(y[i].b[1].x), fabsf(y[i].b[1].y))));
+      if (lane.is_new(i0 + i)) top = fmaxf(top, most);
     }
-    uint32_t bits = __reduce_max_sync(kFull, __float_as_uint(top));
+    // the largest; of the finite ones, once there is an infinity (a NaN is never the larger)
+    uint32_t bits = exchange(0, __float_as_uint(top));
     if (__builtin_expect(bits >= 0x7F800000u, 0)) {
       bits = 0;
 #pragma unroll
-      for (int i = 0; i < R::kLoads; ++i) {
-        if (!lane.is_step(i)) continue;
-        const Eight y = turned(i);
-        const float x[8] = {y.a[0].x, y.a[0].y, y.a[1].x, y.a[1].y, y.b[0].x, y.b[0].y, y.b[1].x, y.b[1].y};
+      for (int i = 0; i < kN; ++i) {
+        const float x[8] = {y[i].a[0].x, y[i].a[0].y, y[i].a[1].x, y[i].a[1].y, y[i].b[0].x, y[i].b[0].y, y[i].b[1].x, y[i].b[1].y};
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const uint32_t a = __float_as_uint(x[k]) & 0x7FFFFFFFu;
-          if (lane.is_new(i) && a < 0x7F800000u) bits = max(bits, a);
+          if (lane.is_new(i0 + i) && a < 0x7F800000u) bits = max(bits, a);
         }
       }
-      bits = __reduce_max_sync(kFull, bits);
+      bits = exchange(1, bits);
     }
     const uint32_t e = max(scale_byte(__uint_as_float(bits)), before);
     const float mul = __uint_as_float((254u - e) << 23);
-    uint8_t* to = codes + lane.row0 * D;
+    uint8_t* to = codes + (i0 * R::kAtOnce + lane.row0) * D;
 #pragma unroll
-    for (int i = 0; i < R::kLoads; ++i) {
-      if (!lane.is_step(i)) continue;
-      const Eight y = turned(i);
-      if (!lane.is_new(i)) continue;
-      *reinterpret_cast<uint32_t*>(to + i * R::kAtOnce * D + lane.at_a) = __byte_perm(code2(y.a[0], mul), code2(y.a[1], mul), 0x5410);
-      *reinterpret_cast<uint32_t*>(to + i * R::kAtOnce * D + lane.at_b) = __byte_perm(code2(y.b[0], mul), code2(y.b[1], mul), 0x5410);
+    for (int i = 0; i < kN; ++i) {
+      if (!lane.is_new(i0 + i)) continue;
+      *reinterpret_cast<uint32_t*>(to + i * R::kAtOnce * D + lane.at_a) = __byte_perm(code2(y[i].a[0], mul), code2(y[i].a[1], mul), 0x5410);
+      *reinterpret_cast<uint32_t*>(to + i * R::kAtOnce * D + lane.at_b) = __byte_perm(code2(y[i].b[0], mul), code2(y[i].b[1], mul), 0x5410);
     }
-    if (b.first > 0 && e > before) shrink_rows<D>(codes + 8 * lane.l, lane.row0, b.first, before, e);
-    if ((threadIdx.x & 31) == 0) *scale = (uint8_t)e;
+    if ((warp & 1) == 0) {
+      if (b.first > 0 && e > before) shrink_rows<D>(codes + 8 * lane.l, lane.row0, b.first, before, e);
+      if ((threadIdx.x & 31) == 0) *scale = (uint8_t)e;
+    }
+    // (what the other reads of `tops` it has read before the next head's exchange is complete)
+    asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
   }
 }
 
@@ -259,9 +266,14 @@ __device__ __forceinline__ void values(const RopeParams& p, const Block& b, int 
   }
 }
 
+// How the heads of a kind are shared by CTAs: n of them, `per` heads each.
+struct Shares {
+  int n, per;
+};
+
 // blockIdx.y: shares of the queries' heads, then of the keys', then of the values', so that a CTA has one code.
 template <int D, bool kHalf, bool kInter>
-__global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(const __grid_constant__ RopeParams p, int q_shares, int kv_shares, int q_per, int kv_per) {
+__global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(const __grid_constant__ RopeParams p, const Shares q, const Shares k, const Shares v) {
   __shared__ __align__(16) float sheets[kBlockTokens][D];      // of a token: cosines of its pairs, then sines
   const int warp = threadIdx.x >> 5;
   const int slot = blockIdx.x;
@@ -288,31 +300,56 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
   if (!have && speaks) atomicAdd(p.status + NVFP4MLA_STAT_BAD_PAGE, 1);
   block.page = p.cache + page * p.page_bytes;
 
-  const int kind = (int)blockIdx.y < q_shares ? 0 : ((int)blockIdx.y < q_shares + kv_shares ? 1 : 2);
-  const int share = blockIdx.y - (kind == 0 ? 0 : (kind == 1 ? q_shares : q_shares + kv_shares));
-  const int per = kind == 0 ? q_per : kv_per, head = share * per + warp, end = min(kind == 0 ? p.heads : p.kv_heads, (share + 1) * per);
+  const int kind = (int)blockIdx.y < q.n ? 0 : ((int)blockIdx.y < q.n + k.n ? 1 : 2);
+  const int share = blockIdx.y - (kind == 0 ? 0 : (kind == 1 ? q.n : q.n + k.n)), per = kind == 0 ? q.per : (kind == 1 ? k.per : v.per);
+  const int head = share * per, end = min(kind == 0 ? p.heads : p.kv_heads, head + per);
   if (kind != 0 && !have) return;
   if (kind == 2) {
-    values<D, kHalf>(p, block, head, end);
+    values<D, kHalf>(p, block, head + warp, end);
     return;
   }
+  // cosines and sines, four pairs at a time: a thread a row and quad
   const int half = p.rot / 2;
+  {
+    const int row = threadIdx.x & 15;
+    const bool vec = (reinterpret_cast<uintptr_t>(p.cos_sin) & 15) == 0;
+    const float nan = __int_as_float(0x7fc00000);          // no position of the table: NaN, and counted
 #pragma unroll 1
-  for (int i = threadIdx.x; i < (block.behind - block.first) * half; i += kRopeWarps * 32) {
-    const int row = block.first + i / half, pair = i - i / half * half;
-    int axis = 0;
-    if (p.positions != nullptr) {
+    for (int pair = (threadIdx.x >> 4) * 4; pair < half && row >= block.first && row < block.behind; pair += kRopeWarps * 32 / 16 * 4) {
+      auto axis_of = [&](int i) {
+        int axis = 0;
 #pragma unroll
-      for (int a = 0; a < kMaxAxes - 1; ++a) axis += a + 1 < p.axes && pair >= p.ends[a] ? 1 : 0;
+        for (int a = 0; a < kMaxAxes - 1; ++a) axis += a + 1 < p.axes && i >= p.ends[a] ? 1 : 0;
+        return axis;
+      };
+      auto position = [&](int axis) { return p.positions != nullptr ? (int64_t)__ldg(p.positions + axis * p.axis_stride + block.token + row) : t0 + row; };
+      const int axis = axis_of(pair);
+      float4 c = make_float4(nan, nan, nan, nan), s = c;
+      if (vec && axis_of(pair + 3) == axis) {
+        const int64_t at = position(axis);
+        if (at >= 0 && at < p.max_positions) {
+          c = __ldg(reinterpret_cast<const float4*>(p.cos_sin + at * p.rot + pair));
+          s = __ldg(reinterpret_cast<const float4*>(p.cos_sin + at * p.rot + half + pair));
+        }
+      } else {
+        float cs[4], ss[4];
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          const int64_t at = position(axis_of(pair + k));
+          const bool in = at >= 0 && at < p.max_positions;
+          const float x = in ? __ldg(p.cos_sin + at * p.rot + pair + k) : nan, y = in ? __ldg(p.cos_sin + at * p.rot + half + pair + k) : nan;
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            cs[n] = n == k ? x : cs[n];
+            ss[n] = n == k ? y : ss[n];
+          }
+        }
+        c = make_float4(cs[0], cs[1], cs[2], cs[3]);
+        s = make_float4(ss[0], ss[1], ss[2], ss[3]);
+      }
+      *reinterpret_cast<float4*>(sheets[row] + pair) = c;
+      *reinterpret_cast<float4*>(sheets[row] + half + pair) = s;
     }
-    const int64_t at = p.positions != nullptr ? (int64_t)__ldg(p.positions + axis * p.axis_stride + block.token + row) : t0 + row;
-    float c = __int_as_float(0x7fc00000), s = c;           // no position of the table: NaN, and counted
-    if (at >= 0 && at < p.max_positions) {
-      c = __ldg(p.cos_sin + at * p.rot + pair);
-      s = __ldg(p.cos_sin + at * p.rot + half + pair);
-    }
-    sheets[row][pair] = c;
-    sheets[row][half + pair] = s;
   }
   if (blockIdx.y == 0 && (int)threadIdx.x >= block.first && (int)threadIdx.x < block.behind && p.status != nullptr) {
     bool bad = false;
@@ -323,7 +360,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) rope_kernel(cons
     if (bad) atomicAdd(p.status + NVFP4MLA_STAT_BAD_INDEX, 1);
   }
   __syncthreads();
-  if (kind == 0) queries<D, kHalf, kInter>(p, block, sheets, head, end);
+  if (kind == 0) queries<D, kHalf, kInter>(p, block, sheets, head + warp, end);
   else keys<D, kHalf, kInter>(p, block, sheets, head, end);
 }
 
@@ -331,17 +368,16 @@ template <int D, bool kHalf>
 void launch(const RopeParams& p, bool interleaved, cudaStream_t stream) {
   // CTAs enough for every SM to hold its own, and no more shares of a block than leave each warp a head
   const int64_t want = (int64_t)2 * kRopeBlocks * device_sm_count(), blocks = p.slots < want ? (want + p.slots - 1) / p.slots : 1;
-  auto shares_of = [&](int heads, int most) {
-    const int each = (heads + kRopeWarps - 1) / kRopeWarps;
-    return each < most ? each : most;
-  };
-  auto per_of = [&](int heads, int shares) { return ((heads + shares - 1) / shares + kRopeWarps - 1) / kRopeWarps * kRopeWarps; };
   const int most = (int)(blocks < 65535 / 4 ? blocks : 65535 / 4);
-  const int q_per = per_of(p.heads, shares_of(p.heads, most)), kv_per = per_of(p.kv_heads, shares_of(p.kv_heads, most));
-  const int q_shares = (p.heads + q_per - 1) / q_per, kv_shares = (p.kv_heads + kv_per - 1) / kv_per;
-  const dim3 grid((unsigned)p.slots, (unsigned)(q_shares + 2 * kv_shares));
-  if (interleaved) rope_kernel<D, kHalf, true><<<grid, kRopeWarps * 32, 0, stream>>>(p, q_shares, kv_shares, q_per, kv_per);
-  else rope_kernel<D, kHalf, false><<<grid, kRopeWarps * 32, 0, stream>>>(p, q_shares, kv_shares, q_per, kv_per);
+  auto shares = [&](int heads, int at_once) {
+    const int each = (heads + at_once - 1) / at_once, n = each < most ? each : most;
+    const int per = ((heads + n - 1) / n + at_once - 1) / at_once * at_once;
+    return Shares{(heads + per - 1) / per, per};
+  };
+  const Shares q = shares(p.heads, kRopeWarps), k = shares(p.kv_heads, kRopeWarps / 2), v = shares(p.kv_heads, kRopeWarps);
+  const dim3 grid((unsigned)p.slots, (unsigned)(q.n + k.n + v.n));
+  if (interleaved) rope_kernel<D, kHalf, true><<<grid, kRopeWarps * 32, 0, stream>>>(p, q, k, v);
+  else rope_kernel<D, kHalf, false><<<grid, kRopeWarps * 32, 0, stream>>>(p, q, k, v);
 }
 
 }  // namespace
