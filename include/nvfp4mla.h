@@ -620,7 +620,7 @@ size_t kv8_decode_tree_workspace_size(int B, int Q, int H, int kv_heads, int hea
  *
  * NaN, infinities and the sizes of scores as kv8_decode. The two operands that are held in fewer bits:
  *   queries  off by at most 2^-17 of the row's largest magnitude (bf16: exact from 2^-9 of it on, fp16: 2^-6)
- *   weights  off by at most 2^-12 of itself, or 2^-34 of the largest such product of the row's attended positions
+ *   weights  off by at most 2^-12 of itself, or 2^-33 of the largest such product of the row's attended positions
  *            if that is more; the sum that divides is one of unrounded exponentials
  *
  *   masks             uint64 [B, Q], 8-byte aligned
@@ -674,8 +674,9 @@ size_t spec_verify_workspace_size(int B, int Q, int64_t V);
  *   accepted          int32 [B]: how many
  *   workspace         device scratch, 256-byte aligned, spec_verify_workspace_size bytes; contents need no
  *                     initialisation. Calls that share one must be ordered.
- * All pointers: device memory of the current device. More than INT32_MAX chunks of 1,024 logits return
- * NVFP4MLA_ERR_UNSUPPORTED.
+ * All pointers: device memory of the current device. tokens, path and accepted overlap neither one another nor an
+ * input (of drafts, parents, uniforms, temperatures: refused). More than INT32_MAX chunks of 1,024 logits, or INT32_MAX / 8
+ * requests, return NVFP4MLA_ERR_UNSUPPORTED.
  */
 int spec_verify(const void* logits, int64_t logits_row_stride, int dtype, const float* draft_probs, int64_t probs_row_stride,
                 const int32_t* drafts, const int32_t* parents, const float* uniforms, const float* temperatures, int B,
@@ -693,7 +694,7 @@ int spec_verify(const void* logits, int64_t logits_row_stride, int dtype, const 
  *   accepted          int32 [B]; < 0: leave the request out
  *   new_lens          int32 [B] (output): base + 1 + accepted[b], for kv_pages_trim; seq_lens[b] of a request that
  *                     is left out, or refused (and counted, NVFP4MLA_STAT_BAD_SLOT): another path than that, or
- *                     fewer than Q tokens
+ *                     fewer than Q tokens. Overlaps no input (seq_lens, path, accepted: refused)
  *   layers, layer_stride  caches of num_pages pages each, layer_stride bytes apart (a multiple of 16; not read
  *                     when layers is 1), that share the table
  *   everything else   as kv8_append. A place whose table entry is no page of the cache is not read or not
@@ -743,7 +744,8 @@ int kv_pages_free(int32_t* page_table, int64_t max_pages_per_seq, int32_t* seq_l
                   void* stream);
 
 /* kv_pages_trim: sequence s is cut to new_lens[s] tokens (int32 [num_seqs]): the entries behind become -1, their
- * pages' counts go down by one. A new length below 0 or above seq_lens[s] is refused and counted. */
+ * pages' counts go down by one. A new length below 0 or above seq_lens[s] is refused and counted. (A page that a fork
+ * shares may become a sequence's part-full last one: what is appended to it then shows in the other sequence too.) */
 int kv_pages_trim(int32_t* page_table, int64_t max_pages_per_seq, int32_t* seq_lens, int num_seqs, int32_t* refcounts,
                   int64_t num_pages, const int32_t* new_lens, int32_t* dev_status, void* stream);
 

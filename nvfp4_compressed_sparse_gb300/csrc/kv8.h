@@ -120,6 +120,7 @@ struct VerifyParams {
 };
 int verify_chunks(int64_t V);
 int verify_entries(int64_t V);
+int verify_requests();           // at most, of a call
 cudaError_t launch_spec_verify(const VerifyParams& p, int type, cudaStream_t stream);   // type: NVFP4MLA_BF16, _FP16 or _FP32
 
 // The three arrays of the page operators, and the caches whose pages they move.

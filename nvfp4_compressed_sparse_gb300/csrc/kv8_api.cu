@@ -25,6 +25,11 @@ static bool any_null(std::initializer_list<const void*> ptrs) {
   return false;
 }
 static bool optional_ok(const void* p) { return p == nullptr || pointer_kind(p) == kPtrDevice; }
+// Of [a, a + n) and [b, b + m); a null pointer overlaps nothing.
+static bool overlap(const void* a, size_t n, const void* b, size_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + m && y < x + n;
+}
 static bool words_aligned(std::initializer_list<const void*> ptrs) {
   for (const void* p : ptrs)
     if (!aligned(p, 4)) return false;
@@ -316,6 +321,9 @@ int kv8_keep(void* cache, int64_t layers, int64_t layer_stride, int64_t num_page
   if (!aligned(cache, 128) || (layers > 1 && layer_stride % 16 != 0)) return NVFP4MLA_ERR_ALIGNMENT;
   if (!words_aligned({page_table, seq_lens, path, accepted, new_lens, dev_status})) return NVFP4MLA_ERR_ALIGNMENT;
   if (!all_device({cache, page_table, seq_lens, path, accepted, new_lens}) || !optional_ok(dev_status)) return NVFP4MLA_ERR_INVALID_ARG;
+  const size_t n = (size_t)B * sizeof(int32_t);
+  // (a request is read by many warps, one of which writes its new length)
+  if (overlap(new_lens, n, seq_lens, n) || overlap(new_lens, n, accepted, n) || overlap(new_lens, n, path, n * Q)) return NVFP4MLA_ERR_INVALID_ARG;
   if (layers > INT32_MAX / (2 * kv_heads) / B) return NVFP4MLA_ERR_UNSUPPORTED;
   const KeepParams p{static_cast<uint8_t*>(cache), layers, layers > 1 ? layer_stride : 0, num_pages, page_bytes, page_table,
                      max_pages_per_seq, seq_lens, path, accepted, B, Q, kv_heads, new_lens, dev_status};
@@ -347,6 +355,7 @@ int spec_verify(const void* logits, int64_t logits_row_stride, int dtype, const 
                 int32_t* dev_status, void* stream) {
   if (!verify_sizes_ok(B, Q, V) || dtype < NVFP4MLA_BF16 || dtype > NVFP4MLA_FP32) return NVFP4MLA_ERR_INVALID_ARG;
   if (logits_row_stride < 0 || probs_row_stride < 0) return NVFP4MLA_ERR_INVALID_ARG;
+  if (B > verify_requests()) return NVFP4MLA_ERR_UNSUPPORTED;
   if (any_null({logits, drafts, parents, uniforms, tokens, path, accepted})) return NVFP4MLA_ERR_INVALID_ARG;
   const VerifyWorkspace w = verify_workspace(B, Q, V);
   if (workspace == nullptr || workspace_bytes < w.total) return NVFP4MLA_ERR_WORKSPACE;
@@ -354,6 +363,14 @@ int spec_verify(const void* logits, int64_t logits_row_stride, int dtype, const 
   if (!words_aligned({draft_probs, drafts, parents, uniforms, temperatures, tokens, path, accepted, dev_status})) return NVFP4MLA_ERR_ALIGNMENT;
   if (!all_device({logits, drafts, parents, uniforms, tokens, path, accepted, workspace})) return NVFP4MLA_ERR_INVALID_ARG;
   if (!optional_ok(draft_probs) || !optional_ok(temperatures) || !optional_ok(dev_status)) return NVFP4MLA_ERR_INVALID_ARG;
+  // (a request's inputs are read by several CTAs, one of which writes its results)
+  const size_t n = (size_t)B * Q * sizeof(int32_t), n1 = (size_t)B * sizeof(int32_t);
+  const struct { const void* at; size_t bytes; } out[3] = {{tokens, n}, {path, n}, {accepted, n1}};
+  for (int i = 0; i < 3; ++i) {
+    if (overlap(out[i].at, out[i].bytes, drafts, n) || overlap(out[i].at, out[i].bytes, parents, n) || overlap(out[i].at, out[i].bytes, uniforms, n) ||
+        overlap(out[i].at, out[i].bytes, temperatures, n1) || overlap(out[i].at, out[i].bytes, out[(i + 1) % 3].at, out[(i + 1) % 3].bytes))
+      return NVFP4MLA_ERR_INVALID_ARG;
+  }
   VerifyParams p{};
   p.chunks = verify_chunks(V);
   if ((int64_t)B * Q > INT32_MAX / p.chunks) return NVFP4MLA_ERR_UNSUPPORTED;

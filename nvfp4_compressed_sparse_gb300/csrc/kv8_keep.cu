@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepParams p) 
       if (speaks && lane == 0 && p.status != nullptr) atomicAdd(p.status + NVFP4MLA_STAT_BAD_PAGE, 1);
       continue;
     }
-    int top = 0;
+    int top = -1;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       byte[i] = -1;
@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepParams p) 
       top = max(top, byte[i]);
     }
     top = __reduce_max_sync(kFull, top);
+    if (top < 0) continue;           // none has a page
     __syncwarp();                    // every row and byte has been read
     uint8_t* to = cache + page * p.page_bytes;
     uint8_t* codes = to + kv8_codes_off(p.kv_heads, D, which, head) + (t0 % kPageTokens) * D + at16;

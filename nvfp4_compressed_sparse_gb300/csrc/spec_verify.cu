@@ -76,7 +76,7 @@ __device__ __forceinline__ Rate rate_of(const VerifyParams& p, int b) {
   const float t = p.temperatures != nullptr ? p.temperatures[b] : 1.f;
   if (!(t > 0.f)) return Rate{-1.f, 0.f};
   constexpr float kHi = 1.4426950408889634f, kLo = (float)(1.4426950408889634 - (double)kHi);
-  float hi = kHi / t;
+  float hi = fmaxf(kHi / t, 4e-39f);                  // (not 0, of an infinite t: -inf times it stays what it is)
   if (!(hi < 3e38f)) return Rate{3e38f, 1e-38f};
   if (hi > 1e-30f) hi = __uint_as_float(__float_as_uint(hi) - 1);        // at or below the quotient
   return Rate{hi, fmaxf((fmaf(-hi, t, kHi) + kLo) / t, 1e-38f)};
@@ -462,7 +462,7 @@ struct Walker {
           }
           __syncwarp();
           ++refused;
-          left = kProbs ? -1.f : left - r;
+          left = kProbs ? -1.f : fmaxf(left - r, 0.f);      // (below 0 after a refusal that was asked for)
         }
       }
       if (yes) {
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
     sh.parent[tid] = up;
     sh.token[tid] = x;
     const float u = p.uniforms[r];
-    sh.u[tid] = u == u ? fmaxf(u, 0.f) : __int_as_float(0x7f800000);
+    sh.u[tid] = u < 1.f ? fmaxf(u, 0.f) : __int_as_float(0x7f800000);
     sh.drawn[tid] = kProbs && up >= 0 ? __ldg(w.probs_of(up) + x) : 1.f;
     if (up >= 0) logit = clean(as_float(w.row_of(up)[x]));
   }
@@ -631,6 +631,7 @@ cudaError_t launch(VerifyParams p, cudaStream_t stream) {
 
 int verify_chunks(int64_t V) { return (int)((V + 7) / (kChunkBytes / 4) + 1); }
 int verify_entries(int64_t V) { return verify_chunks(V) * kFine; }
+int verify_requests() { return INT_MAX / kWalkCtas; }
 
 cudaError_t launch_spec_verify(const VerifyParams& p, int type, cudaStream_t stream) {
   if (type == NVFP4MLA_FP32) return launch<float>(p, stream);

@@ -106,7 +106,7 @@ def verify(logits, drafts, parents, uniforms, temperatures=None, draft_probs=Non
     accepted, nearest, bad = np.zeros(B, np.int32), np.full(B, np.inf), 0
     for b in range(B):
         t = 1.0 if temperatures is None else float(temperatures[b])
-        u = [max(0.0, float(x)) if x == x else np.inf for x in uniforms[b]]
+        u = [max(0.0, float(x)) if x < 1 else np.inf for x in uniforms[b]]
         node = [j == 0 or (0 <= parents[b, j] < j and 0 <= drafts[b, j] < V) for j in range(Q)]
         bad += sum(1 for j in range(1, Q) if parents[b, j] != -1 and not node[j])
         at, n = 0, 0
@@ -182,6 +182,8 @@ def keep(caches, page_table, seq_lens, path, accepted, kv_heads: int, head_dim: 
                 continue
             bad_pages += sum(1 for s in src.values() if page_of(s) < 0)
             src = {t: s for t, s in src.items() if page_of(s) >= 0}
+            if not src:
+                continue
             for layer in range(len(caches)):
                 codes0, scales0 = kv8.parts(before[layer], kv_heads, head_dim)
                 codes, scales = kv8.parts(caches[layer], kv_heads, head_dim)

@@ -80,6 +80,7 @@ def test_verify_checks(lib):
     need = lib.spec_verify_workspace_size(2, 5, 100)
     assert verify(lib, ws=0) == WORKSPACE and verify(lib, wb=need - 1) == WORKSPACE and verify(lib, wb=need) == INVALID
     assert lib.spec_verify_workspace_size(2, 65, 100) == lib.spec_verify_workspace_size(0, 5, 100) == 0
+    assert verify(lib, B=(1 << 28), Q=1, V=1, wb=1 << 60) == UNSUPPORTED     # a cluster of eight each
     assert verify(lib, logits=A + 2, dt=1) == INVALID   # two-byte logits may begin there: addresses that are no device memory
 
 

@@ -187,6 +187,37 @@ def test_rope_leaves_out_and_counts_bad_data():
     assert np.array_equal(cache[untouched], c.cache[untouched])
 
 
+def test_rope_leaves_rows_of_no_request_alone():
+    """A padded batch: tokens before the first request, behind the last one, and of requests without new tokens."""
+    c = Rope([5, 7, 0, 64], [3, 0, 20, 2], 3, 1, 64, "bf16", 64, seed=9)
+    pad = lambda x: torch.cat([x[:2], x, x[:7]])  # noqa: E731
+    c.q, c.k, c.v = pad(c.q), pad(c.k), pad(c.v)
+    c.cu, c.n = c.cu + 2, c.n + 9
+    q_out = torch.full((c.n, 3, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    out, cache = c.run(q_out=q_out)
+    assert np.all(f64(out)[:2] == 7) and np.all(f64(out)[-7:] == 7)
+    (q, _), _ = c.turned(False)
+    c.n, c.cu = c.n - 9, c.cu - 2
+    c.q, c.k, c.v = c.q[2:-7], c.k[2:-7], c.v[2:-7]
+    c.check(out[2:-7], cache, False)
+    assert not np.array_equal(cache, c.cache) and q.shape == out.shape
+
+
+def test_rope_table_at_any_word():
+    """Cosines and sines that do not begin at 16 bytes, and axes that part within four pairs."""
+    c = Rope([2, 70], [33, 7], 8, 4, 128, "bf16", 96, axes=3, positions=True, seed=10)
+    c.sections = [3, 10, 35]
+    want = c.run()
+    c.check(*want, False)
+    room = torch.zeros(c.sheet.size + 3, device="cuda")
+    sheet = room[3:].view(*c.sheet.shape)
+    sheet.copy_(torch.from_numpy(c.sheet))
+    d = dev(c.cache, torch.uint8)
+    out = m.kv8_append_rope(*(x.to("cuda") for x in (c.q, c.k, c.v)), sheet, dev(c.cu), dev(c.lens), dev(c.table), d, q_weight=c.weights[0].to("cuda"),
+                            k_weight=c.weights[1].to("cuda"), eps=c.eps, positions=dev(c.positions), sections=c.sections)
+    assert torch.equal(out, want[0]) and np.array_equal(d.cpu().numpy(), want[1])
+
+
 def test_rope_special_values():
     """Zeros, infinities, NaN and the largest numbers in queries and keys, with and without norms."""
     for norm in (False, True):
@@ -217,9 +248,10 @@ def check_tree(out, lse, ref, adds, what=""):
 
     A score is a sum of D products in fp32, off by at most (D + 8) 2^-24 of reach; a query's elements are held to 2^-17 of the row's
     largest: 2^-17 of span. A weight is off by that, by the exponential's 2^-21, and by its rounding to fp16: half a step, 2^-12, or,
-    below 2^-14, half of 2^-24; as the column's largest such product is held at 2^9 at least, that is 2^-25 / 2^9 = 2^-34 of it. The
-    sum that divides is one of unrounded weights; both sums are made of `adds` additions in 32 bits, each off by at most a step of what it has reached. The output is rounded once to its type; one that
-    the type does not hold becomes an infinity."""
+    below 2^-14, half of 2^-24. The reference of a column's products is a power of two of which the largest product is more than
+    half, and what is at the reference is held as 2^9: so the largest is held above 2^8, of which 2^-25 is less than 2^-33. The sum
+    that divides is one of unrounded weights; both sums are made of `adds` additions in 32 bits, each off by at most a step of what
+    it has reached. The output is rounded once to its type; one that the type does not hold becomes an infinity."""
     r_out, r_lse, mass, reach, spread, span = ref
     dz = (r_out.shape[-1] + 8) * 2.0 ** -24 * reach + 2.0 ** -17 * span
     dw = 2 * (dz + 2.0 ** -21) + 2.0 ** -12 + adds * 2.0 ** -23
@@ -228,7 +260,7 @@ def check_tree(out, lse, ref, adds, what=""):
     got, got_lse = f64(out), f64(lse)
     nan = np.isnan(r_out)
     assert np.array_equal(np.isnan(got), nan), f"{what}: NaN in other places"
-    tol = half * np.abs(r_out) + (1 + half) * (dw[..., None] * mass + 2.0 ** -34 * spread) + tiny
+    tol = half * np.abs(r_out) + (1 + half) * (dw[..., None] * mass + 2.0 ** -33 * spread) + tiny
     most = torch.finfo(out.dtype).max * (1 + half)           # what is nearer to it than to the largest number
     with np.errstate(invalid="ignore"):
         got = np.where((got == np.copysign(np.inf, r_out)) & (np.abs(r_out) + tol >= most), r_out, got)
@@ -400,6 +432,54 @@ def test_tree_results_are_the_same_on_every_run():
         assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("Hk,G,D,Q", [(1, 128, 64, 64), (256, 1, 64, 2), (256, 2, 128, 1)])
+def test_tree_largest_sizes(Hk, G, D, Q):
+    """64 column tiles of one head; as many heads as a page may have."""
+    rng = np.random.default_rng(13)
+    c = Case([Q + 1, 70 + Q], Hk, D, "bf16", Q, G, seed=13)
+    _, masks = trees(rng, 2, Q)
+    check_tree(*run_tree(c, masks), tree_reference(c, masks), 500)
+
+
+def test_tree_waits_are_bounded_and_the_next_calls_are_right():
+    """A step whose tiles never come (a testing flag) gives up after its limit, says so, and leaves workspace
+    and device fit for the next step, a replay of a captured one over the same workspace included."""
+    c = Case([3000, 200], 2, 64, "bf16", 6, 2, seed=14)
+    _, masks = trees(np.random.default_rng(14), 2, 6)
+    ref = tree_reference(c, masks)
+    ws = torch.zeros(m.kv8_decode_tree_workspace_size(2, 6, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    args = (c.q, dev(c.cache, torch.uint8), dev(c.table), dev(c.lens), dev(masks.view(np.int64), torch.int64), 2, c.scale)
+    out, lse = m.kv8_decode_tree(*args, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.kv8_decode_tree(*args, out=out, lse=lse, workspace=ws)
+    status = dev(np.zeros(4))
+    m.kv8_decode_tree(*args, workspace=ws, dev_status=status, test_timeout=True)
+    torch.cuda.synchronize()
+    assert status[2] > 0 and status[[0, 1, 3]].tolist() == [0, 0, 0]
+    for _ in range(2):
+        out.fill_(7)
+        g.replay()
+        check_tree(out, lse, ref, 1500)
+    check_tree(*m.kv8_decode_tree(*args, workspace=ws), ref, 1500)
+
+
+def test_tree_two_calls_at_once():
+    """On two streams, each with its own workspace: what each gives alone."""
+    cases = [Case([2500, 300, 64], 2, 128, "bf16", 12, 4, seed=15), Case([900, 1800], 1, 64, "fp16", 30, 4, seed=16)]
+    masks = [trees(np.random.default_rng(i), len(c.lens), c.q.shape[1])[1] for i, c in enumerate(cases)]
+    args = [(c.q, dev(c.cache, torch.uint8), dev(c.table), dev(c.lens), dev(k.view(np.int64), torch.int64), c.Hk, c.scale) for c, k in zip(cases, masks)]
+    want = [m.kv8_decode_tree(*a) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    for _ in range(10):
+        got = [m.kv8_decode_tree(*a, stream=s) for a, s in zip(args, streams)]
+        torch.cuda.synchronize()
+        for (x, y), (w, z) in zip(got, want):
+            assert torch.equal(x.view(torch.int16), w.view(torch.int16)) and torch.equal(y, z)
+
+
 # ------------------------------------------------------------------ verification
 def verify_case(rng, B, Q, V, dtype, probs, width=2, chain=False):
     logits = rng.standard_normal((B, Q, V)) * 1.5
@@ -514,6 +594,46 @@ def test_verify_uniforms_at_the_ends():
     assert list(np.minimum(run_verify(c)[2], 1)) == [1, 1, 0, 0, 0, 1]
 
 
+def test_verify_uniforms_of_one_and_more_refuse():
+    """Whatever the probabilities are, and what is left then is not below 0."""
+    rng = np.random.default_rng(27)
+    for probs in (False, True):
+        c = verify_case(rng, 6, 4, 300, torch.float32, probs)
+        c["parents"][:] = [-1, 0, 0, 0]
+        c["temperatures"][:] = 1
+        c["logits"][:, 0, 200:] = -float("inf")
+        c["drafts"][:, 1:] = [[3, 5, 250]] * 6               # 250: no probability
+        c["logits"][:, 0, [3, 5]] = 30.0                     # what is left behind them is near 0
+        c["uniforms"][:, 1:] = [[1, 2, 0.5], [float("nan"), 7, 0.9], [1, 1, 1], [float("inf"), 1, 0], [1.5, 1.5, 0.25], [2, 2, 0.75]]
+        if probs:
+            c["draft_probs"][:, 0, 3] = 1e-6                 # far less than the target's
+        got = run_verify(c)
+        assert np.all(got[2] == 0) and np.all(got[0][:, 0] < 200)
+
+
+def test_verify_temperatures_at_the_ends():
+    """An infinite one: all that are not -inf are equally likely; a tiny one: the largest is all there is."""
+    rng = np.random.default_rng(28)
+    for probs in (False, True):
+        c = verify_case(rng, 6, 5, 1300, torch.float32, probs, chain=True)
+        c["logits"][:, :, 900:] = -float("inf")
+        c["temperatures"][:] = [float("inf"), 3e38, 1e30, 1e-40, 1e-30, float("inf")]
+        c["drafts"][3:5, 1:] = f64(c["logits"]).argmax(-1)[3:5, :-1]
+        got = check_verify(c)
+        assert np.all(got[2][3:5] == 4)
+
+
+def test_verify_refuses_results_over_inputs():
+    c = verify_case(np.random.default_rng(29), 2, 3, 50, torch.float32, False)
+    logits, drafts, parents, u = (torch.as_tensor(c[k]).to("cuda") for k in ("logits", "drafts", "parents", "uniforms"))
+    both = torch.zeros((2, 2, 3), dtype=torch.int32, device="cuda")
+    for kw in (dict(tokens=drafts), dict(path=parents), dict(tokens=u.view(torch.int32)), dict(accepted=drafts[0, :2]),
+               dict(tokens=both[0], path=both[0]), dict(path=both[1], accepted=both[1, 0, 1:])):
+        with pytest.raises(m.NvFp4MlaError):
+            m.spec_verify(logits, drafts, parents, u, **kw)
+    m.spec_verify(logits, drafts, parents, u, tokens=both[0], path=both[1])
+
+
 def test_verify_leaves_out_and_counts_bad_drafts():
     rng = np.random.default_rng(24)
     c = verify_case(rng, 4, 6, 500, torch.float32, False, chain=True)
@@ -622,6 +742,30 @@ def test_keep_leaves_out_and_counts_bad_data():
     assert bad == 5 and bad_pages >= 2 and status.tolist() == [0, bad_pages, 0, bad]
 
 
+def test_keep_leaves_a_block_whose_drafts_have_no_page():
+    """Two drafts on a page that is none, for a block that gets nothing else: its scale bytes, too, stay."""
+    rng = np.random.default_rng(32)
+    caches, table, lens, path, count = keep_case(rng, [67], 20, 1, 128)
+    path[:], count[:] = -1, 2
+    path[0, :2] = [17, 18]             # positions 64 and 65, to 48 and 49
+    table[0, 1] = -1
+    d, status = dev(caches, torch.uint8), dev(np.zeros(4))
+    new = m.kv8_keep(d[0], dev(table), dev(lens), dev(path), dev(count), 1, 128, dev_status=status)
+    assert np.array_equal(d.cpu().numpy(), caches) and new.tolist() == [50] and status.tolist() == [0, 2, 0, 0]
+    want = caches.copy()
+    assert spec.keep(want, table, lens, path, count, 1, 128)[1:] == (2, 0) and np.array_equal(want, caches)
+
+
+def test_keep_refuses_new_lengths_over_inputs():
+    rng = np.random.default_rng(33)
+    caches, table, lens, path, count = keep_case(rng, [100, 130], 10, 2, 64)
+    d, t, n, p, a = dev(caches, torch.uint8), dev(table), dev(lens), dev(path), dev(count)
+    for new in (n, a, p[0, :2], p[1, 8:]):
+        with pytest.raises(m.NvFp4MlaError):
+            m.kv8_keep(d[0], t, n, p, a, 2, 64, new_lens=new)
+    assert np.array_equal(d.cpu().numpy(), caches)
+
+
 def test_trim():
     rng = np.random.default_rng(31)
     lens = np.array([0, 1, 64, 65, 200, 640, 300, 128, 5000], np.int32)
@@ -691,3 +835,96 @@ def test_speculative_steps():
         assert np.array_equal(cache.cpu().numpy(), before)
         for a, b in ((dt, table), (dl, lens), (dr, refs)):
             assert np.array_equal(a.cpu().numpy(), b)
+
+
+def step_args(rng, B, Q, Hk, G, D, V, old, pages, layers=1, first=0):
+    """What a step needs, on the device, with sequences of `old` tokens whose pages begin at number `first`."""
+    H, lens = Hk * G, np.asarray(old, np.int32)
+    table, refs, at = np.full((B, 8), -1, np.int32), np.zeros(pages, np.int32), first
+    for b, n in enumerate(-(-lens // 64)):
+        table[b, :n] = np.arange(at, at + n)
+        refs[at:at + n] = 1
+        at += n
+    refs[:first] = 1
+    small = rng.integers(0, 0x78, (layers, at - first, m.kv8_page_bytes(Hk, D)), dtype=np.uint8)
+    for x in small:
+        kv8.parts(x, Hk, D)[1][:] = rng.integers(118, 131, kv8.parts(x, Hk, D)[1].shape)
+    cache = torch.zeros((layers, pages, small.shape[2]), dtype=torch.uint8, device="cuda")
+    cache[:, first:at] = torch.from_numpy(small).to("cuda")
+    parents, masks = trees(rng, B, Q)
+    depth = np.array([[max(1, len(spec.bits(x, Q))) - 1 for x in row] for row in masks])
+    angle = np.arange(600)[:, None] * 10000.0 ** (-np.arange(D // 2) / (D // 2))
+    rows = lambda heads: torch.from_numpy(rng.standard_normal((B * Q, heads, D))).to(torch.bfloat16).to("cuda")  # noqa: E731
+    c = verify_case(rng, B, Q, V, torch.float32, True)
+    put = lambda x: torch.as_tensor(x).to("cuda")  # noqa: E731
+    return dict(cache=cache, table=dev(table), lens=dev(lens), refs=dev(refs), q=rows(H), k=rows(Hk), v=rows(Hk), cu=dev(np.arange(B + 1) * Q),
+                add=dev(np.full(B, Q)), at=dev((lens[:, None] + depth).reshape(-1)), masks=dev(masks.view(np.int64), torch.int64),
+                parents=dev(parents), sheet=put(np.concatenate([np.cos(angle), np.sin(angle)], 1).astype(np.float32)), logits=put(c["logits"]),
+                drafts=dev(c["drafts"]), uniforms=put(c["uniforms"]), temperatures=put(c["temperatures"]), probs=put(c["draft_probs"]),
+                q_out=torch.zeros((B * Q, H, D), dtype=torch.bfloat16, device="cuda"),
+                out=torch.zeros((layers, B, Q, H, D), dtype=torch.bfloat16, device="cuda"), lse=torch.zeros((layers, B, Q, H), device="cuda"),
+                tokens=torch.zeros((B, Q), dtype=torch.int32, device="cuda"), path=torch.zeros((B, Q), dtype=torch.int32, device="cuda"),
+                accepted=torch.zeros(B, dtype=torch.int32, device="cuda"), new=torch.zeros(B, dtype=torch.int32, device="cuda"),
+                ws=torch.empty(m.kv8_decode_tree_workspace_size(B, Q, H, Hk, D), dtype=torch.uint8, device="cuda"),
+                ws2=torch.empty(m.spec_verify_workspace_size(B, Q, V), dtype=torch.uint8, device="cuda"))
+
+
+def run_step(a, Hk):
+    layers, B, Q, H, D = a["out"].shape
+    m.kv_pages_extend(a["table"], a["lens"], a["refs"], a["add"])
+    for i in range(layers):
+        m.kv8_append_rope(a["q"], a["k"], a["v"], a["sheet"], a["cu"], a["lens"], a["table"], a["cache"][i], positions=a["at"], q_out=a["q_out"])
+        m.kv8_decode_tree(a["q_out"].view(B, Q, H, D), a["cache"][i], a["table"], a["lens"], a["masks"], Hk, D ** -0.5, out=a["out"][i], lse=a["lse"][i],
+                          workspace=a["ws"])
+    m.spec_verify(a["logits"], a["drafts"], a["parents"], a["uniforms"], a["temperatures"], a["probs"], tokens=a["tokens"], path=a["path"],
+                  accepted=a["accepted"], workspace=a["ws2"])
+    m.kv8_keep(a["cache"], a["table"], a["lens"], a["path"], a["accepted"], Hk, D, new_lens=a["new"], layered=True)
+    m.kv_pages_trim(a["table"], a["lens"], a["refs"], a["new"])
+
+
+def test_a_captured_step_replays():
+    """A whole step in one graph, replayed over other tables, tokens and logits: what the calls do one by one."""
+    one, two = (step_args(np.random.default_rng(50 + i), 5, 14, 2, 3, 128, 1200, [60 + i, 3, 128 - i, 200, 1], 60, layers=2) for i in range(2))
+    start = {k: x.clone() for k, x in one.items()}
+    run_step(one, 2)                   # (loads the kernels)
+    for k, x in one.items():
+        x.copy_(start[k])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run_step(one, 2)
+    for source in (start, {k: x.clone() for k, x in two.items()}, start):
+        for k in one:
+            one[k].copy_(source[k])
+            two[k].copy_(source[k])
+        g.replay()
+        run_step(two, 2)
+        torch.cuda.synchronize()
+        for k in one:
+            if k not in ("ws", "ws2"):
+                assert torch.equal(one[k].view(torch.uint8), two[k].view(torch.uint8)), k
+
+
+def test_a_step_far_into_a_large_pool():
+    """Pages whose bytes lie beyond 2^32: the results of the same step in a small pool."""
+    big = step_args(np.random.default_rng(60), 3, 20, 8, 2, 128, 500, [50, 100, 200], 34000, first=33900)
+    small = step_args(np.random.default_rng(60), 3, 20, 8, 2, 128, 500, [50, 100, 200], 100, first=0)
+    assert big["cache"].stride(1) * 33900 > 1 << 32
+    run_step(big, 8)
+    run_step(small, 8)
+    torch.cuda.synchronize()
+    for k in ("q_out", "out", "lse", "tokens", "path", "accepted", "lens"):
+        assert torch.equal(big[k].view(torch.uint8), small[k].view(torch.uint8)), k
+    assert torch.equal(torch.where(big["table"] >= 0, big["table"] - 33900, -1), small["table"])
+    assert torch.equal(big["cache"][:, 33900:], small["cache"])
+
+
+def test_steps_of_no_requests():
+    """B = 0, N = 0: nothing is enqueued, and nothing refused."""
+    e = lambda *n, t=torch.int32: torch.zeros(n, dtype=t, device="cuda")  # noqa: E731
+    bf, cache = torch.bfloat16, torch.zeros((3, m.kv8_page_bytes(2, 64)), dtype=torch.uint8, device="cuda")
+    x = e(0, 2, 64, t=bf)
+    assert m.kv8_append_rope(e(0, 4, 64, t=bf), x, x, e(10, 64, t=torch.float32), e(1), e(0), e(0, 2), cache).shape == (0, 4, 64)
+    assert m.kv8_append_rope(e(0, 4, 64, t=bf), x, x, e(10, 64, t=torch.float32), e(3), e(2), e(2, 2), cache).shape == (0, 4, 64)
+    assert m.kv8_decode_tree(e(0, 5, 4, 64, t=bf), cache, e(0, 2), e(0), e(0, 5, t=torch.int64), 2, 0.1)[0].shape == (0, 5, 4, 64)
+    assert m.spec_verify(e(0, 5, 9, t=torch.float32), e(0, 5), e(0, 5), e(0, 5, t=torch.float32))[0].shape == (0, 5)
+    assert m.kv8_keep(cache, e(0, 2), e(0), e(0, 5), e(0), 2, 64).shape == (0,)
