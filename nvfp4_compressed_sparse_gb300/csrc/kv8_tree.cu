@@ -13,20 +13,31 @@
 //   S  8-bit products, as in kv8_decode: keys are used as they lie in the cache, and a query is a sum of E4M3
 //      numbers (two of a bf16, three of an fp16, the row's largest element at 2^7 to 2^8): what is left after them is
 //      half of E4M3's smallest step, 2^-10, 2^-17 of the largest. The parts are further steps along K: one sum.
-//   O  fp16 products of weights in fp16 and codes, which an fp16 holds exactly. A column's largest is 2^9 to 2^16,
-//      so half a step is 2^-12 of it, and at the lower end 2^-25 in those units: 2^-34 of the largest. (Weights as
-//      8-bit parts, as kv8_decode has them, need four for such a range: twice the tensor time, and some thirty
-//      instructions for a pair of weights where a conversion is one. There the codes need no conversion instead,
-//      which is 2 D a token and does not grow with the columns.)
+//   O  fp16 products of weights in fp16 and codes, which an fp16 holds exactly. A column's largest is held above 2^8
+//      and below 2^16, so half a step is 2^-12 of a weight, and at the lower end 2^-25 in those units: 2^-33 of the
+//      largest. (Weights as 8-bit parts, as kv8_decode has them, need four for such a range: twice the tensor time, and
+//      some thirty instructions for a pair of weights where a conversion is one. There the codes need no conversion
+//      instead, which is 2 D a token and does not grow with the columns.)
 //
-// One CTA per SM, persistent; the pages of all (request, key/value head, column tile) units form one sequence, cut
-// into one contiguous range a CTA. Its warps:
-//   0        producer: page numbers, then each page's keys (TMA, swizzled), values (as they lie) and scale bytes
+// One CTA per SM, persistent; the tiles (two pages, 128 tokens: one product's N) of all units (request, key/value head,
+// 128 columns) form one sequence, cut into one contiguous range a CTA. Its warps:
+//   0        producer: page numbers, then each tile's keys (TMA, swizzled), values (as they lie) and scale bytes
 //   1        issues S = q K;  3: issues O += w V (two threads, so that neither waits for the other)
+//   2        what the units' columns attend to, and their queries into L2, up to two units ahead
 //   4-7      feeders: the unit's queries as parts, then each page's values as fp16
-//   8-15     softmax: two streams, which take the pages in turn, a warpgroup each (thread = column, so that maxima
-//            and sums need no exchange). A stream has two buffers of S, w in the place of its S, and its own O, m, W, l
+//   8-15     softmax: a warpgroup a page of each tile, a thread a column, so that maxima and sums need no exchange
+//            but one between a column's two threads. S has three buffers, w lies in the place of its S, O is one
 // A unit that several CTAs share leaves means and sums in the workspace, which join_kernel adds up.
+//
+// Measured, back to back, against 6.77 TB/s of measured copy bandwidth: 16 requests of 2,000 to 16,000 tokens, 32 nodes of
+// 32 heads over 8 of 128: 94 us (45 % of it); one of 131,001 tokens, 16 nodes of 64 heads: 90 us (44 %); 24 requests of
+// 900 to 9,000 tokens, 64 nodes of 32 heads over 4 of 64, a window of 4,096, fp16: 91 us; one request of 1,000 tokens:
+// 20 us. A tile of 128 columns takes some 2,000 cycles, in which the tensor cores work for 1,100, and the softmax's chain
+// (its scores' arrival, 64 exponentials a thread, the two threads' vote, the weights' store) is as long as the tile is;
+// so is the feeders'. A unit costs some 11,000 more: its queries, its first and masked tiles, its results. What was tried
+// and not kept, in the order of the first three: a stream of tiles, and an O, for each warpgroup (112, 99, 100 us); keys
+// and values in rings of their own (92, 86, 113); queries fetched a tile ahead (100, 93, 92); the blocks of a page unrolled
+// instead of two at a time (97, 91, 95: the code of all warps together counts).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -130,15 +141,16 @@ __device__ __forceinline__ uint2 codes4(uint32_t w) {
       : "r"(w));
   return r;
 }
-// (a, b) as kParts pairs of E4M3 numbers whose sum they are, but for the last one's rounding. |a|, |b| < 256.
+// A pair of fp16 as kParts pairs of E4M3 numbers whose sum it is, but for the last one's rounding. Magnitudes below 256: what
+// a part leaves an fp16 holds exactly.
 template <int kParts>
-__device__ __forceinline__ void split(float a, float b, uint32_t (&part)[kParts]) {
-  float2 left = make_float2(a, b);
+__device__ __forceinline__ void split(uint32_t h, uint32_t (&part)[kParts]) {
 #pragma unroll
   for (int i = 0; i < kParts; ++i) {
-    part[i] = f32x2_to_e4m3x2(left.x, left.y);
-    const uint32_t h = e4m3x2_to_f16x2(part[i]);
-    left = __ffma2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h)), make_float2(-1.f, -1.f), left);
+    part[i] = f16x2_to_e4m3x2(h);
+    const uint32_t held = e4m3x2_to_f16x2(part[i]);
+    const __half2 left = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&held));
+    h = *reinterpret_cast<const uint32_t*>(&left);
   }
 }
 // bits lo .. hi - 1 of 64, none if there are none
@@ -266,6 +278,56 @@ struct Cta {
     __syncwarp();
   }
 
+  // ---------------------------------------------------------------- what a unit's columns attend to (warp 2)
+  __device__ __forceinline__ int node_of(int col) const { return (int)(((uint64_t)(uint32_t)col * p.group_inverse) >> 24); }   // col / group
+  // Ahead of the others, by up to two units, as it waits for memory alone.
+  __device__ void columns(Walk w) {
+    const int lane = threadIdx.x & 31, ncols = p.Q * p.group;
+    const uint64_t bits_of = p.Q == 64 ? ~0ull : (1ull << p.Q) - 1;
+    for (uint32_t seg = 0; w.left > 0; ++seg, w.next(p)) {
+      const uint32_t buf = seg & 1;
+      if (!wait_warp(&ctl->done[buf], ((seg >> 1) & 1) ^ 1)) return;     // the unit before the last is written
+      const int base = w.len - p.Q;
+      const uint64_t* masks = p.masks + (int64_t)w.b * p.Q;
+      uint64_t some = 0, all = ~0ull;
+      int first = INT_MAX, last = 0;
+#pragma unroll 1
+      for (int j = lane; j < p.Q; j += 32) {
+        const uint64_t mask = __ldg(masks + j);
+        if (mask == 0) continue;
+        some |= mask & bits_of;
+        all &= mask & bits_of;
+        const int lo = p.window > 0 ? max(0, base + max(1, __popcll(mask & bits_of)) - p.window) : 0;
+        first = min(first, lo);
+        last = max(last, lo);
+      }
+      const uint32_t some0 = __reduce_or_sync(kFull, (uint32_t)some), some1 = __reduce_or_sync(kFull, (uint32_t)(some >> 32));
+      const uint32_t all0 = __reduce_and_sync(kFull, (uint32_t)all), all1 = __reduce_and_sync(kFull, (uint32_t)(all >> 32));
+      first = __reduce_min_sync(kFull, first);
+      last = __reduce_max_sync(kFull, last);
+      if (lane == 0) {
+        ctl->any_mask[buf] = (uint64_t)some1 << 32 | some0;
+        ctl->all_mask[buf] = ((uint64_t)all1 << 32 | all0) & bits_of;
+        ctl->any_lo[buf] = first;
+        ctl->all_lo[buf] = last;
+      }
+#pragma unroll 1
+      for (int c = lane; c < kCols; c += 32) {
+        const int col = w.ct * kCols + c, j = node_of(col);
+        const uint64_t mask = col < ncols ? __ldg(masks + j) : 0;
+        const int place = base + max(1, __popcll(mask & bits_of)) - 1;
+        ctl->mask[buf][c] = mask & bits_of;
+        ctl->lo[buf][c] = mask == 0 ? INT_MAX : (p.window > 0 ? max(0, place - p.window + 1) : 0);
+        // (the next unit's queries come from memory while this one's tiles are at work)
+        if (col < ncols)
+          for (int k = 0; k < D * 2; k += 128) prefetch_l2(reinterpret_cast<const uint8_t*>(p.q + ((int64_t)w.b * p.Q + j) * p.q_token_stride + (w.kvh * p.group + col - j * p.group) * p.q_head_stride) + k);
+        ctl->row[buf][c] = col < ncols ? (w.b * p.Q + j) * p.H + w.kvh * p.group + (col - j * p.group) : -1;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->q_full[buf]);
+    }
+  }
+
   // ---------------------------------------------------------------- S = q K (warp 1, one thread)
   __device__ void issue_s(Walk w, uint32_t tmem) {
     constexpr uint32_t kId = idesc_e4m3(kCols, kTile, false, false);
@@ -330,88 +392,58 @@ struct Cta {
   }
 
   // ---------------------------------------------------------------- feeders (warps 4-7)
-  // The unit's queries, and what its columns attend to.
-  template <bool kHalf>
-  __device__ void queries(const Walk& w, uint32_t buf) {
-    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = 32 / kAtOnce, kTogether = 2, kAhead = 8;    // rounds whose chains, and loads, are under way together (little code: it is fetched once a unit)
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, sub = lane / kLanes, ch = lane % kLanes;
-    const int ncols = p.Q * p.group, base = w.len - p.Q;
-    auto node_of = [&](int col) { return (int)(((uint64_t)(uint32_t)col * p.group_inverse) >> 24); };   // col / group
-    auto load = [&](int round) {
-      const int col = w.ct * kCols + warp * 32 + round * kAtOnce + sub;
-      if (round >= kRounds || col >= ncols) return make_uint4(0u, 0u, 0u, 0u);
-      const int j = node_of(col), h = w.kvh * p.group + col - j * p.group;
-      return *reinterpret_cast<const uint4*>(p.q + ((int64_t)w.b * p.Q + j) * p.q_token_stride + h * p.q_head_stride + ch * 8);
-    };
-    const uint64_t* masks = p.masks + (int64_t)w.b * p.Q;
-    const uint64_t bits_of = p.Q == 64 ? ~0ull : (1ull << p.Q) - 1;
-    uint4 v[kAhead];
+  static constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = 32 / kAtOnce;    // of a row; rows of a load; loads of a lane
+  // The unit's queries, on their way: a warp has 32 rows.
+  __device__ __forceinline__ void fetch(const Walk& w, uint4 (&v)[kRounds]) {
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+    // a lane a column: where its row is
+    const int col = w.ct * kCols + warp * 32 + lane, j = node_of(col);
+    const int64_t mine = col < p.Q * p.group ? ((int64_t)w.b * p.Q + j) * p.q_token_stride + (w.kvh * p.group + col - j * p.group) * p.q_head_stride : -1;
 #pragma unroll
-    for (int r = 0; r < kAhead; ++r) v[r] = load(r);
-    {
-      // a lane a column: what it attends to
-      const int c = warp * 32 + lane, col = w.ct * kCols + c, j = node_of(col);
-      const uint64_t mask = col < ncols ? masks[j] : 0;
-      const int place = base + max(1, __popcll(mask & bits_of)) - 1;
-      ctl->mask[buf][c] = mask & bits_of;
-      ctl->lo[buf][c] = mask == 0 ? INT_MAX : (p.window > 0 ? max(0, place - p.window + 1) : 0);
-      ctl->row[buf][c] = col < ncols ? (w.b * p.Q + j) * p.H + w.kvh * p.group + (col - j * p.group) : -1;
+    for (int r = 0; r < kRounds; ++r) {
+      const int64_t at = __shfl_sync(kFull, mine, r * kAtOnce + lane / kLanes);
+      v[r] = make_uint4(0u, 0u, 0u, 0u);
+      if (at >= 0) v[r] = *reinterpret_cast<const uint4*>(p.q + at + (lane % kLanes) * 8);
     }
-    if (warp == 0) {
-      uint64_t some = 0, all = ~0ull;
-      int first = INT_MAX, last = 0;
-      for (int j = lane; j < p.Q; j += 32) {
-        const uint64_t mask = masks[j];
-        if (mask == 0) continue;
-        some |= mask & bits_of;
-        all &= mask & bits_of;
-        const int lo = p.window > 0 ? max(0, base + max(1, __popcll(mask & bits_of)) - p.window) : 0;
-        first = min(first, lo);
-        last = max(last, lo);
-      }
-      const uint32_t some0 = __reduce_or_sync(kFull, (uint32_t)some), some1 = __reduce_or_sync(kFull, (uint32_t)(some >> 32));
-      const uint32_t all0 = __reduce_and_sync(kFull, (uint32_t)all), all1 = __reduce_and_sync(kFull, (uint32_t)(all >> 32));
-      first = __reduce_min_sync(kFull, first);
-      last = __reduce_max_sync(kFull, last);
-      if (lane == 0) {
-        ctl->any_mask[buf] = (uint64_t)some1 << 32 | some0;
-        ctl->all_mask[buf] = ((uint64_t)all1 << 32 | all0) & bits_of;
-        ctl->any_lo[buf] = first;
-        ctl->all_lo[buf] = last;
-      }
-    }
+  }
+  // And as parts.
+  template <bool kHalf>
+  __device__ __forceinline__ void queries(uint4 (&v)[kRounds], uint32_t buf) {
+    constexpr int kTogether = 4;         // loads whose chains are under way together
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, sub = lane / kLanes, ch = lane % kLanes;
 #pragma unroll 1
     for (int r0 = 0; r0 < kRounds; r0 += kTogether) {
       uint4 x[kTogether];
-      uint32_t top[kTogether];
+      uint32_t top[kTogether / 2];       // of two rows
 #pragma unroll
-      for (int i = 0; i < kTogether; ++i) {
-        x[i] = v[i];
-        top[i] = __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu), __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
-        top[i] = max(top[i] & 0xFFFFu, top[i] >> 16);
+      for (int i = 0; i < kTogether; ++i) x[i] = v[i];
+#pragma unroll
+      for (int i = 0; i + kTogether < kRounds; ++i) v[i] = v[i + kTogether];
+#pragma unroll
+      for (int i = 0; i < kTogether; i += 2) {
+        auto most = [&](const uint4& y) { return __vmaxu2(__vmaxu2(y.x & 0x7FFF7FFFu, y.y & 0x7FFF7FFFu), __vmaxu2(y.z & 0x7FFF7FFFu, y.w & 0x7FFF7FFFu)); };
+        const uint32_t a = most(x[i]), b = most(x[i + 1]);
+        top[i / 2] = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
       }
-#pragma unroll
-      for (int i = 0; i + kTogether < kAhead; ++i) v[i] = v[i + kTogether];
-#pragma unroll
-      for (int i = 0; i < kTogether; ++i) v[kAhead - kTogether + i] = load(r0 + kAhead + i);
 #pragma unroll
       for (int d = 1; d < kLanes; d <<= 1)
 #pragma unroll
-        for (int i = 0; i < kTogether; ++i) top[i] = max(top[i], __shfl_xor_sync(kFull, top[i], d));
+        for (int i = 0; i < kTogether / 2; ++i) top[i] = __vmaxu2(top[i], __shfl_xor_sync(kFull, top[i], d));
 #pragma unroll
       for (int i = 0; i < kTogether; ++i) {
         const int n = warp * 32 + (r0 + i) * kAtOnce + sub;
-        const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        const bool finite = top[i] < (kHalf ? 0x7C00u : 0x7F80u);
+        const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, most = (top[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+        const bool finite = most < (kHalf ? 0x7C00u : 0x7F80u);
         // the largest magnitude goes to [128, 256): a power of two, exact
-        const int e = (int)(__float_as_uint(widen2<kHalf>(top[i]).x) >> 23) - 127;
-        const int sh = top[i] == 0 || !finite ? 0 : min(7 - e, 126);
-        const float mul = finite ? __uint_as_float((uint32_t)(sh + 127) << 23) : 0.f;
+        const int e = (int)(__float_as_uint(widen2<kHalf>(most).x) >> 23) - 127;
+        const int sh = most == 0 || !finite ? 0 : min(7 - e, 126);
+        const float mul = __uint_as_float((uint32_t)(sh + 127) << 23);
         uint32_t part[4][kQ];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float2 y = widen2<kHalf>(ws[k]);
-          split(finite ? y.x * mul : 0.f, finite ? y.y * mul : 0.f, part[k]);
+          // (fp16 is off by 2^-25 at most, where the parts' last is off by 2^-10; a row with an infinity or a NaN has f)
+          const float2 y = __fmul2_rn(widen2<kHalf>(ws[k]), make_float2(mul, mul));
+          split(narrow2<true>(y.x, y.y), part[k]);
         }
         const int chunk = D == 128 ? ((ch >> 1) ^ (n & 7)) : ((ch >> 1) ^ ((n >> 1) & 3));
 #pragma unroll
@@ -441,10 +473,12 @@ struct Cta {
   }
   __device__ __noinline__ uint4 without_nans(uint4 x, int t, int c, uint32_t buf, int base) {
     uint8_t* byte = reinterpret_cast<uint8_t*>(&x);
+#pragma unroll 1
     for (int k = 0; k < 16; ++k) {
       if ((byte[k] & 0x7F) != 0x7F) continue;
       byte[k] = 0;
       const int d = c * 16 + k;
+#pragma unroll 1
       for (int n = 0; n < kCols; ++n) {
         const bool attends = t < base ? t >= ctl->lo[buf][n] : ((ctl->mask[buf][n] >> (t - base)) & 1) != 0;
         if (attends) atomicOr(&ctl->poison[buf][n][d >> 5], 1u << (d & 31));
@@ -465,30 +499,37 @@ struct Cta {
     bool ok = true;
     for (uint32_t seg = 0; w.left > 0; ++seg, w.next(p)) {
       const uint32_t buf = seg & 1;
+      uint4 q[kRounds];
+      fetch(w, q);
       ok = ok && wait_warp(&ctl->q_empty, (seg & 1) ^ 1);              // the products with the last unit's queries are complete
       ok = ok && wait_warp(&ctl->done[buf], ((seg >> 1) & 1) ^ 1);     // and the unit's before that is written
       if (ok) {
-        queries<kHalf>(w, buf);
+        queries<kHalf>(q, buf);
         fence_proxy_async_smem();
       }
       if (bar_any(kBarFeeders, kFeeders, !ok)) return;
       if (lane == 0) mbar_arrive(&ctl->q_full[buf]);
+      ok = wait_warp(&ctl->q_full[buf], (seg >> 1) & 1);                 // what the columns attend to
       const int base = w.len - p.Q, all_lo = ctl->all_lo[buf], any_lo = ctl->any_lo[buf];
       for (int i = 0; ok && i < w.count; ++i, ++t) {
         ok = wait_warp(&ctl->full[ring.st], ring.phase);
         if (t >= 2) ok = ok && wait_warp(&ctl->o_done[used.st], used.phase);
         if (!ok) break;
+#pragma unroll 1
         for (int half = 0; half < kHalves; ++half) {
           const int t0 = (w.first + w.at + i) * kTile + half * kPageTokens;
           const uint8_t* from = stages + ring.st * S::kStageBytes + (kHalves + half) * S::kCodes;
           uint8_t* img = vimg + (vbuf.st * kHalves + half) * S::kVBytes;
           const bool page_ok = ((ctl->pages_ok[ring.st] >> half) & 1) != 0;
           if (page_ok && t0 >= all_lo && t0 + kPageTokens <= base) {
-            uint4 x[kLoads];
+#pragma unroll 1
+            for (int k0 = 0; k0 < kLoads; k0 += 2) {
+              uint4 x[2];
 #pragma unroll
-            for (int k = 0; k < kLoads; ++k) x[k] = *reinterpret_cast<const uint4*>(from + (tid + k * kFeeders) * 16);
+              for (int k = 0; k < 2; ++k) x[k] = *reinterpret_cast<const uint4*>(from + (tid + (k0 + k) * kFeeders) * 16);
 #pragma unroll
-            for (int k = 0; k < kLoads; ++k) put_values(img, x[k], (tid + k * kFeeders) / kChunks, (tid + k * kFeeders) % kChunks);
+              for (int k = 0; k < 2; ++k) put_values(img, x[k], (tid + (k0 + k) * kFeeders) / kChunks, (tid + (k0 + k) * kFeeders) % kChunks);
+            }
           } else {
             const uint64_t any = page_ok ? bits(any_lo - t0, base - t0) | nodes_at(ctl->any_mask[buf], base, t0) : 0;
             const uint64_t all = page_ok ? bits(all_lo - t0, base - t0) | nodes_at(ctl->all_mask[buf], base, t0) : 0;
@@ -675,8 +716,9 @@ struct Cta {
         least_ev = __all_sync(kFull, plain) ? (int)highest - 80 + 127 : 256;
       };
       int t0 = (w.first + w.at) * kTile + half * kPageTokens;
+      bool there = false;                                // the next tile's scores, as far as is known
       for (int i = 0; ok && i < w.count; ++i, t0 += kTile) {
-        ok = wait_warp(&ctl->full[ring.st], ring.phase) && wait_warp(&ctl->s_full[at.st], at.phase);
+        if (!__all_sync(kFull, there)) ok = wait_warp(&ctl->full[ring.st], ring.phase) && wait_warp(&ctl->s_full[at.st], at.phase);
         tc_fence_after();
         if (!idle) {
           const bool page_ok = ((ctl->pages_ok[ring.st] >> half) & 1) != 0, whole = ok && page_ok && t0 >= all_lo && t0 + kPageTokens <= base;
@@ -693,27 +735,34 @@ struct Cta {
           // One exponential serves w and l where fp32 holds the one beside the other: the smallest that matters to l,
           // 2^-40, has a weight above 2^-120.
           if (fits) {
-            uint32_t s[2][32];
-            tmem_ld32(s_at, s[0]);
-            tmem_ld32(s_at + 32, s[1]);
-            tmem_wait_ld();
+            uint2 left = sc;
+#pragma unroll 1
+            for (int part = 0; part < 64; part += 32) {
+              uint32_t s[32];
+              tmem_ld32(s_at + part, s);
+              tmem_wait_ld();
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const uint32_t kb = (sc.x >> (8 * b)) & 0xFFu, vb = (sc.y >> (8 * b)) & 0xFFu;
-              const float c = f * __uint_as_float(kb << 23);
-              const float k0 = (__uint_as_float(0x4B000000u | vb) - 8388735.f) + offset;     // whole numbers: exact
-              const float2 cc = make_float2(c, c), kk = make_float2(k0, k0);
-              float2 sum = make_float2(0.f, 0.f);
+              for (int k = 0; k < 16; ++k) out[k] = out[16 + k];
 #pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                const float2 a = __ffma2_rn(pair_of(s[b >> 1], (b & 1) * 16 + k), cc, kk);
-                const float2 e = make_float2(ex2_approx(a.x), ex2_approx(a.y));
-                sum = __fadd2_rn(sum, e);
-                out[b * 8 + k / 2] = narrow2<true>(e.x, e.y);
+              for (int b = 0; b < 2; ++b) {
+                const uint32_t kb = (left.x >> (8 * b)) & 0xFFu, vb = (left.y >> (8 * b)) & 0xFFu;
+                const float c = f * __uint_as_float(kb << 23);
+                const float k0 = (__uint_as_float(0x4B000000u | vb) - 8388735.f) + offset;     // whole numbers: exact
+                const float2 cc = make_float2(c, c), kk = make_float2(k0, k0);
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                  const float2 a = __ffma2_rn(pair_of(s, b * 16 + k), cc, kk);
+                  const float2 e = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+                  sum = __fadd2_rn(sum, e);
+                  out[16 + b * 8 + k / 2] = narrow2<true>(e.x, e.y);
+                }
+                const float both = sum.x + sum.y;
+                most = fmaxf(most, both);
+                more = fmaf(both * back, __uint_as_float((254u - vb) << 23), more);
               }
-              const float both = sum.x + sum.y;
-              most = fmaxf(most, both);
-              more = fmaf(both * back, __uint_as_float((254u - vb) << 23), more);
+              left.x >>= 16;
+              left.y >>= 16;
             }
           }
           if (__builtin_expect(!bar_any(kBarQuarter + warp, 64, !fits || most > kMostWeights), 1)) {
@@ -728,18 +777,21 @@ struct Cta {
             ok = !bar_any(kBarQuarter + warp, 64, !careful(refs, half, s_at, f, sc, mine, i > 0 ? at_rest : nullptr, rest_phase, o_at));
             known();
           }
-          tmem_wait_st();
-          tc_fence_before();
         }
-        __syncwarp();
-        if (ok && lane == 0) {
-          mbar_arrive(&ctl->w_full[at.st]);
-          mbar_arrive(&ctl->empty[ring.st]);
-        }
+        uint64_t *const done = &ctl->w_full[at.st], *const free = &ctl->empty[ring.st];
         at_rest = &ctl->o_done[at.st];
         rest_phase = at.phase;
         ring.next();
         at.next();
+        // (asked for here, the answer comes while the weights are stored)
+        there = mbar_test(&ctl->full[ring.st], ring.phase) & mbar_test(&ctl->s_full[at.st], at.phase) & (i + 1 < w.count);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (ok && lane == 0) {
+          mbar_arrive(done);
+          mbar_arrive(free);
+        }
       }
       // ---- the segment's end: half of the dims each
       ok = ok && wait_warp(at_rest, rest_phase);
@@ -824,7 +876,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
       mbar_init(&ctl->empty[i], (kFeeders + kSoftmaxThreads) / 32);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->q_full[i], 4);
+      mbar_init(&ctl->q_full[i], kFeeders / 32 + 1);
       mbar_init(&ctl->done[i], kSoftmaxThreads / 32);
       mbar_init(&ctl->drain[i], 1);
       ctl->any_poison[i] = 0;
@@ -906,6 +958,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     } else if (warp == 1) {
       if (lane == 0) c.issue_s(w, tmem);
       __syncwarp();
+    } else if (warp == 2) {
+      c.columns(w);
     } else if (warp == 3) {
       if (lane == 0) c.issue_o(w, tmem);
       __syncwarp();
