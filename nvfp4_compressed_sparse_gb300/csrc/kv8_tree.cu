@@ -30,9 +30,9 @@
 // A unit that several CTAs share leaves means and sums in the workspace, which join_kernel adds up.
 //
 // Measured, back to back, against 6.77 TB/s of measured copy bandwidth: 16 requests of 2,000 to 16,000 tokens, 32 nodes of
-// 32 heads over 8 of 128: 94 us (45 % of it); one of 131,001 tokens, 16 nodes of 64 heads: 90 us (44 %); 24 requests of
-// 900 to 9,000 tokens, 64 nodes of 32 heads over 4 of 64, a window of 4,096, fp16: 91 us; one request of 1,000 tokens:
-// 20 us. A tile of 128 columns takes some 2,000 cycles, in which the tensor cores work for 1,100, and the softmax's chain
+// 32 heads over 8 of 128: 94 us (45 % of it); one of 131,001 tokens, 16 nodes of 64 heads: 91 us (44 %); 24 requests of
+// 900 to 9,000 tokens, 64 nodes of 32 heads over 4 of 64, a window of 4,096, fp16: 87 us; one request of 1,000 tokens:
+// 19 us. A tile of 128 columns takes some 2,000 cycles, in which the tensor cores work for 1,100, and the softmax's chain
 // (its scores' arrival, 64 exponentials a thread, the two threads' vote, the weights' store) is as long as the tile is;
 // so is the feeders'. A unit costs some 11,000 more: its queries, its first and masked tiles, its results. What was tried
 // and not kept, in the order of the first three: a stream of tiles, and an O, for each warpgroup (112, 99, 100 us); keys
@@ -591,9 +591,30 @@ struct Cta {
     bar_sync(kBarQuarter + warp, 64);
   }
 
-  // A page's weights in the place of its scores, with whatever is rare: positions that the column does not attend to,
-  // new references, and scores or scales so wide that sum and weights need an exponential each. Both halves' threads of
-  // a quarter of the columns come here together. (at_rest: the barrier of the product before, or null; false: a wait gave up.)
+  // The scores of positions that a column does not attend to become -inf, and the scale bytes of a block that has no other,
+  // which may be anything, those of 1. (Loops: code that runs a few times costs what its fetching costs.)
+  static __device__ __noinline__ uint2 leave_out(uint32_t s_at, uint64_t mine, uint2 sc) {
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+      __syncwarp();
+      uint32_t s[16];
+      tmem_ld16(s_at + 16 * b, s);
+      tmem_wait_ld();
+      const uint32_t in = (uint32_t)(mine >> (16 * b)) & 0xFFFFu;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) s[k] = (in >> k) & 1 ? s[k] : 0xFF800000u;
+      tmem_st16(s_at + 16 * b, s);
+      const uint32_t at = in == 0 ? 0xFFu << (8 * b) : 0u;
+      sc.x = (sc.x & ~at) | (0x7F7F7F7Fu & at);
+      sc.y = (sc.y & ~at) | (0x7F7F7F7Fu & at);
+    }
+    tmem_wait_st();
+    return sc;
+  }
+
+  // A page's weights in the place of its scores, with whatever is rarer: new references, and scores or scales so
+  // wide that sum and weights need an exponential each. Both halves' threads of a quarter of the columns come here together.
+  // (at_rest: the barrier of the product before, or null; false: a wait gave up.)
   __device__ __noinline__ bool careful(Refs& refs, int half, uint32_t s_at, float f, uint2 sc, uint64_t mine, uint64_t* at_rest, uint32_t parity, uint32_t o_at) {
     Refs t = refs;
     const int warp = (threadIdx.x >> 5) & 3, r = threadIdx.x & 127;
@@ -721,17 +742,24 @@ struct Cta {
         if (!__all_sync(kFull, there)) ok = wait_warp(&ctl->full[ring.st], ring.phase) && wait_warp(&ctl->s_full[at.st], at.phase);
         tc_fence_after();
         if (!idle) {
-          const bool page_ok = ((ctl->pages_ok[ring.st] >> half) & 1) != 0, whole = ok && page_ok && t0 >= all_lo && t0 + kPageTokens <= base;
-          const uint2 sc = reinterpret_cast<const uint2*>(&ctl->scales[ring.st][half])[w.kvh & 1];
+          const bool page_ok = ((ctl->pages_ok[ring.st] >> half) & 1) != 0, whole = page_ok && t0 >= all_lo && t0 + kPageTokens <= base;
+          uint2 sc = reinterpret_cast<const uint2*>(&ctl->scales[ring.st][half])[w.kvh & 1];
           const uint32_t s_at = quarter + at.st * kTile + half * kPageTokens;
-          if (__builtin_expect(least_ev > 255, 0) && !bar_any(kBarQuarter + warp, 64, !whole)) {
+          uint64_t mine = ~0ull;
+          if (__builtin_expect(!whole, 0)) {
+            // (what a padding node's column sums is not wanted: it attends to what any does, for references of the page's size)
+            mine = page_ok ? (lo == INT_MAX ? bits(ctl->any_lo[buf] - t0, base - t0) | nodes_at(ctl->any_mask[buf], base, t0) : bits(lo - t0, base - t0) | nodes_at(ctl->mask[buf][r], base, t0)) : 0;
+            sc = leave_out(s_at, mine, sc);
+          }
+          if (__builtin_expect(least_ev > 255, 0) && !bar_any(kBarQuarter + warp, 64, !ok)) {
             start(refs, half, s_at, f, sc);
             known();
           }
           const uint32_t ev2 = __vminu2(__byte_perm(sc.y, 0u, 0x4140), __byte_perm(sc.y, 0u, 0x4342));
           uint32_t out[32];
           float more = 0.f, most = 0.f;
-          const bool fits = whole && (int)min(ev2 & 0xFFu, ev2 >> 16) >= least_ev;
+          // (of the warp: its loads are made by all lanes together)
+          const bool fits = __all_sync(kFull, ok && (int)min(ev2 & 0xFFu, ev2 >> 16) >= least_ev);
           // One exponential serves w and l where fp32 holds the one beside the other: the smallest that matters to l,
           // 2^-40, has a weight above 2^-120.
           if (fits) {
@@ -746,7 +774,7 @@ struct Cta {
 #pragma unroll
               for (int b = 0; b < 2; ++b) {
                 const uint32_t kb = (left.x >> (8 * b)) & 0xFFu, vb = (left.y >> (8 * b)) & 0xFFu;
-                const float c = f * __uint_as_float(kb << 23);
+                const float c = fmaf(f, __uint_as_float(kb << 23), 1e-37f);      // (not 0: -inf times it stays what it is)
                 const float k0 = (__uint_as_float(0x4B000000u | vb) - 8388735.f) + offset;     // whole numbers: exact
                 const float2 cc = make_float2(c, c), kk = make_float2(k0, k0);
                 float2 sum = make_float2(0.f, 0.f);
@@ -772,7 +800,6 @@ struct Cta {
             ok = false;
             break;
           } else {
-            const uint64_t mine = whole ? ~0ull : (page_ok ? bits(lo == INT_MAX ? 64 : lo - t0, base - t0) | nodes_at(ctl->mask[buf][r], base, t0) : 0);
             // (both halves' warps of a quarter go on together, or give up together)
             ok = !bar_any(kBarQuarter + warp, 64, !careful(refs, half, s_at, f, sc, mine, i > 0 ? at_rest : nullptr, rest_phase, o_at));
             known();
@@ -799,7 +826,7 @@ struct Cta {
       tc_fence_before();
       if (bar_any(kBarSoftmax, kSoftmaxThreads, !ok)) return;
       tc_fence_after();
-      const bool pad = row < 0 || lo == INT_MAX;         // a padding node's column: whatever was summed is not wanted
+      const bool pad = lo == INT_MAX;                    // no node: whatever was summed is not wanted
       const float top = refs.none() || pad ? kNone : refs.m, sum = pad ? 0.f : ctl->l[0][r] + ctl->l[1][r];
       // what O is multiplied by makes it the weighted mean at once, in two factors that stay far from fp32's ends
       const int up = max(0, min(126, (int)((__float_as_uint(sum) >> 23) & 0xFFu) - 127));

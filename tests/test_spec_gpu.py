@@ -369,6 +369,29 @@ def test_tree_wide_scores_and_scales():
         check_tree(*run_tree(c, masks, q=q), tree_reference(c, masks, q=q), 1000)
 
 
+def test_tree_blocks_that_hold_anything():
+    """Codes and scale bytes of every value where nothing is attended to (behind the end, before the window), and blocks with the
+    smallest scale byte, 0, among those that are attended to in part."""
+    for D, window in ((64, 0), (128, 40)):
+        rng = np.random.default_rng(17)
+        c = Case([70, 200, 131, 64 + 16], 2, D, "bf16", 12, 3, seed=17)
+        _, masks = trees(rng, 4, 12)
+        codes, scales = kv8.parts(c.cache, 2, D)
+        for b, n in enumerate(c.lens):
+            first = max(0, n - 12 + 1 - window) if window else 0
+            for t in range(c.table.shape[1] * 64):
+                page = c.table[b, t // 64]
+                if page < 0 or first <= t < n:
+                    continue
+                codes[page, :, :, t % 64] = rng.integers(0, 256, codes[page, :, :, 0].shape)
+                if t % 16 == 0 and (t >= n or t + 16 <= first):
+                    scales[page, :, :, t % 64 // 16] = rng.choice([0, 1, 120, 254, 255], scales[page, :, :, 0].shape)
+            t = n - 1
+            scales[c.table[b, t // 64], 0, 0, t % 64 // 16] = 0
+            scales[c.table[b, t // 64], 1, 1, t % 64 // 16] = 0
+        check_tree(*run_tree(c, masks, window), tree_reference(c, masks, window), 500, f"{D}")
+
+
 def test_tree_bad_pages_are_left_out_and_counted():
     c = Case([64 * 5 + 3, 64 * 4, 100], 2, 64, "bf16", 6, 2, seed=9)
     _, masks = trees(np.random.default_rng(9), 3, 6)
