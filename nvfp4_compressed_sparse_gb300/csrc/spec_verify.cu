@@ -6,12 +6,20 @@
 // children were drawn from; a draft without one stands for itself, q(x) = 1, and its refusal takes x out of
 // r.) When no child is taken, the next token is drawn from r by its running sum.
 //
-// What bounds it. Every row of logits is read once, for its largest value and its sum of exponentials.
-// stats_kernel does that by chunks of 4 KB, a warp each, whose values stay in registers; the chunks' sums are
-// kept, since with them a token can be drawn by reading a single chunk again. walk_kernel has a CTA a request
-// (with draft distributions a cluster of eight, since what a refusal leaves is a sum over the vocabulary): all
-// nodes' probabilities are found at once, so that the walk itself is a few comparisons. Running sums over chunks
-// are in 64 bits: what is drawn changes where they cross a border between tokens.
+// What bounds it. Every row of logits is read once, for its largest value and its sum of exponentials: memory, where there
+// are many rows. stats_kernel does that by chunks of 4 KB, a warp each, whose values stay in registers; the chunks' sums
+// are kept, since with them a token can be drawn by reading a single chunk again. walk_kernel has a CTA a request (with
+// draft distributions a cluster of eight, since what a refusal leaves is a sum over the vocabulary): all nodes'
+// probabilities are found at once, so that the walk itself is a few comparisons. It is a chain of some eight dependent
+// reads, and of code that runs once. Running sums over chunks are in 64 bits: what is drawn changes where they cross a
+// border between tokens.
+//
+// Measured, back to back, against 6.77 TB/s of measured copy bandwidth: 64 chains of 5 nodes over 128,000 bf16 logits with
+// draft distributions 32 us (53 % of it, over logits and the distributions of refusing nodes: some 17 us are stats_kernel's,
+// 15 the walk's), 16 trees of 32 over 100,003 without 31 us (49 %: 21 and 10), one chain of 5 over 32,000 fp32 10 us (all
+// latency). What was tried and not kept: chunks that come to shared memory ahead of a warp's work, by a ring of three a
+// warp (37 to 40, 37 and 12 us); a walk in 64 bits, or unrolled (its code is fetched once a call, some 16 cycles an
+// instruction); the next distribution brought to L2 (no difference).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -27,7 +35,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kChunkBytes = 4096;      // of a row that a warp takes: eight 16-byte loads a lane, all in flight
-constexpr int kStatsThreads = 256;
+constexpr int kStatsThreads = 128;
 constexpr int kWalkCtas = 8;           // of a request, with draft distributions
 constexpr int kMaxNodes = 64;
 constexpr int kFine = 8;               // warps' loads of a chunk
@@ -122,6 +130,35 @@ __device__ __forceinline__ float warp_max(float x) {
   return r;
 }
 
+// The largest logit of some loads; a NaN counts as none. Pairs of 16 bits are compared as they are.
+template <int kLoads>
+__device__ __forceinline__ float largest_of(const uint4 (&w)[kLoads], const float*) {
+  float m = neg_inf();
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i)
+    m = fmaxf(fmaxf(fmaxf(m, __uint_as_float(w[i].x)), fmaxf(__uint_as_float(w[i].y), __uint_as_float(w[i].z))), __uint_as_float(w[i].w));
+  return m;
+}
+template <int kLoads, typename T>
+__device__ __forceinline__ float largest_of(const uint4 (&w)[kLoads], const T*) {
+  uint32_t m[2] = {w[0].x, w[0].y};
+  auto more = [](uint32_t& m, uint32_t x) {
+    if constexpr (__is_same(T, __half)) asm("max.f16x2 %0, %0, %1;" : "+r"(m) : "r"(x));
+    else asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x));
+  };
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    more(m[0], w[i].x);
+    more(m[1], w[i].y);
+    more(m[0], w[i].z);
+    more(m[1], w[i].w);
+  }
+  more(m[0], m[1]);
+  float two[8];
+  widen(make_uint4(m[0], m[0], m[0], m[0]), two, (const T*)nullptr);
+  return fmaxf(fmaxf(two[0], two[1]), neg_inf());        // (-inf, should all of them be NaN)
+}
+
 // A chunk's largest logit, and the sum of its exponentials against that; greedy: where the largest is first.
 template <typename T>
 __global__ void __launch_bounds__(kStatsThreads) stats_kernel(const __grid_constant__ VerifyParams p) {
@@ -136,15 +173,7 @@ __global__ void __launch_bounds__(kStatsThreads) stats_kernel(const __grid_const
 #pragma unroll
   for (int i = 0; i < V::kLoads; ++i) w[i] = load_vec(row, at + (i * 32 + lane) * V::kN, p.V);
   const Rate rate = rate_of(p, r / p.Q);
-  float m = neg_inf();
-#pragma unroll
-  for (int i = 0; i < V::kLoads; ++i) {
-    float x[V::kN];
-    widen(w[i], x, row);
-#pragma unroll
-    for (int k = 0; k < V::kN; ++k) m = fmaxf(m, x[k]);
-  }
-  m = warp_max(m);
+  const float m = warp_max(largest_of(w, row));
   const int64_t to = (int64_t)r * p.chunks + chunk;
   if (rate.hi < 0.f) {
     int where = INT_MAX;
@@ -291,8 +320,8 @@ struct Walker {
   __device__ __forceinline__ double* entry_sums() const { return p.entry_sum + (int64_t)b * p.chunks * kFine; }
 
   // The entries' sums, and from there of all: sh.sum, the same in every CTA. A lane of warp 0 has a run of them; returns
-  // what lies before it. again: not the first time.
-  __device__ double sums(int j, int refused, bool again) {
+  // what lies before it, and what it has. again: not the first time.
+  __device__ double2 sums(int j, int refused, bool again) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = entries(j, refused);
     double* to = entry_sums();
     if (again) {                         // (all have read the sums before these)
@@ -342,7 +371,7 @@ struct Walker {
     double mine = 0., incl = 0.;
     if (warp == 0) {
       const int per = (n + 31) / 32;
-#pragma unroll 4
+#pragma unroll 8
       for (int i = 0; i < per; ++i) mine += lane * per + i < n ? __ldcg(to + lane * per + i) : 0.;
       incl = mine;
 #pragma unroll 1
@@ -357,36 +386,47 @@ struct Walker {
       }
     }
     __syncthreads();
-    return incl - mine;
+    return make_double2(incl - mine, mine);
   }
 
   // The first token whose running sum of what is left at node j exceeds `share` of it all, else the last that has
-  // anything: the threads of one CTA, behind sums(), whose result is `before`.
-  __device__ int draw(int j, float share, double before, int refused) {
+  // anything: the threads of one CTA, behind sums(), whose result is `run`.
+  __device__ int draw(int j, float share, double2 run, int refused) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = entries(j, refused);
     if (warp == 0) {
       const double* of = entry_sums();
       const double want = (double)share * sh.sum;
       const int per = (n + 31) / 32;
-      int first = -1, last = -1;
-      double at_first = 0., at_last = 0.;
+      // the lane whose run crosses the border, else the last that has anything; and there, 32 entries at a time
+      const unsigned some = __ballot_sync(kFull, run.y > 0.), past = __ballot_sync(kFull, run.y > 0. && run.x + run.y > want);
+      if (some != 0) {
+        const int of_lane = past != 0 ? __ffs(past) - 1 : 31 - __clz(some);
+        double before = __shfl_sync(kFull, run.x, of_lane);
+        int entry = -1;
+        double at_entry = 0.;
 #pragma unroll 1
-      for (int i = lane * per; i < min(n, (lane + 1) * per); ++i) {
-        const double s = __ldcg(of + i);
-        if (s > 0.) {
-          last = i;
-          at_last = before;
-          if (first < 0 && before + s > want) {
-            first = i;
-            at_first = before;
+        for (int i0 = 0; i0 < per; i0 += 32) {
+          const int i = of_lane * per + i0 + lane;
+          const double x = i0 + lane < per && i < n ? __ldcg(of + i) : 0.;
+          double incl = x;
+#pragma unroll 1
+          for (int d = 1; d < 32; d <<= 1) {
+            const double o = __shfl_up_sync(kFull, incl, d);
+            if (lane >= d) incl += o;
           }
+          const unsigned has = __ballot_sync(kFull, x > 0.), over = __ballot_sync(kFull, x > 0. && before + incl > want);
+          const int pick = over != 0 ? __ffs(over) - 1 : 31 - __clz(has);
+          if (has != 0) {
+            entry = __shfl_sync(kFull, i, pick);
+            at_entry = __shfl_sync(kFull, before + (incl - x), pick);
+          }
+          if (over != 0) break;
+          before += __shfl_sync(kFull, incl, 31);
         }
-        before += s;
-      }
-      const unsigned past = __ballot_sync(kFull, first >= 0), some = __ballot_sync(kFull, last >= 0);
-      if (past != 0 ? lane == __ffs(past) - 1 : (some != 0 && lane == 31 - __clz(some))) {
-        sh.entry = past != 0 ? first : last;
-        sh.need = (float)(want - (past != 0 ? at_first : at_last));
+        if (lane == 0 && entry >= 0) {
+          sh.entry = entry;
+          sh.need = (float)(want - at_entry);
+        }
       }
     }
     __syncthreads();
@@ -578,12 +618,12 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
   const int at = sh.at, count = sh.count;
   int refused = sh.refused, next = greedy ? sh.best[at] : -1;
   if (!greedy && sh.top[at] != neg_inf()) {
-    double before = w.sums(at, refused, again);
+    double2 run = w.sums(at, refused, again);
     if (!(sh.sum > 0.) && refused > 0) {   // nothing is left: from the target's own
       refused = 0;
-      before = w.sums(at, 0, true);
+      run = w.sums(at, 0, true);
     }
-    if (rank == 0) next = w.draw(at, sh.u[0], before, refused);
+    if (rank == 0) next = w.draw(at, sh.u[0], run, refused);
   }
   if (rank == 0) {
     if (tid == 0) {
