@@ -728,11 +728,12 @@ def spec_verify(logits, drafts, parents, uniforms, temperatures=None, draft_prob
     accepted [B]. A step of no requests (B = 0) enqueues nothing."""
     import torch
     i32, f32 = torch.int32, torch.float32
-    types = {torch.bfloat16: 0, torch.float16: 1, f32: 2}     # NVFP4MLA_BF16, _FP16, _FP32
-    if logits.dtype not in types:
-        raise TypeError(f"logits: expected torch.bfloat16, torch.float16 or torch.float32, got {logits.dtype}")
+    dtype = logits.dtype
+    dt = 0 if dtype is torch.bfloat16 else 1 if dtype is torch.float16 else 2 if dtype is f32 else -1     # NVFP4MLA_BF16, _FP16, _FP32
+    if dt < 0:
+        raise TypeError(f"logits: expected torch.bfloat16, torch.float16 or torch.float32, got {dtype}")
     index = logits.get_device()
-    lp = _ptr_of(logits, "logits", logits.dtype, index, 3, False)
+    lp = _ptr_of(logits, "logits", dtype, index, 3, False)
     pp = None if draft_probs is None else _ptr_of(draft_probs, "draft_probs", f32, index, 3, False)
     B, Q, V = logits.shape
     if draft_probs is not None and draft_probs.shape != logits.shape:
@@ -749,28 +750,30 @@ def spec_verify(logits, drafts, parents, uniforms, temperatures=None, draft_prob
     if not drafts.shape == parents.shape == uniforms.shape == (B, Q) or (temperatures is not None and temperatures.shape[0] != B):
         raise ValueError("drafts, parents and uniforms must be [B, Q], temperatures [B]")
     fresh = [None] * 3
-    with _taken_on(stream if tokens is None or path is None or accepted is None or workspace is None else None):
-        if tokens is None:
-            tokens = fresh[0] = torch.empty((B, Q), dtype=i32, device=logits.device)
-        if path is None:
-            path = fresh[1] = torch.empty((B, Q), dtype=i32, device=logits.device)
-        if accepted is None:
-            accepted = fresh[2] = torch.empty(B, dtype=i32, device=logits.device)
-        if workspace is None:
-            workspace = torch.empty(max(spec_verify_workspace_size(B, Q, V), 1), dtype=torch.uint8, device=logits.device)
-        elif not workspace.is_contiguous():
-            raise ValueError("workspace: must be contiguous")
+    if tokens is None or path is None or accepted is None or workspace is None:
+        with _taken_on(stream):
+            if tokens is None:
+                tokens = fresh[0] = torch.empty((B, Q), dtype=i32, device=logits.device)
+            if path is None:
+                path = fresh[1] = torch.empty((B, Q), dtype=i32, device=logits.device)
+            if accepted is None:
+                accepted = fresh[2] = torch.empty(B, dtype=i32, device=logits.device)
+            if workspace is None:
+                workspace = torch.empty(max(spec_verify_workspace_size(B, Q, V), 1), dtype=torch.uint8, device=logits.device)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
     outs = [_ptr_of(tokens, "tokens", i32, index, 2), _ptr_of(path, "path", i32, index, 2), _ptr_of(accepted, "accepted", i32, index, 1)]
     if tokens.shape != (B, Q) or path.shape != (B, Q) or accepted.shape[0] != B:
         raise ValueError("tokens and path must be [B, Q], accepted [B]")
     if B == 0:
         return tokens, path, accepted
-    rc = load_library().spec_verify(lp, steps[0], types[logits.dtype], pp, steps[1], dp, np_, up, tp, B, Q, V, *outs,
+    rc = load_library().spec_verify(lp, steps[0], dt, pp, steps[1], dp, np_, up, tp, B, Q, V, *outs,
                                     workspace.data_ptr(), workspace.nbytes, _status_ptr(dev_status, index),
                                     _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "spec_verify")
-    _keep(stream, *fresh)
+    if stream is not None:
+        _keep(stream, *fresh)
     return tokens, path, accepted
 
 

@@ -6,6 +6,10 @@
 // with the scale bytes of their blocks, takes the largest byte for the block, and writes the rows again
 // under that. A draft never moves to a higher place, and the i-th accepted one lies at i or above: what a
 // block reads, the blocks before it have not written.
+//
+// What bounds it: latency. A block is four dependent reads (the path, the table, the scale bytes beside the rows) and a
+// write; a step's bytes are few. Measured, back to back: 16 trees of 32 nodes, eight heads of 128 in eight layers (2 MB), with
+// kv_pages_trim behind it: 6.9 us, 128 trees of 12 in four layers of four heads of 64 the same.
 #include "../../include/nvfp4mla.h"
 #include "kv8.h"
 #include "kv8_codes.cuh"

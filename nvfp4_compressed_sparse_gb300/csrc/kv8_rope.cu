@@ -10,10 +10,15 @@
 // dims side by side where pairs are neighbours, so that nothing but the sum of squares crosses lanes; behind the turned
 // dims it has eight dims of its own.
 //
-// A CTA takes a block of 16 tokens of one request and a share of its rows' heads: it stages the cosines and
-// sines of its tokens once, then each warp takes a head at a time.
-#include <cmath>
-
+// A CTA takes a block of 16 tokens of one request and a share of the heads of one kind (queries, keys, values: one code a
+// CTA): it stages the cosines and sines of its tokens once, then a warp takes a query's or value's head at a time, two warps
+// a key's, whose rows stay in registers until the block's scale is known. Shares are cut finer where blocks are few, down to
+// a head a warp, so that every SM has CTAs.
+//
+// Measured, back to back, against 6.77 TB/s of measured copy bandwidth: 34,700 prompt tokens of 32 query heads over 8 of
+// 128: 146 us (81 %); 512 tokens of 16 trees 5.1 us, one token of 64 requests 7.3 us (both a chain of dependent reads: the
+// request of a block, its lengths, positions, angles, rows). A warp a key head, whose rows are turned twice, took 159 us;
+// kinds mixed in a CTA 235.
 #include "../../include/nvfp4mla.h"
 #include "kv8.h"
 #include "kv8_codes.cuh"

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256) free_kernel(const PageState s, const int3
 }
 
 // ------------------------------------------------------------------ trim
-// A block a sequence, whose thread reads the one entry that most trims give back, if any.
+// A warp a sequence, an entry a lane: a chain of two reads and an atomic, some 3 us of a step's end.
 __global__ void __launch_bounds__(32) trim_kernel(const PageState s, const int32_t* new_lens) {
   const int seq = blockIdx.x;
   const int len = s.lens[seq], now = new_lens[seq];
