@@ -30,9 +30,9 @@
 // A unit that several CTAs share leaves means and sums in the workspace, which join_kernel adds up.
 //
 // Measured, back to back, against 6.77 TB/s of measured copy bandwidth: 16 requests of 2,000 to 16,000 tokens, 32 nodes of
-// 32 heads over 8 of 128: 94 us (45 % of it); one of 131,001 tokens, 16 nodes of 64 heads: 91 us (44 %); 24 requests of
-// 900 to 9,000 tokens, 64 nodes of 32 heads over 4 of 64, a window of 4,096, fp16: 87 us; one request of 1,000 tokens:
-// 19 us. A tile of 128 columns takes some 2,000 cycles, in which the tensor cores work for 1,100, and the softmax's chain
+// 32 heads over 8 of 128: 94 us (45 % of it); one of 131,001 tokens, 16 nodes of 64 heads: 88 us (45 %); 24 requests of
+// 900 to 9,000 tokens, 64 nodes of 32 heads over 4 of 64, a window of 4,096, fp16: 88 us; one request of 1,000 tokens:
+// 17 us. A tile of 128 columns takes some 2,000 cycles, in which the tensor cores work for 1,100, and the softmax's chain
 // (its scores' arrival, 64 exponentials a thread, the two threads' vote, the weights' store) is as long as the tile is;
 // so is the feeders'. A unit costs some 11,000 more: its queries, its first and masked tiles, its results. What was tried
 // and not kept, in the order of the first three: a stream of tiles, and an O, for each warpgroup (112, 99, 100 us); keys
@@ -393,11 +393,11 @@ struct Cta {
 
   // ---------------------------------------------------------------- feeders (warps 4-7)
   static constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = 32 / kAtOnce;    // of a row; rows of a load; loads of a lane
-  // The unit's queries, on their way: a warp has 32 rows.
+  // The unit's queries, on their way: a warp has 32 rows, a load's of every fourth, so that few rows are shared by all warps.
   __device__ __forceinline__ void fetch(const Walk& w, uint4 (&v)[kRounds]) {
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
     // a lane a column: where its row is
-    const int col = w.ct * kCols + warp * 32 + lane, j = node_of(col);
+    const int col = w.ct * kCols + (lane / kAtOnce * 4 + warp) * kAtOnce + lane % kAtOnce, j = node_of(col);
     const int64_t mine = col < p.Q * p.group ? ((int64_t)w.b * p.Q + j) * p.q_token_stride + (w.kvh * p.group + col - j * p.group) * p.q_head_stride : -1;
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
@@ -408,11 +408,21 @@ struct Cta {
   }
   // And as parts.
   template <bool kHalf>
-  __device__ __forceinline__ void queries(uint4 (&v)[kRounds], uint32_t buf) {
+  __device__ __forceinline__ void queries(uint4 (&v)[kRounds], uint32_t buf, int rows) {
     constexpr int kTogether = 4;         // loads whose chains are under way together
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, sub = lane / kLanes, ch = lane % kLanes;
 #pragma unroll 1
     for (int r0 = 0; r0 < kRounds; r0 += kTogether) {
+      if (r0 * 4 * kAtOnce >= rows) {
+        // no column: zeros, so that nothing rare comes of them
+#pragma unroll 1
+        for (int n = (r0 * 4 + warp) * kAtOnce + sub; n < kCols; n += 4 * kAtOnce) {
+#pragma unroll
+          for (int q = 0; q < kQ; ++q) *reinterpret_cast<uint2*>(qimg + q * S::kQImage + n * D + ch * 8) = make_uint2(0u, 0u);
+          if (ch == 0) ctl->f[buf][n] = 0.f;
+        }
+        break;
+      }
       uint4 x[kTogether];
       uint32_t top[kTogether / 2];       // of two rows
 #pragma unroll
@@ -431,7 +441,7 @@ struct Cta {
         for (int i = 0; i < kTogether / 2; ++i) top[i] = __vmaxu2(top[i], __shfl_xor_sync(kFull, top[i], d));
 #pragma unroll
       for (int i = 0; i < kTogether; ++i) {
-        const int n = warp * 32 + (r0 + i) * kAtOnce + sub;
+        const int n = ((r0 + i) * 4 + warp) * kAtOnce + sub;
         const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, most = (top[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
         const bool finite = most < (kHalf ? 0x7C00u : 0x7F80u);
         // the largest magnitude goes to [128, 256): a power of two, exact
@@ -504,7 +514,7 @@ struct Cta {
       ok = ok && wait_warp(&ctl->q_empty, (seg & 1) ^ 1);              // the products with the last unit's queries are complete
       ok = ok && wait_warp(&ctl->done[buf], ((seg >> 1) & 1) ^ 1);     // and the unit's before that is written
       if (ok) {
-        queries<kHalf>(q, buf);
+        queries<kHalf>(q, buf, p.Q * p.group - w.ct * kCols);
         fence_proxy_async_smem();
       }
       if (bar_any(kBarFeeders, kFeeders, !ok)) return;
@@ -1004,12 +1014,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   }
 }
 
-// Means of a shared unit's parts, added by the sums that they are of: a lane a column, D / 8 dims a warp.
+// Means of a shared unit's parts, added by the sums that they are of: a lane a column, eight dims a warp. (Four and 16 take
+// as long where units are many, and 16 some 2 us more where one is long.)
 template <int D, bool kHalf>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Kv8TreeParams p) {
-  constexpr int kN = D / 32;                             // four dims each
+  constexpr int kN = 2;                             // four dims each
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = blockIdx.x, r = blockIdx.y * 32 + lane;
+  const int lane = threadIdx.x & 31, warp = 8 * blockIdx.z + (threadIdx.x >> 5), first = blockIdx.x, r = blockIdx.y * 32 + lane;
   const Shared s = reinterpret_cast<const Shared*>(p.arrived)[first];
   const int col = s.ct * kCols + r, j = (int)(((uint64_t)(uint32_t)col * p.group_inverse) >> 24);
   if (s.last < 0 || col >= p.Q * p.group) return;
@@ -1077,7 +1088,7 @@ cudaError_t launch(const Kv8TreeParams& p, cudaStream_t stream) {
   cfg.numAttrs = 1;
   err = cudaLaunchKernelEx(&cfg, tree_kernel<D, kHalf>, p);
   if (err != cudaSuccess) return err;
-  cfg.gridDim = dim3((unsigned)p.ctas, kCols / 32, 1);
+  cfg.gridDim = dim3((unsigned)p.ctas, kCols / 32, D / 64);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join_kernel<D, kHalf>, p);
