@@ -848,6 +848,7 @@ struct Cta {
 #pragma unroll 1
         for (int k0 = 0; k0 < D / 2; k0 += 16) {
           const int d0 = half * (D / 2) + k0;
+          __syncwarp();
           uint32_t a[16];
           tmem_ld16(o_at + d0, a);
           tmem_wait_ld();

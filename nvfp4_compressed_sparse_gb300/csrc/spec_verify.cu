@@ -15,8 +15,8 @@
 // border between tokens.
 //
 // Measured, back to back, against 6.77 TB/s of measured copy bandwidth: 64 chains of 5 nodes over 128,000 bf16 logits with
-// draft distributions 32 us (53 % of it, over logits and the distributions of refusing nodes: some 17 us are stats_kernel's,
-// 15 the walk's), 16 trees of 32 over 100,003 without 31 us (49 %: 21 and 10), one chain of 5 over 32,000 fp32 10 us (all
+// draft distributions 31 us (55 % of it, over logits and the distributions of refusing nodes: some 17 us are stats_kernel's,
+// 14 the walk's), 16 trees of 32 over 100,003 without 31 us (49 %: 21 and 10), one chain of 5 over 32,000 fp32 10 us (all
 // latency). What was tried and not kept: chunks that come to shared memory ahead of a warp's work, by a ring of three a
 // warp (37 to 40, 37 and 12 us); a walk in 64 bits, or unrolled (its code is fetched once a call, some 16 cycles an
 // instruction); the next distribution brought to L2 (no difference).
@@ -261,11 +261,14 @@ struct Walker {
   };
   // What is left, after `refused` refusals at node j, of the tokens of the load from `at` on: of their probabilities (with
   // draft distributions), or of their exponentials.
-  __device__ __forceinline__ Load rest(int j, int64_t at, int refused) const {
-    const T* row = row_of(j);
-    const float m = sh.top[j], inv = kProbs ? sh.inverse[j] : 1.f;
-    const uint4 w = load_vec(row, at, p.V);
-    Load q;
+  struct Raw {
+    uint4 w;
+    Load q;                              // of the distribution that refusals take off
+  };
+  __device__ __forceinline__ Raw ask(int j, int64_t at, int refused) const {
+    Raw r;
+    r.w = load_vec(row_of(j), at, p.V);
+    Load& q = r.q;
     if (kProbs && refused > 0) {
       const float* from = probs_of(j) + at;
       if (at >= 0 && at + V::kN <= p.V && (reinterpret_cast<uintptr_t>(from) & 15) == 0) {
@@ -276,8 +279,13 @@ struct Walker {
         for (int k = 0; k < V::kN; ++k) q.x[k] = at + k >= 0 && at + k < p.V ? __ldg(from + k) : 0.f;
       }
     }
+    return r;
+  }
+  __device__ __forceinline__ Load rest(const Raw& raw, int j, int64_t at, int refused) const {
+    const float m = sh.top[j], inv = kProbs ? sh.inverse[j] : 1.f;
+    const Load& q = raw.q;
     Load r;
-    widen(w, r.x, row);
+    widen(raw.w, r.x, (const T*)nullptr);
     if (fabsf(m) < __int_as_float(0x7f800000)) {
 #pragma unroll
       for (int k = 0; k < V::kN; ++k) {
@@ -297,6 +305,7 @@ struct Walker {
     }
     return r;
   }
+  __device__ __forceinline__ Load rest(int j, int64_t at, int refused) const { return rest(ask(j, at, refused), j, at, refused); }
   static __device__ __forceinline__ float add_up(const Load& r) {
     float s = 0.f;
 #pragma unroll
@@ -330,9 +339,16 @@ struct Walker {
     }
     const int64_t start = -(int64_t)lead_of(row_of(j));
     if (fine(refused)) {
+      // (the next entry's loads are on their way while this one's are added up)
+      auto at_of = [&](int c) { return start + ((int64_t)c * 32 + lane) * V::kN; };
+      int c = rank * kWarps + warp;
+      Raw next{};
+      if (c < n) next = ask(j, at_of(c), refused);
 #pragma unroll 1
-      for (int c = rank * kWarps + warp; c < n; c += ctas * kWarps) {
-        const float s = rest_of_warp(j, start + ((int64_t)c * 32 + lane) * V::kN, refused);
+      for (; c < n; c += ctas * kWarps) {
+        const Raw now = next;
+        if (c + ctas * kWarps < n) next = ask(j, at_of(c + ctas * kWarps), refused);
+        const float s = warp_sum(add_up(rest(now, j, at_of(c), refused)));
         if (lane == 0) to[c] = (double)s;
       }
     } else if (rank == 0) {
