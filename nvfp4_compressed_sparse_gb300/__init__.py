@@ -587,11 +587,11 @@ def kv8_append_rope(q, k, v, cos_sin, cu_tokens, seq_lens, page_table, cache, q_
     import torch
     lib, i32 = load_library(), torch.int32
     dt = _kv8_dtype(q, "q")
-    index = q.get_device()
-    qp, kp, vp = (_ptr_of(t, name, q.dtype, index, 3, False) for t, name in ((q, "q"), (k, "k"), (v, "v")))
+    index, dtype = q.get_device(), q.dtype
+    qp, kp, vp = _ptr_of(q, "q", dtype, index, 3, False), _ptr_of(k, "k", dtype, index, 3, False), _ptr_of(v, "v", dtype, index, 3, False)
     n, heads, d = q.shape
-    hk = k.shape[1]
-    if v.shape != k.shape or k.shape[0] != n or k.shape[2] != d:
+    kn, hk, kd = k.shape
+    if v.shape != k.shape or kn != n or kd != d:
         raise ValueError("k and v must have the same shape, and q's tokens and dims")
     cp = _ptr_of(cache, "cache", torch.uint8, index, 2)
     pages, page_bytes = cache.shape
@@ -603,11 +603,10 @@ def kv8_append_rope(q, k, v, cos_sin, cu_tokens, seq_lens, page_table, cache, q_
     if cu_tokens.shape[0] != B + 1 or page_table.shape[0] != B:
         raise ValueError("shape mismatch")
     sheet = _ptr_of(cos_sin, "cos_sin", torch.float32, index, 2)
-    weights = []
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        weights.append(None if t is None else _ptr_of(t, name, q.dtype, index, 1))
-        if t is not None and t.shape[0] != d:
-            raise ValueError(f"{name} must have head_dim entries")
+    qw = None if q_weight is None else _ptr_of(q_weight, "q_weight", dtype, index, 1)
+    kw = None if k_weight is None else _ptr_of(k_weight, "k_weight", dtype, index, 1)
+    if (qw is not None and q_weight.shape[0] != d) or (kw is not None and k_weight.shape[0] != d):
+        raise ValueError("q_weight and k_weight must have head_dim entries")
     axes, at, step, parts = 1, None, 0, None
     if positions is not None:
         at = _ptr_of(positions, "positions", i32, index, positions.dim(), False)
@@ -622,17 +621,18 @@ def kv8_append_rope(q, k, v, cos_sin, cu_tokens, seq_lens, page_table, cache, q_
     fresh = None
     if q_out is None:
         with _taken_on(stream):
-            q_out = fresh = torch.empty((n, heads, d), dtype=q.dtype, device=q.device)
-    op = _ptr_of(q_out, "q_out", q.dtype, index, 3, False)
+            q_out = fresh = torch.empty((n, heads, d), dtype=dtype, device=q.device)
+    op = qp if q_out is q else _ptr_of(q_out, "q_out", dtype, index, 3, False)
     if q_out.shape != q.shape:
         raise ValueError("q_out must have q's shape")
-    (q0, q1), (k0, k1), (v0, v1), (o0, o1) = (_rows(t, n) for t in (q, k, v, q_out))
-    rc = lib.kv8_append_rope(qp, q0, q1, kp, k0, k1, vp, v0, v1, dt, n, cup, sp, pp, page_table.shape[1], B, heads, hk, d, *weights,
+    (q0, q1), (k0, k1), (v0, v1), (o0, o1) = _rows(q, n), _rows(k, n), _rows(v, n), _rows(q_out, n)
+    rc = lib.kv8_append_rope(qp, q0, q1, kp, k0, k1, vp, v0, v1, dt, n, cup, sp, pp, page_table.shape[1], B, heads, hk, d, qw, kw,
                              float(eps), sheet, *cos_sin.shape, 1 if interleaved else 0, at, step, parts, axes, op, o0, o1, cp,
                              pages, _status_ptr(dev_status, index), _raw_stream(stream, index))
     if rc != 0:
         raise NvFp4MlaError(rc, "kv8_append_rope")
-    _keep(stream, fresh)
+    if stream is not None:
+        _keep(stream, fresh)
     return q_out
 
 
