@@ -30,8 +30,8 @@
 // A unit that several CTAs share leaves means and sums in the workspace, which join_kernel adds up.
 //
 // Measured, back to back, against 6.77 TB/s of measured copy bandwidth: 16 requests of 2,000 to 16,000 tokens, 32 nodes of
-// 32 heads over 8 of 128: 94 us (45 % of it); one of 131,001 tokens, 16 nodes of 64 heads: 88 us (45 %); 24 requests of
-// 900 to 9,000 tokens, 64 nodes of 32 heads over 4 of 64, a window of 4,096, fp16: 88 us; one request of 1,000 tokens:
+// 32 heads over 8 of 128: 94 us (45 % of it); one of 131,001 tokens, 16 nodes of 64 heads: 89 us (45 %); 24 requests of
+// 900 to 9,000 tokens, 64 nodes of 32 heads over 4 of 64, a window of 4,096, fp16: 89 us; one request of 1,000 tokens:
 // 17 us. A tile of 128 columns takes some 2,000 cycles, in which the tensor cores work for 1,100, and the softmax's chain
 // (its scores' arrival, 64 exponentials a thread, the two threads' vote, the weights' store) is as long as the tile is;
 // so is the feeders'. A unit costs some 11,000 more: its queries, its first and masked tiles, its results. What was tried
