@@ -614,8 +614,9 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
   if (tid < Q && sh.parent[tid] >= 0 && !greedy) {
     const int up = sh.parent[tid];
     const float m = sh.top[up], d = logit - m, a = d * rate.hi;
-    // exp2 of a, and of what rounding took from it
-    const float e = exp2f(a), have = logit == neg_inf() ? 0.f : (logit == m ? 1.f : fmaf(e, 0.69314718f * (fmaf(d, rate.hi, -a) + d * rate.lo), e));
+    // exp2 of a, and of what rounding took from it; 0 where that is 0, as of a distance so wide (from +inf, of the type's lowest
+    // number) that d or a is infinite, when the rest is none
+    const float e = exp2f(a), have = logit == m ? (m == neg_inf() ? 0.f : 1.f) : (e > 0.f ? fmaf(e, 0.69314718f * (fmaf(d, rate.hi, -a) + d * rate.lo), e) : 0.f);
     sh.have[tid] = have * sh.inverse[up];
   }
   __syncthreads();

@@ -634,6 +634,48 @@ def test_verify_uniforms_of_one_and_more_refuse():
         assert np.all(got[2] == 0) and np.all(got[0][:, 0] < 200)
 
 
+@pytest.mark.parametrize("probs", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_verify_siblings_of_tokens_far_below(dtype, probs):
+    """Drafts whose logit is the type's lowest number have no probability, and their refusal takes nothing from what is left for
+    the siblings behind them."""
+    rng = np.random.default_rng(70)
+    dt = {**DTYPES, "fp32": torch.float32}[dtype]
+    c = verify_case(rng, 12, 6, 600, dt, probs)
+    c["parents"][:] = [-1, 0, 0, 0, 0, 0]
+    c["logits"][:, 0, 400:] = torch.finfo(dt).min
+    likely = np.argsort(-f64(c["logits"])[:, 0], axis=1)
+    c["drafts"][:, [1, 4]] = rng.integers(400, 600, (12, 2))
+    c["drafts"][:, [2, 3, 5]] = likely[:, [2, 3, 1]]
+    c["temperatures"][:] = np.repeat([0.6, 1, 1.4], 4)
+    c["uniforms"][:, 1:] = rng.uniform(0.6, 0.99, (12, 5))
+    if probs:
+        np.put_along_axis(c["draft_probs"][:, 0], c["drafts"][:, 1:], np.float32(0.05), 1)
+    got = check_verify(c)
+    assert np.all(got[2] <= 1) and not np.isin(got[1][:, 0], [1, 4]).any() and (got[2] == 0).any()
+
+
+def test_verify_siblings_beside_infinite_distances():
+    """A finite draft beside logits of +inf, and one beside two equal largest at a temperature next to 0: refused, with all left for
+    the next."""
+    rng = np.random.default_rng(71)
+    for probs in (False, True):
+        c = verify_case(rng, 12, 5, 700, torch.float32, probs)
+        c["parents"][:] = [-1, 0, 0, 0, 0]
+        c["temperatures"][:] = [1, 0.7, 1e-30, 1, 1e-40, 1e-38] * 2
+        c["logits"][[0, 1, 3, 6, 7, 9], 0, 5] = c["logits"][[0, 1, 3, 6, 7, 9], 0, 9] = c["logits"][[0, 1, 3, 6, 7, 9], 0, 300] = float("inf")
+        c["logits"][:, 0, 5] = c["logits"][:, 0, 9] = c["logits"][:, 0].max(-1).values.clamp(min=40.0)
+        c["drafts"][:, 1:] = [3, 9, 40, 5]
+        c["uniforms"][:, 1:] = np.column_stack([rng.uniform(0.1, 0.9, 12), rng.uniform(0.7, 0.99, 12), rng.uniform(0.1, 0.9, 12), rng.uniform(0.1, 0.4, 12)])
+        if probs:
+            c["draft_probs"][:, 0] = 0
+            c["draft_probs"][:, 0, [3, 9, 40, 5]] = 0.25
+        got = check_verify(c)
+        assert not np.isin(got[1][:, 0], [1, 3]).any()
+        if not probs:
+            assert not (got[1][:, 0] == 2).any()             # u of 0.7 and more, where half or a third is its own
+
+
 def test_verify_temperatures_at_the_ends():
     """An infinite one: all that are not -inf are equally likely; a tiny one: the largest is all there is."""
     rng = np.random.default_rng(28)
