@@ -652,10 +652,11 @@ size_t spec_verify_workspace_size(int B, int Q, int64_t V);
  * the target's own. Greedy, temperature 0: a child is accepted when its token is the smallest of those with
  * the largest logit, which is the next token too.
  *
- * Logits may be -inf (never drawn, and so is a NaN). Of a row with +inf those are equally likely, and the
- * only ones. Where a row has nothing else but -inf, none of its children is accepted and the next token is -1
- * (counted). A decision or a draw that is nearer to a border than the rounding of exponentials and sums in
- * fp32 (some 1e-7 of the probability) may fall to either side, the same on every run.
+ * Logits may be -inf (never drawn, and so is a NaN), and one that lies 2^128 or more below the row's largest
+ * counts as -inf. Of a row with +inf those are equally likely, and the only ones. Where a row has nothing
+ * else but -inf, none of its children is accepted and the next token is -1 (counted). A decision or a draw
+ * that is nearer to a border than the rounding of exponentials and sums in fp32 (some 1e-7 of the
+ * probability) may fall to either side, the same on every run.
  *
  *   logits            dtype [B, Q, V]; row (b, j) begins (b*Q + j) * logits_row_stride elements in; aligned to
  *                     its elements
@@ -667,7 +668,8 @@ size_t spec_verify_workspace_size(int B, int Q, int64_t V);
  *                     (NVFP4MLA_STAT_BAD_INDEX)
  *   uniforms          fp32 [B, Q], of [0, 1); below is 0, a NaN or 1 and more refuse, or draw the last token
  *                     that has a probability
- *   temperatures      fp32 [B], or NULL: 1. What is not above 0 is greedy
+ *   temperatures      fp32 [B], or NULL: 1. What is not above 0 is greedy; an infinite one: all but -inf equally
+ *                     likely; one below 4.9e-39 counts as that
  *   B, Q, V           B >= 1, 1 <= Q <= NVFP4MLA_MAX_NODES, 1 <= V <= NVFP4MLA_MAX_VOCABULARY
  *   tokens            int32 [B, Q]: the accepted drafts' tokens, the next token, -1
  *   path              int32 [B, Q]: the accepted nodes, -1 behind them

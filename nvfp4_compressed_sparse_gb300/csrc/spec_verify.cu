@@ -75,8 +75,9 @@ __device__ __forceinline__ void widen(const uint4& w, float (&x)[8], const T*) {
 __device__ __forceinline__ float clean(float v) { return v != v ? neg_inf() : v; }
 
 // log2(e) / temperature as hi + lo: rounded to one fp32, its error would grow with a logit's distance from the
-// largest. lo > 0, so that an infinite distance stays one. hi < 0: greedy, which is asked for by 0 (and by what is no
-// temperature).
+// largest. Both above 0, so that an infinite distance stays one, but by no more than fp32's smallest step: at an infinite
+// temperature the largest finite distance, 2^128, then costs a weight 2 x 2^-149 x 2^128 = 2^-20 of an exponent.
+// hi < 0: greedy, which is asked for by 0 (and by what is no temperature).
 struct Rate {
   float hi, lo;
 };
@@ -84,10 +85,11 @@ __device__ __forceinline__ Rate rate_of(const VerifyParams& p, int b) {
   const float t = p.temperatures != nullptr ? p.temperatures[b] : 1.f;
   if (!(t > 0.f)) return Rate{-1.f, 0.f};
   constexpr float kHi = 1.4426950408889634f, kLo = (float)(1.4426950408889634 - (double)kHi);
-  float hi = fmaxf(kHi / t, 4e-39f);                  // (not 0, of an infinite t: -inf times it stays what it is)
-  if (!(hi < 3e38f)) return Rate{3e38f, 1e-38f};
+  const float step = __int_as_float(1);
+  float hi = fmaxf(kHi / t, step);
+  if (!(hi < 3e38f)) return Rate{3e38f, step};
   if (hi > 1e-30f) hi = __uint_as_float(__float_as_uint(hi) - 1);        // at or below the quotient
-  return Rate{hi, fmaxf((fmaf(-hi, t, kHi) + kLo) / t, 1e-38f)};
+  return Rate{hi, fmaxf((fmaf(-hi, t, kHi) + kLo) / t, step)};
 }
 // exp((x - m) / T) for x <= m; 0 for x = -inf, 1 for x = m whatever they are.
 __device__ __forceinline__ float weight(float x, float m, Rate rate) {

@@ -688,6 +688,29 @@ def test_verify_temperatures_at_the_ends():
         assert np.all(got[2][3:5] == 4)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_verify_large_temperatures_over_the_whole_range(dtype):
+    """Logits at the type's lowest number at temperatures of its size: as likely as softmax(logits / T) says, at an infinite one as
+    all others. (A rate is off by two of fp32's smallest steps, an exponent by 2 x 2^-149 x 2^128, a weight by 2^-20.5 of itself and
+    so a share, p (1 - p) of that, by less than 2^-22: within check_verify's bound.)"""
+    rng = np.random.default_rng(72)
+    dt = {**DTYPES, "fp32": torch.float32}[dtype]
+    for probs in (False, True):
+        for V in (40, 1300):
+            c = verify_case(rng, 10, 4, V, dt, probs)
+            c["parents"][:] = [-1, 0, 0, 1]
+            c["logits"][:, :, 1::2] = torch.finfo(dt).min
+            c["logits"][:, :, 2::5] = -float("inf")
+            c["temperatures"][:] = [float("inf"), 3.4e38, 3e38, 2e38, 1e38, 5e37, 2e37, 1e37, 1e36, 1e31]
+            check_verify(c)
+            c["uniforms"][:, 1:] = 1                         # every child refused: draws
+            got = check_verify(c)
+            assert np.all(got[2] == 0)
+            c["uniforms"][:, 0] = 0.999                      # (a draw from the far end of what is left)
+            got = check_verify(c)
+            assert np.all(got[0][:3, 0] > V // 2)
+
+
 def test_verify_refuses_results_over_inputs():
     c = verify_case(np.random.default_rng(29), 2, 3, 50, torch.float32, False)
     logits, drafts, parents, u = (torch.as_tensor(c[k]).to("cuda") for k in ("logits", "drafts", "parents", "uniforms"))
