@@ -875,6 +875,36 @@ def test_trim():
     assert np.array_equal(dt.cpu().numpy(), table) and status.tolist() == [0, 0, 0, 2]
 
 
+def test_rope_keep_and_trim_on_another_stream():
+    """What they take for their results, they take on that stream; what they give is what the current stream's call gives."""
+    c = Rope([0, 15, 40], [3, 20, 33], 4, 2, 64, "bf16", 32, positions=True, seed=73)
+    rng = np.random.default_rng(73)
+    caches, table, lens, path, count = keep_case(rng, [70, 150, 90, 33], 12, 2, 64, layers=2)
+    refs = np.bincount(table[table >= 0], minlength=caches.shape[1]).astype(np.int32)
+    put = lambda x: x.to("cuda")  # noqa: E731
+
+    def step(stream):
+        rope, keep = dev(c.cache, torch.uint8), dev(caches, torch.uint8)
+        args = (put(c.q), put(c.k), put(c.v), put(torch.from_numpy(c.sheet)), dev(c.cu), dev(c.lens), dev(c.table))
+        weights = dict(q_weight=put(c.weights[0]), k_weight=put(c.weights[1]), eps=c.eps, positions=dev(c.positions[0]))
+        dt, dl, dr, dp, da = dev(table), dev(lens), dev(refs), dev(path), dev(count)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        q = m.kv8_append_rope(*args, rope, **weights, stream=stream)
+        new = m.kv8_keep(keep, dt, dl, dp, da, 2, 64, stream=stream, layered=True)
+        m.kv_pages_trim(dt, dl, dr, new, stream=stream)
+        if stream is not None:
+            torch.cuda.current_stream().wait_stream(stream)
+        return q.clone(), rope, new.clone(), keep, dt, dl, dr
+
+    want = step(None)
+    c.check(want[0], want[1].cpu().numpy(), False)
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        for a, b in zip(step(side), want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 # ------------------------------------------------------------------ together
 def test_speculative_steps():
     """Several steps as a server makes them: room, rotated drafts, attention, verification, the accepted ones kept. Tables as the
