@@ -747,7 +747,8 @@ int kv_pages_free(int32_t* page_table, int64_t max_pages_per_seq, int32_t* seq_l
 
 /* kv_pages_trim: sequence s is cut to new_lens[s] tokens (int32 [num_seqs]): the entries behind become -1, their
  * pages' counts go down by one. A new length below 0 or above seq_lens[s] is refused and counted. (A page that a fork
- * shares may become a sequence's part-full last one: what is appended to it then shows in the other sequence too.) */
+ * shares may become a sequence's part-full last one: what is appended to it then shows in the other sequence too.)
+ * new_lens may be seq_lens itself, and overlaps none of the state otherwise (refused). */
 int kv_pages_trim(int32_t* page_table, int64_t max_pages_per_seq, int32_t* seq_lens, int num_seqs, int32_t* refcounts,
                   int64_t num_pages, const int32_t* new_lens, int32_t* dev_status, void* stream);
 

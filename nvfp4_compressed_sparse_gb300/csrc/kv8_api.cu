@@ -451,6 +451,11 @@ int kv_pages_trim(int32_t* page_table, int64_t max_pages_per_seq, int32_t* seq_l
   const int rc = check_state(page_table, max_pages_per_seq, seq_lens, true, num_seqs, refcounts, num_pages, dev_status, &s);
   if (rc != NVFP4MLA_OK) return rc;
   if (!all_device({new_lens})) return NVFP4MLA_ERR_INVALID_ARG;
+  // (a warp a sequence: what one reads, no other may write)
+  const size_t n = (size_t)num_seqs * sizeof(int32_t);
+  if ((new_lens != seq_lens && overlap(new_lens, n, seq_lens, n)) || overlap(new_lens, n, page_table, n * max_pages_per_seq) ||
+      overlap(new_lens, n, refcounts, (size_t)num_pages * sizeof(int32_t)))
+    return NVFP4MLA_ERR_INVALID_ARG;
   return status_of(launch_pages_trim(s, new_lens, static_cast<cudaStream_t>(stream)));
 }
 

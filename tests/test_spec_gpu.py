@@ -875,6 +875,21 @@ def test_trim():
     assert np.array_equal(dt.cpu().numpy(), table) and status.tolist() == [0, 0, 0, 2]
 
 
+def test_trim_refuses_new_lengths_over_the_state():
+    """But seq_lens itself, which cuts nothing."""
+    room = torch.full((5,), 70, dtype=torch.int32, device="cuda")
+    table = torch.tensor([[0, 1], [2, 3], [4, 5], [6, 7]], dtype=torch.int32, device="cuda")
+    refs = torch.ones(16, dtype=torch.int32, device="cuda")
+    lens = room[:4]
+    for new in (room[1:], table.view(-1)[2:6], refs[8:12]):
+        with pytest.raises(m.NvFp4MlaError):
+            m.kv_pages_trim(table, lens, refs, new)
+    m.kv_pages_trim(table, lens, refs, lens)
+    assert room.tolist() == [70] * 5 and table.view(-1).tolist() == list(range(8)) and refs.tolist() == [1] * 16
+    m.kv_pages_trim(table, lens, refs, dev([64, 70, 1, 0]))
+    assert lens.tolist() == [64, 70, 1, 0] and table.tolist() == [[0, -1], [2, 3], [4, -1], [-1, -1]]
+
+
 def test_rope_keep_and_trim_on_another_stream():
     """What they take for their results, they take on that stream; what they give is what the current stream's call gives."""
     c = Rope([0, 15, 40], [3, 20, 33], 4, 2, 64, "bf16", 32, positions=True, seed=73)
