@@ -518,8 +518,9 @@ int kv8_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, con
  * as 0x7F.
  *
  *   q                 dtype [num_tokens, heads, head_dim], strides as k's
- *   q_out             the same shape, strides of its own; it may be q itself, and must not otherwise
- *                     overlap q, k or v. Rows of no request, or of one that is left out, are not written
+ *   q_out             the same shape, strides of its own, of at least head_dim where an axis has more than one
+ *                     entry (else refused); it may be q itself, under the same strides (else refused), and must not
+ *                     otherwise overlap q, k or v. Rows of no request, or of one that is left out, are not written
  *   heads             >= 1 (any number beside kv_heads, <= 32,768)
  *   q_weight, k_weight  dtype [head_dim], 16-byte aligned, or NULL: no norm of that kind
  *   eps               >= 0, finite

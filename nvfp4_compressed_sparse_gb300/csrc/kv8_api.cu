@@ -120,6 +120,10 @@ int kv8_append_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride
     if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16)) return NVFP4MLA_ERR_ALIGNMENT;
     if (((q_token_stride | q_head_stride | out_token_stride | out_head_stride) & 7) != 0 || !words_aligned({cos_sin, positions}))
       return NVFP4MLA_ERR_ALIGNMENT;
+    // rows of q_out that overlap one another, or q's under other strides: a row would be read or kept by chance
+    const bool tokens = num_tokens > 1, more = heads > 1;
+    if ((tokens && out_token_stride < head_dim) || (more && out_head_stride < head_dim)) return NVFP4MLA_ERR_INVALID_ARG;
+    if (q == q_out && ((tokens && q_token_stride != out_token_stride) || (more && q_head_stride != out_head_stride))) return NVFP4MLA_ERR_INVALID_ARG;
   }
   const int rc = check_append(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, dtype, num_tokens, cu_tokens,
                               seq_lens, page_table, max_pages_per_seq, B, kv_heads, head_dim, cache, num_pages, dev_status, &p);

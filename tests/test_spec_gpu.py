@@ -203,6 +203,22 @@ def test_rope_leaves_rows_of_no_request_alone():
     assert not np.array_equal(cache, c.cache) and q.shape == out.shape
 
 
+def test_rope_refuses_rows_that_overlap():
+    """Results of all heads, or tokens, in one place; the queries' own memory in another order. Axes of one entry have any stride."""
+    c = Rope([2], [6], 6, 2, 128, "bf16", 128, seed=11)
+    q = c.q.to("cuda")
+    room = torch.zeros((6, 6, 128), dtype=torch.bfloat16, device="cuda")
+    for out in (room[:, :1].expand(6, 6, 128), room[:1].expand(6, 6, 128), room.view(-1).as_strided((6, 6, 128), (64, 768, 1)), q.transpose(0, 1)):
+        with pytest.raises(m.NvFp4MlaError):
+            c.run(q=q, q_out=out)
+    assert torch.equal(q.cpu(), c.q) and not room.any()
+    out, cache = c.run(q=q, q_out=room.transpose(0, 1))
+    c.check(out, cache, False)
+    one = Rope([2], [1], 6, 2, 128, "bf16", 128, seed=12)
+    out, cache = one.run(q_out=room.view(-1).as_strided((1, 6, 128), (8, 128, 1)))
+    one.check(out, cache, False)
+
+
 def test_rope_table_at_any_word():
     """Cosines and sines that do not begin at 16 bytes, and axes that part within four pairs."""
     c = Rope([2, 70], [33, 7], 8, 4, 128, "bf16", 96, axes=3, positions=True, seed=10)
