@@ -621,7 +621,7 @@ size_t kv8_decode_tree_workspace_size(int B, int Q, int H, int kv_heads, int hea
  *
  * NaN, infinities and the sizes of scores as kv8_decode. The two operands that are held in fewer bits:
  *   queries  off by at most 2^-17 of the row's largest magnitude (bf16: exact from 2^-9 of it on, fp16: 2^-6)
- *   weights  off by at most 2^-12 of itself, or 2^-33 of the largest such product of the row's attended positions
+ *   weights  off by at most 2^-11 of itself, or 2^-33 of the largest such product of the row's attended positions
  *            if that is more; the sum that divides is one of unrounded exponentials
  *
  *   masks             uint64 [B, Q], 8-byte aligned

@@ -14,10 +14,10 @@
 //      numbers (two of a bf16, three of an fp16, the row's largest element at 2^7 to 2^8): what is left after them is
 //      half of E4M3's smallest step, 2^-10, 2^-17 of the largest. The parts are further steps along K: one sum.
 //   O  fp16 products of weights in fp16 and codes, which an fp16 holds exactly. A column's largest is held above 2^8
-//      and below 2^16, so half a step is 2^-12 of a weight, and at the lower end 2^-25 in those units: 2^-33 of the
-//      largest. (Weights as 8-bit parts, as kv8_decode has them, need four for such a range: twice the tensor time, and
-//      some thirty instructions for a pair of weights where a conversion is one. There the codes need no conversion
-//      instead, which is 2 D a token and does not grow with the columns.)
+//      and below 2^16, so half a step is 2^-11 of a weight just above a power of two (2^-12 just below one), and at
+//      the lower end 2^-25 in those units: 2^-33 of the largest. (Weights as 8-bit parts, as kv8_decode has them, need
+//      four for such a range: twice the tensor time, and some thirty instructions for a pair of weights where a conversion
+//      is one. There the codes need no conversion instead, which is 2 D a token and does not grow with the columns.)
 //
 // One CTA per SM, persistent; the tiles (two pages, 128 tokens: one product's N) of all units (request, key/value head,
 // 128 columns) form one sequence, cut into one contiguous range a CTA. Its warps:

@@ -331,6 +331,33 @@ def test_tree_of_a_chain_is_kv8_decode():
         check_tree(*run_tree(c, masks, window), ref, 1500)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_tree_weights_just_above_a_power_of_two(D):
+    """Keys that are all alike, so that all weights of a column round the same way and nothing averages out. Half a step of an fp16 is
+    2^-11 of a weight just above a power of two; that and, as small as the rest of check_tree's bound is here, little else is what
+    an output may be off by beside its own rounding. Some come to more than 2^-12 would allow: the bound is not too wide."""
+    Hk, Q, n = 1, 64, 200
+    k, v = np.zeros((n, Hk, D)), np.tile(1 + np.arange(D) % 8 / 8, (n, Hk, 1))
+    k[:, :, 0] = 1
+    cache, table, lens = np.zeros((4, kv8.page_bytes(Hk, D)), np.uint8), np.arange(4, dtype=np.int32)[None], np.array([n], np.int32)
+    kv8.append(cache, k, v, [0, n], lens, table, Hk, D)
+    q = torch.zeros((1, Q, 2, D), dtype=torch.float16)
+    q[..., 0] = 1 + torch.arange(2 * Q).view(1, Q, 2) / 1024
+    masks = (np.uint64(1) << np.arange(Q, dtype=np.uint64))[None]
+    half, beyond = 2.0 ** -11, False
+    for s in (0.0, 3e-4, 6.7e-4, 6.9e-4):                # weights of 2^(8 + s + c / 1024), c = 0 .. 127
+        scale = float(np.log(2) * (1 + s))
+        out, lse = m.kv8_decode_tree(q.to("cuda"), dev(cache, torch.uint8), dev(table), dev(lens), dev(masks.view(np.int64), torch.int64), Hk, scale)
+        r, _, mass, reach, _, span = spec.decode_tree(f64(q), cache, table, lens, masks, Hk, scale)
+        dz = (D + 8) * 2.0 ** -24 * reach + 2.0 ** -17 * span
+        rest = (2 * (dz + 2.0 ** -21) + n * 2.0 ** -23)[..., None]
+        off = np.abs(f64(out) - r)
+        assert np.all(off <= half * np.abs(r) + (1 + half) * (2.0 ** -11 + rest) * mass)
+        beyond |= bool(np.any(off > half * np.abs(r) + (1 + half) * (2.0 ** -12 + rest) * mass))
+        assert np.all(np.isfinite(f64(lse)))
+    assert beyond
+
+
 def test_tree_masks_of_any_kind():
     """No node, only bits behind Q, only others' bits, sequences shorter than the tree and empty ones."""
     rng = np.random.default_rng(5)
