@@ -604,7 +604,8 @@ int kv8_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, int
  * the newest token that is certain, the others drafts, each with a parent of a smaller number. The step:
  * kv_pages_extend and kv8_append_rope (with the nodes' places in the text as positions) make room for and
  * write them, kv8_decode_tree attends, spec_verify says which drafts stand, kv8_keep and kv_pages_trim
- * take the others out.
+ * take the others out. One trace of these stays: where drafts raised the scale of a block that they shared
+ * with certain tokens, those of its older codes that became subnormal were rounded again (as by kv8_append).
  */
 #define NVFP4MLA_MAX_NODES 64     /* nodes of a tree, node 0 among them           */
 
@@ -623,6 +624,10 @@ size_t kv8_decode_tree_workspace_size(int B, int Q, int H, int kv_heads, int hea
  *   queries  off by at most 2^-17 of the row's largest magnitude (bf16: exact from 2^-9 of it on, fp16: 2^-6)
  *   weights  off by at most 2^-11 of itself, or 2^-33 of the largest such product of the row's attended positions
  *            if that is more; the sum that divides is one of unrounded exponentials
+ * These are wider than kv8_decode's, which a chain (each node the child of the one before) of up to 16 nodes can
+ * go to as well: in fp16 the weights' half step is as large as the output's own, in bf16 an eighth of it. Time goes
+ * by 128 (node, query head) columns of a key/value head: fewer cost nearly what 128 do, one more as much again. So a
+ * chain of up to 16 columns, Q x H / kv_heads, is faster in kv8_decode, a longer one here.
  *
  *   masks             uint64 [B, Q], 8-byte aligned
  *   Q                 1 .. NVFP4MLA_MAX_NODES

@@ -710,7 +710,8 @@ def kv8_decode_tree(q, cache, page_table, seq_lens, masks, kv_heads: int, softma
                     workspace=None, dev_status=None, max_ctas: int = 0, stream=None, test_timeout: bool = False):
     """kv8_decode for trees of up to 64 nodes, the Q newest tokens of each request: masks int64 [B, Q], bit i of node j's:
     it attends to node i (its ancestors and itself; 0: padding, out 0 and lse -inf). All nodes attend to what lies before
-    the tree; window (0, or at least Q): as far back as the node's place in the text allows."""
+    the tree; window (0, or at least Q): as far back as the node's place in the text allows. A chain of up to 16 columns
+    (Q x H / kv_heads) is faster in kv8_decode, which also holds its operands in more bits."""
     return _decode("kv8_decode_tree", load_library().kv8_decode_tree, kv8_decode_tree_workspace_size, q, cache, page_table, seq_lens,
                    masks, kv_heads, softmax_scale, window, out, lse, workspace, dev_status, max_ctas, stream, test_timeout)
 

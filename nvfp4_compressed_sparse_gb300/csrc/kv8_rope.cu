@@ -11,13 +11,16 @@
 // dims it has eight dims of its own.
 //
 // A CTA takes a block of 16 tokens of one request and a share of the heads of one kind (queries, keys, values: one code a
-// CTA): it stages the cosines and sines of its tokens once, then a warp takes a query's or value's head at a time, two warps
-// a key's, whose rows stay in registers until the block's scale is known. Shares are cut finer where blocks are few, down to
-// a head a warp, so that every SM has CTAs.
+// CTA): it stages the cosines and sines of its tokens once, then a warp takes a query's or value's head at a time, two
+// warps a key's, whose turned rows are held until the block's scale is known: in registers, but for 40 to 76 bytes a thread
+// at 128 dims, where the 64 registers that leave room for four CTAs an SM do not hold all of a key warp's (none at 64).
+// Shares are cut finer where blocks are few, down to a head a warp, so that every SM has CTAs.
 //
 // Measured, back to back, against 6.77 TB/s of measured copy bandwidth: 34,700 prompt tokens of 32 query heads over 8 of
-// 128: 146 us (81 %); 512 tokens of 16 trees 5.1 us, one token of 64 requests 7.3 us (both a chain of dependent reads: the
-// request of a block, its lengths, positions, angles, rows). A warp a key head, whose rows are turned twice, took 159 us;
+// 128: 146 us (81 %); 512 tokens of 16 trees 5.1 us, one token of 64 requests 7.1 us: latency, as a block's request, lengths,
+// positions and angles are read one after the other, and rows, which need none of the angles, only behind the barrier that
+// those wait at. A request has two blocks' CTAs at least, so that with one token each half of them have nothing to do (476 of
+// 924 here, where 608 run at a time). A warp a key head, whose rows are turned twice, took 159 us;
 // kinds mixed in a CTA 235.
 #include "../../include/nvfp4mla.h"
 #include "kv8.h"

@@ -6,17 +6,20 @@
 // children were drawn from; a draft without one stands for itself, q(x) = 1, and its refusal takes x out of
 // r.) When no child is taken, the next token is drawn from r by its running sum.
 //
-// What bounds it. Every row of logits is read once, for its largest value and its sum of exponentials: memory, where there
-// are many rows. stats_kernel does that by chunks of 4 KB, a warp each, whose values stay in registers; the chunks' sums
-// are kept, since with them a token can be drawn by reading a single chunk again. walk_kernel has a CTA a request (with
-// draft distributions a cluster of eight, since what a refusal leaves is a sum over the vocabulary): all nodes'
-// probabilities are found at once, so that the walk itself is a few comparisons. It is a chain of some eight dependent
-// reads, and of code that runs once. Running sums over chunks are in 64 bits: what is drawn changes where they cross a
-// border between tokens.
+// What bounds it. The answer needs the rows of the nodes that the walk reaches, one more than are accepted, and a row of
+// the drafts' distribution for each of those at which a child is refused; which ones these are is known on the way only. So
+// stats_kernel reads every node's row once, for its largest value and its sum of exponentials, before the walk: memory,
+// where there are many rows, most of which a tree's walk does not come to. It goes by chunks of 4 KB, a warp each, whose
+// values stay in registers; the chunks' sums are kept, since with them a token can be drawn by reading a single chunk
+// again. walk_kernel has a CTA a request (with draft distributions a cluster of eight, since what a refusal leaves is a sum
+// over the vocabulary): all nodes' probabilities are found at once, so that the walk itself is a few comparisons. It is a
+// chain of some eight dependent reads, and of code that runs once. Running sums over chunks are in 64 bits: what is drawn
+// changes where they cross a border between tokens.
 //
-// Measured, back to back, against 6.77 TB/s of measured copy bandwidth: 64 chains of 5 nodes over 128,000 bf16 logits with
-// draft distributions 31 us (55 % of it, over logits and the distributions of refusing nodes: some 17 us are stats_kernel's,
-// 14 the walk's), 16 trees of 32 over 100,003 without 31 us (49 %: 21 and 10), one chain of 5 over 32,000 fp32 10 us (all
+// Measured, back to back: 64 chains of 5 nodes over 128,000 bf16 logits with draft distributions 31 us, of which some 17
+// are stats_kernel's (82 MB at 71 % of the 6.77 TB/s of measured copy bandwidth) and 14 the walk's: the rows that were
+// needed, 2.7 of 5 a request, and the distributions are 61 MB, 9 us. 16 trees of 32 over 100,003 without distributions 30
+// us (20 for 99 MB, and 10): of 31 rows a request 2.2 were needed, 7 MB, 1 us. One chain of 5 over 32,000 fp32 10 us (all
 // latency). What was tried and not kept: chunks that come to shared memory ahead of a warp's work, by a ring of three a
 // warp (37 to 40, 37 and 12 us); a walk in 64 bits, or unrolled (its code is fetched once a call, some 16 cycles an
 // instruction); the next distribution brought to L2 (no difference).
